@@ -254,7 +254,8 @@ def prepare(case, seed):
         if c["op"] == "evict":
             s["dst"] = tq.Cache(ctx, c["batch"], c["heads_kv"], _blocks(c["keep"]) * BLK)
         if c["op"] == "attend":
-            s["ws"] = torch.empty(tq.tq_q8_attention_workspace(ctx.handle, c["batch"], c["heads_q"], c["heads_kv"], c["n_q"], nblk * BLK),
+            s["ws"] = torch.empty(tq.tq_q8_attention_workspace(ctx.handle, c["batch"], c["heads_q"], c["heads_kv"], c["n_q"], nblk * BLK,
+                                                                 weights=c["weights"]),
                                   dtype=torch.uint8, device="cuda")
     return s
 
