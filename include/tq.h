@@ -124,6 +124,27 @@
  *  After a sequence holds N tokens, its first nq = group*floor((N-window)/
  *  group) tokens (0 while N < window + group) are quantised and tokens
  *  [nq, N) are in the window.
+ *
+ *  Q8 records (TQ_SCHEME_Q8): a records array of 64-token blocks,
+ *  [batch][heads_kv][ceil(capacity / 64)] blocks of 16384 bytes: the key plane
+ *  (8192 bytes), then the value plane. A plane holds the d = 128 coordinates of
+ *  its 64 tokens as float8 e4m3 numbers (1 sign, 4 exponent, 3 mantissa bits;
+ *  largest value 448): token t of the block has coordinate c at byte
+ *  1024 (t / 8) + 128 (c / 16) + 16 (t mod 8) + c mod 16, so every group of 8
+ *  tokens is one contiguous KB and the plane is a tensor-core operand as it
+ *  lies. Each plane of a block has one scale 2^e (float32, k_stats / v_stats
+ *  [batch][heads_kv][ceil(capacity / 64)], pool-indexed when paged): a
+ *  coordinate stands for code * 2^e.
+ *    Quantisation: the new tokens that one call writes into a block need the
+ *  least whole e >= -100 with max |x| <= 448 * 2^e. A block whose first slot the
+ *  call writes takes that e; one that already held tokens keeps its e unless the
+ *  new tokens need a larger one, and its older codes are then rounded again to
+ *  code * 2^(e_old - e). A code is x * 2^-e rounded to the nearest e4m3 number
+ *  (ties to even). x * 2^-e is exact, so codes and scales are bit-exact. Numbers
+ *  beyond 1.875 * 2^127 are cut to it first (they would round to 2^128). The
+ *  cache holds finite numbers only: an infinity is stored as +-448 * 2^e and a
+ *  NaN as 0, e being taken over the finite coordinates, and the device error
+ *  word is set to TQ_ERR_NONFINITE.
  */
 #ifndef TQ_H
 #define TQ_H
@@ -148,17 +169,20 @@ typedef enum {
   TQ_ERR_TIMEOUT = 5,     /* (device) a bounded wait gave up                 */
   TQ_ERR_STATE = 6,       /* the call does not fit the context's scheme      */
   TQ_ERR_ALIGN = 7,       /* a pointer is not 16-byte aligned                */
-  TQ_ERR_WORKSPACE = 8    /* the workspace is smaller than tq_workspace_size */
+  TQ_ERR_WORKSPACE = 8,   /* the workspace is smaller than tq_workspace_size */
+  TQ_ERR_NONFINITE = 9    /* (device) an infinity or a NaN was quantised (TQ_SCHEME_Q8) */
 } tq_status;
 
 typedef enum {
   TQ_SCHEME_KV = 0,
   TQ_SCHEME_KQV = 1,
   TQ_SCHEME_QKQV = 2,
-  TQ_SCHEME_KIVI = 3
+  TQ_SCHEME_KIVI = 3,
+  TQ_SCHEME_Q8 = 4 /* 8-bit floating point, one scale per 64 tokens and head */
 } tq_scheme;
 
-typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
+/* TQ_F16 is taken by tq_rotary, tq_q8_append and tq_q8_attention. */
+typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
 /* The rotation of the rotated roles (KQV and QKQV keys and values). */
 typedef enum {
@@ -194,12 +218,14 @@ typedef enum {
  * sets the device error word to TQ_ERR_ARG. The table is read, never written,
  * by the library; the caller owns it and may change entries between calls (in
  * stream order). Results are the contiguous layout's, bit for bit, whatever the
- * mapping. */
+ * mapping. TQ_SCHEME_Q8 caches page the same way in their 64-token blocks: the
+ * table is [batch][heads_kv][ceil(capacity / 64)] and the scales lie at the pool
+ * block's index. */
 typedef struct tq_cache {
   int batch, heads_kv, capacity;
   uint8_t *records;                          /* TQ schemes: the blocked records (or the pool) */
   uint8_t *k_codes;  uint8_t *v_codes;       /* KIVI: 2-bit codes */
-  uint16_t *k_stats; uint16_t *v_stats;      /* KIVI: fp16 (zero, step) */
+  uint16_t *k_stats; uint16_t *v_stats;      /* KIVI: fp16 (zero, step); Q8: float32 scales of the blocks */
   uint16_t *k_window; uint16_t *v_window;    /* KIVI: bf16 ring buffers */
   const int32_t *block_table;                /* TQ schemes: NULL (contiguous) or the block table */
   int pool_blocks;                           /* blocks in the pool when block_table != NULL */
@@ -223,7 +249,7 @@ const char *tq_status_str(int status);
 /* Create a context ([KVQuant++] "Deployment and use": a quantiser from
  * head_dim and num_bits; [TQ-stats] "Quantisation schemes": the scheme and
  * its budget). d: head dimension (this build: 128). bits: the budget n in
- * bits per coordinate, 2..4 (TQ_SCHEME_KIVI: must be 2). scheme: a
+ * bits per coordinate, 2..4 (TQ_SCHEME_KIVI: must be 2; TQ_SCHEME_Q8: must be 8). scheme: a
  * tq_scheme. seed: selects D and S. Fits the needed codebooks on the host
  * (fp64), draws D and S, copies them to the current device.
  * *out receives the handle (NULL on failure). */
@@ -460,6 +486,127 @@ tq_status tq_get_device_error(const tq_ctx *ctx, void *stream, int *code);
  * context's GPU must be current. Errors: TQ_ERR_ARG (null context, budget
  * above 2e9, another device current), TQ_ERR_CUDA (launch). */
 tq_status tq_selftest_bounded_wait(const tq_ctx *ctx, unsigned long long budget_ns, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and the 8-bit cache's own calls (TQ_SCHEME_Q8)
+ *
+ * A Q8 context also takes tq_cache_sizes_get, tq_append_quantize,
+ * tq_decode_attention (any number of query heads per KV head, splits ignored),
+ * tq_decode_step and tq_dequantize; the calls below add rotation, strides,
+ * ragged batches, many query tokens, masks and eviction. They want the
+ * context's device to be current (TQ_ERR_ARG otherwise), keep no state between
+ * calls and may be captured into a graph. Two calls may run at once on two
+ * streams if neither writes what the other reads or writes (a workspace is
+ * written).
+ *
+ * Strides are in elements, of the batch, head and token dimension in this order;
+ * the d coordinates are contiguous. Every pointer must be 16-byte aligned and
+ * every stride a multiple of 16 bytes (TQ_ERR_ALIGN otherwise).
+ * ------------------------------------------------------------------------- */
+
+/* The rotation of positions that tq_rotary and tq_q8_append use. Pair i of the
+ * first `dim` coordinates (a multiple of 8, at most d) turns by pos * f_i radians:
+ * (a, b) -> gain (a cos - b sin, b cos + a sin), f_i = base^(-2i / dim). The pairs
+ * are (2i, 2i + 1) when interleaved, (i, i + dim / 2) otherwise; coordinates from
+ * dim on pass through. factor > 1 stretches the rotation for contexts longer than
+ * original_len: with r = original_len f_i / (2 pi) turns in the original length
+ * and s = min(max((r - low) / (high - low), 0), 1), f_i becomes
+ * (1 - s) f_i / factor + s f_i (slow pairs are interpolated, fast ones kept;
+ * low = high = 0 divides every f_i by the factor). Positions are whole numbers of
+ * any sign; angles are formed in 64-bit fixed point, so they are as exact at
+ * position 2^31 as at 1. Copied by value: nothing is allocated, and calls already
+ * enqueued or captured keep the rotation they were made with. */
+typedef struct tq_rope {
+  int dim, interleaved;
+  double base, factor, original_len, low, high, gain;
+} tq_rope;
+tq_status tq_set_rope(tq_ctx *ctx, const tq_rope *rope);
+
+/* Rotate x into y (the same buffer and strides, or one that does not overlap):
+ * [batch][heads][n][d] of `dtype`, token t of sequence b at position
+ * d_positions[b * n + t]. transpose = 1 turns by the opposite angle (the
+ * gradient's form). The rotation is computed in fp32 and rounded once.
+ * TQ_ERR_STATE before tq_set_rope. Any scheme's context. */
+tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides, void *d_y, const int64_t *y_strides,
+                    int dtype, int batch, int heads, int n, const int32_t *d_positions, int transpose, void *stream);
+
+/* Append new tokens to a Q8 cache ("cache write"), as tq_append_quantize does,
+ * with strides, ragged batches and the rotation of the keys.
+ *   d_k, d_v    : [batch][heads_kv][n_new][d] of `dtype` under k_strides, v_strides
+ *   d_seq_lens  : int32 [batch]: token t of sequence b goes to slot d_seq_lens[b] + t
+ *   d_new_lens  : int32 [batch], or NULL: sequence b brings its first
+ *                 d_new_lens[b] tokens only (0..n_new; the rest is not read)
+ *   rope        : 1 rotates the keys first (rounded to `dtype`, as tq_rotary
+ *                 would return them)
+ *   d_positions : int32 [batch][n_new], or NULL: token t is at position
+ *                 d_seq_lens[b] + t
+ * A sequence whose slots would lie outside the cache is skipped whole
+ * (TQ_ERR_CAPACITY in the device error word); so is one whose d_new_lens[b] is out
+ * of range (TQ_ERR_ARG). Two sequences of one call must not share a block. */
+tq_status tq_q8_append(const tq_ctx *ctx, const tq_cache *cache, const void *d_k, const int64_t *k_strides,
+                       const void *d_v, const int64_t *v_strides, int dtype, int batch, int heads_kv, int n_new,
+                       const int32_t *d_seq_lens, const int32_t *d_new_lens, int rope, const int32_t *d_positions,
+                       void *stream);
+
+/* Attention of n_q query tokens per sequence over a Q8 cache. Fields that may be
+ * NULL or 0 are optional; zero the struct first. */
+typedef struct tq_q8_attn {
+  int batch, heads_q, heads_kv; /* heads_q a multiple of heads_kv */
+  int n_q;                      /* query tokens per sequence, >= 1 */
+  int max_len;                  /* >= every d_seq_lens[b], <= the capacity */
+  int q_dtype;                  /* TQ_F32, TQ_BF16 or TQ_F16 */
+  int out_dtype;                /* q_dtype, or TQ_F32 */
+  const void *d_q;              /* [batch][heads_q][n_q][d] under q_strides */
+  int64_t q_strides[3];
+  void *d_out;                  /* [batch][heads_q][n_q][d] under out_strides */
+  int64_t out_strides[3];
+  const int32_t *d_seq_lens;    /* [batch]: tokens in the cache, the query tokens' own among them */
+  const int32_t *d_new_lens;    /* [batch] or NULL (n_q): query tokens of each sequence; later rows are not written */
+  /* t = scale q.k, then softcap tanh(t / softcap), then t - slope |q position - k position| */
+  float scale;                  /* 0: 1 / sqrt(d) */
+  float softcap;                /* 0: none */
+  const float *d_slopes;        /* [heads_q] or NULL */
+  const int32_t *d_q_positions; /* [batch][n_q], or NULL: query i is at its slot d_seq_lens[b] - new + i */
+  const int32_t *d_k_positions; /* [batch][heads_kv][capacity], or NULL: a key is at its slot */
+  /* [batch][n_q] or NULL: query i sees the slots [begin, end), cut to [0, d_seq_lens[b]);
+   * by default [0, its own slot + 1) */
+  const int32_t *d_key_begin, *d_key_end;
+  /* [batch][heads_kv][capacity] or NULL: weights = weights_in (0 when NULL) + the probabilities each slot got,
+   * summed over the group's heads and the sequence's query tokens. Both may be one buffer. */
+  const float *d_weights_in;
+  float *d_weights;
+  float *d_lse;                 /* [batch][heads_q][n_q] or NULL: log of the softmax's sum, natural; -inf for an empty row */
+} tq_q8_attn;
+
+/* out = softmax(t) V_hat over the slots each query sees; a query that sees none
+ * yields zeros. d_workspace: >= tq_q8_attention_workspace(...) bytes for these
+ * sizes (weights: 1 when d_weights is set), no initial contents required. A d_seq_lens[b] outside [0, max_len] or a d_new_lens[b]
+ * outside [0, n_q] is cut to that range, and a bad block-table entry's tokens are
+ * taken as unseen; both set the device error word to TQ_ERR_ARG. Rounding: the
+ * products are exact in fp32 sums; the probabilities enter the value sums with 11
+ * significant bits when out_dtype has 16 bits, with 22 when it is TQ_F32. */
+tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
+                                    int weights, size_t *out);
+tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, void *d_workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Cut every sequence of `src` to at most `keep` tokens into `dst`, another cache of
+ * the same context, batch and KV heads whose memory does not overlap. Per sequence
+ * of n tokens and KV head, m = min(n, keep) tokens stay: all of them when n <=
+ * keep, else the first `sink`, the last `recent` and those of the rest with the
+ * largest d_weights (equal weights: the lower slot stays; a NaN counts as the
+ * smallest), sink + recent <= keep <= dst capacity. Order is kept; the tokens fill dst slots
+ * 0 .. m - 1 and are rounded to the new blocks' scales; slots m .. 64 ceil(keep / 64) - 1 read 0.
+ *   d_seq_lens  : int32 [batch], each in [0, src capacity] (cut to it otherwise: TQ_ERR_ARG in the error word)
+ *   d_weights   : float [batch][heads_kv][src capacity]
+ *   d_kept      : int32 [batch][heads_kv][keep], out: the kept tokens' slots in src, -1 from m on
+ *   d_dst_lens  : int32 [batch], out: m
+ *   d_dst_weights, d_dst_positions : [batch][heads_kv][dst capacity] or NULL, out: the kept tokens' d_weights
+ *                 and d_positions (int32 [batch][heads_kv][src capacity]; NULL: their slots), 0 from m on */
+tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *dst, int batch, int heads_kv,
+                      const int32_t *d_seq_lens, const float *d_weights, int keep, int sink, int recent,
+                      const int32_t *d_positions, int32_t *d_kept, int32_t *d_dst_lens, float *d_dst_weights,
+                      int32_t *d_dst_positions, void *stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "tq_internal.h"
+#include "tq_q8_host.h"
 
 namespace {
 
@@ -396,6 +397,7 @@ const char *tq_status_str(int s) {
     case TQ_ERR_STATE: return "call does not fit the context's scheme";
     case TQ_ERR_ALIGN: return "pointer not 16-byte aligned";
     case TQ_ERR_WORKSPACE: return "workspace too small";
+    case TQ_ERR_NONFINITE: return "an infinity or a NaN was quantised";
     default: return "unknown status";
   }
 }
@@ -418,9 +420,9 @@ tq_status tq_draw_params(uint64_t seed, int d, int8_t *h_diag, float *h_sketch) 
 tq_status tq_init(int d, int bits, int scheme, uint64_t seed, tq_ctx **out) {
   if (!out) return TQ_ERR_ARG;
   *out = nullptr;
-  if (scheme < TQ_SCHEME_KV || scheme > TQ_SCHEME_KIVI) return TQ_ERR_ARG;
+  if (scheme < TQ_SCHEME_KV || scheme > TQ_SCHEME_Q8) return TQ_ERR_ARG;
   if (d < 4 || (d & (d - 1))) return TQ_ERR_ARG;
-  if (bits < 2 || bits > 4) return TQ_ERR_ARG;
+  if (scheme == TQ_SCHEME_Q8 ? bits != 8 : (bits < 2 || bits > 4)) return TQ_ERR_ARG;
   if (d != tq::kD) return TQ_ERR_UNSUPPORTED;
   if (scheme == TQ_SCHEME_KIVI && bits != 2) return TQ_ERR_UNSUPPORTED;
 
@@ -464,7 +466,7 @@ tq_status tq_init(int d, int bits, int scheme, uint64_t seed, tq_ctx **out) {
     }
     c->sketch_rowmax = (float)(m * (1.0 + 1e-6));
   }
-  if (scheme != TQ_SCHEME_KIVI) build_layout(c);
+  if (is_tq_scheme(scheme)) build_layout(c);
 
   tq::DevParams *hp = (tq::DevParams *)std::calloc(1, sizeof(tq::DevParams));
   if (!hp) {
@@ -527,7 +529,7 @@ tq_status tq_draw_rotation(uint64_t seed, int d, float *h_rotation) {
 
 tq_status tq_set_rotation(tq_ctx *ctx, int rotation) {
   if (!ctx) return TQ_ERR_ARG;
-  if (ctx->scheme == TQ_SCHEME_KIVI) return TQ_ERR_STATE;
+  if (!is_tq_scheme(ctx->scheme)) return TQ_ERR_STATE;
   if (rotation != TQ_ROTATION_WHT && rotation != TQ_ROTATION_DENSE) return TQ_ERR_ARG;
   if (ctx->side_rank) return TQ_ERR_STATE;  // side-code bases are set in the rotated coordinates
   if (rotation == TQ_ROTATION_DENSE && ctx->rotation != TQ_ROTATION_DENSE) {
@@ -574,7 +576,7 @@ tq_status tq_principal_basis(const float *h_x, int n, int d, int rank, float *h_
 
 tq_status tq_set_side_basis(tq_ctx *ctx, int rank, int heads_kv, const float *h_basis) {
   if (!ctx) return TQ_ERR_ARG;
-  if (ctx->scheme == TQ_SCHEME_KIVI || ctx->k.qjl) return TQ_ERR_STATE;
+  if (!is_tq_scheme(ctx->scheme) || ctx->k.qjl) return TQ_ERR_STATE;
   if (rank < 0 || rank > 8) return TQ_ERR_ARG;
   const int d = ctx->d;
   if (ctx->side_u) cudaFree(ctx->side_u);
@@ -668,6 +670,10 @@ tq_status tq_set_kivi(tq_ctx *ctx, int group, int window, int k_per_channel, int
 tq_status tq_cache_sizes_get(const tq_ctx *ctx, int batch, int heads_kv, int capacity, tq_cache_sizes *out) {
   if (!ctx || !out || batch <= 0 || heads_kv <= 0 || capacity <= 0) return TQ_ERR_ARG;
   std::memset(out, 0, sizeof(*out));
+  if (ctx->scheme == TQ_SCHEME_Q8) {
+    tq::q8_cache_sizes(batch, heads_kv, capacity, out);
+    return TQ_OK;
+  }
   const size_t slots = (size_t)batch * heads_kv * capacity;
   const int d = ctx->d;
   if (ctx->scheme == TQ_SCHEME_KIVI) {
@@ -716,6 +722,7 @@ static void set_role_planes(const tq_ctx *ctx, const tq_cache *c, int which, uin
 
 static tq_status check_cache(const tq_ctx *ctx, const tq_cache *c, int batch, int heads_kv) {
   if (!c) return TQ_ERR_ARG;
+  if (ctx->scheme == TQ_SCHEME_Q8) return tq::q8_check_cache(ctx, c, batch, heads_kv);
   if (c->batch != batch || c->heads_kv != heads_kv || c->capacity <= 0) return TQ_ERR_ARG;
   const void *planes[] = {c->records, c->k_codes, c->v_codes, c->k_stats, c->v_stats, c->k_window, c->v_window};
   for (const void *p : planes)
@@ -747,6 +754,14 @@ tq_status tq_append_quantize(const tq_ctx *ctx, const tq_cache *cache, const voi
   if (s != TQ_OK) return s;
   if (!aligned16(d_k) || !aligned16(d_v)) return TQ_ERR_ALIGN;
   if (n_new == 0) return TQ_OK;
+  if (ctx->scheme == TQ_SCHEME_Q8) {
+    const int64_t rows[3] = {(int64_t)heads_kv * n_new * ctx->d, (int64_t)n_new * ctx->d, ctx->d};
+    if (ctx->prof_append_start) cudaEventRecord((cudaEvent_t)ctx->prof_append_start, (cudaStream_t)stream);
+    s = tq_q8_append(ctx, cache, d_k, rows, d_v, rows, dtype, batch, heads_kv, n_new, d_seq_lens, nullptr, 0, nullptr,
+                     stream);
+    if (ctx->prof_append_stop) cudaEventRecord((cudaEvent_t)ctx->prof_append_stop, (cudaStream_t)stream);
+    return s;
+  }
   if (ctx->scheme == TQ_SCHEME_KIVI) {
     tq::KiviAppendArgs a{ctx, cache, d_k, d_v, dtype, batch, heads_kv, n_new, d_seq_lens, &ctx->dparams->error};
     if (ctx->prof_append_start) cudaEventRecord((cudaEvent_t)ctx->prof_append_start, (cudaStream_t)stream);
@@ -828,10 +843,35 @@ static tq_status append_tq_both(const tq_ctx *ctx, const tq_cache *cache, const 
   return s;
 }
 
+static size_t q8_lens_bytes(int batch) { return ((size_t)batch * sizeof(int32_t) + 15) / 16 * 16; }
+
+// One query token per sequence on an 8-bit cache (tq_decode_attention's arguments; arguments checked).
+static tq_status q8_decode(const tq_ctx *ctx, const tq_cache *cache, const void *d_q, int q_dtype, int batch, int heads_q,
+                           int heads_kv, const int32_t *d_seq_lens, int max_len, void *d_workspace, size_t ws_bytes,
+                           float *d_out, void *stream) {
+  tq_q8_attn a{};
+  a.batch = batch, a.heads_q = heads_q, a.heads_kv = heads_kv, a.n_q = 1, a.max_len = max_len;
+  a.q_dtype = q_dtype, a.out_dtype = TQ_F32, a.d_q = d_q, a.d_out = d_out, a.d_seq_lens = d_seq_lens;
+  const int64_t rows[3] = {(int64_t)heads_q * ctx->d, ctx->d, ctx->d};
+  std::memcpy(a.q_strides, rows, sizeof(rows));
+  std::memcpy(a.out_strides, rows, sizeof(rows));
+  const size_t lens = q8_lens_bytes(batch);
+  if (ctx->prof_decode_start) cudaEventRecord((cudaEvent_t)ctx->prof_decode_start, (cudaStream_t)stream);
+  const tq_status s = tq_q8_attention(ctx, cache, &a, (char *)d_workspace + lens, ws_bytes - lens, stream);
+  if (ctx->prof_decode_stop) cudaEventRecord((cudaEvent_t)ctx->prof_decode_stop, (cudaStream_t)stream);
+  return s;
+}
+
 tq_status tq_workspace_size(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int max_len, int splits,
                             size_t *out) {
   if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || max_len <= 0 || splits < 0)
     return TQ_ERR_ARG;
+  if (ctx->scheme == TQ_SCHEME_Q8) {
+    // the decode step's lengths, then the attention's own
+    if (heads_q % heads_kv) return TQ_ERR_ARG;
+    *out = q8_lens_bytes(batch) + tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, 1, max_len, 0);
+    return TQ_OK;
+  }
   int s, chunk;
   tq::choose_splits(batch, heads_kv, max_len, splits, &s, &chunk);
   // prepared queries | decode-tile prefix over batches | decode-step lengths | partial
@@ -869,7 +909,7 @@ tq_status tq_decode_attention(const tq_ctx *ctx, const tq_cache *cache, const vo
   if (q_dtype != TQ_F32 && q_dtype != TQ_BF16) return TQ_ERR_ARG;
   if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || max_len <= 0 || splits < 0) return TQ_ERR_ARG;
   if (heads_q % heads_kv) return TQ_ERR_ARG;
-  if (heads_q / heads_kv > tq::kMaxGroup) return TQ_ERR_UNSUPPORTED;
+  if (ctx->scheme != TQ_SCHEME_Q8 && heads_q / heads_kv > tq::kMaxGroup) return TQ_ERR_UNSUPPORTED;
   tq_status s = check_cache(ctx, cache, batch, heads_kv);
   if (s != TQ_OK) return s;
   if (max_len > cache->capacity) return TQ_ERR_ARG;
@@ -877,6 +917,9 @@ tq_status tq_decode_attention(const tq_ctx *ctx, const tq_cache *cache, const vo
   size_t need = 0;
   tq_workspace_size(ctx, batch, heads_q, heads_kv, max_len, splits, &need);
   if (ws_bytes < need) return TQ_ERR_WORKSPACE;
+  if (ctx->scheme == TQ_SCHEME_Q8)
+    return q8_decode(ctx, cache, d_q, q_dtype, batch, heads_q, heads_kv, d_seq_lens, max_len, d_workspace, ws_bytes, d_out,
+                     stream);
   tq::DecodeArgs a{};
   a.ctx = ctx;
   a.cache = cache;
@@ -903,7 +946,7 @@ tq_status tq_decode_step(const tq_ctx *ctx, const tq_cache *cache, const void *d
   if (kv_dtype != TQ_F32 && kv_dtype != TQ_BF16) return TQ_ERR_ARG;
   if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || max_len <= 0) return TQ_ERR_ARG;
   if (heads_q % heads_kv) return TQ_ERR_ARG;
-  if (heads_q / heads_kv > tq::kMaxGroup) return TQ_ERR_UNSUPPORTED;
+  if (ctx->scheme != TQ_SCHEME_Q8 && heads_q / heads_kv > tq::kMaxGroup) return TQ_ERR_UNSUPPORTED;
   tq_status s = check_cache(ctx, cache, batch, heads_kv);
   if (s != TQ_OK) return s;
   if (max_len > cache->capacity) return TQ_ERR_ARG;
@@ -913,6 +956,15 @@ tq_status tq_decode_step(const tq_ctx *ctx, const tq_cache *cache, const void *d
   size_t need = 0;
   tq_workspace_size(ctx, batch, heads_q, heads_kv, max_len, 0, &need);
   if (ws_bytes < need) return TQ_ERR_WORKSPACE;
+  if (ctx->scheme == TQ_SCHEME_Q8) {
+    int32_t *lens = (int32_t *)d_workspace;
+    s = (tq_status)tq::launch_step_lengths(d_seq_lens, batch, cache->capacity, lens, stream);
+    if (s == TQ_OK)
+      s = tq_append_quantize(ctx, cache, d_k_new, d_v_new, kv_dtype, batch, heads_kv, 1, d_seq_lens, stream);
+    if (s == TQ_OK)
+      s = q8_decode(ctx, cache, d_q, q_dtype, batch, heads_q, heads_kv, lens, max_len, d_workspace, ws_bytes, d_out, stream);
+    return s;
+  }
   if (ctx->scheme != TQ_SCHEME_KIVI) {
     // one decode kernel that also appends the new tokens and prepares the queries
     tq::DecodeArgs a{};
@@ -951,6 +1003,10 @@ tq_status tq_dequantize(const tq_ctx *ctx, const tq_cache *cache, int batch, int
   if (s != TQ_OK) return s;
   if (t1 > cache->capacity) return TQ_ERR_ARG;
   if (t1 == t0) return TQ_OK;
+  if (ctx->scheme == TQ_SCHEME_Q8) {
+    const tq::Q8DequantArgs a{tq::q8_cache(cache), batch, heads_kv, t0, t1, d_k, d_v, &ctx->dparams->error};
+    return (tq_status)tq::launch_q8_dequant(a, stream);
+  }
   if (ctx->scheme == TQ_SCHEME_KIVI) {
     if (!d_seq_lens) return TQ_ERR_ARG;
     tq::KiviDequantArgs a{ctx, cache, batch, heads_kv, t0, t1, d_seq_lens, d_k, d_v};
@@ -997,6 +1053,13 @@ tq_status tq_dequantize(const tq_ctx *ctx, const tq_cache *cache, int batch, int
 tq_status tq_export_params(const tq_ctx *ctx, int *k_bits, float *k_c, float *k_b, int *v_bits, float *v_c,
                            float *v_b, int8_t *diag, float *sketch) {
   if (!ctx) return TQ_ERR_ARG;
+  if (ctx->scheme == TQ_SCHEME_Q8) {  // no codebooks: codes are e4m3 numbers
+    if (k_bits) *k_bits = 8;
+    if (v_bits) *v_bits = 8;
+    if (diag) std::memcpy(diag, ctx->diag, ctx->d);
+    if (sketch) std::memcpy(sketch, ctx->sketch, sizeof(float) * ctx->d * ctx->d);
+    return TQ_OK;
+  }
   const int Lk = 1 << ctx->k.bits, Lv = 1 << ctx->v.bits;
   if (k_bits) *k_bits = ctx->k.bits;
   if (v_bits) *v_bits = ctx->v.bits;

@@ -82,6 +82,14 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv &f) {
 }
 #endif
 
+// The rotation of positions a context was set to (tq_set_rope), passed to kernels by value: pair
+// i turns by freq[i] * 2^-64 turns a position.
+struct RopeTable {
+  int dim = 0, interleaved = 0;  // dim 0: not set
+  float gain = 1.f;
+  unsigned long long freq[kD / 2] = {};
+};
+
 struct Role {
   int bits = 0;
   bool rotate = false;
@@ -164,6 +172,7 @@ struct tq_ctx {
   int side_rank = 0, side_heads = 0;
   float *side_u = nullptr, *side_ur = nullptr, *side_urs = nullptr;
   tq::DevParams *dparams = nullptr;
+  tq::RopeTable rope;
   // a library-owned stream and two events: the key and value appends of one call
   // run concurrently (fork / join on the caller's stream)
   void *side_stream = nullptr, *ev_fork = nullptr, *ev_join = nullptr;

@@ -1,0 +1,225 @@
+// Append to the 8-bit cache (tq_q8_append, tq_append_quantize of a TQ_SCHEME_Q8 context) and its
+// dequantiser.
+//
+// Per block of 64 token slots and tensor: e = the least whole e >= -100 with max |x| <= 448 * 2^e
+// over the call's new tokens in the block (the maximum with the block's own e when it already held
+// tokens, whose codes are then rounded to the new scale), code = e4m3(x * 2^-e). A power-of-two
+// scale makes x * 2^-e exact, so the codes do not depend on how the division is carried out.
+//
+// Bound by memory: the inputs are read and the codes written once. One CTA handles one block of
+// slots of one tensor for a few heads: thread (t, c) owns 16 coordinates of token slot t, i.e. one
+// 16-byte piece of a core matrix; a warp's loads cover 4 whole rows and its stores runs of 64 bytes. The
+// sines and cosines of a token are formed once for all heads of the CTA.
+
+#include "tq_q8.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = kQ8Block * 8;  // 64 token slots x 8 pieces of 16 coordinates
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
+  __shared__ unsigned long long freq[kD / 2];
+  __shared__ uint32_t red[2][kThreads / 32];
+  const int tid = threadIdx.x, c = tid & 7, t = tid >> 3, warp = tid >> 5;
+  const int b = blockIdx.y, tensor = blockIdx.z & 1, h0 = (blockIdx.z >> 1) * hpc;
+  const int h1 = min(a.heads, h0 + hpc);
+  const bool rope = a.rope && tensor == 0;
+  if (rope && tid < kD / 2) freq[tid] = a.table.freq[tid];
+
+  const int len = __ldg(a.seq_lens + b);
+  int n = a.n_new;
+  if (a.new_lens) {
+    n = __ldg(a.new_lens + b);
+    if (n < 0 || n > a.n_new) {
+      if (tid == 0) set_error(a.error, TQ_ERR_ARG);
+      return;
+    }
+  }
+  if (len < 0 || (long long)len + n > a.c.capacity) {
+    if (tid == 0) set_error(a.error, TQ_ERR_CAPACITY);
+    return;
+  }
+  if (n == 0) return;
+  const int j = len / kQ8Block + blockIdx.x;      // block of the sequence
+  if ((long long)j * kQ8Block >= (long long)len + n) return;
+  const int tok = j * kQ8Block + t - len;         // the new token of this thread's slot
+  const bool fresh = tok >= 0 && tok < n, older = tok < 0;
+  const bool joins = j * kQ8Block < len;          // the block already holds tokens
+  __syncthreads();
+
+  // rotation of coordinates 16 c .. 16 c + 15 (half layout: with the ones dim / 2 away)
+  float cs[16], sn[16];
+  const int dim = a.table.dim, half = dim / 2, c0 = 16 * c;
+  if (rope && fresh && c0 < dim) {
+    const int pos = a.positions ? __ldg(a.positions + (long long)b * a.n_new + tok) : len + tok;
+    if (a.table.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[2 * i] = 1.f, sn[2 * i] = 0.f;
+        if (c0 + 2 * i < dim) {
+          rope_sincos(pos, freq[8 * c + i], &cs[2 * i], &sn[2 * i]);
+          cs[2 * i] *= a.table.gain, sn[2 * i] *= a.table.gain;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        cs[i] = 1.f, sn[i] = 0.f;
+        if (c0 + i < dim) {
+          const bool second = c0 + i >= half;
+          rope_sincos(pos, freq[c0 + i - (second ? half : 0)], &cs[i], &sn[i]);
+          cs[i] *= a.table.gain, sn[i] *= second ? a.table.gain : -a.table.gain;
+        }
+      }
+    }
+  }
+
+  const Q8Strides st = tensor ? a.vs : a.ks;
+  const T *x0 = static_cast<const T *>(tensor ? a.v : a.k) + b * st.b + (fresh ? tok : 0) * st.t;
+  float *scales = tensor ? a.c.vs : a.c.ks;
+  bool odd = false;  // an infinity or a NaN
+  for (int h = h0; h < h1; ++h) {
+    float x[16];
+    uint32_t amax = 0;
+    if (fresh) {
+      const T *row = x0 + h * st.h;
+      load_vec<T, 16>(row + c0, x);
+      if (rope && c0 < dim) {
+        if (a.table.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float e0 = x[2 * i], e1 = x[2 * i + 1];
+            x[2 * i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[2 * i], -sn[2 * i])));
+            x[2 * i + 1] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[2 * i], sn[2 * i])));
+          }
+        } else {
+          // dim is a multiple of 8, so groups of 4 coordinates do not straddle a half
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int i0 = c0 + 4 * g;
+            if (i0 < dim) {
+              float o[4];
+              load_vec<T, 4>(row + (i0 < half ? i0 + half : i0 - half), o);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[4 * g + i] = from_type<T>(to_type<T>(rope_turn(x[4 * g + i], o[i], cs[4 * g + i], sn[4 * g + i])));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
+        if (u >= 0x7f800000u) {
+          odd = true;
+          if (u > 0x7f800000u) x[i] = 0.f;
+          u = 0;
+        }
+        // a number that would round up to 2^128 becomes the largest that stays finite
+        x[i] = fminf(fmaxf(x[i], -kQ8Largest), kQ8Largest);
+        amax = max(amax, min(u, __float_as_uint(kQ8Largest)));
+      }
+    }
+    amax = __reduce_max_sync(kFull, amax);
+    uint32_t *slot = red[h & 1];
+    if ((tid & 31) == 0) slot[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) amax = max(amax, slot[w]);
+    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, ((long long)b * a.heads + h) * a.c.nblk + j, a.error);
+    if (blk < 0) continue;
+    int e = q8_exponent(amax);
+    uint8_t *plane = a.c.records + blk * kQ8BlockBytes + tensor * kQ8Plane;
+    uint4 *piece = reinterpret_cast<uint4 *>(plane + q8_off(t, c0));
+    int shift = 0;
+    if (joins) {
+      const int was = log2i(scales[blk]);
+      e = max(e, was);
+      shift = was - e;
+    }
+    if (fresh) {
+      // exact: e lies in [-100, 120]
+      const float f = pow2i(-e);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = cvt_e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) | (cvt_e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
+      *piece = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (older && shift < 0) {
+      const float f = pow2i(max(shift, -126));
+      uint4 w = *piece;
+      *piece = make_uint4(e4m3x4_scaled(w.x, f), e4m3x4_scaled(w.y, f), e4m3x4_scaled(w.z, f), e4m3x4_scaled(w.w, f));
+    }
+    // the next head's barrier orders this store after every thread's read of the old scale
+    if (joins) __syncthreads();
+    if (tid == 0) scales[blk] = pow2i(e);
+  }
+  if (odd) set_error(a.error, TQ_ERR_NONFINITE);
+}
+
+template <typename T>
+int launch(const Q8AppendArgs &a, int num_sms, cudaStream_t st) {
+  const int touched = (int)(((long long)a.n_new + kQ8Block - 2) / kQ8Block + 1);  // blocks n_new slots can lie in
+  // heads per CTA: all that share the sines, while two thousand threads an SM remain
+  const long long ctas = 2LL * touched * a.batch * a.heads;
+  long long hpc = ctas / ((long long)num_sms * 4);
+  hpc = hpc < 1 ? 1 : hpc > 8 ? 8 : hpc;
+  if (hpc > a.heads) hpc = a.heads;
+  const long long gz = 2 * ((a.heads + hpc - 1) / hpc);
+  if (a.batch > 65535 || gz > 65535) return TQ_ERR_UNSUPPORTED;
+  q8_append_kernel<T><<<dim3((unsigned)touched, (unsigned)a.batch, (unsigned)gz), kThreads, 0, st>>>(a, (int)hpc);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+// One thread per 16 coordinates of a token: code * 2^e, exact.
+__global__ void __launch_bounds__(256) q8_dequant_kernel(const __grid_constant__ Q8DequantArgs a, long long items) {
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (id >= items) return;
+  const int c = (int)(id & 7), n = a.t1 - a.t0;
+  const long long row = id >> 3, bh = row / n;
+  const int s = a.t0 + (int)(row % n);
+  const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + s / kQ8Block, a.error);
+#pragma unroll
+  for (int tensor = 0; tensor < 2; ++tensor) {
+    float *out = tensor ? a.v : a.k;
+    if (!out) continue;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    if (blk >= 0) {
+      const float f = (tensor ? a.c.vs : a.c.ks)[blk];
+      const uint4 w = *reinterpret_cast<const uint4 *>(a.c.records + blk * kQ8BlockBytes + tensor * kQ8Plane +
+                                                       q8_off(s % kQ8Block, 16 * c));
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 lo = e4m3x2_f(ww[i] & 0xffffu), hi = e4m3x2_f(ww[i] >> 16);
+        v[4 * i] = lo.x * f, v[4 * i + 1] = lo.y * f, v[4 * i + 2] = hi.x * f, v[4 * i + 3] = hi.y * f;
+      }
+    }
+    store_vec<float, 16>(out + row * kD + 16 * c, v);
+  }
+}
+
+}  // namespace
+
+int launch_q8_append(const Q8AppendArgs &a, int num_sms, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  switch (a.dtype) {
+    case TQ_F32: return launch<float>(a, num_sms, st);
+    case TQ_BF16: return launch<__nv_bfloat16>(a, num_sms, st);
+    default: return launch<__half>(a, num_sms, st);
+  }
+}
+
+int launch_q8_dequant(const Q8DequantArgs &a, void *stream) {
+  const long long items = (long long)a.batch * a.heads * (a.t1 - a.t0) * 8;
+  const long long grid = (items + 255) / 256;
+  if (grid > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  q8_dequant_kernel<<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(a, items);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+}  // namespace tq

@@ -1,0 +1,615 @@
+// Attention over the 8-bit cache for few query rows per KV head (tq_q8_attention): decode steps,
+// drafts, short prompts. Up to 16 rows (query tokens x heads of the group) are one unit of work with
+// a (sequence, KV head).
+//
+// Mathematics, per unit: S = K Q^T for 128 tokens at a time (token = accumulator lane, row = column),
+// t = log2(e) score, running maximum m and sum l of 2^(t - m) per row, O = sum 2^(t - m) v. The codes of
+// the keys and values are tensor-core operands as they lie in the cache (no conversion, no
+// transposition); queries and probabilities enter as three e4m3 / e5m2 terms (six for fp32 results).
+// A block's scale multiplies the scores of its tokens, and its part of O.
+//
+// Bound by the cache's bytes: 256 per token and KV head, read once. Per SM a tile of 128 tokens
+// (32 KB) may take 1500 clocks at the memory's rate; 4 warpgroups work on 4 tiles at once, each alone on its
+// tile from the score MMAs to the value sums, so that the chain of a tile (two MMA round trips of 400-600
+// clocks, two barriers) is hidden by the other three. One producer warp keeps a ring of 4 or 5
+// tiles filled by bulk copies (whole 8 KB planes). Grid: one CTA per SM; the (sequence, row tile, head, tile) space is
+// cut into equal slices, so ragged batches and long single sequences load every SM alike. A unit that lies in one
+// slice is finished there; one that was cut leaves a partial record per slice, joined by q8_join_kernel.
+
+#include "tq_q8_attend.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kTile = 128;              // tokens of a tile
+constexpr int kStage = 2 * kTile * kD;  // its keys, then its values
+constexpr int kWg = 4;                  // warpgroups, each with a tile of its own
+constexpr int kConsumers = kWg * 128;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kRows = 16;               // rows of a unit = N of the MMAs
+constexpr int kTerm = kRows * 128;      // bytes of one 8-bit term of a Q or P operand
+constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launch
+constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
+
+constexpr int stages_of(int GR) { return GR == 1 ? 5 : 4; }
+constexpr int tmem_stride(int GR) { return 64 * GR; }  // columns of a warpgroup: S, then O of the two blocks
+
+struct Entries {
+  int pre[kEntries + 1];  // tiles (of one head) before each entry
+  int lo[kEntries];       // its first tile
+  int hi[kEntries];       // one past its last visible slot
+};
+
+// A row's key range: query token i of sequence b, whose length is len and whose query tokens number m.
+__device__ __forceinline__ int2 row_range(const Q8AttnArgs &a, int b, int i, int len, int m) {
+  if (i >= m) return make_int2(0, 0);
+  int beg = 0, end = len - m + i + 1;
+  if (a.kbeg) beg = max(0, __ldg(a.kbeg + (long long)b * a.n_q + i));
+  if (a.kend) end = __ldg(a.kend + (long long)b * a.n_q + i);
+  end = min(end, len);
+  return end > beg ? make_int2(beg, end) : make_int2(0, 0);
+}
+
+__device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, int *m, bool report) {
+  int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
+  if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
+  *len = min(max(n, 0), a.max_len);
+  *m = min(max(q, 0), a.n_q);
+}
+
+// What the main kernel tells the join about each CTA's last unit.
+struct Cut {
+  int b, rt, h, parts;  // parts: CTAs that hold a part of it, 0 when it was not cut (or began elsewhere)
+};
+
+struct Shared {
+  uint64_t full[5], empty[5], bar_s[kWg], bar_o[kWg];
+  float4 info[5];            // key scales of the tile's two blocks, value scales (negative: not mapped)
+  float qscale[kRows], slope[kRows];
+  int2 range[kRows];
+  int qpos[kRows];
+  float4 wmax[kWg][kRows];   // row maxima of a warpgroup's four warps
+  float m[kWg][kRows], l[kWg][kRows], lr[kWg][kRows];
+  float lw[kWg][4][kRows], lrw[kWg][4][kRows];
+  uint32_t tmem;
+  int bad, scan[kThreads / 32];
+  Entries ent;
+};
+
+__device__ __forceinline__ void bar_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
+__device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"(kConsumers) : "memory"); }
+
+template <int NR, int GR>
+__global__ void __launch_bounds__(kThreads, 1)
+q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, Cut *cuts) {
+  constexpr int kStages = stages_of(GR);
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Shared sm;
+  uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage, *pbuf = qbuf + GR * 3 * kTerm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, R = G * a.n_q;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 1);
+    for (int w = 0; w < kWg; ++w) mbar_init(&sm.bar_s[w], 1), mbar_init(&sm.bar_o[w], 1);
+    mbar_fence_init();
+    sm.bad = 0;
+  }
+  if (warp == kThreads / 32 - 1) {
+    tmem_alloc(smem_u32(&sm.tmem), kWg * tmem_stride(GR));
+    tmem_relinquish();
+  }
+  pdl_wait();
+
+  // ---- the entries' tiles: one thread each
+  const int E = nb * rts;
+  int count = 0;
+  if (tid < E) {
+    const int b = b0 + tid / rts, r0 = (tid % rts) * kRows;
+    int len, m;
+    seq_sizes(a, b, &len, &m, blockIdx.x == 0);
+    const int i0 = r0 / G, i1 = (min(R, r0 + kRows) - 1) / G;
+    int lo = 0x7fffffff, hi = 0;
+    for (int i = i0; i <= i1; ++i) {
+      const int2 r = row_range(a, b, i, len, m);
+      if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
+    }
+    if (hi == 0) lo = 0;
+    // an entry whose rows see nothing keeps one (empty) tile, so that its zeros are written
+    count = i0 < m ? max(1, (hi + kTile - 1) / kTile - lo / kTile) : 0;
+    sm.ent.lo[tid] = lo / kTile;
+    sm.ent.hi[tid] = hi;
+  }
+  {
+    int x = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sm.scan[warp] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += sm.scan[w];
+    if (tid < E) sm.ent.pre[tid + 1] = before + x;
+    if (tid == 0) sm.ent.pre[0] = 0;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  const long long total = (long long)sm.ent.pre[E] * a.heads_kv;
+  // slices, none of them empty: CTA c < slices has tiles [total c / slices, total (c + 1) / slices)
+  const long long slices = min((long long)gridDim.x, total);
+  const bool idle = blockIdx.x >= slices;
+  const long long g0 = idle ? 0 : total * blockIdx.x / slices, g1 = idle ? 0 : total * (blockIdx.x + 1) / slices;
+  auto locate = [&](long long g, int &e, int &h, int &t, int &cnt) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // the last entry that begins at or before g
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)sm.ent.pre[mid] * a.heads_kv <= g) lo = mid;
+      else hi = mid - 1;
+    }
+    e = lo;
+    cnt = sm.ent.pre[e + 1] - sm.ent.pre[e];
+    const long long in = g - (long long)sm.ent.pre[e] * a.heads_kv;
+    h = (int)(in / cnt);
+    t = (int)(in - (long long)h * cnt);
+  };
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*(volatile int *)&sm.bad) return;
+    if (!mbar_wait_bounded(bar, parity, a.error)) *(volatile int *)&sm.bad = 1;
+  };
+
+  if (warp == kThreads / 32 - 1) {
+    // ================================ producer: one lane finds the sources of one of the next 32 tiles
+    int it = 0;
+    for (long long g = g0; g < g1; g += 32) {
+      long long src[2] = {-1, -1};
+      float4 info = make_float4(-1.f, -1.f, -1.f, -1.f);
+      int bytes[2] = {0, 0};
+      if (g + lane < g1) {
+        int e, h, t, cnt;
+        locate(g + lane, e, h, t, cnt);
+        const int tok = (sm.ent.lo[e] + t) * kTile, n = min(kTile, max(0, sm.ent.hi[e] - tok));
+        const long long v = ((long long)(b0 + e / rts) * a.heads_kv + h) * a.c.nblk + tok / kQ8Block;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int m = min(kQ8Block, n - k * kQ8Block);
+          if (m <= 0) continue;
+          src[k] = q8_block(a.c.btab, a.c.pool_blocks, v + k, a.error);
+          if (src[k] < 0) continue;
+          bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
+          (k ? info.y : info.x) = __ldg(a.c.ks + src[k]);
+          (k ? info.w : info.z) = __ldg(a.c.vs + src[k]);
+        }
+      }
+      const int todo = (int)min(32ll, g1 - g);
+      for (int k = 0; k < todo; ++k, ++it) {
+        const int s = it % kStages;
+        const long long s0 = __shfl_sync(kFull, src[0], k), s1 = __shfl_sync(kFull, src[1], k);
+        const int n0 = __shfl_sync(kFull, bytes[0], k), n1 = __shfl_sync(kFull, bytes[1], k);
+        float4 f;
+        f.x = __shfl_sync(kFull, info.x, k), f.y = __shfl_sync(kFull, info.y, k);
+        f.z = __shfl_sync(kFull, info.z, k), f.w = __shfl_sync(kFull, info.w, k);
+        if (lane == 0) {
+          wait(&sm.empty[s], ((it / kStages) & 1) ^ 1);
+          if (!*(volatile int *)&sm.bad) {
+            sm.info[s] = f;
+            uint8_t *dst = ring + s * kStage;
+            mbar_arrive_expect_tx(&sm.full[s], 2 * (n0 + n1));
+            if (n0) {
+              const uint8_t *p = a.c.records + s0 * kQ8BlockBytes;
+              tma_load_1d(dst, p, n0, &sm.full[s]);
+              tma_load_1d(dst + kTile * kD, p + kQ8Plane, n0, &sm.full[s]);
+            }
+            if (n1) {
+              const uint8_t *p = a.c.records + s1 * kQ8BlockBytes;
+              tma_load_1d(dst + kQ8Plane, p, n1, &sm.full[s]);
+              tma_load_1d(dst + kTile * kD + kQ8Plane, p + kQ8Plane, n1, &sm.full[s]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // every copy lands before the CTA's shared memory goes: the last fill of each stage
+    if (lane == 0) {
+      for (int k = max(0, it - kStages); k < it; ++k)
+        mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, nullptr, kWaitBudgetNs / 8);
+    }
+    __syncwarp();
+  } else {
+    // ================================ consumers
+    const int wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
+    const uint32_t t_s = tmem + wg * tmem_stride(GR), t_o = t_s + 16 * GR;
+    const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+    uint8_t *const pmine = pbuf + wg * GR * 3 * kTerm;
+    uint8_t *const pbyte = pmine + (wt >> 4) * 128 + (wt & 15);
+    const uint32_t idesc_s[2] = {tc_idesc_f8(128, kRows, 0, 0, 0, 0), tc_idesc_f8(128, kRows, 0, 1, 0, 0)};
+    const uint32_t idesc_o[2] = {tc_idesc_f8(128, kRows, 0, 0, 1, 0), tc_idesc_f8(128, kRows, 0, 1, 1, 0)};
+    const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
+    uint32_t phase = 0;  // of this warpgroup's two barriers: its tiles so far
+    long long g = g0;
+    while (g < g1) {
+      int e, h, t0, cnt;
+      locate(g, e, h, t0, cnt);
+      const int b = b0 + e / rts, row0 = (e % rts) * kRows;
+      const long long end = min(g1, g - t0 + cnt);
+      const int first = sm.ent.lo[e], hi = sm.ent.hi[e];
+
+      // ---- the unit's queries: warp w prepares row w
+      {
+        const int row = row0 + warp, i = row / G, hq = h * G + row % G;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        int len, m;
+        seq_sizes(a, b, &len, &m, false);
+        const bool live = warp < NR && row < R && i < m;
+        if (live) {
+          const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
+          if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
+          else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
+          else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, __float_as_uint(x[k]) & 0x7fffffffu);
+        amax = __reduce_max_sync(kFull, amax);
+        const int ex = row_exponent(amax);
+        const float f = pow2i(-ex);
+        uint32_t w[GR][3];
+        if (amax >= 0x7f800000u) {  // an infinity or a NaN: the row's result is NaN
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) w[gr][k] = 0x7f7f7f7fu;
+        } else {
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = x[k] * f;
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) {
+            uint32_t lo[3], hi2[3];
+            split_terms(y[0], y[1], lo);
+            split_terms(y[2], y[3], hi2);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) w[gr][k] = lo[k] | (hi2[k] << 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] *= kGroupScale;
+          }
+        }
+        bar_all();  // everyone is done with the unit before
+        if (warp < NR) {
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              *reinterpret_cast<uint32_t *>(qbuf + (gr * 3 + k) * kTerm + q8_off(warp, 4 * lane)) = w[gr][k];
+          if (lane == 0) {
+            sm.qscale[warp] = pow2i(ex);
+            const int2 rg = live ? row_range(a, b, i, len, m) : make_int2(0, 0);
+            sm.range[warp] = rg;
+            sm.slope[warp] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+            sm.qpos[warp] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : len - m + i;
+          }
+        }
+        fence_proxy_async_shared();
+        bar_all();
+      }
+
+      float m[NR], l[NR], lr[NR], o[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) m[r] = -INFINITY, l[r] = 0.f, lr[r] = 0.f, o[r] = 0.f;
+
+      for (long long gt = g + ((wg - (int)(g - g0)) & (kWg - 1)); gt < end; gt += kWg) {
+        const int it = (int)(gt - g0), s = it % kStages;
+        const int tok0 = (first + t0 + (int)(gt - g)) * kTile, n = min(kTile, max(0, hi - tok0));
+        const uint32_t ring_k = smem_u32(ring + s * kStage), ring_v = ring_k + kTile * kD;
+        wait(&sm.full[s], (it / kStages) & 1);
+        if (wt == 0) {
+          tc_fence_after_sync();
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              const uint32_t q = smem_u32(qbuf + (gr * 3 + k) * kTerm);
+#pragma unroll
+              for (int ks = 0; ks < kD / 32; ++ks)
+                tc_mma_f8(t_s + 16 * gr, tc_sdesc_kmajor(ring_k + 256 * ks, 128, 1024),
+                          tc_sdesc_kmajor(q + 256 * ks, 128, 1024), idesc_s[k == 2], k > 0 || ks > 0);
+            }
+          tc_commit(smem_u32(&sm.bar_s[wg]));
+        }
+        const float4 info = sm.info[s];
+        const float ks = wt < kQ8Block ? info.x : info.y;
+        // value rows of the last K-step past the copied tokens hold whatever the cache holds there
+        if (wt >= n && wt < ((n + 31) & ~31)) {
+          uint8_t *row = ring + s * kStage + kTile * kD + q8_off(wt, 0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + 128 * c) = make_uint4(0, 0, 0, 0);
+        }
+        const int slot = tok0 + wt;
+        int kp = slot;
+        if (a.kpos && slot < hi) kp = __ldg(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
+        wait(&sm.bar_s[wg], phase & 1);
+        tc_fence_after_sync();
+        float t[NR];
+        tmem_ld_cols<NR>(t_s + lanes, t);
+        if constexpr (GR == 2) {
+          float t2[NR];
+          tmem_ld_cols<NR>(t_s + 16 + lanes, t2);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) t[r] = fmaf(t2[r], 1.f / kGroupScale, t[r]);
+        }
+        // ---- scores, and the rows' maxima over the tile
+        float mine = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const int2 rg = sm.range[r];
+          t[r] = q8_score_log2(t[r] * (sm.qscale[r] * ks), sc);
+          if (a.slopes) t[r] = fmaf(-sm.slope[r], (float)__sad(sm.qpos[r], kp, 0u), t[r]);
+          if (slot < rg.x || slot >= rg.y || ks < 0.f) t[r] = -INFINITY;
+          const float w = warp_fmax(t[r]);
+          if (lane == r) mine = w;
+        }
+        if (lane < NR) reinterpret_cast<float *>(&sm.wmax[wg][lane])[w4] = mine;
+        bar_wg(wg);
+        // ---- probabilities (times 2^8), their terms, the sums
+        float corr_any[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float4 x = sm.wmax[wg][r];
+          const float top = fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), m[r]);
+          const float use = top == -INFINITY ? 0.f : top;
+          const float corr = ex2_approx(m[r] - use);
+          m[r] = top;
+          t[r] = ex2_approx(t[r] - use + 8.f);
+          l[r] = fmaf(l[r], corr, t[r]);
+          lr[r] *= corr;
+          o[r] *= corr;
+          corr_any[r] = t[r];
+        }
+#pragma unroll
+        for (int r = 0; r < NR; r += 2) {
+          float p0 = t[r], p1 = r + 1 < NR ? t[r + 1 < NR ? r + 1 : r] : 0.f;
+          uint8_t *at = pbyte + (r >> 3) * 1024 + (r & 7) * 16;
+          float left = 1.f;
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) {
+            uint32_t term[3];
+            split_terms(p0, p1, term);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              at[(gr * 3 + k) * kTerm] = (uint8_t)term[k];
+              if (r + 1 < NR) at[(gr * 3 + k) * kTerm + 16] = (uint8_t)(term[k] >> 8);
+            }
+            if (gr + 1 < GR) p0 *= kGroupScale, p1 *= kGroupScale, left = 1.f / kGroupScale;
+          }
+          // what the terms add up to
+          lr[r] += corr_any[r] - p0 * left;
+          if (r + 1 < NR) lr[r + 1 < NR ? r + 1 : r] += corr_any[r + 1 < NR ? r + 1 : r] - p1 * left;
+        }
+        fence_proxy_async_shared();
+        tc_fence_before_sync();
+        bar_wg(wg);
+        const bool use0 = info.z >= 0.f, use1 = info.w >= 0.f;  // the blocks that were copied
+        if (wt == 0) {
+          tc_fence_after_sync();
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk) {
+            if (!(blk ? use1 : use0)) continue;
+            const int steps = min(2, (n - blk * kQ8Block + 31) / 32);
+            for (int gr = 0; gr < GR; ++gr)
+              for (int k = 0; k < 3; ++k) {
+                const uint32_t p = smem_u32(pmine + (gr * 3 + k) * kTerm) + blk * 512;
+                for (int st = 0; st < steps; ++st)
+                  tc_mma_f8(t_o + (blk * GR + gr) * 16, tc_sdesc_kmajor(ring_v + blk * kQ8Plane + st * 4096, 1024, 128),
+                            tc_sdesc_kmajor(p + 256 * st, 128, 1024), idesc_o[k == 2], k > 0 || st > 0);
+              }
+          }
+          tc_commit(smem_u32(&sm.empty[s]));
+          tc_commit(smem_u32(&sm.bar_o[wg]));
+        }
+        wait(&sm.bar_o[wg], phase & 1);
+        tc_fence_after_sync();
+        ++phase;
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          if (!(blk ? use1 : use0)) continue;
+          const float vs = blk ? info.w : info.z;
+          float d[NR];
+          tmem_ld_cols<NR>(t_o + blk * GR * 16 + lanes, d);
+          if constexpr (GR == 2) {
+            float d2[NR];
+            tmem_ld_cols<NR>(t_o + (blk * GR + 1) * 16 + lanes, d2);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) d[r] = fmaf(d2[r], 1.f / kGroupScale, d[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) o[r] = fmaf(d[r], vs, o[r]);
+        }
+        tc_fence_before_sync();
+      }
+
+      // ---- join the four warpgroups (thread = coordinate of O)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float x = warp_sum(l[r]), y = warp_sum(lr[r]);
+        if (lane == 0) sm.lw[wg][w4][r] = x, sm.lrw[wg][w4][r] = y;
+      }
+      if (wt == 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) sm.m[wg][r] = m[r];
+      }
+      bar_all();
+      if (wt < NR) {
+        sm.l[wg][wt] = sm.lw[wg][0][wt] + sm.lw[wg][1][wt] + sm.lw[wg][2][wt] + sm.lw[wg][3][wt];
+        sm.lr[wg][wt] = sm.lrw[wg][0][wt] + sm.lrw[wg][1][wt] + sm.lrw[wg][2][wt] + sm.lrw[wg][3][wt];
+      }
+      float *mix = reinterpret_cast<float *>(pbuf);  // [kWg - 1][NR][128]; every MMA that read the terms is done
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+        const float f = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - top);
+        o[r] *= f;
+        if (wg) mix[((wg - 1) * NR + r) * 128 + wt] = o[r];
+      }
+      bar_all();
+      if (wg == 0) {
+        const bool whole = t0 == 0 && end == g + cnt;
+        float *part = a.parts + ((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRows * kPartRow;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+          float x = o[r], sl = 0.f, slr = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWg; ++w) {
+            const float mw = sm.m[w][r], f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
+            // a warpgroup without a maximum adds 0, or the NaN of a row whose query is not finite
+            sl = fmaf(sm.l[w][r], mw == -INFINITY && sm.l[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), sl);
+            slr = fmaf(sm.lr[w][r], mw == -INFINITY && sm.lr[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), slr);
+            if (w) x += mix[((w - 1) * NR + r) * 128 + wt];
+          }
+          const int row = row0 + r, i = row / G;
+          int len, mm;
+          seq_sizes(a, b, &len, &mm, false);
+          if (row >= R || i >= mm) continue;
+          if (whole) {
+            const int hq = h * G + row % G;
+            const float y = slr == 0.f ? 0.f : x / slr;
+            const long long off = b * a.os.b + hq * a.os.h + i * a.os.t + wt;
+            if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
+            else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
+            else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
+            if (a.lse && wt == 0)
+              a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (top + log2f(sl) - 8.f) * kLn2;
+          } else {
+            part[r * kPartRow + wt] = x;
+            if (wt == 0) {
+              part[r * kPartRow + kD] = top;
+              part[r * kPartRow + kD + 1] = sl;
+              part[r * kPartRow + kD + 2] = slr;
+            }
+          }
+        }
+        if (wt == 0 && end == g1) {
+          // the CTA's last unit: if it goes on beyond this slice and began in it, the join starts here
+          const long long stop = g - t0 + cnt;
+          int parts = 0;
+          if (t0 == 0 && stop > g1) {
+            parts = 1;
+            for (long long c = blockIdx.x + 1; c < slices && total * c / slices < stop; ++c) ++parts;
+          }
+          cuts[blockIdx.x] = Cut{b, e % rts, h, parts};
+        }
+      }
+      g = end;
+    }
+    if (tid == 0 && g0 >= g1) cuts[blockIdx.x] = Cut{0, 0, 0, 0};
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kThreads / 32 - 1) tmem_dealloc(tmem, kWg * tmem_stride(GR));
+}
+
+// One CTA per (CTA of the main kernel, row): the parts of the unit that was cut there. Four groups of
+// 128 threads (thread = coordinate) take every fourth part; its maximum, sums and O are joined in shared memory.
+__global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8AttnArgs a, const Cut *cuts) {
+  __shared__ float so[4][kD], sl[4], slr[4], stop[4];
+  pdl_wait();
+  const Cut cut = cuts[blockIdx.x];
+  const int r = blockIdx.y, row = cut.rt * kRows + r, G = a.group;
+  if (cut.parts < 2 || row >= G * a.n_q) return;
+  int len, m;
+  seq_sizes(a, cut.b, &len, &m, false);
+  const int i = row / G;
+  if (i >= m) return;
+  const int d = threadIdx.x & 127, grp = threadIdx.x >> 7;
+  auto rec = [&](int p) {
+    return a.parts + (((long long)blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * kRows * kPartRow + r * kPartRow;
+  };
+  float top = -INFINITY;
+  for (int p = grp; p < cut.parts; p += 4) top = fmaxf(top, rec(p)[kD]);
+  if (d == 0) stop[grp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(stop[0], stop[1]), fmaxf(stop[2], stop[3]));
+  float o = 0.f, l = 0.f, lr = 0.f;
+#pragma unroll 4
+  for (int p = grp; p < cut.parts; p += 4) {
+    const float *x = rec(p);
+    const float f = x[kD] == -INFINITY ? 1.f : ex2_approx(x[kD] - top);  // without a maximum: zeros (or NaN)
+    o = fmaf(x[d], f, o);
+    l = fmaf(x[kD + 1], f, l);
+    lr = fmaf(x[kD + 2], f, lr);
+  }
+  so[grp][d] = o;
+  if (d == 0) sl[grp] = l, slr[grp] = lr;
+  __syncthreads();
+  if (grp) return;
+  o = so[0][d] + so[1][d] + so[2][d] + so[3][d];
+  l = sl[0] + sl[1] + sl[2] + sl[3];
+  lr = slr[0] + slr[1] + slr[2] + slr[3];
+  const int hq = cut.h * G + row % G;
+  const float y = lr == 0.f ? 0.f : o / lr;
+  const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + d;
+  if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
+  else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
+  else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
+  if (a.lse && d == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
+}
+
+template <int NR, int GR>
+int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rts, int num_sms, cudaStream_t st) {
+  constexpr int smem = stages_of(GR) * kStage + GR * 3 * kTerm * (1 + kWg);
+  if (cudaFuncSetAttribute(q8_attend_kernel<NR, GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  if (launch_overlapped(true, q8_attend_kernel<NR, GR>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rts, cuts) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  if (launch_overlapped(true, q8_join_kernel, dim3(num_sms, NR), dim3(512), 0, st, a, (const Cut *)cuts) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  return TQ_OK;
+}
+
+}  // namespace
+
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
+  (void)max_len, (void)heads_kv;
+  size_t cuts = (size_t)num_sms * sizeof(Cut);
+  cuts = (cuts + 15) / 16 * 16;
+  const size_t parts = (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
+  const size_t lse = weights ? ((size_t)batch * heads_q * n_q * sizeof(float) + 15) / 16 * 16 : 0;
+  return cuts + parts + lse;
+}
+
+int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  Q8AttnArgs a = args;
+  Cut *cuts = (Cut *)workspace;
+  char *p = (char *)workspace + ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16;
+  a.parts = (float *)p;
+  p += (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
+  if (a.weights && !a.lse) a.lse = (float *)p;
+  const long long R = (long long)a.group * a.n_q;
+  const int rts = (int)((R + kRows - 1) / kRows);
+  if (rts > kEntries || a.weights) return TQ_ERR_UNSUPPORTED;
+  const int per = kEntries / rts;  // sequences of a launch
+  for (int b0 = 0; b0 < a.batch; b0 += per) {
+    const int nb = a.batch - b0 < per ? a.batch - b0 : per;
+    int s;
+    if (a.out_dtype == TQ_F32)
+      s = R == 1 ? launch_rows<1, 2>(a, cuts, b0, nb, rts, num_sms, st)
+          : R <= 4 ? launch_rows<4, 2>(a, cuts, b0, nb, rts, num_sms, st)
+          : R <= 8 ? launch_rows<8, 2>(a, cuts, b0, nb, rts, num_sms, st)
+                   : launch_rows<16, 2>(a, cuts, b0, nb, rts, num_sms, st);
+    else
+      s = R == 1 ? launch_rows<1, 1>(a, cuts, b0, nb, rts, num_sms, st)
+          : R <= 4 ? launch_rows<4, 1>(a, cuts, b0, nb, rts, num_sms, st)
+          : R <= 8 ? launch_rows<8, 1>(a, cuts, b0, nb, rts, num_sms, st)
+                   : launch_rows<16, 1>(a, cuts, b0, nb, rts, num_sms, st);
+    if (s != TQ_OK) return s;
+  }
+  return TQ_OK;
+}
+
+}  // namespace tq

@@ -1,0 +1,106 @@
+// Device code shared by the attention kernels of the 8-bit cache: tensor-core issue on e4m3 / e5m2
+// operands, the expansion of a number into 8-bit terms, and the score of one (query, key) pair.
+//
+// The cache's codes go to the tensor cores as they lie (tcgen05.mma kind::f8f6f4: fp8 products are
+// exact, sums are fp32). The other operand, queries and probabilities, is a sum of 8-bit terms on one
+// scale: x = t0 + t1 + t2 + r, t0 and t1 the e4m3 numbers nearest to what is left (4 significant bits
+// each), t2 the nearest e5m2 number (3 bits, and 2^-16 as its smallest step where e4m3 ends at 2^-9).
+// With the largest magnitude of a row in [128, 256) -- queries by a power of two of their own,
+// probabilities by 2^8 -- |r| <= 2^-11 |x| for |x| >= 2^-2 and <= 2^-13 below (t1 then has its smallest
+// step, 2^-9); bf16 and fp16 queries come out exact but for such small coordinates. Each term is
+// one more pass over the same accumulator. A second group of three terms, of 2^11 r, accumulates apart
+// for results that keep 32 bits.
+#pragma once
+
+#include "tq_q8.cuh"
+#include "tq_tcgen05.cuh"
+
+namespace tq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGroupScale = 2048.f;  // 2^11: the second group holds kGroupScale * r
+
+// Instruction descriptor of kind::f8f6f4, fp32 accumulate: A e4m3, B e4m3 (0) or e5m2 (1); `a_mn`, `b_mn`: the
+// operand is MN-major. Fields as in tc_idesc_f16_f32, formats 0 = e4m3, 1 = e5m2.
+__host__ __device__ constexpr uint32_t tc_idesc_f8(int M, int N, int a_fmt, int b_fmt, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D (TMEM) (+)= A (shared) x B (shared) of 8-bit operands, 32 K-elements; issued by one thread.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// N consecutive columns of this thread's lane, without the wait (tmem_ld_wait follows, then use)
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&f)[N]) {
+  uint32_t v[N];
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]) : "r"(taddr) : "memory");
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(taddr) : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        : "r"(taddr) : "memory");
+  } else {
+    static_assert(N == 16, "");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr) : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// The three terms of (a, b), each a pair of bytes (a's low); a and b become what is left.
+__device__ __forceinline__ void split_terms(float &a, float &b, uint32_t (&term)[3]) {
+  term[0] = cvt_e4m3x2(a, b);
+  float2 f = e4m3x2_f(term[0]);
+  a -= f.x, b -= f.y;
+  term[1] = cvt_e4m3x2(a, b);
+  f = e4m3x2_f(term[1]);
+  a -= f.x, b -= f.y;
+  term[2] = cvt_e5m2x2(a, b);
+  f = e5m2x2_f(term[2]);
+  a -= f.x, b -= f.y;
+}
+
+__device__ __forceinline__ float warp_fmax(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A row's power of two: |x| 2^-e in [128, 256) for its largest |x|; and what undoes it.
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23) - 127 - 7;
+  return max(e, -120);
+}
+
+// log2(e) times the scaled and capped product q.k (the bias comes on top).
+struct Q8Score {
+  float scale, softcap, inv_cap;  // softcap 0: none
+};
+__device__ __forceinline__ float q8_score_log2(float qk, const Q8Score &s) {
+  float x = qk * s.scale;
+  if (s.softcap != 0.f) x = s.softcap * tanhf(x * s.inv_cap);
+  return x * kLog2e;
+}
+
+}  // namespace tq

@@ -1,0 +1,240 @@
+// Eviction from the 8-bit cache by accumulated attention weight (tq_q8_evict): per sequence and KV
+// head keep the first `sink`, the last `recent` and the heaviest of the other tokens, in order, in
+// another cache.
+//
+// q8_select_kernel: weights map to unsigned keys of the same order (NaN lowest); the key of the last
+// token that stays is found digit by digit (11, 11 and 10 bits, from the top) with a histogram of the
+// keys that share the digits found so far; ties at that key go to the lowest slots, and one scan gives
+// every kept slot its place. Keys are read once from memory and stay in shared memory (what does not
+// fit is read again). A cluster of up to 8 CTAs shares one long sequence-head: each holds a run of
+// slots, histograms and counts are added through distributed shared memory.
+// q8_gather_kernel: one CTA per 64-token block of the target and tensor. A thread owns one 16-byte piece (16
+// coordinates of one token); the new block's scale comes from the largest value, and codes are rounded
+// only where their block's scale differs from it. Both bound by memory.
+
+#include <cooperative_groups.h>
+
+#include "tq_q8.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace tq {
+namespace {
+
+constexpr int kSel = 1024;             // threads of a selecting CTA
+constexpr int kBins = 2048;
+constexpr int kSelKeys = 45056;        // keys held in shared memory (176 KB)
+constexpr uint32_t kAlways = 0xffffffffu;  // a slot that stays whatever its weight
+
+// order-preserving key: larger weight, larger key; -0 = +0, NaN below everything; never kAlways
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const uint32_t u = __float_as_uint(w + 0.f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// exclusive prefix sum over the CTA; *total receives the sum (all threads call)
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  const int before = warp ? warp_sums[warp - 1] : 0;
+  __syncthreads();
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__ Q8EvictArgs a) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[kBins];
+  __shared__ int sums[32], found[2], share[2];
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int bh = blockIdx.x / ranks, b = bh / a.heads;
+  int n = __ldg(a.seq_lens + b);
+  if (n < 0 || n > a.src.capacity) {
+    if (tid == 0) set_error(a.error, TQ_ERR_ARG);
+    n = n < 0 ? 0 : a.src.capacity;
+  }
+  const int m = min(n, a.keep);
+  const float *w = a.weights + (long long)bh * a.src.capacity;
+  const int32_t *pos = a.positions ? a.positions + (long long)bh * a.src.capacity : nullptr;
+  int32_t *kept = a.kept + (long long)bh * a.keep;
+  float *dw = a.dst_weights ? a.dst_weights + (long long)bh * a.dst.capacity : nullptr;
+  int32_t *dp = a.dst_positions ? a.dst_positions + (long long)bh * a.dst.capacity : nullptr;
+  if (rank == 0 && tid == 0 && bh % a.heads == 0) a.dst_lens[b] = m;
+
+  // this CTA's run of slots
+  const int run = (n + ranks - 1) / ranks;
+  const int s0 = min(n, rank * run), cnt = min(n, s0 + run) - s0;
+  int pick = n > a.keep ? a.keep - a.sink - a.recent : 0;  // tokens chosen by weight
+  auto make = [&](int i) -> uint32_t {
+    const int s = s0 + i;
+    if (n <= a.keep || s < a.sink || s >= n - a.recent) return kAlways;
+    return weight_key(__ldg(w + s));
+  };
+  auto key = [&](int i) -> uint32_t { return i < kSelKeys ? keys[i] : make(i); };
+  for (int i = tid; i < min(cnt, kSelKeys); i += kSel) keys[i] = make(i);
+  __syncthreads();  // the runs below cross threads, also where nothing is chosen by weight
+
+  uint32_t prefix = 0, mask = 0;  // the digits of the threshold found so far
+  int need = pick;                // tokens still to choose among the keys with these digits
+  if (pick > 0) {                 // the same for every CTA of the cluster
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      hist[tid] = 0, hist[tid + kSel] = 0;
+      __syncthreads();
+      for (int i = tid; i < cnt; i += kSel) {
+        const uint32_t k = key(i);
+        if (k != kAlways && ((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> shift) & digit], 1);
+      }
+      cl.sync();
+      // bins in falling order: thread t sums bins 2047 - 2t and 2046 - 2t over the cluster
+      int hi = 0, lo = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const int *other = cl.map_shared_rank(hist, r);
+        hi += other[kBins - 1 - 2 * tid];
+        lo += other[kBins - 2 - 2 * tid];
+      }
+      int total;
+      const int above = block_scan(hi + lo, sums, &total);
+      if (above < need && need <= above + hi) found[0] = kBins - 1 - 2 * tid, found[1] = need - above;
+      else if (above + hi < need && need <= above + hi + lo) found[0] = kBins - 2 - 2 * tid, found[1] = need - above - hi;
+      cl.sync();  // also: every CTA has read the histograms
+      prefix |= (uint32_t)found[0] << shift;
+      mask |= digit << shift;
+      need = found[1];
+      __syncthreads();
+    }
+  }
+  // a thread's keys are a run of the CTA's; an odd length keeps the shared reads free of conflicts
+  const int per = ((cnt + kSel - 1) / kSel) | 1;
+  const int i0 = min(cnt, tid * per), i1 = min(cnt, i0 + per);
+  int more = 0, ties = 0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    more += (k == kAlways || (pick > 0 && k > prefix)) ? 1 : 0;
+    ties += (pick > 0 && k != kAlways && k == prefix) ? 1 : 0;
+  }
+  int all_ties;
+  int tie = block_scan(ties, sums, &all_ties);
+  if (tid == 0) share[0] = all_ties;
+  cl.sync();
+  for (int r = 0; r < rank; ++r) tie += *cl.map_shared_rank(&share[0], r);
+  const int won = max(0, min(ties, need - tie));  // of this thread's ties, the lowest slots
+  int all_kept;
+  int at = block_scan(more + (pick > 0 ? won : 0), sums, &all_kept);
+  if (tid == 0) share[1] = all_kept;
+  cl.sync();
+  for (int r = 0; r < rank; ++r) at += *cl.map_shared_rank(&share[1], r);
+  int left = pick > 0 ? won : 0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    bool stay = k == kAlways || (pick > 0 && k > prefix);
+    if (!stay && pick > 0 && k == prefix && left > 0) stay = true, --left;
+    if (stay && at < a.keep) {
+      const int s = s0 + i;
+      kept[at] = s;
+      if (dw) dw[at] = __ldg(w + s);
+      if (dp) dp[at] = pos ? __ldg(pos + s) : s;
+      ++at;
+    }
+  }
+  const int me = rank * kSel + tid, everyone = ranks * kSel;
+  for (int i = m + me; i < a.keep; i += everyone) kept[i] = -1;
+  for (int i = m + me; i < a.dst.capacity; i += everyone) {
+    if (dw) dw[i] = 0.f;
+    if (dp) dp[i] = 0;
+  }
+  cl.sync();  // no CTA leaves while another may read its shared memory
+}
+
+constexpr int kGather = kQ8Block * 8;
+
+__global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constant__ Q8EvictArgs a) {
+  __shared__ uint32_t red[kGather / 32];
+  const int tid = threadIdx.x, c = tid & 7, t = tid >> 3;
+  const int j = blockIdx.x, tensor = blockIdx.z;
+  const long long bh = blockIdx.y;
+  const int i = j * kQ8Block + t;
+  const int s = i < a.keep ? __ldg(a.kept + bh * a.keep + i) : -1;
+  uint4 w = make_uint4(0, 0, 0, 0);
+  int e0 = kQ8MinExp;
+  if (s >= 0 && s < a.src.capacity) {
+    const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
+    if (from >= 0) {
+      w = *reinterpret_cast<const uint4 *>(a.src.records + from * kQ8BlockBytes + tensor * kQ8Plane +
+                                           q8_off(s % kQ8Block, 16 * c));
+      e0 = log2i((tensor ? a.src.vs : a.src.ks)[from]);
+    }
+  }
+  // the largest magnitude of the piece: e4m3 magnitudes are ordered as their low seven bits
+  uint32_t top = __vmaxu4(__vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu));
+  top = __vmaxu4(top, top >> 16);
+  top = max(top & 0xffu, (top >> 8) & 0xffu);
+  uint32_t amax = __float_as_uint(e4m3x2_f(top).x * pow2i(e0));
+  amax = __reduce_max_sync(kFull, amax);
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kGather / 32; ++k) amax = max(amax, red[k]);
+  const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
+  if (to < 0) return;
+  const int e = q8_exponent(amax);
+  if (e != e0) {
+    const float f = pow2i(min(max(e0 - e, -126), 126));
+    w = make_uint4(e4m3x4_scaled(w.x, f), e4m3x4_scaled(w.y, f), e4m3x4_scaled(w.z, f), e4m3x4_scaled(w.w, f));
+  }
+  *reinterpret_cast<uint4 *>(a.dst.records + to * kQ8BlockBytes + tensor * kQ8Plane + q8_off(t, 16 * c)) = w;
+  if (tid == 0) (tensor ? a.dst.vs : a.dst.ks)[to] = pow2i(e);
+}
+
+}  // namespace
+
+int launch_q8_evict(const Q8EvictArgs &a, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  const long long bh = (long long)a.batch * a.heads;
+  if (bh > 65535) return TQ_ERR_UNSUPPORTED;
+  // CTAs per sequence-head: one up to 8192 slots (a pass over them is then a few microseconds), up to 8 beyond
+  int ranks = 1;
+  while (ranks < 8 && a.src.capacity > 8192 * ranks) ranks *= 2;
+  const int held = (a.src.capacity + ranks - 1) / ranks;
+  const size_t smem = sizeof(uint32_t) * (size_t)(held < kSelKeys ? held : kSelKeys);
+  if (cudaFuncSetAttribute(q8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(bh * ranks));
+  cfg.blockDim = dim3(kSel);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, q8_select_kernel, a) != cudaSuccess) return TQ_ERR_CUDA;
+  const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
+  q8_gather_kernel<<<dim3((unsigned)blocks, (unsigned)bh, 2), kGather, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+}  // namespace tq

@@ -1,0 +1,209 @@
+// Host side of the 8-bit cache (TQ_SCHEME_Q8) and of rotary positions: argument checks, the
+// rotation's frequencies, dispatch to the launchers.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "tq_q8.h"
+#include "tq_q8_host.h"
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+int size_of(int dtype) { return dtype == TQ_F32 ? 4 : 2; }
+
+bool known(int dtype) { return dtype == TQ_F32 || dtype == TQ_BF16 || dtype == TQ_F16; }
+
+// strides in elements of `dtype`: every row a multiple of 16 bytes away
+bool strides_ok(const int64_t *s, int dtype) {
+  for (int i = 0; i < 3; ++i)
+    if ((s[i] * size_of(dtype)) % 16) return false;
+  return true;
+}
+
+// distinct rows lie apart (a target is never broadcast)
+bool spread(const int64_t *s, int batch, int heads, int n) {
+  return (batch == 1 || s[0]) && (heads == 1 || s[1]) && (n == 1 || s[2]);
+}
+
+tq::Q8Strides strides(const int64_t *s) { return tq::Q8Strides{s[0], s[1], s[2]}; }
+
+tq_status on_device(const tq_ctx *ctx) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return TQ_ERR_CUDA;
+  return cur == ctx->device ? TQ_OK : TQ_ERR_ARG;
+}
+
+// [p, p + n) and [q, q + m) share a byte
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + m && b < a + n;
+}
+
+}  // namespace
+
+namespace tq {
+
+tq_status q8_check_cache(const tq_ctx *ctx, const tq_cache *c, int batch, int heads_kv) {
+  if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
+  if (!c || c->batch != batch || c->heads_kv != heads_kv || c->capacity <= 0) return TQ_ERR_ARG;
+  if (!c->records || !c->k_stats || !c->v_stats) return TQ_ERR_ARG;
+  if (!aligned16(c->records) || !aligned16(c->k_stats) || !aligned16(c->v_stats)) return TQ_ERR_ALIGN;
+  if (c->block_table && c->pool_blocks <= 0) return TQ_ERR_ARG;
+  return TQ_OK;
+}
+
+Q8Cache q8_cache(const tq_cache *c) {
+  return Q8Cache{c->records, (float *)c->k_stats, (float *)c->v_stats, c->block_table, c->pool_blocks,
+                 q8_blocks_of(c->capacity), c->capacity};
+}
+
+void q8_cache_sizes(int batch, int heads_kv, int capacity, tq_cache_sizes *out) {
+  const size_t blocks = (size_t)batch * heads_kv * q8_blocks_of(capacity);
+  out->block_bytes = kQ8BlockBytes;
+  out->records = blocks * kQ8BlockBytes;
+  out->k_stats = out->v_stats = blocks * sizeof(float);
+  out->record_bytes = 2 * kD;
+}
+
+}  // namespace tq
+
+extern "C" {
+
+tq_status tq_set_rope(tq_ctx *ctx, const tq_rope *r) {
+  if (!ctx || !r) return TQ_ERR_ARG;
+  if (r->dim < 8 || r->dim > ctx->d || r->dim % 8) return TQ_ERR_ARG;
+  if (!(r->base > 1.0) || !std::isfinite(r->base) || !(r->factor >= 1.0) || !std::isfinite(r->factor) ||
+      !(r->gain > 0.0) || !std::isfinite(r->gain) || !std::isfinite(r->low) || !std::isfinite(r->high))
+    return TQ_ERR_ARG;
+  const bool even = r->low == 0.0 && r->high == 0.0;  // every pair divided by the factor
+  if (r->factor > 1.0 && !even && (!(r->original_len > 0.0) || !std::isfinite(r->original_len) || !(r->high > r->low)))
+    return TQ_ERR_ARG;
+  tq::RopeTable t;
+  t.dim = r->dim;
+  t.interleaved = r->interleaved ? 1 : 0;
+  t.gain = (float)r->gain;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < r->dim / 2; ++i) {
+    double f = std::pow(r->base, -2.0 * i / r->dim);
+    if (r->factor > 1.0) {
+      double keep = 0.0;
+      if (!even) {
+        keep = (r->original_len * f / two_pi - r->low) / (r->high - r->low);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      }
+      f = (1.0 - keep) * f / r->factor + keep * f;
+    }
+    t.freq[i] = (unsigned long long)std::llrint(std::ldexp(f / two_pi, 63)) * 2ull;  // f <= 1 rad: below 2^62
+  }
+  ctx->rope = t;
+  return TQ_OK;
+}
+
+tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides, void *d_y, const int64_t *y_strides,
+                    int dtype, int batch, int heads, int n, const int32_t *d_positions, int transpose, void *stream) {
+  if (!ctx || !d_x || !d_y || !x_strides || !y_strides || !d_positions) return TQ_ERR_ARG;
+  if (!known(dtype) || batch <= 0 || heads <= 0 || n < 0 || (transpose != 0 && transpose != 1)) return TQ_ERR_ARG;
+  if (!ctx->rope.dim) return TQ_ERR_STATE;
+  if (!aligned16(d_x) || !aligned16(d_y) || !strides_ok(x_strides, dtype) || !strides_ok(y_strides, dtype))
+    return TQ_ERR_ALIGN;
+  if (!spread(y_strides, batch, heads, n)) return TQ_ERR_ARG;
+  if (d_x == d_y && std::memcmp(x_strides, y_strides, 3 * sizeof(int64_t))) return TQ_ERR_ARG;
+  const tq_status s = on_device(ctx);
+  if (s != TQ_OK) return s;
+  if (n == 0) return TQ_OK;
+  const tq::RotaryArgs a{d_x, d_y, strides(x_strides), strides(y_strides), dtype, batch, heads, n, transpose,
+                         d_positions, ctx->rope};
+  return (tq_status)tq::launch_rotary(a, ctx->num_sms, stream);
+}
+
+tq_status tq_q8_append(const tq_ctx *ctx, const tq_cache *cache, const void *d_k, const int64_t *k_strides,
+                       const void *d_v, const int64_t *v_strides, int dtype, int batch, int heads_kv, int n_new,
+                       const int32_t *d_seq_lens, const int32_t *d_new_lens, int rope, const int32_t *d_positions,
+                       void *stream) {
+  if (!ctx || !d_k || !d_v || !k_strides || !v_strides || !d_seq_lens) return TQ_ERR_ARG;
+  if (!known(dtype) || batch <= 0 || heads_kv <= 0 || n_new < 0 || (rope != 0 && rope != 1)) return TQ_ERR_ARG;
+  tq_status s = tq::q8_check_cache(ctx, cache, batch, heads_kv);
+  if (s != TQ_OK) return s;
+  if (rope && !ctx->rope.dim) return TQ_ERR_STATE;
+  if (!aligned16(d_k) || !aligned16(d_v) || !strides_ok(k_strides, dtype) || !strides_ok(v_strides, dtype))
+    return TQ_ERR_ALIGN;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  if (n_new == 0) return TQ_OK;
+  const tq::Q8AppendArgs a{tq::q8_cache(cache), d_k, d_v, strides(k_strides), strides(v_strides), dtype, batch, heads_kv,
+                           n_new, rope, d_seq_lens, d_new_lens, d_positions, &ctx->dparams->error, ctx->rope};
+  return (tq_status)tq::launch_q8_append(a, ctx->num_sms, stream);
+}
+
+tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
+                                    int weights, size_t *out) {
+  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || max_len <= 0)
+    return TQ_ERR_ARG;
+  if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
+  *out = tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q, max_len, weights);
+  return TQ_OK;
+}
+
+tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *p, void *d_workspace,
+                          size_t ws_bytes, void *stream) {
+  if (!ctx || !p || !p->d_q || !p->d_out || !p->d_seq_lens || !d_workspace) return TQ_ERR_ARG;
+  if (p->batch <= 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->heads_q % p->heads_kv || p->n_q <= 0 || p->max_len <= 0)
+    return TQ_ERR_ARG;
+  if (!known(p->q_dtype) || (p->out_dtype != p->q_dtype && p->out_dtype != TQ_F32)) return TQ_ERR_ARG;
+  if (!std::isfinite(p->scale) || !std::isfinite(p->softcap) || p->softcap < 0.f) return TQ_ERR_ARG;
+  if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
+  if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
+  tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
+  if (s != TQ_OK) return s;
+  if (p->max_len > cache->capacity) return TQ_ERR_ARG;
+  if (!aligned16(p->d_q) || !aligned16(p->d_out) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
+      !strides_ok(p->out_strides, p->out_dtype))
+    return TQ_ERR_ALIGN;
+  size_t need = 0;
+  s = tq_q8_attention_workspace(ctx, p->batch, p->heads_q, p->heads_kv, p->n_q, p->max_len, p->d_weights != nullptr, &need);
+  if (s != TQ_OK) return s;
+  if (ws_bytes < need) return TQ_ERR_WORKSPACE;
+  if (!spread(p->out_strides, p->batch, p->heads_q, p->n_q)) return TQ_ERR_ARG;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  tq::Q8AttnArgs a{};
+  a.c = tq::q8_cache(cache);
+  a.batch = p->batch, a.heads_q = p->heads_q, a.heads_kv = p->heads_kv, a.group = p->heads_q / p->heads_kv;
+  a.n_q = p->n_q, a.max_len = p->max_len, a.q_dtype = p->q_dtype, a.out_dtype = p->out_dtype;
+  a.q = p->d_q, a.out = p->d_out, a.qs = strides(p->q_strides), a.os = strides(p->out_strides);
+  a.seq_lens = p->d_seq_lens, a.new_lens = p->d_new_lens;
+  a.scale = p->scale != 0.f ? p->scale : 0.08838834764831845f;  // 1 / sqrt(128)
+  a.softcap = p->softcap, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
+  a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
+  a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
+  a.error = &ctx->dparams->error;
+  return (tq_status)tq::launch_q8_attention(a, d_workspace, ctx->num_sms, stream);
+}
+
+tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *dst, int batch, int heads_kv,
+                      const int32_t *d_seq_lens, const float *d_weights, int keep, int sink, int recent,
+                      const int32_t *d_positions, int32_t *d_kept, int32_t *d_dst_lens, float *d_dst_weights,
+                      int32_t *d_dst_positions, void *stream) {
+  if (!ctx || !d_seq_lens || !d_weights || !d_kept || !d_dst_lens || batch <= 0 || heads_kv <= 0) return TQ_ERR_ARG;
+  tq_status s = tq::q8_check_cache(ctx, src, batch, heads_kv);
+  if (s == TQ_OK) s = tq::q8_check_cache(ctx, dst, batch, heads_kv);
+  if (s != TQ_OK) return s;
+  if (keep <= 0 || sink < 0 || recent < 0 || (long long)sink + recent > keep || keep > dst->capacity) return TQ_ERR_ARG;
+  const size_t grid = (size_t)batch * heads_kv;
+  const size_t sn = src->block_table ? (size_t)src->pool_blocks : grid * tq::q8_blocks_of(src->capacity);
+  const size_t dn = dst->block_table ? (size_t)dst->pool_blocks : grid * tq::q8_blocks_of(dst->capacity);
+  if (overlap(src->records, sn * tq::kQ8BlockBytes, dst->records, dn * tq::kQ8BlockBytes) ||
+      overlap(src->k_stats, sn * 4, dst->k_stats, dn * 4) || overlap(src->v_stats, sn * 4, dst->v_stats, dn * 4))
+    return TQ_ERR_ARG;
+  if ((d_dst_weights && d_dst_weights == d_weights) || (d_dst_positions && d_dst_positions == d_positions))
+    return TQ_ERR_ARG;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  const tq::Q8EvictArgs a{tq::q8_cache(src), tq::q8_cache(dst), batch, heads_kv, keep, sink, recent, d_seq_lens,
+                          d_weights, d_positions, d_kept, d_dst_lens, d_dst_positions, d_dst_weights,
+                          &ctx->dparams->error};
+  return (tq_status)tq::launch_q8_evict(a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,111 @@
+// Rotary positions: y = R(pos) x for [batch][heads][n][128] vectors (tq_rotary).
+//
+// Pair (a, b) -> gain (a cos - b sin, b cos + a sin). Bound by memory: every element is read and
+// written once. A thread owns V + V elements of a row (the two halves of V pairs, or 2V
+// consecutive elements when the pairs are interleaved; a row's coordinates past `dim` pass
+// through), forms their V sines and cosines once and uses them for up to 8 heads of its token, four
+// heads' loads in flight before the first is used. V = 8 (16-byte accesses for 16-bit types) needs
+// dim a multiple of 16, V = 4 covers the other multiples of 8.
+
+#include "tq_q8.cuh"
+
+namespace tq {
+namespace {
+
+template <typename T, int V, bool IL>
+__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a, int hpt, long long items) {
+  constexpr int kRow = kD / (2 * V);  // threads of a row
+  __shared__ unsigned long long freq[kD / 2];
+  if (threadIdx.x < kD / 2) freq[threadIdx.x] = a.rope.freq[threadIdx.x];
+  __syncthreads();
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (id >= items) return;
+  const int j = (int)(id % kRow);
+  long long rest = id / kRow;
+  const int t = (int)(rest % a.n);
+  rest /= a.n;
+  const int chunks = (a.heads + hpt - 1) / hpt;
+  const int h0 = (int)(rest % chunks) * hpt, b = (int)(rest / chunks);
+  const int h1 = min(a.heads, h0 + hpt);
+  const int dim = a.rope.dim;
+  // the two vectors of this thread: the halves of V pairs, or 2V consecutive elements
+  const bool turn = 2 * V * j < dim;
+  const int c0 = IL || !turn ? 2 * V * j : V * j, c1 = IL || !turn ? c0 + V : c0 + dim / 2;
+  float cs[V], sn[V];
+  if (turn) {
+    const int pos = __ldg(a.positions + (long long)b * a.n + t);
+    const float sign = a.transpose ? -a.rope.gain : a.rope.gain;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      rope_sincos(pos, freq[V * j + i], &cs[i], &sn[i]);
+      cs[i] *= a.rope.gain;
+      sn[i] *= sign;
+    }
+  }
+  const T *x = static_cast<const T *>(a.x) + b * a.xs.b + t * a.xs.t;
+  T *y = static_cast<T *>(a.y) + b * a.ys.b + t * a.ys.t;
+  constexpr int kU = 4;
+  for (int h = h0; h < h1; h += kU) {
+    float u[kU][V], w[kU][V];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (h + k < h1) {
+        load_vec<T, V>(x + (h + k) * a.xs.h + c0, u[k]);
+        load_vec<T, V>(x + (h + k) * a.xs.h + c1, w[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (h + k < h1) {
+        if (turn) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if constexpr (IL) {  // pairs (2i, 2i + 1) of the 2V elements
+              float *p = i < V / 2 ? &u[k][2 * i] : &w[k][2 * i - V];
+              const float e0 = p[0], e1 = p[1];
+              p[0] = rope_turn(e0, e1, cs[i], -sn[i]);
+              p[1] = rope_turn(e1, e0, cs[i], sn[i]);
+            } else {
+              const float e0 = u[k][i], e1 = w[k][i];
+              u[k][i] = rope_turn(e0, e1, cs[i], -sn[i]);
+              w[k][i] = rope_turn(e1, e0, cs[i], sn[i]);
+            }
+          }
+        }
+        store_vec<T, V>(y + (h + k) * a.ys.h + c0, u[k]);
+        store_vec<T, V>(y + (h + k) * a.ys.h + c1, w[k]);
+      }
+  }
+}
+
+template <typename T, int V>
+int launch(const RotaryArgs &a, int num_sms, cudaStream_t st) {
+  const long long one = (long long)a.batch * a.n * a.heads * (kD / (2 * V));  // threads at one head each
+  // heads per thread: 8 where that still leaves two thousand threads an SM, else fewer
+  long long hpt = one / ((long long)num_sms * 2048);
+  hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
+  if (hpt > a.heads) hpt = a.heads;
+  const long long items = (long long)a.batch * a.n * ((a.heads + hpt - 1) / hpt) * (kD / (2 * V));
+  const long long grid = (items + 255) / 256;
+  if (grid > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  if (a.rope.interleaved) rotary_kernel<T, V, true><<<(unsigned)grid, 256, 0, st>>>(a, (int)hpt, items);
+  else rotary_kernel<T, V, false><<<(unsigned)grid, 256, 0, st>>>(a, (int)hpt, items);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+template <typename T>
+int launch_t(const RotaryArgs &a, int num_sms, cudaStream_t st) {
+  return a.rope.dim % 16 == 0 ? launch<T, 8>(a, num_sms, st) : launch<T, 4>(a, num_sms, st);
+}
+
+}  // namespace
+
+int launch_rotary(const RotaryArgs &a, int num_sms, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  switch (a.dtype) {
+    case TQ_F32: return launch_t<float>(a, num_sms, st);
+    case TQ_BF16: return launch_t<__nv_bfloat16>(a, num_sms, st);
+    default: return launch_t<__half>(a, num_sms, st);
+  }
+}
+
+}  // namespace tq

@@ -26,15 +26,18 @@ TQ_ERR_TIMEOUT = 5
 TQ_ERR_STATE = 6
 TQ_ERR_ALIGN = 7
 TQ_ERR_WORKSPACE = 8
+TQ_ERR_NONFINITE = 9
 
 TQ_SCHEME_KV = 0
 TQ_SCHEME_KQV = 1
 TQ_SCHEME_QKQV = 2
 TQ_SCHEME_KIVI = 3
-SCHEMES = {"KV": TQ_SCHEME_KV, "KQV": TQ_SCHEME_KQV, "QKQV": TQ_SCHEME_QKQV, "KIVI": TQ_SCHEME_KIVI}
+TQ_SCHEME_Q8 = 4
+SCHEMES = {"KV": TQ_SCHEME_KV, "KQV": TQ_SCHEME_KQV, "QKQV": TQ_SCHEME_QKQV, "KIVI": TQ_SCHEME_KIVI, "Q8": TQ_SCHEME_Q8}
 
 TQ_F32 = 0
 TQ_BF16 = 1
+TQ_F16 = 2
 
 TQ_ROTATION_WHT = 0
 TQ_ROTATION_DENSE = 1
@@ -57,12 +60,29 @@ RECORD_PLANES = ["k_codes", "k_norm", "k_signs", "k_rnorm", "v_codes", "v_norm",
 # separately allocated arrays (records for TQ schemes; the KIVI planes)
 ARRAYS = ["records", "k_codes", "v_codes", "k_stats", "v_stats", "k_window", "v_window"]
 BLOCK_TOKENS = 16
+Q8_BLOCK_TOKENS = 64  # token slots of a block of an 8-bit cache
 
 
 class tq_cache_sizes(ctypes.Structure):
     _fields_ = [("records", _sz), ("block_bytes", _sz), ("plane_offset", _sz * 9), ("plane_bytes", _sz * 9),
                 ("k_codes", _sz), ("v_codes", _sz), ("k_stats", _sz), ("v_stats", _sz), ("k_window", _sz),
                 ("v_window", _sz), ("record_bytes", _sz)]
+
+
+class tq_rope(ctypes.Structure):
+    _fields_ = [("dim", _i), ("interleaved", _i)] + [(n, ctypes.c_double) for n in
+                ("base", "factor", "original_len", "low", "high", "gain")]
+
+
+_strides3 = ctypes.c_int64 * 3
+
+
+class tq_q8_attn(ctypes.Structure):
+    _fields_ = [("batch", _i), ("heads_q", _i), ("heads_kv", _i), ("n_q", _i), ("max_len", _i), ("q_dtype", _i),
+                ("out_dtype", _i), ("d_q", _vp), ("q_strides", _strides3), ("d_out", _vp), ("out_strides", _strides3),
+                ("d_seq_lens", _vp), ("d_new_lens", _vp), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("d_slopes", _vp), ("d_q_positions", _vp), ("d_k_positions", _vp), ("d_key_begin", _vp),
+                ("d_key_end", _vp), ("d_weights_in", _vp), ("d_weights", _vp), ("d_lse", _vp)]
 
 
 _SIGNATURES = {
@@ -94,6 +114,14 @@ _SIGNATURES = {
                                         _vp]),
     "tq_static_scratch_bytes": (_sz, []),
     "tq_selftest_bounded_wait": (_i, [_vp, ctypes.c_ulonglong, _vp]),
+    "tq_set_rope": (_i, [_vp, ctypes.POINTER(tq_rope)]),
+    "tq_rotary": (_i, [_vp, _vp, _strides3, _vp, _strides3, _i, _i, _i, _i, _vp, _i, _vp]),
+    "tq_q8_append": (_i, [_vp, ctypes.POINTER(tq_cache), _vp, _strides3, _vp, _strides3, _i, _i, _i, _i, _vp, _vp, _i,
+                          _vp, _vp]),
+    "tq_q8_attention_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "tq_q8_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.POINTER(tq_q8_attn), _vp, _sz, _vp]),
+    "tq_q8_evict": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.POINTER(tq_cache), _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp,
+                         _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -374,6 +402,142 @@ def tq_selftest_bounded_wait(ctx, budget_ns: int, stream=None) -> None:
 
 
 # ----------------------------------------------------------------------------
+# rotary positions and the 8-bit cache
+# ----------------------------------------------------------------------------
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _any_dtype(dtype: torch.dtype) -> int:
+    codes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+    if dtype not in codes:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return codes[dtype]
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Strides of a [batch][heads][tokens][128] tensor (dimensions of one entry have none)."""
+    _need(t.dim() == 4 and t.shape[-1] == 128 and t.stride(-1) == 1,
+          f"{name}: [batch][heads][tokens][128] with contiguous rows is wanted")
+    return _strides3(*(0 if t.shape[i] == 1 else t.stride(i) for i in range(3)))
+
+
+def _array(t: Optional[torch.Tensor], shape, dtype, device, name: str):
+    """The pointer of a contiguous tensor of this shape and type (None stays None)."""
+    if t is None:
+        return None
+    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.is_contiguous() and t.device == device,
+          f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
+    return _ptr(t)
+
+
+def tq_set_rope(ctx, dim: int = 128, interleaved: bool = False, base: float = 10000.0, factor: float = 1.0,
+                original_len: float = 0.0, low: float = 0.0, high: float = 0.0, gain: float = 1.0) -> None:
+    """The rotation of tq_rotary and tq_q8_append (include/tq.h, tq_rope)."""
+    r = tq_rope(dim, int(interleaved), base, factor, original_len, low, high, gain)
+    check(lib().tq_set_rope(ctx, ctypes.byref(r)), "tq_set_rope")
+
+
+def tq_rotary(ctx, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, transpose: bool = False,
+              stream=None) -> torch.Tensor:
+    """x [batch][heads][tokens][128] (any strides with contiguous rows) turned at positions int32
+    [batch][tokens]; out may be x. Returns out (laid out as x when it is made here)."""
+    xs = _rows(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device, "out: x's shape, type and device are wanted")
+    B, H, n, _ = x.shape
+    pos = _array(positions, (B, n), torch.int32, x.device, "positions")
+    check(lib().tq_rotary(ctx, _ptr(x), xs, _ptr(out), _rows(out, "out"), _any_dtype(x.dtype), B, H, n, pos,
+                          int(transpose), _stream(stream)), "tq_rotary")
+    return out
+
+
+def tq_q8_append(ctx, cache: "Cache", k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,
+                 new_lens: Optional[torch.Tensor] = None, rope: bool = False, positions: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """k, v [batch][heads_kv][tokens][128] (any strides with contiguous rows) into an 8-bit cache at
+    slots seq_lens[b] + t; sequence b brings its first new_lens[b] tokens (all when None)."""
+    B, H, n, _ = k.shape
+    _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device == cache.device,
+          "k and v: one shape and type, on the cache's device")
+    dev = k.device
+    check(lib().tq_q8_append(ctx, ctypes.byref(cache.struct), _ptr(k), _rows(k, "k"), _ptr(v), _rows(v, "v"),
+                             _any_dtype(k.dtype), B, H, n, _array(seq_lens, (B,), torch.int32, dev, "seq_lens"),
+                             _array(new_lens, (B,), torch.int32, dev, "new_lens"), int(rope),
+                             _array(positions, (B, n), torch.int32, dev, "positions"), _stream(stream)), "tq_q8_append")
+
+
+def tq_q8_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, max_len: int,
+                              weights: bool = False) -> int:
+    out = _sz()
+    check(lib().tq_q8_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_len, int(weights), ctypes.byref(out)),
+          "tq_q8_attention_workspace")
+    return out.value
+
+
+def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
+                    new_lens: Optional[torch.Tensor] = None, scale: float = 0.0, softcap: float = 0.0,
+                    slopes: Optional[torch.Tensor] = None, q_positions: Optional[torch.Tensor] = None,
+                    k_positions: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                    key_end: Optional[torch.Tensor] = None, weights_in: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """Attention of q [batch][heads_q][tokens][128] (any strides with contiguous rows) over an 8-bit
+    cache of seq_lens[b] tokens, the query tokens' own among them (include/tq.h, tq_q8_attn). Returns
+    out, of q's type unless out_dtype is torch.float32; made here it is q's shape, contiguous, and
+    rows past new_lens[b] are not written."""
+    B, Hq, n, _ = q.shape
+    H, cap, dev = cache.heads_kv, cache.capacity, q.device
+    _need(dev == cache.device, "q: the cache's device is wanted")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
+    _need(out.shape == q.shape and out.device == dev and out_dtype in (None, out.dtype), "out: q's shape and device are wanted")
+    if workspace is None:
+        workspace = torch.empty(tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
+                                dtype=torch.uint8, device=dev)
+    i32, f32 = torch.int32, torch.float32
+    a = tq_q8_attn(
+        batch=B, heads_q=Hq, heads_kv=H, n_q=n, max_len=max_len, q_dtype=_any_dtype(q.dtype), out_dtype=_any_dtype(out.dtype),
+        d_q=_ptr(q), q_strides=_rows(q, "q"), d_out=_ptr(out), out_strides=_rows(out, "out"),
+        d_seq_lens=_array(seq_lens, (B,), i32, dev, "seq_lens"), d_new_lens=_array(new_lens, (B,), i32, dev, "new_lens"),
+        scale=scale, softcap=softcap, d_slopes=_array(slopes, (Hq,), f32, dev, "slopes"),
+        d_q_positions=_array(q_positions, (B, n), i32, dev, "q_positions"),
+        d_k_positions=_array(k_positions, (B, H, cap), i32, dev, "k_positions"),
+        d_key_begin=_array(key_begin, (B, n), i32, dev, "key_begin"), d_key_end=_array(key_end, (B, n), i32, dev, "key_end"),
+        d_weights_in=_array(weights_in, (B, H, cap), f32, dev, "weights_in"),
+        d_weights=_array(weights, (B, H, cap), f32, dev, "weights"), d_lse=_array(lse, (B, Hq, n), f32, dev, "lse"))
+    check(lib().tq_q8_attention(ctx, ctypes.byref(cache.struct), ctypes.byref(a), _ptr(workspace), workspace.numel(),
+                                _stream(stream)), "tq_q8_attention")
+    return out
+
+
+def tq_q8_evict(ctx, src: "Cache", dst: "Cache", seq_lens: torch.Tensor, weights: torch.Tensor, keep: int, sink: int = 0,
+                recent: int = 0, positions: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                dst_lens: Optional[torch.Tensor] = None, dst_weights: Optional[torch.Tensor] = None,
+                dst_positions: Optional[torch.Tensor] = None, stream=None):
+    """Keep at most `keep` tokens of every sequence of `src` in `dst`: the first `sink`, the last
+    `recent` and the heaviest of the rest. Returns (kept slots [batch][heads_kv][keep], lengths
+    [batch], weights and positions [batch][heads_kv][dst capacity])."""
+    B, H, dev = src.batch, src.heads_kv, src.device
+    _need((dst.batch, dst.heads_kv, dst.device) == (B, H, dev), "dst: the source's batch, KV heads and device are wanted")
+    i32, f32 = torch.int32, torch.float32
+    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=dev) if t is None else t  # noqa: E731
+    kept, dst_lens = new(kept, (B, H, max(keep, 0)), i32), new(dst_lens, (B,), i32)
+    dst_weights, dst_positions = new(dst_weights, (B, H, dst.capacity), f32), new(dst_positions, (B, H, dst.capacity), i32)
+    check(lib().tq_q8_evict(ctx, ctypes.byref(src.struct), ctypes.byref(dst.struct), B, H,
+                            _array(seq_lens, (B,), i32, dev, "seq_lens"), _array(weights, (B, H, src.capacity), f32, dev, "weights"),
+                            keep, sink, recent, _array(positions, (B, H, src.capacity), i32, dev, "positions"),
+                            _array(kept, (B, H, max(keep, 0)), i32, dev, "kept"), _array(dst_lens, (B,), i32, dev, "dst_lens"),
+                            _array(dst_weights, (B, H, dst.capacity), f32, dev, "dst_weights"),
+                            _array(dst_positions, (B, H, dst.capacity), i32, dev, "dst_positions"), _stream(stream)), "tq_q8_evict")
+    return kept, dst_lens, dst_weights, dst_positions
+
+
+# ----------------------------------------------------------------------------
 # device-memory plumbing: a context handle and a cache whose planes torch owns
 # ----------------------------------------------------------------------------
 
@@ -449,6 +613,9 @@ class Cache:
     def __init__(self, ctx: Context, batch: int, heads_kv: int, capacity: int, device="cuda"):
         self.sizes = tq_cache_sizes_get(ctx.handle, batch, heads_kv, capacity)
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.block_tokens = Q8_BLOCK_TOKENS if ctx.scheme == "Q8" else BLOCK_TOKENS
         self.batch, self.heads_kv, self.capacity = batch, heads_kv, capacity
         self.tensors = {}
         self.struct = tq_cache()
@@ -469,7 +636,7 @@ class Cache:
 
     @property
     def blocks_per_seq(self) -> int:
-        return (self.capacity + BLOCK_TOKENS - 1) // BLOCK_TOKENS
+        return (self.capacity + self.block_tokens - 1) // self.block_tokens
 
     def blocks(self) -> torch.Tensor:
         """The records as [batch * heads_kv][blocks_per_seq][block_bytes] (TQ schemes)."""
@@ -480,6 +647,13 @@ class Cache:
         slots (a copy gathered out of the blocks for the TQ schemes' record planes)."""
         if "records" not in self.tensors or name not in RECORD_PLANES:
             return self.tensors[name]
+        if self.block_tokens == Q8_BLOCK_TOKENS:  # [batch * heads_kv][blocks][plane of groups of 8 tokens] -> token rows
+            if name not in ("k_codes", "v_codes"):
+                raise KeyError(name)
+            half = Q8_BLOCK_TOKENS * 128
+            codes = self.blocks()[:, :, (name == "v_codes") * half:][:, :, :half]
+            rows = codes.reshape(self.batch * self.heads_kv, -1, 8, 8, 16).transpose(2, 3)
+            return rows.reshape(self.batch * self.heads_kv, -1, 128)[:, :self.capacity].contiguous().view(-1)
         p = RECORD_PLANES.index(name)
         tok = self.sizes.plane_bytes[p]
         if tok == 0:
@@ -512,6 +686,7 @@ class PagedCache(Cache):
     def __init__(self, ctx: Context, batch: int, heads_kv: int, capacity: int, pool_blocks: int,
                  block_table: torch.Tensor, device="cuda"):
         self.pool_blocks = int(pool_blocks)
+        self.block_tokens = Q8_BLOCK_TOKENS if ctx.scheme == "Q8" else BLOCK_TOKENS
         super().__init__(ctx, batch, heads_kv, capacity, device)
         nblk = self.blocks_per_seq
         assert block_table.dtype == torch.int32 and block_table.is_contiguous()
@@ -523,6 +698,8 @@ class PagedCache(Cache):
     def _array_bytes(self, name: str) -> int:
         if name == "records":
             return self.pool_blocks * self.sizes.block_bytes
+        if name in ("k_stats", "v_stats") and self.block_tokens == Q8_BLOCK_TOKENS:
+            return self.pool_blocks * 4
         return getattr(self.sizes, name)
 
     def blocks(self) -> torch.Tensor:
