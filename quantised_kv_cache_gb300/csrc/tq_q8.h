@@ -87,6 +87,7 @@ struct Q8AttnArgs {
   int *error;
 };
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights);
+int launch_q8_weights(const Q8AttnArgs &a, void *stream);
 int launch_q8_attention(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 
 }  // namespace tq

@@ -16,7 +16,7 @@
 // cut into equal slices, so ragged batches and long single sequences load every SM alike. A unit that lies in one
 // slice is finished there; one that was cut leaves a partial record per slice, joined by q8_join_kernel.
 
-#include "tq_q8_attend.cuh"
+#include "tq_q8_rows.cuh"
 
 namespace tq {
 namespace {
@@ -26,8 +26,6 @@ constexpr int kStage = 2 * kTile * kD;  // its keys, then its values
 constexpr int kWg = 4;                  // warpgroups, each with a tile of its own
 constexpr int kConsumers = kWg * 128;
 constexpr int kThreads = kConsumers + 32;
-constexpr int kRows = 16;               // rows of a unit = N of the MMAs
-constexpr int kTerm = kRows * 128;      // bytes of one 8-bit term of a Q or P operand
 constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launch
 constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
 
@@ -39,23 +37,6 @@ struct Entries {
   int lo[kEntries];       // its first tile
   int hi[kEntries];       // one past its last visible slot
 };
-
-// A row's key range: query token i of sequence b, whose length is len and whose query tokens number m.
-__device__ __forceinline__ int2 row_range(const Q8AttnArgs &a, int b, int i, int len, int m) {
-  if (i >= m) return make_int2(0, 0);
-  int beg = 0, end = len - m + i + 1;
-  if (a.kbeg) beg = max(0, __ldg(a.kbeg + (long long)b * a.n_q + i));
-  if (a.kend) end = __ldg(a.kend + (long long)b * a.n_q + i);
-  end = min(end, len);
-  return end > beg ? make_int2(beg, end) : make_int2(0, 0);
-}
-
-__device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, int *m, bool report) {
-  int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
-  if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
-  *len = min(max(n, 0), a.max_len);
-  *m = min(max(q, 0), a.n_q);
-}
 
 // What the main kernel tells the join about each CTA's last unit.
 struct Cut {
@@ -76,7 +57,6 @@ struct Shared {
   Entries ent;
 };
 
-__device__ __forceinline__ void bar_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
 __device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"(kConsumers) : "memory"); }
 
 template <int NR, int GR>
@@ -241,43 +221,11 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
       // ---- the unit's queries: warp w prepares row w
       {
         const int row = row0 + warp, i = row / G, hq = h * G + row % G;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
         int len, m;
         seq_sizes(a, b, &len, &m, false);
         const bool live = warp < NR && row < R && i < m;
-        if (live) {
-          const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
-          if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
-          else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
-          else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
-        }
-        uint32_t amax = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, __float_as_uint(x[k]) & 0x7fffffffu);
-        amax = __reduce_max_sync(kFull, amax);
-        const int ex = row_exponent(amax);
-        const float f = pow2i(-ex);
         uint32_t w[GR][3];
-        if (amax >= 0x7f800000u) {  // an infinity or a NaN: the row's result is NaN
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-            for (int k = 0; k < 3; ++k) w[gr][k] = 0x7f7f7f7fu;
-        } else {
-          float y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = x[k] * f;
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr) {
-            uint32_t lo[3], hi2[3];
-            split_terms(y[0], y[1], lo);
-            split_terms(y[2], y[3], hi2);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) w[gr][k] = lo[k] | (hi2[k] << 16);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] *= kGroupScale;
-          }
-        }
+        const int ex = row_terms<GR>(a, b, hq, i, live, lane, w);
         bar_all();  // everyone is done with the unit before
         if (warp < NR) {
 #pragma unroll
@@ -592,7 +540,7 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, vo
   if (a.weights && !a.lse) a.lse = (float *)p;
   const long long R = (long long)a.group * a.n_q;
   const int rts = (int)((R + kRows - 1) / kRows);
-  if (rts > kEntries || a.weights) return TQ_ERR_UNSUPPORTED;
+  if (rts > kEntries) return TQ_ERR_UNSUPPORTED;
   const int per = kEntries / rts;  // sequences of a launch
   for (int b0 = 0; b0 < a.batch; b0 += per) {
     const int nb = a.batch - b0 < per ? a.batch - b0 : per;
@@ -609,7 +557,7 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, vo
                    : launch_rows<16, 1>(a, cuts, b0, nb, rts, num_sms, st);
     if (s != TQ_OK) return s;
   }
-  return TQ_OK;
+  return a.weights ? launch_q8_weights(a, stream) : TQ_OK;
 }
 
 }  // namespace tq

@@ -1,0 +1,180 @@
+// Accumulated attention weight of the 8-bit cache (tq_q8_attention with d_weights): per slot the sum,
+// over the group's heads and the sequence's query tokens, of p = 2^(t - lse), t and lse in log2.
+//
+// After the attention has left each row's lse, the scores are formed again from the keys alone: one CTA per 128
+// tokens of a (sequence, KV head), its key tile read once. Four warpgroups take every fourth tile of 16
+// query rows: queries as 8-bit terms, one score MMA chain, and because token = lane = thread, a
+// thread adds its own token's probabilities over all rows in one register -- no atomics, one fixed order.
+// Row tiles that see none of the tokens are skipped.
+
+#include "tq_q8_rows.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kWg = 4;
+constexpr int kThreads = kWg * 128;
+
+struct Shared {
+  uint64_t full, bar_s[kWg];
+  float qscale[kWg][kRows], slope[kWg][kRows], lse[kWg][kRows];
+  int2 range[kWg][kRows];
+  int qpos[kWg][kRows];
+  float sum[kWg][kTile];
+  uint32_t tmem;
+  int bad;
+};
+
+template <int GR>
+__global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_constant__ Q8AttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Shared sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
+  const int tok0 = blockIdx.x * kTile, h = blockIdx.y, b = blockIdx.z;
+  int len, m;
+  seq_sizes(a, b, &len, &m, false);
+  const int n = min(kTile, max(0, len - tok0));
+  const long long bh = (long long)b * a.heads_kv + h, at = bh * a.c.capacity + tok0;
+  if (n == 0) {  // no token here: the weights as they were
+    if (a.weights != a.weights_in && tid < kTile && tok0 + tid < a.c.capacity)
+      a.weights[at + tid] = a.weights_in ? a.weights_in[at + tid] : 0.f;
+    return;
+  }
+  uint8_t *ktile = dyn, *qbuf = dyn + kTile * kD + wg * GR * 3 * kTerm;
+  if (tid == 0) {
+    mbar_init(&sm.full, 1);
+    for (int w = 0; w < kWg; ++w) mbar_init(&sm.bar_s[w], 1);
+    mbar_fence_init();
+    sm.bad = 0;
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&sm.tmem), kWg * 16 * GR);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t t_s = sm.tmem + wg * 16 * GR, lanes = (uint32_t)(32 * w4) << 16;
+  // the keys of the tile's two blocks; a block that is not mapped stays unread and unseen
+  float ks = -1.f;
+  if (wt < n) {
+    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + (tok0 + wt) / kQ8Block, a.error);
+    if (blk >= 0) ks = __ldg(a.c.ks + blk);
+  }
+  if (tid == 0) {
+    int bytes = 0;
+    long long src[2] = {-1, -1};
+    for (int k = 0; k < 2 && k * kQ8Block < n; ++k) {
+      src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok0 / kQ8Block + k, a.error);
+      if (src[k] >= 0) bytes += kQ8Plane;
+    }
+    mbar_arrive_expect_tx(&sm.full, bytes);
+    for (int k = 0; k < 2; ++k)
+      if (src[k] >= 0) tma_load_1d(ktile + k * kQ8Plane, a.c.records + src[k] * kQ8BlockBytes, kQ8Plane, &sm.full);
+  }
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*(volatile int *)&sm.bad) return;
+    if (!mbar_wait_bounded(bar, parity, a.error)) *(volatile int *)&sm.bad = 1;
+  };
+  wait(&sm.full, 0);
+  const int slot = tok0 + wt;
+  const int kp = a.kpos && wt < n ? __ldg(a.kpos + at + wt) : slot;
+  const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
+  const uint32_t idesc[2] = {tc_idesc_f8(128, kRows, 0, 0, 0, 0), tc_idesc_f8(128, kRows, 0, 1, 0, 0)};
+  const int R = a.group * a.n_q, rts = (R + kRows - 1) / kRows;
+  float sum = 0.f;
+  uint32_t phase = 0;
+  for (int rt = wg; rt < rts; rt += kWg) {
+    // ---- the ranges first: does any row of the tile see a token here?
+    int2 rg = make_int2(0, 0);
+    const int mine = rt * kRows + (wt & (kRows - 1)), mi = mine / a.group;
+    if (mine < R) rg = row_range(a, b, mi, len, m);
+    if (!__any_sync(kFull, rg.x < tok0 + n && rg.y > tok0)) continue;  // the same for the four warps
+    if (wt < kRows) sm.range[wg][wt] = rg;
+    for (int k = 0; k < kRows / 4; ++k) {
+      const int r = w4 * (kRows / 4) + k, row = rt * kRows + r, i = row / a.group, hq = h * a.group + row % a.group;
+      const bool live = row < R && i < m;
+      uint32_t w[GR][3];
+      const int ex = row_terms<GR>(a, b, hq, i, live, lane, w);
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint32_t *>(qbuf + (gr * 3 + t) * kTerm + q8_off(r, 4 * lane)) = w[gr][t];
+      if (lane == 0) {
+        sm.qscale[wg][r] = pow2i(ex);
+        sm.slope[wg][r] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+        sm.qpos[wg][r] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : len - m + i;
+        sm.lse[wg][r] = live ? a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] * kLog2e : 0.f;
+      }
+    }
+    fence_proxy_async_shared();
+    tc_fence_before_sync();
+    bar_wg(wg);
+    if (wt == 0) {
+      tc_fence_after_sync();
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+          for (int s = 0; s < kD / 32; ++s)
+            tc_mma_f8(t_s + 16 * gr, tc_sdesc_kmajor(smem_u32(ktile) + 256 * s, 128, 1024),
+                      tc_sdesc_kmajor(smem_u32(qbuf + (gr * 3 + k) * kTerm) + 256 * s, 128, 1024), idesc[k == 2],
+                      k > 0 || s > 0);
+      tc_commit(smem_u32(&sm.bar_s[wg]));
+    }
+    wait(&sm.bar_s[wg], phase & 1);
+    ++phase;
+    tc_fence_after_sync();
+    float t[kRows];
+    tmem_ld_cols<kRows>(t_s + lanes, t);
+    if constexpr (GR == 2) {
+      float t2[kRows];
+      tmem_ld_cols<kRows>(t_s + 16 + lanes, t2);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) t[r] = fmaf(t2[r], 1.f / kGroupScale, t[r]);
+    }
+    tc_fence_before_sync();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int2 see = sm.range[wg][r];
+      if (slot < see.x || slot >= see.y || ks < 0.f) continue;
+      float x = q8_score_log2(t[r] * (sm.qscale[wg][r] * ks), sc);
+      if (a.slopes) x = fmaf(-sm.slope[wg][r], (float)__sad(sm.qpos[wg][r], kp, 0u), x);
+      sum += ex2_approx(x - sm.lse[wg][r]);
+    }
+    bar_wg(wg);  // the rows' arrays and terms are free again
+  }
+  sm.sum[wg][wt] = sum;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (tid < kTile && slot < a.c.capacity) {
+    const float w = (sm.sum[0][wt] + sm.sum[1][wt]) + (sm.sum[2][wt] + sm.sum[3][wt]);
+    a.weights[at + wt] = (a.weights_in ? a.weights_in[at + wt] : 0.f) + (wt < n ? w : 0.f);
+  }
+  if (warp == 0) tmem_dealloc(sm.tmem, kWg * 16 * GR);
+}
+
+template <int GR>
+int launch(const Q8AttnArgs &a, cudaStream_t st) {
+  constexpr int smem = kTile * kD + kWg * GR * 3 * kTerm;
+  if (cudaFuncSetAttribute(q8_weights_kernel<GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  // in place only the tokens in use are touched
+  const int slots = a.weights == a.weights_in ? a.max_len : a.c.capacity;
+  if (a.heads_kv > 65535 || a.batch > 65535) return TQ_ERR_UNSUPPORTED;
+  q8_weights_kernel<GR><<<dim3((unsigned)((slots + kTile - 1) / kTile), (unsigned)a.heads_kv, (unsigned)a.batch), kThreads,
+                          smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_q8_weights(const Q8AttnArgs &a, void *stream) {
+  return a.out_dtype == TQ_F32 ? launch<2>(a, (cudaStream_t)stream) : launch<1>(a, (cudaStream_t)stream);
+}
+
+}  // namespace tq

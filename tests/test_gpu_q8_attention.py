@@ -190,6 +190,94 @@ def test_caps_biases_and_masks(ctx, softcap, bias, mask, positions, B, Hq, H, n,
         assert bool((got[b, :, m[b]:] == 77).all())
 
 
+@pytest.mark.parametrize("case", [(1, 1, 1, 1, [1]), (3, 8, 2, 1, [65, 0, 128]), (2, 40, 2, 1, [300, 77]), (2, 4, 4, 5, [5, 130]),
+                                  (1, 8, 2, 33, [300]), (2, 16, 4, 100, [260, 100]), (1, 32, 8, 1, [1000]), (16, 4, 4, 1, [50 * i + 1 for i in range(16)])],
+                         ids=lambda c: "-".join(map(str, c[:4])) + f"-{max(c[4])}")
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("extra", ["plain", "ragged masked capped biased paged"])
+def test_accumulated_weights(ctx, case, dtype, extra):
+    B, Hq, H, n, lens = case
+    cap = max(max(lens), n) + 70
+    cache, k, v = make(ctx, B, H, cap, lens, seed=sum(lens), paged=extra != "plain")
+    q = queries(5, B, Hq, n, dtype, "tokens")
+    new, kw, ck = [n] * B, {}, {}
+    if extra != "plain":
+        rng = np.random.default_rng(n)
+        new = [int(rng.integers(0, n + 1)) for _ in range(B)]
+        ck = dict(begin=rng.integers(-5, 100, (B, n)), end=rng.integers(0, 400, (B, n)), softcap=15.0, slopes=np.linspace(0.01, 0.3, Hq))
+        kw = dict(key_begin=ints(ck["begin"]), key_end=ints(ck["end"]), softcap=15.0, slopes=torch.as_tensor(ck["slopes"], dtype=F32, device=DEV),
+                  new_lens=ints(new))
+        ck["slopes"] = kw["slopes"].double().cpu().numpy()
+    before = torch.rand(B, H, cap, generator=gen(8), device=DEV)
+    out = torch.zeros_like(q)
+    alone = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, out=out, **kw).clone()
+    both = torch.full_like(before, float("nan"))
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, weights_in=before, weights=both, out=out, **kw)
+    assert torch.equal(got, alone)
+    check(np64(got), np64(q), k, v, lens, new, dtype=dtype, out_dtype=dtype, weights=np64(both), before=np64(before), **ck)
+    fresh = torch.full_like(before, float("nan"))
+    tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, weights=fresh, out=out, **kw)
+    check(np64(got), np64(q), k, v, lens, new, dtype=dtype, out_dtype=dtype, weights=np64(fresh), **ck)
+    place = before.clone()
+    tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, weights_in=place, weights=place, out=out, **kw)
+    assert torch.equal(place, both)
+
+
+def test_a_served_sequence_from_prompt_to_eviction_and_on(ctx):
+    """A prompt is appended and attended, a few tokens are decoded while their attention weight accumulates, the cache is cut by it,
+    and decoding goes on over the kept tokens at their old positions."""
+    B, Hq, H, n, cap, keep = 2, 8, 2, 200, 320, 128
+    tq.tq_set_rope(ctx.handle, 64, interleaved=True)
+    cache, dst = tq.Cache(ctx, B, H, cap, device=DEV), tq.Cache(ctx, B, H, 192, device=DEV)
+    model = {"k": q8.Model(B * H, cap), "v": q8.Model(B * H, cap)}
+    lens = np.zeros(B, int)
+    w = torch.zeros(B, H, cap, device=DEV)
+    slopes = torch.tensor([2.0 ** -(i + 1) for i in range(Hq)], device=DEV)
+
+    def tokens(seed, m):
+        return [queries(seed + i, B, x, m, BF, "tokens") for i, x in enumerate((Hq, H, H))]
+
+    for step, m in enumerate([n] + [1] * 5):
+        q, k, v = tokens(100 * step, m)
+        pos = ints(lens[:, None] + np.arange(m))
+        qr = tq.tq_rotary(ctx.handle, q, pos)
+        kr = tq.tq_rotary(ctx.handle, k, pos)
+        tq.tq_q8_append(ctx.handle, cache, k, v, ints(lens), rope=True)
+        for b in range(B):
+            for h in range(H):
+                model["k"].append(b * H + h, int(lens[b]), np64(kr)[b, h])
+                model["v"].append(b * H + h, int(lens[b]), np64(v)[b, h])
+        lens = lens + m
+        before = np64(w)
+        out = tq.tq_q8_attention(ctx.handle, cache, qr, ints(lens), cap, slopes=slopes, weights_in=w, weights=w)
+        kv, vv = (x.values().reshape(B, H, -1, 128)[:, :, :cap] for x in (model["k"], model["v"]))
+        check(np64(out), np64(qr), kv, vv, lens, [m] * B, dtype=BF, out_dtype=BF, slopes=np64(slopes), weights=np64(w), before=before)
+    kept, dlens, dw, dp = tq.tq_q8_evict(ctx.handle, cache, dst, ints(lens), w, keep, 4, 16)
+    wn = w.cpu().numpy()
+    km, vm = q8.Model(B * H, 192), q8.Model(B * H, 192)
+    places = np.zeros((B, H, 192), int)
+    for b in range(B):
+        for h in range(H):
+            stay = q8.evict(wn[b, h], int(lens[b]), keep, 4, 16)
+            np.testing.assert_array_equal(kept[b, h].cpu().numpy(), stay)
+            places[b, h, :keep] = stay
+            km.append(b * H + h, 0, kv[b, h, stay])
+            vm.append(b * H + h, 0, vv[b, h, stay])
+    q, k, v = tokens(9000, 1)
+    pos = ints(lens[:, None])
+    qr, kr = tq.tq_rotary(ctx.handle, q, pos), tq.tq_rotary(ctx.handle, k, pos)
+    tq.tq_q8_append(ctx.handle, dst, k, v, dlens, rope=True, positions=pos)
+    dp[torch.arange(B)[:, None], torch.arange(H)[None], dlens.long()[:, None]] = pos.expand(B, H)
+    for b in range(B):
+        for h in range(H):
+            km.append(b * H + h, keep, np64(kr)[b, h])
+            vm.append(b * H + h, keep, np64(v)[b, h])
+            places[b, h, keep] = lens[b]
+    out = tq.tq_q8_attention(ctx.handle, dst, qr, dlens + 1, 192, slopes=slopes, q_positions=pos, k_positions=dp, weights_in=dw, weights=dw)
+    check(np64(out), np64(qr), km.values().reshape(B, H, -1, 128), vm.values().reshape(B, H, -1, 128), [keep + 1] * B, [1] * B, dtype=BF,
+          out_dtype=BF, slopes=np64(slopes), q_pos=lens[:, None], k_pos=places)
+
+
 def test_layouts_and_paging_give_the_same_bits(ctx):
     B, Hq, H, n, lens = 3, 8, 4, 2, [500, 130, 64]
     plain, _, _ = make(ctx, B, H, 512, lens, seed=3)
