@@ -23,7 +23,7 @@ LIB = os.path.join(LIBDIR, "libtq.so")
 
 SOURCES = ["tq_host.cpp", "tq_append.cu", "tq_decode.cu", "tq_dequant.cu", "tq_kivi.cu", "tq_noalloc.cu", "tq_decode2.cu", "tq_append2.cu",
            "tq_append_tc.cu", "tq_append_small.cu", "tq_append_bulk.cu", "tq_selftest.cu", "tq_q8_host.cpp",
-           "tq_rotary.cu", "tq_q8_append.cu", "tq_q8_attend.cu", "tq_q8_weights.cu",
+           "tq_rotary.cu", "tq_q8_append.cu", "tq_q8_attend.cu", "tq_q8_prompt.cu", "tq_q8_weights.cu",
            "tq_q8_evict.cu"]
 HEADERS = ["tq_internal.h", "tq_device.cuh", "tq_ptx.cuh", "tq_tcgen05.cuh", "tq_q8.h", "tq_q8_host.h", "tq_q8.cuh",
            "tq_q8_attend.cuh", "tq_q8_rows.cuh"]

@@ -27,6 +27,7 @@ constexpr int kWg = 4;                  // warpgroups, each with a tile of its o
 constexpr int kConsumers = kWg * 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launch
+constexpr long long kFewRows = 64;      // rows up to which this kernel takes a 16-bit call
 constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
 
 constexpr int stages_of(int GR) { return GR == 1 ? 5 : 4; }
@@ -61,7 +62,7 @@ __device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"
 
 template <int NR, int GR>
 __global__ void __launch_bounds__(kThreads, 1)
-q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, Cut *cuts) {
+q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, int rts, Cut *cuts) {
   constexpr int kStages = stages_of(GR);
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
@@ -85,7 +86,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
   const int E = nb * rts;
   int count = 0;
   if (tid < E) {
-    const int b = b0 + tid / rts, r0 = (tid % rts) * kRows;
+    const int b = b0 + tid / rts, r0 = (rt0 + tid % rts) * kRows;
     int len, m;
     seq_sizes(a, b, &len, &m, blockIdx.x == 0);
     const int i0 = r0 / G, i1 = (min(R, r0 + kRows) - 1) / G;
@@ -214,7 +215,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
     while (g < g1) {
       int e, h, t0, cnt;
       locate(g, e, h, t0, cnt);
-      const int b = b0 + e / rts, row0 = (e % rts) * kRows;
+      const int b = b0 + e / rts, row0 = (rt0 + e % rts) * kRows;
       const long long end = min(g1, g - t0 + cnt);
       const int first = sm.ent.lo[e], hi = sm.ent.hi[e];
 
@@ -280,6 +281,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
         int kp = slot;
         if (a.kpos && slot < hi) kp = __ldg(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
         wait(&sm.bar_s[wg], phase & 1);
+        __syncwarp();  // the loads from tensor memory are a warp's
         tc_fence_after_sync();
         float t[NR];
         tmem_ld_cols<NR>(t_s + lanes, t);
@@ -359,6 +361,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
           tc_commit(smem_u32(&sm.bar_o[wg]));
         }
         wait(&sm.bar_o[wg], phase & 1);
+        __syncwarp();
         tc_fence_after_sync();
         ++phase;
 #pragma unroll
@@ -448,7 +451,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rts, 
             parts = 1;
             for (long long c = blockIdx.x + 1; c < slices && total * c / slices < stop; ++c) ++parts;
           }
-          cuts[blockIdx.x] = Cut{b, e % rts, h, parts};
+          cuts[blockIdx.x] = Cut{b, rt0 + e % rts, h, parts};
         }
       }
       g = end;
@@ -508,11 +511,11 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
 }
 
 template <int NR, int GR>
-int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rts, int num_sms, cudaStream_t st) {
+int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
   constexpr int smem = stages_of(GR) * kStage + GR * 3 * kTerm * (1 + kWg);
   if (cudaFuncSetAttribute(q8_attend_kernel<NR, GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  if (launch_overlapped(true, q8_attend_kernel<NR, GR>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rts, cuts) != cudaSuccess)
+  if (launch_overlapped(true, q8_attend_kernel<NR, GR>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
   if (launch_overlapped(true, q8_join_kernel, dim3(num_sms, NR), dim3(512), 0, st, a, (const Cut *)cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
@@ -521,41 +524,54 @@ int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rts, int num
 
 }  // namespace
 
-size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
-  (void)max_len, (void)heads_kv;
-  size_t cuts = (size_t)num_sms * sizeof(Cut);
-  cuts = (cuts + 15) / 16 * 16;
-  const size_t parts = (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
+// Workspace: the log-sums when the weights need them, then either kernel's records (few rows: cuts and parts).
+static size_t few_bytes(int num_sms) {
+  return ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16 + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
+}
+
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int weights) {
   const size_t lse = weights ? ((size_t)batch * heads_q * n_q * sizeof(float) + 15) / 16 * 16 : 0;
-  return cuts + parts + lse;
+  const size_t few = few_bytes(num_sms);
+  size_t many = 0;
+  if ((long long)(heads_q / heads_kv) * n_q > kFewRows) many = q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
+  return lse + (few > many ? few : many);
 }
 
 int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   Q8AttnArgs a = args;
-  Cut *cuts = (Cut *)workspace;
-  char *p = (char *)workspace + ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16;
-  a.parts = (float *)p;
-  p += (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
-  if (a.weights && !a.lse) a.lse = (float *)p;
+  char *many = (char *)workspace;
+  if (a.weights) {
+    if (!a.lse) a.lse = (float *)many;
+    many += ((size_t)a.batch * a.heads_q * a.n_q * sizeof(float) + 15) / 16 * 16;
+  }
+  Cut *cuts = (Cut *)many;
+  a.parts = (float *)(many + ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16);
   const long long R = (long long)a.group * a.n_q;
-  const int rts = (int)((R + kRows - 1) / kRows);
-  if (rts > kEntries) return TQ_ERR_UNSUPPORTED;
-  const int per = kEntries / rts;  // sequences of a launch
-  for (int b0 = 0; b0 < a.batch; b0 += per) {
-    const int nb = a.batch - b0 < per ? a.batch - b0 : per;
-    int s;
-    if (a.out_dtype == TQ_F32)
-      s = R == 1 ? launch_rows<1, 2>(a, cuts, b0, nb, rts, num_sms, st)
-          : R <= 4 ? launch_rows<4, 2>(a, cuts, b0, nb, rts, num_sms, st)
-          : R <= 8 ? launch_rows<8, 2>(a, cuts, b0, nb, rts, num_sms, st)
-                   : launch_rows<16, 2>(a, cuts, b0, nb, rts, num_sms, st);
-    else
-      s = R == 1 ? launch_rows<1, 1>(a, cuts, b0, nb, rts, num_sms, st)
-          : R <= 4 ? launch_rows<4, 1>(a, cuts, b0, nb, rts, num_sms, st)
-          : R <= 8 ? launch_rows<8, 1>(a, cuts, b0, nb, rts, num_sms, st)
-                   : launch_rows<16, 1>(a, cuts, b0, nb, rts, num_sms, st);
+  // many rows with results of 16 bits: rows as lanes. Its 256-row units cost a fifth of a microsecond a row tile
+  // of 16 less from about 64 rows on, and waste less of the tensor cores
+  if (R > kFewRows && a.out_dtype != TQ_F32) {
+    const int s = launch_q8_prompt(a, many, num_sms, stream);
     if (s != TQ_OK) return s;
+  } else {
+    const int all = (int)((R + kRows - 1) / kRows);  // row tiles of a sequence; at most kEntries of all in a launch
+    const int per = all < kEntries ? kEntries / all : 1;
+    for (int b0 = 0; b0 < a.batch; b0 += per)
+      for (int rt0 = 0; rt0 < all; rt0 += kEntries) {
+        const int nb = a.batch - b0 < per ? a.batch - b0 : per, rts = all - rt0 < kEntries ? all - rt0 : kEntries;
+        int s;
+        if (a.out_dtype == TQ_F32)
+          s = R == 1 ? launch_rows<1, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 4 ? launch_rows<4, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 8 ? launch_rows<8, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+                       : launch_rows<16, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st);
+        else
+          s = R == 1 ? launch_rows<1, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 4 ? launch_rows<4, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 8 ? launch_rows<8, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+                       : launch_rows<16, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st);
+        if (s != TQ_OK) return s;
+      }
   }
   return a.weights ? launch_q8_weights(a, stream) : TQ_OK;
 }

@@ -65,19 +65,21 @@ def make(ctx, B, H, cap, lens, seed=0, paged=False, poison=True, spread=0.5):
 
 def check(got, q, k, v, lens, new, *, dtype, out_dtype, begin=None, end=None, scale=None, softcap=0.0, slopes=None, q_pos=None,
           k_pos=None, lse=None, weights=None, before=None, rows=None):
-    """Every element within the bound. Per query: the products' sums are off by at most 130 U of the sum of
-    their magnitudes (fp32, any order, three scalings), the query's own 8-bit terms by 2^-11 of
-    each coordinate (none of a 16-bit one, whose 8 or 11 bits the three terms hold) and 2^-20 of the row's largest (terms end at
-    2^-13 where that lies in [128, 256)), for float32 results by 2^-22 and 2^-31; capping, bias and the exponent add a few U of what they
-    handle; a probability's relative error is twice the largest score error (its own and the sum's) and 2^-20 for
-    the two exponentials. Probabilities enter the value sums with a relative error of 2^-11 (2^-22 for float32
-    results) and 2^-21 of the largest (2^-32; theirs is 2^8), in numerator and denominator; sums over tiles of 128 add U each; the result
-    is rounded to its type."""
+    """Every element within the bound. Per query: the products' sums are off by at most 130 U of the sum of their magnitudes (fp32,
+    any order, three scalings). A query enters as 8-bit terms with its row's largest coordinate in [128, 256): 16-bit
+    coordinates of at least 2^-9 of the largest exactly, smaller ones within 2^-20 of it (three terms end at 2^-13; two, for many
+    rows in bf16, at 2^-10: 2^-17), float32 ones within 2^-22 of themselves and 2^-31 of the largest (six terms).
+    Capping, bias and the exponent add a few U of what they handle (a cap by the short tanh of many rows 2^-21 of the cap); a probability's relative error is twice the
+    largest score error (its own and the sum's) and 2^-20 for the two exponentials. Probabilities enter the value sums as terms of
+    their 2^8-fold: 2^-11 of each and 2^-21 of the largest (three terms), 2^-8 and 2^-18 (two, many rows in bf16), 2^-22 and 2^-32
+    (six), never more than itself; many rows fold value scales up to 2^4 apart into them, which brings the second nearer by 2^4.
+    Sums over tiles of 128 add U each; the result is rounded to its type."""
     B, Hq, n, _ = q.shape
     H = k.shape[1]
     G = Hq // H
     sc = 1 / np.sqrt(128.0) if scale is None else scale
     wide = out_dtype == F32
+    many = G * n > 64 and not wide
     worst = 0.0
     wsum = np.zeros((B, H, k.shape[2])) if weights is not None else None
     wtol = np.zeros_like(wsum) if weights is not None else None
@@ -98,24 +100,31 @@ def check(got, q, k, v, lens, new, *, dtype, out_dtype, begin=None, end=None, sc
             if L == 0 or m == 0:
                 assert not got[b, hq, :m].any()
                 continue
-            dq = (2.0 ** -31 if wide else 2.0 ** -20) * np.abs(qq).max(-1, keepdims=True) + (2.0 ** -22 if dtype == F32 else 0.0) * np.abs(qq)
+            big = np.abs(qq).max(-1, keepdims=True)
+            if dtype == F32:
+                dq = 2.0 ** -22 * np.abs(qq) + 2.0 ** -31 * big
+            else:
+                dq = np.where(np.abs(qq) < 2.0 ** -9 * big, (2.0 ** -31 if wide else 2.0 ** -17 if many and dtype == BF else 2.0 ** -20) * big, 0.0)
             e = sc * (dq @ np.abs(kk).T) + 130 * U * sc * (np.abs(qq) @ np.abs(kk).T)
             dist = np.abs(qp[:, None] - kp[None])
-            e = e + 8 * U * (softcap + np.abs(sl * dist) + sc * np.abs(qq @ kk.T))
+            e = e + 8 * U * (softcap * (2 if many else 1) + np.abs(sl * dist) + sc * np.abs(qq @ kk.T))
             e = np.where(p > 0, e, 0).max(-1, keepdims=True) if L else e
             rel = 2 * e + 2.0 ** -20
-            term, floor = (2.0 ** -22, 2.0 ** -32) if wide else (2.0 ** -11, 2.0 ** -21)
+            term, floor = (2.0 ** -22, 2.0 ** -32) if wide else (2.0 ** -8, 2.0 ** -14) if many and dtype == BF else (2.0 ** -11, 2.0 ** -17 if many else 2.0 ** -21)
             mass = p @ np.abs(vv)
-            tol = (rel + 2 * term + 2 * (140 + L / 128) * U) * mass
-            tol += 2 * floor * p.max(-1, keepdims=True) * np.abs(vv).sum(0) + np.abs(want) * torch.finfo(out_dtype).eps / 2 * 1.01
+            tol = (rel + 2 * (140 + L / 128) * U) * mass
+            tol += 2 * (np.minimum(p, term * p + floor * p.max(-1, keepdims=True)) @ np.abs(vv)) + np.abs(want) * torch.finfo(out_dtype).eps / 2 * 1.01
             tol += 1e-30 if wide or out_dtype == BF else 2.0 ** -25
             err = np.abs(got[b, hq, :m] - want)
+            # a number from half a step past the type's largest on rounds to infinity
+            past = np.abs(want) + tol >= float(torch.finfo(out_dtype).max) * (1 + torch.finfo(out_dtype).eps / 4)
+            err = np.where(past & (got[b, hq, :m] == np.where(want < 0, -np.inf, np.inf)), 0.0, err)
             assert np.all(err <= tol), (b, hq, (err / tol).max())
             worst = max(worst, (err / tol).max())
             if lse is not None:
                 empty = np.isneginf(wl)
                 assert np.array_equal(np.isneginf(lse[b, hq, :m]), empty)
-                d = np.abs(lse[b, hq, :m] - wl)[~empty]
+                d = np.abs(lse[b, hq, :m][~empty] - wl[~empty])
                 assert np.all(d <= (e[:, 0] + 2.0 ** -20 + (140 + L / 128) * U + 4 * U * np.abs(wl))[~empty])
             if weights is not None:
                 wsum[b, h, :L] += p.sum(0)
@@ -154,11 +163,64 @@ def test_causal_attention(ctx, case, dtype, out):
     check(np64(got), np64(q), k, v, lens, [n] * B, dtype=dtype, out_dtype=out, lse=np64(lse))
 
 
+PROMPTS = [  # B, heads_q, heads_kv, n_q, lens
+    (1, 1, 1, 65, [65]), (1, 1, 1, 128, [128]), (2, 2, 1, 129, [129, 1]), (1, 4, 1, 64, [64]), (1, 8, 2, 200, [1000]),
+    (3, 3, 1, 100, [100, 300, 163]), (2, 14, 2, 77, [400, 77]), (1, 16, 1, 257, [300]), (5, 4, 4, 70, [70, 71, 700, 128, 191]),
+    (1, 2, 2, 1000, [1300]), (1, 1, 1, 70, [9000]),
+]
+
+
+@pytest.mark.parametrize("case", PROMPTS, ids=lambda c: "-".join(map(str, c[:4])) + f"-{max(c[4])}")
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, HF), (F32, F32)])
+def test_prompts(ctx, case, dtype, out):
+    B, Hq, H, n, lens = case
+    cap = max(max(lens), n) + 70
+    cache, k, v = make(ctx, B, H, cap, lens, seed=sum(lens), paged=sum(lens) % 2 == 1)
+    q = queries(5, B, Hq, n, dtype, "tokens" if B % 2 else "heads")
+    lse = torch.empty(B, Hq, n, device=DEV)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, lse=lse, out_dtype=out)
+    check(np64(got), np64(q), k, v, lens, [n] * B, dtype=dtype, out_dtype=out, lse=np64(lse))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_prompts_whose_blocks_have_far_apart_values(ctx, dtype):
+    """Value scales of neighbouring blocks differ by up to 2^16, a block of zeros among them."""
+    B, Hq, H, n, N, cap = 1, 6, 2, 90, 640, 704
+    cache = tq.Cache(ctx, B, H, cap, device=DEV)
+    k, v = queries(1, B, H, N, BF), torch.randn(B, H, N, 128, generator=gen(2), device=DEV)
+    for j, e in enumerate([0, 16, 12, 8, 3, 0, 0, -8, 5, 5]):
+        v[:, :, 64 * j:64 * j + 64] *= 2.0 ** e if j != 6 else 0.0
+    tq.tq_q8_append(ctx.handle, cache, k, v.to(BF), ints([0]))
+    kv, vv = (np64(t) for t in tq.tq_dequantize(ctx.handle, cache, 0, cap))
+    q = queries(3, B, Hq, n, dtype)
+    rng = np.random.default_rng(1)
+    begin = rng.integers(0, N, (B, n))
+    end = np.minimum(begin + rng.integers(1, 200, (B, n)), N)
+    for kw in ({}, dict(key_begin=ints(begin), key_end=ints(end))):
+        got = tq.tq_q8_attention(ctx.handle, cache, q, ints([N]), cap, out_dtype=dtype, **kw)
+        check(np64(got), np64(q), kv, vv, [N], [n], dtype=dtype, out_dtype=dtype, begin=begin if kw else None, end=end if kw else None)
+
+
+def test_prompts_over_unmapped_blocks():
+    ctx = tq.Context(128, 8, "Q8", 1)
+    cache, k, v = make(ctx, 1, 2, 320, [300], seed=4, paged=True)
+    q = queries(5, 1, 4, 80, BF)
+    cache.block_table[0, 0, 1], cache.block_table[0, 1, 4] = -1, cache.pool_blocks
+    cache.block_table[0, 1, 2], cache.block_table[0, 1, 3] = -1, -1
+    end = ints([[300] * 80])
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints([300]), 320, key_end=end)
+    assert tq.tq_get_device_error(ctx.handle) == tq.TQ_ERR_ARG
+    k2, v2 = np.concatenate([k[:, :1, :64], k[:, :1, 128:300]], 2), np.concatenate([v[:, :1, :64], v[:, :1, 128:300]], 2)
+    check(np64(got[:, :2]), np64(q[:, :2]), k2, v2, [236], [80], dtype=BF, out_dtype=BF, end=[[236] * 80])
+    check(np64(got[:, 2:]), np64(q[:, 2:]), k[:, 1:], v[:, 1:], [128], [80], dtype=BF, out_dtype=BF, end=[[128] * 80])
+    ctx.close()
+
+
 @pytest.mark.parametrize("softcap,bias,mask,positions", [
     (20.0, False, "causal", False), (0.0, True, "causal", False), (30.0, True, "window", False), (0.0, False, "window", False),
     (0.0, False, "documents", False), (5.0, True, "documents", True), (0.0, True, "causal", True), (0.0, False, "empty", False)])
 @pytest.mark.parametrize("B,Hq,H,n,lens,new", [(2, 4, 2, 1, [400, 3], None), (3, 8, 2, 6, [300, 6, 0], [6, 4, 0]), (2, 6, 2, 40, [333, 129], [40, 17])])
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
 def test_caps_biases_and_masks(ctx, softcap, bias, mask, positions, B, Hq, H, n, lens, new, dtype):
     cap = 448
     rng = np.random.default_rng(n)
