@@ -339,8 +339,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         tc_fence_after_sync();
         // never 0, so that an unseen score of -inf stays -inf (products so small make no difference)
         const float c = fmaxf(qs * fmaxf(ks, 0.f) * (EXTRA ? 1.f : a.scale * kLog2e), 1e-30f);
-        // a score in log2 (EXTRA), or the raw product (the scaling is in c)
-        auto score = [&](float x, int i) {
+        // a score in log2 (EXTRA), or the raw product (the scaling is in c); MASK: unseen ones are -inf
+        auto score = [&](float x, int i, auto mask) {
           if constexpr (EXTRA) {
             x = capped_log2(x * c * sc.scale, sc);
             if (a.slopes) {
@@ -349,18 +349,27 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               x = fmaf(-slope, (float)__sad(qp, kp, 0u), x);
             }
           }
-          if (masked && (i < from || i >= to)) x = -INFINITY;
+          if constexpr (decltype(mask)::value) x = i >= from && i < to ? x : -INFINITY;
           return x;
         };
         // ---- the row's maximum over this half
         float top = -INFINITY;
+        auto maximum = [&](auto mask) {
+          float top1 = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[16];
-          tmem_ld_cols<16>(t_s + mine + 64 * half + 16 * q, x);
+          for (int q = 0; q < 4; ++q) {
+            float x[16];
+            tmem_ld_cols<16>(t_s + mine + 64 * half + 16 * q, x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) top = fmaxf(top, score(x[i], 16 * q + i));
-        }
+            for (int i = 0; i < 16; i += 4) {
+              top = fmaxf(top, fmaxf(score(x[i], 16 * q + i, mask), score(x[i + 1], 16 * q + i + 1, mask)));
+              top1 = fmaxf(top1, fmaxf(score(x[i + 2], 16 * q + i + 2, mask), score(x[i + 3], 16 * q + i + 3, mask)));
+            }
+          }
+          top = fmaxf(top, top1);
+        };
+        if (masked) maximum(std::true_type{});
+        else maximum(std::false_type{});
         if constexpr (!EXTRA) top = top == -INFINITY ? top : top * c;
         sm.top[rt][half][lrow] = top;
         bar_rt(rt);
@@ -375,53 +384,57 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         if (both && !apart) fold = __int_as_float((127 << 23) + __float_as_int(half ? vs1 : vs0) - __float_as_int(vmax));
         const float shift = 8.f - use + (float)log2i(fold);
         // ---- probabilities times 2^8, their terms over the scores they come from, their sum
-        float sum0 = 0.f, sum1 = 0.f;
-        uint32_t held[4];
+        float2 sum = make_float2(0.f, 0.f);
+        auto probabilities = [&](auto mask) {
+          const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+          uint32_t held[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[16];
-          const uint32_t at = t_s + mine + 64 * half + 16 * q;
-          tmem_ld_cols<16>(at, x);
-          uint32_t w[TERMS][4];
+          for (int q = 0; q < 4; ++q) {
+            float x[16];
+            tmem_ld_cols<16>(t_s + mine + 64 * half + 16 * q, x);
+            uint32_t w[TERMS][4];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            uint32_t t[TERMS][2];
+            for (int i = 0; i < 16; i += 4) {
+              uint32_t t[TERMS][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int k = i + 2 * u;
-              const float y0 = score(x[k], 16 * q + k), y1 = score(x[k + 1], 16 * q + k + 1);
-              const float p0 = ex2_approx(EXTRA ? y0 + shift : fmaf(y0, c, shift));
-              const float p1 = ex2_approx(EXTRA ? y1 + shift : fmaf(y1, c, shift));
-              sum0 += p0, sum1 += p1;
-              const __half2 hp = __floats2half2_rn(p0, p1);
-              uint32_t left = *reinterpret_cast<const uint32_t *>(&hp);
-              t[0][u] = h2_e4m3(left);
-              left = h2_sub(left, e4m3_h2(t[0][u]));
-              t[1][u] = h2_e4m3(left);
-              if constexpr (TERMS == 3) {
-                left = h2_sub(left, e4m3_h2(t[1][u]));
-                t[2][u] = h2_e5m2(left);
+              for (int u = 0; u < 2; ++u) {
+                const int k = i + 2 * u;
+                float2 y = make_float2(score(x[k], 16 * q + k, mask), score(x[k + 1], 16 * q + k + 1, mask));
+                y = EXTRA ? __fadd2_rn(y, shift2) : __ffma2_rn(y, c2, shift2);
+                y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                sum = __fadd2_rn(sum, y);
+                const __half2 hp = __floats2half2_rn(y.x, y.y);
+                uint32_t left = *reinterpret_cast<const uint32_t *>(&hp);
+                t[0][u] = h2_e4m3(left);
+                left = h2_sub(left, e4m3_h2(t[0][u]));
+                t[1][u] = h2_e4m3(left);
+                if constexpr (TERMS == 3) {
+                  left = h2_sub(left, e4m3_h2(t[1][u]));
+                  t[2][u] = h2_e5m2(left);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < TERMS; ++k) w[k][i / 4] = __byte_perm(t[k][0], t[k][1], 0x5410);
+            }
+            // a K-step's 32 tokens have 32 score columns; its term k goes to columns 8 k .. 8 k + 7 of them, where
+            // the scores were read by now, but for the third term's first half: that waits for the next 16
+            const uint32_t to = t_s + mine + 64 * half + 32 * (q >> 1) + 4 * (q & 1);
+            tmem_st_x4(to, w[0]);
+            tmem_st_x4(to + 8, w[1]);
+            if constexpr (TERMS == 3) {
+              if (q & 1) {
+                tmem_st_x4(to + 12, held);
+                tmem_st_x4(to + 16, w[2]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) held[i] = w[2][i];
               }
             }
-#pragma unroll
-            for (int k = 0; k < TERMS; ++k) w[k][i / 4] = t[k][0] | (t[k][1] << 16);
           }
-          // a K-step's 32 tokens have 32 score columns; its term k goes to columns 8 k .. 8 k + 7 of them, where
-          // the scores were read by now, but for the third term's first half: that waits for the next 16
-          const uint32_t to = t_s + mine + 64 * half + 32 * (q >> 1) + 4 * (q & 1);
-          tmem_st_x4(to, w[0]);
-          tmem_st_x4(to + 8, w[1]);
-          if constexpr (TERMS == 3) {
-            if (q & 1) {
-              tmem_st_x4(to + 12, held);
-              tmem_st_x4(to + 16, w[2]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) held[i] = w[2][i];
-            }
-          }
-        }
-        l = fmaf(l, corr, (sum0 + sum1) / fold);
+        };
+        if (masked) probabilities(std::true_type{});
+        else probabilities(std::false_type{});
+        l = fmaf(l, corr, (sum.x + sum.y) / fold);
         // value rows past the copied tokens, up to a whole K-step, hold what the cache holds there
         if (n < kTile && (n & 31)) {
           const int t = n + (tid & 255);
