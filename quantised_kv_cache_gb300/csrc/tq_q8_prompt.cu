@@ -6,7 +6,8 @@
 // (A operand). Two row tiles of 128 share a CTA and its key / value ring; each has two
 // threads a row, one for each 64-token block of a tile, and runs its own chain (scores, softmax, value
 // sums), so that one tile's tensor work hides behind the other's exponentials. O stays in registers (64
-// coordinates a thread), where the running maximum's corrections and the blocks' value scales multiply it.
+// coordinates a thread), where the running maximum's corrections and the blocks' value scales multiply it. MMAs and
+// copies are issued by warps of their own: an issue waits while the tensor cores' queue is full.
 //
 // Bound by issue and the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
 // product and two passes) and about 7 instructions an element. TERMS = 2 for bf16 (8 significant bits of
@@ -25,10 +26,11 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kUnit = 256;             // rows of a unit: two row tiles
-constexpr int kThreads = 512;
+constexpr int kSoft = 512;              // softmax threads; then a warpgroup of controllers:
+constexpr int kThreads = kSoft + 128;   // warps 16 and 17 issue a row tile's MMAs each, warp 18 the copies, warp 19 nothing
+constexpr int kRegsSoft = 112, kRegsControl = 32;  // 512 * 112 + 128 * 32 = 640 * 96, what the block is launched with
 constexpr int kStage = 2 * kTile * kD;
 constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
-constexpr int kAhead = 64;             // tiles whose sources are looked up at once
 constexpr int kPartRow = kD + 4;       // O, m, l, 2 pad
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
 
@@ -106,15 +108,44 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p) {
 }
 
 struct Shared {
-  uint64_t full[4], empty[4], bar_s[2], bar_o[2];
-  float4 info[kAhead];        // key scales of a tile's two blocks, value scales (negative: not there)
-  long long src[kAhead][2];   // its blocks
+  uint64_t full[4], empty[4];
+  uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2];  // of a row tile: queries, scores, probabilities, value sums are there
+  float4 info[4];             // of a stage: key scales of the tile's two blocks, value scales (negative: not there)
   float top[2][2][128];       // [row tile][half]: row maxima, then sums
   uint32_t tmem;
   int bad;
 };
 
+// The unit of work at tile g of the slice that ends at g1: entry e, KV head h, from tile t0 of its cnt on, up to g = end.
+struct Unit {
+  int e, h, b, pair, t0, cnt;
+  long long end;
+};
+__device__ __forceinline__ Unit unit_at(const Plan &p, int heads, long long g, long long g1) {
+  Unit u;
+  int lo = 0, hi = p.entries - 1;
+  while (lo < hi) {  // the last entry that begins at or before g
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)p.pre[mid] * heads <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  u.e = lo, u.cnt = p.pre[lo + 1] - p.pre[lo];
+  const long long in = g - (long long)p.pre[lo] * heads;
+  u.h = (int)(in / u.cnt), u.t0 = (int)(in - (long long)u.h * u.cnt);
+  u.b = lo / p.pairs, u.pair = lo % p.pairs;
+  u.end = min(g1, g - u.t0 + u.cnt);
+  return u;
+}
+
+// A tile's two blocks have value scales too far apart to be folded into one sum.
+__device__ __forceinline__ bool scales_apart(const float4 &f) {
+  return f.z >= 0.f && f.w >= 0.f && fminf(f.z, f.w) < fmaxf(f.z, f.w) * kFold;
+}
+
 __device__ __forceinline__ void bar_rt(int rt) { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // D (TMEM) (+)= A (TMEM, four 8-bit K-elements per column) x B (shared); issued by one thread.
 __device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -170,173 +201,211 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   __shared__ Shared sm;
   uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage;  // [row tile][term][128 x 128]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rt = tid >> 8, half = (tid >> 7) & 1, lrow = tid & 127, w4 = warp & 3;
-  const int G = a.group, R = G * a.n_q;
-  const bool leader = (tid & 255) == 0;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 2);
-    for (int r = 0; r < 2; ++r) mbar_init(&sm.bar_s[r], 1), mbar_init(&sm.bar_o[r], 1);
+    for (int r = 0; r < 2; ++r) {
+      mbar_init(&sm.bar_s[r], 1), mbar_init(&sm.bar_o[r], 1);
+      mbar_init(&sm.bar_q[r], 8), mbar_init(&sm.bar_p[r], 8);  // a row tile's warps
+    }
     mbar_fence_init();
     sm.bad = 0;
   }
-  if (warp == 0) {
+  if (warp == kSoft / 32 + 2) {
     tmem_alloc(smem_u32(&sm.tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = sm.tmem, t_s = tmem + rt * 256, t_o = t_s + 128;
-  const uint32_t mine = ((uint32_t)(32 * w4) << 16);
+  const uint32_t tmem = sm.tmem;
 
   const long long total = (long long)p.pre[p.entries] * a.heads_kv;
   const long long slices = min((long long)gridDim.x, total);
   const bool idle = blockIdx.x >= slices;
   const long long g0 = idle ? 0 : total * blockIdx.x / slices, g1 = idle ? 0 : total * (blockIdx.x + 1) / slices;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      if (mbar_try_wait(bar, parity)) return;
     if (*(volatile int *)&sm.bad) return;
     if (!mbar_wait_bounded(bar, parity, a.error)) *(volatile int *)&sm.bad = 1;
   };
-  const uint32_t idesc_s[2] = {tc_idesc_f8(128, 128, 0, 0, 0, 0), tc_idesc_f8(128, 128, 1, 0, 0, 0)};
-  const uint32_t idesc_o[2] = {tc_idesc_f8(128, 128, 0, 0, 0, 1), tc_idesc_f8(128, 128, 1, 0, 0, 1)};
-  const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
-  int it = 0;              // tiles done before the current chunk: stages and phases count on
-  int filled = 0;          // tiles whose copies were issued (thread 0)
-  uint32_t phase_s = 0, phase_o = 0;
 
-  long long g = g0;
-  while (g < g1) {
-    // ---- the unit at g
-    int e;
-    {
-      int lo = 0, hi = p.entries - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((long long)p.pre[mid] * a.heads_kv <= g) lo = mid;
-        else hi = mid - 1;
+  if (warp >= kSoft / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == kSoft / 32 + 2) {
+      // ================================ copies: a lane finds the sources of one of a unit's next 32 tiles
+      int it = 0;
+      for (long long g = g0; g < g1;) {
+        const Unit u = unit_at(p, a.heads_kv, g, g1);
+        const Entry en = p.entry[u.e];
+        const long long blocks = ((long long)u.b * a.heads_kv + u.h) * a.c.nblk;
+        for (int k0 = 0; g + k0 < u.end; k0 += 32) {
+          const int todo = (int)min(32ll, u.end - g - k0);
+          long long src[2] = {-1, -1};
+          float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
+          int bytes[2] = {0, 0};
+          if (lane < todo) {
+            const int tok = (en.lo + u.t0 + k0 + lane) * kTile, n = min(kTile, max(0, en.hi - tok));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int m = min(kQ8Block, n - k * kQ8Block);
+              if (m <= 0) continue;
+              src[k] = q8_block(a.c.btab, a.c.pool_blocks, blocks + tok / kQ8Block + k, a.error);
+              if (src[k] < 0) continue;
+              bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
+              (k ? f.y : f.x) = __ldg(a.c.ks + src[k]);
+              (k ? f.w : f.z) = __ldg(a.c.vs + src[k]);
+            }
+          }
+          for (int k = 0; k < todo; ++k, ++it) {
+            const int s = it % kStages;
+            const long long s0 = __shfl_sync(kFull, src[0], k), s1 = __shfl_sync(kFull, src[1], k);
+            const int n0 = __shfl_sync(kFull, bytes[0], k), n1 = __shfl_sync(kFull, bytes[1], k);
+            float4 x;
+            x.x = __shfl_sync(kFull, f.x, k), x.y = __shfl_sync(kFull, f.y, k);
+            x.z = __shfl_sync(kFull, f.z, k), x.w = __shfl_sync(kFull, f.w, k);
+            if (lane == 0) {
+              wait(&sm.empty[s], ((it / kStages) & 1) ^ 1);
+              if (!*(volatile int *)&sm.bad) {
+                sm.info[s] = x;
+                uint8_t *dst = ring + s * kStage;
+                mbar_arrive_expect_tx(&sm.full[s], 2 * (n0 + n1));
+                if (n0) {
+                  const uint8_t *q = a.c.records + s0 * kQ8BlockBytes;
+                  tma_load_1d(dst, q, n0, &sm.full[s]);
+                  tma_load_1d(dst + kTile * kD, q + kQ8Plane, n0, &sm.full[s]);
+                }
+                if (n1) {
+                  const uint8_t *q = a.c.records + s1 * kQ8BlockBytes;
+                  tma_load_1d(dst + kQ8Plane, q, n1, &sm.full[s]);
+                  tma_load_1d(dst + kTile * kD + kQ8Plane, q + kQ8Plane, n1, &sm.full[s]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+        }
+        g = u.end;
       }
-      e = lo;
+      // every copy lands before the CTA's shared memory goes: the last fill of each stage
+      if (lane == 0)
+        for (int k = max(0, it - kStages); k < it; ++k)
+          mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, nullptr, kWaitBudgetNs / 8);
+      __syncwarp();
+    } else if (warp < kSoft / 32 + 2) {
+      // ================================ a row tile's MMAs, one thread
+      if (lane == 0) {
+        const int rt = warp - kSoft / 32;
+        const uint32_t t_s = tmem + rt * 256, t_o = t_s + 128, q = smem_u32(qbuf + rt * TERMS * kQTerm);
+        uint32_t units = 0, probs = 0;
+        int it = 0;
+        for (long long g = g0; g < g1; ++units) {
+          const Unit u = unit_at(p, a.heads_kv, g, g1);
+          const int first = p.entry[u.e].lo + u.t0, hi = p.entry[u.e].hi, todo = (int)(u.end - g);
+          wait(&sm.bar_q[rt], units & 1);
+          for (int j = 0; j <= todo; ++j) {
+            // the value sums of tile j - 1, then the scores of tile j over its probabilities: in this order, as issued
+            if (j > 0) {
+              const int s = (it + j - 1) % kStages, n = min(kTile, max(0, hi - (first + j - 1) * kTile));
+              const float4 f = sm.info[s];
+              const bool apart = scales_apart(f);
+              const uint32_t vt = smem_u32(ring + s * kStage) + kTile * kD;
+              for (int part = 0; part <= (int)apart; ++part) {  // the two blocks at once, or one after the other
+                wait(&sm.bar_p[rt], probs & 1);
+                ++probs;
+                tc_fence_after_sync();
+                bool more = false;
+                for (int t = 0; t < TERMS; ++t)
+                  for (int k = 2 * part; k < (apart ? 2 * part + 2 : 4); ++k) {
+                    if (k * 32 >= n || (k < 2 ? f.z : f.w) < 0.f) continue;
+                    tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
+                                 tc_idesc_f8(128, 128, t == 2, 0, 0, 1), more);
+                    more = true;
+                  }
+                if (part == (int)apart) tc_commit(smem_u32(&sm.empty[s]));
+                tc_commit(smem_u32(&sm.bar_o[rt]));
+              }
+            }
+            if (j < todo) {
+              const int s = (it + j) % kStages;
+              wait(&sm.full[s], ((it + j) / kStages) & 1);
+              tc_fence_after_sync();
+              const uint32_t kt = smem_u32(ring + s * kStage);
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                for (int k = 0; k < kD / 32; ++k)
+                  tc_mma_f8(t_s, tc_sdesc_kmajor(q + t * kQTerm + 256 * k, 128, 1024), tc_sdesc_kmajor(kt + 256 * k, 128, 1024),
+                            tc_idesc_f8(128, 128, t == 2, 0, 0, 0), t > 0 || k > 0);
+              tc_commit(smem_u32(&sm.bar_s[rt]));
+            }
+          }
+          it += todo;
+          g = u.end;
+        }
+      }
+      __syncwarp();
     }
-    const int cnt = p.pre[e + 1] - p.pre[e];
-    const long long in = g - (long long)p.pre[e] * a.heads_kv;
-    const int h = (int)(in / cnt), t0 = (int)(in - (long long)h * cnt);
-    const int b = e / p.pairs, pair = e % p.pairs;
-    const long long end = min(g1, g - t0 + cnt);
-    const Entry en = p.entry[e];
-    int len, m;
-    seq_sizes(a, b, &len, &m, false);
-    const long long bh = (long long)b * a.heads_kv + h;
+  } else {
+    // ================================ softmax and output: two threads a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int rt = tid >> 8, half = (tid >> 7) & 1, lrow = tid & 127;
+    const uint32_t t_s = tmem + rt * 256 + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half, t_o = t_s + 128;
+    const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
+    int it = 0;  // tiles done: stages and phases count on
+    uint32_t sums = 0;
+    long long g = g0;
+    while (g < g1) {
+      const Unit u = unit_at(p, a.heads_kv, g, g1);
+      const int first = p.entry[u.e].lo + u.t0, hi = p.entry[u.e].hi, maxbeg = p.entry[u.e].maxbeg,
+                minend = p.entry[u.e].minend;
+      const long long bh = (long long)u.b * a.heads_kv + u.h;
+      int len, m;
+      seq_sizes(a, u.b, &len, &m, false);
+      const int G = a.group, R = G * a.n_q;
 
-    // ---- queries: a warp prepares 16 rows, their terms to shared memory, their powers of two kept for a moment there
-    __syncthreads();
+      // ---- queries: a warp prepares 16 rows of its row tile (whose score MMAs of the unit before are done)
+      bar_rt(rt);
 #pragma unroll 4
-    for (int k = 0; k < 16; ++k) {
-      const int r = warp * 16 + k, row = pair * kUnit + r, i = row / G;
-      uint32_t w[1][3];
-      const int ex = row_terms<1>(a, b, h * G + row % G, i, row < R && i < m, lane, w);
+      for (int k = 0; k < 16; ++k) {
+        const int r = (warp & 7) * 16 + k, row = u.pair * kUnit + rt * 128 + r, i = row / G;
+        uint32_t w[1][3];
+        const int ex = row_terms<1>(a, u.b, u.h * G + row % G, i, row < R && i < m, lane, w);
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-        *reinterpret_cast<uint32_t *>(qbuf + ((r >> 7) * TERMS + t) * kQTerm + q8_off(r & 127, 4 * lane)) = w[0][t];
-      if (lane == 0) sm.top[r >> 7][0][r & 127] = pow2i(ex);
-    }
-    fence_proxy_async_shared();
-    __syncthreads();
-    const float qs = sm.top[rt][0][lrow];
-    const int row = pair * kUnit + rt * 128 + lrow, qi = row / G, hq = h * G + row % G;
-    const bool live = row < R && qi < m;
-    const int2 rg = live ? row_range(a, b, qi, len, m) : make_int2(0, 0);
-    const float slope = EXTRA && live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-    const int qp = !EXTRA || !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + qi) : len - m + qi;
-
-    float2 o[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = make_float2(0.f, 0.f);
-    float mx = -INFINITY, l = 0.f;
-
-    for (long long c0 = g; c0 < end; c0 += kAhead) {
-      const int todo = (int)min((long long)kAhead, end - c0);
-      const int tile0 = en.lo + t0 + (int)(c0 - g);
-      __syncthreads();
-      if (tid < todo) {  // the chunk's sources
-        const int tok = (tile0 + tid) * kTile, n = min(kTile, max(0, en.hi - tok));
-        float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          long long blk = -1;
-          if (n > k * kQ8Block) blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok / kQ8Block + k, a.error);
-          if (blk >= 0) {
-            (k ? f.y : f.x) = __ldg(a.c.ks + blk);
-            (k ? f.w : f.z) = __ldg(a.c.vs + blk);
-          }
-          sm.src[tid][k] = blk;
-        }
-        sm.info[tid] = f;
+        for (int t = 0; t < TERMS; ++t)
+          *reinterpret_cast<uint32_t *>(qbuf + (rt * TERMS + t) * kQTerm + q8_off(r, 4 * lane)) = w[0][t];
+        if (lane == 0) sm.top[rt][0][r] = pow2i(ex);
       }
-      __syncthreads();
-      const int last = it + todo;
-      auto fill = [&](int upto, bool block) {  // thread 0: issue the copies of tiles < upto (and beyond, while stages are free)
-        while (filled < last) {
-          const int s = filled % kStages;
-          if (filled >= kStages) {
-            const uint32_t par = ((filled / kStages) & 1) ^ 1;
-            if (filled < upto && block) wait(&sm.empty[s], par);
-            else if (!mbar_test_wait(&sm.empty[s], par)) return;
-          }
-          if (*(volatile int *)&sm.bad) return;
-          const int k = filled - it, tok = (tile0 + k) * kTile, n = min(kTile, max(0, en.hi - tok));
-          uint8_t *dst = ring + s * kStage;
-          const long long b0 = sm.src[k][0], b1 = sm.src[k][1];
-          const int n0 = b0 >= 0 ? (min(kQ8Block, n) + 31) / 32 * 32 * kD : 0;
-          const int n1 = b1 >= 0 ? (n - kQ8Block + 31) / 32 * 32 * kD : 0;
-          mbar_arrive_expect_tx(&sm.full[s], 2 * (n0 + n1));
-          if (n0) {
-            const uint8_t *q = a.c.records + b0 * kQ8BlockBytes;
-            tma_load_1d(dst, q, n0, &sm.full[s]);
-            tma_load_1d(dst + kTile * kD, q + kQ8Plane, n0, &sm.full[s]);
-          }
-          if (n1) {
-            const uint8_t *q = a.c.records + b1 * kQ8BlockBytes;
-            tma_load_1d(dst + kQ8Plane, q, n1, &sm.full[s]);
-            tma_load_1d(dst + kTile * kD + kQ8Plane, q + kQ8Plane, n1, &sm.full[s]);
-          }
-          ++filled;
-        }
-      };
-      auto scores = [&](int j) {  // a leader: S of tile j
-        if (tid == 0) fill(j + 1, true);
-        const int s = j % kStages;
-        wait(&sm.full[s], (j / kStages) & 1);
-        tc_fence_after_sync();
-        const uint32_t kt = smem_u32(ring + s * kStage);
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-          const uint32_t q = smem_u32(qbuf + (rt * TERMS + t) * kQTerm);
-#pragma unroll
-          for (int k = 0; k < kD / 32; ++k)
-            tc_mma_f8(t_s, tc_sdesc_kmajor(q + 256 * k, 128, 1024), tc_sdesc_kmajor(kt + 256 * k, 128, 1024),
-                      idesc_s[t == 2], t > 0 || k > 0);
-        }
-        tc_commit(smem_u32(&sm.bar_s[rt]));
-      };
-      if (leader) scores(it);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.bar_q[rt]);
+      bar_rt(rt);
+      const float qs = sm.top[rt][0][lrow];
+      const int row = u.pair * kUnit + rt * 128 + lrow, qi = row / G, hq = u.h * G + row % G;
+      const bool live = row < R && qi < m;
+      const int2 rg = live ? row_range(a, u.b, qi, len, m) : make_int2(0, 0);
+      const float slope = EXTRA && live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+      const int qp = !EXTRA || !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)u.b * a.n_q + qi) : len - m + qi;
+      bar_rt(rt);
 
-      for (int j = it; j < last; ++j) {
-        const int s = j % kStages, tok0 = (tile0 + j - it) * kTile, n = min(kTile, max(0, en.hi - tok0));
-        const float4 f = sm.info[j - it];
+      float o[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) o[i] = 0.f;
+      float mx = -INFINITY, l = 0.f;
+      const int todo = (int)(u.end - g);
+      for (int j = 0; j < todo; ++j) {
+        const int s = (it + j) % kStages, tok0 = (first + j) * kTile, n = min(kTile, max(0, hi - tok0));
+        wait(&sm.full[s], ((it + j) / kStages) & 1);
+        const float4 f = sm.info[s];
         const float ks = half ? f.y : f.x;
-        uint8_t *const vt = ring + s * kStage + kTile * kD;
-        const bool masked = !(en.maxbeg <= tok0 && en.minend >= tok0 + kTile) || f.x < 0.f || f.y < 0.f;
-        // bits of the 64 tokens of this half that the row sees
-        int from = 0, to = 64;
+        const bool masked = !(maxbeg <= tok0 && minend >= tok0 + kTile) || f.x < 0.f || f.y < 0.f;
+        int from = 0, to = 64;  // the tokens of this half that the row sees
         if (masked) {
           from = min(max(rg.x - tok0 - 64 * half, 0), 64), to = min(max(rg.y - tok0 - 64 * half, 0), 64);
           if (ks < 0.f) to = 0;
         }
-        wait(&sm.bar_s[rt], phase_s & 1);
-        ++phase_s;
-        __syncwarp();
-        tc_fence_after_sync();
         // never 0, so that an unseen score of -inf stays -inf (products so small make no difference)
         const float c = fmaxf(qs * fmaxf(ks, 0.f) * (EXTRA ? 1.f : a.scale * kLog2e), 1e-30f);
         // a score in log2 (EXTRA), or the raw product (the scaling is in c); MASK: unseen ones are -inf
@@ -345,13 +414,16 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             x = capped_log2(x * c * sc.scale, sc);
             if (a.slopes) {
               const int slot = tok0 + 64 * half + i;
-              const int kp = a.kpos ? (slot < en.hi ? __ldg(a.kpos + bh * a.c.capacity + slot) : 0) : slot;
+              const int kp = a.kpos ? (slot < hi ? __ldg(a.kpos + bh * a.c.capacity + slot) : 0) : slot;
               x = fmaf(-slope, (float)__sad(qp, kp, 0u), x);
             }
           }
           if constexpr (decltype(mask)::value) x = i >= from && i < to ? x : -INFINITY;
           return x;
         };
+        wait(&sm.bar_s[rt], (it + j) & 1);
+        __syncwarp();  // tensor memory is read by whole warps
+        tc_fence_after_sync();
         // ---- the row's maximum over this half
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
@@ -359,7 +431,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float x[16];
-            tmem_ld_cols<16>(t_s + mine + 64 * half + 16 * q, x);
+            tmem_ld_cols<16>(t_s + 16 * q, x);
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
               top = fmaxf(top, fmaxf(score(x[i], 16 * q + i, mask), score(x[i + 1], 16 * q + i + 1, mask)));
@@ -378,39 +450,39 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         const float corr = ex2_approx(mx - use);
         mx = top;
         // ---- the two blocks' value scales: folded into the probabilities, or two sums
-        const float vs0 = f.z, vs1 = f.w, vmax = fmaxf(fmaxf(vs0, vs1), 0.f);
-        const bool both = vs0 >= 0.f && vs1 >= 0.f, apart = both && fminf(vs0, vs1) < vmax * kFold;
+        const bool apart = scales_apart(f);
+        const float vmax = fmaxf(fmaxf(f.z, f.w), 0.f);
         float fold = 1.f;
-        if (both && !apart) fold = __int_as_float((127 << 23) + __float_as_int(half ? vs1 : vs0) - __float_as_int(vmax));
+        if (f.z >= 0.f && f.w >= 0.f && !apart)
+          fold = __int_as_float((127 << 23) + __float_as_int(half ? f.w : f.z) - __float_as_int(vmax));
         const float shift = 8.f - use + (float)log2i(fold);
         // ---- probabilities times 2^8, their terms over the scores they come from, their sum
         float2 sum = make_float2(0.f, 0.f);
         auto probabilities = [&](auto mask) {
-          const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
           uint32_t held[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float x[16];
-            tmem_ld_cols<16>(t_s + mine + 64 * half + 16 * q, x);
+            tmem_ld_cols<16>(t_s + 16 * q, x);
             uint32_t w[TERMS][4];
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
               uint32_t t[TERMS][2];
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int k = i + 2 * u;
-                float2 y = make_float2(score(x[k], 16 * q + k, mask), score(x[k + 1], 16 * q + k + 1, mask));
-                y = EXTRA ? __fadd2_rn(y, shift2) : __ffma2_rn(y, c2, shift2);
-                y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                sum = __fadd2_rn(sum, y);
-                const __half2 hp = __floats2half2_rn(y.x, y.y);
+              for (int v = 0; v < 2; ++v) {
+                const int k = i + 2 * v;
+                const float y0 = score(x[k], 16 * q + k, mask), y1 = score(x[k + 1], 16 * q + k + 1, mask);
+                const float p0 = ex2_approx(EXTRA ? y0 + shift : fmaf(y0, c, shift));
+                const float p1 = ex2_approx(EXTRA ? y1 + shift : fmaf(y1, c, shift));
+                sum.x += p0, sum.y += p1;
+                const __half2 hp = __floats2half2_rn(p0, p1);
                 uint32_t left = *reinterpret_cast<const uint32_t *>(&hp);
-                t[0][u] = h2_e4m3(left);
-                left = h2_sub(left, e4m3_h2(t[0][u]));
-                t[1][u] = h2_e4m3(left);
+                t[0][v] = h2_e4m3(left);
+                left = h2_sub(left, e4m3_h2(t[0][v]));
+                t[1][v] = h2_e4m3(left);
                 if constexpr (TERMS == 3) {
-                  left = h2_sub(left, e4m3_h2(t[1][u]));
-                  t[2][u] = h2_e5m2(left);
+                  left = h2_sub(left, e4m3_h2(t[1][v]));
+                  t[2][v] = h2_e5m2(left);
                 }
               }
 #pragma unroll
@@ -418,13 +490,13 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             }
             // a K-step's 32 tokens have 32 score columns; its term k goes to columns 8 k .. 8 k + 7 of them, where
             // the scores were read by now, but for the third term's first half: that waits for the next 16
-            const uint32_t to = t_s + mine + 64 * half + 32 * (q >> 1) + 4 * (q & 1);
-            tmem_st_x4(to, w[0]);
-            tmem_st_x4(to + 8, w[1]);
+            const uint32_t at = t_s + 32 * (q >> 1) + 4 * (q & 1);
+            tmem_st_x4(at, w[0]);
+            tmem_st_x4(at + 8, w[1]);
             if constexpr (TERMS == 3) {
               if (q & 1) {
-                tmem_st_x4(to + 12, held);
-                tmem_st_x4(to + 16, w[2]);
+                tmem_st_x4(at + 12, held);
+                tmem_st_x4(at + 16, w[2]);
               } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) held[i] = w[2][i];
@@ -436,127 +508,87 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         else probabilities(std::false_type{});
         l = fmaf(l, corr, (sum.x + sum.y) / fold);
         // value rows past the copied tokens, up to a whole K-step, hold what the cache holds there
-        if (n < kTile && (n & 31)) {
+        if (n & 31) {
           const int t = n + (tid & 255);
           if (t < ((n + 31) & ~31)) {
+            uint8_t *vt = ring + s * kStage + kTile * kD;
 #pragma unroll
             for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(vt + q8_off(t, 16 * k)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_shared();
         }
         tmem_st_wait();
-        auto values = [&](int from_step, int to_step) {  // a leader: D = P V over the K-steps
-          bool first = true;
+        // O = O corr + vs D
+        auto add = [&](float vs, float by) {
+          if (!__all_sync(kFull, by == 1.f)) {
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t)
-            for (int k = from_step; k < to_step; ++k) {
-              if (k * 32 >= n || (k < 2 ? vs0 : vs1) < 0.f) continue;
-              tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(smem_u32(vt) + 4096 * k, 1024, 128), idesc_o[t == 2],
-                           !first);
-              first = false;
-            }
-        };
-        auto add = [&](float vs, float by) {  // O = O by + vs D
-          const bool same = __all_sync(kFull, by == 1.f);
-          const float2 v2 = make_float2(vs, vs), b2 = make_float2(by, by);
+            for (int i = 0; i < 64; ++i) o[i] *= by;
+          }
+          if (vs < 0.f) return;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float d[16];
-            tmem_ld_cols<16>(t_o + mine + 64 * half + 16 * q, d);
+            tmem_ld_cols<16>(t_o + 16 * q, d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float2 &y = o[8 * q + i];
-              if (!same) y = __fmul2_rn(y, b2);
-              y = __ffma2_rn(make_float2(d[2 * i], d[2 * i + 1]), v2, y);
-            }
+            for (int i = 0; i < 16; ++i) o[16 * q + i] = fmaf(d[i], vs, o[16 * q + i]);
           }
         };
-        tc_fence_before_sync();
-        bar_rt(rt);
-        const bool some = vs0 >= 0.f || vs1 >= 0.f;
-        if (!apart) {
-          if (leader) {
-            tc_fence_after_sync();
-            values(0, 4);
-            tc_commit(smem_u32(&sm.empty[s]));
-            tc_commit(smem_u32(&sm.bar_o[rt]));
-            if (tid == 0) fill(0, false);
-          }
-          wait(&sm.bar_o[rt], phase_o & 1);
-          ++phase_o;
+        for (int part = 0; part <= (int)apart; ++part) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.bar_p[rt]);
+          wait(&sm.bar_o[rt], sums & 1);
+          ++sums;
+          __syncwarp();
           tc_fence_after_sync();
-          if (leader && j + 1 < last) scores(j + 1);
-          __syncwarp();
-          if (some) add(vmax, corr);
-          else
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __fmul2_rn(o[i], make_float2(corr, corr));
-        } else {
-          for (int k = 0; k < 2; ++k) {
-            if (leader) {
-              tc_fence_after_sync();
-              values(2 * k, 2 * k + 2);
-              if (k) tc_commit(smem_u32(&sm.empty[s]));
-              tc_commit(smem_u32(&sm.bar_o[rt]));
-            }
-            wait(&sm.bar_o[rt], phase_o & 1);
-            ++phase_o;
-            __syncwarp();
-            tc_fence_after_sync();
-            add(k ? vs1 : vs0, k ? 1.f : corr);
-            tc_fence_before_sync();
-            bar_rt(rt);
-          }
-          if (leader && j + 1 < last) scores(j + 1);
-          __syncwarp();
+          add(!apart ? (f.z < 0.f && f.w < 0.f ? -1.f : vmax) : part ? f.w : f.z, part ? 1.f : corr);
         }
-        tc_fence_before_sync();
       }
-      it = last;
-    }
+      it += todo;
 
-    // ---- the unit's rows
-    sm.top[rt][half][lrow] = l;
-    bar_rt(rt);
-    l += sm.top[rt][half ^ 1][lrow];
-    const bool whole = t0 == 0 && end == g + cnt;
-    if (live) {
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long off = b * a.os.b + hq * a.os.h + qi * a.os.t + 64 * half;
+      // ---- the unit's rows
+      sm.top[rt][half][lrow] = l;
+      bar_rt(rt);
+      l += sm.top[rt][half ^ 1][lrow];
+      const bool whole = u.t0 == 0 && u.end == g + u.cnt;
+      if (live) {
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const long long off = u.b * a.os.b + hq * a.os.h + qi * a.os.t + 64 * half;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float y[8];
+          for (int q = 0; q < 8; ++q) {
+            float y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[2 * i] = o[4 * q + i].x * inv, y[2 * i + 1] = o[4 * q + i].y * inv;
-          if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) + off + 8 * q, y);
-          else store_vec<__half, 8>(static_cast<__half *>(a.out) + off + 8 * q, y);
+            for (int i = 0; i < 8; ++i) y[i] = o[8 * q + i] * inv;
+            if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) + off + 8 * q, y);
+            else store_vec<__half, 8>(static_cast<__half *>(a.out) + off + 8 * q, y);
+          }
+          if (a.lse && !half) a.lse[((long long)u.b * a.heads_q + hq) * a.n_q + qi] = (mx + log2f(l) - 8.f) * kLn2;
+        } else {
+          float *part = p.parts + (((long long)blockIdx.x * 2 + (u.t0 == 0 ? 1 : 0)) * kUnit + rt * 128 + lrow) * kPartRow;
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            reinterpret_cast<float4 *>(part + 64 * half)[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          if (!half) part[kD] = mx, part[kD + 1] = l;
         }
-        if (a.lse && !half) a.lse[((long long)b * a.heads_q + hq) * a.n_q + qi] = (mx + log2f(l) - 8.f) * kLn2;
-      } else {
-        float *part = p.parts + (((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kUnit + rt * 128 + lrow) * kPartRow;
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          reinterpret_cast<float4 *>(part + 64 * half)[q] = make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
-        if (!half) part[kD] = mx, part[kD + 1] = l;
       }
-    }
-    if (tid == 0 && end == g1) {
-      const long long stop = g - t0 + cnt;
-      int parts = 0;
-      if (t0 == 0 && stop > g1) {
-        parts = 1;
-        for (long long k = blockIdx.x + 1; k < slices && total * k / slices < stop; ++k) ++parts;
+      if (tid == 0 && u.end == g1) {
+        const long long stop = g - u.t0 + u.cnt;
+        int parts = 0;
+        if (u.t0 == 0 && stop > g1) {
+          parts = 1;
+          for (long long k = blockIdx.x + 1; k < slices && total * k / slices < stop; ++k) ++parts;
+        }
+        p.cuts[blockIdx.x] = Cut{u.b, u.pair, u.h, parts};
       }
-      p.cuts[blockIdx.x] = Cut{b, pair, h, parts};
+      g = u.end;
     }
-    g = end;
+    if (tid == 0 && idle) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0};
   }
-  if (tid == 0 && idle) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0};
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == kSoft / 32 + 2) tmem_dealloc(tmem, 512);
 }
 
 // The rows of a unit that was cut: one warp per row, lane = 4 coordinates.
