@@ -45,7 +45,9 @@ struct Cut {
 };
 
 struct Shared {
-  uint64_t full[5], empty[5], bar_s[kWg], bar_o[kWg];
+  // A tile's arrival barrier is one of stages x warpgroups, so that its earlier use was the same warpgroup's: a
+  // warpgroup that is ahead would take a parity of a stage's older, still incomplete copy for its own.
+  uint64_t full[5 * kWg], empty[5], bar_s[kWg], bar_o[kWg];
   float4 info[5];            // key scales of the tile's two blocks, value scales (negative: not mapped)
   float qscale[kRows], slope[kRows];
   int2 range[kRows];
@@ -71,7 +73,8 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   const int G = a.group, R = G * a.n_q;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 1);
+    for (int s = 0; s < kStages * kWg; ++s) mbar_init(&sm.full[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.empty[s], 1);
     for (int w = 0; w < kWg; ++w) mbar_init(&sm.bar_s[w], 1), mbar_init(&sm.bar_o[w], 1);
     mbar_fence_init();
     sm.bad = 0;
@@ -178,16 +181,17 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           if (!*(volatile int *)&sm.bad) {
             sm.info[s] = f;
             uint8_t *dst = ring + s * kStage;
-            mbar_arrive_expect_tx(&sm.full[s], 2 * (n0 + n1));
+            uint64_t *full = &sm.full[it % (kStages * kWg)];
+            mbar_arrive_expect_tx(full, 2 * (n0 + n1));
             if (n0) {
               const uint8_t *p = a.c.records + s0 * kQ8BlockBytes;
-              tma_load_1d(dst, p, n0, &sm.full[s]);
-              tma_load_1d(dst + kTile * kD, p + kQ8Plane, n0, &sm.full[s]);
+              tma_load_1d(dst, p, n0, full);
+              tma_load_1d(dst + kTile * kD, p + kQ8Plane, n0, full);
             }
             if (n1) {
               const uint8_t *p = a.c.records + s1 * kQ8BlockBytes;
-              tma_load_1d(dst + kQ8Plane, p, n1, &sm.full[s]);
-              tma_load_1d(dst + kTile * kD + kQ8Plane, p + kQ8Plane, n1, &sm.full[s]);
+              tma_load_1d(dst + kQ8Plane, p, n1, full);
+              tma_load_1d(dst + kTile * kD + kQ8Plane, p + kQ8Plane, n1, full);
             }
           }
         }
@@ -197,7 +201,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     // every copy lands before the CTA's shared memory goes: the last fill of each stage
     if (lane == 0) {
       for (int k = max(0, it - kStages); k < it; ++k)
-        mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, nullptr, kWaitBudgetNs / 8);
+        mbar_wait_bounded(&sm.full[k % (kStages * kWg)], (k / (kStages * kWg)) & 1, nullptr, kWaitBudgetNs / 8);
     }
     __syncwarp();
   } else {
@@ -207,8 +211,8 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     const uint32_t lanes = (uint32_t)(32 * w4) << 16;
     uint8_t *const pmine = pbuf + wg * GR * 3 * kTerm;
     uint8_t *const pbyte = pmine + (wt >> 4) * 128 + (wt & 15);
-    const uint32_t idesc_s[2] = {tc_idesc_f8(128, kRows, 0, 0, 0, 0), tc_idesc_f8(128, kRows, 0, 1, 0, 0)};
-    const uint32_t idesc_o[2] = {tc_idesc_f8(128, kRows, 0, 0, 1, 0), tc_idesc_f8(128, kRows, 0, 1, 1, 0)};
+    const bool issue = elect_lane();  // of the warpgroup's first warp
+    const uint32_t u_s = warp_uniform(t_s), u_o = warp_uniform(t_o), u_q = smem_u32(qbuf), u_p = warp_uniform(smem_u32(pmine));
     const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
     uint32_t phase = 0;  // of this warpgroup's two barriers: its tiles so far
     long long g = g0;
@@ -253,21 +257,23 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       for (long long gt = g + ((wg - (int)(g - g0)) & (kWg - 1)); gt < end; gt += kWg) {
         const int it = (int)(gt - g0), s = it % kStages;
         const int tok0 = (first + t0 + (int)(gt - g)) * kTile, n = min(kTile, max(0, hi - tok0));
-        const uint32_t ring_k = smem_u32(ring + s * kStage), ring_v = ring_k + kTile * kD;
-        wait(&sm.full[s], (it / kStages) & 1);
-        if (wt == 0) {
+        wait(&sm.full[it % (kStages * kWg)], (it / (kStages * kWg)) & 1);
+        if (w4 == 0) {
+          __syncwarp();
           tc_fence_after_sync();
+          const uint32_t ring_k = warp_uniform(smem_u32(ring + s * kStage));
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const uint32_t q = smem_u32(qbuf + (gr * 3 + k) * kTerm);
+            for (int k = 0; k < 3; ++k)
 #pragma unroll
               for (int ks = 0; ks < kD / 32; ++ks)
-                tc_mma_f8(t_s + 16 * gr, tc_sdesc_kmajor(ring_k + 256 * ks, 128, 1024),
-                          tc_sdesc_kmajor(q + 256 * ks, 128, 1024), idesc_s[k == 2], k > 0 || ks > 0);
-            }
-          tc_commit(smem_u32(&sm.bar_s[wg]));
+                if (issue)
+                  tc_mma_f8(u_s + 16 * gr, tc_sdesc_kmajor(ring_k + 256 * ks, 128, 1024),
+                            tc_sdesc_kmajor(u_q + (gr * 3 + k) * kTerm + 256 * ks, 128, 1024),
+                            tc_idesc_f8(128, kRows, 0, k == 2, 0, 0), k > 0 || ks > 0);
+          if (issue) tc_commit(smem_u32(&sm.bar_s[wg]));
+          __syncwarp();
         }
         const float4 info = sm.info[s];
         const float ks = wt < kQ8Block ? info.x : info.y;
@@ -343,22 +349,29 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         tc_fence_before_sync();
         bar_wg(wg);
         const bool use0 = info.z >= 0.f, use1 = info.w >= 0.f;  // the blocks that were copied
-        if (wt == 0) {
+        if (w4 == 0) {
           tc_fence_after_sync();
+          const uint32_t ring_v = warp_uniform(smem_u32(ring + s * kStage + kTile * kD));
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             if (!(blk ? use1 : use0)) continue;
-            const int steps = min(2, (n - blk * kQ8Block + 31) / 32);
+            const bool two = n - blk * kQ8Block > 32;  // K-steps of 32 tokens
+#pragma unroll
             for (int gr = 0; gr < GR; ++gr)
-              for (int k = 0; k < 3; ++k) {
-                const uint32_t p = smem_u32(pmine + (gr * 3 + k) * kTerm) + blk * 512;
-                for (int st = 0; st < steps; ++st)
-                  tc_mma_f8(t_o + (blk * GR + gr) * 16, tc_sdesc_kmajor(ring_v + blk * kQ8Plane + st * 4096, 1024, 128),
-                            tc_sdesc_kmajor(p + 256 * st, 128, 1024), idesc_o[k == 2], k > 0 || st > 0);
-              }
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+                  if (issue && (st == 0 || two))
+                    tc_mma_f8(u_o + (blk * GR + gr) * 16, tc_sdesc_kmajor(ring_v + blk * kQ8Plane + st * 4096, 1024, 128),
+                              tc_sdesc_kmajor(u_p + (gr * 3 + k) * kTerm + blk * 512 + 256 * st, 128, 1024),
+                              tc_idesc_f8(128, kRows, 0, k == 2, 1, 0), k > 0 || st > 0);
           }
-          tc_commit(smem_u32(&sm.empty[s]));
-          tc_commit(smem_u32(&sm.bar_o[wg]));
+          if (issue) {
+            tc_commit(smem_u32(&sm.empty[s]));
+            tc_commit(smem_u32(&sm.bar_o[wg]));
+          }
+          __syncwarp();
         }
         wait(&sm.bar_o[wg], phase & 1);
         __syncwarp();

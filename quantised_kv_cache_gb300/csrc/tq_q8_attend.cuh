@@ -27,7 +27,22 @@ __host__ __device__ constexpr uint32_t tc_idesc_f8(int M, int N, int a_fmt, int 
   return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D (TMEM) (+)= A (shared) x B (shared) of 8-bit operands, 32 K-elements; issued by one thread.
+// MMAs are issued by a whole warp in uniform control flow, one elected lane of which executes them, with descriptors
+// from values the compiler knows to be the same in every lane: those stay in uniform registers, where the
+// instruction takes them from. Issued in a branch of one thread each MMA cost about 200 clocks to set up (measured for a
+// chain of 128 x 128 x 32 products), so 66, their own time.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// D (TMEM) (+)= A (shared) x B (shared) of 8-bit operands, 32 K-elements; executed by one lane.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           bool accumulate) {
   asm volatile(

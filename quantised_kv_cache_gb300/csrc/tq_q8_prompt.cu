@@ -147,7 +147,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// D (TMEM) (+)= A (TMEM, four 8-bit K-elements per column) x B (shared); issued by one thread.
+// D (TMEM) (+)= A (TMEM, four 8-bit K-elements per column) x B (shared); executed by one lane.
 __device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                              bool accumulate) {
   asm volatile(
@@ -295,10 +295,11 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, nullptr, kWaitBudgetNs / 8);
       __syncwarp();
     } else if (warp < kSoft / 32 + 2) {
-      // ================================ a row tile's MMAs, one thread
-      if (lane == 0) {
+      // ================================ a row tile's MMAs
+      {
+        const bool issue = elect_lane();
         const int rt = warp - kSoft / 32;
-        const uint32_t t_s = tmem + rt * 256, t_o = t_s + 128, q = smem_u32(qbuf + rt * TERMS * kQTerm);
+        const uint32_t t_s = warp_uniform(tmem + rt * 256), t_o = t_s + 128, q = warp_uniform(smem_u32(qbuf + rt * TERMS * kQTerm));
         uint32_t units = 0, probs = 0;
         int it = 0;
         for (long long g = g0; g < g1; ++units) {
@@ -311,35 +312,39 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               const int s = (it + j - 1) % kStages, n = min(kTile, max(0, hi - (first + j - 1) * kTile));
               const float4 f = sm.info[s];
               const bool apart = scales_apart(f);
-              const uint32_t vt = smem_u32(ring + s * kStage) + kTile * kD;
+              const uint32_t vt = warp_uniform(smem_u32(ring + s * kStage) + kTile * kD);
               for (int part = 0; part <= (int)apart; ++part) {  // the two blocks at once, or one after the other
                 wait(&sm.bar_p[rt], probs & 1);
                 ++probs;
                 tc_fence_after_sync();
                 bool more = false;
+#pragma unroll
                 for (int t = 0; t < TERMS; ++t)
-                  for (int k = 2 * part; k < (apart ? 2 * part + 2 : 4); ++k) {
-                    if (k * 32 >= n || (k < 2 ? f.z : f.w) < 0.f) continue;
-                    tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if (k * 32 >= n || (k < 2 ? f.z : f.w) < 0.f || (apart && k / 2 != part)) continue;
+                    if (issue) tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
                                  tc_idesc_f8(128, 128, t == 2, 0, 0, 1), more);
                     more = true;
                   }
-                if (part == (int)apart) tc_commit(smem_u32(&sm.empty[s]));
-                tc_commit(smem_u32(&sm.bar_o[rt]));
+                if (issue && part == (int)apart) tc_commit(smem_u32(&sm.empty[s]));
+                if (issue) tc_commit(smem_u32(&sm.bar_o[rt]));
+                __syncwarp();
               }
             }
             if (j < todo) {
               const int s = (it + j) % kStages;
               wait(&sm.full[s], ((it + j) / kStages) & 1);
               tc_fence_after_sync();
-              const uint32_t kt = smem_u32(ring + s * kStage);
+              const uint32_t kt = warp_uniform(smem_u32(ring + s * kStage));
 #pragma unroll
               for (int t = 0; t < TERMS; ++t)
 #pragma unroll
                 for (int k = 0; k < kD / 32; ++k)
-                  tc_mma_f8(t_s, tc_sdesc_kmajor(q + t * kQTerm + 256 * k, 128, 1024), tc_sdesc_kmajor(kt + 256 * k, 128, 1024),
+                  if (issue) tc_mma_f8(t_s, tc_sdesc_kmajor(q + t * kQTerm + 256 * k, 128, 1024), tc_sdesc_kmajor(kt + 256 * k, 128, 1024),
                             tc_idesc_f8(128, 128, t == 2, 0, 0, 0), t > 0 || k > 0);
-              tc_commit(smem_u32(&sm.bar_s[rt]));
+              if (issue) tc_commit(smem_u32(&sm.bar_s[rt]));
+              __syncwarp();
             }
           }
           it += todo;

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   const int slot = tok0 + wt;
   const int kp = a.kpos && wt < n ? __ldg(a.kpos + at + wt) : slot;
   const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
-  const uint32_t idesc[2] = {tc_idesc_f8(128, kRows, 0, 0, 0, 0), tc_idesc_f8(128, kRows, 0, 1, 0, 0)};
+  const bool issue = elect_lane();  // of the warpgroup's first warp
+  const uint32_t u_s = warp_uniform(t_s), u_k = smem_u32(ktile), u_q = warp_uniform(smem_u32(qbuf));
   const int R = a.group * a.n_q, rts = (R + kRows - 1) / kRows;
   float sum = 0.f;
   uint32_t phase = 0;
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     fence_proxy_async_shared();
     tc_fence_before_sync();
     bar_wg(wg);
-    if (wt == 0) {
+    if (w4 == 0) {
       tc_fence_after_sync();
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr)
@@ -120,12 +121,15 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
         for (int k = 0; k < 3; ++k)
 #pragma unroll
           for (int s = 0; s < kD / 32; ++s)
-            tc_mma_f8(t_s + 16 * gr, tc_sdesc_kmajor(smem_u32(ktile) + 256 * s, 128, 1024),
-                      tc_sdesc_kmajor(smem_u32(qbuf + (gr * 3 + k) * kTerm) + 256 * s, 128, 1024), idesc[k == 2],
-                      k > 0 || s > 0);
-      tc_commit(smem_u32(&sm.bar_s[wg]));
+            if (issue)
+              tc_mma_f8(u_s + 16 * gr, tc_sdesc_kmajor(u_k + 256 * s, 128, 1024),
+                        tc_sdesc_kmajor(u_q + (gr * 3 + k) * kTerm + 256 * s, 128, 1024),
+                        tc_idesc_f8(128, kRows, 0, k == 2, 0, 0), k > 0 || s > 0);
+      if (issue) tc_commit(smem_u32(&sm.bar_s[wg]));
+      __syncwarp();
     }
     wait(&sm.bar_s[wg], phase & 1);
+    __syncwarp();
     ++phase;
     tc_fence_after_sync();
     float t[kRows];

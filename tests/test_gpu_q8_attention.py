@@ -492,6 +492,25 @@ def test_two_streams_and_replayed_graphs(ctx):
         assert torch.equal(twin.tensors[name], caches[0].tensors[name])
 
 
+@pytest.mark.parametrize("B,Hq,H,n,N", [(8, 32, 32, 1, 4096), (2, 32, 8, 1, 20000), (1, 16, 8, 300, 5000)])
+def test_back_to_back_calls_give_the_same_bits(ctx, B, Hq, H, n, N):
+    """Many calls without a pause between them: tiles' copies land in any order, CTAs follow one another on an SM."""
+    cache = tq.Cache(ctx, B, H, N, device=DEV)
+    k = queries(1, B, H, N, BF)
+    tq.tq_q8_append(ctx.handle, cache, k, k, ints([0] * B))
+    lens = ints([N] * B)
+    for dtype in (BF, F32) if n == 1 else (BF, HF):
+        q = queries(2, B, Hq, n, dtype)
+        ws = torch.empty(tq.tq_q8_attention_workspace(ctx.handle, B, Hq, H, n, N), dtype=torch.uint8, device=DEV)
+        want = tq.tq_q8_attention(ctx.handle, cache, q, lens, N, workspace=ws).clone()
+        out, bad = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device=DEV)
+        for i in range(1500 if n == 1 else 300):
+            tq.tq_q8_attention(ctx.handle, cache, q, lens, N, workspace=ws, out=out)
+            if i % 50 == 49:
+                bad += (out != want).sum()
+        assert int(bad) == 0
+
+
 def test_a_cache_past_32_bits(ctx):
     """5.6 GB of blocks: the last sequence-head's last tokens lie past 2^32 bytes."""
     B, H, cap = 1, 8, 2_730_000
