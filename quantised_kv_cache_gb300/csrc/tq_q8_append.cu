@@ -7,9 +7,11 @@
 // scale makes x * 2^-e exact, so the codes do not depend on how the division is carried out.
 //
 // Bound by memory: the inputs are read and the codes written once. One CTA handles one block of
-// slots of one tensor for a few heads: thread (t, c) owns 16 coordinates of token slot t, i.e. one
-// 16-byte piece of a core matrix; a warp's loads cover 4 whole rows and its stores runs of 64 bytes. The
-// sines and cosines of a token are formed once for all heads of the CTA.
+// slots of one tensor for a few heads: thread (t, j) owns 16 coordinates of token slot t, one 16-byte
+// piece of a core matrix, or, for a rotation of halves, the two 8-byte pieces that hold 8 pairs, so that it needs nobody
+// else's coordinates and 8 sines. Those are formed once for all heads of the CTA; the next head's inputs are
+// loaded before the current one's maximum is awaited. (Halves of a rotation that is no multiple of 16
+// wide do not split into such pieces: there the partners are loaded a second time.)
 
 #include "tq_q8.cuh"
 
@@ -18,15 +20,28 @@ namespace {
 
 constexpr int kThreads = kQ8Block * 8;  // 64 token slots x 8 pieces of 16 coordinates
 
+// How the keys are rotated: not at all; every pair inside its thread; halves with partners loaded again.
+enum Rope { kNone = 0, kOwn = 1, kPartner = 2 };
+
+// 8 consecutive inputs as they lie in memory
 template <typename T>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
-  __shared__ unsigned long long freq[kD / 2];
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void floats(float *v) const { unpack8<T>(w, v); }
+};
+
+template <typename T, int ROPE>
+__global__ void __launch_bounds__(kThreads, ROPE == kPartner || sizeof(T) == 4 ? 1 : 2)
+q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   __shared__ uint32_t red[2][kThreads / 32];
-  const int tid = threadIdx.x, c = tid & 7, t = tid >> 3, warp = tid >> 5;
+  const int tid = threadIdx.x, j = tid & 7, t = tid >> 3, warp = tid >> 5;
   const int b = blockIdx.y, tensor = blockIdx.z & 1, h0 = (blockIdx.z >> 1) * hpc;
   const int h1 = min(a.heads, h0 + hpc);
-  const bool rope = a.rope && tensor == 0;
-  if (rope && tid < kD / 2) freq[tid] = a.table.freq[tid];
+  const bool rope = ROPE != kNone && tensor == 0;
 
   const int len = __ldg(a.seq_lens + b);
   int n = a.n_new;
@@ -42,36 +57,30 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_consta
     return;
   }
   if (n == 0) return;
-  const int j = len / kQ8Block + blockIdx.x;      // block of the sequence
-  if ((long long)j * kQ8Block >= (long long)len + n) return;
-  const int tok = j * kQ8Block + t - len;         // the new token of this thread's slot
+  const int blk0 = len / kQ8Block + blockIdx.x;   // block of the sequence
+  if ((long long)blk0 * kQ8Block >= (long long)len + n) return;
+  const int tok = blk0 * kQ8Block + t - len;      // the new token of this thread's slot
   const bool fresh = tok >= 0 && tok < n, older = tok < 0;
-  const bool joins = j * kQ8Block < len;          // the block already holds tokens
-  __syncthreads();
+  const bool joins = blk0 * kQ8Block < len;       // the block already holds tokens
 
-  // rotation of coordinates 16 c .. 16 c + 15 (half layout: with the ones dim / 2 away)
-  float cs[16], sn[16];
-  const int dim = a.table.dim, half = dim / 2, c0 = 16 * c;
-  if (rope && fresh && c0 < dim) {
+  // this thread's coordinates: 8 from c0 on, 8 from c1 on
+  const int dim = a.table.dim, half = dim / 2;
+  const bool turn = rope && 16 * j < dim;
+  const bool halves = ROPE == kOwn && turn && !a.table.interleaved;
+  const int c0 = halves ? 8 * j : 16 * j, c1 = halves ? half + 8 * j : c0 + 8;
+  constexpr int kSines = ROPE == kPartner ? 16 : 8;
+  float cs[kSines], sn[kSines];
+  if (turn && fresh) {
     const int pos = a.positions ? __ldg(a.positions + (long long)b * a.n_new + tok) : len + tok;
-    if (a.table.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[2 * i] = 1.f, sn[2 * i] = 0.f;
-        if (c0 + 2 * i < dim) {
-          rope_sincos(pos, freq[8 * c + i], &cs[2 * i], &sn[2 * i]);
-          cs[2 * i] *= a.table.gain, sn[2 * i] *= a.table.gain;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        cs[i] = 1.f, sn[i] = 0.f;
-        if (c0 + i < dim) {
-          const bool second = c0 + i >= half;
-          rope_sincos(pos, freq[c0 + i - (second ? half : 0)], &cs[i], &sn[i]);
-          cs[i] *= a.table.gain, sn[i] *= second ? a.table.gain : -a.table.gain;
-        }
+    for (int i = 0; i < kSines; ++i) {
+      cs[i] = 1.f, sn[i] = 0.f;
+      // pair of coordinate(s) i: kOwn 8 j + i in both layouts; kPartner the coordinate's own, sign by its half
+      const bool second = ROPE == kPartner && c0 + i >= half;
+      const int f = ROPE == kPartner ? c0 + i - (second ? half : 0) : 8 * j + i;
+      if (ROPE == kPartner ? c0 + i < dim : 2 * f < dim) {
+        rope_sincos(pos, a.table.freq[f], &cs[i], &sn[i]);
+        cs[i] *= a.table.gain, sn[i] *= ROPE == kPartner && !second ? -a.table.gain : a.table.gain;
       }
     }
   }
@@ -80,28 +89,37 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_consta
   const T *x0 = static_cast<const T *>(tensor ? a.v : a.k) + b * st.b + (fresh ? tok : 0) * st.t;
   float *scales = tensor ? a.c.vs : a.c.ks;
   bool odd = false;  // an infinity or a NaN
+  Raw8<T> in0, in1;
+  if (fresh) in0.load(x0 + h0 * st.h + c0), in1.load(x0 + h0 * st.h + c1);
   for (int h = h0; h < h1; ++h) {
     float x[16];
     uint32_t amax = 0;
     if (fresh) {
-      const T *row = x0 + h * st.h;
-      load_vec<T, 16>(row + c0, x);
-      if (rope && c0 < dim) {
-        if (a.table.interleaved) {
+      in0.floats(x), in1.floats(x + 8);
+      if (h + 1 < h1) in0.load(x0 + (h + 1) * st.h + c0), in1.load(x0 + (h + 1) * st.h + c1);
+      if (turn) {
+        if constexpr (ROPE == kOwn) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float e0 = x[2 * i], e1 = x[2 * i + 1];
-            x[2 * i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[2 * i], -sn[2 * i])));
-            x[2 * i + 1] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[2 * i], sn[2 * i])));
+            if (halves) {
+              const float e0 = x[i], e1 = x[i + 8];
+              x[i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[i], -sn[i])));
+              x[i + 8] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[i], sn[i])));
+            } else {
+              if (16 * j + 2 * i >= dim) continue;  // past the rotated coordinates
+              const float e0 = x[2 * i], e1 = x[2 * i + 1];
+              x[2 * i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[i], -sn[i])));
+              x[2 * i + 1] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[i], sn[i])));
+            }
           }
-        } else {
+        } else if constexpr (ROPE == kPartner) {
           // dim is a multiple of 8, so groups of 4 coordinates do not straddle a half
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const int i0 = c0 + 4 * g;
             if (i0 < dim) {
               float o[4];
-              load_vec<T, 4>(row + (i0 < half ? i0 + half : i0 - half), o);
+              load_vec<T, 4>(x0 + h * st.h + (i0 < half ? i0 + half : i0 - half), o);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 x[4 * g + i] = from_type<T>(to_type<T>(rope_turn(x[4 * g + i], o[i], cs[4 * g + i], sn[4 * g + i])));
@@ -126,13 +144,11 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_consta
     uint32_t *slot = red[h & 1];
     if ((tid & 31) == 0) slot[warp] = amax;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) amax = max(amax, slot[w]);
-    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, ((long long)b * a.heads + h) * a.c.nblk + j, a.error);
+    amax = __reduce_max_sync(kFull, slot[tid & (kThreads / 32 - 1)]);
+    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, ((long long)b * a.heads + h) * a.c.nblk + blk0, a.error);
     if (blk < 0) continue;
     int e = q8_exponent(amax);
     uint8_t *plane = a.c.records + blk * kQ8BlockBytes + tensor * kQ8Plane;
-    uint4 *piece = reinterpret_cast<uint4 *>(plane + q8_off(t, c0));
     int shift = 0;
     if (joins) {
       const int was = log2i(scales[blk]);
@@ -146,14 +162,19 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         w[i] = cvt_e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) | (cvt_e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
-      *piece = make_uint4(w[0], w[1], w[2], w[3]);
+      if (halves) {
+        *reinterpret_cast<uint2 *>(plane + q8_off(t, c0)) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(plane + q8_off(t, c1)) = make_uint2(w[2], w[3]);
+      } else {
+        *reinterpret_cast<uint4 *>(plane + q8_off(t, c0)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     } else if (older && shift < 0) {
       const float f = pow2i(max(shift, -126));
-      uint4 w = *piece;
+      uint4 *piece = reinterpret_cast<uint4 *>(plane + q8_off(t, 16 * j));
+      const uint4 w = *piece;
       *piece = make_uint4(e4m3x4_scaled(w.x, f), e4m3x4_scaled(w.y, f), e4m3x4_scaled(w.z, f), e4m3x4_scaled(w.w, f));
     }
-    // the next head's barrier orders this store after every thread's read of the old scale
-    if (joins) __syncthreads();
+    if (joins) __syncthreads();  // every thread has read the old scale
     if (tid == 0) scales[blk] = pow2i(e);
   }
   if (odd) set_error(a.error, TQ_ERR_NONFINITE);
@@ -169,7 +190,10 @@ int launch(const Q8AppendArgs &a, int num_sms, cudaStream_t st) {
   if (hpc > a.heads) hpc = a.heads;
   const long long gz = 2 * ((a.heads + hpc - 1) / hpc);
   if (a.batch > 65535 || gz > 65535) return TQ_ERR_UNSUPPORTED;
-  q8_append_kernel<T><<<dim3((unsigned)touched, (unsigned)a.batch, (unsigned)gz), kThreads, 0, st>>>(a, (int)hpc);
+  const dim3 grid((unsigned)touched, (unsigned)a.batch, (unsigned)gz);
+  if (!a.rope) q8_append_kernel<T, kNone><<<grid, kThreads, 0, st>>>(a, (int)hpc);
+  else if (a.table.interleaved || a.table.dim % 16 == 0) q8_append_kernel<T, kOwn><<<grid, kThreads, 0, st>>>(a, (int)hpc);
+  else q8_append_kernel<T, kPartner><<<grid, kThreads, 0, st>>>(a, (int)hpc);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

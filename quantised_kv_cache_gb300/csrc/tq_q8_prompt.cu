@@ -143,6 +143,9 @@ __device__ __forceinline__ bool scales_apart(const float4 &f) {
 }
 
 __device__ __forceinline__ void bar_rt(int rt) { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); }
+// The row tiles take turns at the exponentials: turn_take waits for the other's turn_pass.
+__device__ __forceinline__ void turn_take(int rt) { asm volatile("bar.sync %0, 512;" ::"r"(3 + rt) : "memory"); }
+__device__ __forceinline__ void turn_pass(int rt) { asm volatile("bar.arrive %0, 512;" ::"r"(4 - rt) : "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -360,6 +363,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
     const uint32_t t_s = tmem + rt * 256 + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half, t_o = t_s + 128;
     const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
     int it = 0;  // tiles done: stages and phases count on
+    if (!EXTRA && rt == 1 && g0 < g1) turn_pass(rt);
     uint32_t sums = 0;
     long long g = g0;
     while (g < g1) {
@@ -429,6 +433,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         wait(&sm.bar_s[rt], (it + j) & 1);
         __syncwarp();  // tensor memory is read by whole warps
         tc_fence_after_sync();
+        if constexpr (!EXTRA) turn_take(rt);
         // ---- the row's maximum over this half
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
@@ -521,6 +526,9 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(vt + q8_off(t, 16 * k)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_shared();
+        }
+        if constexpr (!EXTRA) {
+          if (rt == 0 || u.end < g1 || j + 1 < todo) turn_pass(rt);
         }
         tmem_st_wait();
         // O = O corr + vs D
