@@ -8,6 +8,7 @@ there is no fallback implementation.
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -119,7 +120,7 @@ _SIGNATURES = {
     "tq_q8_append": (_i, [_vp, ctypes.POINTER(tq_cache), _vp, _strides3, _vp, _strides3, _i, _i, _i, _i, _vp, _vp, _i,
                           _vp, _vp]),
     "tq_q8_attention_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
-    "tq_q8_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.POINTER(tq_q8_attn), _vp, _sz, _vp]),
+    "tq_q8_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),  # a packed tq_q8_attn
     "tq_q8_evict": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.POINTER(tq_cache), _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp,
                          _vp, _vp, _vp, _vp]),
 }
@@ -405,32 +406,48 @@ def tq_selftest_bounded_wait(ctx, budget_ns: int, stream=None) -> None:
 # rotary positions and the 8-bit cache
 # ----------------------------------------------------------------------------
 
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# A call of a few microseconds on the GPU must not wait for its own marshalling: the helpers below look at each
+# tensor once, pass pointers as plain integers and keep the stride arrays they made.
+
+_ANY_DTYPE = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+_i32, _f32 = torch.int32, torch.float32
+_stride_arrays = {}
 
 
 def _any_dtype(dtype: torch.dtype) -> int:
-    codes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
-    if dtype not in codes:
+    code = _ANY_DTYPE.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    return codes[dtype]
+    return code
+
+
+def _raw_stream(stream, index: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _rows(t: torch.Tensor, name: str):
-    """Strides of a [batch][heads][tokens][128] tensor (dimensions of one entry have none)."""
-    _need(t.dim() == 4 and t.shape[-1] == 128 and t.stride(-1) == 1,
-          f"{name}: [batch][heads][tokens][128] with contiguous rows is wanted")
-    return _strides3(*(0 if t.shape[i] == 1 else t.stride(i) for i in range(3)))
+    """(shape, strides as int64[3]) of a [batch][heads][tokens][128] tensor; dimensions of one entry have no stride."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 4 or shape[3] != 128 or st[3] != 1:
+        raise ValueError(f"{name}: [batch][heads][tokens][128] with contiguous rows is wanted")
+    key = (st[0] if shape[0] != 1 else 0, st[1] if shape[1] != 1 else 0, st[2] if shape[2] != 1 else 0)
+    a = _stride_arrays.get(key)
+    if a is None:
+        if len(_stride_arrays) > 4096:
+            _stride_arrays.clear()
+        a = _stride_arrays[key] = _strides3(*key)
+    return shape, a
 
 
-def _array(t: Optional[torch.Tensor], shape, dtype, device, name: str):
-    """The pointer of a contiguous tensor of this shape and type (None stays None)."""
+def _array(t: Optional[torch.Tensor], shape, dtype, index: int, name: str):
+    """The address of a contiguous tensor of this shape and type on device `index` (None stays None)."""
     if t is None:
         return None
-    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.is_contiguous() and t.device == device,
-          f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
-    return _ptr(t)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on the cache's or input's device is wanted")
+    return t.data_ptr()
 
 
 def tq_set_rope(ctx, dim: int = 128, interleaved: bool = False, base: float = 10000.0, factor: float = 1.0,
@@ -444,14 +461,20 @@ def tq_rotary(ctx, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch
               stream=None) -> torch.Tensor:
     """x [batch][heads][tokens][128] (any strides with contiguous rows) turned at positions int32
     [batch][tokens]; out may be x. Returns out (laid out as x when it is made here)."""
-    xs = _rows(x, "x")
+    shape, xs = _rows(x, "x")
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("x: a CUDA tensor is wanted")
     if out is None:
         out = torch.empty_like(x)
-    _need(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device, "out: x's shape, type and device are wanted")
-    B, H, n, _ = x.shape
-    pos = _array(positions, (B, n), torch.int32, x.device, "positions")
-    check(lib().tq_rotary(ctx, _ptr(x), xs, _ptr(out), _rows(out, "out"), _any_dtype(x.dtype), B, H, n, pos,
-                          int(transpose), _stream(stream)), "tq_rotary")
+    elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != index:
+        raise ValueError("out: x's shape, type and device are wanted")
+    B, H, n, _ = shape
+    pos = _array(positions, (B, n), _i32, index, "positions")
+    status = lib().tq_rotary(ctx, x.data_ptr(), xs, out.data_ptr(), _rows(out, "out")[1], _any_dtype(x.dtype), B, H, n, pos,
+                             transpose, _raw_stream(stream, index))
+    if status:
+        check(status, "tq_rotary")
     return out
 
 
@@ -460,14 +483,18 @@ def tq_q8_append(ctx, cache: "Cache", k: torch.Tensor, v: torch.Tensor, seq_lens
                  stream=None) -> None:
     """k, v [batch][heads_kv][tokens][128] (any strides with contiguous rows) into an 8-bit cache at
     slots seq_lens[b] + t; sequence b brings its first new_lens[b] tokens (all when None)."""
-    B, H, n, _ = k.shape
-    _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device == cache.device,
-          "k and v: one shape and type, on the cache's device")
-    dev = k.device
-    check(lib().tq_q8_append(ctx, ctypes.byref(cache.struct), _ptr(k), _rows(k, "k"), _ptr(v), _rows(v, "v"),
-                             _any_dtype(k.dtype), B, H, n, _array(seq_lens, (B,), torch.int32, dev, "seq_lens"),
-                             _array(new_lens, (B,), torch.int32, dev, "new_lens"), int(rope),
-                             _array(positions, (B, n), torch.int32, dev, "positions"), _stream(stream)), "tq_q8_append")
+    shape, ks = _rows(k, "k")
+    vshape, vs = _rows(v, "v")
+    index = cache.device_index
+    if vshape != shape or v.dtype is not k.dtype or k.get_device() != index or v.get_device() != index or index < 0:
+        raise ValueError("k and v: one shape and type, on the cache's device")
+    B, H, n, _ = shape
+    status = lib().tq_q8_append(ctx, cache.struct, k.data_ptr(), ks, v.data_ptr(), vs, _any_dtype(k.dtype), B, H, n,
+                                _array(seq_lens, (B,), _i32, index, "seq_lens"),
+                                _array(new_lens, (B,), _i32, index, "new_lens"), rope,
+                                _array(positions, (B, n), _i32, index, "positions"), _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_append")
 
 
 def tq_q8_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, max_len: int,
@@ -476,6 +503,10 @@ def tq_q8_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q:
     check(lib().tq_q8_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_len, int(weights), ctypes.byref(out)),
           "tq_q8_attention_workspace")
     return out.value
+
+
+# tq_q8_attn's fields in order, NULL pointers as 0
+_pack_attn = struct.Struct("@7iP3qP3qPPff8P")
 
 
 def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
@@ -490,28 +521,32 @@ def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor
     cache of seq_lens[b] tokens, the query tokens' own among them (include/tq.h, tq_q8_attn). Returns
     out, of q's type unless out_dtype is torch.float32; made here it is q's shape, contiguous, and
     rows past new_lens[b] are not written."""
-    B, Hq, n, _ = q.shape
-    H, cap, dev = cache.heads_kv, cache.capacity, q.device
-    _need(dev == cache.device, "q: the cache's device is wanted")
+    shape, qs = _rows(q, "q")
+    B, Hq, n, _ = shape
+    H, cap, index = cache.heads_kv, cache.capacity, cache.device_index
+    if q.get_device() != index or index < 0:
+        raise ValueError("q: the cache's device is wanted")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
-    _need(out.shape == q.shape and out.device == dev and out_dtype in (None, out.dtype), "out: q's shape and device are wanted")
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != shape or out.get_device() != index or out_dtype not in (None, out.dtype):
+        raise ValueError("out: q's shape and device are wanted")
     if workspace is None:
         workspace = torch.empty(tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
-                                dtype=torch.uint8, device=dev)
-    i32, f32 = torch.int32, torch.float32
-    a = tq_q8_attn(
-        batch=B, heads_q=Hq, heads_kv=H, n_q=n, max_len=max_len, q_dtype=_any_dtype(q.dtype), out_dtype=_any_dtype(out.dtype),
-        d_q=_ptr(q), q_strides=_rows(q, "q"), d_out=_ptr(out), out_strides=_rows(out, "out"),
-        d_seq_lens=_array(seq_lens, (B,), i32, dev, "seq_lens"), d_new_lens=_array(new_lens, (B,), i32, dev, "new_lens"),
-        scale=scale, softcap=softcap, d_slopes=_array(slopes, (Hq,), f32, dev, "slopes"),
-        d_q_positions=_array(q_positions, (B, n), i32, dev, "q_positions"),
-        d_k_positions=_array(k_positions, (B, H, cap), i32, dev, "k_positions"),
-        d_key_begin=_array(key_begin, (B, n), i32, dev, "key_begin"), d_key_end=_array(key_end, (B, n), i32, dev, "key_end"),
-        d_weights_in=_array(weights_in, (B, H, cap), f32, dev, "weights_in"),
-        d_weights=_array(weights, (B, H, cap), f32, dev, "weights"), d_lse=_array(lse, (B, Hq, n), f32, dev, "lse"))
-    check(lib().tq_q8_attention(ctx, ctypes.byref(cache.struct), ctypes.byref(a), _ptr(workspace), workspace.numel(),
-                                _stream(stream)), "tq_q8_attention")
+                                dtype=torch.uint8, device=q.device)
+    os = _rows(out, "out")[1]
+    rows, slots = (B, n), (B, H, cap)
+    a = _pack_attn.pack(
+        B, Hq, H, n, max_len, _any_dtype(q.dtype), _any_dtype(out.dtype), q.data_ptr(), qs[0], qs[1], qs[2], out.data_ptr(), os[0],
+        os[1], os[2], _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
+        scale, softcap, _array(slopes, (Hq,), _f32, index, "slopes") or 0,
+        _array(q_positions, rows, _i32, index, "q_positions") or 0, _array(k_positions, slots, _i32, index, "k_positions") or 0,
+        _array(key_begin, rows, _i32, index, "key_begin") or 0, _array(key_end, rows, _i32, index, "key_end") or 0,
+        _array(weights_in, slots, _f32, index, "weights_in") or 0, _array(weights, slots, _f32, index, "weights") or 0,
+        _array(lse, (B, Hq, n), _f32, index, "lse") or 0)
+    status = lib().tq_q8_attention(ctx, cache.struct, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_attention")
     return out
 
 
@@ -522,18 +557,26 @@ def tq_q8_evict(ctx, src: "Cache", dst: "Cache", seq_lens: torch.Tensor, weights
     """Keep at most `keep` tokens of every sequence of `src` in `dst`: the first `sink`, the last
     `recent` and the heaviest of the rest. Returns (kept slots [batch][heads_kv][keep], lengths
     [batch], weights and positions [batch][heads_kv][dst capacity])."""
-    B, H, dev = src.batch, src.heads_kv, src.device
-    _need((dst.batch, dst.heads_kv, dst.device) == (B, H, dev), "dst: the source's batch, KV heads and device are wanted")
-    i32, f32 = torch.int32, torch.float32
-    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=dev) if t is None else t  # noqa: E731
-    kept, dst_lens = new(kept, (B, H, max(keep, 0)), i32), new(dst_lens, (B,), i32)
-    dst_weights, dst_positions = new(dst_weights, (B, H, dst.capacity), f32), new(dst_positions, (B, H, dst.capacity), i32)
-    check(lib().tq_q8_evict(ctx, ctypes.byref(src.struct), ctypes.byref(dst.struct), B, H,
-                            _array(seq_lens, (B,), i32, dev, "seq_lens"), _array(weights, (B, H, src.capacity), f32, dev, "weights"),
-                            keep, sink, recent, _array(positions, (B, H, src.capacity), i32, dev, "positions"),
-                            _array(kept, (B, H, max(keep, 0)), i32, dev, "kept"), _array(dst_lens, (B,), i32, dev, "dst_lens"),
-                            _array(dst_weights, (B, H, dst.capacity), f32, dev, "dst_weights"),
-                            _array(dst_positions, (B, H, dst.capacity), i32, dev, "dst_positions"), _stream(stream)), "tq_q8_evict")
+    B, H, index, dev = src.batch, src.heads_kv, src.device_index, src.device
+    if (dst.batch, dst.heads_kv, dst.device_index) != (B, H, index):
+        raise ValueError("dst: the source's batch, KV heads and device are wanted")
+    some, from_, to = (B, H, max(keep, 0)), (B, H, src.capacity), (B, H, dst.capacity)
+    if kept is None:
+        kept = torch.empty(some, dtype=_i32, device=dev)
+    if dst_lens is None:
+        dst_lens = torch.empty((B,), dtype=_i32, device=dev)
+    if dst_weights is None:
+        dst_weights = torch.empty(to, dtype=_f32, device=dev)
+    if dst_positions is None:
+        dst_positions = torch.empty(to, dtype=_i32, device=dev)
+    status = lib().tq_q8_evict(
+        ctx, src.struct, dst.struct, B, H, _array(seq_lens, (B,), _i32, index, "seq_lens"),
+        _array(weights, from_, _f32, index, "weights"), keep, sink, recent, _array(positions, from_, _i32, index, "positions"),
+        _array(kept, some, _i32, index, "kept"), _array(dst_lens, (B,), _i32, index, "dst_lens"),
+        _array(dst_weights, to, _f32, index, "dst_weights"), _array(dst_positions, to, _i32, index, "dst_positions"),
+        _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_evict")
     return kept, dst_lens, dst_weights, dst_positions
 
 
@@ -615,6 +658,7 @@ class Cache:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device_index = -1 if self.device.index is None else self.device.index  # as Tensor.get_device()
         self.block_tokens = Q8_BLOCK_TOKENS if ctx.scheme == "Q8" else BLOCK_TOKENS
         self.batch, self.heads_kv, self.capacity = batch, heads_kv, capacity
         self.tensors = {}
