@@ -34,6 +34,7 @@ struct RotaryArgs {
   int dtype, batch, heads, n, transpose;
   const int32_t *positions;
   RopeTable rope;
+  int by_token = 0;  // a token's heads lie nearer to each other than a head's tokens (set by the launcher)
 };
 int launch_rotary(const RotaryArgs &a, int num_sms, void *stream);
 

@@ -37,7 +37,7 @@ struct Raw8 {
 template <typename T, int ROPE>
 __global__ void __launch_bounds__(kThreads, ROPE == kPartner || sizeof(T) == 4 ? 1 : 2)
 q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
-  __shared__ uint32_t red[2][kThreads / 32];
+  __shared__ uint32_t red[4][kThreads / 32];
   const int tid = threadIdx.x, j = tid & 7, t = tid >> 3, warp = tid >> 5;
   const int b = blockIdx.y, tensor = blockIdx.z & 1, h0 = (blockIdx.z >> 1) * hpc;
   const int h1 = min(a.heads, h0 + hpc);
@@ -128,23 +128,29 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
-        if (u >= 0x7f800000u) {
-          odd = true;
-          if (u > 0x7f800000u) x[i] = 0.f;
-          u = 0;
-        }
-        // a number that would round up to 2^128 becomes the largest that stays finite
-        x[i] = fminf(fmaxf(x[i], -kQ8Largest), kQ8Largest);
-        amax = max(amax, min(u, __float_as_uint(kQ8Largest)));
-      }
+      for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
     }
-    amax = __reduce_max_sync(kFull, amax);
-    uint32_t *slot = red[h & 1];
-    if ((tid & 31) == 0) slot[warp] = amax;
-    __syncthreads();
-    amax = __reduce_max_sync(kFull, slot[tid & (kThreads / 32 - 1)]);
+    auto block_max = [&](uint32_t v, uint32_t *slot) {
+      v = __reduce_max_sync(kFull, v);
+      if ((tid & 31) == 0) slot[warp] = v;
+      __syncthreads();
+      return __reduce_max_sync(kFull, slot[tid & (kThreads / 32 - 1)]);
+    };
+    amax = block_max(amax, red[h & 1]);
+    if (amax > __float_as_uint(kQ8Largest)) {  // the whole CTA: numbers that are not finite, or would round up to 2^128
+      amax = 0;
+      if (fresh) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
+          odd |= u >= 0x7f800000u;
+          if (u > 0x7f800000u) x[i] = 0.f;
+          x[i] = fminf(fmaxf(x[i], -kQ8Largest), kQ8Largest);
+          amax = max(amax, u >= 0x7f800000u ? 0u : min(u, __float_as_uint(kQ8Largest)));
+        }
+      }
+      amax = block_max(amax, red[2 + (h & 1)]);
+    }
     const long long blk = q8_block(a.c.btab, a.c.pool_blocks, ((long long)b * a.heads + h) * a.c.nblk + blk0, a.error);
     if (blk < 0) continue;
     int e = q8_exponent(amax);

@@ -8,8 +8,8 @@
 // every kept slot its place. Keys are read once from memory and stay in shared memory (what does not
 // fit is read again). A cluster of up to 8 CTAs shares one long sequence-head: each holds a run of
 // slots, histograms and counts are added through distributed shared memory.
-// q8_gather_kernel: one CTA per 64-token block of the target and tensor. A thread owns one 16-byte piece (16
-// coordinates of one token); the new block's scale comes from the largest value, and codes are rounded
+// q8_gather_kernel: one CTA per 64-token block of the target. A thread owns one 16-byte piece (16
+// coordinates of one token) of the keys and one of the values; the new block's scale comes from the largest value, and codes are rounded
 // only where their block's scale differs from it. Both bound by memory.
 
 #include <cooperative_groups.h>
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
     return weight_key(__ldg(w + s));
   };
   auto key = [&](int i) -> uint32_t { return i < kSelKeys ? keys[i] : make(i); };
+#pragma unroll 8
   for (int i = tid; i < min(cnt, kSelKeys); i += kSel) keys[i] = make(i);
   __syncthreads();  // the runs below cross threads, also where nothing is chosen by weight
 
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
       const uint32_t digit = pass == 2 ? 1023u : 2047u;
       hist[tid] = 0, hist[tid + kSel] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = tid; i < cnt; i += kSel) {
         const uint32_t k = key(i);
         if (k != kAlways && ((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> shift) & digit], 1);
@@ -170,41 +172,47 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
 constexpr int kGather = kQ8Block * 8;
 
 __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constant__ Q8EvictArgs a) {
-  __shared__ uint32_t red[kGather / 32];
+  __shared__ uint32_t red[2][kGather / 32];
   const int tid = threadIdx.x, c = tid & 7, t = tid >> 3;
-  const int j = blockIdx.x, tensor = blockIdx.z;
+  const int j = blockIdx.x;
   const long long bh = blockIdx.y;
   const int i = j * kQ8Block + t;
   const int s = i < a.keep ? __ldg(a.kept + bh * a.keep + i) : -1;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  int e0 = kQ8MinExp;
+  const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
+  uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  int e0[2] = {kQ8MinExp, kQ8MinExp};
   if (s >= 0 && s < a.src.capacity) {
     const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
     if (from >= 0) {
-      w = *reinterpret_cast<const uint4 *>(a.src.records + from * kQ8BlockBytes + tensor * kQ8Plane +
-                                           q8_off(s % kQ8Block, 16 * c));
-      e0 = log2i((tensor ? a.src.vs : a.src.ks)[from]);
+      const uint8_t *p = a.src.records + from * kQ8BlockBytes + q8_off(s % kQ8Block, 16 * c);
+      w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+      w[1] = __ldg(reinterpret_cast<const uint4 *>(p + kQ8Plane));
+      e0[0] = log2i(__ldg(a.src.ks + from));
+      e0[1] = log2i(__ldg(a.src.vs + from));
     }
   }
-  // the largest magnitude of the piece: e4m3 magnitudes are ordered as their low seven bits
-  uint32_t top = __vmaxu4(__vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu));
-  top = __vmaxu4(top, top >> 16);
-  top = max(top & 0xffu, (top >> 8) & 0xffu);
-  uint32_t amax = __float_as_uint(e4m3x2_f(top).x * pow2i(e0));
-  amax = __reduce_max_sync(kFull, amax);
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kGather / 32; ++k) amax = max(amax, red[k]);
-  const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
-  if (to < 0) return;
-  const int e = q8_exponent(amax);
-  if (e != e0) {
-    const float f = pow2i(min(max(e0 - e, -126), 126));
-    w = make_uint4(e4m3x4_scaled(w.x, f), e4m3x4_scaled(w.y, f), e4m3x4_scaled(w.z, f), e4m3x4_scaled(w.w, f));
+  for (int k = 0; k < 2; ++k) {
+    // the largest magnitude of the piece: e4m3 magnitudes are ordered as their low seven bits
+    uint32_t top = __vmaxu4(__vmaxu4(w[k].x & 0x7f7f7f7fu, w[k].y & 0x7f7f7f7fu),
+                            __vmaxu4(w[k].z & 0x7f7f7f7fu, w[k].w & 0x7f7f7f7fu));
+    top = __vmaxu4(top, top >> 16);
+    top = max(top & 0xffu, (top >> 8) & 0xffu);
+    const uint32_t amax = __reduce_max_sync(kFull, __float_as_uint(e4m3x2_f(top).x * pow2i(e0[k])));
+    if ((tid & 31) == 0) red[k][tid >> 5] = amax;
   }
-  *reinterpret_cast<uint4 *>(a.dst.records + to * kQ8BlockBytes + tensor * kQ8Plane + q8_off(t, 16 * c)) = w;
-  if (tid == 0) (tensor ? a.dst.vs : a.dst.ks)[to] = pow2i(e);
+  __syncthreads();
+  if (to < 0) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int e = q8_exponent(__reduce_max_sync(kFull, red[k][tid & (kGather / 32 - 1)]));
+    if (e != e0[k]) {
+      const float f = pow2i(min(max(e0[k] - e, -126), 126));
+      w[k] = make_uint4(e4m3x4_scaled(w[k].x, f), e4m3x4_scaled(w[k].y, f), e4m3x4_scaled(w[k].z, f), e4m3x4_scaled(w[k].w, f));
+    }
+    *reinterpret_cast<uint4 *>(a.dst.records + to * kQ8BlockBytes + k * kQ8Plane + q8_off(t, 16 * c)) = w[k];
+    if (tid == 0) (k ? a.dst.vs : a.dst.ks)[to] = pow2i(e);
+  }
 }
 
 }  // namespace
@@ -233,7 +241,7 @@ int launch_q8_evict(const Q8EvictArgs &a, void *stream) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, q8_select_kernel, a) != cudaSuccess) return TQ_ERR_CUDA;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
-  q8_gather_kernel<<<dim3((unsigned)blocks, (unsigned)bh, 2), kGather, 0, st>>>(a);
+  q8_gather_kernel<<<dim3((unsigned)blocks, (unsigned)bh), kGather, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -22,10 +22,12 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
   if (id >= items) return;
   const int j = (int)(id % kRow);
   long long rest = id / kRow;
-  const int t = (int)(rest % a.n);
-  rest /= a.n;
-  const int chunks = (a.heads + hpt - 1) / hpt;
-  const int h0 = (int)(rest % chunks) * hpt, b = (int)(rest / chunks);
+  // neighbouring threads on rows that lie together: of one token's heads, or of one head's tokens
+  const int chunks = (a.heads + hpt - 1) / hpt, inner = a.by_token ? chunks : a.n, outer = a.by_token ? a.n : chunks;
+  const int i0 = (int)(rest % inner);
+  rest /= inner;
+  const int i1 = (int)(rest % outer), b = (int)(rest / outer);
+  const int t = a.by_token ? i1 : i0, h0 = (a.by_token ? i0 : i1) * hpt;
   const int h1 = min(a.heads, h0 + hpt);
   const int dim = a.rope.dim;
   // the two vectors of this thread: the halves of V pairs, or 2V consecutive elements
@@ -99,8 +101,10 @@ int launch_t(const RotaryArgs &a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int launch_rotary(const RotaryArgs &a, int num_sms, void *stream) {
+int launch_rotary(const RotaryArgs &args, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
+  RotaryArgs a = args;
+  a.by_token = a.xs.h < a.xs.t;
   switch (a.dtype) {
     case TQ_F32: return launch_t<float>(a, num_sms, st);
     case TQ_BF16: return launch_t<__nv_bfloat16>(a, num_sms, st);
