@@ -98,28 +98,6 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
     }
   }
 }
-// 8 elements held in 16-byte words
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 *q, float *v) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[4 * i] = __uint_as_float(q[i].x), v[4 * i + 1] = __uint_as_float(q[i].y);
-      v[4 * i + 2] = __uint_as_float(q[i].z), v[4 * i + 3] = __uint_as_float(q[i].w);
-    }
-  } else {
-    const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-      }
-    }
-  }
-}
 template <typename T>
 __device__ __forceinline__ T to_type(float x) {
   if constexpr (sizeof(T) == 4) return x;

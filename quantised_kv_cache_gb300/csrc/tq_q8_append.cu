@@ -23,16 +23,60 @@ constexpr int kThreads = kQ8Block * 8;  // 64 token slots x 8 pieces of 16 coord
 // How the keys are rotated: not at all; every pair inside its thread; halves with partners loaded again.
 enum Rope { kNone = 0, kOwn = 1, kPartner = 2 };
 
-// 8 consecutive inputs as they lie in memory
+// 16 coordinates of a token as they lie in memory: 8 in w[0 .. H - 1], 8 in w[H ..]. Two of a 16-bit type stay packed in a
+// word until they are scaled, so that magnitudes are compared two at a time.
 template <typename T>
-struct Raw8 {
-  uint4 w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T *p) {
+struct Piece {
+  static constexpr int kWords = 4 * (int)sizeof(T), H = kWords / 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T *p, const T *q) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    for (int i = 0; i < H / 4; ++i) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + i), y = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      w[H + 4 * i] = y.x, w[H + 4 * i + 1] = y.y, w[H + 4 * i + 2] = y.z, w[H + 4 * i + 3] = y.w;
+    }
   }
-  __device__ __forceinline__ void floats(float *v) const { unpack8<T>(w, v); }
+  // coordinates 2 i and 2 i + 1
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+  }
+  __device__ __forceinline__ void set(int i, float2 v) {  // rounded to T
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(v.x), w[2 * i + 1] = __float_as_uint(v.y);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(v.x, v.y);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  // the largest magnitude's bits in T (ordered as the magnitudes; infinities and NaN on top)
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu);
+      return max(m & 0xffffu, m >> 16);
+    }
+  }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t t) {
+    if constexpr (sizeof(T) == 4) return t;
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value) return t << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)t)));
+  }
 };
+
+__device__ __forceinline__ float tame(float x) { return x != x ? 0.f : fminf(fmaxf(x, -kQ8Largest), kQ8Largest); }
 
 template <typename T, int ROPE>
 __global__ void __launch_bounds__(kThreads, ROPE == kPartner || sizeof(T) == 4 ? 1 : 2)
@@ -89,46 +133,45 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   const T *x0 = static_cast<const T *>(tensor ? a.v : a.k) + b * st.b + (fresh ? tok : 0) * st.t;
   float *scales = tensor ? a.c.vs : a.c.ks;
   bool odd = false;  // an infinity or a NaN
-  Raw8<T> in0, in1;
-  if (fresh) in0.load(x0 + h0 * st.h + c0), in1.load(x0 + h0 * st.h + c1);
+  Piece<T> next;
+  if (fresh) next.load(x0 + h0 * st.h + c0, x0 + h0 * st.h + c1);
   for (int h = h0; h < h1; ++h) {
-    float x[16];
-    uint32_t amax = 0;
-    if (fresh) {
-      in0.floats(x), in1.floats(x + 8);
-      if (h + 1 < h1) in0.load(x0 + (h + 1) * st.h + c0), in1.load(x0 + (h + 1) * st.h + c1);
-      if (turn) {
-        if constexpr (ROPE == kOwn) {
+    Piece<T> in = next;
+    if (fresh && h + 1 < h1) next.load(x0 + (h + 1) * st.h + c0, x0 + (h + 1) * st.h + c1);
+    if (turn && fresh) {
+      if constexpr (ROPE == kOwn) {
+        if (halves) {  // pair i: coordinates i of the two eights
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = in.pair(i), v = in.pair(i + 4);
+            in.set(i, make_float2(rope_turn(u.x, v.x, cs[2 * i], -sn[2 * i]), rope_turn(u.y, v.y, cs[2 * i + 1], -sn[2 * i + 1])));
+            in.set(i + 4, make_float2(rope_turn(v.x, u.x, cs[2 * i], sn[2 * i]), rope_turn(v.y, u.y, cs[2 * i + 1], sn[2 * i + 1])));
+          }
+        } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (halves) {
-              const float e0 = x[i], e1 = x[i + 8];
-              x[i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[i], -sn[i])));
-              x[i + 8] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[i], sn[i])));
-            } else {
-              if (16 * j + 2 * i >= dim) continue;  // past the rotated coordinates
-              const float e0 = x[2 * i], e1 = x[2 * i + 1];
-              x[2 * i] = from_type<T>(to_type<T>(rope_turn(e0, e1, cs[i], -sn[i])));
-              x[2 * i + 1] = from_type<T>(to_type<T>(rope_turn(e1, e0, cs[i], sn[i])));
-            }
+            if (16 * j + 2 * i >= dim) continue;  // past the rotated coordinates
+            const float2 u = in.pair(i);
+            in.set(i, make_float2(rope_turn(u.x, u.y, cs[i], -sn[i]), rope_turn(u.y, u.x, cs[i], sn[i])));
           }
-        } else if constexpr (ROPE == kPartner) {
-          // dim is a multiple of 8, so groups of 4 coordinates do not straddle a half
+        }
+      } else if constexpr (ROPE == kPartner) {
+        // dim is a multiple of 8, so groups of 4 coordinates do not straddle a half
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int i0 = c0 + 4 * g;
-            if (i0 < dim) {
-              float o[4];
-              load_vec<T, 4>(x0 + h * st.h + (i0 < half ? i0 + half : i0 - half), o);
+        for (int g = 0; g < 4; ++g) {
+          const int i0 = c0 + 4 * g;
+          if (i0 < dim) {
+            float o[4];
+            load_vec<T, 4>(x0 + h * st.h + (i0 < half ? i0 + half : i0 - half), o);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[4 * g + i] = from_type<T>(to_type<T>(rope_turn(x[4 * g + i], o[i], cs[4 * g + i], sn[4 * g + i])));
+            for (int i = 0; i < 2; ++i) {
+              const float2 u = in.pair(2 * g + i);
+              const int k = 4 * g + 2 * i;
+              in.set(2 * g + i, make_float2(rope_turn(u.x, o[2 * i], cs[k], sn[k]), rope_turn(u.y, o[2 * i + 1], cs[k + 1], sn[k + 1])));
             }
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
     }
     auto block_max = [&](uint32_t v, uint32_t *slot) {
       v = __reduce_max_sync(kFull, v);
@@ -136,17 +179,18 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
       __syncthreads();
       return __reduce_max_sync(kFull, slot[tid & (kThreads / 32 - 1)]);
     };
-    amax = block_max(amax, red[h & 1]);
-    if (amax > __float_as_uint(kQ8Largest)) {  // the whole CTA: numbers that are not finite, or would round up to 2^128
+    uint32_t amax = Piece<T>::float_bits(block_max(fresh ? in.top() : 0u, red[h & 1]));
+    const bool wild = amax > __float_as_uint(kQ8Largest);  // the whole CTA's: not finite, or would round up to 2^128
+    if (wild) {
       amax = 0;
       if (fresh) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
-          odd |= u >= 0x7f800000u;
-          if (u > 0x7f800000u) x[i] = 0.f;
-          x[i] = fminf(fmaxf(x[i], -kQ8Largest), kQ8Largest);
-          amax = max(amax, u >= 0x7f800000u ? 0u : min(u, __float_as_uint(kQ8Largest)));
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = in.pair(i);
+          const uint32_t u0 = __float_as_uint(v.x) & 0x7fffffffu, u1 = __float_as_uint(v.y) & 0x7fffffffu;
+          odd |= max(u0, u1) >= 0x7f800000u;
+          amax = max(amax, u0 >= 0x7f800000u ? 0u : min(u0, __float_as_uint(kQ8Largest)));
+          amax = max(amax, u1 >= 0x7f800000u ? 0u : min(u1, __float_as_uint(kQ8Largest)));
         }
       }
       amax = block_max(amax, red[2 + (h & 1)]);
@@ -162,12 +206,16 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
       shift = was - e;
     }
     if (fresh) {
-      // exact: e lies in [-100, 120]
-      const float f = pow2i(-e);
+      const float f = pow2i(-e);  // exact: e lies in [-100, 120]
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = cvt_e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) | (cvt_e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
+      for (int i = 0; i < 4; ++i) {
+        float2 u = in.pair(2 * i), v = in.pair(2 * i + 1);
+        if (wild) {  // NaN to 0, infinities and what is too large to the largest number that stays finite
+          u = make_float2(tame(u.x), tame(u.y)), v = make_float2(tame(v.x), tame(v.y));
+        }
+        w[i] = cvt_e4m3x2(u.x * f, u.y * f) | (cvt_e4m3x2(v.x * f, v.y * f) << 16);
+      }
       if (halves) {
         *reinterpret_cast<uint2 *>(plane + q8_off(t, c0)) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2 *>(plane + q8_off(t, c1)) = make_uint2(w[2], w[3]);

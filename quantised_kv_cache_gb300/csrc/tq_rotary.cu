@@ -3,8 +3,8 @@
 // Pair (a, b) -> gain (a cos - b sin, b cos + a sin). Bound by memory: every element is read and
 // written once. A thread owns V + V elements of a row (the two halves of V pairs, or 2V
 // consecutive elements when the pairs are interleaved; a row's coordinates past `dim` pass
-// through), forms their V sines and cosines once and uses them for up to 8 heads of its token, four
-// heads' loads in flight before the first is used. V = 8 (16-byte accesses for 16-bit types) needs
+// through), forms their V sines and cosines once and uses them for up to 4 heads of its token, all
+// loads in flight before the first is used. V = 8 (16-byte accesses for 16-bit types) needs
 // dim a multiple of 16, V = 4 covers the other multiples of 8.
 
 #include "tq_q8.cuh"
@@ -12,8 +12,44 @@
 namespace tq {
 namespace {
 
+// V consecutive elements as they lie in memory
+template <typename T, int V>
+struct Words {
+  static constexpr int kWords = V * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(p);
+      w[0] = x.x, w[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ void store(T *p) const {
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+      else if constexpr (std::is_same<T, __nv_bfloat16>::value) v[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+      else v[i] = __half2float(__ushort_as_half((unsigned short)((i & 1) ? w[i / 2] >> 16 : w[i / 2])));
+    }
+  }
+};
+
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a, int hpt, long long items) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) rotary_kernel(const __grid_constant__ RotaryArgs a, int hpt, long long items) {
   constexpr int kRow = kD / (2 * V);  // threads of a row
   __shared__ unsigned long long freq[kD / 2];
   if (threadIdx.x < kD / 2) freq[threadIdx.x] = a.rope.freq[threadIdx.x];
@@ -48,33 +84,39 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
   T *y = static_cast<T *>(a.y) + b * a.ys.b + t * a.ys.t;
   constexpr int kU = 4;
   for (int h = h0; h < h1; h += kU) {
-    float u[kU][V], w[kU][V];
+    Words<T, V> u[kU], w[kU];  // as they lie in memory: four heads' loads in flight take 32 registers of a 16-bit type
 #pragma unroll
     for (int k = 0; k < kU; ++k)
       if (h + k < h1) {
-        load_vec<T, V>(x + (h + k) * a.xs.h + c0, u[k]);
-        load_vec<T, V>(x + (h + k) * a.xs.h + c1, w[k]);
+        u[k].load(x + (h + k) * a.xs.h + c0);
+        w[k].load(x + (h + k) * a.xs.h + c1);
       }
 #pragma unroll
     for (int k = 0; k < kU; ++k)
       if (h + k < h1) {
+        T *const p = y + (h + k) * a.ys.h + c0, *const q = y + (h + k) * a.ys.h + c1;
         if (turn) {
+          float d[V], e[V];
+          u[k].floats(d), w[k].floats(e);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             if constexpr (IL) {  // pairs (2i, 2i + 1) of the 2V elements
-              float *p = i < V / 2 ? &u[k][2 * i] : &w[k][2 * i - V];
-              const float e0 = p[0], e1 = p[1];
-              p[0] = rope_turn(e0, e1, cs[i], -sn[i]);
-              p[1] = rope_turn(e1, e0, cs[i], sn[i]);
+              float *const r = i < V / 2 ? &d[2 * i] : &e[2 * i - V];
+              const float e0 = r[0], e1 = r[1];
+              r[0] = rope_turn(e0, e1, cs[i], -sn[i]);
+              r[1] = rope_turn(e1, e0, cs[i], sn[i]);
             } else {
-              const float e0 = u[k][i], e1 = w[k][i];
-              u[k][i] = rope_turn(e0, e1, cs[i], -sn[i]);
-              w[k][i] = rope_turn(e1, e0, cs[i], sn[i]);
+              const float e0 = d[i], e1 = e[i];
+              d[i] = rope_turn(e0, e1, cs[i], -sn[i]);
+              e[i] = rope_turn(e1, e0, cs[i], sn[i]);
             }
           }
+          store_vec<T, V>(p, d);
+          store_vec<T, V>(q, e);
+        } else {
+          u[k].store(p);
+          w[k].store(q);
         }
-        store_vec<T, V>(y + (h + k) * a.ys.h + c0, u[k]);
-        store_vec<T, V>(y + (h + k) * a.ys.h + c1, w[k]);
       }
   }
 }
@@ -82,9 +124,9 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
 template <typename T, int V>
 int launch(const RotaryArgs &a, int num_sms, cudaStream_t st) {
   const long long one = (long long)a.batch * a.n * a.heads * (kD / (2 * V));  // threads at one head each
-  // heads per thread: 8 where that still leaves two thousand threads an SM, else fewer
+  // heads per thread: 4 where that still leaves two thousand threads an SM, else fewer
   long long hpt = one / ((long long)num_sms * 2048);
-  hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
+  hpt = hpt < 1 ? 1 : hpt > 4 ? 4 : hpt;
   if (hpt > a.heads) hpt = a.heads;
   const long long items = (long long)a.batch * a.n * ((a.heads + hpt - 1) / hpt) * (kD / (2 * V));
   const long long grid = (items + 255) / 256;
