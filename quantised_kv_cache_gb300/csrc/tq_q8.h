@@ -67,7 +67,7 @@ struct Q8EvictArgs {
   float *dst_weights;
   int *error;
 };
-int launch_q8_evict(const Q8EvictArgs &a, void *stream);
+int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream);
 
 // Attention: the struct of the ABI with its defaults filled in, and the workspace carved up.
 struct Q8AttnArgs {

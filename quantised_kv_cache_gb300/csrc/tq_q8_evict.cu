@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSel = 1024;             // threads of a selecting CTA
 constexpr int kBins = 2048;
+constexpr int kMaxRanks = 8;           // CTAs of a cluster
 constexpr int kSelKeys = 45056;        // keys held in shared memory (176 KB)
 constexpr uint32_t kAlways = 0xffffffffu;  // a slot that stays whatever its weight
 
@@ -62,7 +63,7 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
 
 __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__ Q8EvictArgs a) {
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
+  __shared__ __align__(8) int hist[kBins];
   __shared__ int sums[32], found[2], share[2];
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -111,11 +112,12 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
       cl.sync();
       // bins in falling order: thread t sums bins 2047 - 2t and 2046 - 2t over the cluster
       int hi = 0, lo = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const int *other = cl.map_shared_rank(hist, r);
-        hi += other[kBins - 1 - 2 * tid];
-        lo += other[kBins - 2 - 2 * tid];
-      }
+#pragma unroll
+      for (int r = 0; r < kMaxRanks; ++r)  // unrolled: the remote loads of all ranks in flight at once
+        if (r < ranks) {
+          const int2 x = *reinterpret_cast<const int2 *>(cl.map_shared_rank(hist, r) + kBins - 2 - 2 * tid);
+          hi += x.y, lo += x.x;
+        }
       int total;
       const int above = block_scan(hi + lo, sums, &total);
       if (above < need && need <= above + hi) found[0] = kBins - 1 - 2 * tid, found[1] = need - above;
@@ -140,13 +142,15 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   int tie = block_scan(ties, sums, &all_ties);
   if (tid == 0) share[0] = all_ties;
   cl.sync();
-  for (int r = 0; r < rank; ++r) tie += *cl.map_shared_rank(&share[0], r);
+#pragma unroll
+  for (int r = 0; r < kMaxRanks; ++r) tie += r < rank ? *cl.map_shared_rank(&share[0], r) : 0;
   const int won = max(0, min(ties, need - tie));  // of this thread's ties, the lowest slots
   int all_kept;
   int at = block_scan(more + (pick > 0 ? won : 0), sums, &all_kept);
   if (tid == 0) share[1] = all_kept;
   cl.sync();
-  for (int r = 0; r < rank; ++r) at += *cl.map_shared_rank(&share[1], r);
+#pragma unroll
+  for (int r = 0; r < kMaxRanks; ++r) at += r < rank ? *cl.map_shared_rank(&share[1], r) : 0;
   int left = pick > 0 ? won : 0;
   for (int i = i0; i < i1; ++i) {
     const uint32_t k = key(i);
@@ -171,59 +175,65 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
 
 constexpr int kGather = kQ8Block * 8;
 
-__global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constant__ Q8EvictArgs a) {
-  __shared__ uint32_t red[2][kGather / 32];
+// `per` consecutive blocks of the target; the next block's indices are loaded ahead.
+__global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constant__ Q8EvictArgs a, int per) {
+  __shared__ uint32_t red[2][2][kGather / 32];
   const int tid = threadIdx.x, c = tid & 7, t = tid >> 3;
-  const int j = blockIdx.x;
   const long long bh = blockIdx.y;
-  const int i = j * kQ8Block + t;
-  const int s = i < a.keep ? __ldg(a.kept + bh * a.keep + i) : -1;
-  const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
-  uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  int e0[2] = {kQ8MinExp, kQ8MinExp};
-  if (s >= 0 && s < a.src.capacity) {
-    const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
-    if (from >= 0) {
-      const uint8_t *p = a.src.records + from * kQ8BlockBytes + q8_off(s % kQ8Block, 16 * c);
-      w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-      w[1] = __ldg(reinterpret_cast<const uint4 *>(p + kQ8Plane));
-      e0[0] = log2i(__ldg(a.src.ks + from));
-      e0[1] = log2i(__ldg(a.src.vs + from));
+  const int blocks = (a.keep + kQ8Block - 1) / kQ8Block, j0 = blockIdx.x * per, j1 = min(blocks, j0 + per);
+  const int32_t *kept = a.kept + bh * a.keep;
+  auto index = [&](int j) { return j * kQ8Block + t < a.keep ? __ldg(kept + j * kQ8Block + t) : -1; };
+  int next = index(j0);
+  for (int j = j0; j < j1; ++j) {
+    const int s = next;
+    if (j + 1 < j1) next = index(j + 1);
+    const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
+    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    int e0[2] = {kQ8MinExp, kQ8MinExp};
+    if (s >= 0 && s < a.src.capacity) {
+      const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
+      if (from >= 0) {
+        const uint8_t *p = a.src.records + from * kQ8BlockBytes + q8_off(s % kQ8Block, 16 * c);
+        w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[1] = __ldg(reinterpret_cast<const uint4 *>(p + kQ8Plane));
+        e0[0] = log2i(__ldg(a.src.ks + from));
+        e0[1] = log2i(__ldg(a.src.vs + from));
+      }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    // the largest magnitude of the piece: e4m3 magnitudes are ordered as their low seven bits
-    uint32_t top = __vmaxu4(__vmaxu4(w[k].x & 0x7f7f7f7fu, w[k].y & 0x7f7f7f7fu),
-                            __vmaxu4(w[k].z & 0x7f7f7f7fu, w[k].w & 0x7f7f7f7fu));
-    top = __vmaxu4(top, top >> 16);
-    top = max(top & 0xffu, (top >> 8) & 0xffu);
-    const uint32_t amax = __reduce_max_sync(kFull, __float_as_uint(e4m3x2_f(top).x * pow2i(e0[k])));
-    if ((tid & 31) == 0) red[k][tid >> 5] = amax;
-  }
-  __syncthreads();
-  if (to < 0) return;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int e = q8_exponent(__reduce_max_sync(kFull, red[k][tid & (kGather / 32 - 1)]));
-    if (e != e0[k]) {
-      const float f = pow2i(min(max(e0[k] - e, -126), 126));
-      w[k] = make_uint4(e4m3x4_scaled(w[k].x, f), e4m3x4_scaled(w[k].y, f), e4m3x4_scaled(w[k].z, f), e4m3x4_scaled(w[k].w, f));
+    for (int k = 0; k < 2; ++k) {
+      // the largest magnitude of the piece: e4m3 magnitudes are ordered as their low seven bits
+      uint32_t top = __vmaxu4(__vmaxu4(w[k].x & 0x7f7f7f7fu, w[k].y & 0x7f7f7f7fu),
+                              __vmaxu4(w[k].z & 0x7f7f7f7fu, w[k].w & 0x7f7f7f7fu));
+      top = __vmaxu4(top, top >> 16);
+      top = max(top & 0xffu, (top >> 8) & 0xffu);
+      const uint32_t amax = __reduce_max_sync(kFull, __float_as_uint(e4m3x2_f(top).x * pow2i(e0[k])));
+      if ((tid & 31) == 0) red[j & 1][k][tid >> 5] = amax;
     }
-    *reinterpret_cast<uint4 *>(a.dst.records + to * kQ8BlockBytes + k * kQ8Plane + q8_off(t, 16 * c)) = w[k];
-    if (tid == 0) (k ? a.dst.vs : a.dst.ks)[to] = pow2i(e);
+    __syncthreads();
+    if (to < 0) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = q8_exponent(__reduce_max_sync(kFull, red[j & 1][k][tid & (kGather / 32 - 1)]));
+      if (e != e0[k]) {
+        const float f = pow2i(min(max(e0[k] - e, -126), 126));
+        w[k] = make_uint4(e4m3x4_scaled(w[k].x, f), e4m3x4_scaled(w[k].y, f), e4m3x4_scaled(w[k].z, f), e4m3x4_scaled(w[k].w, f));
+      }
+      *reinterpret_cast<uint4 *>(a.dst.records + to * kQ8BlockBytes + k * kQ8Plane + q8_off(t, 16 * c)) = w[k];
+      if (tid == 0) (k ? a.dst.vs : a.dst.ks)[to] = pow2i(e);
+    }
   }
 }
 
 }  // namespace
 
-int launch_q8_evict(const Q8EvictArgs &a, void *stream) {
+int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   const long long bh = (long long)a.batch * a.heads;
   if (bh > 65535) return TQ_ERR_UNSUPPORTED;
   // CTAs per sequence-head: one up to 8192 slots (a pass over them is then a few microseconds), up to 8 beyond
   int ranks = 1;
-  while (ranks < 8 && a.src.capacity > 8192 * ranks) ranks *= 2;
+  while (ranks < kMaxRanks && a.src.capacity > 8192 * ranks) ranks *= 2;
   const int held = (a.src.capacity + ranks - 1) / ranks;
   const size_t smem = sizeof(uint32_t) * (size_t)(held < kSelKeys ? held : kSelKeys);
   if (cudaFuncSetAttribute(q8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) != cudaSuccess)
@@ -241,7 +251,9 @@ int launch_q8_evict(const Q8EvictArgs &a, void *stream) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, q8_select_kernel, a) != cudaSuccess) return TQ_ERR_CUDA;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
-  q8_gather_kernel<<<dim3((unsigned)blocks, (unsigned)bh), kGather, 0, st>>>(a);
+  // blocks per CTA: 4 where at least four rounds of four CTAs an SM remain
+  const int per = (long long)blocks * bh >= 16LL * 4 * num_sms ? 4 : 1;
+  q8_gather_kernel<<<dim3((unsigned)((blocks + per - 1) / per), (unsigned)bh), kGather, 0, st>>>(a, per);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -203,7 +203,7 @@ tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *ds
   const tq::Q8EvictArgs a{tq::q8_cache(src), tq::q8_cache(dst), batch, heads_kv, keep, sink, recent, d_seq_lens,
                           d_weights, d_positions, d_kept, d_dst_lens, d_dst_positions, d_dst_weights,
                           &ctx->dparams->error};
-  return (tq_status)tq::launch_q8_evict(a, stream);
+  return (tq_status)tq::launch_q8_evict(a, ctx->num_sms, stream);
 }
 
 }  // extern "C"
