@@ -8,7 +8,7 @@
 // every kept slot its place. Keys are read once from memory and stay in shared memory (what does not
 // fit is read again). A cluster of up to 8 CTAs shares one long sequence-head: each holds a run of
 // slots, histograms and counts are added through distributed shared memory.
-// q8_gather_kernel: one CTA per 64-token block of the target. A thread owns one 16-byte piece (16
+// q8_gather_kernel: one CTA per 64-token block of the target (or per few). A thread owns one 16-byte piece (16
 // coordinates of one token) of the keys and one of the values; the new block's scale comes from the largest value, and codes are rounded
 // only where their block's scale differs from it. Both bound by memory.
 
@@ -64,6 +64,7 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
 __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__ Q8EvictArgs a) {
   extern __shared__ uint32_t keys[];
   __shared__ __align__(8) int hist[kBins];
+  __shared__ __align__(8) int added[kBins / 2];
   __shared__ int sums[32], found[2], share[2];
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -75,7 +76,6 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   }
   const int m = min(n, a.keep);
   const float *w = a.weights + (long long)bh * a.src.capacity;
-  const int32_t *pos = a.positions ? a.positions + (long long)bh * a.src.capacity : nullptr;
   int32_t *kept = a.kept + (long long)bh * a.keep;
   float *dw = a.dst_weights ? a.dst_weights + (long long)bh * a.dst.capacity : nullptr;
   int32_t *dp = a.dst_positions ? a.dst_positions + (long long)bh * a.dst.capacity : nullptr;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
     return weight_key(__ldg(w + s));
   };
   auto key = [&](int i) -> uint32_t { return i < kSelKeys ? keys[i] : make(i); };
-#pragma unroll 8
+#pragma unroll 16
   for (int i = tid; i < min(cnt, kSelKeys); i += kSel) keys[i] = make(i);
   __syncthreads();  // the runs below cross threads, also where nothing is chosen by weight
 
@@ -112,12 +112,22 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
       cl.sync();
       // bins in falling order: thread t sums bins 2047 - 2t and 2046 - 2t over the cluster
       int hi = 0, lo = 0;
+      if (ranks == 1) {
+        hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
+      } else {
+        // each rank adds up its share of the bins, then reads the others' sums (loads of all ranks in flight at once)
+        const int part = kBins / ranks;
+        if (tid < part) {
+          int x = 0;
 #pragma unroll
-      for (int r = 0; r < kMaxRanks; ++r)  // unrolled: the remote loads of all ranks in flight at once
-        if (r < ranks) {
-          const int2 x = *reinterpret_cast<const int2 *>(cl.map_shared_rank(hist, r) + kBins - 2 - 2 * tid);
-          hi += x.y, lo += x.x;
+          for (int r = 0; r < kMaxRanks; ++r) x += r < ranks ? cl.map_shared_rank(hist, r)[rank * part + tid] : 0;
+          added[tid] = x;
         }
+        cl.sync();
+        const int first = kBins - 2 - 2 * tid;  // both bins are one rank's
+        const int2 x = *reinterpret_cast<const int2 *>(cl.map_shared_rank(added, first / part) + first % part);
+        hi = x.y, lo = x.x;
+      }
       int total;
       const int above = block_scan(hi + lo, sums, &total);
       if (above < need && need <= above + hi) found[0] = kBins - 1 - 2 * tid, found[1] = need - above;
@@ -157,16 +167,12 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
     bool stay = k == kAlways || (pick > 0 && k > prefix);
     if (!stay && pick > 0 && k == prefix && left > 0) stay = true, --left;
     if (stay && at < a.keep) {
-      const int s = s0 + i;
-      kept[at] = s;
-      if (dw) dw[at] = __ldg(w + s);
-      if (dp) dp[at] = pos ? __ldg(pos + s) : s;
-      ++at;
+      kept[at++] = s0 + i;
     }
   }
   const int me = rank * kSel + tid, everyone = ranks * kSel;
   for (int i = m + me; i < a.keep; i += everyone) kept[i] = -1;
-  for (int i = m + me; i < a.dst.capacity; i += everyone) {
+  for (int i = a.keep + me; i < a.dst.capacity; i += everyone) {  // (the gathering kernel writes the first `keep`)
     if (dw) dw[i] = 0.f;
     if (dp) dp[i] = 0;
   }
@@ -190,7 +196,13 @@ __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constan
     const long long to = q8_block(a.dst.btab, a.dst.pool_blocks, bh * a.dst.nblk + j, a.error);
     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     int e0[2] = {kQ8MinExp, kQ8MinExp};
-    if (s >= 0 && s < a.src.capacity) {
+    const bool live = s >= 0 && s < a.src.capacity;
+    if (c < 2 && j * kQ8Block + t < a.keep) {  // its weight and position
+      const long long at = bh * a.dst.capacity + j * kQ8Block + t, of = bh * a.src.capacity + s;
+      if (c == 0 && a.dst_weights) a.dst_weights[at] = live ? __ldg(a.weights + of) : 0.f;
+      if (c == 1 && a.dst_positions) a.dst_positions[at] = !live ? 0 : a.positions ? __ldg(a.positions + of) : s;
+    }
+    if (live) {
       const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
       if (from >= 0) {
         const uint8_t *p = a.src.records + from * kQ8BlockBytes + q8_off(s % kQ8Block, 16 * c);
