@@ -110,8 +110,9 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   // this thread's coordinates: 8 from c0 on, 8 from c1 on
   const int dim = a.table.dim, half = dim / 2;
   const bool turn = rope && 16 * j < dim;
-  const bool halves = ROPE == kOwn && turn && !a.table.interleaved;
-  const int c0 = halves ? 8 * j : 16 * j, c1 = halves ? half + 8 * j : c0 + 8;
+  // (without a rotation too two eights 64 apart: a row's loads of a warp are then whole lines)
+  const bool split = (ROPE == kOwn && turn && !a.table.interleaved) || !rope;
+  const int c0 = split ? 8 * j : 16 * j, c1 = !split ? c0 + 8 : rope ? half + 8 * j : kD / 2 + 8 * j;
   constexpr int kSines = ROPE == kPartner ? 16 : 8;
   float cs[kSines], sn[kSines];
   if (turn && fresh) {
@@ -140,7 +141,7 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
     if (fresh && h + 1 < h1) next.load(x0 + (h + 1) * st.h + c0, x0 + (h + 1) * st.h + c1);
     if (turn && fresh) {
       if constexpr (ROPE == kOwn) {
-        if (halves) {  // pair i: coordinates i of the two eights
+        if (split) {  // pair i: coordinates i of the two eights
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 u = in.pair(i), v = in.pair(i + 4);
@@ -216,7 +217,7 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
         }
         w[i] = cvt_e4m3x2(u.x * f, u.y * f) | (cvt_e4m3x2(v.x * f, v.y * f) << 16);
       }
-      if (halves) {
+      if (split) {
         *reinterpret_cast<uint2 *>(plane + q8_off(t, c0)) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2 *>(plane + q8_off(t, c1)) = make_uint2(w[2], w[3]);
       } else {

@@ -184,7 +184,8 @@ constexpr int kGather = kQ8Block * 8;
 // `per` consecutive blocks of the target; the next block's indices are loaded ahead.
 __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constant__ Q8EvictArgs a, int per) {
   __shared__ uint32_t red[2][2][kGather / 32];
-  const int tid = threadIdx.x, c = tid & 7, t = tid >> 3;
+  // a warp: one 16-byte column of 32 tokens, whose pieces lie 8 to a 128-byte line
+  const int tid = threadIdx.x, t = tid & 63, c = tid >> 6;
   const long long bh = blockIdx.y;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block, j0 = blockIdx.x * per, j1 = min(blocks, j0 + per);
   const int32_t *kept = a.kept + bh * a.keep;
