@@ -85,9 +85,11 @@ struct Q8AttnArgs {
   float *weights;
   float *lse;   // [batch][heads_q][n_q], natural log (workspace when the caller gives none but the weights need it)
   float *parts; // partial softmax records
+  float *scores = nullptr;  // [batch][heads_kv][group x n_q][scores_ld] in log2, kept for the weights (or NULL)
+  long long scores_ld = 0;
   int *error;
 };
-size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int weights);
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights);
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q);
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 int launch_q8_weights(const Q8AttnArgs &a, void *stream);

@@ -1,20 +1,22 @@
 // Attention over the 8-bit cache for few query rows per KV head (tq_q8_attention): decode steps,
-// drafts, short prompts. Up to 16 rows (query tokens x heads of the group) are one unit of work with
+// drafts, short prompts. Up to 16 rows (query tokens x heads of the group; 8 for 32-bit results) are one unit of work with
 // a (sequence, KV head).
 //
 // Mathematics, per unit: S = K Q^T for 128 tokens at a time (token = accumulator lane, row = column),
 // t = log2(e) score, running maximum m and sum l of 2^(t - m) per row, O = sum 2^(t - m) v. The codes of
 // the keys and values are tensor-core operands as they lie in the cache (no conversion, no
-// transposition); queries and probabilities enter as three e4m3 / e5m2 terms (six for fp32 results).
-// A block's scale multiplies the scores of its tokens, and its part of O.
+// transposition); queries and probabilities enter as 4 e5m2 terms (8 for fp32 results), side by side in
+// one operand. A block's scale multiplies the scores of its tokens, and its part of O.
 //
 // Bound by the cache's bytes: 256 per token and KV head, read once. Per SM a tile of 128 tokens
-// (32 KB) may take 1500 clocks at the memory's rate; 4 warpgroups work on 4 tiles at once, each alone on its
-// tile from the score MMAs to the value sums, so that the chain of a tile (two MMA round trips of 400-600
-// clocks, two barriers) is hidden by the other three. One producer warp keeps a ring of 4 or 5
+// (32 KB) may take 1500 clocks at the memory's rate; its 8 MMAs of 128 x (16 .. 64) x 32 take 43 to 50 each, the
+// time of reading the 128-row operand. 4 warpgroups work on 4 tiles at once, each alone on its
+// tile from the score MMAs to the value sums, so that the chain of a tile (two MMA round trips, three barriers) is hidden by
+// the other three. One producer warp keeps a ring of 5
 // tiles filled by bulk copies (whole 8 KB planes). Grid: one CTA per SM; the (sequence, row tile, head, tile) space is
 // cut into equal slices, so ragged batches and long single sequences load every SM alike. A unit that lies in one
 // slice is finished there; one that was cut leaves a partial record per slice, joined by q8_join_kernel.
+// The probabilities' sum for the output counts what their terms hold, that of the log-sum the numbers themselves.
 
 #include "tq_q8_rows.cuh"
 
@@ -30,8 +32,9 @@ constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launc
 constexpr long long kFewRows = 64;      // rows up to which this kernel takes a 16-bit call
 constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
 
-constexpr int stages_of(int GR) { return GR == 1 ? 5 : 4; }
-constexpr int tmem_stride(int GR) { return 64 * GR; }  // columns of a warpgroup: S, then O of the two blocks
+constexpr int kStages = 5;
+constexpr int kRows = 16;               // rows of a partial record
+constexpr int rows_of(int T) { return T == 8 ? 8 : 16; }  // rows of a unit: what tensor memory holds the terms' columns of
 
 struct Entries {
   int pre[kEntries + 1];  // tiles (of one head) before each entry
@@ -47,8 +50,8 @@ struct Cut {
 struct Shared {
   // A tile's arrival barrier is one of stages x warpgroups, so that its earlier use was the same warpgroup's: a
   // warpgroup that is ahead would take a parity of a stage's older, still incomplete copy for its own.
-  uint64_t full[5 * kWg], empty[5], bar_s[kWg], bar_o[kWg];
-  float4 info[5];            // key scales of the tile's two blocks, value scales (negative: not mapped)
+  uint64_t full[kStages * kWg], empty[kStages], bar_s[kWg], bar_o[kWg];
+  float4 info[kStages];      // key scales of the tile's two blocks, value scales (negative: not mapped)
   float qscale[kRows], slope[kRows];
   int2 range[kRows];
   int qpos[kRows];
@@ -62,13 +65,15 @@ struct Shared {
 
 __device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"(kConsumers) : "memory"); }
 
-template <int NR, int GR>
+template <int NR, int T>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, int rts, Cut *cuts) {
-  constexpr int kStages = stages_of(GR);
+  constexpr int kUnitRows = rows_of(T), kN = stacked_rows(NR, T), kOp = kN * 128;  // an operand's rows and bytes
+  constexpr int kCols = 2 * kN;  // a warpgroup's columns: S, in its place O of the first block, then O of the second
+  static_assert(NR <= kUnitRows && kWg * kCols <= 512 && (kWg - 1) * NR * 512 <= kWg * kOp, "");
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
-  uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage, *pbuf = qbuf + GR * 3 * kTerm;
+  uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage, *pbuf = qbuf + kOp;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, R = G * a.n_q;
 
@@ -80,7 +85,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     sm.bad = 0;
   }
   if (warp == kThreads / 32 - 1) {
-    tmem_alloc(smem_u32(&sm.tmem), kWg * tmem_stride(GR));
+    tmem_alloc(smem_u32(&sm.tmem), kWg * kCols);
     tmem_relinquish();
   }
   pdl_wait();
@@ -89,10 +94,10 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   const int E = nb * rts;
   int count = 0;
   if (tid < E) {
-    const int b = b0 + tid / rts, r0 = (rt0 + tid % rts) * kRows;
+    const int b = b0 + tid / rts, r0 = (rt0 + tid % rts) * kUnitRows;
     int len, m;
     seq_sizes(a, b, &len, &m, blockIdx.x == 0);
-    const int i0 = r0 / G, i1 = (min(R, r0 + kRows) - 1) / G;
+    const int i0 = r0 / G, i1 = (min(R, r0 + kUnitRows) - 1) / G;
     int lo = 0x7fffffff, hi = 0;
     for (int i = i0; i <= i1; ++i) {
       const int2 r = row_range(a, b, i, len, m);
@@ -207,19 +212,19 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   } else {
     // ================================ consumers
     const int wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
-    const uint32_t t_s = tmem + wg * tmem_stride(GR), t_o = t_s + 16 * GR;
+    const uint32_t t_s = tmem + wg * kCols;
     const uint32_t lanes = (uint32_t)(32 * w4) << 16;
-    uint8_t *const pmine = pbuf + wg * GR * 3 * kTerm;
+    uint8_t *const pmine = pbuf + wg * kOp;
     uint8_t *const pbyte = pmine + (wt >> 4) * 128 + (wt & 15);
     const bool issue = elect_lane();  // of the warpgroup's first warp
-    const uint32_t u_s = warp_uniform(t_s), u_o = warp_uniform(t_o), u_q = smem_u32(qbuf), u_p = warp_uniform(smem_u32(pmine));
+    const uint32_t u_s = warp_uniform(t_s), u_q = smem_u32(qbuf), u_p = warp_uniform(smem_u32(pmine));
     const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
     uint32_t phase = 0;  // of this warpgroup's two barriers: its tiles so far
     long long g = g0;
     while (g < g1) {
       int e, h, t0, cnt;
       locate(g, e, h, t0, cnt);
-      const int b = b0 + e / rts, row0 = (rt0 + e % rts) * kRows;
+      const int b = b0 + e / rts, row0 = (rt0 + e % rts) * kUnitRows;
       const long long end = min(g1, g - t0 + cnt);
       const int first = sm.ent.lo[e], hi = sm.ent.hi[e];
 
@@ -229,15 +234,12 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         int len, m;
         seq_sizes(a, b, &len, &m, false);
         const bool live = warp < NR && row < R && i < m;
-        uint32_t w[GR][3];
-        const int ex = row_terms<GR>(a, b, hq, i, live, lane, w);
+        uint32_t w[T];
+        const int ex = row_e5m2<T>(a, b, hq, i, live, lane, w);
         bar_all();  // everyone is done with the unit before
         if (warp < NR) {
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *reinterpret_cast<uint32_t *>(qbuf + (gr * 3 + k) * kTerm + q8_off(warp, 4 * lane)) = w[gr][k];
+          for (int k = 0; k < T; ++k) *reinterpret_cast<uint32_t *>(qbuf + q8_off(k * NR + warp, 4 * lane)) = w[k];
           if (lane == 0) {
             sm.qscale[warp] = pow2i(ex);
             const int2 rg = live ? row_range(a, b, i, len, m) : make_int2(0, 0);
@@ -263,15 +265,10 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           tc_fence_after_sync();
           const uint32_t ring_k = warp_uniform(smem_u32(ring + s * kStage));
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-              for (int ks = 0; ks < kD / 32; ++ks)
-                if (issue)
-                  tc_mma_f8(u_s + 16 * gr, tc_sdesc_kmajor(ring_k + 256 * ks, 128, 1024),
-                            tc_sdesc_kmajor(u_q + (gr * 3 + k) * kTerm + 256 * ks, 128, 1024),
-                            tc_idesc_f8(128, kRows, 0, k == 2, 0, 0), k > 0 || ks > 0);
+          for (int ks = 0; ks < kD / 32; ++ks)
+            if (issue)
+              tc_mma_f8(u_s, tc_sdesc_kmajor(ring_k + 256 * ks, 128, 1024), tc_sdesc_kmajor(u_q + 256 * ks, 128, 1024),
+                        tc_idesc_f8(128, kN, 0, 1, 0, 0), ks > 0);
           if (issue) tc_commit(smem_u32(&sm.bar_s[wg]));
           __syncwarp();
         }
@@ -290,13 +287,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         __syncwarp();  // the loads from tensor memory are a warp's
         tc_fence_after_sync();
         float t[NR];
-        tmem_ld_cols<NR>(t_s + lanes, t);
-        if constexpr (GR == 2) {
-          float t2[NR];
-          tmem_ld_cols<NR>(t_s + 16 + lanes, t2);
-#pragma unroll
-          for (int r = 0; r < NR; ++r) t[r] = fmaf(t2[r], 1.f / kGroupScale, t[r]);
-        }
+        tmem_term_sums<NR, T>(t_s + lanes, t);
         // ---- scores, and the rows' maxima over the tile
         float mine = -INFINITY;
 #pragma unroll
@@ -305,13 +296,13 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           t[r] = q8_score_log2(t[r] * (sm.qscale[r] * ks), sc);
           if (a.slopes) t[r] = fmaf(-sm.slope[r], (float)__sad(sm.qpos[r], kp, 0u), t[r]);
           if (slot < rg.x || slot >= rg.y || ks < 0.f) t[r] = -INFINITY;
+          if (a.scores && row0 + r < R) a.scores[((((long long)b * a.heads_kv + h) * R + row0 + r) * a.scores_ld) + slot] = t[r];
           const float w = warp_fmax(t[r]);
           if (lane == r) mine = w;
         }
         if (lane < NR) reinterpret_cast<float *>(&sm.wmax[wg][lane])[w4] = mine;
         bar_wg(wg);
-        // ---- probabilities (times 2^8), their terms, the sums
-        float corr_any[NR];
+        // ---- probabilities (times 2^15), their terms, the sums
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float4 x = sm.wmax[wg][r];
@@ -319,31 +310,25 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           const float use = top == -INFINITY ? 0.f : top;
           const float corr = ex2_approx(m[r] - use);
           m[r] = top;
-          t[r] = ex2_approx(t[r] - use + 8.f);
+          t[r] = ex2_approx(t[r] - use + 15.f);
           l[r] = fmaf(l[r], corr, t[r]);
-          lr[r] *= corr;
+          lr[r] = fmaf(lr[r], corr, t[r]);
           o[r] *= corr;
-          corr_any[r] = t[r];
         }
 #pragma unroll
         for (int r = 0; r < NR; r += 2) {
-          float p0 = t[r], p1 = r + 1 < NR ? t[r + 1 < NR ? r + 1 : r] : 0.f;
-          uint8_t *at = pbyte + (r >> 3) * 1024 + (r & 7) * 16;
-          float left = 1.f;
+          const int r1 = r + 1 < NR ? r + 1 : r;
+          float p0 = t[r], p1 = t[r1];
+          uint32_t term[T];
+          split_e5m2<T>(p0, p1, term);
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) {
-            uint32_t term[3];
-            split_terms(p0, p1, term);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              at[(gr * 3 + k) * kTerm] = (uint8_t)term[k];
-              if (r + 1 < NR) at[(gr * 3 + k) * kTerm + 16] = (uint8_t)(term[k] >> 8);
-            }
-            if (gr + 1 < GR) p0 *= kGroupScale, p1 *= kGroupScale, left = 1.f / kGroupScale;
+          for (int k = 0; k < T; ++k) {
+            const int n0 = k * NR + r, n1 = k * NR + r1;
+            pbyte[(n0 >> 3) * 1024 + (n0 & 7) * 16] = (uint8_t)term[k];
+            if (r1 > r) pbyte[(n1 >> 3) * 1024 + (n1 & 7) * 16] = (uint8_t)(term[k] >> 8);
           }
-          // what the terms add up to
-          lr[r] += corr_any[r] - p0 * left;
-          if (r + 1 < NR) lr[r + 1 < NR ? r + 1 : r] += corr_any[r + 1 < NR ? r + 1 : r] - p1 * left;
+          lr[r] -= p0;  // what the terms do not hold
+          if (r1 > r) lr[r1] -= p1;
         }
         fence_proxy_async_shared();
         tc_fence_before_sync();
@@ -357,15 +342,10 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
             if (!(blk ? use1 : use0)) continue;
             const bool two = n - blk * kQ8Block > 32;  // K-steps of 32 tokens
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-              for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int st = 0; st < 2; ++st)
-                  if (issue && (st == 0 || two))
-                    tc_mma_f8(u_o + (blk * GR + gr) * 16, tc_sdesc_kmajor(ring_v + blk * kQ8Plane + st * 4096, 1024, 128),
-                              tc_sdesc_kmajor(u_p + (gr * 3 + k) * kTerm + blk * 512 + 256 * st, 128, 1024),
-                              tc_idesc_f8(128, kRows, 0, k == 2, 1, 0), k > 0 || st > 0);
+            for (int st = 0; st < 2; ++st)
+              if (issue && (st == 0 || two))
+                tc_mma_f8(u_s + blk * kN, tc_sdesc_kmajor(ring_v + blk * kQ8Plane + st * 4096, 1024, 128),
+                          tc_sdesc_kmajor(u_p + blk * 512 + 256 * st, 128, 1024), tc_idesc_f8(128, kN, 0, 1, 1, 0), st > 0);
           }
           if (issue) {
             tc_commit(smem_u32(&sm.empty[s]));
@@ -382,17 +362,12 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           if (!(blk ? use1 : use0)) continue;
           const float vs = blk ? info.w : info.z;
           float d[NR];
-          tmem_ld_cols<NR>(t_o + blk * GR * 16 + lanes, d);
-          if constexpr (GR == 2) {
-            float d2[NR];
-            tmem_ld_cols<NR>(t_o + (blk * GR + 1) * 16 + lanes, d2);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) d[r] = fmaf(d2[r], 1.f / kGroupScale, d[r]);
-          }
+          tmem_term_sums<NR, T>(t_s + blk * kN + lanes, d);
 #pragma unroll
           for (int r = 0; r < NR; ++r) o[r] = fmaf(d[r], vs, o[r]);
         }
         tc_fence_before_sync();
+        bar_wg(wg);  // the next scores take the place of these sums
       }
 
       // ---- join the four warpgroups (thread = coordinate of O)
@@ -446,7 +421,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
             else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
             else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
             if (a.lse && wt == 0)
-              a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (top + log2f(sl) - 8.f) * kLn2;
+              a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (top + log2f(sl) - 15.f) * kLn2;
           } else {
             part[r * kPartRow + wt] = x;
             if (wt == 0) {
@@ -474,16 +449,16 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == kThreads / 32 - 1) tmem_dealloc(tmem, kWg * tmem_stride(GR));
+  if (warp == kThreads / 32 - 1) tmem_dealloc(tmem, kWg * kCols);
 }
 
 // One CTA per (CTA of the main kernel, row): the parts of the unit that was cut there. Four groups of
 // 128 threads (thread = coordinate) take every fourth part; its maximum, sums and O are joined in shared memory.
-__global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8AttnArgs a, const Cut *cuts) {
+__global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8AttnArgs a, int unit_rows, const Cut *cuts) {
   __shared__ float so[4][kD], sl[4], slr[4], stop[4];
   pdl_wait();
   const Cut cut = cuts[blockIdx.x];
-  const int r = blockIdx.y, row = cut.rt * kRows + r, G = a.group;
+  const int r = blockIdx.y, row = cut.rt * unit_rows + r, G = a.group;
   if (cut.parts < 2 || row >= G * a.n_q) return;
   int len, m;
   seq_sizes(a, cut.b, &len, &m, false);
@@ -520,69 +495,77 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
   if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
   else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
   else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
-  if (a.lse && d == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
+  if (a.lse && d == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 15.f) * kLn2;
 }
 
-template <int NR, int GR>
+template <int NR, int T>
 int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
-  constexpr int smem = stages_of(GR) * kStage + GR * 3 * kTerm * (1 + kWg);
-  if (cudaFuncSetAttribute(q8_attend_kernel<NR, GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  constexpr int smem = kStages * kStage + stacked_rows(NR, T) * 128 * (1 + kWg);
+  if (cudaFuncSetAttribute(q8_attend_kernel<NR, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  if (launch_overlapped(true, q8_attend_kernel<NR, GR>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
+  if (launch_overlapped(true, q8_attend_kernel<NR, T>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
-  if (launch_overlapped(true, q8_join_kernel, dim3(num_sms, NR), dim3(512), 0, st, a, (const Cut *)cuts) != cudaSuccess)
+  if (launch_overlapped(true, q8_join_kernel, dim3(num_sms, NR), dim3(512), 0, st, a, rows_of(T), (const Cut *)cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
   return TQ_OK;
 }
 
+// The scores are kept for the weights when they fit into this much workspace; else they are formed again.
+constexpr size_t kScoreBytes = size_t(256) << 20;
+size_t score_bytes(int batch, int heads_q, int n_q, int max_len) {
+  const size_t n = (size_t)batch * heads_q * n_q * ((max_len + kTile - 1) / kTile * kTile) * sizeof(float);
+  return n <= kScoreBytes ? n : 0;
+}
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
 }  // namespace
 
-// Workspace: the log-sums when the weights need them, then either kernel's records (few rows: cuts and parts).
-static size_t few_bytes(int num_sms) {
-  return ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16 + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
-}
-
-size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int weights) {
-  const size_t lse = weights ? ((size_t)batch * heads_q * n_q * sizeof(float) + 15) / 16 * 16 : 0;
-  const size_t few = few_bytes(num_sms);
-  size_t many = 0;
-  if ((long long)(heads_q / heads_kv) * n_q > kFewRows) many = q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
-  return lse + (few > many ? few : many);
+// Workspace: for the weights the log-sums and, for few rows, the scores; then either kernel's records (few rows: cuts and parts).
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
+  const bool few_rows = (long long)(heads_q / heads_kv) * n_q <= kFewRows;
+  const size_t lse = weights ? round16((size_t)batch * heads_q * n_q * sizeof(float)) : 0;
+  const size_t scores = weights && few_rows ? score_bytes(batch, heads_q, n_q, max_len) : 0;
+  const size_t few = round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
+  const size_t many = few_rows ? 0 : q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
+  return lse + scores + (few > many ? few : many);
 }
 
 int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   Q8AttnArgs a = args;
-  char *many = (char *)workspace;
-  if (a.weights) {
-    if (!a.lse) a.lse = (float *)many;
-    many += ((size_t)a.batch * a.heads_q * a.n_q * sizeof(float) + 15) / 16 * 16;
-  }
-  Cut *cuts = (Cut *)many;
-  a.parts = (float *)(many + ((size_t)num_sms * sizeof(Cut) + 15) / 16 * 16);
   const long long R = (long long)a.group * a.n_q;
-  // many rows with results of 16 bits: rows as lanes. Its 256-row units cost a fifth of a microsecond a row tile
-  // of 16 less from about 64 rows on, and waste less of the tensor cores
+  char *w = (char *)workspace;
+  if (a.weights) {
+    if (!a.lse) a.lse = (float *)w;
+    w += round16((size_t)a.batch * a.heads_q * a.n_q * sizeof(float));
+    const size_t scores = R <= kFewRows ? score_bytes(a.batch, a.heads_q, a.n_q, a.max_len) : 0;
+    if (scores) a.scores = (float *)w, a.scores_ld = (a.max_len + kTile - 1) / kTile * kTile;
+    w += scores;
+  }
+  // many rows with results of 16 bits: rows as lanes
   if (R > kFewRows && a.out_dtype != TQ_F32) {
-    const int s = launch_q8_prompt(a, many, num_sms, stream);
+    const int s = launch_q8_prompt(a, w, num_sms, stream);
     if (s != TQ_OK) return s;
   } else {
-    const int all = (int)((R + kRows - 1) / kRows);  // row tiles of a sequence; at most kEntries of all in a launch
+    Cut *cuts = (Cut *)w;
+    a.parts = (float *)(w + round16((size_t)num_sms * sizeof(Cut)));
+    const int unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
+    if ((R + unit - 1) / unit > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    const int all = (int)((R + unit - 1) / unit);  // row tiles of a sequence; at most kEntries of all in a launch
     const int per = all < kEntries ? kEntries / all : 1;
     for (int b0 = 0; b0 < a.batch; b0 += per)
       for (int rt0 = 0; rt0 < all; rt0 += kEntries) {
         const int nb = a.batch - b0 < per ? a.batch - b0 : per, rts = all - rt0 < kEntries ? all - rt0 : kEntries;
         int s;
         if (a.out_dtype == TQ_F32)
-          s = R == 1 ? launch_rows<1, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-              : R <= 4 ? launch_rows<4, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-              : R <= 8 ? launch_rows<8, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-                       : launch_rows<16, 2>(a, cuts, b0, nb, rt0, rts, num_sms, st);
+          s = R == 1 ? launch_rows<1, 8>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 4 ? launch_rows<4, 8>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+                       : launch_rows<8, 8>(a, cuts, b0, nb, rt0, rts, num_sms, st);
         else
-          s = R == 1 ? launch_rows<1, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-              : R <= 4 ? launch_rows<4, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-              : R <= 8 ? launch_rows<8, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st)
-                       : launch_rows<16, 1>(a, cuts, b0, nb, rt0, rts, num_sms, st);
+          s = R == 1 ? launch_rows<1, 4>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 4 ? launch_rows<4, 4>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+              : R <= 8 ? launch_rows<8, 4>(a, cuts, b0, nb, rt0, rts, num_sms, st)
+                       : launch_rows<16, 4>(a, cuts, b0, nb, rt0, rts, num_sms, st);
         if (s != TQ_OK) return s;
       }
   }

@@ -3,13 +3,12 @@
 //
 // The cache's codes go to the tensor cores as they lie (tcgen05.mma kind::f8f6f4: fp8 products are
 // exact, sums are fp32). The other operand, queries and probabilities, is a sum of 8-bit terms on one
-// scale: x = t0 + t1 + t2 + r, t0 and t1 the e4m3 numbers nearest to what is left (4 significant bits
-// each), t2 the nearest e5m2 number (3 bits, and 2^-16 as its smallest step where e4m3 ends at 2^-9).
-// With the largest magnitude of a row in [128, 256) -- queries by a power of two of their own,
-// probabilities by 2^8 -- |r| <= 2^-11 |x| for |x| >= 2^-2 and <= 2^-13 below (t1 then has its smallest
-// step, 2^-9); bf16 and fp16 queries come out exact but for such small coordinates. Each term is
-// one more pass over the same accumulator. A second group of three terms, of 2^11 r, accumulates apart
-// for results that keep 32 bits.
+// scale, each the number nearest to what the ones before have left:
+//  - few rows: e5m2 terms (3 significant bits each, down to 2^-16) with a row's largest magnitude near 2^15, so that T
+//    terms leave 2^-3T of any number that is not 2^-32 of the largest. The terms of all rows lie side by side
+//    in one operand: its N is small whatever T, and an MMA of so few columns takes the time of its other operand.
+//  - many rows: e4m3 terms (4 bits each, down to 2^-9), two of them, or a third in e5m2, with the largest in [128, 256):
+//    2^-8 (2^-11) of numbers from 2^-2 on, 2^-10 (2^-13) below. Each is one more pass over the same accumulator.
 #pragma once
 
 #include "tq_q8.cuh"
@@ -19,7 +18,6 @@ namespace tq {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGroupScale = 2048.f;  // 2^11: the second group holds kGroupScale * r
 
 // Instruction descriptor of kind::f8f6f4, fp32 accumulate: A e4m3, B e4m3 (0) or e5m2 (1); `a_mn`, `b_mn`: the
 // operand is MN-major. Fields as in tc_idesc_f16_f32, formats 0 = e4m3, 1 = e5m2.
@@ -70,6 +68,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&f)[N]) {
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
         : "r"(taddr) : "memory");
+  } else if constexpr (N == 32) {
+    tmem_ld_x32(taddr, v);
   } else {
     static_assert(N == 16, "");
     asm volatile(
@@ -83,17 +83,25 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&f)[N]) {
   for (int i = 0; i < N; ++i) f[i] = __uint_as_float(v[i]);
 }
 
-// The three terms of (a, b), each a pair of bytes (a's low); a and b become what is left.
-__device__ __forceinline__ void split_terms(float &a, float &b, uint32_t (&term)[3]) {
+// The three terms (e4m3, e4m3, e5m2) of (a, b), each a pair of bytes (a's low).
+__device__ __forceinline__ void split_terms(float a, float b, uint32_t (&term)[3]) {
   term[0] = cvt_e4m3x2(a, b);
   float2 f = e4m3x2_f(term[0]);
   a -= f.x, b -= f.y;
   term[1] = cvt_e4m3x2(a, b);
   f = e4m3x2_f(term[1]);
-  a -= f.x, b -= f.y;
-  term[2] = cvt_e5m2x2(a, b);
-  f = e5m2x2_f(term[2]);
-  a -= f.x, b -= f.y;
+  term[2] = cvt_e5m2x2(a - f.x, b - f.y);
+}
+// T e5m2 terms; a and b become what is left.
+template <int T>
+__device__ __forceinline__ void split_e5m2(float &a, float &b, uint32_t (&term)[T]) {
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    term[k] = cvt_e5m2x2(a, b);
+    const uint32_t h = __byte_perm(term[k], 0, 0x1404);  // an e5m2 number is the upper byte of the fp16 one
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    a -= f.x, b -= f.y;
+  }
 }
 
 __device__ __forceinline__ float warp_fmax(float v) {
@@ -102,9 +110,9 @@ __device__ __forceinline__ float warp_fmax(float v) {
   return r;
 }
 
-// A row's power of two: |x| 2^-e in [128, 256) for its largest |x|; and what undoes it.
-__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
-  const int e = (int)(amax_bits >> 23) - 127 - 7;
+// A row's power of two e: |x| 2^-e in [2^top, 2^(top + 1)) for its largest |x|.
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits, int top) {
+  const int e = (int)(amax_bits >> 23) - 127 - top;
   return max(e, -120);
 }
 

@@ -143,7 +143,7 @@ tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, i
   if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || max_len <= 0)
     return TQ_ERR_ARG;
   if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
-  *out = tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q, weights);
+  *out = tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q, max_len, weights);
   return TQ_OK;
 }
 

@@ -380,11 +380,11 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 #pragma unroll 4
       for (int k = 0; k < 16; ++k) {
         const int r = (warp & 7) * 16 + k, row = u.pair * kUnit + rt * 128 + r, i = row / G;
-        uint32_t w[1][3];
-        const int ex = row_terms<1>(a, u.b, u.h * G + row % G, i, row < R && i < m, lane, w);
+        uint32_t w[3];
+        const int ex = row_terms(a, u.b, u.h * G + row % G, i, row < R && i < m, lane, w);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
-          *reinterpret_cast<uint32_t *>(qbuf + (rt * TERMS + t) * kQTerm + q8_off(r, 4 * lane)) = w[0][t];
+          *reinterpret_cast<uint32_t *>(qbuf + (rt * TERMS + t) * kQTerm + q8_off(r, 4 * lane)) = w[t];
         if (lane == 0) sm.top[rt][0][r] = pow2i(ex);
       }
       fence_proxy_async_shared();

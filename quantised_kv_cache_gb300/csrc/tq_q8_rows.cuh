@@ -1,13 +1,9 @@
-// Query rows of the 8-bit cache's attention kernels that hold 16 rows per operand: their key ranges and
-// their 8-bit terms.
+// Query rows of the 8-bit cache's attention kernels: their key ranges and their 8-bit terms.
 #pragma once
 
 #include "tq_q8_attend.cuh"
 
 namespace tq {
-
-constexpr int kRows = 16;           // rows of an operand = N of the MMAs
-constexpr int kTerm = kRows * 128;  // bytes of one 8-bit term of a Q or P operand
 
 // A row's key range: query token i of sequence b, whose length is len and whose query tokens number m.
 __device__ __forceinline__ int2 row_range(const Q8AttnArgs &a, int b, int i, int len, int m) {
@@ -26,12 +22,11 @@ __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, 
   *m = min(max(q, 0), a.n_q);
 }
 
-// Row (head hq, query token i) of sequence b, a whole warp: coordinates 4 lane .. 4 lane + 3 scaled by the row's power of
-// two 2^-e and split into terms, four bytes each; returns e. A row with an infinity or a NaN becomes all NaN.
-template <int GR>
-__device__ __forceinline__ int row_terms(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane,
-                                         uint32_t (&w)[GR][3]) {
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+// Row (head hq, query token i) of sequence b, a whole warp: coordinates 4 lane .. 4 lane + 3 in x, 0 when not live;
+// returns the bits of the row's largest magnitude.
+__device__ __forceinline__ uint32_t row_load(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, float (&x)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = 0.f;
   if (live) {
     const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
     if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
@@ -41,29 +36,55 @@ __device__ __forceinline__ int row_terms(const Q8AttnArgs &a, int b, int hq, int
   uint32_t amax = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) amax = max(amax, __float_as_uint(x[k]) & 0x7fffffffu);
-  amax = __reduce_max_sync(kFull, amax);
-  const int e = row_exponent(amax);
-  if (amax >= 0x7f800000u) {
+  return __reduce_max_sync(kFull, amax);
+}
+
+// A row's terms, four bytes each, of its coordinates times 2^-e (e is returned). A row with an infinity or a NaN becomes
+// all NaN. Many rows: e4m3, e4m3, e5m2.
+__device__ __forceinline__ int row_terms(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[3]) {
+  float x[4];
+  const uint32_t amax = row_load(a, b, hq, i, live, lane, x);
+  const int e = row_exponent(amax, 7);
+  const float f = pow2i(-e);
+  uint32_t lo[3], hi[3];
+  split_terms(x[0] * f, x[1] * f, lo);
+  split_terms(x[2] * f, x[3] * f, hi);
 #pragma unroll
-    for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) w[gr][k] = 0x7f7f7f7fu;
-    return e;
-  }
+  for (int k = 0; k < 3; ++k) w[k] = amax >= 0x7f800000u ? 0x7f7f7f7fu : lo[k] | (hi[k] << 16);
+  return e;
+}
+// Few rows: T e5m2 terms.
+template <int T>
+__device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[T]) {
+  float x[4];
+  const uint32_t amax = row_load(a, b, hq, i, live, lane, x);
+  const int e = row_exponent(amax, 14);
   const float f = pow2i(-e);
 #pragma unroll
   for (int k = 0; k < 4; ++k) x[k] *= f;
+  uint32_t lo[T], hi[T];
+  split_e5m2<T>(x[0], x[1], lo);
+  split_e5m2<T>(x[2], x[3], hi);
 #pragma unroll
-  for (int gr = 0; gr < GR; ++gr) {
-    uint32_t lo[3], hi[3];
-    split_terms(x[0], x[1], lo);
-    split_terms(x[2], x[3], hi);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) w[gr][k] = lo[k] | (hi[k] << 16);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] *= kGroupScale;
-  }
+  for (int k = 0; k < T; ++k) w[k] = amax >= 0x7f800000u ? 0x7f7f7f7fu : lo[k] | (hi[k] << 16);
   return e;
+}
+
+// Few rows: term k of row r is operand row k NR + r. An accumulator's columns are summed over the terms, the small ones first.
+__host__ __device__ constexpr int stacked_rows(int NR, int T) { return T * NR < 16 ? 16 : T * NR; }
+template <int NR, int T>
+__device__ __forceinline__ void tmem_term_sums(uint32_t taddr, float (&out)[NR]) {
+  constexpr int C = NR * T < 32 ? NR * T : 32, kParts = NR * T / C;
+#pragma unroll
+  for (int part = kParts - 1; part >= 0; --part) {
+    float v[C];
+    tmem_ld_cols<C>(taddr + part * C, v);
+#pragma unroll
+    for (int k = C / NR - 1; k >= 0; --k)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        out[r] = part == kParts - 1 && k == C / NR - 1 ? v[k * NR + r] : out[r] + v[k * NR + r];
+  }
 }
 
 __device__ __forceinline__ void bar_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }

@@ -1,10 +1,13 @@
 // Accumulated attention weight of the 8-bit cache (tq_q8_attention with d_weights): per slot the sum,
-// over the group's heads and the sequence's query tokens, of p = 2^(t - lse), t and lse in log2.
+// over the group's heads and the sequence's query tokens, of p = 2^(t - lse), t and lse in log2. No atomics, one fixed
+// order of the sum.
 //
-// After the attention has left each row's lse, the scores are formed again from the keys alone: one CTA per 128
-// tokens of a (sequence, KV head), its key tile read once. Four warpgroups take every fourth tile of 16
-// query rows: queries as 8-bit terms, one score MMA chain, and because token = lane = thread, a
-// thread adds its own token's probabilities over all rows in one register -- no atomics, one fixed order.
+// q8_kept_kernel, few rows: the attention has kept its scores (4 bytes a row and token, beside the 256 of the cache that it reads);
+// a thread adds up 4 tokens' probabilities over the rows. Bound by those scores' bytes.
+// q8_weights_kernel, many rows: after the attention has left each row's lse, the scores are formed again from the keys alone: one CTA per 128
+// tokens of a (sequence, KV head), its key tile read once. Four warpgroups take every fourth tile of query
+// rows: queries as e5m2 terms, one score MMA chain, and because token = lane = thread, a
+// thread adds its own token's probabilities over all rows in one register.
 // Row tiles that see none of the tokens are skipped.
 
 #include "tq_q8_rows.cuh"
@@ -16,6 +19,10 @@ constexpr int kTile = 128;
 constexpr int kWg = 4;
 constexpr int kThreads = kWg * 128;
 
+constexpr int kRows = 16;                                 // rows at most
+constexpr int rows_of(int T) { return T == 8 ? 8 : 16; }  // rows of a tile: 64 operand rows of terms
+constexpr int kN = 64, kOp = kN * 128;
+
 struct Shared {
   uint64_t full, bar_s[kWg];
   float qscale[kWg][kRows], slope[kWg][kRows], lse[kWg][kRows];
@@ -26,8 +33,10 @@ struct Shared {
   int bad;
 };
 
-template <int GR>
+template <int T>
 __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_constant__ Q8AttnArgs a) {
+  constexpr int NR = rows_of(T);
+  static_assert(stacked_rows(NR, T) == kN, "");
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
@@ -41,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
       a.weights[at + tid] = a.weights_in ? a.weights_in[at + tid] : 0.f;
     return;
   }
-  uint8_t *ktile = dyn, *qbuf = dyn + kTile * kD + wg * GR * 3 * kTerm;
+  uint8_t *ktile = dyn, *qbuf = dyn + kTile * kD + wg * kOp;
   if (tid == 0) {
     mbar_init(&sm.full, 1);
     for (int w = 0; w < kWg; ++w) mbar_init(&sm.bar_s[w], 1);
@@ -49,13 +58,13 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     sm.bad = 0;
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(&sm.tmem), kWg * 16 * GR);
+    tmem_alloc(smem_u32(&sm.tmem), kWg * kN);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t t_s = sm.tmem + wg * 16 * GR, lanes = (uint32_t)(32 * w4) << 16;
+  const uint32_t t_s = sm.tmem + wg * kN, lanes = (uint32_t)(32 * w4) << 16;
   // the keys of the tile's two blocks; a block that is not mapped stays unread and unseen
   float ks = -1.f;
   if (wt < n) {
@@ -83,26 +92,23 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
   const bool issue = elect_lane();  // of the warpgroup's first warp
   const uint32_t u_s = warp_uniform(t_s), u_k = smem_u32(ktile), u_q = warp_uniform(smem_u32(qbuf));
-  const int R = a.group * a.n_q, rts = (R + kRows - 1) / kRows;
+  const int R = a.group * a.n_q, rts = (R + NR - 1) / NR;
   float sum = 0.f;
   uint32_t phase = 0;
   for (int rt = wg; rt < rts; rt += kWg) {
     // ---- the ranges first: does any row of the tile see a token here?
     int2 rg = make_int2(0, 0);
-    const int mine = rt * kRows + (wt & (kRows - 1)), mi = mine / a.group;
+    const int mine = rt * NR + (wt & (NR - 1)), mi = mine / a.group;
     if (mine < R) rg = row_range(a, b, mi, len, m);
     if (!__any_sync(kFull, rg.x < tok0 + n && rg.y > tok0)) continue;  // the same for the four warps
-    if (wt < kRows) sm.range[wg][wt] = rg;
-    for (int k = 0; k < kRows / 4; ++k) {
-      const int r = w4 * (kRows / 4) + k, row = rt * kRows + r, i = row / a.group, hq = h * a.group + row % a.group;
+    if (wt < NR) sm.range[wg][wt] = rg;
+    for (int k = 0; k < NR / 4; ++k) {
+      const int r = w4 * (NR / 4) + k, row = rt * NR + r, i = row / a.group, hq = h * a.group + row % a.group;
       const bool live = row < R && i < m;
-      uint32_t w[GR][3];
-      const int ex = row_terms<GR>(a, b, hq, i, live, lane, w);
+      uint32_t w[T];
+      const int ex = row_e5m2<T>(a, b, hq, i, live, lane, w);
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-          *reinterpret_cast<uint32_t *>(qbuf + (gr * 3 + t) * kTerm + q8_off(r, 4 * lane)) = w[gr][t];
+      for (int t = 0; t < T; ++t) *reinterpret_cast<uint32_t *>(qbuf + q8_off(t * NR + r, 4 * lane)) = w[t];
       if (lane == 0) {
         sm.qscale[wg][r] = pow2i(ex);
         sm.slope[wg][r] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
@@ -116,15 +122,10 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     if (w4 == 0) {
       tc_fence_after_sync();
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-          for (int s = 0; s < kD / 32; ++s)
-            if (issue)
-              tc_mma_f8(u_s + 16 * gr, tc_sdesc_kmajor(u_k + 256 * s, 128, 1024),
-                        tc_sdesc_kmajor(u_q + (gr * 3 + k) * kTerm + 256 * s, 128, 1024),
-                        tc_idesc_f8(128, kRows, 0, k == 2, 0, 0), k > 0 || s > 0);
+      for (int s = 0; s < kD / 32; ++s)
+        if (issue)
+          tc_mma_f8(u_s, tc_sdesc_kmajor(u_k + 256 * s, 128, 1024), tc_sdesc_kmajor(u_q + 256 * s, 128, 1024),
+                    tc_idesc_f8(128, kN, 0, 1, 0, 0), s > 0);
       if (issue) tc_commit(smem_u32(&sm.bar_s[wg]));
       __syncwarp();
     }
@@ -132,17 +133,11 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     __syncwarp();
     ++phase;
     tc_fence_after_sync();
-    float t[kRows];
-    tmem_ld_cols<kRows>(t_s + lanes, t);
-    if constexpr (GR == 2) {
-      float t2[kRows];
-      tmem_ld_cols<kRows>(t_s + 16 + lanes, t2);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) t[r] = fmaf(t2[r], 1.f / kGroupScale, t[r]);
-    }
+    float t[NR];
+    tmem_term_sums<NR, T>(t_s + lanes, t);
     tc_fence_before_sync();
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < NR; ++r) {
       const int2 see = sm.range[wg][r];
       if (slot < see.x || slot >= see.y || ks < 0.f) continue;
       float x = q8_score_log2(t[r] * (sm.qscale[wg][r] * ks), sc);
@@ -159,26 +154,68 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     const float w = (sm.sum[0][wt] + sm.sum[1][wt]) + (sm.sum[2][wt] + sm.sum[3][wt]);
     a.weights[at + wt] = (a.weights_in ? a.weights_in[at + wt] : 0.f) + (wt < n ? w : 0.f);
   }
-  if (warp == 0) tmem_dealloc(sm.tmem, kWg * 16 * GR);
+  if (warp == 0) tmem_dealloc(sm.tmem, kWg * kN);
 }
 
-template <int GR>
-int launch(const Q8AttnArgs &a, cudaStream_t st) {
-  constexpr int smem = kTile * kD + kWg * GR * 3 * kTerm;
-  if (cudaFuncSetAttribute(q8_weights_kernel<GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+constexpr int kKept = 128;  // threads of 4 tokens each
+
+__global__ void __launch_bounds__(kKept) q8_kept_kernel(const __grid_constant__ Q8AttnArgs a) {
+  __shared__ float lse[64];
+  __shared__ int2 range[64];
+  const int slot = (blockIdx.x * kKept + threadIdx.x) * 4, h = blockIdx.y, b = blockIdx.z, R = a.group * a.n_q;
+  int len, m;
+  seq_sizes(a, b, &len, &m, false);
+  const long long bh = (long long)b * a.heads_kv + h;
+  if ((int)threadIdx.x < R) {  // R is at most 64
+    const int i = threadIdx.x / a.group, hq = h * a.group + threadIdx.x % a.group;
+    range[threadIdx.x] = row_range(a, b, i, len, m);
+    lse[threadIdx.x] = i < m ? a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] * kLog2e : 0.f;
+  }
+  __syncthreads();
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  if (slot < len) {
+    const float *t = a.scores + bh * R * a.scores_ld + slot;
+#pragma unroll 4
+    for (int r = 0; r < R; ++r) {
+      const int2 see = range[r];
+      if (slot + 4 <= see.x || slot >= see.y) continue;
+      const float4 x = *reinterpret_cast<const float4 *>(t + r * a.scores_ld);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (slot + k >= see.x && slot + k < see.y && v[k] != -INFINITY) sum[k] += ex2_approx(v[k] - lse[r]);
+    }
+  }
+  const long long at = bh * a.c.capacity + slot;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (slot + k < a.c.capacity && (slot + k < len || a.weights != a.weights_in))
+      a.weights[at + k] = (a.weights_in ? a.weights_in[at + k] : 0.f) + sum[k];
+}
+
+template <int T>
+int launch(const Q8AttnArgs &a, int slots, cudaStream_t st) {
+  constexpr int smem = kTile * kD + kWg * kOp;
+  if (cudaFuncSetAttribute(q8_weights_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  // in place only the tokens in use are touched
-  const int slots = a.weights == a.weights_in ? a.max_len : a.c.capacity;
-  if (a.heads_kv > 65535 || a.batch > 65535) return TQ_ERR_UNSUPPORTED;
-  q8_weights_kernel<GR><<<dim3((unsigned)((slots + kTile - 1) / kTile), (unsigned)a.heads_kv, (unsigned)a.batch), kThreads,
-                          smem, st>>>(a);
+  q8_weights_kernel<T><<<dim3((unsigned)((slots + kTile - 1) / kTile), (unsigned)a.heads_kv, (unsigned)a.batch), kThreads,
+                         smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_q8_weights(const Q8AttnArgs &a, void *stream) {
-  return a.out_dtype == TQ_F32 ? launch<2>(a, (cudaStream_t)stream) : launch<1>(a, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  // in place only the tokens in use are touched
+  const int slots = a.weights == a.weights_in ? a.max_len : a.c.capacity;
+  if (a.heads_kv > 65535 || a.batch > 65535) return TQ_ERR_UNSUPPORTED;
+  if (a.scores) {
+    q8_kept_kernel<<<dim3((unsigned)((slots + 4LL * kKept - 1) / (4 * kKept)), (unsigned)a.heads_kv, (unsigned)a.batch), kKept, 0,
+                     st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  }
+  return a.out_dtype == TQ_F32 ? launch<8>(a, slots, st) : launch<4>(a, slots, st);
 }
 
 }  // namespace tq
