@@ -165,6 +165,31 @@ __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&v)[4
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
+// 16 columns of this thread's lane on their way to v, and the wait for them (and any others): v may be used after it. A
+// loop loads the next 16 after waiting for these, so that they arrive while these are worked on.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two e4m3 (e5m2) bytes of an fp16 pair, and back
@@ -438,17 +463,24 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
           float top1 = -INFINITY;
+          uint32_t w[2][16];
+          tmem_ld_start(t_s, w[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            tmem_ld_done(w[q & 1]);
+            if (q < 3) tmem_ld_start(t_s + 16 * (q + 1), w[(q + 1) & 1]);
             float x[16];
-            tmem_ld_cols<16>(t_s + 16 * q, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = score(__uint_as_float(w[q & 1][i]), 16 * q + i, mask);
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-              top = fmaxf(top, fmaxf(score(x[i], 16 * q + i, mask), score(x[i + 1], 16 * q + i + 1, mask)));
-              top1 = fmaxf(top1, fmaxf(score(x[i + 2], 16 * q + i + 2, mask), score(x[i + 3], 16 * q + i + 3, mask)));
+              top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+              top1 = fmaxf(top1, fmaxf(x[i + 2], x[i + 3]));
             }
+            if constexpr (EXTRA) tmem_st_x16(t_s + 16 * q, x);  // capped, biased and masked once
           }
           top = fmaxf(top, top1);
+          if constexpr (EXTRA) tmem_st_wait();
         };
         if (masked) maximum(std::true_type{});
         else maximum(std::false_type{});
@@ -469,30 +501,33 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         // ---- probabilities times 2^8, their terms over the scores they come from, their sum
         float2 sum = make_float2(0.f, 0.f);
         auto probabilities = [&](auto mask) {
-          uint32_t held[4];
+          uint32_t held[4], v[2][16];
+          tmem_ld_start(t_s, v[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float x[16];
-            tmem_ld_cols<16>(t_s + 16 * q, x);
+            uint32_t(&x)[16] = v[q & 1];
+            tmem_ld_done(x);
+            if (q < 3) tmem_ld_start(t_s + 16 * (q + 1), v[(q + 1) & 1]);
             uint32_t w[TERMS][4];
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
               uint32_t t[TERMS][2];
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                const int k = i + 2 * v;
-                const float y0 = score(x[k], 16 * q + k, mask), y1 = score(x[k + 1], 16 * q + k + 1, mask);
+              for (int u = 0; u < 2; ++u) {
+                const int k = i + 2 * u;
+                float y0 = __uint_as_float(x[k]), y1 = __uint_as_float(x[k + 1]);
+                if constexpr (!EXTRA) y0 = score(y0, 16 * q + k, mask), y1 = score(y1, 16 * q + k + 1, mask);
                 const float p0 = ex2_approx(EXTRA ? y0 + shift : fmaf(y0, c, shift));
                 const float p1 = ex2_approx(EXTRA ? y1 + shift : fmaf(y1, c, shift));
                 sum.x += p0, sum.y += p1;
                 const __half2 hp = __floats2half2_rn(p0, p1);
                 uint32_t left = *reinterpret_cast<const uint32_t *>(&hp);
-                t[0][v] = h2_e4m3(left);
-                left = h2_sub(left, e4m3_h2(t[0][v]));
-                t[1][v] = h2_e4m3(left);
+                t[0][u] = h2_e4m3(left);
+                left = h2_sub(left, e4m3_h2(t[0][u]));
+                t[1][u] = h2_e4m3(left);
                 if constexpr (TERMS == 3) {
-                  left = h2_sub(left, e4m3_h2(t[1][v]));
-                  t[2][v] = h2_e5m2(left);
+                  left = h2_sub(left, e4m3_h2(t[1][u]));
+                  t[2][u] = h2_e5m2(left);
                 }
               }
 #pragma unroll
@@ -538,12 +573,14 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             for (int i = 0; i < 64; ++i) o[i] *= by;
           }
           if (vs < 0.f) return;
+          uint32_t d[2][16];
+          tmem_ld_start(t_o, d[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float d[16];
-            tmem_ld_cols<16>(t_o + 16 * q, d);
+            tmem_ld_done(d[q & 1]);
+            if (q < 3) tmem_ld_start(t_o + 16 * (q + 1), d[(q + 1) & 1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[16 * q + i] = fmaf(d[i], vs, o[16 * q + i]);
+            for (int i = 0; i < 16; ++i) o[16 * q + i] = fmaf(__uint_as_float(d[q & 1][i]), vs, o[16 * q + i]);
           }
         };
         for (int part = 0; part <= (int)apart; ++part) {
