@@ -339,22 +339,33 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             if (j > 0) {
               const int s = (it + j - 1) % kStages, n = min(kTile, max(0, hi - (first + j - 1) * kTile));
               const float4 f = sm.info[s];
-              const bool apart = scales_apart(f);
+              const bool apart = scales_apart(f), whole = n == kTile && f.z >= 0.f && f.w >= 0.f && !apart;
               const uint32_t vt = warp_uniform(smem_u32(ring + s * kStage) + kTile * kD);
               for (int part = 0; part <= (int)apart; ++part) {  // the two blocks at once, or one after the other
                 wait(&sm.bar_p[rt], probs & 1);
                 ++probs;
                 tc_fence_after_sync();
-                bool more = false;
+                if (whole) {  // nothing to decide between the MMAs
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t)
+                  for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if (k * 32 >= n || (k < 2 ? f.z : f.w) < 0.f || (apart && k / 2 != part)) continue;
-                    if (issue) tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
-                                 tc_idesc_f8(128, 128, t == 2, 0, 0, 1), more);
-                    more = true;
-                  }
+                    for (int k = 0; k < 4; ++k)
+                      if (issue)
+                        tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
+                                     tc_idesc_f8(128, 128, t == 2, 0, 0, 1), t > 0 || k > 0);
+                } else {
+                  bool more = false;
+#pragma unroll
+                  for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      if (k * 32 >= n || (k < 2 ? f.z : f.w) < 0.f || (apart && k / 2 != part)) continue;
+                      if (issue)
+                        tc_mma_f8_ts(t_o, t_s + 32 * k + 8 * t, tc_sdesc_kmajor(vt + 4096 * k, 1024, 128),
+                                     tc_idesc_f8(128, 128, t == 2, 0, 0, 1), more);
+                      more = true;
+                    }
+                }
                 if (issue && part == (int)apart) tc_commit(smem_u32(&sm.empty[s]));
                 if (issue) tc_commit(smem_u32(&sm.bar_o[rt]));
                 __syncwarp();
@@ -463,24 +474,37 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
           float top1 = -INFINITY;
-          uint32_t w[2][16];
-          tmem_ld_start(t_s, w[0]);
+          if constexpr (EXTRA) {  // capped, biased and masked once, here; long code, not unrolled four times
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              float x[16];
+              tmem_ld_cols<16>(t_s + 16 * q, x);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_done(w[q & 1]);
-            if (q < 3) tmem_ld_start(t_s + 16 * (q + 1), w[(q + 1) & 1]);
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = score(__uint_as_float(w[q & 1][i]), 16 * q + i, mask);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-              top1 = fmaxf(top1, fmaxf(x[i + 2], x[i + 3]));
+              for (int i = 0; i < 16; ++i) {
+                x[i] = score(x[i], 16 * q + i, mask);
+                top = fmaxf(top, x[i]);
+              }
+              tmem_st_x16(t_s + 16 * q, x);
             }
-            if constexpr (EXTRA) tmem_st_x16(t_s + 16 * q, x);  // capped, biased and masked once
+            tmem_st_wait();
+          } else {
+            uint32_t w[2][16];
+            tmem_ld_start(t_s, w[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld_done(w[q & 1]);
+              if (q < 3) tmem_ld_start(t_s + 16 * (q + 1), w[(q + 1) & 1]);
+              float x[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = score(__uint_as_float(w[q & 1][i]), 16 * q + i, mask);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                top1 = fmaxf(top1, fmaxf(x[i + 2], x[i + 3]));
+              }
+            }
+            top = fmaxf(top, top1);
           }
-          top = fmaxf(top, top1);
-          if constexpr (EXTRA) tmem_st_wait();
         };
         if (masked) maximum(std::true_type{});
         else maximum(std::false_type{});
