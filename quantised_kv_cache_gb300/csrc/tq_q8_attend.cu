@@ -446,6 +446,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     }
     if (tid == 0 && g0 >= g1) cuts[blockIdx.x] = Cut{0, 0, 0, 0};
   }
+  if (*(volatile int *)&sm.bad) settle();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

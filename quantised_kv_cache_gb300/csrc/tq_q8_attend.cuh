@@ -51,8 +51,14 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// N consecutive columns of this thread's lane, without the wait (tmem_ld_wait follows, then use)
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// After a wait that ran out: time for the tensor-core operations in flight to end (they take microseconds) before tensor
+// memory is given back.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < 2000000ull) __nanosleep(10000);
+}
+
+// N consecutive columns of this thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&f)[N]) {
   uint32_t v[N];

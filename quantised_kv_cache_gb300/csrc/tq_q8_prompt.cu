@@ -659,6 +659,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
     }
     if (tid == 0 && idle) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0};
   }
+  if (*(volatile int *)&sm.bad) settle();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

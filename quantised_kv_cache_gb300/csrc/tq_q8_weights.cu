@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
     bar_wg(wg);  // the rows' arrays and terms are free again
   }
   sm.sum[wg][wt] = sum;
+  if (*(volatile int *)&sm.bad) settle();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

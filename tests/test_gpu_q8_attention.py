@@ -67,12 +67,12 @@ def check(got, q, k, v, lens, new, *, dtype, out_dtype, begin=None, end=None, sc
           k_pos=None, lse=None, weights=None, before=None, rows=None):
     """Every element within the bound. Per query: the products' sums are off by at most 130 U of the sum of their magnitudes (fp32,
     any order, three scalings). A query enters as 8-bit terms with its row's largest coordinate in [128, 256): 16-bit
-    coordinates of at least 2^-9 of the largest exactly, smaller ones within 2^-20 of it (three terms end at 2^-13; two, for many
-    rows in bf16, at 2^-10: 2^-17), float32 ones within 2^-22 of themselves and 2^-31 of the largest (six terms).
+    coordinates of at least 2^-9 of the largest exactly, smaller ones within 2^-20 of it (for many rows three terms end at 2^-13, two, in
+    bf16, at 2^-10: 2^-17; for few rows all terms are e5m2 and end far below), float32 ones within 2^-22 of themselves and 2^-31 of the largest (8 terms).
     Capping, bias and the exponent add a few U of what they handle (a cap by the short tanh of many rows 2^-21 of the cap); a probability's relative error is twice the
     largest score error (its own and the sum's) and 2^-20 for the two exponentials. Probabilities enter the value sums as terms of
-    their 2^8-fold: 2^-11 of each and 2^-21 of the largest (three terms), 2^-8 and 2^-18 (two, many rows in bf16), 2^-22 and 2^-32
-    (six), never more than itself; many rows fold value scales up to 2^4 apart into them, which brings the second nearer by 2^4.
+    their 2^8-fold: 2^-11 of each and 2^-21 of the largest (three terms; four e5m2 ones do better), 2^-8 and 2^-18 (two, many rows in bf16), 2^-22 and 2^-32
+    (8), never more than itself; many rows fold value scales up to 2^4 apart into them, which brings the second nearer by 2^4.
     Sums over tiles of 128 add U each; the result is rounded to its type."""
     B, Hq, n, _ = q.shape
     H = k.shape[1]
@@ -490,6 +490,47 @@ def test_two_streams_and_replayed_graphs(ctx):
         pos += 1
     for name in twin.tensors:
         assert torch.equal(twin.tensors[name], caches[0].tensors[name])
+
+
+@pytest.mark.parametrize("B,Hq,H,n,lens,dtype", [
+    (600, 2, 1, 1, [1 + (37 * i) % 200 for i in range(600)], BF),   # more sequences than one launch takes
+    (3, 2, 1, 2100, [2100, 2101, 2200], F32)])                      # more row tiles than one launch takes
+def test_more_units_than_one_launch_takes(ctx, B, Hq, H, n, lens, dtype):
+    cap = max(lens)
+    cache, k, v = make(ctx, B, H, cap, lens, seed=1)
+    q = queries(5, B, Hq, n, dtype)
+    w = torch.zeros(B, H, cap, device=DEV)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, weights=w)
+    if n > 1:  # the last rows
+        m = 40
+        check(np64(got[:, :, -m:]), np64(q[:, :, -m:]), k, v, lens, [m] * B, dtype=dtype, out_dtype=dtype)
+        assert abs(float(w.sum()) / (B * Hq * n) - 1) < 1e-4
+    else:
+        check(np64(got), np64(q), k, v, lens, [1] * B, dtype=dtype, out_dtype=dtype, weights=np64(w))
+
+
+def test_no_query_tokens_at_all(ctx):
+    cache, _, _ = make(ctx, 2, 2, 128, [100, 5], seed=1)
+    for n in (1, 3, 100):
+        q = queries(5, 2, 4, n, BF)
+        out, w = torch.full_like(q, 5.0), torch.ones(2, 2, 128, device=DEV)
+        tq.tq_q8_attention(ctx.handle, cache, q, ints([100, 5]), 128, new_lens=ints([0, 0]), out=out, weights_in=w, weights=w)
+        assert bool((out == 5).all()) and bool((w == 1).all())
+
+
+def test_weights_of_more_scores_than_are_kept(ctx):
+    """64 rows over a million slots: the scores are formed again."""
+    N, cap, m = 1_049_000, 1_050_000, 200
+    cache = tq.Cache(ctx, 1, 1, cap, device=DEV)
+    k, v = queries(1, 1, 1, m, BF), queries(2, 1, 1, m, BF)
+    tq.tq_q8_append(ctx.handle, cache, k, v, ints([N - m]))
+    q = queries(3, 1, 16, 4, BF)
+    begin, end = ints([[N - m] * 4]), ints([[N - 3 + i for i in range(4)]])
+    w = torch.zeros(1, 1, cap, device=DEV)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints([N]), cap, key_begin=begin, key_end=end, weights=w)
+    kv, vv = (np64(t) for t in tq.tq_dequantize(ctx.handle, cache, N - m, N))
+    check(np64(got), np64(q), kv, vv, [m], [4], dtype=BF, out_dtype=BF, weights=np64(w[..., N - m:N]))
+    assert not bool(w[..., :N - m].any()) and not bool(w[..., N:].any())
 
 
 @pytest.mark.parametrize("B,Hq,H,n,N", [(8, 32, 32, 1, 4096), (2, 32, 8, 1, 20000), (1, 16, 8, 300, 5000)])
