@@ -127,22 +127,27 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[N]) {
 
 // cos and sin of 2 pi (pos * freq mod 1), freq in units of 2^-64 turns: the 64-bit product wraps at
 // whole turns, so the angle is exact to 2^-32 turns at any position. The top 2 bits (rounded) are the
-// quadrant; the rest, |x| <= pi / 4, goes through the Taylor polynomials of sine (to x^9, the next
-// term is below 2e-9) and cosine (to x^10, below 2e-10).
+// quadrant; the rest, |x| <= pi / 4, is kept in two parts (x + lo: the integer and 2 pi / 2^32 each split where
+// float32 ends) and goes through the Taylor polynomials of sine (to x^9, the next
+// term is below 2e-9) and cosine (to x^10, below 2e-10), so that little more than the last rounding is lost.
 __device__ __forceinline__ void rope_sincos(int pos, unsigned long long freq, float *c, float *s) {
   const uint32_t u = (uint32_t)(((unsigned long long)(long long)pos * freq) >> 32);
   const uint32_t q = (u + 0x20000000u) >> 30;
-  const float x = (float)(int)(u - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const int r = (int)(u - (q << 30));
+  const float kUnit = 1.46291811e-9f, kUnitLo = -4.07094027e-17f;  // 2 pi / 2^32 and what float32 drops of it
+  const float rh = (float)(r & ~63), rl = (float)(r & 63);
+  const float x = __fmul_rn(rh, kUnit);
+  const float lo = fmaf(rh, kUnit, -x) + fmaf(rl, kUnit, rh * kUnitLo);
   const float z = x * x;
   float sn = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
   sn = fmaf(z, sn, 8.3333333e-3f);
   sn = fmaf(z, sn, -1.6666667e-1f);
-  sn = fmaf(x * z, sn, x);
+  sn = fmaf(x * z, sn, lo) + x;
   float cs = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
   cs = fmaf(z, cs, -1.3888889e-3f);
   cs = fmaf(z, cs, 4.1666667e-2f);
   cs = fmaf(z, cs, -0.5f);
-  cs = fmaf(z, cs, 1.f);
+  cs = fmaf(z, cs, -x * lo) + 1.f;
   const bool swap = q & 1;
   const float a = swap ? cs : sn, b = swap ? sn : cs;
   *s = (q & 2) ? -a : a;
