@@ -413,15 +413,37 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 
       // ---- queries: a warp prepares 16 rows of its row tile (whose score MMAs of the unit before are done)
       bar_rt(rt);
-#pragma unroll 4
-      for (int k = 0; k < 16; ++k) {
-        const int r = (warp & 7) * 16 + k, row = u.pair * kUnit + rt * 128 + r, i = row / G;
-        uint32_t w[3];
-        const int ex = row_terms(a, u.b, u.h * G + row % G, i, row < R && i < m, lane, w);
+#pragma unroll 1
+      for (int k0 = 0; k0 < 16; k0 += 8) {
+        // eight rows' loads in flight: no branch in their way, a row that is not there loads another and counts as 0
+        uint2 raw[8];
+        const int first_row = u.pair * kUnit + rt * 128 + (warp & 7) * 16 + k0;
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
-          *reinterpret_cast<uint32_t *>(qbuf + (rt * TERMS + t) * kQTerm + q8_off(r, 4 * lane)) = w[t];
-        if (lane == 0) sm.top[rt][0][r] = pow2i(ex);
+        for (int k = 0; k < 8; ++k) {
+          const int row = min(first_row + k, R - 1), i = row / G;
+          const long long off = u.b * a.qs.b + (u.h * G + row - i * G) * a.qs.h + min(i, m - 1) * a.qs.t + 4 * lane;
+          raw[k] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = (warp & 7) * 16 + k0 + k, row = first_row + k;
+          float x[4];
+          if (a.q_dtype == TQ_BF16) {
+            x[0] = __uint_as_float(raw[k].x << 16), x[1] = __uint_as_float(raw[k].x & 0xffff0000u);
+            x[2] = __uint_as_float(raw[k].y << 16), x[3] = __uint_as_float(raw[k].y & 0xffff0000u);
+          } else {
+            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&raw[k].x));
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&raw[k].y));
+            x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+          }
+          if (row >= R || row / G >= m) x[0] = x[1] = x[2] = x[3] = 0.f;
+          uint32_t w[3];
+          const int ex = row_terms(x, w);
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t)
+            *reinterpret_cast<uint32_t *>(qbuf + (rt * TERMS + t) * kQTerm + q8_off(r, 4 * lane)) = w[t];
+          if (lane == 0) sm.top[rt][0][r] = pow2i(ex);
+        }
       }
       fence_proxy_async_shared();
       __syncwarp();

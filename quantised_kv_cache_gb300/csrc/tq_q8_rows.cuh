@@ -22,28 +22,18 @@ __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, 
   *m = min(max(q, 0), a.n_q);
 }
 
-// Row (head hq, query token i) of sequence b, a whole warp: coordinates 4 lane .. 4 lane + 3 in x, 0 when not live;
-// returns the bits of the row's largest magnitude.
-__device__ __forceinline__ uint32_t row_load(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, float (&x)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = 0.f;
-  if (live) {
-    const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
-    if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
-    else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
-    else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
-  }
+// The bits of a row's largest magnitude, a lane holding four of its coordinates.
+__device__ __forceinline__ uint32_t row_top(const float (&x)[4]) {
   uint32_t amax = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) amax = max(amax, __float_as_uint(x[k]) & 0x7fffffffu);
   return __reduce_max_sync(kFull, amax);
 }
 
-// A row's terms, four bytes each, of its coordinates times 2^-e (e is returned). A row with an infinity or a NaN becomes
-// all NaN. Many rows: e4m3, e4m3, e5m2.
-__device__ __forceinline__ int row_terms(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[3]) {
-  float x[4];
-  const uint32_t amax = row_load(a, b, hq, i, live, lane, x);
+// A row's terms, four bytes each, of its coordinates times 2^-e (e is returned); a whole warp. A row with an infinity or a
+// NaN becomes all NaN. Many rows: e4m3, e4m3, e5m2.
+__device__ __forceinline__ int row_terms(const float (&x)[4], uint32_t (&w)[3]) {
+  const uint32_t amax = row_top(x);
   const int e = row_exponent(amax, 7);
   const float f = pow2i(-e);
   uint32_t lo[3], hi[3];
@@ -56,8 +46,14 @@ __device__ __forceinline__ int row_terms(const Q8AttnArgs &a, int b, int hq, int
 // Few rows: T e5m2 terms.
 template <int T>
 __device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[T]) {
-  float x[4];
-  const uint32_t amax = row_load(a, b, hq, i, live, lane, x);
+  float x[4] = {0.f, 0.f, 0.f, 0.f};  // coordinates 4 lane .. 4 lane + 3 of row (head hq, query token i) of sequence b
+  if (live) {
+    const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
+    if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
+    else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
+    else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
+  }
+  const uint32_t amax = row_top(x);
   const int e = row_exponent(amax, 14);
   const float f = pow2i(-e);
 #pragma unroll
