@@ -31,7 +31,7 @@ constexpr int kThreads = kSoft + 128;   // warps 16 and 17 issue a row tile's MM
 constexpr int kRegsSoft = 112, kRegsControl = 32;  // 512 * 112 + 128 * 32 = 640 * 96, what the block is launched with
 constexpr int kStage = 2 * kTile * kD;
 constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
-constexpr int kPartRow = kD + 4;       // O, m, l, 2 pad
+constexpr int kPart = kUnit * (kD + 2);  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
 
 constexpr int stages_of(int terms) { return terms == 2 ? 4 : 3; }
@@ -49,7 +49,7 @@ struct Plan {
   int *pre;       // [entries + 1] tiles (of one head) before each entry
   Entry *entry;   // [entries]
   Cut *cuts;      // [CTAs]
-  float *parts;   // [CTAs][2][kUnit][kPartRow]
+  float *parts;   // [CTAs][2][kPart]
   int entries, pairs;
 };
 
@@ -661,11 +661,12 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           }
           if (a.lse && !half) a.lse[((long long)u.b * a.heads_q + hq) * a.n_q + qi] = (mx + log2f(l) - 8.f) * kLn2;
         } else {
-          float *part = p.parts + (((long long)blockIdx.x * 2 + (u.t0 == 0 ? 1 : 0)) * kUnit + rt * 128 + lrow) * kPartRow;
+          float *part = p.parts + ((long long)blockIdx.x * 2 + (u.t0 == 0 ? 1 : 0)) * kPart;
+          const int r = rt * 128 + lrow;
 #pragma unroll
           for (int q = 0; q < 16; ++q)
-            reinterpret_cast<float4 *>(part + 64 * half)[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          if (!half) part[kD] = mx, part[kD + 1] = l;
+            reinterpret_cast<float4 *>(part)[(16 * half + q) * kUnit + r] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          if (!half) part[kUnit * kD + r] = mx, part[kUnit * (kD + 1) + r] = l;
         }
       }
       if (tid == 0 && u.end == g1) {
@@ -688,38 +689,35 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   if (warp == kSoft / 32 + 2) tmem_dealloc(tmem, 512);
 }
 
-// The rows of a unit that was cut: one warp per row, lane = 4 coordinates.
-__global__ void __launch_bounds__(256) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
+// The rows of a unit that was cut: lane = row, a warp per 4 coordinates; 32 rows a CTA.
+__global__ void __launch_bounds__(1024) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts < 2) return;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), row = cut.pair * kUnit + r, G = a.group;
+  const int col = threadIdx.x >> 5, r = blockIdx.y * 32 + (threadIdx.x & 31), row = cut.pair * kUnit + r, G = a.group;
   int len, m;
   seq_sizes(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (row >= G * a.n_q || i >= m) return;
-  auto rec = [&](int k) {
-    return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kUnit * kPartRow + (long long)r * kPartRow;
-  };
+  auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kPart; };
   float top = -INFINITY;
-  for (int k = lane; k < cut.parts; k += 32) top = fmaxf(top, rec(k)[kD]);
-  top = warp_max(top);
+  for (int k = 0; k < cut.parts; ++k) top = fmaxf(top, rec(k)[kUnit * kD + r]);
   float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
 #pragma unroll 4
   for (int k = 0; k < cut.parts; ++k) {
     const float *x = rec(k);
-    const float f = x[kD] == -INFINITY ? 1.f : ex2_approx(x[kD] - top);  // without a maximum: zeros (or NaN)
-    const float4 y = reinterpret_cast<const float4 *>(x)[lane];
+    const float mk = x[kUnit * kD + r], f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
+    const float4 y = reinterpret_cast<const float4 *>(x)[col * kUnit + r];
     o[0] = fmaf(y.x, f, o[0]), o[1] = fmaf(y.y, f, o[1]), o[2] = fmaf(y.z, f, o[2]), o[3] = fmaf(y.w, f, o[3]);
-    l = fmaf(x[kD + 1], f, l);
+    l = fmaf(x[kUnit * (kD + 1) + r], f, l);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int k = 0; k < 4; ++k) o[k] *= inv;
   const int hq = cut.h * G + row % G;
-  const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + 4 * lane;
+  const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + 4 * col;
   if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(a.out) + off, o);
   else store_vec<__half, 4>(static_cast<__half *>(a.out) + off, o);
-  if (a.lse && lane == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
+  if (a.lse && col == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
 }
 
 template <int TERMS, bool EXTRA>
@@ -730,7 +728,7 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   q8_entries_kernel<<<(p.entries + 7) / 8, 256, 0, st>>>(a, p);
   q8_prefix_kernel<<<1, 1024, 0, st>>>(p);
   q8_prompt_kernel<TERMS, EXTRA><<<num_sms, kThreads, smem, st>>>(a, p);
-  q8_prompt_join_kernel<<<dim3(num_sms, kUnit / 8), 256, 0, st>>>(a, p);
+  q8_prompt_join_kernel<<<dim3(num_sms, kUnit / 32), 1024, 0, st>>>(a, p);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -740,8 +738,8 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q) {
   const size_t pairs = ((size_t)group * n_q + kUnit - 1) / kUnit, entries = pairs * batch;
-  return round16((entries + 1) * sizeof(int)) + entries * sizeof(Entry) + (size_t)num_sms * sizeof(Cut) +
-         (size_t)num_sms * 2 * kUnit * kPartRow * sizeof(float);
+  return round16((entries + 1) * sizeof(int)) + entries * sizeof(Entry) + round16((size_t)num_sms * sizeof(Cut)) +
+         (size_t)num_sms * 2 * kPart * sizeof(float);
 }
 
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream) {
@@ -752,7 +750,7 @@ int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *st
   char *w = (char *)workspace;
   p.pre = (int *)w, w += round16((size_t)(entries + 1) * sizeof(int));
   p.entry = (Entry *)w, w += (size_t)entries * sizeof(Entry);
-  p.cuts = (Cut *)w, w += (size_t)num_sms * sizeof(Cut);
+  p.cuts = (Cut *)w, w += round16((size_t)num_sms * sizeof(Cut));
   p.parts = (float *)w;
   cudaStream_t st = (cudaStream_t)stream;
   const bool extra = a.softcap != 0.f || a.slopes != nullptr || !(a.scale > 0.f);
