@@ -87,6 +87,7 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   const int h1 = min(a.heads, h0 + hpc);
   const bool rope = ROPE != kNone && tensor == 0;
 
+  pdl_wait();
   const int len = __ldg(a.seq_lens + b);
   int n = a.n_new;
   if (a.new_lens) {
@@ -246,10 +247,9 @@ int launch(const Q8AppendArgs &a, int num_sms, cudaStream_t st) {
   const long long gz = 2 * ((a.heads + hpc - 1) / hpc);
   if (a.batch > 65535 || gz > 65535) return TQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)touched, (unsigned)a.batch, (unsigned)gz);
-  if (!a.rope) q8_append_kernel<T, kNone><<<grid, kThreads, 0, st>>>(a, (int)hpc);
-  else if (a.table.interleaved || a.table.dim % 16 == 0) q8_append_kernel<T, kOwn><<<grid, kThreads, 0, st>>>(a, (int)hpc);
-  else q8_append_kernel<T, kPartner><<<grid, kThreads, 0, st>>>(a, (int)hpc);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  auto *kernel = !a.rope ? q8_append_kernel<T, kNone>
+                 : a.table.interleaved || a.table.dim % 16 == 0 ? q8_append_kernel<T, kOwn> : q8_append_kernel<T, kPartner>;
+  return launch_overlapped(true, kernel, grid, dim3(kThreads), 0, st, a, (int)hpc) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 // One thread per 16 coordinates of a token: code * 2^e, exact.

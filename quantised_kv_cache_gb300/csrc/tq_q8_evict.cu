@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int bh = blockIdx.x / ranks, b = bh / a.heads;
+  pdl_wait();
   int n = __ldg(a.seq_lens + b);
   if (n < 0 || n > a.src.capacity) {
     if (tid == 0) set_error(a.error, TQ_ERR_ARG);
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constan
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block, j0 = blockIdx.x * per, j1 = min(blocks, j0 + per);
   const int32_t *kept = a.kept + bh * a.keep;
   auto index = [&](int j) { return j * kQ8Block + t < a.keep ? __ldg(kept + j * kQ8Block + t) : -1; };
+  pdl_wait();
   int next = index(j0);
   for (int j = j0; j < j1; ++j) {
     const int s = next;
@@ -256,18 +258,20 @@ int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream) {
   cfg.blockDim = dim3(kSel);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the launch overlaps the kernel before it
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, q8_select_kernel, a) != cudaSuccess) return TQ_ERR_CUDA;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
   // blocks per CTA: 4 where at least four rounds of four CTAs an SM remain
   const int per = (long long)blocks * bh >= 16LL * 4 * num_sms ? 4 : 1;
-  q8_gather_kernel<<<dim3((unsigned)((blocks + per - 1) / per), (unsigned)bh), kGather, 0, st>>>(a, per);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)bh);
+  return launch_overlapped(true, q8_gather_kernel, grid, dim3(kGather), 0, st, a, per) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // namespace tq

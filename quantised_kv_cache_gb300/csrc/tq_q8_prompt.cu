@@ -56,6 +56,7 @@ struct Plan {
 // One warp per entry (sequence, 256 rows).
 __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__ Q8AttnArgs a, Plan p) {
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  pdl_wait();
   if (e >= p.entries) return;
   const int b = e / p.pairs, r0 = (e % p.pairs) * kUnit, G = a.group, R = G * a.n_q;
   int len, m;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p) {
   __shared__ int warp_sum_[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
+  pdl_wait();
   if (tid == 0) p.pre[0] = 0;
   for (int e0 = 0; e0 < p.entries; e0 += 1024) {
     const int e = e0 + tid;
@@ -247,6 +249,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem;
+  pdl_wait();
 
   const long long total = (long long)p.pre[p.entries] * a.heads_kv;
   const long long slices = min((long long)gridDim.x, total);
@@ -691,6 +694,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 
 // The rows of a unit that was cut: lane = row, a warp per 4 coordinates; 32 rows a CTA.
 __global__ void __launch_bounds__(1024) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
+  pdl_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts < 2) return;
   const int col = threadIdx.x >> 5, r = blockIdx.y * 32 + (threadIdx.x & 31), row = cut.pair * kUnit + r, G = a.group;
@@ -725,11 +729,11 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   constexpr int smem = stages_of(TERMS) * kStage + 2 * TERMS * kQTerm;
   if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  q8_entries_kernel<<<(p.entries + 7) / 8, 256, 0, st>>>(a, p);
-  q8_prefix_kernel<<<1, 1024, 0, st>>>(p);
-  q8_prompt_kernel<TERMS, EXTRA><<<num_sms, kThreads, smem, st>>>(a, p);
-  q8_prompt_join_kernel<<<dim3(num_sms, kUnit / 32), 1024, 0, st>>>(a, p);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  cudaError_t e = launch_overlapped(true, q8_entries_kernel, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_join_kernel, dim3(num_sms, kUnit / 32), dim3(1024), 0, st, a, p);
+  return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }

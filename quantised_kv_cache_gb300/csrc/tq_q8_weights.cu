@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
   const int tok0 = blockIdx.x * kTile, h = blockIdx.y, b = blockIdx.z;
   int len, m;
+  pdl_wait();
   seq_sizes(a, b, &len, &m, false);
   const int n = min(kTile, max(0, len - tok0));
   const long long bh = (long long)b * a.heads_kv + h, at = bh * a.c.capacity + tok0;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kKept) q8_kept_kernel(const __grid_constant__ 
   __shared__ int2 range[64];
   const int slot = (blockIdx.x * kKept + threadIdx.x) * 4, h = blockIdx.y, b = blockIdx.z, R = a.group * a.n_q;
   int len, m;
+  pdl_wait();
   seq_sizes(a, b, &len, &m, false);
   const long long bh = (long long)b * a.heads_kv + h;
   if ((int)threadIdx.x < R) {  // R is at most 64
@@ -199,9 +201,8 @@ int launch(const Q8AttnArgs &a, int slots, cudaStream_t st) {
   constexpr int smem = kTile * kD + kWg * kOp;
   if (cudaFuncSetAttribute(q8_weights_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  q8_weights_kernel<T><<<dim3((unsigned)((slots + kTile - 1) / kTile), (unsigned)a.heads_kv, (unsigned)a.batch), kThreads,
-                         smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  const dim3 grid((unsigned)((slots + kTile - 1) / kTile), (unsigned)a.heads_kv, (unsigned)a.batch);
+  return launch_overlapped(true, q8_weights_kernel<T>, grid, dim3(kThreads), smem, st, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -212,9 +213,8 @@ int launch_q8_weights(const Q8AttnArgs &a, void *stream) {
   const int slots = a.weights == a.weights_in ? a.max_len : a.c.capacity;
   if (a.heads_kv > 65535 || a.batch > 65535) return TQ_ERR_UNSUPPORTED;
   if (a.scores) {
-    q8_kept_kernel<<<dim3((unsigned)((slots + 4LL * kKept - 1) / (4 * kKept)), (unsigned)a.heads_kv, (unsigned)a.batch), kKept, 0,
-                     st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    const dim3 grid((unsigned)((slots + 4LL * kKept - 1) / (4 * kKept)), (unsigned)a.heads_kv, (unsigned)a.batch);
+    return launch_overlapped(true, q8_kept_kernel, grid, dim3(kKept), 0, st, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
   }
   return a.out_dtype == TQ_F32 ? launch<8>(a, slots, st) : launch<4>(a, slots, st);
 }

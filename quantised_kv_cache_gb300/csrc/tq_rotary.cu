@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) rotary_kernel(con
   __syncthreads();
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   if (id >= items) return;
+  pdl_wait();
   const int j = (int)(id % kRow);
   long long rest = id / kRow;
   // neighbouring threads on rows that lie together: of one token's heads, or of one head's tokens
@@ -131,9 +132,9 @@ int launch(const RotaryArgs &a, int num_sms, cudaStream_t st) {
   const long long items = (long long)a.batch * a.n * ((a.heads + hpt - 1) / hpt) * (kD / (2 * V));
   const long long grid = (items + 255) / 256;
   if (grid > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
-  if (a.rope.interleaved) rotary_kernel<T, V, true><<<(unsigned)grid, 256, 0, st>>>(a, (int)hpt, items);
-  else rotary_kernel<T, V, false><<<(unsigned)grid, 256, 0, st>>>(a, (int)hpt, items);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  auto *kernel = a.rope.interleaved ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>;
+  const cudaError_t e = launch_overlapped(true, kernel, dim3((unsigned)grid), dim3(256), 0, st, a, (int)hpt, items);
+  return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 template <typename T>
