@@ -585,7 +585,7 @@ typedef struct tq_q8_attn {
  * taken as unseen; both set the device error word to TQ_ERR_ARG. Rounding: the
  * products of codes with 16-bit queries are exact, their sums fp32; the
  * probabilities enter the value sums with 24 significant bits when out_dtype is
- * TQ_F32, else with 12 for up to 64 query rows (n_q x group) per KV head and, beyond, with 11 for TQ_F16 and
+ * TQ_F32, else with 12 for up to 16 query rows (n_q x group) per KV head and, beyond, with 11 for TQ_F16 and
  * 8 for TQ_BF16 (whose queries then lose coordinates below 2^-17 of a row's largest); the
  * softmax's sum is fp32 throughout. */
 tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,

@@ -29,7 +29,10 @@ constexpr int kWg = 4;                  // warpgroups, each with a tile of its o
 constexpr int kConsumers = kWg * 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launch
-constexpr long long kFewRows = 64;      // rows up to which this kernel takes a 16-bit call
+// Rows up to which this kernel takes a 16-bit call: one unit. 16 rows of one sequence over 16384 tokens, 8 KV heads: 40 us
+// here, 40 (bf16) or 47 (fp16) in the kernel for many rows, 148 against 176 or 214 in a batch of 8; 20 rows (two units, which
+// read the cache twice): 64 against 43 or 50, in a batch of 8 243 against 177 or 214.
+constexpr long long kFewRows = 16;
 constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
 
 constexpr int kStages = 5;
@@ -511,11 +514,13 @@ int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts
   return TQ_OK;
 }
 
-// The scores are kept for the weights when they fit into this much workspace; else they are formed again.
-constexpr size_t kScoreBytes = size_t(256) << 20;
-size_t score_bytes(int batch, int heads_q, int n_q, int max_len) {
+// The scores of up to 64 rows (no more bytes than the cache that they come from) are kept for the weights when they fit into a
+// GB of workspace; else they are formed again. 16 sequences of 16384 tokens, 8 KV heads, 4 rows: 111 us kept, 706 formed again.
+constexpr long long kKeptRows = 64;
+constexpr size_t kScoreBytes = size_t(1) << 30;
+size_t score_bytes(int batch, int heads_q, long long rows, int n_q, int max_len) {
   const size_t n = (size_t)batch * heads_q * n_q * ((max_len + kTile - 1) / kTile * kTile) * sizeof(float);
-  return n <= kScoreBytes ? n : 0;
+  return rows <= kKeptRows && n <= kScoreBytes ? n : 0;
 }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
@@ -523,11 +528,11 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 // Workspace: for the weights the log-sums and, for few rows, the scores; then either kernel's records (few rows: cuts and parts).
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
-  const bool few_rows = (long long)(heads_q / heads_kv) * n_q <= kFewRows;
+  const long long R = (long long)(heads_q / heads_kv) * n_q;
   const size_t lse = weights ? round16((size_t)batch * heads_q * n_q * sizeof(float)) : 0;
-  const size_t scores = weights && few_rows ? score_bytes(batch, heads_q, n_q, max_len) : 0;
+  const size_t scores = weights ? score_bytes(batch, heads_q, R, n_q, max_len) : 0;
   const size_t few = round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
-  const size_t many = few_rows ? 0 : q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
+  const size_t many = R <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
   return lse + scores + (few > many ? few : many);
 }
 
@@ -535,16 +540,16 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, vo
   cudaStream_t st = (cudaStream_t)stream;
   Q8AttnArgs a = args;
   const long long R = (long long)a.group * a.n_q;
+  const bool few = R <= kFewRows || a.out_dtype == TQ_F32;
   char *w = (char *)workspace;
   if (a.weights) {
     if (!a.lse) a.lse = (float *)w;
     w += round16((size_t)a.batch * a.heads_q * a.n_q * sizeof(float));
-    const size_t scores = R <= kFewRows ? score_bytes(a.batch, a.heads_q, a.n_q, a.max_len) : 0;
-    if (scores) a.scores = (float *)w, a.scores_ld = (a.max_len + kTile - 1) / kTile * kTile;
+    const size_t scores = score_bytes(a.batch, a.heads_q, R, a.n_q, a.max_len);
+    if (scores && few) a.scores = (float *)w, a.scores_ld = (a.max_len + kTile - 1) / kTile * kTile;
     w += scores;
   }
-  // many rows with results of 16 bits: rows as lanes
-  if (R > kFewRows && a.out_dtype != TQ_F32) {
+  if (!few) {  // rows as lanes
     const int s = launch_q8_prompt(a, w, num_sms, stream);
     if (s != TQ_OK) return s;
   } else {

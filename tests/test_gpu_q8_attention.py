@@ -79,7 +79,7 @@ def check(got, q, k, v, lens, new, *, dtype, out_dtype, begin=None, end=None, sc
     G = Hq // H
     sc = 1 / np.sqrt(128.0) if scale is None else scale
     wide = out_dtype == F32
-    many = G * n > 64 and not wide
+    many = G * n > 16 and not wide
     worst = 0.0
     wsum = np.zeros((B, H, k.shape[2])) if weights is not None else None
     wtol = np.zeros_like(wsum) if weights is not None else None
