@@ -239,9 +239,10 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
 template <typename T>
 int launch(const Q8AppendArgs &a, int num_sms, cudaStream_t st) {
   const int touched = (int)(((long long)a.n_new + kQ8Block - 2) / kQ8Block + 1);  // blocks n_new slots can lie in
-  // heads per CTA: all that share the sines, while two thousand threads an SM remain
+  // Heads per CTA (they share the sines and the CTA's start): as many as leave two CTAs an SM, up to 8. 4 sequences, 8 heads: 64 new
+  // tokens 4.3 us at one head, 6.6 at 4; 1024 tokens 13.1 at one, 10.1 at 4; 16384 tokens 174 at one, 96 at 4, 86 at 8.
   const long long ctas = 2LL * touched * a.batch * a.heads;
-  long long hpc = ctas / ((long long)num_sms * 4);
+  long long hpc = (ctas + 2LL * num_sms - 1) / (2LL * num_sms);
   hpc = hpc < 1 ? 1 : hpc > 8 ? 8 : hpc;
   if (hpc > a.heads) hpc = a.heads;
   const long long gz = 2 * ((a.heads + hpc - 1) / hpc);

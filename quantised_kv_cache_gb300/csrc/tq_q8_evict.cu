@@ -246,9 +246,14 @@ int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   const long long bh = (long long)a.batch * a.heads;
   if (bh > 65535) return TQ_ERR_UNSUPPORTED;
-  // CTAs per sequence-head: one up to 8192 slots (a pass over them is then a few microseconds), up to 8 beyond
+  // CTAs per sequence-head: as many as keep 2048 slots each while all run at once, and enough to hold the keys in shared memory.
+  // Clusters of 8 fill only half of the SMs (a GPC takes whole clusters). 8 heads of 131072 slots: 37 us with 8 CTAs each, 46 with
+  // 4, 104 with 2 (keys read again), 219 with 1; 16 heads: 70 with 8, 56 with 4; 64 heads: 202, 150, 177, 293; 128
+  // heads of 8192 slots: 76 with 1, 89 with 2; 32 heads: 37 with 1, 33 with 4.
   int ranks = 1;
-  while (ranks < kMaxRanks && a.src.capacity > 8192 * ranks) ranks *= 2;
+  while (ranks < kMaxRanks && (a.src.capacity > (long long)kSelKeys * ranks ||
+                               (a.src.capacity > 2048LL * ranks && 2 * ranks * bh <= (ranks == 4 ? num_sms / 2 : num_sms))))
+    ranks *= 2;
   const int held = (a.src.capacity + ranks - 1) / ranks;
   const size_t smem = sizeof(uint32_t) * (size_t)(held < kSelKeys ? held : kSelKeys);
   if (cudaFuncSetAttribute(q8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) != cudaSuccess)
@@ -268,8 +273,9 @@ int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream) {
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, q8_select_kernel, a) != cudaSuccess) return TQ_ERR_CUDA;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
-  // blocks per CTA: 4 where at least four rounds of four CTAs an SM remain
-  const int per = (long long)blocks * bh >= 16LL * 4 * num_sms ? 4 : 1;
+  // blocks per CTA: 2 or 4 where sixteen CTAs an SM remain (8064 blocks: 75.6 us with 1, 72.9 with 2, 72.8 with 4; 512: 37.6, 37.9, 40.7)
+  const long long rounds = (long long)blocks * bh / (16LL * num_sms);
+  const int per = rounds >= 4 ? 4 : rounds >= 2 ? 2 : 1;
   const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)bh);
   return launch_overlapped(true, q8_gather_kernel, grid, dim3(kGather), 0, st, a, per) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
