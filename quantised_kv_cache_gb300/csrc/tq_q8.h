@@ -92,7 +92,9 @@ struct Q8AttnArgs {
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights);
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q);
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
-int launch_q8_weights(const Q8AttnArgs &a, void *stream);
+// `terms`: of the queries, where 16-bit results' scores were not kept
+size_t q8_weights_workspace(int num_sms, int batch, int heads_kv, int group, int n_q, int max_len);
+int launch_q8_weights(const Q8AttnArgs &a, int terms, void *workspace, int num_sms, void *stream);
 int launch_q8_attention(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 
 }  // namespace tq

@@ -526,14 +526,17 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// Workspace: for the weights the log-sums and, for few rows, the scores; then either kernel's records (few rows: cuts and parts).
+// Workspace: for the weights the log-sums and, for few rows, the scores; then either kernel's records (few rows: cuts and parts), in
+// whose place the weights' row tiles come.
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
   const long long R = (long long)(heads_q / heads_kv) * n_q;
   const size_t lse = weights ? round16((size_t)batch * heads_q * n_q * sizeof(float)) : 0;
   const size_t scores = weights ? score_bytes(batch, heads_q, R, n_q, max_len) : 0;
   const size_t few = round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
   const size_t many = R <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
-  return lse + scores + (few > many ? few : many);
+  const size_t tiles = weights && (R > kFewRows || !scores) ? q8_weights_workspace(num_sms, batch, heads_kv, heads_q / heads_kv, n_q, max_len) : 0;
+  const size_t records = few > many ? few : many;
+  return lse + scores + (records > tiles ? records : tiles);
 }
 
 int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, void *stream) {
@@ -575,7 +578,8 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, vo
         if (s != TQ_OK) return s;
       }
   }
-  return a.weights ? launch_q8_weights(a, stream) : TQ_OK;
+  // the attention's records are read by now: their place serves the weights
+  return a.weights ? launch_q8_weights(a, few || a.q_dtype != TQ_BF16 ? 3 : 2, w, num_sms, stream) : TQ_OK;
 }
 
 }  // namespace tq

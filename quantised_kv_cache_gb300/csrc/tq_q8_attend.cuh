@@ -132,4 +132,34 @@ __device__ __forceinline__ float q8_score_log2(float qk, const Q8Score &s) {
   return x * kLog2e;
 }
 
+// cap tanh(x / cap) in log2 units with tanh = 1 - 2 / (1 + e^2x): off by a few 2^-24 of the cap
+__device__ __forceinline__ float capped_log2(float x, const Q8Score &s) {
+  if (s.softcap == 0.f) return x * kLog2e;
+  const float y = fminf(fmaxf(x * s.inv_cap, -10.f), 10.f);
+  const float e = ex2_approx(y * (2.f * kLog2e));
+  return s.softcap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 16 columns of this thread's lane on their way to v, and the wait for them (and any others): v may be used after it. A
+// loop loads the next 16 after waiting for these, so that they arrive while these are worked on.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
 }  // namespace tq

@@ -148,9 +148,6 @@ __device__ __forceinline__ void bar_rt(int rt) { asm volatile("bar.sync %0, 256;
 // The row tiles take turns at the exponentials: turn_take waits for the other's turn_pass.
 __device__ __forceinline__ void turn_take(int rt) { asm volatile("bar.sync %0, 512;" ::"r"(3 + rt) : "memory"); }
 __device__ __forceinline__ void turn_pass(int rt) { asm volatile("bar.arrive %0, 512;" ::"r"(4 - rt) : "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // D (TMEM) (+)= A (TMEM, four 8-bit K-elements per column) x B (shared); executed by one lane.
 __device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -165,23 +162,6 @@ __device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, u
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3])
-               : "memory");
-}
-// 16 columns of this thread's lane on their way to v, and the wait for them (and any others): v may be used after it. A
-// loop loads the next 16 after waiting for these, so that they arrive while these are worked on.
-__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const float (&v)[16]) {
@@ -213,14 +193,6 @@ __device__ __forceinline__ uint32_t e4m3_h2(uint32_t b) {
 __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
   const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<__half2 *>(&y));
   return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// cap tanh(x / cap) in log2 units with tanh = 1 - 2 / (1 + e^2x): off by a few 2^-24 of the cap
-__device__ __forceinline__ float capped_log2(float x, const Q8Score &s) {
-  if (s.softcap == 0.f) return x * kLog2e;
-  const float y = fminf(fmaxf(x * s.inv_cap, -10.f), 10.f);
-  const float e = ex2_approx(y * (2.f * kLog2e));
-  return s.softcap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
 }
 
 template <int TERMS, bool EXTRA>
@@ -418,28 +390,14 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       bar_rt(rt);
 #pragma unroll 1
       for (int k0 = 0; k0 < 16; k0 += 8) {
-        // eight rows' loads in flight: no branch in their way, a row that is not there loads another and counts as 0
         uint2 raw[8];
         const int first_row = u.pair * kUnit + rt * 128 + (warp & 7) * 16 + k0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = min(first_row + k, R - 1), i = row / G;
-          const long long off = u.b * a.qs.b + (u.h * G + row - i * G) * a.qs.h + min(i, m - 1) * a.qs.t + 4 * lane;
-          raw[k] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
-        }
+        load_rows(a, u.b, u.h, m, first_row, lane, raw);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = (warp & 7) * 16 + k0 + k, row = first_row + k;
           float x[4];
-          if (a.q_dtype == TQ_BF16) {
-            x[0] = __uint_as_float(raw[k].x << 16), x[1] = __uint_as_float(raw[k].x & 0xffff0000u);
-            x[2] = __uint_as_float(raw[k].y << 16), x[3] = __uint_as_float(raw[k].y & 0xffff0000u);
-          } else {
-            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&raw[k].x));
-            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&raw[k].y));
-            x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
-          }
-          if (row >= R || row / G >= m) x[0] = x[1] = x[2] = x[3] = 0.f;
+          row_floats(a, raw[k], row < R && row / G < m, x);
           uint32_t w[3];
           const int ex = row_terms(x, w);
 #pragma unroll

@@ -66,6 +66,28 @@ __device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int 
   return e;
 }
 
+// Many rows: 4 coordinates a lane of eight rows of 16-bit queries from first_row on, their loads in flight at once: no branch in their
+// way, a row that is not there loads another (and counts as 0).
+__device__ __forceinline__ void load_rows(const Q8AttnArgs &a, int b, int h, int m, int first_row, int lane, uint2 (&raw)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = min(first_row + k, a.group * a.n_q - 1), i = row / a.group;
+    const long long off = b * a.qs.b + (h * a.group + row - i * a.group) * a.qs.h + min(i, max(m - 1, 0)) * a.qs.t + 4 * lane;
+    raw[k] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
+  }
+}
+__device__ __forceinline__ void row_floats(const Q8AttnArgs &a, uint2 raw, bool live, float (&x)[4]) {
+  if (a.q_dtype == TQ_BF16) {
+    x[0] = __uint_as_float(raw.x << 16), x[1] = __uint_as_float(raw.x & 0xffff0000u);
+    x[2] = __uint_as_float(raw.y << 16), x[3] = __uint_as_float(raw.y & 0xffff0000u);
+  } else {
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&raw.x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&raw.y));
+    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+  }
+  if (!live) x[0] = x[1] = x[2] = x[3] = 0.f;
+}
+
 // Few rows: term k of row r is operand row k NR + r. An accumulator's columns are summed over the terms, the small ones first.
 __host__ __device__ constexpr int stacked_rows(int NR, int T) { return T * NR < 16 ? 16 : T * NR; }
 template <int NR, int T>
