@@ -132,12 +132,22 @@ __device__ __forceinline__ float q8_score_log2(float qk, const Q8Score &s) {
   return x * kLog2e;
 }
 
-// cap tanh(x / cap) in log2 units with tanh = 1 - 2 / (1 + e^2x): off by a few 2^-24 of the cap
-__device__ __forceinline__ float capped_log2(float x, const Q8Score &s) {
-  if (s.softcap == 0.f) return x * kLog2e;
-  const float y = fminf(fmaxf(x * s.inv_cap, -10.f), 10.f);
-  const float e = ex2_approx(y * (2.f * kLog2e));
-  return s.softcap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+// scale (times a row's and a block's) x, capped, in log2 units: cap tanh(y) with tanh = 1 - 2 / (1 + e^2y), off by a few 2^-24 of the
+// cap; an infinite e^2y gives 1, a zero one -1. `in` and `cap` from score_cap.
+struct ScoreCap {
+  float in, cap;  // cap 0: none
+};
+__device__ __forceinline__ ScoreCap score_cap(float scale, float softcap) {
+  return softcap == 0.f ? ScoreCap{scale * kLog2e, 0.f} : ScoreCap{scale * (2.f * kLog2e) / softcap, softcap * kLog2e};
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// x times c, which holds in
+__device__ __forceinline__ float capped_log2(float x, float c, float cap) {
+  return cap == 0.f ? x * c : fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(x * c)), cap);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {

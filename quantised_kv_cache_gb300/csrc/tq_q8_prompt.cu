@@ -32,6 +32,7 @@ constexpr int kRegsSoft = 112, kRegsControl = 32;  // 512 * 112 + 128 * 32 = 640
 constexpr int kStage = 2 * kTile * kD;
 constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
 constexpr int kPart = kUnit * (kD + 2);  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
+// Capped or biased scores run without turns (measured at 2048 of 8192 tokens: 653 us, 713 with them).
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
 
 constexpr int stages_of(int terms) { return terms == 2 ? 4 : 3; }
@@ -372,7 +373,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int rt = tid >> 8, half = (tid >> 7) & 1, lrow = tid & 127;
     const uint32_t t_s = tmem + rt * 256 + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half, t_o = t_s + 128;
-    const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
+    const ScoreCap sc = EXTRA ? score_cap(a.scale, a.softcap) : ScoreCap{};
     int it = 0;  // tiles done: stages and phases count on
     if (!EXTRA && rt == 1 && g0 < g1) turn_pass(rt);
     uint32_t sums = 0;
@@ -435,20 +436,15 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           if (ks < 0.f) to = 0;
         }
         // never 0, so that an unseen score of -inf stays -inf (products so small make no difference)
-        const float c = fmaxf(qs * fmaxf(ks, 0.f) * (EXTRA ? 1.f : a.scale * kLog2e), 1e-30f);
-        // a score in log2 (EXTRA), or the raw product (the scaling is in c); MASK: unseen ones are -inf
+        const float c = EXTRA ? qs * fmaxf(ks, 0.f) * sc.in : fmaxf(qs * fmaxf(ks, 0.f) * (a.scale * kLog2e), 1e-30f);
+        // the raw product (the scaling is in c); MASK: unseen ones are -inf
         auto score = [&](float x, int i, auto mask) {
-          if constexpr (EXTRA) {
-            x = capped_log2(x * c * sc.scale, sc);
-            if (a.slopes) {
-              const int slot = tok0 + 64 * half + i;
-              const int kp = a.kpos ? (slot < hi ? __ldg(a.kpos + bh * a.c.capacity + slot) : 0) : slot;
-              x = fmaf(-slope, (float)__sad(qp, kp, 0u), x);
-            }
-          }
           if constexpr (decltype(mask)::value) x = i >= from && i < to ? x : -INFINITY;
           return x;
         };
+        // where keys are at their slots, the distance of slot i of this half is |far - i|
+        const int slot0 = tok0 + 64 * half;
+        const float far = EXTRA && a.slopes && !a.kpos ? (float)((long long)qp - slot0) : 0.f;
         wait(&sm.bar_s[rt], (it + j) & 1);
         __syncwarp();  // tensor memory is read by whole warps
         tc_fence_after_sync();
@@ -457,11 +453,28 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
           float top1 = -INFINITY;
-          if constexpr (EXTRA) {  // capped, biased and masked once, here; long code, not unrolled four times
-#pragma unroll 1
+          if constexpr (EXTRA) {  // scaled to log2, capped, biased and masked once, here
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
+              uint32_t w[16];
+              tmem_ld_start(t_s + 16 * q, w);  // (the next 16 ahead, as below, would spill: 633 against 528 us capped)
+              tmem_ld_done(w);
               float x[16];
-              tmem_ld_cols<16>(t_s + 16 * q, x);
+              if (sc.cap == 0.f) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * c;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = capped_log2(__uint_as_float(w[i]), c, sc.cap);
+              }
+              if (a.kpos && a.slopes) {
+                const int32_t *kp = a.kpos + bh * a.c.capacity + slot0 + 16 * q;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, (float)__sad(qp, slot0 + 16 * q + i < hi ? __ldg(kp + i) : 0, 0u), x[i]);
+              } else if (a.slopes) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, fabsf(far - (float)(16 * q + i)), x[i]);
+              }
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 x[i] = score(x[i], 16 * q + i, mask);

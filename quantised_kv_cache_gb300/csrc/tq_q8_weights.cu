@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256) q8_row_tiles_kernel(const __grid_constant
       const int ex = row_terms(x, t);
 #pragma unroll
       for (int j = 0; j < TERMS; ++j) *reinterpret_cast<uint32_t *>(dyn + j * kTerm + q8_off(r0 + k, 4 * lane)) = t[j];
-      if (lane == 0) cl[r0 + k].x = pow2i(ex) * a.scale * (EXTRA ? 1.f : kLog2e);
+      if (lane == 0) cl[r0 + k].x = pow2i(ex) * score_cap(a.scale, a.softcap).in;
     }
   }
   if (tid < kTileRows) {
@@ -350,7 +350,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
       if (blk >= 0) ks = __ldg(a.c.ks + blk);
     }
     const int kp = EXTRA && a.kpos && tok < n ? __ldg(a.kpos + at + tok) : slot;
-    const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
+    const float cap = score_cap(a.scale, a.softcap).cap;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float k1 = fmaxf(ks, 0.f);
     float sum0 = 0.f, sum1 = 0.f;
@@ -380,7 +380,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
               const float4 c = *reinterpret_cast<const float4 *>(cl + r);
               float x0 = __uint_as_float(v[q & 1][i]), x1 = __uint_as_float(v[q & 1][i + 1]);
               if constexpr (EXTRA) {
-                x0 = capped_log2(x0 * (c.x * k1), sc), x1 = capped_log2(x1 * (c.z * k1), sc);
+                x0 = capped_log2(x0, c.x * k1, cap), x1 = capped_log2(x1, c.z * k1, cap);
                 if (a.slopes) {
                   const float4 e = *reinterpret_cast<const float4 *>(extra + r);
                   x0 = fmaf(-e.x, (float)__sad(__float_as_int(e.y), kp, 0u), x0);
