@@ -16,8 +16,8 @@
 //
 // Two blocks of a tile share one value sum, the smaller scale folded into its probabilities; where the scales are more than
 // 2^4 apart that would cost precision, and the blocks' sums are formed one after the other.
-// Work split: as in the kernel for few rows, equal slices of the (sequence, 256 rows, head, tile) space, cut units
-// joined afterwards; a small kernel finds each unit's tiles first.
+// Work split: as in the kernel for few rows, equal slices of the (sequence, 256 rows, head, tile) space, a unit's start counted
+// as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first.
 
 #include "tq_q8_rows.cuh"
 
@@ -48,6 +48,8 @@ struct Cut {
 
 struct Plan {
   int *pre;       // [entries + 1] tiles (of one head) before each entry
+  int *starts;    // [entries + 1] entries with tiles before each
+  long long *cut; // [CTAs + 1] where the slices of the tiles begin
   Entry *entry;   // [entries]
   Cut *cuts;      // [CTAs]
   float *parts;   // [CTAs][2][kPart]
@@ -82,31 +84,55 @@ __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__
   }
 }
 
-// Prefix sum of the entries' tiles, one CTA.
-__global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p) {
-  __shared__ int warp_sum_[32];
+// What a unit's start (its queries, the first tile's chain alone) costs, in tiles.
+constexpr int kStart = 3;
+
+// Prefix sums of the entries' tiles and the slices, one CTA. Slices are equal in tiles and starts, and none is empty (an
+// interval of kStart + 1 holds a tile); with fewer than two tiles a CTA, in tiles alone, so that as many CTAs as possible work.
+__global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p, int heads, int ctas) {
+  __shared__ int warp_tiles[32], warp_starts[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int base = 0;
+  int base = 0, base_starts = 0;
   pdl_wait();
-  if (tid == 0) p.pre[0] = 0;
+  if (tid == 0) p.pre[0] = 0, p.starts[0] = 0;
   for (int e0 = 0; e0 < p.entries; e0 += 1024) {
     const int e = e0 + tid;
-    int x = e < p.entries ? p.pre[e + 1] : 0;
+    int x = e < p.entries ? p.pre[e + 1] : 0, y = x > 0 ? 1 : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
+      const int x1 = __shfl_up_sync(kFull, x, o), y1 = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) x += x1, y += y1;
     }
-    if (lane == 31) warp_sum_[warp] = x;
+    if (lane == 31) warp_tiles[warp] = x, warp_starts[warp] = y;
     __syncthreads();
-    int before = base, all = base;
+    int before = base, all = base, sbefore = base_starts, sall = base_starts;
     for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warp_sum_[w];
-      all += warp_sum_[w];
+      if (w < warp) before += warp_tiles[w], sbefore += warp_starts[w];
+      all += warp_tiles[w], sall += warp_starts[w];
     }
-    if (e < p.entries) p.pre[e + 1] = before + x;
-    base = all;
+    if (e < p.entries) p.pre[e + 1] = before + x, p.starts[e + 1] = sbefore + y;
+    base = all, base_starts = sall;
     __syncthreads();
+  }
+  const long long tiles = (long long)base * heads;
+  const int start = tiles >= 2LL * ctas ? kStart : 0;
+  const long long total = tiles + (long long)start * base_starts * heads;
+  const long long slices = min((long long)ctas, total / (start + 1));
+  for (int k = tid; k <= ctas; k += 1024) {
+    long long g = tiles;
+    if (k < slices) {
+      const long long c = total * k / slices;
+      int lo = 0, hi = p.entries - 1;
+      while (lo < hi) {  // the last entry that begins at or before c
+        const int mid = (lo + hi + 1) >> 1;
+        if (((long long)p.pre[mid] + (long long)start * p.starts[mid]) * heads <= c) lo = mid;
+        else hi = mid - 1;
+      }
+      const int cnt = p.pre[lo + 1] - p.pre[lo], each = cnt + start;
+      const long long in = c - ((long long)p.pre[lo] + (long long)start * p.starts[lo]) * heads;
+      g = (long long)p.pre[lo] * heads + in / each * cnt + max(0, (int)(in % each) - start);
+    }
+    p.cut[k] = g;
   }
 }
 
@@ -224,10 +250,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   const uint32_t tmem = sm.tmem;
   pdl_wait();
 
-  const long long total = (long long)p.pre[p.entries] * a.heads_kv;
-  const long long slices = min((long long)gridDim.x, total);
-  const bool idle = blockIdx.x >= slices;
-  const long long g0 = idle ? 0 : total * blockIdx.x / slices, g1 = idle ? 0 : total * (blockIdx.x + 1) / slices;
+  const long long g0 = p.cut[blockIdx.x], g1 = p.cut[blockIdx.x + 1];
+  const bool idle = g0 >= g1;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
     for (int i = 0; i < 8; ++i)
@@ -648,7 +672,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         int parts = 0;
         if (u.t0 == 0 && stop > g1) {
           parts = 1;
-          for (long long k = blockIdx.x + 1; k < slices && total * k / slices < stop; ++k) ++parts;
+          for (int k = blockIdx.x + 1; k < (int)gridDim.x && p.cut[k] < stop; ++k) ++parts;
         }
         p.cuts[blockIdx.x] = Cut{u.b, u.pair, u.h, parts};
       }
@@ -701,7 +725,7 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
   cudaError_t e = launch_overlapped(true, q8_entries_kernel, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p, a.heads_kv, num_sms);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_join_kernel, dim3(num_sms, kUnit / 32), dim3(1024), 0, st, a, p);
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
@@ -713,7 +737,7 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q) {
   const size_t pairs = ((size_t)group * n_q + kUnit - 1) / kUnit, entries = pairs * batch;
-  return round16((entries + 1) * sizeof(int)) + entries * sizeof(Entry) + round16((size_t)num_sms * sizeof(Cut)) +
+  return 2 * round16((entries + 1) * sizeof(int)) + round16((size_t)(num_sms + 1) * sizeof(long long)) + entries * sizeof(Entry) + round16((size_t)num_sms * sizeof(Cut)) +
          (size_t)num_sms * 2 * kPart * sizeof(float);
 }
 
@@ -724,6 +748,8 @@ int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *st
   p.entries = (int)entries, p.pairs = (int)pairs;
   char *w = (char *)workspace;
   p.pre = (int *)w, w += round16((size_t)(entries + 1) * sizeof(int));
+  p.starts = (int *)w, w += round16((size_t)(entries + 1) * sizeof(int));
+  p.cut = (long long *)w, w += round16((size_t)(num_sms + 1) * sizeof(long long));
   p.entry = (Entry *)w, w += (size_t)entries * sizeof(Entry);
   p.cuts = (Cut *)w, w += round16((size_t)num_sms * sizeof(Cut));
   p.parts = (float *)w;
