@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   int32_t *kept = a.kept + (long long)bh * a.keep;
   float *dw = a.dst_weights ? a.dst_weights + (long long)bh * a.dst.capacity : nullptr;
   int32_t *dp = a.dst_positions ? a.dst_positions + (long long)bh * a.dst.capacity : nullptr;
-  if (rank == 0 && tid == 0 && bh % a.heads == 0) a.dst_lens[b] = m;
 
   // this CTA's run of slots
   const int run = (n + ranks - 1) / ranks;
@@ -192,6 +191,10 @@ __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constan
   const int32_t *kept = a.kept + bh * a.keep;
   auto index = [&](int j) { return j * kQ8Block + t < a.keep ? __ldg(kept + j * kQ8Block + t) : -1; };
   pdl_wait();
+  if (blockIdx.x == 0 && bh % a.heads == 0 && tid == 0) {  // here, where no other thread reads the lengths: they may be updated in place
+    const int b = (int)(bh / a.heads);
+    a.dst_lens[b] = min(min(max(a.seq_lens[b], 0), a.src.capacity), a.keep);
+  }
   int next = index(j0);
   for (int j = j0; j < j1; ++j) {
     const int s = next;

@@ -315,6 +315,21 @@ def test_eviction_of_a_ragged_batch(ctx):
     check_evict(ctx, src, dst, lens, w, keep, 16, 500, None)
 
 
+def test_eviction_updates_the_lengths_in_place(ctx):
+    """The lengths' own array as the target: every head of a sequence has read its length by then."""
+    B, H, cap, keep = 8, 16, 4096, 1000
+    src, dst = tq.Cache(ctx, B, H, cap, device=DEV), tq.Cache(ctx, B, H, keep, device=DEV)
+    lens = [4096, 3000, 1001, 1000, 999, 1, 0, 2222]
+    fill(ctx, src, lens, 5)
+    w = torch.rand(B, H, cap, generator=gen(1), device=DEV)
+    want = [t.clone() for t in tq.tq_q8_evict(ctx.handle, src, dst, ints(lens), w, keep, 16, 500)]
+    for _ in range(20):
+        own = ints(lens)
+        got = tq.tq_q8_evict(ctx.handle, src, dst, own, w, keep, 16, 500, dst_lens=own)
+        assert got[1] is own and own.tolist() == [min(n, keep) for n in lens]
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_eviction_of_more_slots_than_shared_memory_holds(ctx):
     cap = 8 * 45056 + 30001  # the rest of each CTA's run is read again
     src, dst = tq.Cache(ctx, 1, 1, cap, device=DEV), tq.Cache(ctx, 1, 1, 200, device=DEV)
