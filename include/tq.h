@@ -558,7 +558,7 @@ typedef struct tq_q8_attn {
   int out_dtype;                /* q_dtype, or TQ_F32 */
   const void *d_q;              /* [batch][heads_q][n_q][d] under q_strides */
   int64_t q_strides[3];
-  void *d_out;                  /* [batch][heads_q][n_q][d] under out_strides */
+  void *d_out;                  /* [batch][heads_q][n_q][d] under out_strides; shares no memory with the queries */
   int64_t out_strides[3];
   const int32_t *d_seq_lens;    /* [batch]: tokens in the cache, the query tokens' own among them */
   const int32_t *d_new_lens;    /* [batch] or NULL (n_q): query tokens of each sequence; later rows are not written */
@@ -603,7 +603,7 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
  *   d_seq_lens  : int32 [batch], each in [0, src capacity] (cut to it otherwise: TQ_ERR_ARG in the error word)
  *   d_weights   : float [batch][heads_kv][src capacity]
  *   d_kept      : int32 [batch][heads_kv][keep], out: the kept tokens' slots in src, -1 from m on
- *   d_dst_lens  : int32 [batch], out: m
+ *   d_dst_lens  : int32 [batch], out: m (may be d_seq_lens)
  *   d_dst_weights, d_dst_positions : [batch][heads_kv][dst capacity] or NULL, out: the kept tokens' d_weights
  *                 and d_positions (int32 [batch][heads_kv][src capacity]; NULL: their slots), 0 from m on */
 tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *dst, int batch, int heads_kv,

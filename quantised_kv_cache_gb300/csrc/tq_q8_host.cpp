@@ -156,6 +156,7 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (!std::isfinite(p->scale) || !std::isfinite(p->softcap) || p->softcap < 0.f) return TQ_ERR_ARG;
   if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
   if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
+  if (p->d_out == p->d_q) return TQ_ERR_ARG;  // the weights read the queries again after the results are written
   tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
   if (s != TQ_OK) return s;
   if (p->max_len > cache->capacity) return TQ_ERR_ARG;

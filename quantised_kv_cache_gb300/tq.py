@@ -722,8 +722,8 @@ class Cache:
 
 class PagedCache(Cache):
     """A TQ-scheme cache in the paged layout (include/tq.h, "Paged layout"): `records` is a
-    pool of `pool_blocks` 16-token blocks and `block_table` (int32, on the device,
-    [batch][heads_kv][ceil(capacity / 16)]) maps each sequence-head's blocks into it; -1
+    pool of `pool_blocks` 16-token blocks (Q8: 64) and `block_table` (int32, on the device,
+    [batch][heads_kv][ceil(capacity / 16)], Q8: / 64) maps each sequence-head's blocks into it; -1
     marks an entry no call may reach. The table is the caller's: change it in place (in
     stream order) to remap blocks."""
 

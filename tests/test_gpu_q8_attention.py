@@ -533,6 +533,77 @@ def test_weights_of_more_scores_than_are_kept(ctx):
     assert not bool(w[..., :N - m].any()) and not bool(w[..., N:].any())
 
 
+@pytest.mark.parametrize("case", [(1, 4, 1, 700, [900]), (1, 8, 1, 1100, [1300]), (2, 4, 2, 130, [257, 200]), (1, 8, 8, 40, [513]), (3, 20, 2, 2, [256, 1, 0]),
+                                  (16, 8, 4, 70, [500 + 9 * i for i in range(16)])], ids=lambda c: "-".join(map(str, c[:4])) + f"-{max(c[4])}")
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("extra", ["causal", "documents", "capped biased", "placed"])
+def test_weights_of_many_rows(ctx, case, dtype, extra):
+    """Row tiles that are split over CTAs, that fill the ring many times, that see none of a CTA's tokens, that end early."""
+    B, Hq, H, n, lens = case
+    cap = max(lens) + 90
+    cache, k, v = make(ctx, B, H, cap, lens, seed=sum(lens), paged=extra == "placed")
+    q = queries(5, B, Hq, n, dtype, "tokens")
+    kw, ck, new = {}, {}, [min(n, L) for L in lens]
+    at = np.array([[L - m + i for i in range(n)] for L, m in zip(lens, new)])
+    if extra == "documents":
+        ck = dict(begin=np.maximum(at // 190 * 190, 0), end=at + 1)
+        kw = dict(key_begin=ints(ck["begin"]), key_end=ints(ck["end"]))
+    elif extra != "causal":
+        slopes = torch.linspace(0.01, 0.2, Hq, device=DEV)
+        ck, kw = dict(softcap=15.0, slopes=slopes.double().cpu().numpy()), dict(softcap=15.0, slopes=slopes)
+        if extra == "placed":
+            rng = np.random.default_rng(n)
+            ck.update(q_pos=rng.integers(0, 500, (B, n)), k_pos=rng.integers(0, 500, (B, H, cap)))
+            kw.update(q_positions=ints(ck["q_pos"]), k_positions=ints(ck["k_pos"]))
+    before = torch.rand(B, H, cap, generator=gen(8), device=DEV)
+    w, out = torch.full_like(before, float("nan")), torch.zeros_like(q)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, new_lens=ints(new), weights_in=before, weights=w, out=out, **kw)
+    check(np64(got), np64(q), k, v, lens, new, dtype=dtype, out_dtype=dtype, weights=np64(w), before=np64(before), **ck)
+    for b, L in enumerate(lens):
+        assert torch.equal(w[b, :, L:], before[b, :, L:])
+    place = before.clone()
+    tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, new_lens=ints(new), weights_in=place, weights=place, out=out, **kw)
+    assert torch.equal(place, w)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_weights_of_few_rows_and_more_slots_than_scores_are_kept_for(ctx, dtype):
+    """128 heads over two million slots, nearly all beyond the sequence: more than a GB of scores would be kept."""
+    H, cap, n = 8, 2_100_000, 300
+    nblk = -(-cap // 64)
+    table = torch.zeros(1, H, nblk, dtype=torch.int32, device=DEV)
+    table[0, :, :8] = torch.arange(8 * H, device=DEV, dtype=torch.int32).flip(0).view(H, 8)
+    cache = tq.PagedCache(ctx, 1, H, cap, pool_blocks=8 * H, block_table=table)
+    k, v = queries(1, 1, H, n, BF), queries(2, 1, H, n, BF)
+    tq.tq_q8_append(ctx.handle, cache, k, v, ints([0]))
+    q = queries(3, 1, 128, 1, dtype)
+    assert 128 * cap * 4 > 1 << 30
+    w = torch.zeros(1, H, cap, device=DEV)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints([n]), cap, weights_in=w, weights=w)
+    kv, vv = (np64(t) for t in tq.tq_dequantize(ctx.handle, cache, 0, n))
+    check(np64(got), np64(q), kv, vv, [n], [1], dtype=dtype, out_dtype=dtype, weights=np64(w[..., :n]))
+    assert not bool(w[..., n:].any())
+
+
+@pytest.mark.parametrize("B,Hq,H,n,N", [(1, 8, 1, 300, 1000), (4, 32, 8, 8, 3000), (16, 16, 16, 20, 700)])
+def test_back_to_back_weights_give_the_same_bits(ctx, B, Hq, H, n, N):
+    cache = tq.Cache(ctx, B, H, N, device=DEV)
+    k = queries(1, B, H, N, BF)
+    tq.tq_q8_append(ctx.handle, cache, k, k, ints([0] * B))
+    lens = ints([N] * B)
+    for dtype in (BF, HF):
+        q = queries(2, B, Hq, n, dtype)
+        ws = torch.empty(tq.tq_q8_attention_workspace(ctx.handle, B, Hq, H, n, N, weights=True), dtype=torch.uint8, device=DEV)
+        out, want = torch.empty_like(q), torch.empty(B, H, N, device=DEV)
+        tq.tq_q8_attention(ctx.handle, cache, q, lens, N, workspace=ws, out=out, weights=want)
+        w, bad = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device=DEV)
+        for i in range(300):
+            tq.tq_q8_attention(ctx.handle, cache, q, lens, N, workspace=ws, out=out, weights=w)
+            if i % 25 == 24:
+                bad += (w != want).sum()
+        assert int(bad) == 0
+
+
 @pytest.mark.parametrize("B,Hq,H,n,N", [(8, 32, 32, 1, 4096), (2, 32, 8, 1, 20000), (1, 16, 8, 300, 5000)])
 def test_back_to_back_calls_give_the_same_bits(ctx, B, Hq, H, n, N):
     """Many calls without a pause between them: tiles' copies land in any order, CTAs follow one another on an SM."""
@@ -601,6 +672,7 @@ def test_refusals(ctx):
     refused(tq.TQ_ERR_ARG, att, h, cache, q, lens, 128, out=torch.zeros(2, 4, 1, 128, device=DEV, dtype=HF))
     refused(tq.TQ_ERR_ARG, att, h, cache, q, lens, 128, out=torch.zeros(2, 1, 1, 128, device=DEV, dtype=BF).expand(2, 4, 1, 128))
     refused(tq.TQ_ERR_WORKSPACE, att, h, cache, q, lens, 128, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    refused(tq.TQ_ERR_ARG, att, h, cache, q, lens, 128, out=q)
     odd = torch.zeros(2, 4, 1, 132, dtype=BF, device=DEV)[..., :128]
     refused(tq.TQ_ERR_ALIGN, att, h, cache, odd, lens, 128)
     with pytest.raises(ValueError):
