@@ -3,15 +3,18 @@
 // order of the sum.
 //
 // q8_kept_kernel: the attention for few rows has kept its scores (4 bytes a row and token, beside the 256 of the cache that it
-// reads); a thread adds up 4 tokens' probabilities over the rows. Bound by those scores' bytes.
+// reads); a thread adds up 4 tokens' probabilities over the rows. Bound by those scores' bytes: 10 us for 6 rows of 4 x 16383 tokens and 8 heads.
 // Else, after the attention has left each row's lse, the scores are formed again from the keys alone: token = accumulator lane =
 // thread, which adds its own token's probabilities over all rows in registers.
 // q8_weights_many_kernel, 16-bit results: a CTA holds the keys of 256 tokens; row tiles of 128 queries (their terms made once, by
 // q8_row_tiles_kernel) pass through a ring, those that see none of the tokens left out. Two accumulators per token tile, so that
 // the MMAs of one row tile (66 clocks each, 4 TERMS a tile) run under the exponentials of the other: bound by those, 1024 clocks for 128 x 128
-// at 16 a clock. Where tokens alone give too few CTAs the row tiles are split, and the splits' sums added in order.
+// at 16 a clock. Where tokens alone give too few CTAs the row tiles are split, and the splits' sums added in order. Measured: 2048 query
+// tokens over 8192, 32 query and 8 KV heads: 190 us beside the attention's 304, half the exponentials' rate; 16 sequences of 16384
+// tokens and 64 rows: 300 us, a CTA's start for one row tile.
 // q8_weights_kernel, 32-bit results: one CTA per 128 tokens, its key tile read once; four warpgroups take every fourth tile of 8
-// rows: 8 e5m2 terms side by side, one score MMA chain. Row tiles that see none of the tokens are skipped.
+// rows: 8 e5m2 terms side by side, one score MMA chain. Row tiles that see none of the tokens are skipped. Measured: 128 query tokens of
+// 2048, 32 query and 8 KV heads: 62 us beside the attention's 100.
 
 #include "tq_q8_rows.cuh"
 

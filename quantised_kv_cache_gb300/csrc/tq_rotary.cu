@@ -3,9 +3,11 @@
 // Pair (a, b) -> gain (a cos - b sin, b cos + a sin). Bound by memory: every element is read and
 // written once. A thread owns V + V elements of a row (the two halves of V pairs, or 2V
 // consecutive elements when the pairs are interleaved; a row's coordinates past `dim` pass
-// through), forms their V sines and cosines once and uses them for up to 4 heads of its token, all
-// loads in flight before the first is used. V = 8 (16-byte accesses for 16-bit types) needs
-// dim a multiple of 16, V = 4 covers the other multiples of 8.
+// through), forms their V sines and cosines once and uses them for several heads of its token, the
+// loads of four in flight before the first is used (one at a time: 71 us where four take 45). V = 8
+// (16-byte accesses for 16-bit types) needs dim a multiple of 16, V = 4 covers the other multiples of 8.
+// Measured: 16384 tokens of 32 heads in bf16, 64 of 128 coordinates interleaved: 44 us, 6.1 TB/s, 0.90 of a
+// plain copy; what is left is the loads' latency (7 of 10 stalled warps) and the sines (ALU 38 % busy). 16 tokens: 2.6 us, a launch.
 
 #include "tq_q8.cuh"
 
