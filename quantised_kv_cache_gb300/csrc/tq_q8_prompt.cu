@@ -691,8 +691,9 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   if (warp == kSoft / 32 + 2) tmem_dealloc(tmem, 512);
 }
 
-// The rows of a unit that was cut: lane = row, a warp per 4 coordinates; 32 rows a CTA.
-__global__ void __launch_bounds__(1024) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
+// The rows of a unit that was cut: lane = row, a warp per kJoin times 4 coordinates; 32 rows a CTA.
+constexpr int kJoin = 2;  // (2048 of 8192 tokens: 303 us with 1, 299.5 with 2 or 4; 64 rows of 16384 tokens, joined of 18 parts: 44, 44, 47)
+__global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   pdl_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts < 2) return;
@@ -704,22 +705,30 @@ __global__ void __launch_bounds__(1024) q8_prompt_join_kernel(const __grid_const
   auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kPart; };
   float top = -INFINITY;
   for (int k = 0; k < cut.parts; ++k) top = fmaxf(top, rec(k)[kUnit * kD + r]);
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
+  float o[kJoin][4], l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kJoin; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+#pragma unroll 2
   for (int k = 0; k < cut.parts; ++k) {
     const float *x = rec(k);
     const float mk = x[kUnit * kD + r], f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
-    const float4 y = reinterpret_cast<const float4 *>(x)[col * kUnit + r];
-    o[0] = fmaf(y.x, f, o[0]), o[1] = fmaf(y.y, f, o[1]), o[2] = fmaf(y.z, f, o[2]), o[3] = fmaf(y.w, f, o[3]);
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      const float4 y = reinterpret_cast<const float4 *>(x)[(col + 32 / kJoin * j) * kUnit + r];
+      o[j][0] = fmaf(y.x, f, o[j][0]), o[j][1] = fmaf(y.y, f, o[j][1]), o[j][2] = fmaf(y.z, f, o[j][2]), o[j][3] = fmaf(y.w, f, o[j][3]);
+    }
     l = fmaf(x[kUnit * (kD + 1) + r], f, l);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] *= inv;
   const int hq = cut.h * G + row % G;
-  const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + 4 * col;
-  if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(a.out) + off, o);
-  else store_vec<__half, 4>(static_cast<__half *>(a.out) + off, o);
+#pragma unroll
+  for (int j = 0; j < kJoin; ++j) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[j][k] *= inv;
+    const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + 4 * (col + 32 / kJoin * j);
+    if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(a.out) + off, o[j]);
+    else store_vec<__half, 4>(static_cast<__half *>(a.out) + off, o[j]);
+  }
   if (a.lse && col == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
 }
 
@@ -731,7 +740,7 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   cudaError_t e = launch_overlapped(true, q8_entries_kernel, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p, a.heads_kv, num_sms);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_join_kernel, dim3(num_sms, kUnit / 32), dim3(1024), 0, st, a, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_join_kernel, dim3(num_sms, kUnit / 32), dim3(1024 / kJoin), 0, st, a, p);
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
