@@ -65,10 +65,10 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
 }
 
 __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__ Q8EvictArgs a) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(8) int hist[kBins];
   __shared__ __align__(8) int added[kBins / 2];
-  __shared__ int sums[32], found[2], share[2];
+  __shared__ int sums[32], found[2], share[2], warp_more[kSel / 32], warp_ties[kSel / 32];
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int bh = blockIdx.x / ranks, b = bh / a.heads;
@@ -88,17 +88,16 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   const int run = (n + ranks - 1) / ranks;
   const int s0 = min(n, rank * run), cnt = min(n, s0 + run) - s0;
   int pick = n > a.keep ? a.keep - a.sink - a.recent : 0;  // tokens chosen by weight
-  auto make = [&](int i) -> uint32_t {
-    const int s = s0 + i;
-    if (n <= a.keep || s < a.sink || s >= n - a.recent) return kAlways;
-    return weight_key(__ldg(w + s));
-  };
+  // slots from the sink to the recent ones have a key, of their weight; where all stay, none
+  const int low = n <= a.keep ? cnt : a.sink - s0, high = n - a.recent - s0, held = min(cnt, kSelKeys);
+  auto make = [&](int i) -> uint32_t { return i < low || i >= high ? kAlways : weight_key(__ldg(w + s0 + i)); };
   auto key = [&](int i) -> uint32_t { return i < kSelKeys ? keys[i] : make(i); };
 #pragma unroll 16
-  for (int i = tid; i < min(cnt, kSelKeys); i += kSel) keys[i] = make(i);
+  for (int i = tid; i < held; i += kSel) keys[i] = make(i);
+  if (tid < (-held & 3)) keys[held + tid] = kAlways;  // whole groups of four
   __syncthreads();  // the runs below cross threads, also where nothing is chosen by weight
 
-  uint32_t prefix = 0, mask = 0;  // the digits of the threshold found so far
+  uint32_t prefix = pick > 0 ? 0 : kAlways, mask = 0;  // the digits of the threshold found so far
   int need = pick;                // tokens still to choose among the keys with these digits
   if (pick > 0) {                 // the same for every CTA of the cluster
 #pragma unroll 1
@@ -107,11 +106,15 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
       const uint32_t digit = pass == 2 ? 1023u : 2047u;
       hist[tid] = 0, hist[tid + kSel] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int i = tid; i < cnt; i += kSel) {
-        const uint32_t k = key(i);
+      auto count = [&](uint32_t k) {
         if (k != kAlways && ((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> shift) & digit], 1);
+      };
+#pragma unroll 4
+      for (int i = 4 * tid; i < held; i += 4 * kSel) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(keys + i);
+        count(k.x), count(k.y), count(k.z), count(k.w);
       }
+      for (int i = kSelKeys + tid; i < cnt; i += kSel) count(make(i));
       cl.sync();
       // bins in falling order: thread t sums bins 2047 - 2t and 2046 - 2t over the cluster
       int hi = 0, lo = 0;
@@ -142,36 +145,58 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
       __syncthreads();
     }
   }
-  // a thread's keys are a run of the CTA's; an odd length keeps the shared reads free of conflicts
-  const int per = ((cnt + kSel - 1) / kSel) | 1;
-  const int i0 = min(cnt, tid * per), i1 = min(cnt, i0 + per);
+  // Every warp's run of the CTA's slots, 32 at a time in their order: how many stay for their weight, how many tie, then the places.
+  const int lane = tid & 31, warp = tid >> 5, seg = (cnt + kSel - 1) / kSel * 32;
+  const int i0 = min(cnt, warp * seg), i1 = min(cnt, i0 + seg);
+  auto above = [&](uint32_t k) { return k == kAlways || k > prefix; };
+  auto equal = [&](uint32_t k) { return k == prefix && k != kAlways; };
   int more = 0, ties = 0;
-  for (int i = i0; i < i1; ++i) {
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t k = key(i);
-    more += (k == kAlways || (pick > 0 && k > prefix)) ? 1 : 0;
-    ties += (pick > 0 && k != kAlways && k == prefix) ? 1 : 0;
+    more += above(k) ? 1 : 0;
+    ties += equal(k) ? 1 : 0;
   }
-  int all_ties;
-  int tie = block_scan(ties, sums, &all_ties);
-  if (tid == 0) share[0] = all_ties;
+  more = __reduce_add_sync(kFull, more), ties = __reduce_add_sync(kFull, ties);
+  if (lane == 0) warp_more[warp] = more, warp_ties[warp] = ties;
+  __syncthreads();
+  auto scan = [&](int x) {  // inclusive, over the lanes: lane l holds warp l's number
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const int its = warp_ties[lane];
+  int tie = scan(its);
+  if (tid == 31) share[0] = tie;
   cl.sync();
+  tie -= its;
 #pragma unroll
   for (int r = 0; r < kMaxRanks; ++r) tie += r < rank ? *cl.map_shared_rank(&share[0], r) : 0;
-  const int won = max(0, min(ties, need - tie));  // of this thread's ties, the lowest slots
-  int all_kept;
-  int at = block_scan(more + (pick > 0 ? won : 0), sums, &all_kept);
-  if (tid == 0) share[1] = all_kept;
+  const int won = max(0, min(its, need - tie));  // of that warp's ties, the lowest slots
+  const int stays = warp_more[lane] + won;
+  int at = scan(stays);
+  if (tid == 31) share[1] = at;
   cl.sync();
+  at -= stays;
 #pragma unroll
   for (int r = 0; r < kMaxRanks; ++r) at += r < rank ? *cl.map_shared_rank(&share[1], r) : 0;
-  int left = pick > 0 ? won : 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    bool stay = k == kAlways || (pick > 0 && k > prefix);
-    if (!stay && pick > 0 && k == prefix && left > 0) stay = true, --left;
-    if (stay && at < a.keep) {
-      kept[at++] = s0 + i;
-    }
+  at = __shfl_sync(kFull, at, warp);
+  int left = __shfl_sync(kFull, won, warp);
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int base = i0; base < i1; base += 32) {
+    const int i = base + lane;
+    const uint32_t k = i < i1 ? key(i) : 0u;
+    const uint32_t tied = __ballot_sync(kFull, i < i1 && equal(k));
+    const bool stay = i < i1 && (above(k) || (equal(k) && __popc(tied & below) < left));
+    left = max(0, left - __popc(tied));
+    const uint32_t all = __ballot_sync(kFull, stay);
+    const int place = at + __popc(all & below);
+    if (stay && place < a.keep) kept[place] = s0 + i;
+    at += __popc(all);
   }
   const int me = rank * kSel + tid, everyone = ranks * kSel;
   for (int i = m + me; i < a.keep; i += everyone) kept[i] = -1;
@@ -260,7 +285,7 @@ int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream) {
   while (ranks < kMaxRanks && (a.src.capacity > (long long)kSelKeys * ranks ||
                                (a.src.capacity > 2048LL * ranks && 2 * ranks * bh <= (ranks == 4 ? num_sms / 2 : num_sms))))
     ranks *= 2;
-  const int held = (a.src.capacity + ranks - 1) / ranks;
+  const int held = ((a.src.capacity + ranks - 1) / ranks + 3) / 4 * 4;
   const size_t smem = sizeof(uint32_t) * (size_t)(held < kSelKeys ? held : kSelKeys);
   if (cudaFuncSetAttribute(q8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4) != cudaSuccess)
     return TQ_ERR_CUDA;
