@@ -4,16 +4,16 @@
 //
 // q8_select_kernel: weights map to unsigned keys of the same order (NaN lowest); the key of the last
 // token that stays is found digit by digit (11, 11 and 10 bits, from the top) with a histogram of the
-// keys that share the digits found so far; ties at that key go to the lowest slots, and one scan gives
-// every kept slot its place. Keys are read once from memory and stay in shared memory (what does not
+// keys that share the digits found so far; ties at that key go to the lowest slots, and the warps' runs of slots
+// are walked in order to give every kept one its place. Keys are read once from memory and stay in shared memory (what does not
 // fit is read again). A cluster of up to 8 CTAs shares one long sequence-head: each holds a run of
 // slots, histograms and counts are added through distributed shared memory.
-// Bound by its chain of passes and cluster barriers (8 heads of 131072 slots: 26 us, where reading the weights takes 1).
+// Bound by its chain of passes and cluster barriers (8 heads of 131072 slots: 25 us, where reading the weights takes 1).
 // q8_gather_kernel: one CTA per 64-token block of the target (or per few). A thread owns one 16-byte piece (16
 // coordinates of one token) of the keys and one of the values; the new block's scale comes from the largest value, and codes are rounded
 // only where their block's scale differs from it. Bound by memory: a kept token's pieces lie 16 bytes wide among its neighbours', so
 // that at one token in two kept three quarters of the source's sectors are read. 128 sequence-heads of 8192 slots cut to 4000:
-// 52 us for both caches' 227 MB, 4.4 TB/s, the ALU 65 % busy with rounding; with its selection 73 us.
+// 52 us for both caches' 227 MB, 4.4 TB/s, the ALU 65 % busy with rounding; with its selection 72 us.
 
 #include <cooperative_groups.h>
 

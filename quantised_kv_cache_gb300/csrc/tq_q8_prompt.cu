@@ -10,9 +10,9 @@
 // copies are issued by warps of their own: an issue waits while the tensor cores' queue is full.
 //
 // Bound by issue, then the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
-// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 304 us in
-// bf16 (792 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 356 us
-// in fp16; ALU 53 % and tensor cores 33 % busy, the rest the wait of each for the other. Capped 528 us, biased 458 us (three
+// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 300 us in
+// bf16 (802 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 352 us
+// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 528 us, biased 458 us (three
 // exponentials or reciprocals an element, the capped scores stored and read again). TERMS = 2 for bf16 (8 significant bits of
 // q and p, what a bf16 operand would hold), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
 // through fp16 pairs, in which the differences to the terms are exact.
