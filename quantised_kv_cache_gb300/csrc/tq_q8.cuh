@@ -55,11 +55,6 @@ __device__ __forceinline__ float2 e4m3x2_f(uint32_t b) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-__device__ __forceinline__ float2 e5m2x2_f(uint32_t b) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
 
 // Four e4m3 codes times 2^shift, rounded to e4m3 again.
 __device__ __forceinline__ uint32_t e4m3x4_scaled(uint32_t w, float f) {
@@ -103,12 +98,6 @@ __device__ __forceinline__ T to_type(float x) {
   if constexpr (sizeof(T) == 4) return x;
   else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float2bfloat16_rn(x);
   else return __float2half_rn(x);
-}
-template <typename T>
-__device__ __forceinline__ float from_type(T x) {
-  if constexpr (sizeof(T) == 4) return x;
-  else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __bfloat162float(x);
-  else return __half2float(x);
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[N]) {

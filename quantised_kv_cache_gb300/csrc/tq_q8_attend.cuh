@@ -62,10 +62,7 @@ __device__ __forceinline__ void settle() {
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&f)[N]) {
   uint32_t v[N];
-  if constexpr (N == 1) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(v[0]) : "r"(taddr) : "memory");
-  } else if constexpr (N == 4) {
+  if constexpr (N == 4) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(taddr) : "memory");
   } else if constexpr (N == 8) {
