@@ -34,8 +34,8 @@ constexpr int kConsumers = kWg * 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kEntries = 512;           // (sequence, row tile) pairs of a launch
 // Rows up to which this kernel takes a 16-bit call: one unit. 16 rows of one sequence over 16384 tokens, 8 KV heads: 40 us
-// here, 40 (bf16) or 47 (fp16) in the kernel for many rows, 148 against 176 or 214 in a batch of 8; 20 rows (two units, which
-// read the cache twice): 64 against 43 or 50, in a batch of 8 243 against 177 or 214.
+// here, 40 (bf16) or 47 (fp16) in the kernel for many rows, 148 against 120 or 169 in a batch of 8; 20 rows (two units, which
+// read the cache twice): 64 against 43 or 49, in a batch of 8 243 against 120 or 169. Up to 16 rows also keep 12 bits in both types.
 constexpr long long kFewRows = 16;
 constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, rounded l, pad
 

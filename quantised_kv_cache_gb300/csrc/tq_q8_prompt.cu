@@ -20,7 +20,8 @@
 // Two blocks of a tile share one value sum, the smaller scale folded into its probabilities; where the scales are more than
 // 2^4 apart that would cost precision, and the blocks' sums are formed one after the other.
 // Work split: as in the kernel for few rows, equal slices of the (sequence, 256 rows, head, tile) space, a unit's start counted
-// as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first.
+// as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first. Up to 128 rows over many tiles
+// are units of one row tile: the two row tiles of a CTA then work on slices of their own (APART).
 
 #include "tq_q8_rows.cuh"
 
@@ -28,17 +29,18 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kUnit = 256;             // rows of a unit: two row tiles
+// Rows of a unit: two row tiles, or, APART, one: then the two row tiles of a CTA hold units of their own, with half of the ring each.
+constexpr int unit_rows(bool apart) { return apart ? 128 : 256; }
 constexpr int kSoft = 512;              // softmax threads; then a warpgroup of controllers:
-constexpr int kThreads = kSoft + 128;   // warps 16 and 17 issue a row tile's MMAs each, warp 18 the copies, warp 19 nothing
+constexpr int kThreads = kSoft + 128;   // warps 16 and 17 issue a row tile's MMAs each, warp 18 the copies, warp 19 nothing (APART: the second row tile's)
 constexpr int kRegsSoft = 112, kRegsControl = 32;  // 512 * 112 + 128 * 32 = 640 * 96, what the block is launched with
 constexpr int kStage = 2 * kTile * kD;
 constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
-constexpr int kPart = kUnit * (kD + 2);  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
+constexpr int part_of(int unit) { return unit * (kD + 2); }  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
 // Capped or biased scores run without turns (measured at 2048 of 8192 tokens: 653 us, 713 with them).
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
 
-constexpr int stages_of(int terms) { return terms == 2 ? 4 : 3; }
+constexpr int stages_of(int terms, bool apart) { return terms == 2 || apart ? 4 : 3; }
 
 struct Entry {
   int lo, hi;          // first tile, one past the last visible slot
@@ -52,11 +54,11 @@ struct Cut {
 struct Plan {
   int *pre;       // [entries + 1] tiles (of one head) before each entry
   int *starts;    // [entries + 1] entries with tiles before each
-  long long *cut; // [CTAs + 1] where the slices of the tiles begin
+  long long *cut; // [slices + 1] where the slices of the tiles begin (APART: two a CTA, else one)
   Entry *entry;   // [entries]
-  Cut *cuts;      // [CTAs]
-  float *parts;   // [CTAs][2][kPart]
-  int entries, pairs;
+  Cut *cuts;      // [slices]
+  float *parts;   // [slices][2] records
+  int entries, pairs, unit;  // pairs: units of a sequence (and head); unit: their rows
 };
 
 // One warp per entry (sequence, 256 rows).
@@ -64,10 +66,10 @@ __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   pdl_wait();
   if (e >= p.entries) return;
-  const int b = e / p.pairs, r0 = (e % p.pairs) * kUnit, G = a.group, R = G * a.n_q;
+  const int b = e / p.pairs, r0 = (e % p.pairs) * p.unit, G = a.group, R = G * a.n_q;
   int len, m;
   seq_sizes(a, b, &len, &m, lane == 0);
-  const int i0 = r0 / G, i1 = min(m - 1, (min(R, r0 + kUnit) - 1) / G);
+  const int i0 = r0 / G, i1 = min(m - 1, (min(R, r0 + p.unit) - 1) / G);
   int lo = 0x7fffffff, hi = 0, maxbeg = 0, minend = 0x7fffffff;
   for (int i = i0 + lane; i <= i1; i += 32) {
     const int2 r = row_range(a, b, i, len, m);
@@ -226,17 +228,18 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-template <int TERMS, bool EXTRA>
+template <int TERMS, bool EXTRA, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
-  constexpr int kStages = stages_of(TERMS);
+  constexpr int kStages = stages_of(TERMS, APART), kUnit = unit_rows(APART);
+  constexpr bool kTurns = !EXTRA && !APART;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
   uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage;  // [row tile][term][128 x 128]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 2);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], APART ? 1 : 2);
     for (int r = 0; r < 2; ++r) {
       mbar_init(&sm.bar_s[r], 1), mbar_init(&sm.bar_o[r], 1);
       mbar_init(&sm.bar_q[r], 8), mbar_init(&sm.bar_p[r], 8);  // a row tile's warps
@@ -254,7 +257,12 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   const uint32_t tmem = sm.tmem;
   pdl_wait();
 
-  const long long g0 = p.cut[blockIdx.x], g1 = p.cut[blockIdx.x + 1];
+  // the row tile that a warp belongs to (0 for the copies of both), its slice, and the ring's stage and its phase for the slice's tile `it`
+  const int rt = warp < kSoft / 32 ? warp >> 3 : APART || warp < kSoft / 32 + 2 ? warp & 1 : 0;
+  const int slice = APART ? rt * gridDim.x + blockIdx.x : blockIdx.x, slices = APART ? 2 * gridDim.x : gridDim.x;
+  auto stage = [&](int it) { return APART ? 2 * rt + (it & 1) : it % kStages; };
+  auto turn = [&](int it) { return (uint32_t)(APART ? it >> 1 : it / kStages) & 1; };
+  const long long g0 = p.cut[slice], g1 = p.cut[slice + 1];
   const bool idle = g0 >= g1;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
@@ -266,7 +274,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 
   if (warp >= kSoft / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == kSoft / 32 + 2) {
+    if (warp == kSoft / 32 + 2 || (APART && warp == kSoft / 32 + 3)) {
       // ================================ copies: a lane finds the sources of one of a unit's next 32 tiles
       int it = 0;
       for (long long g = g0; g < g1;) {
@@ -292,14 +300,14 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             }
           }
           for (int k = 0; k < todo; ++k, ++it) {
-            const int s = it % kStages;
+            const int s = stage(it);
             const long long s0 = __shfl_sync(kFull, src[0], k), s1 = __shfl_sync(kFull, src[1], k);
             const int n0 = __shfl_sync(kFull, bytes[0], k), n1 = __shfl_sync(kFull, bytes[1], k);
             float4 x;
             x.x = __shfl_sync(kFull, f.x, k), x.y = __shfl_sync(kFull, f.y, k);
             x.z = __shfl_sync(kFull, f.z, k), x.w = __shfl_sync(kFull, f.w, k);
             if (lane == 0) {
-              wait(&sm.empty[s], ((it / kStages) & 1) ^ 1);
+              wait(&sm.empty[s], turn(it) ^ 1);
               if (!*(volatile int *)&sm.bad) {
                 sm.info[s] = x;
                 uint8_t *dst = ring + s * kStage;
@@ -323,14 +331,13 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       }
       // every copy lands before the CTA's shared memory goes: the last fill of each stage
       if (lane == 0)
-        for (int k = max(0, it - kStages); k < it; ++k)
-          mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1, nullptr, kWaitBudgetNs / 8);
+        for (int k = max(0, it - (APART ? 2 : kStages)); k < it; ++k)
+          mbar_wait_bounded(&sm.full[stage(k)], turn(k), nullptr, kWaitBudgetNs / 8);
       __syncwarp();
     } else if (warp < kSoft / 32 + 2) {
       // ================================ a row tile's MMAs
       {
         const bool issue = elect_lane();
-        const int rt = warp - kSoft / 32;
         const uint32_t t_s = warp_uniform(tmem + rt * 256), t_o = t_s + 128, q = warp_uniform(smem_u32(qbuf + rt * TERMS * kQTerm));
         uint32_t units = 0, probs = 0;
         int it = 0;
@@ -341,7 +348,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           for (int j = 0; j <= todo; ++j) {
             // the value sums of tile j - 1, then the scores of tile j over its probabilities: in this order, as issued
             if (j > 0) {
-              const int s = (it + j - 1) % kStages, n = min(kTile, max(0, hi - (first + j - 1) * kTile));
+              const int s = stage(it + j - 1), n = min(kTile, max(0, hi - (first + j - 1) * kTile));
               const float4 f = sm.info[s];
               const bool apart = scales_apart(f), whole = n == kTile && f.z >= 0.f && f.w >= 0.f && !apart;
               const uint32_t vt = warp_uniform(smem_u32(ring + s * kStage) + kTile * kD);
@@ -376,8 +383,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               }
             }
             if (j < todo) {
-              const int s = (it + j) % kStages;
-              wait(&sm.full[s], ((it + j) / kStages) & 1);
+              const int s = stage(it + j);
+              wait(&sm.full[s], turn(it + j));
               tc_fence_after_sync();
               const uint32_t kt = warp_uniform(smem_u32(ring + s * kStage));
 #pragma unroll
@@ -399,11 +406,11 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   } else {
     // ================================ softmax and output: two threads a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int rt = tid >> 8, half = (tid >> 7) & 1, lrow = tid & 127;
+    const int half = (tid >> 7) & 1, lrow = tid & 127, in_unit = (APART ? 0 : rt * 128) + lrow;
     const uint32_t t_s = tmem + rt * 256 + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half, t_o = t_s + 128;
     const ScoreCap sc = EXTRA ? score_cap(a.scale, a.softcap) : ScoreCap{};
     int it = 0;  // tiles done: stages and phases count on
-    if (!EXTRA && rt == 1 && g0 < g1) turn_pass(rt);
+    if (kTurns && rt == 1 && g0 < g1) turn_pass(rt);
     uint32_t sums = 0;
     long long g = g0;
     while (g < g1) {
@@ -420,7 +427,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 #pragma unroll 1
       for (int k0 = 0; k0 < 16; k0 += 8) {
         uint2 raw[8];
-        const int first_row = u.pair * kUnit + rt * 128 + (warp & 7) * 16 + k0;
+        const int first_row = u.pair * kUnit + (APART ? 0 : rt * 128) + (warp & 7) * 16 + k0;
         load_rows(a, u.b, u.h, m, first_row, lane, raw);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -440,7 +447,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       if (lane == 0) mbar_arrive(&sm.bar_q[rt]);
       bar_rt(rt);
       const float qs = sm.top[rt][0][lrow];
-      const int row = u.pair * kUnit + rt * 128 + lrow, qi = row / G, hq = u.h * G + row % G;
+      const int row = u.pair * kUnit + in_unit, qi = row / G, hq = u.h * G + row % G;
       const bool live = row < R && qi < m;
       const int2 rg = live ? row_range(a, u.b, qi, len, m) : make_int2(0, 0);
       const float slope = EXTRA && live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
@@ -453,8 +460,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       float mx = -INFINITY, l = 0.f;
       const int todo = (int)(u.end - g);
       for (int j = 0; j < todo; ++j) {
-        const int s = (it + j) % kStages, tok0 = (first + j) * kTile, n = min(kTile, max(0, hi - tok0));
-        wait(&sm.full[s], ((it + j) / kStages) & 1);
+        const int s = stage(it + j), tok0 = (first + j) * kTile, n = min(kTile, max(0, hi - tok0));
+        wait(&sm.full[s], turn(it + j));
         const float4 f = sm.info[s];
         const float ks = half ? f.y : f.x;
         const bool masked = !(maxbeg <= tok0 && minend >= tok0 + kTile) || f.x < 0.f || f.y < 0.f;
@@ -476,7 +483,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         wait(&sm.bar_s[rt], (it + j) & 1);
         __syncwarp();  // tensor memory is read by whole warps
         tc_fence_after_sync();
-        if constexpr (!EXTRA) turn_take(rt);
+        if constexpr (kTurns) turn_take(rt);
         // ---- the row's maximum over this half
         float top = -INFINITY;
         auto maximum = [&](auto mask) {
@@ -610,7 +617,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           }
           fence_proxy_async_shared();
         }
-        if constexpr (!EXTRA) {
+        if constexpr (kTurns) {
           if (rt == 0 || u.end < g1 || j + 1 < todo) turn_pass(rt);
         }
         tmem_st_wait();
@@ -663,26 +670,26 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           }
           if (a.lse && !half) a.lse[((long long)u.b * a.heads_q + hq) * a.n_q + qi] = (mx + log2f(l) - 8.f) * kLn2;
         } else {
-          float *part = p.parts + ((long long)blockIdx.x * 2 + (u.t0 == 0 ? 1 : 0)) * kPart;
-          const int r = rt * 128 + lrow;
+          float *part = p.parts + ((long long)slice * 2 + (u.t0 == 0 ? 1 : 0)) * part_of(kUnit);
+          const int r = in_unit;
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             reinterpret_cast<float4 *>(part)[(16 * half + q) * kUnit + r] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           if (!half) part[kUnit * kD + r] = mx, part[kUnit * (kD + 1) + r] = l;
         }
       }
-      if (tid == 0 && u.end == g1) {
+      if ((APART ? (tid & 255) == 0 : tid == 0) && u.end == g1) {
         const long long stop = g - u.t0 + u.cnt;
         int parts = 0;
         if (u.t0 == 0 && stop > g1) {
           parts = 1;
-          for (int k = blockIdx.x + 1; k < (int)gridDim.x && p.cut[k] < stop; ++k) ++parts;
+          for (int k = slice + 1; k < slices && p.cut[k] < stop; ++k) ++parts;
         }
-        p.cuts[blockIdx.x] = Cut{u.b, u.pair, u.h, parts};
+        p.cuts[slice] = Cut{u.b, u.pair, u.h, parts};
       }
       g = u.end;
     }
-    if (tid == 0 && idle) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0};
+    if ((APART ? (tid & 255) == 0 : tid == 0) && idle) p.cuts[slice] = Cut{0, 0, 0, 0};
   }
   if (*(volatile int *)&sm.bad) settle();
   tc_fence_before_sync();
@@ -693,7 +700,9 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
 
 // The rows of a unit that was cut: lane = row, a warp per kJoin times 4 coordinates; 32 rows a CTA.
 constexpr int kJoin = 2;  // (2048 of 8192 tokens: 303 us with 1, 299.5 with 2 or 4; 64 rows of 16384 tokens, joined of 18 parts: 44, 44, 47)
+template <bool APART>
 __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
+  constexpr int kUnit = unit_rows(APART);
   pdl_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts < 2) return;
@@ -702,13 +711,14 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   seq_sizes(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (row >= G * a.n_q || i >= m) return;
-  auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kPart; };
+  auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * part_of(kUnit); };
   float top = -INFINITY;
+#pragma unroll 8
   for (int k = 0; k < cut.parts; ++k) top = fmaxf(top, rec(k)[kUnit * kD + r]);
   float o[kJoin][4], l = 0.f;
 #pragma unroll
   for (int j = 0; j < kJoin; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int k = 0; k < cut.parts; ++k) {
     const float *x = rec(k);
     const float mk = x[kUnit * kD + r], f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
@@ -732,39 +742,56 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   if (a.lse && col == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
 }
 
-template <int TERMS, bool EXTRA>
+template <int TERMS, bool EXTRA, bool APART>
 int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
-  constexpr int smem = stages_of(TERMS) * kStage + 2 * TERMS * kQTerm;
-  if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  constexpr int smem = stages_of(TERMS, APART) * kStage + 2 * TERMS * kQTerm;
+  const int slices = APART ? 2 * num_sms : num_sms;
+  if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
   cudaError_t e = launch_overlapped(true, q8_entries_kernel, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p, a.heads_kv, num_sms);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_join_kernel, dim3(num_sms, kUnit / 32), dim3(1024 / kJoin), 0, st, a, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p, a.heads_kv, slices);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA, APART>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
+  if (e == cudaSuccess)
+    e = launch_overlapped(true, q8_prompt_join_kernel<APART>, dim3(slices, unit_rows(APART) / 32), dim3(1024 / kJoin), 0, st, a, p);
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+// Up to 128 rows are one row tile, and the other of a shared unit would have no rows: with units apart every row tile works, but twice as
+// many slices are joined and each has half of the ring. So where a CTA has a dozen tiles. 64 rows, 8 KV heads, bf16 (fp16): 8 sequences of
+// 16384 tokens (54 tiles a CTA) 121 us apart, 165 us (170, 198) not, capped 178 and 284; 2 of them (13) 59 and 63 (73, 73); one (7) 49 and 45.
+bool units_apart(const Q8AttnArgs &a, int num_sms) {
+  const long long tiles = (long long)a.batch * a.heads_kv * ((a.max_len + kTile - 1) / kTile);
+  return (long long)a.group * a.n_q <= unit_rows(true) && tiles >= 12LL * num_sms;
+}
+template <int TERMS, bool EXTRA>
+int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
+  return p.unit == unit_rows(true) ? launch<TERMS, EXTRA, true>(a, p, num_sms, st) : launch<TERMS, EXTRA, false>(a, p, num_sms, st);
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
+// Enough for either kind of units.
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q) {
-  const size_t pairs = ((size_t)group * n_q + kUnit - 1) / kUnit, entries = pairs * batch;
-  return 2 * round16((entries + 1) * sizeof(int)) + round16((size_t)(num_sms + 1) * sizeof(long long)) + entries * sizeof(Entry) + round16((size_t)num_sms * sizeof(Cut)) +
-         (size_t)num_sms * 2 * kPart * sizeof(float);
+  const size_t entries = ((size_t)group * n_q + unit_rows(false) - 1) / unit_rows(false) * batch, slices = 2 * (size_t)num_sms;
+  return 2 * round16((entries + 1) * sizeof(int)) + round16((slices + 1) * sizeof(long long)) + entries * sizeof(Entry) +
+         round16(slices * sizeof(Cut)) + slices * 2 * part_of(unit_rows(true)) * sizeof(float);
 }
 
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream) {
-  const long long pairs = ((long long)a.group * a.n_q + kUnit - 1) / kUnit, entries = pairs * a.batch;
+  const bool apart = units_apart(a, num_sms);
+  const long long unit = unit_rows(apart), pairs = ((long long)a.group * a.n_q + unit - 1) / unit, entries = pairs * a.batch;
+  const int slices = apart ? 2 * num_sms : num_sms;
   if (entries > 1 << 24) return TQ_ERR_UNSUPPORTED;
   Plan p;
-  p.entries = (int)entries, p.pairs = (int)pairs;
+  p.entries = (int)entries, p.pairs = (int)pairs, p.unit = (int)unit;
   char *w = (char *)workspace;
   p.pre = (int *)w, w += round16((size_t)(entries + 1) * sizeof(int));
   p.starts = (int *)w, w += round16((size_t)(entries + 1) * sizeof(int));
-  p.cut = (long long *)w, w += round16((size_t)(num_sms + 1) * sizeof(long long));
+  p.cut = (long long *)w, w += round16((size_t)(slices + 1) * sizeof(long long));
   p.entry = (Entry *)w, w += (size_t)entries * sizeof(Entry);
-  p.cuts = (Cut *)w, w += round16((size_t)num_sms * sizeof(Cut));
+  p.cuts = (Cut *)w, w += round16((size_t)slices * sizeof(Cut));
   p.parts = (float *)w;
   cudaStream_t st = (cudaStream_t)stream;
   const bool extra = a.softcap != 0.f || a.slopes != nullptr || !(a.scale > 0.f);

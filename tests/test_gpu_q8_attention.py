@@ -170,6 +170,31 @@ PROMPTS = [  # B, heads_q, heads_kv, n_q, lens
 ]
 
 
+@pytest.mark.parametrize("case", [(4, 16, 8, 10, [700, 0, 1, 129], 7500), (4, 8, 8, 128, [300, 128, 1000, 131], 7500), (2, 64, 8, 8, [900, 65], 14720),
+                                  (1, 40, 8, 5, [29000], 30000), (30, 18, 1, 1, [64 * i for i in range(30)], 8000)],
+                         ids=lambda c: "-".join(map(str, c[:4])) + f"-{max(c[4])}")
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("extra", ["plain", "masked capped biased paged"])
+def test_rows_of_one_tile_over_many_slots(ctx, case, dtype, extra):
+    """Enough slots for two units a CTA at once, each with half of the ring: mostly beyond the sequences, or really long."""
+    B, Hq, H, n, lens, cap = case
+    assert 16 < Hq // H * n <= 128 and B * H * -(-cap // 128) >= 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    cache, k, v = make(ctx, B, H, cap, lens, seed=sum(lens), paged=extra != "plain", poison=False)
+    q = queries(5, B, Hq, n, dtype, "tokens")
+    kw, ck, new = {}, {}, [min(n, L) for L in lens]
+    if extra != "plain":
+        rng = np.random.default_rng(n)
+        ck = dict(begin=rng.integers(-5, 100, (B, n)), end=rng.integers(0, 2 * max(lens), (B, n)), softcap=15.0)
+        slopes = torch.linspace(0.01, 0.2, Hq, device=DEV)
+        kw = dict(key_begin=ints(ck["begin"]), key_end=ints(ck["end"]), softcap=15.0, slopes=slopes)
+        ck["slopes"] = slopes.double().cpu().numpy()
+    lse, out = torch.zeros(B, Hq, n, device=DEV), torch.full_like(q, 77.0)
+    got = tq.tq_q8_attention(ctx.handle, cache, q, ints(lens), cap, new_lens=ints(new), lse=lse, out=out, **kw)
+    check(np64(got), np64(q), k, v, lens, new, dtype=dtype, out_dtype=dtype, lse=np64(lse), **ck)
+    for b in range(B):
+        assert bool((got[b, :, new[b]:] == 77).all())
+
+
 @pytest.mark.parametrize("case", PROMPTS, ids=lambda c: "-".join(map(str, c[:4])) + f"-{max(c[4])}")
 @pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, HF), (F32, F32)])
 def test_prompts(ctx, case, dtype, out):
@@ -604,7 +629,7 @@ def test_back_to_back_weights_give_the_same_bits(ctx, B, Hq, H, n, N):
         assert int(bad) == 0
 
 
-@pytest.mark.parametrize("B,Hq,H,n,N", [(8, 32, 32, 1, 4096), (2, 32, 8, 1, 20000), (1, 16, 8, 300, 5000)])
+@pytest.mark.parametrize("B,Hq,H,n,N", [(8, 32, 32, 1, 4096), (2, 32, 8, 1, 20000), (1, 16, 8, 300, 5000), (8, 32, 8, 8, 4000)])
 def test_back_to_back_calls_give_the_same_bits(ctx, B, Hq, H, n, N):
     """Many calls without a pause between them: tiles' copies land in any order, CTAs follow one another on an SM."""
     cache = tq.Cache(ctx, B, H, N, device=DEV)
