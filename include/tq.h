@@ -583,10 +583,14 @@ typedef struct tq_q8_attn {
  * sizes (weights: 1 when d_weights is set), no initial contents required. A d_seq_lens[b] outside [0, max_len] or a d_new_lens[b]
  * outside [0, n_q] is cut to that range, and a bad block-table entry's tokens are
  * taken as unseen; both set the device error word to TQ_ERR_ARG. Rounding: the
- * products of codes with 16-bit queries are exact, their sums fp32; the
- * probabilities enter the value sums with 24 significant bits when out_dtype is
- * TQ_F32, else with 12 for up to 16 query rows (n_q x group) per KV head and, beyond, with 11 for TQ_F16 and
- * 8 for TQ_BF16 (whose queries then lose coordinates below 2^-17 of a row's largest); the
+ * products of codes with 16-bit queries are exact, their sums fp32. A probability
+ * enters the value sums with 24 significant bits when out_dtype is TQ_F32, else with 12
+ * for up to 16 query rows (n_q x group) per KV head; one below 2^-8 (2^-20) of the row's
+ * largest so far is within 2^-32 of that one instead. Beyond 16 rows it has 11 bits for
+ * TQ_F16 and 8 for TQ_BF16 (whose queries then lose coordinates below 2^-17 of a row's
+ * largest); one below 2^-14 (2^-10) of the row's largest among the same 128 slots is within
+ * 2^-25 (2^-18) of that one, 2^4 times as much at most where the two 64-slot blocks' value scales differ: together
+ * below 2^-15 (2^-8) of the 128 slots' own probability. The
  * softmax's sum is fp32 throughout. */
 tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
                                     int weights, size_t *out);

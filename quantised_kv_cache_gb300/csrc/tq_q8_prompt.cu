@@ -10,15 +10,18 @@
 // copies are issued by warps of their own: an issue waits while the tensor cores' queue is full.
 //
 // Bound by issue, then the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
-// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 300 us in
-// bf16 (802 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 352 us
+// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 302 us in
+// bf16 (798 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 352 us
 // in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 528 us, biased 458 us (three
 // exponentials or reciprocals an element, the capped scores stored and read again). TERMS = 2 for bf16 (8 significant bits of
 // q and p, what a bf16 operand would hold), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
 // through fp16 pairs, in which the differences to the terms are exact.
 //
 // Two blocks of a tile share one value sum, the smaller scale folded into its probabilities; where the scales are more than
-// 2^4 apart that would cost precision, and the blocks' sums are formed one after the other.
+// 2^4 apart that would cost precision, and the blocks' sums are formed one after the other. The terms of a probability end at a fixed
+// step (2^-17 of 2^8 for two of them), so it is relative to the row's largest of its own sum, not to the running maximum: the smaller ones of a
+// tile after a heavy key keep their bits, and what a tile's terms drop is below 2^-8 of its own mass. The way to the running maximum is a factor of the
+// whole sum, formed while the tensor cores work (302 us where the running maximum as the reference takes 297).
 // Work split: as in the kernel for few rows, equal slices of the (sequence, 256 rows, head, tile) space, a unit's start counted
 // as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first. Up to 128 rows over many tiles
 // are units of one row tile: the two row tiles of a CTA then work on slices of their own (APART).
@@ -39,6 +42,7 @@ constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
 constexpr int part_of(int unit) { return unit * (kD + 2); }  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
 // Capped or biased scores run without turns (measured at 2048 of 8192 tokens: 653 us, 713 with them).
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
+constexpr float kLowest = -3e38f;      // in place of a maximum of -inf: an unseen score stays -inf beside it, its factor is 0
 
 constexpr int stages_of(int terms, bool apart) { return terms == 2 || apart ? 4 : 3; }
 
@@ -542,17 +546,16 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         if constexpr (!EXTRA) top = top == -INFINITY ? top : top * c;
         sm.top[rt][half][lrow] = top;
         bar_rt(rt);
-        top = fmaxf(fmaxf(top, sm.top[rt][half ^ 1][lrow]), mx);
-        const float use = top == -INFINITY ? 0.f : top;
-        const float corr = ex2_approx(mx - use);
-        mx = top;
-        // ---- the two blocks' value scales: folded into the probabilities, or two sums
+        const float other = sm.top[rt][half ^ 1][lrow];
+        // ---- the two blocks' value scales, in log2: the smaller is folded into its block's probabilities (`fold` for this block, `fold1`
+        // for the other), or each block has a sum of its own. Probabilities are relative to the row's largest (folded) one of their sum
         const bool apart = scales_apart(f);
-        const float vmax = fmaxf(fmaxf(f.z, f.w), 0.f);
-        float fold = 1.f;
-        if (f.z >= 0.f && f.w >= 0.f && !apart)
-          fold = __int_as_float((127 << 23) + __float_as_int(half ? f.w : f.z) - __float_as_int(vmax));
-        const float shift = 8.f - use + (float)log2i(fold);
+        float fold = 0.f, fold1 = apart ? -INFINITY : 0.f;
+        if (f.z != f.w && f.z >= 0.f && f.w >= 0.f && !apart) {
+          const float d = (float)(log2i(half ? f.w : f.z) - log2i(half ? f.z : f.w));
+          fold = fminf(d, 0.f), fold1 = fminf(-d, 0.f);
+        }
+        const float shift = 8.f + fold - fmaxf(fmaxf(top + fold, other + fold1), kLowest);
         // ---- probabilities times 2^8, their terms over the scores they come from, their sum
         float2 sum = make_float2(0.f, 0.f);
         auto probabilities = [&](auto mask) {
@@ -606,7 +609,6 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         };
         if (masked) probabilities(std::true_type{});
         else probabilities(std::false_type{});
-        l = fmaf(l, corr, (sum.x + sum.y) / fold);
         // value rows past the copied tokens, up to a whole K-step, hold what the cache holds there
         if (n & 31) {
           const int t = n + (tid & 255);
@@ -621,13 +623,14 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           if (rt == 0 || u.end < g1 || j + 1 < todo) turn_pass(rt);
         }
         tmem_st_wait();
-        // O = O corr + vs D
-        auto add = [&](float vs, float by) {
-          if (!__all_sync(kFull, by == 1.f)) {
+        // O = O corr + vs by D
+        auto add = [&](float vs, float by, float corr) {
+          if (!__all_sync(kFull, corr == 1.f)) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) o[i] *= by;
+            for (int i = 0; i < 64; ++i) o[i] *= corr;
           }
-          if (vs < 0.f) return;
+          if (!__any_sync(kFull, vs >= 0.f)) return;  // (a vote, which the compiler knows to be the warp's: 305 us where a comparison took 311)
+          vs *= by;
           uint32_t d[2][16];
           tmem_ld_start(t_o, d[0]);
 #pragma unroll
@@ -638,15 +641,26 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             for (int i = 0; i < 16; ++i) o[16 * q + i] = fmaf(__uint_as_float(d[q & 1][i]), vs, o[16 * q + i]);
           }
         };
-        for (int part = 0; part <= (int)apart; ++part) {
+        float corr = 1.f, by = 1.f, use = 0.f;
+        for (int blk = 0; blk <= (int)apart; ++blk) {
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.bar_p[rt]);
+          if (blk == 0) {  // while the sum is formed: from the probabilities' reference to the running maximum
+            const float run = fmaxf(fmaxf(top, other), mx);
+            use = fmaxf(run, kLowest);
+            corr = ex2_approx(mx - use), by = ex2_approx(8.f - shift - use);
+            mx = run;
+            l = fmaf(l, corr, (sum.x + sum.y) * by);
+          }
           wait(&sm.bar_o[rt], sums & 1);
           ++sums;
           __syncwarp();
           tc_fence_after_sync();
-          add(!apart ? (f.z < 0.f && f.w < 0.f ? -1.f : vmax) : part ? f.w : f.z, part ? 1.f : corr);
+          // this block's scale and factor, which have the same product as the other's where one is folded
+          const float mine = half ? f.w : f.z, its = half ? f.z : f.w;
+          const bool swap = apart ? blk != half : mine < 0.f;
+          add(swap ? its : mine, apart && swap ? ex2_approx(other - use) : by, blk ? 1.f : corr);
         }
       }
       it += todo;
