@@ -564,7 +564,7 @@ typedef struct tq_q8_attn {
   const int32_t *d_new_lens;    /* [batch] or NULL (n_q): query tokens of each sequence; later rows are not written */
   /* t = scale q.k, then softcap tanh(t / softcap), then t - slope |q position - k position| */
   float scale;                  /* 0: 1 / sqrt(d) */
-  float softcap;                /* 0: none */
+  float softcap;                /* 0 (or 2^40 and above): none; at least 2^-60 */
   const float *d_slopes;        /* [heads_q] or NULL */
   const int32_t *d_q_positions; /* [batch][n_q], or NULL: query i is at its slot d_seq_lens[b] - new + i */
   const int32_t *d_k_positions; /* [batch][heads_kv][capacity], or NULL: a key is at its slot */
@@ -590,7 +590,8 @@ typedef struct tq_q8_attn {
  * TQ_F16 and 8 for TQ_BF16 (whose queries then lose coordinates below 2^-17 of a row's
  * largest); one below 2^-14 (2^-10) of the row's largest among the same 128 slots is within
  * 2^-25 (2^-18) of that one, 2^4 times as much at most where the two 64-slot blocks' value scales differ: together
- * below 2^-15 (2^-8) of the 128 slots' own probability. The
+ * below 2^-15 (2^-8) of the 128 slots' own probability. A capped score is within 2^-21 of the cap there, and
+ * within 2^-19 of itself where the cap is above 128. The
  * softmax's sum is fp32 throughout. */
 tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
                                     int weights, size_t *out);

@@ -129,7 +129,7 @@ __device__ __forceinline__ float q8_score_log2(float qk, const Q8Score &s) {
   return x * kLog2e;
 }
 
-// scale (times a row's and a block's) x, capped, in log2 units: cap tanh(y) with tanh = 1 - 2 / (1 + e^2y), off by a few 2^-24 of the
+// scale (times a row's and a block's) x, capped, in log2 units: cap tanh(y) with tanh = 1 - 2 / (1 + e^2y), off by less than 2^-21 of the
 // cap; an infinite e^2y gives 1, a zero one -1. `in` and `cap` from score_cap.
 struct ScoreCap {
   float in, cap;  // cap 0: none
@@ -142,9 +142,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// x times c, which holds in
+// x times c, which holds in. LONG, for caps above kShortCap, where a few 2^-24 of the cap would show: below |y| = 1/4 the Taylor series of
+// tanh (the next term is below 2^-26 of it), so that a score is off by less than 2^-19 of itself.
+constexpr float kShortCap = 128.f;
+// What kernels for many rows do to scores (a kernel each: where one branched on the cap, caps below took 2 % longer): nothing, a cap or a
+// bias, a cap above kShortCap (and perhaps a bias).
+enum Extra { kPlain = 0, kCapOrBias = 1, kLongCaps = 2 };
+template <bool LONG>
 __device__ __forceinline__ float capped_log2(float x, float c, float cap) {
-  return cap == 0.f ? x * c : fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(x * c)), cap);
+  const float u = x * c;
+  if (!LONG && cap == 0.f) return u;
+  const float far = fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(u)), cap);
+  if (!LONG) return far;
+  const float y = u * (0.5f * kLn2), z = y * y;
+  float s = fmaf(z, 2.1869489e-2f, -5.3968254e-2f);
+  s = fmaf(z, s, 1.3333333e-1f);
+  s = fmaf(z, s, -3.3333333e-1f);
+  return fabsf(y) < 0.25f ? cap * fmaf(y * z, s, y) : far;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {

@@ -37,6 +37,10 @@ tq_status on_device(const tq_ctx *ctx) {
   return cur == ctx->device ? TQ_OK : TQ_ERR_ARG;
 }
 
+// Caps of scores: from kNoCap on cap tanh(t / cap) is t to its last bit below 2^28; a smaller one than kLeastCap has no reciprocal
+// beside a large scale.
+constexpr float kNoCap = 1099511627776.f, kLeastCap = 8.6736174e-19f;  // 2^40, 2^-60
+
 // [p, p + n) and [q, q + m) share a byte
 bool overlap(const void *p, size_t n, const void *q, size_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
@@ -153,7 +157,8 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (p->batch <= 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->heads_q % p->heads_kv || p->n_q <= 0 || p->max_len <= 0)
     return TQ_ERR_ARG;
   if (!known(p->q_dtype) || (p->out_dtype != p->q_dtype && p->out_dtype != TQ_F32)) return TQ_ERR_ARG;
-  if (!std::isfinite(p->scale) || !std::isfinite(p->softcap) || p->softcap < 0.f) return TQ_ERR_ARG;
+  if (!std::isfinite(p->scale) || !std::isfinite(p->softcap)) return TQ_ERR_ARG;
+  if (p->softcap != 0.f && !(p->softcap >= kLeastCap)) return TQ_ERR_ARG;  // (negative ones among them)
   if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
   if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
   if (p->d_out == p->d_q) return TQ_ERR_ARG;  // the weights read the queries again after the results are written
@@ -176,7 +181,7 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   a.q = p->d_q, a.out = p->d_out, a.qs = strides(p->q_strides), a.os = strides(p->out_strides);
   a.seq_lens = p->d_seq_lens, a.new_lens = p->d_new_lens;
   a.scale = p->scale != 0.f ? p->scale : 0.08838834764831845f;  // 1 / sqrt(128)
-  a.softcap = p->softcap, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
+  a.softcap = p->softcap < kNoCap ? p->softcap : 0.f, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
   a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
   a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
   a.error = &ctx->dparams->error;

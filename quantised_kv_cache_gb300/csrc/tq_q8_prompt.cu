@@ -13,8 +13,8 @@
 // product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 302 us in
 // bf16 (798 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 352 us
 // in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 528 us, biased 458 us (three
-// exponentials or reciprocals an element, the capped scores stored and read again). TERMS = 2 for bf16 (8 significant bits of
-// q and p, what a bf16 operand would hold), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
+// exponentials or reciprocals an element, the capped scores stored and read again; caps above 128, whose small scores go through a series, 589 us). TERMS = 2 for bf16 (8 significant bits of
+// q and p, down to 2^-18 of the largest of either), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
 // through fp16 pairs, in which the differences to the terms are exact.
 //
 // Two blocks of a tile share one value sum, the smaller scale folded into its probabilities; where the scales are more than
@@ -232,7 +232,7 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-template <int TERMS, bool EXTRA, bool APART>
+template <int TERMS, int EXTRA, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   constexpr int kStages = stages_of(TERMS, APART), kUnit = unit_rows(APART);
@@ -504,7 +504,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
                 for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * c;
               } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = capped_log2(__uint_as_float(w[i]), c, sc.cap);
+                for (int i = 0; i < 16; ++i) x[i] = capped_log2<EXTRA == kLongCaps>(__uint_as_float(w[i]), c, sc.cap);
               }
               if (a.kpos && a.slopes) {
                 const int32_t *kp = a.kpos + bh * a.c.capacity + slot0 + 16 * q;
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   if (a.lse && col == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
 }
 
-template <int TERMS, bool EXTRA, bool APART>
+template <int TERMS, int EXTRA, bool APART>
 int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   constexpr int smem = stages_of(TERMS, APART) * kStage + 2 * TERMS * kQTerm;
   const int slices = APART ? 2 * num_sms : num_sms;
@@ -777,7 +777,7 @@ bool units_apart(const Q8AttnArgs &a, int num_sms) {
   const long long tiles = (long long)a.batch * a.heads_kv * ((a.max_len + kTile - 1) / kTile);
   return (long long)a.group * a.n_q <= unit_rows(true) && tiles >= 12LL * num_sms;
 }
-template <int TERMS, bool EXTRA>
+template <int TERMS, int EXTRA>
 int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   return p.unit == unit_rows(true) ? launch<TERMS, EXTRA, true>(a, p, num_sms, st) : launch<TERMS, EXTRA, false>(a, p, num_sms, st);
 }
@@ -808,10 +808,10 @@ int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *st
   p.cuts = (Cut *)w, w += round16((size_t)slices * sizeof(Cut));
   p.parts = (float *)w;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool extra = a.softcap != 0.f || a.slopes != nullptr || !(a.scale > 0.f);
+  const bool extra = a.softcap != 0.f || a.slopes != nullptr || !(a.scale > 0.f), far = a.softcap > kShortCap;
   if (a.q_dtype == TQ_BF16)
-    return extra ? launch<2, true>(a, p, num_sms, st) : launch<2, false>(a, p, num_sms, st);
-  return extra ? launch<3, true>(a, p, num_sms, st) : launch<3, false>(a, p, num_sms, st);
+    return far ? launch<2, kLongCaps>(a, p, num_sms, st) : extra ? launch<2, kCapOrBias>(a, p, num_sms, st) : launch<2, kPlain>(a, p, num_sms, st);
+  return far ? launch<3, kLongCaps>(a, p, num_sms, st) : extra ? launch<3, kCapOrBias>(a, p, num_sms, st) : launch<3, kPlain>(a, p, num_sms, st);
 }
 
 }  // namespace tq

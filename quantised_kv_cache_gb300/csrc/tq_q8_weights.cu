@@ -178,7 +178,7 @@ struct Many {
 };
 
 // The query rows' terms and numbers, one CTA per 128 rows: made once here, read by every CTA of tokens that the rows see.
-template <int TERMS, bool EXTRA>
+template <int TERMS>
 __global__ void __launch_bounds__(256) q8_row_tiles_kernel(const __grid_constant__ Q8AttnArgs a, Many w) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int see[4][4];
@@ -237,7 +237,7 @@ struct ManyShared {
   int bad;
 };
 
-template <int TERMS, bool EXTRA>
+template <int TERMS, int EXTRA>
 __global__ void __launch_bounds__(kManyThreads, 1)
 q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Many w) {
   constexpr int kS = many_stages(TERMS), kBytes = tile_bytes(TERMS);
@@ -383,7 +383,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
               const float4 c = *reinterpret_cast<const float4 *>(cl + r);
               float x0 = __uint_as_float(v[q & 1][i]), x1 = __uint_as_float(v[q & 1][i + 1]);
               if constexpr (EXTRA) {
-                x0 = capped_log2(x0, c.x * k1, cap), x1 = capped_log2(x1, c.z * k1, cap);
+                x0 = capped_log2<EXTRA == kLongCaps>(x0, c.x * k1, cap), x1 = capped_log2<EXTRA == kLongCaps>(x1, c.z * k1, cap);
                 if (a.slopes) {
                   const float4 e = *reinterpret_cast<const float4 *>(extra + r);
                   x0 = fmaf(-e.x, (float)__sad(__float_as_int(e.y), kp, 0u), x0);
@@ -453,7 +453,7 @@ Many many_of(int num_sms, int batch, int heads_kv, int group, int n_q, int max_l
   return w;
 }
 
-template <int TERMS, bool EXTRA>
+template <int TERMS, int EXTRA>
 int launch_many(const Q8AttnArgs &a, Many w, int slots, void *workspace, cudaStream_t st) {
   const size_t tiles = (size_t)a.batch * a.heads_kv * w.rts;
   char *p = (char *)workspace;
@@ -461,14 +461,14 @@ int launch_many(const Q8AttnArgs &a, Many w, int slots, void *workspace, cudaStr
   w.see = (int4 *)p, p += tiles * sizeof(int4);
   w.parts = w.splits > 1 ? (float *)p : nullptr;
   constexpr int smem = kTokens * kD + many_stages(TERMS) * tile_bytes(TERMS);
-  if (cudaFuncSetAttribute(q8_row_tiles_kernel<TERMS, EXTRA>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_bytes(TERMS)) != cudaSuccess ||
+  if (cudaFuncSetAttribute(q8_row_tiles_kernel<TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_bytes(TERMS)) != cudaSuccess ||
       cudaFuncSetAttribute(q8_weights_many_kernel<TERMS, EXTRA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
   const dim3 rows((unsigned)w.rts, (unsigned)a.heads_kv, (unsigned)a.batch);
   const int last = w.parts ? a.max_len : slots;
   const dim3 grid((unsigned)((long long)((last + kTokens - 1) / kTokens) * w.splits), (unsigned)a.heads_kv, (unsigned)a.batch);
   const dim3 sum((unsigned)((slots + 255) / 256), (unsigned)a.heads_kv, (unsigned)a.batch);
-  cudaError_t e = launch_overlapped(true, q8_row_tiles_kernel<TERMS, EXTRA>, rows, dim3(256), tile_bytes(TERMS), st, a, w);
+  cudaError_t e = launch_overlapped(true, q8_row_tiles_kernel<TERMS>, rows, dim3(256), tile_bytes(TERMS), st, a, w);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_weights_many_kernel<TERMS, EXTRA>, grid, dim3(kManyThreads), smem, st, a, w);
   if (e == cudaSuccess && w.parts) e = launch_overlapped(true, q8_weights_sum_kernel, sum, dim3(256), 0, st, a, w);
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
@@ -539,9 +539,14 @@ int launch_q8_weights(const Q8AttnArgs &a, int terms, void *workspace, int num_s
   if (a.out_dtype == TQ_F32) return launch_wide(a, slots, st);
   size_t bytes;
   const Many m = many_of(num_sms, a.batch, a.heads_kv, a.group, a.n_q, a.max_len, &bytes);
-  const bool extra = a.softcap != 0.f || a.slopes != nullptr;
-  if (terms == 2) return extra ? launch_many<2, true>(a, m, slots, workspace, st) : launch_many<2, false>(a, m, slots, workspace, st);
-  return extra ? launch_many<3, true>(a, m, slots, workspace, st) : launch_many<3, false>(a, m, slots, workspace, st);
+  const bool extra = a.softcap != 0.f || a.slopes != nullptr, far = a.softcap > kShortCap;
+  if (terms == 2)
+    return far     ? launch_many<2, kLongCaps>(a, m, slots, workspace, st)
+           : extra ? launch_many<2, kCapOrBias>(a, m, slots, workspace, st)
+                   : launch_many<2, kPlain>(a, m, slots, workspace, st);
+  return far     ? launch_many<3, kLongCaps>(a, m, slots, workspace, st)
+         : extra ? launch_many<3, kCapOrBias>(a, m, slots, workspace, st)
+                 : launch_many<3, kPlain>(a, m, slots, workspace, st);
 }
 
 }  // namespace tq
