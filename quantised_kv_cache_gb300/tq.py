@@ -166,6 +166,17 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, make, *args, **kw) -> torch.Tensor:
+    """make(*args, **kw) for a call on `stream` (None: the current one) to write. It belongs to that stream's pool, so that it is not
+    handed out again under the call's kernels, and is kept from reuse until the caller's stream is done with it as well."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return TQ_F32
@@ -275,9 +286,9 @@ def tq_decode_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Te
     Hkv = cache.struct.heads_kv
     need = tq_workspace_size(ctx, B, Hq, Hkv, max_len, splits)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+        out = _made(stream, torch.empty, (B, Hq, d), dtype=torch.float32, device=q.device)
     check(lib().tq_decode_attention(ctx, ctypes.byref(cache.struct), _ptr(q), _dtype_code(q), B, Hq, Hkv,
                                     _ptr(seq_lens), max_len, splits, _ptr(workspace), workspace.numel(),
                                     _ptr(out), _stream(stream)), "tq_decode_attention")
@@ -296,9 +307,9 @@ def tq_decode_step(ctx, cache: "Cache", q: torch.Tensor, k_new: torch.Tensor, v_
     assert seq_lens.dtype == torch.int32 and seq_lens.is_cuda
     need = tq_workspace_size(ctx, B, Hq, Hkv, max_len, 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+        out = _made(stream, torch.empty, (B, Hq, d), dtype=torch.float32, device=q.device)
     check(lib().tq_decode_step(ctx, ctypes.byref(cache.struct), _ptr(q), _dtype_code(q), _ptr(k_new), _ptr(v_new),
                                _dtype_code(k_new), B, Hq, Hkv, _ptr(seq_lens), max_len, _ptr(workspace),
                                workspace.numel(), _ptr(out), _stream(stream)), "tq_decode_step")
@@ -311,7 +322,7 @@ def tq_decode_attention_static(ctx, cache: "Cache", q: torch.Tensor, seq_lens: t
     B, Hq, d = q.shape
     assert q.is_contiguous() and seq_lens.dtype == torch.int32
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+        out = _made(stream, torch.empty, (B, Hq, d), dtype=torch.float32, device=q.device)
     check(lib().tq_decode_attention_static(ctx, ctypes.byref(cache.struct), _ptr(q), _dtype_code(q), B, Hq,
                                            cache.struct.heads_kv, _ptr(seq_lens), max_len, splits, _ptr(out),
                                            _stream(stream)), "tq_decode_attention_static")
@@ -327,9 +338,9 @@ def tq_dequantize(ctx, cache: "Cache", t0: int, t1: int, seq_lens: Optional[torc
     B, H = cache.struct.batch, cache.struct.heads_kv
     dev = cache.device
     if k_out is None:
-        k_out = torch.empty((B, H, t1 - t0, 128), dtype=torch.float32, device=dev)
+        k_out = _made(stream, torch.empty, (B, H, t1 - t0, 128), dtype=torch.float32, device=dev)
     if v_out is None:
-        v_out = torch.empty((B, H, t1 - t0, 128), dtype=torch.float32, device=dev)
+        v_out = _made(stream, torch.empty, (B, H, t1 - t0, 128), dtype=torch.float32, device=dev)
     check(lib().tq_dequantize(ctx, ctypes.byref(cache.struct), B, H, t0, t1, _ptr(seq_lens), _ptr(k_out),
                               _ptr(v_out), _stream(stream)), "tq_dequantize")
     return k_out, v_out
@@ -466,7 +477,7 @@ def tq_rotary(ctx, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch
     if index < 0:
         raise ValueError("x: a CUDA tensor is wanted")
     if out is None:
-        out = torch.empty_like(x)
+        out = _made(stream, torch.empty_like, x)
     elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != index:
         raise ValueError("out: x's shape, type and device are wanted")
     B, H, n, _ = shape
@@ -527,12 +538,12 @@ def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor
     if q.get_device() != index or index < 0:
         raise ValueError("q: the cache's device is wanted")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _made(stream, torch.empty, shape, dtype=out_dtype or q.dtype, device=q.device)
     elif out.shape != shape or out.get_device() != index or out_dtype not in (None, out.dtype):
         raise ValueError("out: q's shape and device are wanted")
     if workspace is None:
-        workspace = torch.empty(tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
+                          dtype=torch.uint8, device=q.device)
     os = _rows(out, "out")[1]
     rows, slots = (B, n), (B, H, cap)
     a = _pack_attn.pack(
@@ -562,13 +573,13 @@ def tq_q8_evict(ctx, src: "Cache", dst: "Cache", seq_lens: torch.Tensor, weights
         raise ValueError("dst: the source's batch, KV heads and device are wanted")
     some, from_, to = (B, H, max(keep, 0)), (B, H, src.capacity), (B, H, dst.capacity)
     if kept is None:
-        kept = torch.empty(some, dtype=_i32, device=dev)
+        kept = _made(stream, torch.empty, some, dtype=_i32, device=dev)
     if dst_lens is None:
-        dst_lens = torch.empty((B,), dtype=_i32, device=dev)
+        dst_lens = _made(stream, torch.empty, (B,), dtype=_i32, device=dev)
     if dst_weights is None:
-        dst_weights = torch.empty(to, dtype=_f32, device=dev)
+        dst_weights = _made(stream, torch.empty, to, dtype=_f32, device=dev)
     if dst_positions is None:
-        dst_positions = torch.empty(to, dtype=_i32, device=dev)
+        dst_positions = _made(stream, torch.empty, to, dtype=_i32, device=dev)
     status = lib().tq_q8_evict(
         ctx, src.struct, dst.struct, B, H, _array(seq_lens, (B,), _i32, index, "seq_lens"),
         _array(weights, from_, _f32, index, "weights"), keep, sink, recent, _array(positions, from_, _i32, index, "positions"),
