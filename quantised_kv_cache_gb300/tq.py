@@ -433,9 +433,10 @@ def _any_dtype(dtype: torch.dtype) -> int:
 
 
 def _raw_stream(stream, index: int) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(index)
+    """The stream of a call whose tensors lie on device `index`, which has to be the current one."""
+    if index != torch.cuda.current_device() or (stream is not None and stream.device_index != index):
+        raise ValueError("the tensors, the stream and the current device: one device is wanted")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -544,6 +545,8 @@ def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor
     if workspace is None:
         workspace = _made(stream, torch.empty, tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
                           dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on q's device is wanted")
     os = _rows(out, "out")[1]
     rows, slots = (B, n), (B, H, cap)
     a = _pack_attn.pack(
