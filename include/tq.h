@@ -499,6 +499,10 @@ tq_status tq_selftest_bounded_wait(const tq_ctx *ctx, unsigned long long budget_
  * streams if neither writes what the other reads or writes (a workspace is
  * written).
  *
+ * What a call writes shares no memory with anything else that it writes or reads unless its description allows it. Vectors that do
+ * are refused (TQ_ERR_ARG), and so are strided ones of which neither their extents nor their strides show that they lie apart; so are
+ * weights, log-sums, lengths and positions, but not tables, caches and workspaces.
+ *
  * Strides are in elements, of the batch, head and token dimension in this order;
  * the d coordinates are contiguous. Every pointer must be 16-byte aligned and
  * every stride a multiple of 16 bytes (TQ_ERR_ALIGN otherwise).

@@ -24,9 +24,12 @@ bool strides_ok(const int64_t *s, int dtype) {
   return true;
 }
 
-// distinct rows lie apart (a target is never broadcast)
+// distinct rows lie apart in every dimension (a target is never broadcast)
 bool spread(const int64_t *s, int batch, int heads, int n) {
-  return (batch == 1 || s[0]) && (heads == 1 || s[1]) && (n == 1 || s[2]);
+  const int64_t size[3] = {batch, heads, n};
+  for (int i = 0; i < 3; ++i)
+    if (size[i] > 1 && s[i] > -tq::kD && s[i] < tq::kD) return false;
+  return true;
 }
 
 tq::Q8Strides strides(const int64_t *s) { return tq::Q8Strides{s[0], s[1], s[2]}; }
@@ -41,11 +44,62 @@ tq_status on_device(const tq_ctx *ctx) {
 // beside a large scale.
 constexpr float kNoCap = 1099511627776.f, kLeastCap = 8.6736174e-19f;  // 2^40, 2^-60
 
-// [p, p + n) and [q, q + m) share a byte
-bool overlap(const void *p, size_t n, const void *q, size_t m) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + m && b < a + n;
+typedef __int128 wide;
+
+// Rows of `row` bytes at p + i stride[0] + j stride[1] + k stride[2], i < size[0] and so on.
+struct Region {
+  const void *p;
+  wide stride[3];
+  int64_t size[3], row;
+};
+Region rows(const void *p, const int64_t *s, int dtype, int batch, int heads, int n) {
+  const int e = size_of(dtype);
+  return Region{p, {(wide)s[0] * e, (wide)s[1] * e, (wide)s[2] * e}, {batch, heads, n}, (int64_t)tq::kD * e};
 }
+// contiguous bytes (none for NULL)
+Region bytes(const void *p, size_t n) { return Region{p, {0, 0, 0}, {1, 1, 1}, p ? (int64_t)n : 0}; }
+
+// The first byte's offset from p and the length of the rows along those dimensions whose stride is no multiple of `period`
+// (0: along all of them).
+void extent(const Region &r, wide period, wide *first, wide *length) {
+  *first = 0, *length = r.row;
+  for (int i = 0; i < 3; ++i) {
+    if (r.size[i] <= 1 || (period && r.stride[i] % period == 0)) continue;
+    const wide d = r.stride[i] * (r.size[i] - 1);
+    *length += d < 0 ? -d : d;
+    if (d < 0) *first += d;
+  }
+}
+
+// False when the regions share no byte: their extents lie apart, or the parts of them that repeat at one of their strides do (a
+// fused projection's queries and keys, say). True for regions that share one, and for those that neither test can tell.
+bool overlap(const Region &a, const Region &b) {
+  if (!a.row || !b.row) return false;
+  const wide apart = (wide)(uintptr_t)b.p - (wide)(uintptr_t)a.p;
+  for (int k = -1; k < 6; ++k) {
+    const Region &r = k < 3 ? a : b;
+    wide period = 0, a0, b0, na, nb;
+    if (k >= 0) {
+      period = r.size[k % 3] > 1 ? r.stride[k % 3] : 0;
+      if (period == 0) continue;
+      if (period < 0) period = -period;
+    }
+    extent(a, period, &a0, &na);
+    extent(b, period, &b0, &nb);
+    wide d = apart + b0 - a0;  // from a's first byte to b's
+    if (period == 0) {
+      if (d >= na || -d >= nb) return false;
+      continue;
+    }
+    d %= period;
+    if (d < 0) d += period;
+    if (d >= na && period - d >= nb) return false;
+  }
+  return true;
+}
+
+// A buffer that is updated in place, or regions that lie apart.
+bool same_or_apart(const Region &a, const Region &b) { return a.p == b.p || !overlap(a, b); }
 
 }  // namespace
 
@@ -115,7 +169,9 @@ tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides
   if (!aligned16(d_x) || !aligned16(d_y) || !strides_ok(x_strides, dtype) || !strides_ok(y_strides, dtype))
     return TQ_ERR_ALIGN;
   if (!spread(y_strides, batch, heads, n)) return TQ_ERR_ARG;
-  if (d_x == d_y && std::memcmp(x_strides, y_strides, 3 * sizeof(int64_t))) return TQ_ERR_ARG;
+  if (!(d_x == d_y && !std::memcmp(x_strides, y_strides, 3 * sizeof(int64_t))) &&
+      overlap(rows(d_x, x_strides, dtype, batch, heads, n), rows(d_y, y_strides, dtype, batch, heads, n)))
+    return TQ_ERR_ARG;
   const tq_status s = on_device(ctx);
   if (s != TQ_OK) return s;
   if (n == 0) return TQ_OK;
@@ -161,7 +217,6 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (p->softcap != 0.f && !(p->softcap >= kLeastCap)) return TQ_ERR_ARG;  // (negative ones among them)
   if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
   if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
-  if (p->d_out == p->d_q) return TQ_ERR_ARG;  // the weights read the queries again after the results are written
   tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
   if (s != TQ_OK) return s;
   if (p->max_len > cache->capacity) return TQ_ERR_ARG;
@@ -173,6 +228,14 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (s != TQ_OK) return s;
   if (ws_bytes < need) return TQ_ERR_WORKSPACE;
   if (!spread(p->out_strides, p->batch, p->heads_q, p->n_q)) return TQ_ERR_ARG;
+  const Region q = rows(p->d_q, p->q_strides, p->q_dtype, p->batch, p->heads_q, p->n_q);
+  const Region out = rows(p->d_out, p->out_strides, p->out_dtype, p->batch, p->heads_q, p->n_q);
+  const size_t slots = (size_t)p->batch * p->heads_kv * cache->capacity * sizeof(float);
+  const Region weights = bytes(p->d_weights, slots), lse = bytes(p->d_lse, (size_t)p->batch * p->heads_q * p->n_q * sizeof(float));
+  // (the queries are read again, for the weights, after the results are written)
+  if (overlap(q, out) || overlap(q, weights) || overlap(q, lse) || overlap(out, weights) || overlap(out, lse) || overlap(weights, lse) ||
+      !same_or_apart(weights, bytes(p->d_weights_in, slots)))
+    return TQ_ERR_ARG;
   if ((s = on_device(ctx)) != TQ_OK) return s;
   tq::Q8AttnArgs a{};
   a.c = tq::q8_cache(cache);
@@ -200,11 +263,19 @@ tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *ds
   const size_t grid = (size_t)batch * heads_kv;
   const size_t sn = src->block_table ? (size_t)src->pool_blocks : grid * tq::q8_blocks_of(src->capacity);
   const size_t dn = dst->block_table ? (size_t)dst->pool_blocks : grid * tq::q8_blocks_of(dst->capacity);
-  if (overlap(src->records, sn * tq::kQ8BlockBytes, dst->records, dn * tq::kQ8BlockBytes) ||
-      overlap(src->k_stats, sn * 4, dst->k_stats, dn * 4) || overlap(src->v_stats, sn * 4, dst->v_stats, dn * 4))
+  if (overlap(bytes(src->records, sn * tq::kQ8BlockBytes), bytes(dst->records, dn * tq::kQ8BlockBytes)) ||
+      overlap(bytes(src->k_stats, sn * 4), bytes(dst->k_stats, dn * 4)) || overlap(bytes(src->v_stats, sn * 4), bytes(dst->v_stats, dn * 4)))
     return TQ_ERR_ARG;
-  if ((d_dst_weights && d_dst_weights == d_weights) || (d_dst_positions && d_dst_positions == d_positions))
-    return TQ_ERR_ARG;
+  const Region lens = bytes(d_seq_lens, batch * sizeof(int32_t));
+  const Region in[] = {lens, bytes(d_weights, grid * src->capacity * 4), bytes(d_positions, grid * src->capacity * 4)};
+  const Region outs[] = {bytes(d_dst_lens, batch * sizeof(int32_t)), bytes(d_kept, grid * keep * 4),
+                         bytes(d_dst_weights, grid * dst->capacity * 4), bytes(d_dst_positions, grid * dst->capacity * 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (i == 0 && j == 0 ? !same_or_apart(outs[i], in[j]) : overlap(outs[i], in[j])) return TQ_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return TQ_ERR_ARG;
+  }
   if ((s = on_device(ctx)) != TQ_OK) return s;
   const tq::Q8EvictArgs a{tq::q8_cache(src), tq::q8_cache(dst), batch, heads_kv, keep, sink, recent, d_seq_lens,
                           d_weights, d_positions, d_kept, d_dst_lens, d_dst_positions, d_dst_weights,

@@ -1,0 +1,156 @@
+"""The 8-bit cache's and the rotary calls' host side on a machine without a GPU: what is refused before anything is enqueued, and
+what is not.
+
+The calls take a context that lies in memory only (tq_init needs a GPU): right after the checks the library asks for the current
+device, and fails (TQ_ERR_CUDA), so that a call's status tells whether its arguments were taken. Addresses are numbers; nothing
+reads them."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from conftest import ROOT
+from quantised_kv_cache_gb300 import tq
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would be enqueued")
+
+SMS = 152
+TAKEN = tq.TQ_ERR_CUDA
+
+
+@pytest.fixture(scope="module")
+def ctx(tmp_path_factory):
+    cxx, cuda_inc = shutil.which("g++"), "/usr/local/cuda/include"
+    if cxx is None or not os.path.isdir(cuda_inc):
+        pytest.skip("needs g++ and the CUDA headers")
+    from quantised_kv_cache_gb300 import build
+    build.build()
+    d = tmp_path_factory.mktemp("ctx")
+    (d / "ctx.cpp").write_text('#include "tq_internal.h"\n'
+                               'extern "C" tq_ctx *make(int scheme, int sms) {\n'
+                               "  tq_ctx *c = new tq_ctx();\n"
+                               "  c->d = tq::kD, c->scheme = scheme, c->bits = 8, c->num_sms = sms, c->device = -1;\n"
+                               "  return c;\n}\n"
+                               'extern "C" const unsigned long long *turns(const tq_ctx *c) { return c->rope.freq; }\n')
+    csrc = os.path.join(ROOT, "quantised_kv_cache_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-I", csrc, "-I", os.path.join(ROOT, "include"), "-I", cuda_inc,
+                    str(d / "ctx.cpp"), "-o", str(d / "ctx.so")], check=True, capture_output=True)
+    L = ctypes.CDLL(str(d / "ctx.so"))
+    L.make.restype, L.turns.restype = ctypes.c_void_p, ctypes.POINTER(ctypes.c_ulonglong)
+    L.turns.argtypes = [ctypes.c_void_p]
+    c = ctypes.c_void_p(L.make(tq.TQ_SCHEME_Q8, SMS))
+    tq.tq_set_rope(c)
+    c.turns = lambda: L.turns(c)
+    return c
+
+
+def cache(batch=2, heads=4, capacity=1024, at=1 << 40):
+    c = tq.tq_cache()
+    c.batch, c.heads_kv, c.capacity = batch, heads, capacity
+    c.records, c.k_stats, c.v_stats = at, at + (1 << 36), at + (2 << 36)
+    return c
+
+
+S = tq._strides3
+BASE = 1 << 20
+ELSEWHERE = 1 << 34
+
+
+# ------------------------------------------------------------------------------------------------ outputs that overlap
+
+B, H, N, D = 2, 8, 16, 128
+FUSED = (N * 3 * H * D, D, 3 * H * D)  # [batch][token][3 H heads][d], 2 bytes an element
+
+
+def rotary(ctx, x, xs, y, ys, dtype=tq.TQ_BF16):
+    return tq.lib().tq_rotary(ctx, x, S(*xs), y, S(*ys), dtype, B, H, N, 1 << 30, 0, None)
+
+
+@pytest.mark.parametrize("x,xs,y,ys,want", [
+    (BASE, (H * N * D, N * D, D), BASE, (H * N * D, N * D, D), TAKEN),                 # in place
+    (BASE, FUSED, BASE, FUSED, TAKEN),                                                 # in place, a part of a fused projection
+    (BASE, FUSED, BASE + 2 * H * D, FUSED, TAKEN),                                     # one part into another
+    (BASE + 4 * H * D, FUSED, BASE, FUSED, TAKEN),
+    (BASE, FUSED, BASE + 2 * (H - 1) * D, FUSED, tq.TQ_ERR_ARG),                       # parts that share a head
+    (BASE, FUSED, BASE + 2 * 3 * H * D, FUSED, tq.TQ_ERR_ARG),                         # a token later
+    (BASE, (H * N * D, N * D, D), BASE + 2 * D, (H * N * D, N * D, D), tq.TQ_ERR_ARG),  # a row later
+    (BASE, (H * N * D, N * D, D), BASE + 2 * B * H * N * D - 16, (H * N * D, N * D, D), tq.TQ_ERR_ARG),  # the last 16 bytes
+    (BASE, (H * N * D, N * D, D), BASE + 2 * B * H * N * D, (H * N * D, N * D, D), TAKEN),
+    (BASE + 2 * B * H * N * D, (H * N * D, N * D, D), BASE, (H * N * D, N * D, D), TAKEN),
+    (BASE, (H * N * D, N * D, D), BASE, (H * N * D, D, H * D), tq.TQ_ERR_ARG),         # in place, transposed
+    (BASE, (2 * H * N * D, 2 * N * D, D), BASE + 2 * N * D, (2 * H * N * D, 2 * N * D, D), TAKEN),      # halves of every head's tokens
+    (BASE, (2 * H * N * D, 2 * N * D, 2 * D), BASE + 2 * D, (2 * H * N * D, 2 * N * D, 2 * D), TAKEN),  # every other token
+    (BASE, (2 * H * N * D, 2 * N * D, 2 * D), BASE + D, (2 * H * N * D, 2 * N * D, 2 * D), tq.TQ_ERR_ARG),
+    (BASE + 2 * (N - 1) * D, (H * N * D, N * D, -D), BASE, (H * N * D, N * D, D), tq.TQ_ERR_ARG),       # the same rows backwards
+    (BASE, (0, 0, D), BASE + 2 * N * D, (H * N * D, N * D, D), TAKEN),                 # a broadcast input before its output
+    (BASE, (0, 0, D), BASE + 2 * N * D - 2 * D, (H * N * D, N * D, D), tq.TQ_ERR_ARG),
+])
+def test_rotary_outputs_that_overlap_their_input(ctx, x, xs, y, ys, want):
+    assert rotary(ctx, x, xs, y, ys) == want
+
+
+@pytest.mark.parametrize("ys", [(0, N * D, D), (H * N * D, 64, D), (H * N * D, N * D, 120), (H * N * D, N * D, -64)])
+def test_targets_whose_own_rows_overlap(ctx, ys):
+    assert rotary(ctx, BASE, (H * N * D, N * D, D), ELSEWHERE, ys) == tq.TQ_ERR_ARG
+    assert attention(ctx, batch=B, heads_q=H, heads_kv=4, n_q=N, d_out=ELSEWHERE, out_strides=S(*ys)) == tq.TQ_ERR_ARG
+
+
+def attention(ctx, c=None, ws=1 << 42, ws_bytes=1 << 40, **kw):
+    a = tq.tq_q8_attn(batch=2, heads_q=8, heads_kv=4, n_q=3, max_len=1024, q_dtype=tq.TQ_BF16, out_dtype=tq.TQ_BF16, d_q=BASE, d_out=ELSEWHERE,
+                      d_seq_lens=1 << 30)
+    n, h = kw.get("n_q", 3), kw.get("heads_q", 8)
+    a.q_strides = a.out_strides = S(h * n * D, n * D, D)
+    for name, value in kw.items():
+        setattr(a, name, value)
+    return tq.lib().tq_q8_attention(ctx, ctypes.byref(c or cache(a.batch, a.heads_kv)), bytes(a), ws, ws_bytes, None)
+
+
+def test_attention_outputs_that_overlap(ctx):
+    size = 2 * 8 * 3 * D
+    slots = 2 * 4 * 1024 * 4
+    assert attention(ctx) == TAKEN
+    for at, status in ((BASE, tq.TQ_ERR_ARG), (BASE + 2 * size - 16, tq.TQ_ERR_ARG), (BASE + 2 * size, TAKEN), (BASE - 2 * size, TAKEN),
+                       (BASE - 2 * size + 16, tq.TQ_ERR_ARG)):
+        assert attention(ctx, d_out=at) == status
+        assert attention(ctx, d_out=at, out_dtype=tq.TQ_F32) == (TAKEN if status == TAKEN and at > BASE else tq.TQ_ERR_ARG)
+    w = 1 << 36
+    assert attention(ctx, d_weights=w) == TAKEN
+    assert attention(ctx, d_weights=w, d_weights_in=w) == TAKEN
+    assert attention(ctx, d_weights=w, d_weights_in=w + slots) == TAKEN
+    assert attention(ctx, d_weights=w, d_weights_in=w + 4) == tq.TQ_ERR_ARG
+    assert attention(ctx, d_weights=w, d_weights_in=w - slots + 4) == tq.TQ_ERR_ARG
+    assert attention(ctx, d_weights=w, d_lse=w + slots) == TAKEN
+    assert attention(ctx, d_weights=w, d_lse=w + slots - 4) == tq.TQ_ERR_ARG
+    assert attention(ctx, d_weights=w, d_lse=ELSEWHERE + 2 * size - 4) == tq.TQ_ERR_ARG
+    assert attention(ctx, d_weights=BASE + 2 * size - 4) == tq.TQ_ERR_ARG
+
+
+def evict(ctx, **kw):
+    a = dict(lens=1 << 30, weights=1 << 31, positions=1 << 32, kept=1 << 33, dst_lens=ELSEWHERE, dst_weights=1 << 35, dst_positions=1 << 36)
+    a.update(kw)
+    src, dst = cache(2, 4, 1024), cache(2, 4, 512, at=1 << 44)
+    return tq.lib().tq_q8_evict(ctx, ctypes.byref(src), ctypes.byref(dst), 2, 4, a["lens"], a["weights"], 256, 4, 16, a["positions"], a["kept"],
+                                a["dst_lens"], a["dst_weights"], a["dst_positions"], None)
+
+
+def test_eviction_outputs_that_overlap(ctx):
+    from_, to, kept = 2 * 4 * 1024 * 4, 2 * 4 * 512 * 4, 2 * 4 * 256 * 4
+    assert evict(ctx) == TAKEN
+    assert evict(ctx, dst_lens=1 << 30) == TAKEN  # the lengths' own place
+    assert evict(ctx, dst_lens=(1 << 30) + 4) == tq.TQ_ERR_ARG
+    for out, size in (("dst_weights", to), ("dst_positions", to), ("kept", kept)):
+        for src, bytes_ in (("weights", from_), ("positions", from_), ("lens", 8)):
+            at = dict(lens=1 << 30, weights=1 << 31, positions=1 << 32)[src]
+            assert evict(ctx, **{out: at}) == tq.TQ_ERR_ARG
+            assert evict(ctx, **{out: at + bytes_ - 4}) == tq.TQ_ERR_ARG
+            assert evict(ctx, **{out: at - size + 4}) == tq.TQ_ERR_ARG
+            assert evict(ctx, **{out: at + bytes_}) == TAKEN and evict(ctx, **{out: at - size}) == TAKEN
+    assert evict(ctx, dst_weights=1 << 36) == tq.TQ_ERR_ARG
+    assert evict(ctx, kept=(1 << 35) + to - 4) == tq.TQ_ERR_ARG
+    assert evict(ctx, dst_positions=(1 << 33) + kept - 4) == tq.TQ_ERR_ARG
+    assert evict(ctx, dst_lens=(1 << 33) + 4) == tq.TQ_ERR_ARG
+    assert evict(ctx, positions=None, dst_weights=None, dst_positions=None) == TAKEN
