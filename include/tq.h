@@ -583,8 +583,10 @@ typedef struct tq_q8_attn {
 } tq_q8_attn;
 
 /* out = softmax(t) V_hat over the slots each query sees; a query that sees none
- * yields zeros. d_workspace: >= tq_q8_attention_workspace(...) bytes for these
- * sizes (weights: 1 when d_weights is set), no initial contents required. A d_seq_lens[b] outside [0, max_len] or a d_new_lens[b]
+ * yields zeros. d_workspace: no initial contents required, tq_q8_attention_workspace(...) bytes for these sizes (weights: 0 without d_weights,
+ * 1 with them, 2 with them and results of 16 bits only) or for larger ones: what serves a call serves every call of the same heads
+ * and no more sequences, query tokens and max_len. With weights there is room for the scores of calls that keep them; where a workspace has
+ * none they are formed again (slower; the weights' last bits may differ). A d_seq_lens[b] outside [0, max_len] or a d_new_lens[b]
  * outside [0, n_q] is cut to that range, and a bad block-table entry's tokens are
  * taken as unseen; both set the device error word to TQ_ERR_ARG. Rounding: the
  * products of codes with 16-bit queries are exact, their sums fp32. A probability

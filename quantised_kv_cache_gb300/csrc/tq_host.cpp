@@ -869,7 +869,7 @@ tq_status tq_workspace_size(const tq_ctx *ctx, int batch, int heads_q, int heads
   if (ctx->scheme == TQ_SCHEME_Q8) {
     // the decode step's lengths, then the attention's own
     if (heads_q % heads_kv) return TQ_ERR_ARG;
-    *out = q8_lens_bytes(batch) + tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, 1, max_len, 0);
+    *out = q8_lens_bytes(batch) + tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, 1, max_len, 0, nullptr);
     return TQ_OK;
   }
   int s, chunk;

@@ -89,12 +89,14 @@ struct Q8AttnArgs {
   long long scores_ld = 0;
   int *error;
 };
-size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights);
+// The workspace with room for all that is worth keeping; *least (if not NULL): what the call cannot do without, which never falls as
+// the batch, the query tokens or max_len grow. `weights`: 0 none, 1 with results of either size, 2 with results of 16 bits
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights, size_t *least);
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q);
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 // `terms`: of the queries, where 16-bit results' scores were not kept
 size_t q8_weights_workspace(int num_sms, int batch, int heads_kv, int group, int n_q, int max_len);
 int launch_q8_weights(const Q8AttnArgs &a, int terms, void *workspace, int num_sms, void *stream);
-int launch_q8_attention(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
+int launch_q8_attention(const Q8AttnArgs &a, void *workspace, size_t ws_bytes, int num_sms, void *stream);
 
 }  // namespace tq

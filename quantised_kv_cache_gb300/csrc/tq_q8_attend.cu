@@ -22,6 +22,8 @@
 // latency and the join. 32-bit results, 4 sequences of up to 16383 tokens, 8 KV heads of 6 rows: 53 us where the bytes take 13: a CTA has 17 tiles,
 // and the chain of each (8 terms to form, 64 operand columns) shows. One sequence of 1000 tokens: 16 us with its weights, all latency.
 
+#include <algorithm>
+
 #include "tq_q8_rows.cuh"
 
 namespace tq {
@@ -518,32 +520,36 @@ int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts
   return TQ_OK;
 }
 
-// The scores of up to 64 rows (no more bytes than the cache that they come from) are kept for the weights when they fit into a
-// GB of workspace; else they are formed again. 16 sequences of 16384 tokens, 8 KV heads, 4 rows: 111 us kept, 706 formed again.
+// The scores of up to 64 rows that this kernel forms (no more bytes than the cache that they come from) are kept for the weights where they
+// fit into a GB and into the workspace; else they are formed again. 16 sequences of 16384 tokens, 8 KV heads, 4 rows: 111 us kept, 706
+// formed again.
 constexpr long long kKeptRows = 64;
 constexpr size_t kScoreBytes = size_t(1) << 30;
-size_t score_bytes(int batch, int heads_q, long long rows, int n_q, int max_len) {
+size_t score_bytes(int batch, int heads_q, long long rows, int n_q, int max_len, bool half) {
   const size_t n = (size_t)batch * heads_q * n_q * ((max_len + kTile - 1) / kTile * kTile) * sizeof(float);
-  return rows <= kKeptRows && n <= kScoreBytes ? n : 0;
+  return rows <= (half ? kFewRows : kKeptRows) && n <= kScoreBytes ? n : 0;
 }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// Workspace: for the weights the log-sums and, for few rows, the scores; then either kernel's records (few rows: cuts and parts), in
-// whose place the weights' row tiles come.
-size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights) {
-  const long long R = (long long)(heads_q / heads_kv) * n_q;
-  const size_t lse = weights ? round16((size_t)batch * heads_q * n_q * sizeof(float)) : 0;
-  const size_t scores = weights ? score_bytes(batch, heads_q, R, n_q, max_len) : 0;
-  const size_t few = round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float);
-  const size_t many = R <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, heads_q / heads_kv, n_q);
-  const size_t tiles = weights && (R > kFewRows || !scores) ? q8_weights_workspace(num_sms, batch, heads_kv, heads_q / heads_kv, n_q, max_len) : 0;
-  const size_t records = few > many ? few : many;
-  return lse + scores + (records > tiles ? records : tiles);
+// Workspace: for the weights the log-sums; then, where they are kept, the scores; then either kernel's records (few rows: cuts and parts),
+// in whose place the weights' row tiles come.
+size_t lse_bytes(int batch, int heads_q, int n_q) { return round16((size_t)batch * heads_q * n_q * sizeof(float)); }
+size_t few_bytes(int num_sms) { return round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float); }
+size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights, size_t *least) {
+  const int group = heads_q / heads_kv;
+  const long long R = (long long)group * n_q;
+  const size_t lse = weights ? lse_bytes(batch, heads_q, n_q) : 0;
+  const size_t many = R <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, group, n_q);
+  const size_t tiles = weights ? q8_weights_workspace(num_sms, batch, heads_kv, group, n_q, max_len) : 0;
+  const size_t scores = weights ? score_bytes(batch, heads_q, R, n_q, max_len, weights == 2) : 0;
+  const size_t need = lse + std::max({few_bytes(num_sms), many, tiles});
+  if (least) *least = need;
+  return scores ? std::max(need, lse + scores + few_bytes(num_sms)) : need;
 }
 
-int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, void *stream) {
+int launch_q8_attention(const Q8AttnArgs &args, void *workspace, size_t ws_bytes, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   Q8AttnArgs a = args;
   const long long R = (long long)a.group * a.n_q;
@@ -551,10 +557,12 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, int num_sms, vo
   char *w = (char *)workspace;
   if (a.weights) {
     if (!a.lse) a.lse = (float *)w;
-    w += round16((size_t)a.batch * a.heads_q * a.n_q * sizeof(float));
-    const size_t scores = score_bytes(a.batch, a.heads_q, R, a.n_q, a.max_len);
-    if (scores && few) a.scores = (float *)w, a.scores_ld = (a.max_len + kTile - 1) / kTile * kTile;
-    w += scores;
+    const size_t lse = lse_bytes(a.batch, a.heads_q, a.n_q), scores = few ? score_bytes(a.batch, a.heads_q, R, a.n_q, a.max_len, false) : 0;
+    w += lse;
+    if (scores && ws_bytes >= lse + scores + few_bytes(num_sms)) {
+      a.scores = (float *)w, a.scores_ld = (a.max_len + kTile - 1) / kTile * kTile;
+      w += scores;
+    }
   }
   if (!few) {  // rows as lanes
     const int s = launch_q8_prompt(a, w, num_sms, stream);

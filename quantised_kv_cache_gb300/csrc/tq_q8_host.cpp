@@ -200,10 +200,11 @@ tq_status tq_q8_append(const tq_ctx *ctx, const tq_cache *cache, const void *d_k
 
 tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
                                     int weights, size_t *out) {
-  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || max_len <= 0)
+  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || max_len <= 0 ||
+      weights < 0 || weights > 2)
     return TQ_ERR_ARG;
   if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
-  *out = tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q, max_len, weights);
+  *out = tq::q8_attention_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q, max_len, weights, nullptr);
   return TQ_OK;
 }
 
@@ -223,10 +224,9 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (!aligned16(p->d_q) || !aligned16(p->d_out) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
       !strides_ok(p->out_strides, p->out_dtype))
     return TQ_ERR_ALIGN;
-  size_t need = 0;
-  s = tq_q8_attention_workspace(ctx, p->batch, p->heads_q, p->heads_kv, p->n_q, p->max_len, p->d_weights != nullptr, &need);
-  if (s != TQ_OK) return s;
-  if (ws_bytes < need) return TQ_ERR_WORKSPACE;
+  size_t least = 0;
+  tq::q8_attention_workspace(ctx->num_sms, p->batch, p->heads_q, p->heads_kv, p->n_q, p->max_len, p->d_weights != nullptr, &least);
+  if (ws_bytes < least) return TQ_ERR_WORKSPACE;
   if (!spread(p->out_strides, p->batch, p->heads_q, p->n_q)) return TQ_ERR_ARG;
   const Region q = rows(p->d_q, p->q_strides, p->q_dtype, p->batch, p->heads_q, p->n_q);
   const Region out = rows(p->d_out, p->out_strides, p->out_dtype, p->batch, p->heads_q, p->n_q);
@@ -248,7 +248,7 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
   a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
   a.error = &ctx->dparams->error;
-  return (tq_status)tq::launch_q8_attention(a, d_workspace, ctx->num_sms, stream);
+  return (tq_status)tq::launch_q8_attention(a, d_workspace, ws_bytes, ctx->num_sms, stream);
 }
 
 tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *dst, int batch, int heads_kv,

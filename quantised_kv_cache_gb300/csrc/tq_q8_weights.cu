@@ -441,7 +441,9 @@ __global__ void __launch_bounds__(256) q8_weights_sum_kernel(const __grid_consta
   a.weights[at] = (a.weights_in ? a.weights_in[at] : 0.f) + x;
 }
 
-// Row tiles, splits and workspace for tokens up to max_len. Two CTAs an SM where at least four row tiles each remain.
+// Row tiles, splits and workspace for tokens up to max_len. Two CTAs an SM where at least four row tiles each remain. The sums of splits
+// are fewer than 4 num_sms CTAs' (splits x CTAs < 2 num_sms + CTAs, and there are fewer than 2 num_sms CTAs to split): room for
+// so many is counted whatever max_len is, so that a longer call's workspace serves a shorter one.
 Many many_of(int num_sms, int batch, int heads_kv, int group, int n_q, int max_len, size_t *bytes) {
   Many w{};
   const long long rts = ((long long)group * n_q + kTileRows - 1) / kTileRows, bh = (long long)batch * heads_kv;
@@ -449,7 +451,7 @@ Many many_of(int num_sms, int batch, int heads_kv, int group, int n_q, int max_l
   long long splits = (2LL * num_sms + ctas - 1) / ctas;
   if (splits > (rts + 3) / 4) splits = (rts + 3) / 4;
   w.rts = (int)rts, w.splits = (int)splits, w.slots = (max_len + kTokens - 1) / kTokens * kTokens;
-  *bytes = (size_t)bh * rts * (tile_bytes(3) + sizeof(int4)) + (splits > 1 ? (size_t)splits * bh * w.slots * sizeof(float) : 0);
+  *bytes = (size_t)bh * rts * (tile_bytes(3) + sizeof(int4)) + (rts > 4 ? 4 * (size_t)num_sms * kTokens * sizeof(float) : 0);
   return w;
 }
 

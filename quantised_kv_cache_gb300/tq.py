@@ -510,9 +510,12 @@ def tq_q8_append(ctx, cache: "Cache", k: torch.Tensor, v: torch.Tensor, seq_lens
 
 
 def tq_q8_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, max_len: int,
-                              weights: bool = False) -> int:
+                              weights: bool = False, out_dtype: Optional[torch.dtype] = None) -> int:
+    """Bytes for calls of these sizes and of smaller ones. `out_dtype`: the results' type, where it is known; calls with weights and
+    16-bit results may need less."""
+    kind = 0 if not weights else 1 if out_dtype in (None, torch.float32) else 2
     out = _sz()
-    check(lib().tq_q8_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_len, int(weights), ctypes.byref(out)),
+    check(lib().tq_q8_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_len, kind, ctypes.byref(out)),
           "tq_q8_attention_workspace")
     return out.value
 
@@ -543,7 +546,7 @@ def tq_q8_attention(ctx, cache: "Cache", q: torch.Tensor, seq_lens: torch.Tensor
     elif out.shape != shape or out.get_device() != index or out_dtype not in (None, out.dtype):
         raise ValueError("out: q's shape and device are wanted")
     if workspace is None:
-        workspace = _made(stream, torch.empty, tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None),
+        workspace = _made(stream, torch.empty, tq_q8_attention_workspace(ctx, B, Hq, H, n, max_len, weights is not None, out.dtype),
                           dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on q's device is wanted")

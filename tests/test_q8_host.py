@@ -154,3 +154,59 @@ def test_eviction_outputs_that_overlap(ctx):
     assert evict(ctx, dst_positions=(1 << 33) + kept - 4) == tq.TQ_ERR_ARG
     assert evict(ctx, dst_lens=(1 << 33) + 4) == tq.TQ_ERR_ARG
     assert evict(ctx, positions=None, dst_weights=None, dst_positions=None) == TAKEN
+
+
+# ------------------------------------------------------------------------------------------------ workspaces
+
+def size(ctx, n_q, max_len, batch=8, heads_q=32, heads_kv=8, weights=1):
+    out = ctypes.c_size_t()
+    assert tq.lib().tq_q8_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_len, weights, ctypes.byref(out)) == tq.TQ_OK
+    return out.value
+
+
+def fits(ctx, ws, n_q, max_len, batch=8, heads_q=32, heads_kv=8, weights=1, out_dtype=tq.TQ_BF16):
+    w = dict(d_weights=1 << 45) if weights else {}
+    return attention(ctx, cache(batch, heads_kv, max(max_len, 1 << 19)), ws_bytes=ws, batch=batch, heads_q=heads_q, heads_kv=heads_kv, n_q=n_q,
+                     max_len=max_len, out_dtype=out_dtype, d_out=1 << 46, **w)
+
+
+@pytest.mark.parametrize("weights", [0, 1])
+def test_a_larger_calls_workspace_serves_the_smaller_ones(ctx, weights):
+    """Every size below, in each of sequences, query tokens and slots, whatever the results' type."""
+    sizes = [(b, n, m) for b in (1, 3, 16) for n in (1, 2, 4, 5, 8, 16, 17, 40, 512, 2048)
+             for m in (1, 1000, 9728, 9984, 19456, 100000, 131072, 524288)]
+    for big in [(16, 2048, 524288), (16, 17, 524288), (3, 512, 19456), (16, 40, 9984), (3, 4, 131072), (1, 16, 100000)]:
+        ws = size(ctx, big[1], big[2], big[0], weights=weights)
+        assert fits(ctx, ws, big[1], big[2], big[0], weights=weights) == TAKEN
+        for b, n, m in sizes:
+            if b <= big[0] and n <= big[1] and m <= big[2]:
+                for dt in (tq.TQ_BF16, tq.TQ_F32):
+                    assert fits(ctx, ws, n, m, b, weights=weights, out_dtype=dt) == TAKEN, (big, b, n, m, dt)
+                assert fits(ctx, ws, n, m, b, weights=0) == TAKEN
+
+
+def test_workspaces_of_long_and_of_many_row_calls(ctx):
+    ws = size(ctx, 512, 131072, 8)
+    assert fits(ctx, ws, 1, 131072, 8) == TAKEN
+    ws = size(ctx, 1, 524416, 16)
+    assert fits(ctx, ws, 1, 524288, 16) == TAKEN
+
+
+def test_no_room_for_scores_that_are_not_kept(ctx):
+    """17 to 64 rows with 16-bit results: their scores are formed again, and a sizing call that says so has no room for them."""
+    scores = 32 * 16 * 131072 * 4
+    both, half = size(ctx, 16, 131072, 1, weights=1), size(ctx, 16, 131072, 1, weights=2)
+    assert both > scores and half < scores // 4
+    assert fits(ctx, half, 16, 131072, 1) == TAKEN
+    assert size(ctx, 4, 131072, 1, weights=2) == size(ctx, 4, 131072, 1, weights=1) > 32 * 4 * 131072 * 4  # up to 16 rows they are kept
+    for bad in (-1, 3):
+        out = ctypes.c_size_t()
+        assert tq.lib().tq_q8_attention_workspace(ctx, 1, 8, 8, 1, 100, bad, ctypes.byref(out)) == tq.TQ_ERR_ARG
+
+
+@pytest.mark.parametrize("n_q", [1, 4, 17, 300])
+def test_workspaces_that_are_too_small_are_refused(ctx, n_q):
+    for weights in (0, 1):
+        ws = size(ctx, n_q, 5000, weights=weights)
+        assert fits(ctx, ws, n_q, 5000, weights=weights) == TAKEN
+        assert fits(ctx, 2_000_000, n_q, 5000, weights=weights) == tq.TQ_ERR_WORKSPACE  # below the partial records alone
