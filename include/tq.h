@@ -517,8 +517,8 @@ tq_status tq_selftest_bounded_wait(const tq_ctx *ctx, unsigned long long budget_
  * and s = min(max((r - low) / (high - low), 0), 1), f_i becomes
  * (1 - s) f_i / factor + s f_i (slow pairs are interpolated, fast ones kept;
  * low = high = 0 divides every f_i by the factor). Positions are whole numbers of
- * any sign; angles are formed in 64-bit fixed point, so they are as exact at
- * position 2^31 as at 1. Copied by value: nothing is allocated, and calls already
+ * any sign; angles are formed in 64-bit fixed point from frequencies of
+ * 64 bits and are within 2^-31 turns at every position. Copied by value: nothing is allocated, and calls already
  * enqueued or captured keep the rotation they were made with. */
 typedef struct tq_rope {
   int dim, interleaved;

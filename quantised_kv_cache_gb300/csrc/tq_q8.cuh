@@ -115,7 +115,7 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[N]) {
 }
 
 // cos and sin of 2 pi (pos * freq mod 1), freq in units of 2^-64 turns: the 64-bit product wraps at
-// whole turns, so the angle is exact to 2^-32 turns at any position. The top 2 bits (rounded) are the
+// whole turns, so the angle is off by less than 2^-32 turns from its cut and 2^-34, half a unit of freq 2^31 times, at any position. The top 2 bits (rounded) are the
 // quadrant; the rest, |x| <= pi / 4, is kept in two parts (x + lo: the integer and 2 pi / 2^32 each split where
 // float32 ends) and goes through the Taylor polynomials of sine (to x^9, the next
 // term is below 2e-9) and cosine (to x^10, below 2e-10), so that little more than the last rounding is lost.

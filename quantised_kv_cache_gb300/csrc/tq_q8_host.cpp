@@ -101,6 +101,38 @@ bool overlap(const Region &a, const Region &b) {
 // A buffer that is updated in place, or regions that lie apart.
 bool same_or_apart(const Region &a, const Region &b) { return a.p == b.p || !overlap(a, b); }
 
+// Numbers of about 106 bits, as sums of two doubles (Dekker, "A floating-point technique for extending the available precision",
+// 1971; Knuth's two-sum): a frequency is needed to 2^-64 turns.
+struct Long {
+  double hi, lo;
+};
+Long two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Long operator+(Long a, Long b) {
+  const Long s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + a.lo + b.lo);
+}
+Long operator-(Long a, Long b) { return a + Long{-b.hi, -b.lo}; }
+Long operator*(Long a, Long b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Long operator/(Long a, Long b) {
+  const double q = a.hi / b.hi;
+  const Long r = a - Long{q, 0.0} * b;
+  const double q1 = r.hi / b.hi;
+  const Long r1 = r - Long{q1, 0.0} * b;
+  return two_sum(q, q1) + Long{r1.hi / b.hi, 0.0};
+}
+Long power(Long x, int n) {
+  Long y{1.0, 0.0};
+  for (; n; n >>= 1, x = x * x)
+    if (n & 1) y = y * x;
+  return y;
+}
+
 }  // namespace
 
 namespace tq {
@@ -138,24 +170,33 @@ tq_status tq_set_rope(tq_ctx *ctx, const tq_rope *r) {
       !(r->gain > 0.0) || !std::isfinite(r->gain) || !std::isfinite(r->low) || !std::isfinite(r->high))
     return TQ_ERR_ARG;
   const bool even = r->low == 0.0 && r->high == 0.0;  // every pair divided by the factor
-  if (r->factor > 1.0 && !even && (!(r->original_len > 0.0) || !std::isfinite(r->original_len) || !(r->high > r->low)))
+  if (r->factor > 1.0 && !even && (!(r->original_len > 0.0) || !std::isfinite(r->original_len) || !(r->high > r->low) || !std::isfinite(r->high - r->low)))
     return TQ_ERR_ARG;
   tq::RopeTable t;
   t.dim = r->dim;
   t.interleaved = r->interleaved ? 1 : 0;
   t.gain = (float)r->gain;
-  const double two_pi = 6.283185307179586476925286766559;
-  for (int i = 0; i < r->dim / 2; ++i) {
-    double f = std::pow(r->base, -2.0 * i / r->dim);
+  const Long two_pi{6.283185307179586, 2.4492935982947064e-16}, one{1.0, 0.0};
+  // f_1 = base^(-2 / dim) by a step of Newton's for f_1^(dim / 2) = 1 / base from its double; the others are its powers
+  const int pairs = r->dim / 2;
+  const Long guess{std::pow(r->base, -1.0 / pairs), 0.0}, there = power(guess, pairs);
+  const Long ratio = guess + guess * (one / Long{r->base, 0.0} - there) / (there * Long{(double)pairs, 0.0});
+  Long f{1.0, 0.0};
+  for (int i = 0; i < pairs; ++i, f = f * ratio) {
+    Long g = f;
     if (r->factor > 1.0) {
-      double keep = 0.0;
+      Long keep{0.0, 0.0};
       if (!even) {
-        keep = (r->original_len * f / two_pi - r->low) / (r->high - r->low);
-        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        const double about = (r->original_len * f.hi / two_pi.hi - r->low) / (r->high - r->low);  // (may be infinite)
+        if (about > -1.0 && about < 2.0) keep = (Long{r->original_len, 0.0} * f / two_pi - Long{r->low, 0.0}) / two_sum(r->high, -r->low);
+        else keep.hi = about;
+        keep = keep.hi < 0.0 ? Long{0.0, 0.0} : keep.hi >= 1.0 ? one : keep;
       }
-      f = (1.0 - keep) * f / r->factor + keep * f;
+      g = (one - keep) * f / Long{r->factor, 0.0} + keep * f;
     }
-    t.freq[i] = (unsigned long long)std::llrint(std::ldexp(f / two_pi, 63)) * 2ull;  // f <= 1 rad: below 2^62
+    const Long turns = g / two_pi;  // at most 1 / (2 pi)
+    const double hi = std::ldexp(turns.hi, 64), whole = std::floor(hi);
+    t.freq[i] = (unsigned long long)whole + (unsigned long long)std::llrint(hi - whole + std::ldexp(turns.lo, 64));
   }
   ctx->rope = t;
   return TQ_OK;

@@ -210,3 +210,36 @@ def test_workspaces_that_are_too_small_are_refused(ctx, n_q):
         ws = size(ctx, n_q, 5000, weights=weights)
         assert fits(ctx, ws, n_q, 5000, weights=weights) == TAKEN
         assert fits(ctx, 2_000_000, n_q, 5000, weights=weights) == tq.TQ_ERR_WORKSPACE  # below the partial records alone
+
+
+# ------------------------------------------------------------------------------------------------ frequencies
+
+def exact_turns(dim, base=10000.0, factor=1.0, original_len=0.0, low=0.0, high=0.0):
+    """2^64 f_i / (2 pi) in 60 decimal digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    base, factor, original_len, low, high = (Decimal(x) for x in (base, factor, original_len, low, high))
+    out = []
+    for i in range(dim // 2):
+        f = (-(Decimal(2 * i) / dim) * base.ln()).exp()
+        if factor > 1:
+            keep = Decimal(0)
+            if low or high:
+                keep = min(max((original_len * f / two_pi - low) / (high - low), Decimal(0)), Decimal(1))
+            f = (1 - keep) * f / factor + keep * f
+        out.append(f / two_pi * 2 ** 64)
+    return out
+
+
+@pytest.mark.parametrize("kw", [dict(dim=128), dict(dim=64, base=500000.0), dict(dim=72, base=1e6), dict(dim=8, base=1.0000001), dict(dim=128, base=1e300),
+                                dict(dim=128, base=37.3, factor=7.3), dict(dim=128, base=500000.0, factor=8.0, original_len=8192.0, low=1.0, high=4.0),
+                                dict(dim=96, base=1e4, factor=31.7, original_len=4096.5, low=0.7, high=32.1),
+                                dict(dim=64, factor=2.0, original_len=1e308, low=0.0, high=1e-300)], ids=str)
+def test_frequencies_to_the_last_of_64_bits(ctx, kw):
+    """A position turns by its multiple of the frequency, so that an error of the frequency grows to 2^31 times itself: it is half a unit
+    of 2^-64 turns (and what 106-bit arithmetic leaves), 2^-34 turns at the farthest position."""
+    tq.tq_set_rope(ctx, **kw)
+    turns = ctx.turns()
+    for i, want in enumerate(exact_turns(**kw)):
+        assert abs(int(turns[i]) - want) <= 0.51, (i, float(int(turns[i]) - want))
