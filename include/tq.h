@@ -588,7 +588,8 @@ typedef struct tq_q8_attn {
  * and no more sequences, query tokens and max_len. With weights there is room for the scores of calls that keep them; where a workspace has
  * none they are formed again (slower; the weights' last bits may differ). A d_seq_lens[b] outside [0, max_len] or a d_new_lens[b]
  * outside [0, n_q] is cut to that range, and a bad block-table entry's tokens are
- * taken as unseen; both set the device error word to TQ_ERR_ARG. Rounding: the
+ * taken as unseen; both set the device error word to TQ_ERR_ARG. (Blocks before the first and past the last slot that
+ * a sequence's query tokens see need no entry.) Rounding: the
  * products of codes with 16-bit queries are exact, their sums fp32. A probability
  * enters the value sums with 24 significant bits when out_dtype is TQ_F32, else with 12
  * for up to 16 query rows (n_q x group) per KV head; one below 2^-8 (2^-20) of the row's

@@ -47,7 +47,7 @@ constexpr int rows_of(int T) { return T == 8 ? 8 : 16; }  // rows of a unit: wha
 
 struct Entries {
   int pre[kEntries + 1];  // tiles (of one head) before each entry
-  int lo[kEntries];       // its first tile
+  int lo[kEntries];       // its first visible slot
   int hi[kEntries];       // one past its last visible slot
 };
 
@@ -115,7 +115,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     if (hi == 0) lo = 0;
     // an entry whose rows see nothing keeps one (empty) tile, so that its zeros are written
     count = i0 < m ? max(1, (hi + kTile - 1) / kTile - lo / kTile) : 0;
-    sm.ent.lo[tid] = lo / kTile;
+    sm.ent.lo[tid] = lo;
     sm.ent.hi[tid] = hi;
   }
   {
@@ -169,12 +169,12 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       if (g + lane < g1) {
         int e, h, t, cnt;
         locate(g + lane, e, h, t, cnt);
-        const int tok = (sm.ent.lo[e] + t) * kTile, n = min(kTile, max(0, sm.ent.hi[e] - tok));
+        const int lo = sm.ent.lo[e], tok = (lo / kTile + t) * kTile, n = min(kTile, max(0, sm.ent.hi[e] - tok));
         const long long v = ((long long)(b0 + e / rts) * a.heads_kv + h) * a.c.nblk + tok / kQ8Block;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int m = min(kQ8Block, n - k * kQ8Block);
-          if (m <= 0) continue;
+          if (m <= 0 || tok + (k + 1) * kQ8Block <= lo) continue;  // no row sees a token of it
           src[k] = q8_block(a.c.btab, a.c.pool_blocks, v + k, a.error);
           if (src[k] < 0) continue;
           bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
@@ -235,7 +235,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       locate(g, e, h, t0, cnt);
       const int b = b0 + e / rts, row0 = (rt0 + e % rts) * kUnitRows;
       const long long end = min(g1, g - t0 + cnt);
-      const int first = sm.ent.lo[e], hi = sm.ent.hi[e];
+      const int first = sm.ent.lo[e] / kTile, hi = sm.ent.hi[e];
 
       // ---- the unit's queries: warp w prepares row w
       {

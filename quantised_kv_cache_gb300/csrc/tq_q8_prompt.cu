@@ -47,7 +47,7 @@ constexpr float kLowest = -3e38f;      // in place of a maximum of -inf: an unse
 constexpr int stages_of(int terms, bool apart) { return terms == 2 || apart ? 4 : 3; }
 
 struct Entry {
-  int lo, hi;          // first tile, one past the last visible slot
+  int lo, hi;          // first visible slot, one past the last
   int maxbeg, minend;  // slots in [maxbeg, minend) are seen by every row that is written
 };
 
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__
   minend = __reduce_min_sync(kFull, minend);
   if (lane == 0) {
     if (hi == 0) lo = 0;
-    p.entry[e] = Entry{lo / kTile, hi, maxbeg, minend};
+    p.entry[e] = Entry{lo, hi, maxbeg, minend};
     // rows that see nothing keep one tile, so that their zeros are written
     p.pre[e + 1] = i0 < m ? max(1, (hi + kTile - 1) / kTile - lo / kTile) : 0;
   }
@@ -291,11 +291,11 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
           int bytes[2] = {0, 0};
           if (lane < todo) {
-            const int tok = (en.lo + u.t0 + k0 + lane) * kTile, n = min(kTile, max(0, en.hi - tok));
+            const int tok = (en.lo / kTile + u.t0 + k0 + lane) * kTile, n = min(kTile, max(0, en.hi - tok));
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int m = min(kQ8Block, n - k * kQ8Block);
-              if (m <= 0) continue;
+              if (m <= 0 || tok + (k + 1) * kQ8Block <= en.lo) continue;  // no row sees a token of it
               src[k] = q8_block(a.c.btab, a.c.pool_blocks, blocks + tok / kQ8Block + k, a.error);
               if (src[k] < 0) continue;
               bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
@@ -347,7 +347,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         int it = 0;
         for (long long g = g0; g < g1; ++units) {
           const Unit u = unit_at(p, a.heads_kv, g, g1);
-          const int first = p.entry[u.e].lo + u.t0, hi = p.entry[u.e].hi, todo = (int)(u.end - g);
+          const int first = p.entry[u.e].lo / kTile + u.t0, hi = p.entry[u.e].hi, todo = (int)(u.end - g);
           wait(&sm.bar_q[rt], units & 1);
           for (int j = 0; j <= todo; ++j) {
             // the value sums of tile j - 1, then the scores of tile j over its probabilities: in this order, as issued
@@ -419,7 +419,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
     long long g = g0;
     while (g < g1) {
       const Unit u = unit_at(p, a.heads_kv, g, g1);
-      const int first = p.entry[u.e].lo + u.t0, hi = p.entry[u.e].hi, maxbeg = p.entry[u.e].maxbeg,
+      const int first = p.entry[u.e].lo / kTile + u.t0, hi = p.entry[u.e].hi, maxbeg = p.entry[u.e].maxbeg,
                 minend = p.entry[u.e].minend;
       const long long bh = (long long)u.b * a.heads_kv + u.h;
       int len, m;

@@ -4,6 +4,7 @@
 //
 // q8_kept_kernel: the attention for few rows has kept its scores (4 bytes a row and token, beside the 256 of the cache that it
 // reads); a thread adds up 4 tokens' probabilities over the rows. Bound by those scores' bytes: 10 us for 6 rows of 4 x 16383 tokens and 8 heads.
+// (Blocks without a place in the pool are reported by the attention, where a row sees them; here they are left out.)
 // Else, after the attention has left each row's lse, the scores are formed again from the keys alone: token = accumulator lane =
 // thread, which adds its own token's probabilities over all rows in registers.
 // q8_weights_many_kernel, 16-bit results: a CTA holds the keys of 256 tokens; row tiles of 128 queries (their terms made once, by
@@ -72,14 +73,14 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   // the keys of the tile's two blocks; a block that is not mapped stays unread and unseen
   float ks = -1.f;
   if (wt < n) {
-    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + (tok0 + wt) / kQ8Block, a.error);
+    const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + (tok0 + wt) / kQ8Block, nullptr);
     if (blk >= 0) ks = __ldg(a.c.ks + blk);
   }
   if (tid == 0) {
     int bytes = 0;
     long long src[2] = {-1, -1};
     for (int k = 0; k < 2 && k * kQ8Block < n; ++k) {
-      src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok0 / kQ8Block + k, a.error);
+      src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok0 / kQ8Block + k, nullptr);
       if (src[k] >= 0) bytes += kQ8Plane;
     }
     mbar_arrive_expect_tx(&sm.full, bytes);
@@ -284,7 +285,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
     // ================================ copies: the keys, then every row tile that sees a token of them
     long long src = -1;
     if (lane < kTokens / kQ8Block && lane * kQ8Block < n)
-      src = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok0 / kQ8Block + lane, a.error);
+      src = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + tok0 / kQ8Block + lane, nullptr);
     const int planes = __popc(__ballot_sync(kFull, src >= 0));
     if (lane == 0) mbar_arrive_expect_tx(&sm.keys, planes * kQ8Plane);
     __syncwarp();
@@ -349,7 +350,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
     const int tt = warp >> 3, half = (warp >> 2) & 1, tok = tt * kTile + (tid & 127), slot = tok0 + tok;
     float ks = -1.f;
     if (tok < n) {
-      const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + slot / kQ8Block, a.error);
+      const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + slot / kQ8Block, nullptr);
       if (blk >= 0) ks = __ldg(a.c.ks + blk);
     }
     const int kp = EXTRA && a.kpos && tok < n ? __ldg(a.kpos + at + tok) : slot;
