@@ -747,7 +747,7 @@ tq_status tq_cache_bytes(const tq_ctx *ctx, int batch, int heads_kv, int capacit
 tq_status tq_append_quantize(const tq_ctx *ctx, const tq_cache *cache, const void *d_k, const void *d_v,
                              int dtype, int batch, int heads_kv, int n_new, const int32_t *d_seq_lens,
                              void *stream) {
-  if (!ctx || !d_k || !d_v || !d_seq_lens) return TQ_ERR_ARG;
+  if (!ctx || !d_seq_lens || (n_new != 0 && (!d_k || !d_v))) return TQ_ERR_ARG;
   if (dtype != TQ_F32 && dtype != TQ_BF16) return TQ_ERR_ARG;
   if (batch <= 0 || heads_kv <= 0 || n_new < 0) return TQ_ERR_ARG;
   tq_status s = check_cache(ctx, cache, batch, heads_kv);

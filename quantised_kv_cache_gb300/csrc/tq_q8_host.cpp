@@ -204,9 +204,11 @@ tq_status tq_set_rope(tq_ctx *ctx, const tq_rope *r) {
 
 tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides, void *d_y, const int64_t *y_strides,
                     int dtype, int batch, int heads, int n, const int32_t *d_positions, int transpose, void *stream) {
-  if (!ctx || !d_x || !d_y || !x_strides || !y_strides || !d_positions) return TQ_ERR_ARG;
+  if (!ctx || !x_strides || !y_strides) return TQ_ERR_ARG;
   if (!known(dtype) || batch <= 0 || heads <= 0 || n < 0 || (transpose != 0 && transpose != 1)) return TQ_ERR_ARG;
   if (!ctx->rope.dim) return TQ_ERR_STATE;
+  if (n == 0) return on_device(ctx);  // no vectors, which then have no addresses
+  if (!d_x || !d_y || !d_positions) return TQ_ERR_ARG;
   if (!aligned16(d_x) || !aligned16(d_y) || !strides_ok(x_strides, dtype) || !strides_ok(y_strides, dtype))
     return TQ_ERR_ALIGN;
   if (!spread(y_strides, batch, heads, n)) return TQ_ERR_ARG;
@@ -215,7 +217,6 @@ tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides
     return TQ_ERR_ARG;
   const tq_status s = on_device(ctx);
   if (s != TQ_OK) return s;
-  if (n == 0) return TQ_OK;
   const tq::RotaryArgs a{d_x, d_y, strides(x_strides), strides(y_strides), dtype, batch, heads, n, transpose,
                          d_positions, ctx->rope};
   return (tq_status)tq::launch_rotary(a, ctx->num_sms, stream);
@@ -225,15 +226,16 @@ tq_status tq_q8_append(const tq_ctx *ctx, const tq_cache *cache, const void *d_k
                        const void *d_v, const int64_t *v_strides, int dtype, int batch, int heads_kv, int n_new,
                        const int32_t *d_seq_lens, const int32_t *d_new_lens, int rope, const int32_t *d_positions,
                        void *stream) {
-  if (!ctx || !d_k || !d_v || !k_strides || !v_strides || !d_seq_lens) return TQ_ERR_ARG;
+  if (!ctx || !k_strides || !v_strides || !d_seq_lens) return TQ_ERR_ARG;
   if (!known(dtype) || batch <= 0 || heads_kv <= 0 || n_new < 0 || (rope != 0 && rope != 1)) return TQ_ERR_ARG;
   tq_status s = tq::q8_check_cache(ctx, cache, batch, heads_kv);
   if (s != TQ_OK) return s;
   if (rope && !ctx->rope.dim) return TQ_ERR_STATE;
+  if (n_new == 0) return on_device(ctx);
+  if (!d_k || !d_v) return TQ_ERR_ARG;
   if (!aligned16(d_k) || !aligned16(d_v) || !strides_ok(k_strides, dtype) || !strides_ok(v_strides, dtype))
     return TQ_ERR_ALIGN;
   if ((s = on_device(ctx)) != TQ_OK) return s;
-  if (n_new == 0) return TQ_OK;
   const tq::Q8AppendArgs a{tq::q8_cache(cache), d_k, d_v, strides(k_strides), strides(v_strides), dtype, batch, heads_kv,
                            n_new, rope, d_seq_lens, d_new_lens, d_positions, &ctx->dparams->error, ctx->rope};
   return (tq_status)tq::launch_q8_append(a, ctx->num_sms, stream);

@@ -243,3 +243,21 @@ def test_frequencies_to_the_last_of_64_bits(ctx, kw):
     turns = ctx.turns()
     for i, want in enumerate(exact_turns(**kw)):
         assert abs(int(turns[i]) - want) <= 0.51, (i, float(int(turns[i]) - want))
+
+
+# ------------------------------------------------------------------------------------------------ nothing to do
+
+def test_calls_of_no_tokens_need_no_vectors(ctx):
+    """A tensor without elements has no address. (As they have nothing to enqueue the calls end at the device's check.)"""
+    L, s = tq.lib(), S(0, 0, 0)
+    c = ctypes.byref(cache())
+    assert L.tq_rotary(ctx, None, s, None, s, tq.TQ_BF16, 2, 4, 0, None, 0, None) == TAKEN
+    assert L.tq_q8_append(ctx, c, None, s, None, s, tq.TQ_BF16, 2, 4, 0, 1 << 30, None, 0, None, None) == TAKEN
+    assert L.tq_append_quantize(ctx, c, None, None, tq.TQ_BF16, 2, 4, 0, 1 << 30, None) == tq.TQ_OK
+    # with tokens they do
+    assert L.tq_rotary(ctx, None, s, ELSEWHERE, s, tq.TQ_BF16, 1, 1, 1, 1 << 30, 0, None) == tq.TQ_ERR_ARG
+    assert L.tq_rotary(ctx, BASE, s, ELSEWHERE, s, tq.TQ_BF16, 1, 1, 1, None, 0, None) == tq.TQ_ERR_ARG
+    assert L.tq_q8_append(ctx, c, BASE, s, None, s, tq.TQ_BF16, 2, 4, 1, 1 << 30, None, 0, None, None) == tq.TQ_ERR_ARG
+    # and other arguments are checked all the same
+    assert L.tq_rotary(ctx, None, s, None, s, 7, 2, 4, 0, None, 0, None) == tq.TQ_ERR_ARG
+    assert L.tq_q8_append(ctx, c, None, s, None, s, tq.TQ_BF16, 2, 4, 0, None, None, 0, None, None) == tq.TQ_ERR_ARG
