@@ -671,6 +671,7 @@ tq_status tq_cache_sizes_get(const tq_ctx *ctx, int batch, int heads_kv, int cap
   if (!ctx || !out || batch <= 0 || heads_kv <= 0 || capacity <= 0) return TQ_ERR_ARG;
   std::memset(out, 0, sizeof(*out));
   if (ctx->scheme == TQ_SCHEME_Q8) {
+    if (capacity > tq::kQ8MostSlots) return TQ_ERR_UNSUPPORTED;
     tq::q8_cache_sizes(batch, heads_kv, capacity, out);
     return TQ_OK;
   }

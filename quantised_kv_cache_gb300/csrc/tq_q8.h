@@ -12,6 +12,7 @@ constexpr int kQ8Block = 64;                   // token slots of a block
 constexpr int kQ8Plane = kQ8Block * kD;        // bytes of its key (or value) plane
 constexpr int kQ8BlockBytes = 2 * kQ8Plane;
 constexpr int kQ8MinExp = -100;                // smallest exponent of a block's scale
+constexpr int kQ8MostSlots = 0x7fffffff - 1023;  // of a sequence: the ends of its last block and tile stay within 32 bits
 
 inline int q8_blocks_of(int capacity) { return (capacity + kQ8Block - 1) / kQ8Block; }
 
@@ -92,6 +93,9 @@ struct Q8AttnArgs {
 // The workspace with room for all that is worth keeping; *least (if not NULL): what the call cannot do without, which never falls as
 // the batch, the query tokens or max_len grow. `weights`: 0 none, 1 with results of either size, 2 with results of 16 bits
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights, size_t *least);
+// the units and tiles of this call, and the workspace's, fit into the kernels' 32-bit numbers
+bool q8_attention_fits(const Q8AttnArgs &a, int num_sms);
+bool q8_prompt_fits(const Q8AttnArgs &a, int num_sms);
 size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q);
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 // `terms`: of the queries, where 16-bit results' scores were not kept

@@ -549,11 +549,19 @@ size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv,
   return scores ? std::max(need, lse + scores + few_bytes(num_sms)) : need;
 }
 
+static bool few_rows(const Q8AttnArgs &a) { return (long long)a.group * a.n_q <= kFewRows || a.out_dtype == TQ_F32; }
+
+bool q8_attention_fits(const Q8AttnArgs &a, int num_sms) {
+  if ((long long)a.group * a.n_q > 0x7fffffff - 1023) return false;                // a KV head's rows
+  if (a.weights && (a.heads_kv > 65535 || a.batch > 65535)) return false;          // grid dimensions of the weights' launches
+  return few_rows(a) || q8_prompt_fits(a, num_sms);
+}
+
 int launch_q8_attention(const Q8AttnArgs &args, void *workspace, size_t ws_bytes, int num_sms, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   Q8AttnArgs a = args;
   const long long R = (long long)a.group * a.n_q;
-  const bool few = R <= kFewRows || a.out_dtype == TQ_F32;
+  const bool few = few_rows(a);
   char *w = (char *)workspace;
   if (a.weights) {
     if (!a.lse) a.lse = (float *)w;
@@ -571,12 +579,14 @@ int launch_q8_attention(const Q8AttnArgs &args, void *workspace, size_t ws_bytes
     Cut *cuts = (Cut *)w;
     a.parts = (float *)(w + round16((size_t)num_sms * sizeof(Cut)));
     const int unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
-    if ((R + unit - 1) / unit > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
-    const int all = (int)((R + unit - 1) / unit);  // row tiles of a sequence; at most kEntries of all in a launch
-    const int per = all < kEntries ? kEntries / all : 1;
+    const int all = (int)((R + unit - 1) / unit);  // row tiles of a sequence
+    // (sequence, row tile) pairs of a launch: as many as their table holds, and as keep the number of their tiles within 32 bits
+    const long long tiles = (a.max_len + kTile - 1) / kTile;
+    const int most = tiles * kEntries <= 0x7fffffff ? kEntries : (int)(0x7fffffff / tiles);
+    const int per = all < most ? most / all : 1;
     for (int b0 = 0; b0 < a.batch; b0 += per)
-      for (int rt0 = 0; rt0 < all; rt0 += kEntries) {
-        const int nb = a.batch - b0 < per ? a.batch - b0 : per, rts = all - rt0 < kEntries ? all - rt0 : kEntries;
+      for (int rt0 = 0; rt0 < all; rt0 += most) {
+        const int nb = a.batch - b0 < per ? a.batch - b0 : per, rts = all - rt0 < most ? all - rt0 : most;
         int s;
         if (a.out_dtype == TQ_F32)
           s = R == 1 ? launch_rows<1, 8>(a, cuts, b0, nb, rt0, rts, num_sms, st)

@@ -140,6 +140,7 @@ namespace tq {
 tq_status q8_check_cache(const tq_ctx *ctx, const tq_cache *c, int batch, int heads_kv) {
   if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
   if (!c || c->batch != batch || c->heads_kv != heads_kv || c->capacity <= 0) return TQ_ERR_ARG;
+  if (c->capacity > kQ8MostSlots) return TQ_ERR_UNSUPPORTED;
   if (!c->records || !c->k_stats || !c->v_stats) return TQ_ERR_ARG;
   if (!aligned16(c->records) || !aligned16(c->k_stats) || !aligned16(c->v_stats)) return TQ_ERR_ALIGN;
   if (c->block_table && c->pool_blocks <= 0) return TQ_ERR_ARG;
@@ -279,7 +280,6 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (overlap(q, out) || overlap(q, weights) || overlap(q, lse) || overlap(out, weights) || overlap(out, lse) || overlap(weights, lse) ||
       !same_or_apart(weights, bytes(p->d_weights_in, slots)))
     return TQ_ERR_ARG;
-  if ((s = on_device(ctx)) != TQ_OK) return s;
   tq::Q8AttnArgs a{};
   a.c = tq::q8_cache(cache);
   a.batch = p->batch, a.heads_q = p->heads_q, a.heads_kv = p->heads_kv, a.group = p->heads_q / p->heads_kv;
@@ -290,6 +290,8 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   a.softcap = p->softcap < kNoCap ? p->softcap : 0.f, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
   a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
   a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
+  if (!tq::q8_attention_fits(a, ctx->num_sms)) return TQ_ERR_UNSUPPORTED;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
   a.error = &ctx->dparams->error;
   return (tq_status)tq::launch_q8_attention(a, d_workspace, ws_bytes, ctx->num_sms, stream);
 }

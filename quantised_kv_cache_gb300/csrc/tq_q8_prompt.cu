@@ -793,11 +793,21 @@ size_t q8_prompt_workspace(int num_sms, int batch, int group, int n_q) {
          round16(slices * sizeof(Cut)) + slices * 2 * part_of(unit_rows(true)) * sizeof(float);
 }
 
+static long long units_of(const Q8AttnArgs &a, bool apart) {
+  const long long unit = unit_rows(apart);
+  return ((long long)a.group * a.n_q + unit - 1) / unit;
+}
+
+// Entries' tiles are counted in 32 bits.
+bool q8_prompt_fits(const Q8AttnArgs &a, int num_sms) {
+  const long long entries = units_of(a, units_apart(a, num_sms)) * a.batch, tiles = (a.max_len + kTile - 1) / kTile;
+  return entries <= 1 << 24 && entries * tiles <= 0x7fffffff;
+}
+
 int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream) {
   const bool apart = units_apart(a, num_sms);
-  const long long unit = unit_rows(apart), pairs = ((long long)a.group * a.n_q + unit - 1) / unit, entries = pairs * a.batch;
+  const long long unit = unit_rows(apart), pairs = units_of(a, apart), entries = pairs * a.batch;
   const int slices = apart ? 2 * num_sms : num_sms;
-  if (entries > 1 << 24) return TQ_ERR_UNSUPPORTED;
   Plan p;
   p.entries = (int)entries, p.pairs = (int)pairs, p.unit = (int)unit;
   char *w = (char *)workspace;

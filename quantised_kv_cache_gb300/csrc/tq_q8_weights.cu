@@ -534,7 +534,6 @@ int launch_q8_weights(const Q8AttnArgs &a, int terms, void *workspace, int num_s
   cudaStream_t st = (cudaStream_t)stream;
   // in place only the tokens in use are touched
   const int slots = a.weights == a.weights_in ? a.max_len : a.c.capacity;
-  if (a.heads_kv > 65535 || a.batch > 65535) return TQ_ERR_UNSUPPORTED;
   if (a.scores) {
     const dim3 grid((unsigned)((slots + 4LL * kKept - 1) / (4 * kKept)), (unsigned)a.heads_kv, (unsigned)a.batch);
     return launch_overlapped(true, q8_kept_kernel, grid, dim3(kKept), 0, st, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;

@@ -261,3 +261,27 @@ def test_calls_of_no_tokens_need_no_vectors(ctx):
     # and other arguments are checked all the same
     assert L.tq_rotary(ctx, None, s, None, s, 7, 2, 4, 0, None, 0, None) == tq.TQ_ERR_ARG
     assert L.tq_q8_append(ctx, c, None, s, None, s, tq.TQ_BF16, 2, 4, 0, None, None, 0, None, None) == tq.TQ_ERR_ARG
+
+
+# ------------------------------------------------------------------------------------------------ sizes past the kernels' indices
+
+def test_sizes_that_no_launch_or_index_holds_are_refused_before_anything_runs(ctx):
+    big = dict(ws_bytes=1 << 62)
+    for kw in (dict(batch=65536, heads_q=1, heads_kv=1, n_q=1), dict(batch=1, heads_q=65536, heads_kv=65536, n_q=1)):
+        c = cache(kw["batch"], kw["heads_kv"])
+        assert attention(ctx, c, d_out=1 << 50, **kw, **big) == TAKEN
+        assert attention(ctx, c, d_out=1 << 50, d_weights=1 << 52, **kw, **big) == tq.TQ_ERR_UNSUPPORTED
+    # rows of a KV head, and units x tiles, in 32 bits
+    most = 2 ** 31 - 1024
+    long = cache(1, 1, most)
+    assert attention(ctx, long, batch=1, heads_q=1, heads_kv=1, n_q=1, max_len=most, **big) == TAKEN
+    assert attention(ctx, cache(1, 1), batch=1, heads_q=64, heads_kv=1, n_q=1 << 26, d_out=1 << 60, **big) == tq.TQ_ERR_UNSUPPORTED
+    assert attention(ctx, long, batch=1, heads_q=1, heads_kv=1, n_q=129 * 256, max_len=most, **big) == tq.TQ_ERR_UNSUPPORTED
+    assert attention(ctx, long, batch=1, heads_q=1, heads_kv=1, n_q=128 * 256, max_len=most, **big) == TAKEN
+    # slots whose block or tile ends past 2^31
+    for capacity, want in ((most, TAKEN), (most + 1, tq.TQ_ERR_UNSUPPORTED), (2 ** 31 - 1, tq.TQ_ERR_UNSUPPORTED)):
+        c = cache(1, 1, capacity)
+        assert attention(ctx, c, batch=1, heads_q=1, heads_kv=1, n_q=1, max_len=64) == want
+        assert tq.lib().tq_q8_append(ctx, ctypes.byref(c), BASE, S(0, 0, 0), BASE, S(0, 0, 0), tq.TQ_BF16, 1, 1, 1, 1 << 30, None, 0, None, None) == want
+        out = tq.tq_cache_sizes()
+        assert tq.lib().tq_cache_sizes_get(ctx, 1, 1, capacity, ctypes.byref(out)) == (tq.TQ_OK if want == TAKEN else want)
