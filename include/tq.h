@@ -504,8 +504,9 @@ tq_status tq_selftest_bounded_wait(const tq_ctx *ctx, unsigned long long budget_
  * weights, log-sums, lengths and positions, but not tables, caches and workspaces.
  *
  * Strides are in elements, of the batch, head and token dimension in this order;
- * the d coordinates are contiguous. Every pointer must be 16-byte aligned and
- * every stride a multiple of 16 bytes (TQ_ERR_ALIGN otherwise).
+ * the d coordinates are contiguous. Vectors, cache planes and workspaces must be
+ * 16-byte aligned, every stride a multiple of 16 bytes, and arrays of lengths, ranges,
+ * positions, slopes, weights and log-sums 4-byte aligned (TQ_ERR_ALIGN otherwise).
  * ------------------------------------------------------------------------- */
 
 /* The rotation of positions that tq_rotary and tq_q8_append use. Pair i of the

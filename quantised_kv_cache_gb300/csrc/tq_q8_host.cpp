@@ -13,6 +13,12 @@ namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// arrays of 4-byte numbers (NULL among them)
+template <typename... P>
+bool aligned4(const P *...p) {
+  return ((((uintptr_t)p & 3u) == 0) && ...);
+}
+
 int size_of(int dtype) { return dtype == TQ_F32 ? 4 : 2; }
 
 bool known(int dtype) { return dtype == TQ_F32 || dtype == TQ_BF16 || dtype == TQ_F16; }
@@ -144,6 +150,7 @@ tq_status q8_check_cache(const tq_ctx *ctx, const tq_cache *c, int batch, int he
   if (!c->records || !c->k_stats || !c->v_stats) return TQ_ERR_ARG;
   if (!aligned16(c->records) || !aligned16(c->k_stats) || !aligned16(c->v_stats)) return TQ_ERR_ALIGN;
   if (c->block_table && c->pool_blocks <= 0) return TQ_ERR_ARG;
+  if (!aligned4(c->block_table)) return TQ_ERR_ALIGN;
   return TQ_OK;
 }
 
@@ -210,7 +217,7 @@ tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides
   if (!ctx->rope.dim) return TQ_ERR_STATE;
   if (n == 0) return on_device(ctx);  // no vectors, which then have no addresses
   if (!d_x || !d_y || !d_positions) return TQ_ERR_ARG;
-  if (!aligned16(d_x) || !aligned16(d_y) || !strides_ok(x_strides, dtype) || !strides_ok(y_strides, dtype))
+  if (!aligned16(d_x) || !aligned16(d_y) || !aligned4(d_positions) || !strides_ok(x_strides, dtype) || !strides_ok(y_strides, dtype))
     return TQ_ERR_ALIGN;
   if (!spread(y_strides, batch, heads, n)) return TQ_ERR_ARG;
   if (!(d_x == d_y && !std::memcmp(x_strides, y_strides, 3 * sizeof(int64_t))) &&
@@ -234,7 +241,8 @@ tq_status tq_q8_append(const tq_ctx *ctx, const tq_cache *cache, const void *d_k
   if (rope && !ctx->rope.dim) return TQ_ERR_STATE;
   if (n_new == 0) return on_device(ctx);
   if (!d_k || !d_v) return TQ_ERR_ARG;
-  if (!aligned16(d_k) || !aligned16(d_v) || !strides_ok(k_strides, dtype) || !strides_ok(v_strides, dtype))
+  if (!aligned16(d_k) || !aligned16(d_v) || !aligned4(d_seq_lens, d_new_lens, d_positions) || !strides_ok(k_strides, dtype) ||
+      !strides_ok(v_strides, dtype))
     return TQ_ERR_ALIGN;
   if ((s = on_device(ctx)) != TQ_OK) return s;
   const tq::Q8AppendArgs a{tq::q8_cache(cache), d_k, d_v, strides(k_strides), strides(v_strides), dtype, batch, heads_kv,
@@ -266,7 +274,9 @@ tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_
   if (s != TQ_OK) return s;
   if (p->max_len > cache->capacity) return TQ_ERR_ARG;
   if (!aligned16(p->d_q) || !aligned16(p->d_out) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
-      !strides_ok(p->out_strides, p->out_dtype))
+      !strides_ok(p->out_strides, p->out_dtype) ||
+      !aligned4(p->d_seq_lens, p->d_new_lens, p->d_slopes, p->d_q_positions, p->d_k_positions, p->d_key_begin, p->d_key_end, p->d_weights_in,
+                p->d_weights, p->d_lse))
     return TQ_ERR_ALIGN;
   size_t least = 0;
   tq::q8_attention_workspace(ctx->num_sms, p->batch, p->heads_q, p->heads_kv, p->n_q, p->max_len, p->d_weights != nullptr, &least);
@@ -305,6 +315,7 @@ tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *ds
   if (s == TQ_OK) s = tq::q8_check_cache(ctx, dst, batch, heads_kv);
   if (s != TQ_OK) return s;
   if (keep <= 0 || sink < 0 || recent < 0 || (long long)sink + recent > keep || keep > dst->capacity) return TQ_ERR_ARG;
+  if (!aligned4(d_seq_lens, d_weights, d_positions, d_kept, d_dst_lens, d_dst_weights, d_dst_positions)) return TQ_ERR_ALIGN;
   const size_t grid = (size_t)batch * heads_kv;
   const size_t sn = src->block_table ? (size_t)src->pool_blocks : grid * tq::q8_blocks_of(src->capacity);
   const size_t dn = dst->block_table ? (size_t)dst->pool_blocks : grid * tq::q8_blocks_of(dst->capacity);

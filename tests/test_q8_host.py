@@ -285,3 +285,30 @@ def test_sizes_that_no_launch_or_index_holds_are_refused_before_anything_runs(ct
         assert tq.lib().tq_q8_append(ctx, ctypes.byref(c), BASE, S(0, 0, 0), BASE, S(0, 0, 0), tq.TQ_BF16, 1, 1, 1, 1 << 30, None, 0, None, None) == want
         out = tq.tq_cache_sizes()
         assert tq.lib().tq_cache_sizes_get(ctx, 1, 1, capacity, ctypes.byref(out)) == (tq.TQ_OK if want == TAKEN else want)
+
+
+# ------------------------------------------------------------------------------------------------ alignment
+
+def test_alignment_of_every_pointer(ctx):
+    """Vectors, planes and workspaces: 16 bytes. Numbers of 4 bytes: their own size."""
+    L = tq.lib()
+    rows = S(H * N * D, N * D, D)
+    assert rotary(ctx, BASE + 8, rows, ELSEWHERE, rows) == tq.TQ_ERR_ALIGN
+    assert rotary(ctx, BASE, rows, ELSEWHERE + 2, rows) == tq.TQ_ERR_ALIGN
+    for at, want in (((1 << 30) + 2, tq.TQ_ERR_ALIGN), ((1 << 30) + 4, TAKEN)):
+        assert L.tq_rotary(ctx, BASE, rows, ELSEWHERE, rows, tq.TQ_BF16, B, H, N, at, 0, None) == want
+        kv = S(4 * N * D, N * D, D)
+
+        def append(lens=1 << 30, new=None, pos=None):
+            return L.tq_q8_append(ctx, ctypes.byref(cache()), BASE, kv, BASE, kv, tq.TQ_BF16, 2, 4, N, lens, new, 1, pos, None)
+
+        assert append(lens=at) == append(new=at) == append(pos=at) == want
+        for name in ("d_seq_lens", "d_new_lens", "d_slopes", "d_key_begin", "d_key_end", "d_q_positions", "d_weights", "d_lse"):
+            assert attention(ctx, **{name: at}) == want, name
+        assert attention(ctx, d_weights=1 << 50, d_weights_in=at) == want
+        assert attention(ctx, d_q_positions=1 << 50, d_k_positions=at) == want
+        paged = cache()
+        paged.block_table, paged.pool_blocks = at, 100
+        assert attention(ctx, paged) == want
+        for name in ("lens", "weights", "positions", "kept", "dst_lens", "dst_weights", "dst_positions"):
+            assert evict(ctx, **{name: at + (1 << 48)}) == want, name
