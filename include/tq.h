@@ -542,7 +542,8 @@ tq_status tq_rotary(const tq_ctx *ctx, const void *d_x, const int64_t *x_strides
  *   d_new_lens  : int32 [batch], or NULL: sequence b brings its first
  *                 d_new_lens[b] tokens only (0..n_new; the rest is not read)
  *   rope        : 1 rotates the keys first (rounded to `dtype`, as tq_rotary
- *                 would return them)
+ *                 would return them; a last bit of fp32 in a sine or cosine can
+ *                 turn that rounding, and a code, at a tie)
  *   d_positions : int32 [batch][n_new], or NULL: token t is at position
  *                 d_seq_lens[b] + t
  * A sequence whose slots would lie outside the cache is skipped whole
@@ -596,11 +597,12 @@ typedef struct tq_q8_attn {
  * for up to 16 query rows (n_q x group) per KV head; one below 2^-8 (2^-20) of the row's
  * largest so far is within 2^-32 of that one instead. Beyond 16 rows it has 11 bits for
  * TQ_F16 and 8 for TQ_BF16 (whose queries then lose coordinates below 2^-17 of a row's
- * largest); one below 2^-14 (2^-10) of the row's largest among the same 128 slots is within
- * 2^-25 (2^-18) of that one, 2^4 times as much at most where the two 64-slot blocks' value scales differ: together
- * below 2^-15 (2^-8) of the 128 slots' own probability. A capped score is within 2^-21 of the cap there, and
+ * largest); one below 2^-10 of the row's largest among the same 128 slots is within
+ * 2^-21 (2^-18) of that one, up to 2^4 times as much where the two 64-slot blocks' value scales differ: together
+ * below 2^-11 (2^-8) of the 128 slots' own probability. A capped score is within 2^-21 of the cap there, and
  * within 2^-19 of itself where the cap is above 128. The
- * softmax's sum is fp32 throughout. */
+ * softmax's sum is fp32 throughout. Value sums are fp32 before they are divided by the softmax's: values
+ * above 2^80 may overflow. */
 tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_len,
                                     int weights, size_t *out);
 tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, void *d_workspace,

@@ -12,9 +12,9 @@
 // else's coordinates and 8 sines. Those are formed once for all heads of the CTA; the next head's inputs are
 // loaded before the current one's maximum is awaited. (Halves of a rotation that is no multiple of 16
 // wide do not split into such pieces: there the partners are loaded a second time.)
-// Measured: 4 sequences of 16384 tokens, 8 KV heads, rotated, bf16: 85 us, 4.7 TB/s (0.70 of a plain copy; without rotation 70 us, 0.85):
+// Measured: 4 sequences of 16384 tokens, 8 KV heads, rotated, bf16: 85 us, 4.7 TB/s (0.70 of a plain copy; without rotation 68 us, 0.88):
 // the ALU is 58 % busy with conversions and angles, and the CTA's maximum is a barrier per head (a block's maximum is needed
-// before its first code; rows staged through shared memory by asynchronous copies took 98 us). One token of 16 sequences: 3.9 us.
+// before its first code; rows staged through shared memory by asynchronous copies took 98 us); fp16 the same, fp32, at one CTA an SM, 129 us, 5.2 TB/s (117 us, 0.84, without rotation). One token of 16 sequences: 3.9 us.
 
 #include "tq_q8.cuh"
 

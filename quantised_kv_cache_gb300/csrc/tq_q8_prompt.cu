@@ -10,10 +10,11 @@
 // copies are issued by warps of their own: an issue waits while the tensor cores' queue is full.
 //
 // Bound by issue, then the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
-// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 302 us in
-// bf16 (798 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 352 us
-// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 528 us, biased 458 us (three
-// exponentials or reciprocals an element, the capped scores stored and read again; caps above 128, whose small scores go through a series, 589 us). TERMS = 2 for bf16 (8 significant bits of
+// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 301 us in
+// bf16 (800 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 349 us
+// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 494 us (three
+// exponentials or reciprocals an element), caps above 128, whose small scores go through a series, 589 us; biased 426 us. Both store their scores and
+// read them again, without loads ahead and without turns. TERMS = 2 for bf16 (8 significant bits of
 // q and p, down to 2^-18 of the largest of either), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
 // through fp16 pairs, in which the differences to the terms are exact.
 //
@@ -21,8 +22,8 @@
 // 2^4 apart that would cost precision, and the blocks' sums are formed one after the other. The terms of a probability end at a fixed
 // step (2^-17 of 2^8 for two of them), so it is relative to the row's largest of its own sum, not to the running maximum: the smaller ones of a
 // tile after a heavy key keep their bits, and what a tile's terms drop is below 2^-8 of its own mass. The way to the running maximum is a factor of the
-// whole sum, formed while the tensor cores work (302 us where the running maximum as the reference takes 297).
-// Work split: as in the kernel for few rows, equal slices of the (sequence, 256 rows, head, tile) space, a unit's start counted
+// whole sum, formed while the tensor cores work (301 us where the running maximum as the reference takes 297).
+// Work split: as in the kernel for few rows, equal slices of the (sequence, unit of 256 rows, head, tile) space, a unit's start counted
 // as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first. Up to 128 rows over many tiles
 // are units of one row tile: the two row tiles of a CTA then work on slices of their own (APART).
 
@@ -40,7 +41,6 @@ constexpr int kRegsSoft = 112, kRegsControl = 32;  // 512 * 112 + 128 * 32 = 640
 constexpr int kStage = 2 * kTile * kD;
 constexpr int kQTerm = 128 * kD;       // one term of a row tile's queries
 constexpr int part_of(int unit) { return unit * (kD + 2); }  // a partial record: O as 32 columns of 4 coordinates [column][row][4], then m and l [row]
-// Capped or biased scores run without turns (measured at 2048 of 8192 tokens: 653 us, 713 with them).
 constexpr float kFold = 0.0625f;       // blocks' value scales within 2^4 share a sum
 constexpr float kLowest = -3e38f;      // in place of a maximum of -inf: an unseen score stays -inf beside it, its factor is 0
 
@@ -65,7 +65,7 @@ struct Plan {
   int entries, pairs, unit;  // pairs: units of a sequence (and head); unit: their rows
 };
 
-// One warp per entry (sequence, 256 rows).
+// One warp per entry (sequence, unit of rows).
 __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__ Q8AttnArgs a, Plan p) {
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   pdl_wait();
@@ -236,7 +236,7 @@ template <int TERMS, int EXTRA, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   constexpr int kStages = stages_of(TERMS, APART), kUnit = unit_rows(APART);
-  constexpr bool kTurns = !EXTRA && !APART;
+  constexpr bool kTurns = !EXTRA && !APART;  // capped or biased scores run without turns (2048 of 8192 tokens, when they took 653 us: 713 with them)
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
   uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage;  // [row tile][term][128 x 128]

@@ -64,8 +64,9 @@ def test_a_heavy_key_before_a_long_tail(ctx, N, gap, ratio, heads, n, kind, dtyp
     """16 rows a KV head and 17 (units of one row tile), and 300. More KV heads than SMs, all of the same tokens, so that a CTA works on most of a
     sequence by itself: the heavy key's tile is in its slice.
 
-    bf16: a probability has 8 bits, so |d_j| <= 2^-8 p_j, and its smallest step is at most 2^-14 of the largest among 128 tokens (64 of
-    them where it is that large), 2^-8 of their mass; fp16: 2^-11, and 2^-15 of the mass. The scores' own errors (sums of 128 products
+    A probability enters as terms of 2^8 times its ratio to the largest among 128 tokens. bf16: two e4m3 terms leave 2^-8 of numbers from 2^-2 on
+    and 2^-10 (half their smallest step) of smaller ones, so |d_j| <= 2^-8 p_j or 2^-18 of the largest, 2^-14 in a block whose value scale
+    is folded in at 1 : 16, and 64 such are 2^-8 of the tokens' mass. fp16: the third term, e5m2, leaves an eighth of that: 2^-11, and 2^-11 of the mass. The scores' own errors (sums of 128 products
     in fp32, queries' smallest coordinates) are below 2^-11 here. Then the rounding to the type."""
     H = torch.cuda.get_device_properties(0).multi_processor_count + 8
     rest = torch.cat([torch.zeros(1, device=DEV), torch.ones(127, device=DEV)])
@@ -90,7 +91,7 @@ def test_a_heavy_key_before_a_long_tail(ctx, N, gap, ratio, heads, n, kind, dtyp
     got = tq.tq_q8_attention(ctx.handle, cache, q.repeat(1, H, 1, 1), ints([N]), N, key_end=ints(np.full((1, n), N)), softcap=softcap,
                              slopes=None if slopes is None else slopes.repeat(H))
     want, mass = attend(q, kv, vv, softcap, slopes)
-    share = 2.0 ** -8 + 2.0 ** -8 if dtype == BF else 2.0 ** -11 + 2.0 ** -15
+    share = 2.0 ** -8 + 2.0 ** -8 if dtype == BF else 2.0 ** -11 + 2.0 ** -11
     err = (got.view(H, heads, n, 128).double() - want).norm(dim=-1)
     tol = (share + 2.0 ** -11) * mass + want.norm(dim=-1) * torch.finfo(dtype).eps / 2 * 1.01
     assert bool((err <= tol).all()), float((err / tol).max())
