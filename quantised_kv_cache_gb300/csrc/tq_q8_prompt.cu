@@ -10,9 +10,9 @@
 // copies are issued by warps of their own: an issue waits while the tensor cores' queue is full.
 //
 // Bound by issue, then the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
-// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 301 us in
-// bf16 (800 TFLOP/s of the formula's products, 0.42 of a plain bf16 matrix product), 349 us
-// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 494 us (three
+// product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 292 us in
+// bf16 (824 TFLOP/s of the formula's products, 0.43 of a plain bf16 matrix product), 348 us
+// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 492 us (three
 // exponentials or reciprocals an element), caps above 128, whose small scores go through a series, 589 us; biased 426 us. Both store their scores and
 // read them again, without loads ahead and without turns. TERMS = 2 for bf16 (8 significant bits of
 // q and p, down to 2^-18 of the largest of either), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
@@ -22,7 +22,7 @@
 // 2^4 apart that would cost precision, and the blocks' sums are formed one after the other. The terms of a probability end at a fixed
 // step (2^-17 of 2^8 for two of them), so it is relative to the row's largest of its own sum, not to the running maximum: the smaller ones of a
 // tile after a heavy key keep their bits, and what a tile's terms drop is below 2^-8 of its own mass. The way to the running maximum is a factor of the
-// whole sum, formed while the tensor cores work (301 us where the running maximum as the reference takes 297).
+// whole sum, formed while the tensor cores work.
 // Work split: as in the kernel for few rows, equal slices of the (sequence, unit of 256 rows, head, tile) space, a unit's start counted
 // as tiles, and cut units joined afterwards; small kernels find each unit's tiles and the slices first. Up to 128 rows over many tiles
 // are units of one row tile: the two row tiles of a CTA then work on slices of their own (APART).
@@ -555,6 +555,9 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           const float d = (float)(log2i(half ? f.w : f.z) - log2i(half ? f.z : f.w));
           fold = fminf(d, 0.f), fold1 = fminf(-d, 0.f);
         }
+        // This block's scale (the other's where it is not there) is the sum's, beside the way from this block's reference: folded, the two have
+        // the same product in both. Kept in place of both scales over the exponentials: 292 us, 301 with them.
+        const float own = half ? (f.w < 0.f ? f.z : f.w) : f.z < 0.f ? f.w : f.z;
         const float shift = 8.f + fold - fmaxf(fmaxf(top + fold, other + fold1), kLowest);
         // ---- probabilities times 2^8, their terms over the scores they come from, their sum
         float2 sum = make_float2(0.f, 0.f);
@@ -643,6 +646,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         };
         float corr = 1.f, by = 1.f, use = 0.f;
         for (int blk = 0; blk <= (int)apart; ++blk) {
+          const float its = apart ? half ? sm.info[s].z : sm.info[s].w : 0.f;
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.bar_p[rt]);
@@ -657,10 +661,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           ++sums;
           __syncwarp();
           tc_fence_after_sync();
-          // this block's scale and factor, which have the same product as the other's where one is folded
-          const float mine = half ? f.w : f.z, its = half ? f.z : f.w;
-          const bool swap = apart ? blk != half : mine < 0.f;
-          add(swap ? its : mine, apart && swap ? ex2_approx(other - use) : by, blk ? 1.f : corr);
+          const bool swap = apart && blk != half;
+          add(swap ? its : own, swap ? ex2_approx(other - use) : by, blk ? 1.f : corr);
         }
       }
       it += todo;
