@@ -12,7 +12,7 @@
 // Bound by issue, then the tensor cores: per 128 x 128 tile two products of TERMS passes (540 clocks a
 // product and two passes) and about 7 instructions an element. Measured: the last 2048 of 8192 tokens, 32 query and 8 KV heads: 292 us in
 // bf16 (824 TFLOP/s of the formula's products, 0.43 of a plain bf16 matrix product), 348 us
-// in fp16; ALU 56 % and tensor cores 36 % busy, the rest the wait of each for the other. Capped 492 us (three
+// in fp16; ALU 57 % and tensor cores 37 % busy, the rest the wait of each for the other. Capped 492 us (three
 // exponentials or reciprocals an element), caps above 128, whose small scores go through a series, 589 us; biased 426 us. Both store their scores and
 // read them again, without loads ahead and without turns. TERMS = 2 for bf16 (8 significant bits of
 // q and p, down to 2^-18 of the largest of either), 3 for fp16 (11). A term costs half an instruction to make: the probabilities go
