@@ -626,6 +626,74 @@ tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *ds
                       const int32_t *d_positions, int32_t *d_kept, int32_t *d_dst_lens, float *d_dst_weights,
                       int32_t *d_dst_positions, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Long contexts in a Q8 cache: attention over chosen blocks, and behind a shared prefix
+ * ------------------------------------------------------------------------- */
+
+/* Bounds of each block's keys, for tq_q8_select: int8 [block][2][d], the block being a cache's (its pool's, when
+ * paged): coordinate c of the block's keys lies between 4 lo_c 2^e and 4 hi_c 2^e, e the key plane's exponent; lo_c is the
+ * floor of a quarter of its smallest code, hi_c the ceiling of a quarter of its largest (both within +-112). The call
+ * brings up to date the blocks that an append with the same lengths wrote: of sequence b those that hold slots
+ * d_seq_lens[b] .. d_seq_lens[b] + new - 1, over all their tokens below d_seq_lens[b] + new; new is d_new_lens[b], or n_new when that is
+ * NULL. (After an eviction: lengths of 0 and d_new_lens = d_dst_lens.) Other blocks' bounds are left as they are. A sequence whose
+ * slots would lie outside the cache is skipped (TQ_ERR_CAPACITY in the error word), one whose d_new_lens[b] is out of [0, n_new] too (TQ_ERR_ARG).
+ *   d_bounds : 16-byte aligned */
+tq_status tq_q8_bounds(const tq_ctx *ctx, const tq_cache *cache, int batch, int heads_kv, int n_new, const int32_t *d_seq_lens,
+                       const int32_t *d_new_lens, int8_t *d_bounds, void *stream);
+
+/* The blocks that query tokens are to look at. Every `span` query tokens of a sequence and KV head share a list. Fields named as in
+ * tq_q8_attn mean the same; zero the struct first. */
+typedef struct tq_q8_pick {
+  int batch, heads_q, heads_kv;
+  int n_q, span;          /* query tokens per sequence; of a list (>= 1) */
+  int max_len;
+  int keep, sink, recent; /* blocks of a list, >= 1; the first and last ones that are taken whatever their scores, sink + recent <= keep */
+  int q_dtype;
+  const void *d_q;
+  int64_t q_strides[3];
+  const int32_t *d_seq_lens, *d_new_lens, *d_key_begin, *d_key_end;
+  const int8_t *d_bounds; /* of the cache's blocks (tq_q8_bounds) */
+  int32_t *d_blocks;      /* [batch][heads_kv][ceil(n_q / span)][keep], out */
+} tq_q8_pick;
+
+/* A list holds block numbers of its sequence (slot / 64) in ascending order, then -1. A list's rows are its query tokens, with all heads of
+ * the group; a row that sees no slot does not count. The blocks from the first to the last that a row sees: all of them when they are at
+ * most `keep`; else the first `sink`, the last `recent`, and of the rest those of the largest scores (of equals the
+ * lower block). A row's score of a block is sum_c max(w_c lo_c, w_c hi_c), w = the row in whole numbers within +-127: q 2^-x rounded to
+ * nearest even, x the least with every |q| 2^-x < 128 over the list's rows (128 itself is cut); the block's is its rows'
+ * largest times the key plane's scale. All of this is exact, so that the choice is too. For scale > 0, up to the rounding of q and of the
+ * bounds, no key of a block has a larger product with a row. Rows with an infinity or a NaN
+ * do not count (no row left: all scores are 0). Lengths out of range are cut as by tq_q8_attention; blocks with a bad table entry score
+ * below all others; both set the error word to TQ_ERR_ARG.
+ * Workspace: tq_q8_select_workspace(...) bytes for these sizes or larger ones (0: d_workspace may be NULL). */
+tq_status tq_q8_select_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int max_len, size_t *out);
+tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pick *p, void *d_workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* tq_q8_attention over listed blocks alone: a row sees the slots of its range that lie in a block of its list.
+ *   d_blocks : int32 [batch][heads_kv][ceil(n_q / span)][n_blocks], 4-byte aligned, block numbers of the sequence in ascending order; negative
+ *              ones and ones that no row of the list sees are passed over. An entry that is not above the one before it (unless that is
+ *              negative), or past the cache's last block, is passed over too and sets the error word to TQ_ERR_ARG.
+ * a->d_weights and a->d_weights_in have to be NULL (TQ_ERR_UNSUPPORTED). Workspace: of these sizes or larger ones in each but span, which has
+ * to be the same. Results as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
+tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int n_blocks,
+                                           size_t *out);
+tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, const int32_t *d_blocks, int n_blocks,
+                                 int span, void *d_workspace, size_t workspace_bytes, void *stream);
+
+/* tq_q8_attention of a batch whose sequences share a prefix, which is read once for all of them. Sequence b is the first
+ * d_prefix_lens[b] tokens of `prefix` (a cache of batch 1 and the same KV heads and context; each in [0, max_prefix],
+ * max_prefix <= its capacity) followed by the d_seq_lens[b] tokens that `cache` holds for it. Slots and positions count through both: slot s of
+ * the cache is slot d_prefix_lens[b] + s of the sequence, in d_key_begin and d_key_end (default [0, the query's own slot + 1)) and in the bias'
+ * distances. a->max_len bounds d_seq_lens, which count the cache's tokens. a->d_q_positions, a->d_k_positions, a->d_weights and a->d_weights_in have to be
+ * NULL (TQ_ERR_UNSUPPORTED). A d_prefix_lens[b] out of range is cut and sets the error word to TQ_ERR_ARG. The two
+ * parts' sums are joined in fp32 before the one rounding of the result; the prefix's rows are the whole batch's (batch x n_q x group), whose number
+ * decides the precision of its probabilities as in tq_q8_attention. Workspace: of these sizes or larger ones. */
+tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
+                                           size_t *out);
+tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix,
+                                 const tq_cache *cache, const tq_q8_attn *a, void *d_workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

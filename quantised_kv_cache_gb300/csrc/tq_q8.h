@@ -70,6 +70,15 @@ struct Q8EvictArgs {
 };
 int launch_q8_evict(const Q8EvictArgs &a, int num_sms, void *stream);
 
+struct Q8BoundsArgs {
+  Q8Cache c;
+  int batch, heads, n_new;
+  const int32_t *seq_lens, *new_lens;
+  int8_t *bounds;  // [block][2][kD]
+  int *error;
+};
+int launch_q8_bounds(const Q8BoundsArgs &a, void *stream);
+
 // Attention: the struct of the ABI with its defaults filled in, and the workspace carved up.
 struct Q8AttnArgs {
   Q8Cache c;
@@ -90,6 +99,19 @@ struct Q8AttnArgs {
   long long scores_ld = 0;
   int *error;
 };
+// Lists of blocks: q has the queries, lengths and ranges.
+struct Q8SelectArgs {
+  Q8AttnArgs q;
+  const int8_t *bounds;
+  int32_t *blocks;  // [batch][heads_kv][lists][keep]
+  int span, lists, keep, sink, recent;
+  uint32_t *keys = nullptr;  // [batch][heads_kv][lists][keys_ld] scores as ordered numbers, where they are not in shared memory
+  long long keys_ld = 0;
+};
+size_t q8_select_workspace(int batch, int heads_kv, int group, int n_q, int span, int max_len);
+bool q8_select_fits(const Q8SelectArgs &a);
+int launch_q8_select(const Q8SelectArgs &a, void *workspace, int num_sms, void *stream);
+
 // The workspace with room for all that is worth keeping; *least (if not NULL): what the call cannot do without, which never falls as
 // the batch, the query tokens or max_len grow. `weights`: 0 none, 1 with results of either size, 2 with results of 16 bits
 size_t q8_attention_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q, int max_len, int weights, size_t *least);

@@ -104,6 +104,11 @@ bool overlap(const Region &a, const Region &b) {
   return true;
 }
 
+// blocks of a cache's arrays
+size_t blocks_of(const tq_cache *c) {
+  return c->block_table ? (size_t)c->pool_blocks : (size_t)c->batch * c->heads_kv * tq::q8_blocks_of(c->capacity);
+}
+
 // A buffer that is updated in place, or regions that lie apart.
 bool same_or_apart(const Region &a, const Region &b) { return a.p == b.p || !overlap(a, b); }
 
@@ -337,6 +342,63 @@ tq_status tq_q8_evict(const tq_ctx *ctx, const tq_cache *src, const tq_cache *ds
                           d_weights, d_positions, d_kept, d_dst_lens, d_dst_positions, d_dst_weights,
                           &ctx->dparams->error};
   return (tq_status)tq::launch_q8_evict(a, ctx->num_sms, stream);
+}
+
+tq_status tq_q8_bounds(const tq_ctx *ctx, const tq_cache *cache, int batch, int heads_kv, int n_new, const int32_t *d_seq_lens,
+                       const int32_t *d_new_lens, int8_t *d_bounds, void *stream) {
+  if (!ctx || !d_seq_lens || !d_bounds || batch <= 0 || heads_kv <= 0 || n_new < 0) return TQ_ERR_ARG;
+  tq_status s = tq::q8_check_cache(ctx, cache, batch, heads_kv);
+  if (s != TQ_OK) return s;
+  if (!aligned16(d_bounds) || !aligned4(d_seq_lens, d_new_lens)) return TQ_ERR_ALIGN;
+  const size_t blocks = blocks_of(cache);
+  const Region out = bytes(d_bounds, blocks * 2 * tq::kD);
+  if (overlap(out, bytes(d_seq_lens, batch * sizeof(int32_t))) || overlap(out, bytes(d_new_lens, batch * sizeof(int32_t))) ||
+      overlap(out, bytes(cache->records, blocks * tq::kQ8BlockBytes)))
+    return TQ_ERR_ARG;
+  if (n_new == 0) return on_device(ctx);
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  const tq::Q8BoundsArgs a{tq::q8_cache(cache), batch, heads_kv, n_new, d_seq_lens, d_new_lens, d_bounds, &ctx->dparams->error};
+  return (tq_status)tq::launch_q8_bounds(a, stream);
+}
+
+tq_status tq_q8_select_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int max_len, size_t *out) {
+  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || span <= 0 || max_len <= 0) return TQ_ERR_ARG;
+  if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
+  *out = tq::q8_select_workspace(batch, heads_kv, heads_q / heads_kv, n_q, span, max_len);
+  return TQ_OK;
+}
+
+tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pick *p, void *d_workspace, size_t ws_bytes, void *stream) {
+  if (!ctx || !p || !p->d_q || !p->d_seq_lens || !p->d_bounds || !p->d_blocks) return TQ_ERR_ARG;
+  if (p->batch <= 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->heads_q % p->heads_kv || p->n_q <= 0 || p->span <= 0 || p->max_len <= 0)
+    return TQ_ERR_ARG;
+  if (!known(p->q_dtype) || p->keep <= 0 || p->sink < 0 || p->recent < 0 || (long long)p->sink + p->recent > p->keep) return TQ_ERR_ARG;
+  tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
+  if (s != TQ_OK) return s;
+  if (p->max_len > cache->capacity) return TQ_ERR_ARG;
+  if (!aligned16(p->d_q) || !aligned16(p->d_bounds) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
+      !aligned4(p->d_seq_lens, p->d_new_lens, p->d_key_begin, p->d_key_end, p->d_blocks))
+    return TQ_ERR_ALIGN;
+  tq::Q8SelectArgs a{};
+  a.q.c = tq::q8_cache(cache);
+  a.q.batch = p->batch, a.q.heads_q = p->heads_q, a.q.heads_kv = p->heads_kv, a.q.group = p->heads_q / p->heads_kv;
+  a.q.n_q = p->n_q, a.q.max_len = p->max_len, a.q.q_dtype = p->q_dtype, a.q.q = p->d_q, a.q.qs = strides(p->q_strides);
+  a.q.seq_lens = p->d_seq_lens, a.q.new_lens = p->d_new_lens, a.q.kbeg = p->d_key_begin, a.q.kend = p->d_key_end;
+  a.bounds = p->d_bounds, a.blocks = p->d_blocks;
+  a.span = p->span < p->n_q ? p->span : p->n_q, a.lists = (int)(((long long)p->n_q + p->span - 1) / p->span);
+  a.keep = p->keep, a.sink = p->sink, a.recent = p->recent;
+  if (!tq::q8_select_fits(a)) return TQ_ERR_UNSUPPORTED;
+  const size_t need = tq::q8_select_workspace(p->batch, p->heads_kv, a.q.group, p->n_q, p->span, p->max_len);
+  if (ws_bytes < need || (need && !d_workspace)) return TQ_ERR_WORKSPACE;
+  const size_t rowsn = (size_t)p->batch * p->n_q * sizeof(int32_t), lens = p->batch * sizeof(int32_t);
+  const Region out = bytes(p->d_blocks, (size_t)p->batch * p->heads_kv * a.lists * p->keep * sizeof(int32_t));
+  const Region in[] = {rows(p->d_q, p->q_strides, p->q_dtype, p->batch, p->heads_q, p->n_q), bytes(p->d_bounds, blocks_of(cache) * 2 * tq::kD),
+                       bytes(p->d_seq_lens, lens), bytes(p->d_new_lens, lens), bytes(p->d_key_begin, rowsn), bytes(p->d_key_end, rowsn)};
+  for (const Region &r : in)
+    if (overlap(out, r)) return TQ_ERR_ARG;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  a.q.error = &ctx->dparams->error;
+  return (tq_status)tq::launch_q8_select(a, d_workspace, ctx->num_sms, stream);
 }
 
 }  // extern "C"

@@ -43,16 +43,20 @@ __device__ __forceinline__ int row_terms(const float (&x)[4], uint32_t (&w)[3]) 
   for (int k = 0; k < 3; ++k) w[k] = amax >= 0x7f800000u ? 0x7f7f7f7fu : lo[k] | (hi[k] << 16);
   return e;
 }
+// Coordinates 4 lane .. 4 lane + 3 of row (head hq, query token i) of sequence b; zeros for a row that is not live.
+__device__ __forceinline__ void row_coords(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, float (&x)[4]) {
+  x[0] = x[1] = x[2] = x[3] = 0.f;
+  if (!live) return;
+  const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
+  if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
+  else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
+  else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
+}
 // Few rows: T e5m2 terms.
 template <int T>
 __device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[T]) {
-  float x[4] = {0.f, 0.f, 0.f, 0.f};  // coordinates 4 lane .. 4 lane + 3 of row (head hq, query token i) of sequence b
-  if (live) {
-    const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
-    if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
-    else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
-    else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
-  }
+  float x[4];
+  row_coords(a, b, hq, i, live, lane, x);
   const uint32_t amax = row_top(x);
   const int e = row_exponent(amax, 14);
   const float f = pow2i(-e);

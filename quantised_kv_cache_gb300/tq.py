@@ -86,6 +86,12 @@ class tq_q8_attn(ctypes.Structure):
                 ("d_key_end", _vp), ("d_weights_in", _vp), ("d_weights", _vp), ("d_lse", _vp)]
 
 
+class tq_q8_pick(ctypes.Structure):
+    _fields_ = [(n, _i) for n in ("batch", "heads_q", "heads_kv", "n_q", "span", "max_len", "keep", "sink", "recent", "q_dtype")] + [
+                ("d_q", _vp), ("q_strides", _strides3), ("d_seq_lens", _vp), ("d_new_lens", _vp), ("d_key_begin", _vp), ("d_key_end", _vp),
+                ("d_bounds", _vp), ("d_blocks", _vp)]
+
+
 _SIGNATURES = {
     "tq_abi_version": (_i, []),
     "tq_status_str": (ctypes.c_char_p, [_i]),
@@ -123,6 +129,9 @@ _SIGNATURES = {
     "tq_q8_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),  # a packed tq_q8_attn
     "tq_q8_evict": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.POINTER(tq_cache), _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp,
                          _vp, _vp, _vp, _vp]),
+    "tq_q8_bounds": (_i, [_vp, ctypes.POINTER(tq_cache), _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "tq_q8_select_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "tq_q8_select": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),  # a packed tq_q8_pick
 }
 
 _lib = None
@@ -598,6 +607,76 @@ def tq_q8_evict(ctx, src: "Cache", dst: "Cache", seq_lens: torch.Tensor, weights
 
 
 # ----------------------------------------------------------------------------
+# long contexts in an 8-bit cache: attention over chosen blocks, and behind a shared prefix
+# ----------------------------------------------------------------------------
+
+def _bounds_array(bounds: torch.Tensor, cache: "Cache") -> int:
+    return _array(bounds, (cache.bounds_blocks, 2, 128), torch.int8, cache.device_index, "bounds")
+
+
+def tq_q8_bounds(ctx, cache: "Cache", bounds: torch.Tensor, seq_lens: torch.Tensor, n_new: int,
+                 new_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Bring the key bounds (`cache.new_bounds()`, int8 [blocks][2][128]) of the blocks up to date that an append of n_new tokens a
+    sequence (new_lens[b] of them) at lengths seq_lens wrote. Returns bounds."""
+    B, index = cache.batch, cache.device_index
+    status = lib().tq_q8_bounds(ctx, cache.struct, B, cache.heads_kv, n_new, _array(seq_lens, (B,), _i32, index, "seq_lens"),
+                                _array(new_lens, (B,), _i32, index, "new_lens"), _bounds_array(bounds, cache), _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_bounds")
+    return bounds
+
+
+def tq_q8_select_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, span: int, max_len: int) -> int:
+    """Bytes for calls of these sizes and of smaller ones (0: none)."""
+    out = _sz()
+    check(lib().tq_q8_select_workspace(ctx, batch, heads_q, heads_kv, n_q, span, max_len, ctypes.byref(out)), "tq_q8_select_workspace")
+    return out.value
+
+
+# tq_q8_pick's fields in order
+_pack_pick = struct.Struct("@10iP3q6P")
+
+
+def _workspace(workspace: Optional[torch.Tensor], need, stream, index: int, device):
+    """(address, bytes) of a call's workspace, made where the caller brings none."""
+    if workspace is None:
+        n = need()
+        if not n:
+            return None, 0, None
+        workspace = _made(stream, torch.empty, n, dtype=torch.uint8, device=device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on q's device is wanted")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def tq_q8_select(ctx, cache: "Cache", bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor, max_len: int, keep: int, sink: int = 0,
+                 recent: int = 1, span: int = 1, new_lens: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                 key_end: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, blocks: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The blocks that q [batch][heads_q][tokens][128] (any strides with contiguous rows) is to look at, one list for every `span` tokens
+    (include/tq.h, tq_q8_pick). Returns blocks, int32 [batch][heads_kv][ceil(tokens / span)][keep]."""
+    shape, qs = _rows(q, "q")
+    B, Hq, n, _ = shape
+    H, index = cache.heads_kv, cache.device_index
+    if q.get_device() != index or index < 0:
+        raise ValueError("q: the cache's device is wanted")
+    if span < 1 or keep < 1:
+        raise ValueError("span and keep: at least 1 is wanted")
+    lists = (B, H, (n + span - 1) // span, keep)
+    if blocks is None:
+        blocks = _made(stream, torch.empty, lists, dtype=_i32, device=q.device)
+    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_select_workspace(ctx, B, Hq, H, n, span, max_len), stream, index, q.device)
+    a = _pack_pick.pack(B, Hq, H, n, span, max_len, keep, sink, recent, _any_dtype(q.dtype), q.data_ptr(), qs[0], qs[1], qs[2],
+                        _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
+                        _array(key_begin, (B, n), _i32, index, "key_begin") or 0, _array(key_end, (B, n), _i32, index, "key_end") or 0,
+                        _bounds_array(bounds, cache) or 0, _array(blocks, lists, _i32, index, "blocks") or 0)
+    status = lib().tq_q8_select(ctx, cache.struct, a, ws, ws_bytes, _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_select")
+    return blocks
+
+
+# ----------------------------------------------------------------------------
 # device-memory plumbing: a context handle and a cache whose planes torch owns
 # ----------------------------------------------------------------------------
 
@@ -699,6 +778,15 @@ class Cache:
     def blocks_per_seq(self) -> int:
         return (self.capacity + self.block_tokens - 1) // self.block_tokens
 
+    @property
+    def bounds_blocks(self) -> int:
+        """The blocks that the cache's arrays hold."""
+        return self.batch * self.heads_kv * self.blocks_per_seq
+
+    def new_bounds(self) -> torch.Tensor:
+        """Zeroed key bounds for an 8-bit cache (tq_q8_bounds): int8 [blocks][2][128]."""
+        return torch.zeros((self.bounds_blocks, 2, 128), dtype=torch.int8, device=self.device)
+
     def blocks(self) -> torch.Tensor:
         """The records as [batch * heads_kv][blocks_per_seq][block_bytes] (TQ schemes)."""
         return self.tensors["records"].view(self.batch * self.heads_kv, self.blocks_per_seq, self.sizes.block_bytes)
@@ -762,6 +850,10 @@ class PagedCache(Cache):
         if name in ("k_stats", "v_stats") and self.block_tokens == Q8_BLOCK_TOKENS:
             return self.pool_blocks * 4
         return getattr(self.sizes, name)
+
+    @property
+    def bounds_blocks(self) -> int:
+        return self.pool_blocks
 
     def blocks(self) -> torch.Tensor:
         """The sequence-heads' blocks gathered out of the pool through the table (a copy;
