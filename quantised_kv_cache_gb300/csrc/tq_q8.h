@@ -79,6 +79,10 @@ struct Q8BoundsArgs {
 };
 int launch_q8_bounds(const Q8BoundsArgs &a, void *stream);
 
+// Which keys the rows of an attention kernel meet: a cache's; those of listed blocks; a prefix's, the rows of all sequences being one sequence's;
+// a sequence's own behind a prefix, whose part is joined to theirs.
+enum Q8Kind { kWhole = 0, kListed = 1, kPrefix = 2, kOwn = 3 };
+
 // Attention: the struct of the ABI with its defaults filled in, and the workspace carved up.
 struct Q8AttnArgs {
   Q8Cache c;
@@ -98,6 +102,9 @@ struct Q8AttnArgs {
   float *scores = nullptr;  // [batch][heads_kv][group x n_q][scores_ld] in log2, kept for the weights (or NULL)
   long long scores_ld = 0;
   int *error;
+  // kListed: [batch][heads_kv][lists][n_blocks], a list for every `span` query tokens
+  const int32_t *blocks = nullptr;
+  int n_blocks = 0, span = 0, lists = 0;
 };
 // Lists of blocks: q has the queries, lengths and ranges.
 struct Q8SelectArgs {
@@ -123,6 +130,12 @@ int launch_q8_prompt(const Q8AttnArgs &a, void *workspace, int num_sms, void *st
 // `terms`: of the queries, where 16-bit results' scores were not kept
 size_t q8_weights_workspace(int num_sms, int batch, int heads_kv, int group, int n_q, int max_len);
 int launch_q8_weights(const Q8AttnArgs &a, int terms, void *workspace, int num_sms, void *stream);
+size_t q8_listed_workspace(int num_sms, int batch, int group, int n_q, int span);
+bool q8_listed_fits(const Q8AttnArgs &a);
+int launch_q8_listed(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
+size_t q8_listed_many_workspace(int num_sms, int batch, int group, int n_q, int span);
+bool q8_listed_many_fits(const Q8AttnArgs &a);
+int launch_q8_listed_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 int launch_q8_attention(const Q8AttnArgs &a, void *workspace, size_t ws_bytes, int num_sms, void *stream);
 
 }  // namespace tq

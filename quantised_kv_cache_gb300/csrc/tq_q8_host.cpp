@@ -144,6 +144,60 @@ Long power(Long x, int n) {
   return y;
 }
 
+// The checks of tq_q8_attention's arguments that come before its workspace's.
+tq_status check_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *p, const void *d_workspace) {
+  if (!ctx || !p || !p->d_q || !p->d_out || !p->d_seq_lens || !d_workspace) return TQ_ERR_ARG;
+  if (p->batch <= 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->heads_q % p->heads_kv || p->n_q <= 0 || p->max_len <= 0)
+    return TQ_ERR_ARG;
+  if (!known(p->q_dtype) || (p->out_dtype != p->q_dtype && p->out_dtype != TQ_F32)) return TQ_ERR_ARG;
+  if (!std::isfinite(p->scale) || !std::isfinite(p->softcap)) return TQ_ERR_ARG;
+  if (p->softcap != 0.f && !(p->softcap >= kLeastCap)) return TQ_ERR_ARG;  // (negative ones among them)
+  if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
+  if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
+  const tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
+  if (s != TQ_OK) return s;
+  if (p->max_len > cache->capacity) return TQ_ERR_ARG;
+  if (!aligned16(p->d_q) || !aligned16(p->d_out) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
+      !strides_ok(p->out_strides, p->out_dtype) ||
+      !aligned4(p->d_seq_lens, p->d_new_lens, p->d_slopes, p->d_q_positions, p->d_k_positions, p->d_key_begin, p->d_key_end, p->d_weights_in,
+                p->d_weights, p->d_lse))
+    return TQ_ERR_ALIGN;
+  return TQ_OK;
+}
+
+// What an attention call writes.
+struct Written {
+  Region out, lse;
+};
+Written written(const tq_q8_attn *p) {
+  return Written{rows(p->d_out, p->out_strides, p->out_dtype, p->batch, p->heads_q, p->n_q),
+                 bytes(p->d_lse, (size_t)p->batch * p->heads_q * p->n_q * sizeof(float))};
+}
+
+// Its outputs lie apart from one another and from its inputs; the kernels' arguments, all but the error word.
+tq_status attention_args(const tq_cache *cache, const tq_q8_attn *p, tq::Q8AttnArgs *args) {
+  if (!spread(p->out_strides, p->batch, p->heads_q, p->n_q)) return TQ_ERR_ARG;
+  const Region q = rows(p->d_q, p->q_strides, p->q_dtype, p->batch, p->heads_q, p->n_q);
+  const Written w = written(p);
+  const size_t slots = (size_t)p->batch * p->heads_kv * cache->capacity * sizeof(float);
+  const Region weights = bytes(p->d_weights, slots);
+  // (the queries are read again, for the weights, after the results are written)
+  if (overlap(q, w.out) || overlap(q, weights) || overlap(q, w.lse) || overlap(w.out, weights) || overlap(w.out, w.lse) || overlap(weights, w.lse) ||
+      !same_or_apart(weights, bytes(p->d_weights_in, slots)))
+    return TQ_ERR_ARG;
+  tq::Q8AttnArgs &a = *args;
+  a.c = tq::q8_cache(cache);
+  a.batch = p->batch, a.heads_q = p->heads_q, a.heads_kv = p->heads_kv, a.group = p->heads_q / p->heads_kv;
+  a.n_q = p->n_q, a.max_len = p->max_len, a.q_dtype = p->q_dtype, a.out_dtype = p->out_dtype;
+  a.q = p->d_q, a.out = p->d_out, a.qs = strides(p->q_strides), a.os = strides(p->out_strides);
+  a.seq_lens = p->d_seq_lens, a.new_lens = p->d_new_lens;
+  a.scale = p->scale != 0.f ? p->scale : 0.08838834764831845f;  // 1 / sqrt(128)
+  a.softcap = p->softcap < kNoCap ? p->softcap : 0.f, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
+  a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
+  a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
+  return TQ_OK;
+}
+
 }  // namespace
 
 namespace tq {
@@ -267,44 +321,13 @@ tq_status tq_q8_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, i
 
 tq_status tq_q8_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *p, void *d_workspace,
                           size_t ws_bytes, void *stream) {
-  if (!ctx || !p || !p->d_q || !p->d_out || !p->d_seq_lens || !d_workspace) return TQ_ERR_ARG;
-  if (p->batch <= 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->heads_q % p->heads_kv || p->n_q <= 0 || p->max_len <= 0)
-    return TQ_ERR_ARG;
-  if (!known(p->q_dtype) || (p->out_dtype != p->q_dtype && p->out_dtype != TQ_F32)) return TQ_ERR_ARG;
-  if (!std::isfinite(p->scale) || !std::isfinite(p->softcap)) return TQ_ERR_ARG;
-  if (p->softcap != 0.f && !(p->softcap >= kLeastCap)) return TQ_ERR_ARG;  // (negative ones among them)
-  if (p->d_k_positions && !p->d_q_positions) return TQ_ERR_ARG;  // a distance needs both on one scale
-  if (p->d_weights_in && !p->d_weights) return TQ_ERR_ARG;
-  tq_status s = tq::q8_check_cache(ctx, cache, p->batch, p->heads_kv);
+  tq_status s = check_attention(ctx, cache, p, d_workspace);
   if (s != TQ_OK) return s;
-  if (p->max_len > cache->capacity) return TQ_ERR_ARG;
-  if (!aligned16(p->d_q) || !aligned16(p->d_out) || !aligned16(d_workspace) || !strides_ok(p->q_strides, p->q_dtype) ||
-      !strides_ok(p->out_strides, p->out_dtype) ||
-      !aligned4(p->d_seq_lens, p->d_new_lens, p->d_slopes, p->d_q_positions, p->d_k_positions, p->d_key_begin, p->d_key_end, p->d_weights_in,
-                p->d_weights, p->d_lse))
-    return TQ_ERR_ALIGN;
   size_t least = 0;
   tq::q8_attention_workspace(ctx->num_sms, p->batch, p->heads_q, p->heads_kv, p->n_q, p->max_len, p->d_weights != nullptr, &least);
   if (ws_bytes < least) return TQ_ERR_WORKSPACE;
-  if (!spread(p->out_strides, p->batch, p->heads_q, p->n_q)) return TQ_ERR_ARG;
-  const Region q = rows(p->d_q, p->q_strides, p->q_dtype, p->batch, p->heads_q, p->n_q);
-  const Region out = rows(p->d_out, p->out_strides, p->out_dtype, p->batch, p->heads_q, p->n_q);
-  const size_t slots = (size_t)p->batch * p->heads_kv * cache->capacity * sizeof(float);
-  const Region weights = bytes(p->d_weights, slots), lse = bytes(p->d_lse, (size_t)p->batch * p->heads_q * p->n_q * sizeof(float));
-  // (the queries are read again, for the weights, after the results are written)
-  if (overlap(q, out) || overlap(q, weights) || overlap(q, lse) || overlap(out, weights) || overlap(out, lse) || overlap(weights, lse) ||
-      !same_or_apart(weights, bytes(p->d_weights_in, slots)))
-    return TQ_ERR_ARG;
   tq::Q8AttnArgs a{};
-  a.c = tq::q8_cache(cache);
-  a.batch = p->batch, a.heads_q = p->heads_q, a.heads_kv = p->heads_kv, a.group = p->heads_q / p->heads_kv;
-  a.n_q = p->n_q, a.max_len = p->max_len, a.q_dtype = p->q_dtype, a.out_dtype = p->out_dtype;
-  a.q = p->d_q, a.out = p->d_out, a.qs = strides(p->q_strides), a.os = strides(p->out_strides);
-  a.seq_lens = p->d_seq_lens, a.new_lens = p->d_new_lens;
-  a.scale = p->scale != 0.f ? p->scale : 0.08838834764831845f;  // 1 / sqrt(128)
-  a.softcap = p->softcap < kNoCap ? p->softcap : 0.f, a.slopes = p->d_slopes, a.qpos = p->d_q_positions, a.kpos = p->d_k_positions;
-  a.kbeg = p->d_key_begin, a.kend = p->d_key_end;
-  a.weights_in = p->d_weights_in, a.weights = p->d_weights, a.lse = p->d_lse;
+  if ((s = attention_args(cache, p, &a)) != TQ_OK) return s;
   if (!tq::q8_attention_fits(a, ctx->num_sms)) return TQ_ERR_UNSUPPORTED;
   if ((s = on_device(ctx)) != TQ_OK) return s;
   a.error = &ctx->dparams->error;
@@ -399,6 +422,35 @@ tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pic
   if ((s = on_device(ctx)) != TQ_OK) return s;
   a.q.error = &ctx->dparams->error;
   return (tq_status)tq::launch_q8_select(a, d_workspace, ctx->num_sms, stream);
+}
+
+tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int n_blocks,
+                                           size_t *out) {
+  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || span <= 0 || n_blocks <= 0) return TQ_ERR_ARG;
+  if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
+  *out = tq::q8_listed_workspace(ctx->num_sms, batch, heads_q / heads_kv, n_q, span);
+  return TQ_OK;
+}
+
+tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *p, const int32_t *d_blocks, int n_blocks, int span,
+                                 void *d_workspace, size_t ws_bytes, void *stream) {
+  tq_status s = check_attention(ctx, cache, p, d_workspace);
+  if (s != TQ_OK) return s;
+  if (!d_blocks || n_blocks <= 0 || span <= 0) return TQ_ERR_ARG;
+  if (!aligned4(d_blocks)) return TQ_ERR_ALIGN;
+  if (p->d_weights) return TQ_ERR_UNSUPPORTED;
+  if (ws_bytes < tq::q8_listed_workspace(ctx->num_sms, p->batch, p->heads_q / p->heads_kv, p->n_q, span)) return TQ_ERR_WORKSPACE;
+  tq::Q8AttnArgs a{};
+  if ((s = attention_args(cache, p, &a)) != TQ_OK) return s;
+  a.blocks = d_blocks, a.n_blocks = n_blocks;
+  a.span = span < p->n_q ? span : p->n_q, a.lists = (int)(((long long)p->n_q + span - 1) / span);
+  const Region lists = bytes(d_blocks, (size_t)p->batch * p->heads_kv * a.lists * n_blocks * sizeof(int32_t));
+  const Written w = written(p);
+  if (overlap(lists, w.out) || overlap(lists, w.lse)) return TQ_ERR_ARG;
+  if (!tq::q8_listed_fits(a)) return TQ_ERR_UNSUPPORTED;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  a.error = &ctx->dparams->error;
+  return (tq_status)tq::launch_q8_listed(a, d_workspace, ctx->num_sms, stream);
 }
 
 }  // extern "C"

@@ -22,6 +22,37 @@ __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, 
   *m = min(max(q, 0), a.n_q);
 }
 
+// The rows [r0, end) of unit x of a sequence, units of `unit` rows; kListed: of list *list.
+template <int KIND>
+__device__ __forceinline__ void unit_span(const Q8AttnArgs &a, int x, int unit, int *r0, int *end, int *list) {
+  *list = 0, *r0 = x * unit, *end = a.group * a.n_q;
+  if constexpr (KIND == kListed) {
+    const int rows = a.group * a.span, units = (rows + unit - 1) / unit;
+    *list = x / units;
+    *r0 = *list * rows + (x - *list * units) * unit;
+    *end = (int)min((long long)*end, ((long long)*list + 1) * rows);
+  }
+}
+// Tiles of 128 slots that a unit goes through whose rows see slots from lo to hi - 1 (kListed: of two list entries each; a block of
+// number j is among the first j + 1 of its list).
+template <int KIND>
+__device__ __forceinline__ int unit_tiles(const Q8AttnArgs &a, int lo, int hi) {
+  if constexpr (KIND == kListed) return (min(a.n_blocks, (hi + kQ8Block - 1) / kQ8Block) + 1) / 2;
+  return (hi + 127) / 128 - lo / 128;
+}
+// The block of entry k of list `list` of (sequence, head) bh, -1 for none that counts.
+__device__ __forceinline__ int list_entry(const Q8AttnArgs &a, long long bh, int list, int k) {
+  if (k >= a.n_blocks) return -1;
+  const int32_t *p = a.blocks + (bh * a.lists + list) * a.n_blocks + k;
+  const int blk = __ldg(p), before = k ? __ldg(p - 1) : -1;
+  if (blk < 0) return -1;
+  if ((k && before < 0) || blk <= before || blk >= a.c.nblk) {
+    set_error(a.error, TQ_ERR_ARG);
+    return -1;
+  }
+  return blk;
+}
+
 // The bits of a row's largest magnitude, a lane holding four of its coordinates.
 __device__ __forceinline__ uint32_t row_top(const float (&x)[4]) {
   uint32_t amax = 0;

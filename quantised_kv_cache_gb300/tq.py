@@ -131,6 +131,8 @@ _SIGNATURES = {
                          _vp, _vp, _vp, _vp]),
     "tq_q8_bounds": (_i, [_vp, ctypes.POINTER(tq_cache), _i, _i, _i, _vp, _vp, _vp, _vp]),
     "tq_q8_select_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "tq_q8_sparse_attention_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "tq_q8_sparse_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _i, _i, _vp, _sz, _vp]),
     "tq_q8_select": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),  # a packed tq_q8_pick
 }
 
@@ -674,6 +676,63 @@ def tq_q8_select(ctx, cache: "Cache", bounds: torch.Tensor, q: torch.Tensor, seq
     if status:
         check(status, "tq_q8_select")
     return blocks
+
+
+def _attn(cache: "Cache", q: torch.Tensor, seq_lens, max_len, new_lens, scale, softcap, slopes, q_positions, k_positions, key_begin,
+          key_end, lse, out, out_dtype, stream):
+    """(a packed tq_q8_attn without weights, out, the tensors' device index) of an attention call over `cache`."""
+    shape, qs = _rows(q, "q")
+    B, Hq, n, _ = shape
+    H, index = cache.heads_kv, cache.device_index
+    if q.get_device() != index or index < 0:
+        raise ValueError("q: the cache's device is wanted")
+    if out is None:
+        out = _made(stream, torch.empty, shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != shape or out.get_device() != index or out_dtype not in (None, out.dtype):
+        raise ValueError("out: q's shape and device are wanted")
+    os = _rows(out, "out")[1]
+    rows = (B, n)
+    a = _pack_attn.pack(
+        B, Hq, H, n, max_len, _any_dtype(q.dtype), _any_dtype(out.dtype), q.data_ptr(), qs[0], qs[1], qs[2], out.data_ptr(), os[0],
+        os[1], os[2], _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
+        scale, softcap, _array(slopes, (Hq,), _f32, index, "slopes") or 0,
+        _array(q_positions, rows, _i32, index, "q_positions") or 0,
+        _array(k_positions, (B, H, cache.capacity), _i32, index, "k_positions") or 0,
+        _array(key_begin, rows, _i32, index, "key_begin") or 0, _array(key_end, rows, _i32, index, "key_end") or 0, 0, 0,
+        _array(lse, (B, Hq, n), _f32, index, "lse") or 0)
+    return a, out, index
+
+
+def tq_q8_sparse_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, span: int, n_blocks: int) -> int:
+    """Bytes for calls of these sizes, and of smaller ones with the same span."""
+    out = _sz()
+    check(lib().tq_q8_sparse_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, span, n_blocks, ctypes.byref(out)),
+          "tq_q8_sparse_attention_workspace")
+    return out.value
+
+
+def tq_q8_sparse_attention(ctx, cache: "Cache", blocks: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor, max_len: int, span: int = 1,
+                           new_lens: Optional[torch.Tensor] = None, scale: float = 0.0, softcap: float = 0.0,
+                           slopes: Optional[torch.Tensor] = None, q_positions: Optional[torch.Tensor] = None,
+                           k_positions: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                           key_end: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """tq_q8_attention over the blocks of lists alone: blocks int32 [batch][heads_kv][ceil(tokens / span)][any number], one list for
+    every `span` query tokens, as tq_q8_select returns them (include/tq.h)."""
+    a, out, index = _attn(cache, q, seq_lens, max_len, new_lens, scale, softcap, slopes, q_positions, k_positions, key_begin, key_end, lse, out,
+                          out_dtype, stream)
+    B, Hq, n, _ = q.shape
+    if span < 1 or len(blocks.shape) != 4:
+        raise ValueError("span and blocks: at least 1, and lists [batch][heads_kv][ceil(tokens / span)][blocks], are wanted")
+    keep = blocks.shape[3]
+    lists = _array(blocks, (B, cache.heads_kv, (n + span - 1) // span, keep), _i32, index, "blocks")
+    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_sparse_attention_workspace(ctx, B, Hq, cache.heads_kv, n, span, keep), stream,
+                                         index, q.device)
+    status = lib().tq_q8_sparse_attention(ctx, cache.struct, a, lists, keep, span, ws, ws_bytes, _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_sparse_attention")
+    return out
 
 
 # ----------------------------------------------------------------------------
