@@ -681,6 +681,19 @@ tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int hea
 tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, const int32_t *d_blocks, int n_blocks,
                                  int span, void *d_workspace, size_t workspace_bytes, void *stream);
 
+/* tq_q8_attention of a batch whose sequences share a prefix, which is read once for all of them. Sequence b is the first
+ * d_prefix_lens[b] tokens of `prefix` (a cache of batch 1 and the same KV heads and context; each in [0, max_prefix],
+ * max_prefix <= its capacity) followed by the d_seq_lens[b] tokens that `cache` holds for it. Slots and positions count through both: slot s of
+ * the cache is slot d_prefix_lens[b] + s of the sequence, in d_key_begin and d_key_end (default [0, the query's own slot + 1)) and in the bias'
+ * distances. a->max_len bounds d_seq_lens, which count the cache's tokens. a->d_q_positions, a->d_k_positions, a->d_weights and a->d_weights_in have to be
+ * NULL (TQ_ERR_UNSUPPORTED). A d_prefix_lens[b] out of range is cut and sets the error word to TQ_ERR_ARG. The two
+ * parts' sums are joined in fp32 before the one rounding of the result; the prefix's rows are the whole batch's (batch x n_q x group), whose number
+ * decides the precision of its probabilities as in tq_q8_attention. Workspace: of these sizes or larger ones. */
+tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
+                                           size_t *out);
+tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix,
+                                 const tq_cache *cache, const tq_q8_attn *a, void *d_workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

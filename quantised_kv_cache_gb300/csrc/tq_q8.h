@@ -105,7 +105,13 @@ struct Q8AttnArgs {
   // kListed: [batch][heads_kv][lists][n_blocks], a list for every `span` query tokens
   const int32_t *blocks = nullptr;
   int n_blocks = 0, span = 0, lists = 0;
+  // kPrefix (where batch is 1, n_q counts all sequences' tokens, c and max_len are the prefix's) and kOwn
+  const int32_t *prefix_lens = nullptr;
+  int max_prefix = 0, fold = 0, own_max = 0;  // fold: a sequence's query tokens; own_max: bounds seq_lens
+  float *prior = nullptr;                     // the prefix's part of every row, [heads_q][batch x query tokens][kPriorRow]
 };
+// O as the sum of 2^(t - m) v, m, the sum of 2^(t - m), the same of the numbers that entered O, pad
+constexpr int kPriorRow = kD + 4;
 // Lists of blocks: q has the queries, lengths and ranges.
 struct Q8SelectArgs {
   Q8AttnArgs q;
@@ -136,6 +142,14 @@ int launch_q8_listed(const Q8AttnArgs &a, void *workspace, int num_sms, void *st
 size_t q8_listed_many_workspace(int num_sms, int batch, int group, int n_q, int span);
 bool q8_listed_many_fits(const Q8AttnArgs &a);
 int launch_q8_listed_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
+// own: the call's arguments; prefix: its cache
+size_t q8_shared_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q);
+bool q8_shared_fits(const Q8AttnArgs &own, int num_sms);
+int launch_q8_shared(const Q8AttnArgs &own, const Q8Cache &prefix, void *workspace, int num_sms, void *stream);
+bool q8_prefix_many_fits(const Q8AttnArgs &a, int num_sms);
+int launch_q8_prefix_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
+bool q8_own_many_fits(const Q8AttnArgs &a, int num_sms);
+int launch_q8_own_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 int launch_q8_attention(const Q8AttnArgs &a, void *workspace, size_t ws_bytes, int num_sms, void *stream);
 
 }  // namespace tq

@@ -110,11 +110,11 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     const int b = b0 + tid / rts;
     int len, m, r0, end, list;
     unit_span<KIND>(a, rt0 + tid % rts, kUnitRows, &r0, &end, &list);
-    seq_sizes(a, b, &len, &m, blockIdx.x == 0);
+    seq_sizes<KIND>(a, b, &len, &m, blockIdx.x == 0);
     const int i0 = r0 / G, i1 = (min(end, r0 + kUnitRows) - 1) / G;
     int lo = 0x7fffffff, hi = 0;
     for (int i = i0; i <= i1; ++i) {
-      const int2 r = row_range(a, b, i, len, m);
+      const int2 r = row_range<KIND>(a, b, i, len, m);
       if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
     }
     if (hi == 0) lo = 0;
@@ -268,20 +268,20 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       {
         const int row = row0 + warp, i = row / G, hq = h * G + row % G;
         int len, m;
-        seq_sizes(a, b, &len, &m, false);
+        seq_sizes<KIND>(a, b, &len, &m, false);
         const bool live = warp < NR && row < row_end && i < m;
         uint32_t w[T];
-        const int ex = row_e5m2<T>(a, b, hq, i, live, lane, w);
+        const int ex = row_e5m2<T, KIND>(a, b, hq, i, live, lane, w);
         bar_all();  // everyone is done with the unit before
         if (warp < NR) {
 #pragma unroll
           for (int k = 0; k < T; ++k) *reinterpret_cast<uint32_t *>(qbuf + q8_off(k * NR + warp, 4 * lane)) = w[k];
           if (lane == 0) {
             sm.qscale[warp] = pow2i(ex);
-            const int2 rg = live ? row_range(a, b, i, len, m) : make_int2(0, 0);
+            const int2 rg = live ? row_range<KIND>(a, b, i, len, m) : make_int2(0, 0);
             sm.range[warp] = rg;
             sm.slope[warp] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-            sm.qpos[warp] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : len - m + i;
+            sm.qpos[warp] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : query_slot<KIND>(a, i, len, m);
           }
         }
         fence_proxy_async_shared();
@@ -453,17 +453,11 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           }
           const int row = row0 + r, i = row / G;
           int len, mm;
-          seq_sizes(a, b, &len, &mm, false);
+          seq_sizes<KIND>(a, b, &len, &mm, false);
           if (row >= row_end || i >= mm) continue;
           if (whole) {
             const int hq = h * G + row % G;
-            const float y = slr == 0.f ? 0.f : x / slr;
-            const long long off = b * a.os.b + hq * a.os.h + i * a.os.t + wt;
-            if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
-            else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
-            else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
-            if (a.lse && wt == 0)
-              a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (top + log2f(sl) - 15.f) * kLn2;
+            finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f);
           } else {
             part[r * kPartRow + wt] = x;
             if (wt == 0) {
@@ -508,7 +502,7 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
   row += r;
   if (cut.parts < 2 || row >= row_end) return;
   int len, m;
-  seq_sizes(a, cut.b, &len, &m, false);
+  seq_sizes<KIND>(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (i >= m) return;
   const int d = threadIdx.x & 127, grp = threadIdx.x >> 7;
@@ -537,12 +531,7 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
   l = sl[0] + sl[1] + sl[2] + sl[3];
   lr = slr[0] + slr[1] + slr[2] + slr[3];
   const int hq = cut.h * G + row % G;
-  const float y = lr == 0.f ? 0.f : o / lr;
-  const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + d;
-  if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
-  else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
-  else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
-  if (a.lse && d == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 15.f) * kLn2;
+  finish_row<KIND>(a, cut.b, hq, i, d, o, top, l, lr, 15.f);
 }
 
 template <int NR, int T, int KIND>

@@ -453,4 +453,35 @@ tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const
   return (tq_status)tq::launch_q8_listed(a, d_workspace, ctx->num_sms, stream);
 }
 
+tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
+                                           size_t *out) {
+  if (!ctx || !out || batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_q <= 0 || max_prefix <= 0 || max_len <= 0)
+    return TQ_ERR_ARG;
+  if (ctx->scheme != TQ_SCHEME_Q8) return TQ_ERR_STATE;
+  *out = tq::q8_shared_workspace(ctx->num_sms, batch, heads_q, heads_kv, n_q);
+  return TQ_OK;
+}
+
+tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix, const tq_cache *cache,
+                                 const tq_q8_attn *p, void *d_workspace, size_t ws_bytes, void *stream) {
+  tq_status s = check_attention(ctx, cache, p, d_workspace);
+  if (s != TQ_OK) return s;
+  if (!d_prefix_lens || max_prefix <= 0) return TQ_ERR_ARG;
+  if ((s = tq::q8_check_cache(ctx, prefix, 1, p->heads_kv)) != TQ_OK) return s;
+  if (max_prefix > prefix->capacity) return TQ_ERR_ARG;
+  if (!aligned4(d_prefix_lens)) return TQ_ERR_ALIGN;
+  if (p->d_weights || p->d_q_positions) return TQ_ERR_UNSUPPORTED;
+  if (ws_bytes < tq::q8_shared_workspace(ctx->num_sms, p->batch, p->heads_q, p->heads_kv, p->n_q)) return TQ_ERR_WORKSPACE;
+  tq::Q8AttnArgs a{};
+  if ((s = attention_args(cache, p, &a)) != TQ_OK) return s;
+  a.prefix_lens = d_prefix_lens, a.max_prefix = max_prefix;
+  const Region lens = bytes(d_prefix_lens, p->batch * sizeof(int32_t));
+  const Written w = written(p);
+  if (overlap(lens, w.out) || overlap(lens, w.lse)) return TQ_ERR_ARG;
+  if (!tq::q8_shared_fits(a, ctx->num_sms)) return TQ_ERR_UNSUPPORTED;
+  if ((s = on_device(ctx)) != TQ_OK) return s;
+  a.error = &ctx->dparams->error;
+  return (tq_status)tq::launch_q8_shared(a, tq::q8_cache(prefix), d_workspace, ctx->num_sms, stream);
+}
+
 }  // extern "C"

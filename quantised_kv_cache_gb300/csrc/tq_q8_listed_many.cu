@@ -8,26 +8,26 @@ namespace tq {
 namespace {
 
 // A list's units do not reach into the next list's rows. Those of up to 128 rows are one row tile: units apart.
-bool units_apart(long long rows) { return rows <= unit_rows(true); }
-long long units_of(long long rows, int lists) {
-  const long long unit = unit_rows(units_apart(rows));
+bool list_apart(long long rows) { return rows <= unit_rows(true); }
+long long list_units(long long rows, int lists) {
+  const long long unit = unit_rows(list_apart(rows));
   return (rows + unit - 1) / unit * lists;
 }
 
 }  // namespace
 
 size_t q8_listed_many_workspace(int num_sms, int batch, int group, int n_q, int span) {
-  return many_bytes(num_sms, (size_t)units_of((long long)group * span, (n_q + span - 1) / span) * batch);
+  return many_bytes(num_sms, (size_t)list_units((long long)group * span, (n_q + span - 1) / span) * batch);
 }
 
 bool q8_listed_many_fits(const Q8AttnArgs &a) {
-  const long long entries = units_of((long long)a.group * a.span, a.lists) * a.batch, tiles = (std::min(a.n_blocks, a.c.nblk) + 1) / 2;
+  const long long entries = list_units((long long)a.group * a.span, a.lists) * a.batch, tiles = (std::min(a.n_blocks, a.c.nblk) + 1) / 2;
   return entries <= 1 << 24 && entries * tiles <= 0x7fffffff;
 }
 
 int launch_q8_listed_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream) {
   const long long rows = (long long)a.group * a.span;
-  return launch_many<kListed>(a, units_apart(rows), units_of(rows, a.lists), (char *)workspace, num_sms, (cudaStream_t)stream);
+  return launch_many<kListed>(a, list_apart(rows), list_units(rows, a.lists), (char *)workspace, num_sms, (cudaStream_t)stream);
 }
 
 }  // namespace tq

@@ -76,11 +76,11 @@ __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__
   const int b = e / p.pairs, G = a.group;
   int len, m, r0, end, list;
   unit_span<KIND>(a, e % p.pairs, p.unit, &r0, &end, &list);
-  seq_sizes(a, b, &len, &m, lane == 0);
+  seq_sizes<KIND>(a, b, &len, &m, lane == 0);
   const int i0 = r0 / G, i1 = min(m - 1, (min(end, r0 + p.unit) - 1) / G);
   int lo = 0x7fffffff, hi = 0, maxbeg = 0, minend = 0x7fffffff;
   for (int i = i0 + lane; i <= i1; i += 32) {
-    const int2 r = row_range(a, b, i, len, m);
+    const int2 r = row_range<KIND>(a, b, i, len, m);
     if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
     maxbeg = max(maxbeg, r.x);
     minend = min(minend, r.y);  // 0 for a row that sees nothing
@@ -235,6 +235,44 @@ __device__ __forceinline__ uint32_t e4m3_h2(uint32_t b) {
 __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
   const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<__half2 *>(&y));
   return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Coordinates d .. d + N - 1 of a row: o = sum 2^(t - mx + 8) v, l the same of 1. Written to where the kind's results go, joined with the
+// prefix's part where there is one.
+template <int KIND, int N>
+__device__ __forceinline__ void finish_part(const Q8AttnArgs &a, int b, int hq, int i, int d, float (&o)[N], float mx, float l) {
+  if constexpr (KIND == kPrefix) {
+    float *row = a.prior + ((long long)hq * a.n_q + i) * kPriorRow;
+#pragma unroll
+    for (int q = 0; q < N; q += 4) *reinterpret_cast<float4 *>(row + d + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+    if (d == 0) *reinterpret_cast<float4 *>(row + kD) = make_float4(mx - 8.f, l, l, 0.f);
+    return;
+  }
+  float lr = l, m = mx;
+  if constexpr (KIND == kOwn) {
+    const Prior p = prior_of(a, b, hq, i, mx - 8.f);
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(p.row + d + q));
+      o[q] = fmaf(x.x, p.by, o[q] * p.own), o[q + 1] = fmaf(x.y, p.by, o[q + 1] * p.own);
+      o[q + 2] = fmaf(x.z, p.by, o[q + 2] * p.own), o[q + 3] = fmaf(x.w, p.by, o[q + 3] * p.own);
+    }
+    lr = fmaf(__ldg(p.row + kD + 2), p.by, l * p.own);
+    l = fmaf(__ldg(p.row + kD + 1), p.by, l * p.own);
+    m = p.m + 8.f;
+  }
+  const float inv = lr == 0.f ? 0.f : 1.f / lr;
+  const long long off = b * a.os.b + hq * a.os.h + i * a.os.t + d;
+  constexpr int V = N < 8 ? N : 8;
+#pragma unroll
+  for (int q = 0; q < N; q += V) {
+    float y[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) y[k] = o[q + k] * inv;
+    if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, V>(static_cast<__nv_bfloat16 *>(a.out) + off + q, y);
+    else store_vec<__half, V>(static_cast<__half *>(a.out) + off + q, y);
+  }
+  if (a.lse && d == 0) a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (m + log2f(l) - 8.f) * kLn2;
 }
 
 template <int TERMS, int EXTRA, bool APART, int KIND>
@@ -449,7 +487,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
                 minend = p.entry[u.e].minend;
       const long long bh = (long long)u.b * a.heads_kv + u.h;
       int len, m;
-      seq_sizes(a, u.b, &len, &m, false);
+      seq_sizes<KIND>(a, u.b, &len, &m, false);
       const int G = a.group;
       int unit0, unit1, list;
       unit_span<KIND>(a, u.pair, kUnit, &unit0, &unit1, &list);
@@ -460,7 +498,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       for (int k0 = 0; k0 < 16; k0 += 8) {
         uint2 raw[8];
         const int first_row = unit0 + (APART ? 0 : rt * 128) + (warp & 7) * 16 + k0;
-        load_rows(a, u.b, u.h, m, first_row, lane, raw);
+        load_rows<KIND>(a, u.b, u.h, m, first_row, lane, raw);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = (warp & 7) * 16 + k0 + k, row = first_row + k;
@@ -481,9 +519,9 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       const float qs = sm.top[rt][0][lrow];
       const int row = unit0 + in_unit, qi = row / G, hq = u.h * G + row % G;
       const bool live = row < unit1 && qi < m;
-      const int2 rg = live ? row_range(a, u.b, qi, len, m) : make_int2(0, 0);
+      const int2 rg = live ? row_range<KIND>(a, u.b, qi, len, m) : make_int2(0, 0);
       const float slope = EXTRA && live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-      const int qp = !EXTRA || !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)u.b * a.n_q + qi) : len - m + qi;
+      const int qp = !EXTRA || !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)u.b * a.n_q + qi) : query_slot<KIND>(a, qi, len, m);
       bar_rt(rt);
 
       float o[64];
@@ -708,17 +746,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       const bool whole = u.t0 == 0 && u.end == g + u.cnt;
       if (live) {
         if (whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const long long off = u.b * a.os.b + hq * a.os.h + qi * a.os.t + 64 * half;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = o[8 * q + i] * inv;
-            if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(a.out) + off + 8 * q, y);
-            else store_vec<__half, 8>(static_cast<__half *>(a.out) + off + 8 * q, y);
-          }
-          if (a.lse && !half) a.lse[((long long)u.b * a.heads_q + hq) * a.n_q + qi] = (mx + log2f(l) - 8.f) * kLn2;
+          finish_part<KIND>(a, u.b, hq, qi, 64 * half, o, mx, l);
         } else {
           float *part = p.parts + ((long long)slice * 2 + (u.t0 == 0 ? 1 : 0)) * part_of(kUnit);
           const int r = in_unit;
@@ -761,7 +789,7 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   unit_span<KIND>(a, cut.pair, kUnit, &row, &unit1, &list);
   row += r;
   int len, m;
-  seq_sizes(a, cut.b, &len, &m, false);
+  seq_sizes<KIND>(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (row >= unit1 || i >= m) return;
   auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * part_of(kUnit); };
@@ -782,17 +810,9 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
     }
     l = fmaf(x[kUnit * (kD + 1) + r], f, l);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int hq = cut.h * G + row % G;
 #pragma unroll
-  for (int j = 0; j < kJoin; ++j) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[j][k] *= inv;
-    const long long off = cut.b * a.os.b + hq * a.os.h + i * a.os.t + 4 * (col + 32 / kJoin * j);
-    if (a.out_dtype == TQ_BF16) store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(a.out) + off, o[j]);
-    else store_vec<__half, 4>(static_cast<__half *>(a.out) + off, o[j]);
-  }
-  if (a.lse && col == 0) a.lse[((long long)cut.b * a.heads_q + hq) * a.n_q + i] = (top + log2f(l) - 8.f) * kLn2;
+  for (int j = 0; j < kJoin; ++j) finish_part<KIND>(a, cut.b, hq, i, 4 * (col + 32 / kJoin * j), o[j], top, l);
 }
 
 template <int TERMS, int EXTRA, bool APART, int KIND>
@@ -815,6 +835,23 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+// Up to 128 rows are one row tile, and the other of a shared unit would have no rows: with units apart every row tile works, but twice as
+// many slices are joined and each has half of the ring. So where a CTA has a dozen tiles. 64 rows, 8 KV heads, bf16 (fp16): 8 sequences of
+// 16384 tokens (54 tiles a CTA) 121 us apart, 165 us (170, 198) not, capped 178 and 284; 2 of them (13) 59 and 63 (73, 73); one (7) 49 and 45.
+bool units_apart(const Q8AttnArgs &a, int num_sms) {
+  const long long tiles = (long long)a.batch * a.heads_kv * ((a.max_len + kTile - 1) / kTile);
+  return (long long)a.group * a.n_q <= unit_rows(true) && tiles >= 12LL * num_sms;
+}
+long long units_of(const Q8AttnArgs &a, bool apart) {
+  const long long unit = unit_rows(apart);
+  return ((long long)a.group * a.n_q + unit - 1) / unit;
+}
+// Entries' tiles are counted in 32 bits.
+bool many_fits(const Q8AttnArgs &a, int num_sms) {
+  const long long entries = units_of(a, units_apart(a, num_sms)) * a.batch, tiles = (a.max_len + kTile - 1) / kTile;
+  return entries <= 1 << 24 && entries * tiles <= 0x7fffffff;
+}
 
 // Workspace for `entries` units of either kind.
 size_t many_bytes(int num_sms, size_t entries) {

@@ -5,21 +5,75 @@
 
 namespace tq {
 
+// Query token i of a kPrefix call: of which sequence, its number in it, the sequence's lengths (prefix, own, query tokens).
+struct Folded {
+  int b, i, prefix, len, m;
+};
+__device__ __forceinline__ Folded folded(const Q8AttnArgs &a, int i) {
+  Folded f;
+  f.b = i / a.fold, f.i = i - f.b * a.fold;
+  f.prefix = min(max(__ldg(a.prefix_lens + f.b), 0), a.max_prefix);
+  f.len = min(max(__ldg(a.seq_lens + f.b), 0), a.own_max);
+  f.m = a.new_lens ? min(max(__ldg(a.new_lens + f.b), 0), a.fold) : a.fold;
+  return f;
+}
+
 // A row's key range: query token i of sequence b, whose length is len and whose query tokens number m.
+template <int KIND = kWhole>
 __device__ __forceinline__ int2 row_range(const Q8AttnArgs &a, int b, int i, int len, int m) {
   if (i >= m) return make_int2(0, 0);
-  int beg = 0, end = len - m + i + 1;
-  if (a.kbeg) beg = max(0, __ldg(a.kbeg + (long long)b * a.n_q + i));
-  if (a.kend) end = __ldg(a.kend + (long long)b * a.n_q + i);
-  end = min(end, len);
+  int beg = 0, end;
+  if constexpr (KIND == kPrefix) {
+    const Folded f = folded(a, i);
+    if (f.i >= f.m) return make_int2(0, 0);
+    end = f.prefix + f.len - f.m + f.i + 1;
+    if (a.kbeg) beg = max(0, __ldg(a.kbeg + i));
+    if (a.kend) end = __ldg(a.kend + i);
+    end = min(end, f.prefix);
+  } else {
+    end = len - m + i + 1;
+    if (a.kbeg) beg = max(0, __ldg(a.kbeg + (long long)b * a.n_q + i));
+    if (a.kend) end = __ldg(a.kend + (long long)b * a.n_q + i);
+    if constexpr (KIND == kOwn) {  // ranges count the prefix's slots
+      const int prefix = min(max(__ldg(a.prefix_lens + b), 0), a.max_prefix);
+      beg = max(0, beg - prefix);
+      if (a.kend) end = max(end, 0) - prefix;
+    }
+    end = min(end, len);
+  }
   return end > beg ? make_int2(beg, end) : make_int2(0, 0);
 }
 
+template <int KIND = kWhole>
 __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, int *m, bool report) {
-  int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
-  if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
-  *len = min(max(n, 0), a.max_len);
-  *m = min(max(q, 0), a.n_q);
+  if constexpr (KIND == kPrefix) {
+    *len = a.max_len, *m = a.n_q;
+  } else {
+    int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
+    if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
+    if constexpr (KIND == kOwn) {
+      const int prefix = __ldg(a.prefix_lens + b);
+      if (report && (prefix < 0 || prefix > a.max_prefix)) set_error(a.error, TQ_ERR_ARG);
+    }
+    *len = min(max(n, 0), a.max_len);
+    *m = min(max(q, 0), a.n_q);
+  }
+}
+
+// A query's slot, among those that its keys' slots count in.
+template <int KIND>
+__device__ __forceinline__ int query_slot(const Q8AttnArgs &a, int i, int len, int m) {
+  if constexpr (KIND == kPrefix) {
+    const Folded f = folded(a, i);
+    return f.prefix + f.len - f.m + f.i;
+  }
+  return len - m + i;
+}
+
+template <int KIND>
+__device__ __forceinline__ long long query_offset(const Q8AttnArgs &a, int b, int hq, int i) {
+  if constexpr (KIND == kPrefix) b = i / a.fold, i -= b * a.fold;
+  return b * a.qs.b + hq * a.qs.h + i * a.qs.t;
 }
 
 // The rows [r0, end) of unit x of a sequence, units of `unit` rows; kListed: of list *list.
@@ -75,19 +129,20 @@ __device__ __forceinline__ int row_terms(const float (&x)[4], uint32_t (&w)[3]) 
   return e;
 }
 // Coordinates 4 lane .. 4 lane + 3 of row (head hq, query token i) of sequence b; zeros for a row that is not live.
+template <int KIND = kWhole>
 __device__ __forceinline__ void row_coords(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, float (&x)[4]) {
   x[0] = x[1] = x[2] = x[3] = 0.f;
   if (!live) return;
-  const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + 4 * lane;
+  const long long off = query_offset<KIND>(a, b, hq, i) + 4 * lane;
   if (a.q_dtype == TQ_F32) load_vec<float, 4>(static_cast<const float *>(a.q) + off, x);
   else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
   else load_vec<__half, 4>(static_cast<const __half *>(a.q) + off, x);
 }
 // Few rows: T e5m2 terms.
-template <int T>
+template <int T, int KIND = kWhole>
 __device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int i, bool live, int lane, uint32_t (&w)[T]) {
   float x[4];
-  row_coords(a, b, hq, i, live, lane, x);
+  row_coords<KIND>(a, b, hq, i, live, lane, x);
   const uint32_t amax = row_top(x);
   const int e = row_exponent(amax, 14);
   const float f = pow2i(-e);
@@ -103,11 +158,12 @@ __device__ __forceinline__ int row_e5m2(const Q8AttnArgs &a, int b, int hq, int 
 
 // Many rows: 4 coordinates a lane of eight rows of 16-bit queries from first_row on, their loads in flight at once: no branch in their
 // way, a row that is not there loads another (and counts as 0).
+template <int KIND = kWhole>
 __device__ __forceinline__ void load_rows(const Q8AttnArgs &a, int b, int h, int m, int first_row, int lane, uint2 (&raw)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int row = min(first_row + k, a.group * a.n_q - 1), i = row / a.group;
-    const long long off = b * a.qs.b + (h * a.group + row - i * a.group) * a.qs.h + min(i, max(m - 1, 0)) * a.qs.t + 4 * lane;
+    const long long off = query_offset<KIND>(a, b, h * a.group + row - i * a.group, min(i, max(m - 1, 0))) + 4 * lane;
     raw[k] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
   }
 }
@@ -138,6 +194,47 @@ __device__ __forceinline__ void tmem_term_sums(uint32_t taddr, float (&out)[NR])
       for (int r = 0; r < NR; ++r)
         out[r] = part == kParts - 1 && k == C / NR - 1 ? v[k * NR + r] : out[r] + v[k * NR + r];
   }
+}
+
+// A row's part of the prefix, and the factors that bring it and the row's own part (whose sums are relative to 2^m) to one reference.
+struct Prior {
+  const float *row;
+  float m, by, own;  // the reference, the prefix part's factor, the own part's
+};
+__device__ __forceinline__ Prior prior_of(const Q8AttnArgs &a, int b, int hq, int i, float m) {
+  Prior p;
+  p.row = a.prior + (((long long)hq * a.batch + b) * a.n_q + i) * kPriorRow;
+  const float was = __ldg(p.row + kD);
+  p.m = fmaxf(m, was);
+  p.by = was == -INFINITY ? 1.f : ex2_approx(was - p.m);  // without a maximum: zeros (or NaN)
+  p.own = m == -INFINITY ? 1.f : ex2_approx(m - p.m);
+  return p;
+}
+
+// Coordinate d of a row: x = sum 2^(t - top + shift) v, l and lr the same of 1 (lr of the numbers as they entered x). Written to where the kind's
+// results go, joined with the prefix's part where there is one.
+template <int KIND>
+__device__ __forceinline__ void finish_row(const Q8AttnArgs &a, int b, int hq, int i, int d, float x, float top, float l, float lr, float shift) {
+  if constexpr (KIND == kPrefix) {
+    float *row = a.prior + ((long long)hq * a.n_q + i) * kPriorRow;
+    row[d] = x;
+    if (d == 0) row[kD] = top - shift, row[kD + 1] = l, row[kD + 2] = lr;
+    return;
+  }
+  float m = top;
+  if constexpr (KIND == kOwn) {
+    const Prior p = prior_of(a, b, hq, i, top - shift);
+    x = fmaf(__ldg(p.row + d), p.by, x * p.own);
+    l = fmaf(__ldg(p.row + kD + 1), p.by, l * p.own);
+    lr = fmaf(__ldg(p.row + kD + 2), p.by, lr * p.own);
+    m = p.m + shift;
+  }
+  const float y = lr == 0.f ? 0.f : x / lr;
+  const long long off = b * a.os.b + hq * a.os.h + i * a.os.t + d;
+  if (a.out_dtype == TQ_F32) static_cast<float *>(a.out)[off] = y;
+  else if (a.out_dtype == TQ_BF16) static_cast<__nv_bfloat16 *>(a.out)[off] = __float2bfloat16_rn(y);
+  else static_cast<__half *>(a.out)[off] = __float2half_rn(y);
+  if (a.lse && d == 0) a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] = (m + log2f(l) - shift) * kLn2;
 }
 
 __device__ __forceinline__ void bar_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }

@@ -1,0 +1,53 @@
+// Attention of a batch behind a shared prefix in a cache of its own (tq_q8_shared_attention).
+//
+// out = (X1 + X2) / (l1 + l2): the rows' sums over the prefix, X1 = sum 2^(t - m) v and l1 = sum 2^(t - m), then those over the sequence's own
+// tokens, on one reference. Over the prefix the rows of all sequences are the rows of one (its head's, batch x query tokens x
+// group of them), so that its keys and values are read once for the batch and make operands of up to 256 rows. Their parts go to the workspace,
+// where the kernels of the own tokens fetch them as they finish a row: no pass of its own joins them.
+
+#include "tq_q8_few.cuh"
+
+namespace tq {
+
+static bool takes_few(long long rows, int out_dtype) { return rows <= kFewRows || out_dtype == TQ_F32; }
+
+static size_t prior_bytes(int batch, int heads_q, int n_q) { return (size_t)heads_q * batch * n_q * kPriorRow * sizeof(float); }
+
+size_t q8_shared_workspace(int num_sms, int batch, int heads_q, int heads_kv, int n_q) {
+  const int group = heads_q / heads_kv;
+  // (the prefix's rows are one sequence's; their units are no more than the sequences')
+  const size_t many = (long long)group * n_q * batch <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, group, n_q);
+  return prior_bytes(batch, heads_q, n_q) + std::max(few_bytes(num_sms), many);
+}
+
+static Q8AttnArgs of_prefix(const Q8AttnArgs &own, const Q8Cache &prefix) {
+  Q8AttnArgs a = own;
+  a.c = prefix, a.batch = 1, a.n_q = own.batch * own.n_q, a.max_len = own.max_prefix, a.fold = own.n_q, a.own_max = own.max_len;
+  return a;
+}
+
+bool q8_shared_fits(const Q8AttnArgs &own, int num_sms) {
+  if ((long long)own.group * own.n_q * own.batch > 0x7fffffff - 1023) return false;         // rows of the prefix's KV head
+  if ((long long)own.max_prefix + own.max_len > kQ8MostSlots) return false;                 // slots of a sequence
+  const Q8AttnArgs pre = of_prefix(own, own.c);
+  return (takes_few((long long)pre.group * pre.n_q, own.out_dtype) || q8_prefix_many_fits(pre, num_sms)) &&
+         (takes_few((long long)own.group * own.n_q, own.out_dtype) || q8_own_many_fits(own, num_sms));
+}
+
+template <int KIND>
+static int launch_part(const Q8AttnArgs &a, char *w, int num_sms, void *stream, int (*many)(const Q8AttnArgs &, void *, int, void *)) {
+  const long long rows = (long long)a.group * a.n_q, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
+  if (!takes_few(rows, a.out_dtype)) return many(a, w, num_sms, stream);
+  return launch_few<KIND>(a, (int)std::min(rows, 1024ll), (rows + unit - 1) / unit, (a.max_len + kTile - 1) / kTile, w, num_sms,
+                          (cudaStream_t)stream);
+}
+
+int launch_q8_shared(const Q8AttnArgs &args, const Q8Cache &prefix, void *workspace, int num_sms, void *stream) {
+  Q8AttnArgs own = args;
+  own.prior = (float *)workspace;
+  char *w = (char *)workspace + prior_bytes(own.batch, own.heads_q, own.n_q);
+  const int s = launch_part<kPrefix>(of_prefix(own, prefix), w, num_sms, stream, launch_q8_prefix_many);
+  return s != TQ_OK ? s : launch_part<kOwn>(own, w, num_sms, stream, launch_q8_own_many);
+}
+
+}  // namespace tq

@@ -133,6 +133,8 @@ _SIGNATURES = {
     "tq_q8_select_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "tq_q8_sparse_attention_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "tq_q8_sparse_attention": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _i, _i, _vp, _sz, _vp]),
+    "tq_q8_shared_attention_workspace": (_i, [_vp, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "tq_q8_shared_attention": (_i, [_vp, ctypes.POINTER(tq_cache), _vp, _i, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),
     "tq_q8_select": (_i, [_vp, ctypes.POINTER(tq_cache), ctypes.c_char_p, _vp, _sz, _vp]),  # a packed tq_q8_pick
 }
 
@@ -732,6 +734,36 @@ def tq_q8_sparse_attention(ctx, cache: "Cache", blocks: torch.Tensor, q: torch.T
     status = lib().tq_q8_sparse_attention(ctx, cache.struct, a, lists, keep, span, ws, ws_bytes, _raw_stream(stream, index))
     if status:
         check(status, "tq_q8_sparse_attention")
+    return out
+
+
+def tq_q8_shared_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, max_prefix: int, max_len: int) -> int:
+    """Bytes for calls of these sizes and of smaller ones."""
+    out = _sz()
+    check(lib().tq_q8_shared_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_prefix, max_len, ctypes.byref(out)),
+          "tq_q8_shared_attention_workspace")
+    return out.value
+
+
+def tq_q8_shared_attention(ctx, prefix: "Cache", prefix_lens: torch.Tensor, max_prefix: int, cache: "Cache", q: torch.Tensor,
+                           seq_lens: torch.Tensor, max_len: int, new_lens: Optional[torch.Tensor] = None, scale: float = 0.0,
+                           softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                           key_end: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """tq_q8_attention of a batch whose sequences are the first prefix_lens[b] tokens of `prefix` (a cache of batch 1), read once for
+    all of them, followed by the seq_lens[b] tokens that `cache` holds for each; key ranges count through both (include/tq.h)."""
+    a, out, index = _attn(cache, q, seq_lens, max_len, new_lens, scale, softcap, slopes, None, None, key_begin, key_end, lse, out, out_dtype,
+                          stream)
+    B, Hq, n, _ = q.shape
+    if prefix.device_index != index:
+        raise ValueError("prefix: the cache's device is wanted")
+    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_shared_attention_workspace(ctx, B, Hq, cache.heads_kv, n, max_prefix, max_len),
+                                         stream, index, q.device)
+    status = lib().tq_q8_shared_attention(ctx, prefix.struct, _array(prefix_lens, (B,), _i32, index, "prefix_lens"), max_prefix, cache.struct, a,
+                                          ws, ws_bytes, _raw_stream(stream, index))
+    if status:
+        check(status, "tq_q8_shared_attention")
     return out
 
 
