@@ -123,6 +123,7 @@ struct Q8SelectArgs {
 };
 size_t q8_select_workspace(int batch, int heads_kv, int group, int n_q, int span, int max_len);
 bool q8_select_fits(const Q8SelectArgs &a);
+int launch_q8_scores(const Q8SelectArgs &a, int num_sms, void *stream);  // into a.keys
 int launch_q8_select(const Q8SelectArgs &a, void *workspace, int num_sms, void *stream);
 
 // The workspace with room for all that is worth keeping; *least (if not NULL): what the call cannot do without, which never falls as

@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "tq_q8_rows.cuh"
+#include "tq_q8_select.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -25,15 +26,9 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kHeld = 32768;               // scores kept in shared memory (128 KB): 2 M tokens
 constexpr int kOwn = 8;                    // scores a thread of the choosing CTA keeps in registers
-constexpr uint32_t kAlways = 0xffffffffu;  // a block that is taken whatever its score
+// Rows up to which a list's scores are formed here, by products of bytes; more go to the tensor cores.
+constexpr long long kFewRows = 16;
 constexpr int kNone = -0x7fffffff - 1;
-
-// order-preserving; never kAlways; 0 below all numbers
-__device__ __forceinline__ uint32_t score_key(float w) {
-  const uint32_t u = __float_as_uint(w + 0.f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 
 struct Shared {
   uint32_t plus[16][kD / 4], minus[16][kD / 4];  // of 16 rows: w+ and w-, four coordinates a word
@@ -141,7 +136,7 @@ __device__ __forceinline__ void lane_sums(int *s, int lane, int &at) {
   }
 }
 
-// NR: 1, 4 or 16 rows at a time
+// NR: 1, 4 or 16 rows at a time; 0: the scores are there (q8_scores_kernel)
 template <int NR>
 __global__ void __launch_bounds__(kThreads) q8_choose_kernel(const __grid_constant__ Q8SelectArgs a) {
   extern __shared__ __align__(16) uint32_t held[];
@@ -162,6 +157,23 @@ __global__ void __launch_bounds__(kThreads) q8_choose_kernel(const __grid_consta
     if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
   }
   lo = __reduce_min_sync(kFull, lo), hi = __reduce_max_sync(kFull, hi);
+  if constexpr (NR == 0) {
+    if (lane == 0) sm.lo[warp] = lo, sm.hi[warp] = hi;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) lo = min(lo, sm.lo[w]), hi = max(hi, sm.hi[w]);
+    const int first = hi > 0 ? lo / kQ8Block : 0, n = (hi + kQ8Block - 1) / kQ8Block - first;
+    int32_t *out = a.blocks + list * a.keep;
+    const uint32_t *keys = a.keys + list * a.keys_ld + first;
+    if (n <= a.keep) {
+      for (int i = tid; i < a.keep; i += kThreads) out[i] = i < n ? first + i : -1;
+    } else if (n <= kThreads * kOwn) {
+      choose<true>(keys, n, a.keep, first, out, sm);
+    } else {
+      choose<false>(keys, n, a.keep, first, out, sm);
+    }
+    return;
+  } else {
   // ---- the rows' largest coordinate
   const int rows = max(0, tok1 - tok0) * G;
   auto row = [&](int r, float (&x)[4]) {  // a whole warp; whether it counts
@@ -293,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) q8_choose_kernel(const __grid_consta
   const uint32_t *keys = big ? far : held;
   if (n <= kThreads * kOwn) choose<true>(keys, n, a.keep, first, out, sm);
   else choose<false>(keys, n, a.keep, first, out, sm);
+  }
 }
 
 template <int NR>
@@ -319,7 +332,7 @@ long long lists_of(int n_q, int span) { return ((long long)n_q + span - 1) / spa
 
 size_t q8_select_workspace(int batch, int heads_kv, int group, int n_q, int span, int max_len) {
   const size_t blocks = q8_blocks_of(max_len);
-  return blocks <= kHeld ? 0 : (size_t)batch * heads_kv * lists_of(n_q, span) * blocks * sizeof(uint32_t);
+  return blocks <= kHeld && (long long)group * std::min(span, n_q) <= kFewRows ? 0 : (size_t)batch * heads_kv * lists_of(n_q, span) * blocks * sizeof(uint32_t);
 }
 
 bool q8_select_fits(const Q8SelectArgs &a) {
@@ -330,7 +343,11 @@ int launch_q8_select(const Q8SelectArgs &args, void *workspace, int num_sms, voi
   Q8SelectArgs a = args;
   const int blocks = q8_blocks_of(a.q.max_len);
   const long long lists = (long long)a.q.batch * a.q.heads_kv * a.lists, rows = (long long)a.q.group * std::min(a.span, a.q.n_q);
-  if (blocks > kHeld) a.keys = (uint32_t *)workspace, a.keys_ld = blocks;
+  if (blocks > kHeld || rows > kFewRows) a.keys = (uint32_t *)workspace, a.keys_ld = blocks;
+  if (rows > kFewRows) {
+    const int s = launch_q8_scores(a, num_sms, stream);
+    return s != TQ_OK ? s : launch<0>(a, 1, 0, (cudaStream_t)stream);
+  }
   int ranks = 1;
   while (ranks < 8 && lists * ranks * 2 <= num_sms && blocks >= 128 * ranks) ranks *= 2;
   const size_t smem = (size_t)std::min(blocks, kHeld) * sizeof(uint32_t);
