@@ -17,7 +17,7 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kTileBlocks = 128, kTileRows = 256, kK = 2 * kD;
 constexpr int kGroupBytes = kK / 8 * 128;                  // 8 rows of an operand: 32 columns of 8 numbers, 16 bytes each, a row after the other
 constexpr int kABytes = kTileBlocks / 8 * kGroupBytes;     // 64 KB
@@ -27,7 +27,7 @@ struct Shared {
   uint64_t bar;
   uint32_t amax[kWarps];
   int lo[kWarps], hi[kWarps], good[kWarps];
-  float half[kTileBlocks];  // the second half of the columns' maxima
+  float part[3][kTileBlocks];  // the maxima of all quarters of the columns but the first
   uint32_t tmem;
 };
 
@@ -41,24 +41,42 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uin
       : "memory");
 }
 
-// Four signed bytes as fp16 numbers: 1024 + (b + 128) has b + 128 as its lowest bits.
-__device__ __forceinline__ uint2 bytes_h4(uint32_t w) {
-  w ^= 0x80808080u;
-  uint32_t p = __byte_perm(w, 0x64646464u, 0x4140), q = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 base = __half2half2(__ushort_as_half(0x6480));  // 1152
-  const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&p), base), y = __hsub2(*reinterpret_cast<__half2 *>(&q), base);
-  return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-}
+// Eight numbers of a row as they lie.
+template <typename T>
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+  }
+  // the largest magnitude's bits, as of a float32 (16-bit magnitudes have the order of their bits)
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t t = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) t = max(t, max(max(w[k].x & 0x7fffffffu, w[k].y & 0x7fffffffu), max(w[k].z & 0x7fffffffu, w[k].w & 0x7fffffffu)));
+      return t;
+    } else {
+      const uint32_t t = __vmaxu2(__vmaxu2(w[0].x & 0x7fff7fffu, w[0].y & 0x7fff7fffu), __vmaxu2(w[0].z & 0x7fff7fffu, w[0].w & 0x7fff7fffu));
+      const uint32_t h = max(t >> 16, t & 0xffffu);
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return h << 16;
+      else return h >= 0x7c00u ? 0x7f800000u : __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+    }
+  }
+  // numbers 2 k and 2 k + 1
+  __device__ __forceinline__ float2 pair(int k) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint4 v = w[k >> 1];
+      return (k & 1) ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    } else {
+      const uint32_t v = k == 0 ? w[0].x : k == 1 ? w[0].y : k == 2 ? w[0].z : w[0].w;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+      else return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+  }
+};
 
-// Eight coordinates from c on of row r of the list that begins with token tok0.
-__device__ __forceinline__ void row_eight(const Q8AttnArgs &a, int b, int h, int tok0, int r, int c, float (&x)[8]) {
-  const int i = tok0 + r / a.group, hq = h * a.group + r % a.group;
-  const long long off = b * a.qs.b + hq * a.qs.h + i * a.qs.t + c;
-  if (a.q_dtype == TQ_F32) load_vec<float, 8>(static_cast<const float *>(a.q) + off, x);
-  else if (a.q_dtype == TQ_BF16) load_vec<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q) + off, x);
-  else load_vec<__half, 8>(static_cast<const __half *>(a.q) + off, x);
-}
-
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_constant__ Q8SelectArgs a, int tiles, long long total) {
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
@@ -75,11 +93,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = sm.tmem, u_d = warp_uniform(tmem);
   pdl_wait();
   const long long g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
   const bool issue = elect_lane();
-  const uint32_t u_a = smem_u32(abuf), u_b = smem_u32(bbuf);
+  const uint32_t u_a = warp_uniform(smem_u32(abuf)), u_b = warp_uniform(smem_u32(bbuf));
   const int r8 = lane & 7, c8 = lane >> 3;  // a warp's part of an operand's conversion: 8 rows, four columns of 16 bytes
   uint32_t phase = 0;
   bool bad = false;
@@ -105,31 +123,52 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
     __syncthreads();
     const int first = hi > 0 ? lo / kQ8Block : 0, n = (hi + kQ8Block - 1) / kQ8Block - first;
     if (n <= a.keep || t1 * kTileBlocks <= first || t0 * kTileBlocks >= first + n) continue;  // all are taken, or none of these is seen
+    const int ta = max(t0, first / kTileBlocks), tb = min(t1, (first + n + kTileBlocks - 1) / kTileBlocks);
+    // a warp's 8 blocks of a tile: their bounds on the way
+    uint4 v[4];
+    auto fetch = [&](int t) {
+      const int j = t * kTileBlocks + 8 * warp + r8;
+      const long long at = j >= first && j < first + n ? q8_block(a.q.c.btab, a.q.c.pool_blocks, bh * a.q.c.nblk + j, a.q.error) : -1;
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at, 0ll) * kK);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? __ldg(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
+    };
+    fetch(ta);
     // ---- the largest coordinate of the rows that count, and the first of these rows
     const int rows = (tok1 - tok0) * G;
+    constexpr int kTurns = kTileRows / (8 * kWarps);  // a warp has 8 rows of every 128, four lanes a row
+    Eight<T> x[kTurns][4];
+    bool live[kTurns];
     uint32_t amax = 0;
     int good = 0x7fffffff;
-    auto counts = [&](int r, uint32_t top) {  // top: the row's largest
-      const int2 rg = row_range(a.q, b, tok0 + r / G, len, m);
-      return top < 0x7f800000u && rg.y > rg.x;
+    auto load_row = [&](int r, Eight<T> (&y)[4]) {
+      const int i = tok0 + r / G, hq = h * G + r % G;
+      const T *src = static_cast<const T *>(a.q.q) + b * a.q.qs.b + hq * a.q.qs.h + i * a.q.qs.t + 8 * c8;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c].load(src + 32 * c);
     };
-    auto row_largest = [&](int r) {  // of a row that is there; four lanes of a warp share it
-      uint32_t top = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[8];
-        row_eight(a.q, b, h, tok0, r, 8 * (c8 + 4 * c), x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
-      }
+    auto largest = [&](const Eight<T> (&y)[4]) {
+      uint32_t top = max(max(y[0].top(), y[1].top()), max(y[2].top(), y[3].top()));
       top = max(top, __shfl_xor_sync(kFull, top, 8));
       return max(top, __shfl_xor_sync(kFull, top, 16));
     };
-    for (int r0 = 8 * warp; r0 < rows; r0 += 8 * kWarps) {
-      const int r = min(r0 + r8, rows - 1);
-      const uint32_t top = row_largest(r);
-      if (counts(r, top)) amax = max(amax, top), good = min(good, r);
-    }
+    // rows r0 .. r0 + 255 on their way to x; whether they count
+    auto load = [&](int r0) {
+#pragma unroll
+      for (int u = 0; u < kTurns; ++u)
+        if (r0 + 128 * u + 8 * warp < rows) load_row(min(r0 + 128 * u + 8 * warp + r8, rows - 1), x[u]);
+#pragma unroll
+      for (int u = 0; u < kTurns; ++u) {
+        live[u] = false;
+        const int r = r0 + 128 * u + 8 * warp + r8;
+        if (r0 + 128 * u + 8 * warp >= rows) continue;
+        const uint32_t top = largest(x[u]);
+        const int2 rg = row_range(a.q, b, tok0 + min(r, rows - 1) / G, len, m);
+        live[u] = r < rows && top < 0x7f800000u && rg.y > rg.x;
+        if (live[u]) amax = max(amax, top), good = min(good, r);
+      }
+    };
+    for (int r0 = (rows - 1) / kTileRows * kTileRows; r0 >= 0; r0 -= kTileRows) load(r0);  // (x holds the first rows in the end)
     amax = __reduce_max_sync(kFull, amax), good = __reduce_min_sync(kFull, good);
     if (lane == 0) sm.amax[warp] = amax, sm.good[warp] = good;
     __syncthreads();
@@ -138,47 +177,47 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
     const float lift = amax < 0x0d800000u ? pow2i(100) : 1.f;  // as in q8_choose_kernel
     const float by = pow2i(-row_exponent(__float_as_uint(__uint_as_float(amax) * lift), 6));
     const bool none = good == 0x7fffffff;
+    const __half2 zero = __half2half2(__ushort_as_half(0)), most = __half2half2(__ushort_as_half(0x57f0));  // 127
     uint32_t *const keys = a.keys + list * a.keys_ld;
     for (int r0 = 0; r0 < rows && !bad; r0 += kTileRows) {
       // ---- the rows' operand; it is read by no product any more
-      const int cols = min(kTileRows, (rows - r0 + 63) & ~63);
-      for (int q = 8 * warp; q < cols; q += 8 * kWarps) {
-        int r = min(r0 + q + r8, rows - 1);
-        const uint32_t top = row_largest(r);
-        if (!counts(r, top)) r = none ? r : good;
+      if (r0) load(r0);
+      const int cols = rows - r0 <= 128 ? 128 : 256;
+#pragma unroll
+      for (int u = 0; u < kTurns; ++u) {
+        const int q = 128 * u + 8 * warp;
+        if (q >= cols) continue;
+        if (!none && !__all_sync(kFull, live[u])) {  // rows that do not count are copies of one that does
+          if (!live[u]) load_row(good, x[u]);
+        }
         uint8_t *row = bbuf + (q >> 3) * kGroupBytes + r8 * 16;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x[8];
-          row_eight(a.q, b, h, tok0, r, 8 * (c8 + 4 * c), x);
           uint32_t p[4], w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float x0 = none ? 0.f : fminf(fmaxf(rintf(x[2 * k] * lift * by), -127.f), 127.f);
-            const float x1 = none ? 0.f : fminf(fmaxf(rintf(x[2 * k + 1] * lift * by), -127.f), 127.f);
-            const __half2 up = __floats2half2_rn(fmaxf(x0, 0.f), fmaxf(x1, 0.f)), down = __floats2half2_rn(fminf(x0, 0.f), fminf(x1, 0.f));
+            // to nearest even: 1.5 2^23 has steps of 1
+            float2 f = x[u][c].pair(k);
+            f.x = fmaf(f.x * lift, by, 12582912.f) - 12582912.f, f.y = fmaf(f.y * lift, by, 12582912.f) - 12582912.f;
+            __half2 y = __floats2half2_rn(f.x, f.y);
+            if (none) y = zero;
+            const __half2 up = __hmin2(__hmax2(y, zero), most), down = __hmax2(__hmin2(y, zero), __hneg2(most));
             p[k] = *reinterpret_cast<const uint32_t *>(&up), w[k] = *reinterpret_cast<const uint32_t *>(&down);
           }
           *reinterpret_cast<uint4 *>(row + (c8 + 4 * c) * 128) = make_uint4(p[0], p[1], p[2], p[3]);
           *reinterpret_cast<uint4 *>(row + (c8 + 4 * c + 16) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      for (int t = max(t0, first / kTileBlocks); t < min(t1, (first + n + kTileBlocks - 1) / kTileBlocks); ++t) {
+      for (int t = ta; t < tb; ++t) {
         // ---- the blocks' operand: hi, then lo
-        for (int q = 8 * warp; q < kTileBlocks; q += 8 * kWarps) {
-          const int j = t * kTileBlocks + q + r8;
-          const long long at = j >= first && j < first + n ? q8_block(a.q.c.btab, a.q.c.pool_blocks, bh * a.q.c.nblk + j, a.q.error) : -1;
-          const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at, 0ll) * kK);
-          uint8_t *row = abuf + (q >> 3) * kGroupBytes + r8 * 16;
-          uint4 v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? __ldg(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
+        {
+          uint8_t *row = abuf + warp * kGroupBytes + r8 * 16;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int col = (2 * (c8 + 4 * c) + 16) & 31;  // of 8 numbers; the second half of the bounds comes first
-            const uint2 x = bytes_h4(v[c].x), y = bytes_h4(v[c].y), z = bytes_h4(v[c].z), w = bytes_h4(v[c].w);
-            *reinterpret_cast<uint4 *>(row + col * 128) = make_uint4(x.x, x.y, y.x, y.y);
-            *reinterpret_cast<uint4 *>(row + (col + 1) * 128) = make_uint4(z.x, z.y, w.x, w.y);
+            const uint2 y0 = bytes_h4(v[c].x), y1 = bytes_h4(v[c].y), y2 = bytes_h4(v[c].z), y3 = bytes_h4(v[c].w);
+            *reinterpret_cast<uint4 *>(row + col * 128) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+            *reinterpret_cast<uint4 *>(row + (col + 1) * 128) = make_uint4(y2.x, y2.y, y3.x, y3.y);
           }
         }
         fence_proxy_async_shared();
@@ -186,41 +225,42 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
         __syncthreads();
         if (warp == 0) {
           tc_fence_after_sync();
-          const uint32_t idesc = tc_idesc_f16_f32(kTileBlocks, cols);
-#pragma unroll
+          const uint32_t idesc = warp_uniform(tc_idesc_f16_f32(kTileBlocks, cols));
+#pragma unroll 1  // (descriptors of more than one are as many registers)
           for (int k = 0; k < kK / 16; ++k)
-            if (issue) tc_mma_f16(tmem, tc_sdesc_kmajor(u_a + 256 * k, 128, kGroupBytes), tc_sdesc_kmajor(u_b + 256 * k, 128, kGroupBytes), idesc, k > 0);
+            if (issue) tc_mma_f16(u_d, tc_sdesc_kmajor(u_a + 256 * k, 128, kGroupBytes), tc_sdesc_kmajor(u_b + 256 * k, 128, kGroupBytes), idesc, k > 0);
           if (issue) tc_commit(smem_u32(&sm.bar));
           __syncwarp();
         }
+        if (t + 1 < tb) fetch(t + 1);
+        else if (r0 + kTileRows < rows) fetch(ta);
         bad = !mbar_wait_bounded(&sm.bar, phase & 1, a.q.error);
         ++phase;
         bad = __syncthreads_or(bad);
         if (bad) break;
         tc_fence_after_sync();
-        // ---- a lane's maximum: half of its columns a warp
-        const int half = warp >> 2, row = 32 * (warp & 3) + lane, part = cols / 2;
+        // ---- a lane's maximum: a quarter of its columns a warp
+        const int part = warp >> 2, row = 32 * (warp & 3) + lane, each = cols / 4;
         float best = -INFINITY;
-        for (int c = 0; c < part; c += 32) {
-          uint32_t v[32];
-          tmem_ld_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * part + c, v);
+        for (int c = 0; c < each; c += 32) {
+          uint32_t w[32];
+          tmem_ld_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + part * each + c, w);
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) best = fmaxf(best, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+          for (int k = 0; k < 32; k += 2) best = fmaxf(best, fmaxf(__uint_as_float(w[k]), __uint_as_float(w[k + 1])));
         }
-        if (half) sm.half[row] = best;
+        if (part) sm.part[part - 1][row] = best;
         tc_fence_before_sync();
         __syncthreads();
         tc_fence_after_sync();
         const int j = t * kTileBlocks + row;
-        if (!half && j >= first && j < first + n) {
-          best = fmaxf(best, sm.half[row]);
+        if (!part && j >= first && j < first + n) {
+          best = fmaxf(fmaxf(best, sm.part[0][row]), fmaxf(sm.part[1][row], sm.part[2][row]));
           const bool last = r0 + kTileRows >= rows;
           if (r0) best = fmaxf(best, __uint_as_float(keys[j]));
           uint32_t key = __float_as_uint(best);
           if (last) {
             const long long at = q8_block(a.q.c.btab, a.q.c.pool_blocks, bh * a.q.c.nblk + j, a.q.error);
-            const bool sure = j < first + a.sink || j >= first + n - a.recent;
-            key = sure ? kAlways : at < 0 ? 0u : score_key(best * (__ldg(a.q.c.ks + at) * 1.9073486e-6f));
+            key = at < 0 ? 0u : score_key(best * (__ldg(a.q.c.ks + at) * 1.9073486e-6f));
           }
           keys[j] = key;
         }
@@ -241,10 +281,13 @@ int launch_q8_scores(const Q8SelectArgs &a, int num_sms, void *stream) {
   constexpr int smem = kABytes + kBBytes;
   const int tiles = (q8_blocks_of(a.q.max_len) + kTileBlocks - 1) / kTileBlocks;
   const long long total = (long long)a.q.batch * a.q.heads_kv * a.lists * tiles;
-  if (cudaFuncSetAttribute(q8_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
-  return launch_overlapped(true, q8_scores_kernel, dim3((unsigned)std::min((long long)num_sms, total)), dim3(kThreads), smem, (cudaStream_t)stream,
-                           a, tiles, total) == cudaSuccess
-             ? TQ_OK : TQ_ERR_CUDA;
+  auto run = [&](auto kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+    return launch_overlapped(true, kernel, dim3((unsigned)std::min((long long)num_sms, total)), dim3(kThreads), smem, (cudaStream_t)stream, a, tiles,
+                             total) == cudaSuccess
+               ? TQ_OK : TQ_ERR_CUDA;
+  };
+  return a.q.q_dtype == TQ_F32 ? run(q8_scores_kernel<float>) : a.q.q_dtype == TQ_BF16 ? run(q8_scores_kernel<__nv_bfloat16>) : run(q8_scores_kernel<__half>);
 }
 
 }  // namespace tq
