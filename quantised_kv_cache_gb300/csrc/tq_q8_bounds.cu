@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(32 * kWarps) q8_bounds_kernel(const __grid_con
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);  // (sequence, head, block of the new tokens)
   const int bh = (int)(unit / reach), b = bh / a.heads;
+  pdl_trigger();
   pdl_wait();
   if (b >= a.batch) return;
   const int len = __ldg(a.seq_lens + b), m = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;

@@ -101,6 +101,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     tmem_alloc(smem_u32(&sm.tmem), kWg * kCols);
     tmem_relinquish();
   }
+  if constexpr (KIND != kWhole) pdl_trigger();  // the join waits for all of this grid, but its blocks may come as this one's leave
   pdl_wait();
 
   // ---- the entries' tiles: one thread each
@@ -494,6 +495,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
 template <int KIND>
 __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8AttnArgs a, int unit_rows, const Cut *cuts) {
   __shared__ float so[4][kD], sl[4], slr[4], stop[4];
+  if constexpr (KIND != kWhole) pdl_trigger();
   pdl_wait();
   const Cut cut = cuts[blockIdx.x];
   const int r = blockIdx.y, G = a.group;

@@ -71,6 +71,7 @@ struct Plan {
 template <int KIND>
 __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__ Q8AttnArgs a, Plan p) {
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if constexpr (KIND != kWhole) pdl_trigger();  // each of the call's launches waits for all of the one before
   pdl_wait();
   if (e >= p.entries) return;
   const int b = e / p.pairs, G = a.group;
@@ -103,10 +104,12 @@ constexpr int kStart = 3;
 
 // Prefix sums of the entries' tiles and the slices, one CTA. Slices are equal in tiles and starts, and none is empty (an
 // interval of kStart + 1 holds a tile); with fewer than two tiles a CTA, in tiles alone, so that as many CTAs as possible work.
+template <int KIND>
 __global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p, int heads, int ctas) {
   __shared__ int warp_tiles[32], warp_starts[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0, base_starts = 0;
+  if constexpr (KIND != kWhole) pdl_trigger();
   pdl_wait();
   if (tid == 0) p.pre[0] = 0, p.starts[0] = 0;
   for (int e0 = 0; e0 < p.entries; e0 += 1024) {
@@ -302,6 +305,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem;
+  if constexpr (KIND != kWhole) pdl_trigger();
   pdl_wait();
 
   // the row tile that a warp belongs to (0 for the copies of both), its slice, and the ring's stage and its phase for the slice's tile `it`
@@ -781,6 +785,7 @@ constexpr int kJoin = 2;  // (2048 of 8192 tokens: 303 us with 1, 299.5 with 2 o
 template <bool APART, int KIND>
 __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   constexpr int kUnit = unit_rows(APART);
+  if constexpr (KIND != kWhole) pdl_trigger();
   pdl_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts < 2) return;
@@ -822,7 +827,7 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA, APART, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
   cudaError_t e = launch_overlapped(true, q8_entries_kernel<KIND>, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel, dim3(1), dim3(1024), 0, st, p, a.heads_kv, slices);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel<KIND>, dim3(1), dim3(1024), 0, st, p, a.heads_kv, slices);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA, APART, KIND>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
   if (e == cudaSuccess)
     e = launch_overlapped(true, q8_prompt_join_kernel<APART, KIND>, dim3(slices, unit_rows(APART) / 32), dim3(1024 / kJoin), 0, st, a, p);

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) q8_choose_scored_kernel(const __grid
   const long long list = blockIdx.x, bh = list / a.lists;
   const int l = (int)(list - bh * a.lists), b = (int)(bh / a.q.heads_kv);
   for (int i = tid; i < 4 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  pdl_trigger();
   pdl_wait();
   int len, m, lo, hi;
   seq_sizes(a.q, b, &len, &m, false);
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   if (ranks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // the first CTA has begun: its shared memory may be written
   for (int i = tid; i < 4 * kBins; i += kThreads) sm.hist[0][i] = 0;
   if (tid == 0) sm.rows = 0;
+  pdl_trigger();
   pdl_wait();
   // ---- the first rows and the lengths on their way at once: a warp has rows `warp` and, of 16, `warp` + 8
   constexpr int NR = 8 * NT;

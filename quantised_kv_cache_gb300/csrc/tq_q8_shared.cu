@@ -5,7 +5,7 @@
 // group of them), so that its keys and values are read once for the batch and make operands of up to 256 rows. Their parts go to the workspace,
 // where the kernels of the own tokens fetch them as they finish a row: no pass of its own joins them.
 
-#include "tq_q8_few.cuh"
+#include "tq_q8_solo.cuh"
 
 namespace tq {
 
@@ -17,7 +17,7 @@ size_t q8_shared_workspace(int num_sms, int batch, int heads_q, int heads_kv, in
   const int group = heads_q / heads_kv;
   // (the prefix's rows are one sequence's; their units are no more than the sequences')
   const size_t many = (long long)group * n_q * batch <= kFewRows ? 0 : q8_prompt_workspace(num_sms, batch, group, n_q);
-  return prior_bytes(batch, heads_q, n_q) + std::max(few_bytes(num_sms), many);
+  return prior_bytes(batch, heads_q, n_q) + std::max({few_bytes(num_sms), solo_bytes(num_sms), many});
 }
 
 static Q8AttnArgs of_prefix(const Q8AttnArgs &own, const Q8Cache &prefix) {
@@ -38,6 +38,9 @@ template <int KIND>
 static int launch_part(const Q8AttnArgs &a, char *w, int num_sms, void *stream, int (*many)(const Q8AttnArgs &, void *, int, void *)) {
   const long long rows = (long long)a.group * a.n_q, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
   if (!takes_few(rows, a.out_dtype)) return many(a, w, num_sms, stream);
+  if constexpr (KIND == kOwn)
+    if (solo_wins(a, 1, num_sms))
+      return launch_solo<KIND>(a, (int)rows, 1, (a.max_len + kTile - 1) / kTile, w, num_sms, (cudaStream_t)stream);
   return launch_few<KIND>(a, (int)std::min(rows, 1024ll), (rows + unit - 1) / unit, (a.max_len + kTile - 1) / kTile, w, num_sms,
                           (cudaStream_t)stream);
 }
