@@ -25,7 +25,7 @@ SOURCES = ["tq_host.cpp", "tq_append.cu", "tq_decode.cu", "tq_dequant.cu", "tq_k
            "tq_append_tc.cu", "tq_append_small.cu", "tq_append_bulk.cu", "tq_selftest.cu", "tq_q8_host.cpp",
            "tq_rotary.cu", "tq_q8_append.cu", "tq_q8_attend.cu", "tq_q8_prompt.cu", "tq_q8_weights.cu",
            "tq_q8_evict.cu", "tq_q8_bounds.cu", "tq_q8_select.cu", "tq_q8_scores.cu", "tq_q8_listed.cu",
-           "tq_q8_listed_many.cu", "tq_q8_shared.cu", "tq_q8_prefix_many.cu", "tq_q8_own_many.cu"]
+           "tq_q8_listed_many.cu", "tq_q8_shared.cu", "tq_q8_prefix_many.cu", "tq_q8_own_many.cu", "tq_q8_both_many.cu"]
 HEADERS = ["tq_internal.h", "tq_device.cuh", "tq_ptx.cuh", "tq_tcgen05.cuh", "tq_q8.h", "tq_q8_host.h", "tq_q8.cuh",
            "tq_q8_attend.cuh", "tq_q8_rows.cuh", "tq_q8_few.cuh", "tq_q8_many.cuh", "tq_q8_select.cuh", "tq_q8_solo.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -80,8 +80,8 @@ struct Q8BoundsArgs {
 int launch_q8_bounds(const Q8BoundsArgs &a, void *stream);
 
 // Which keys the rows of an attention kernel meet: a cache's; those of listed blocks; a prefix's, the rows of all sequences being one sequence's;
-// a sequence's own behind a prefix, whose part is joined to theirs.
-enum Q8Kind { kWhole = 0, kListed = 1, kPrefix = 2, kOwn = 3 };
+// a sequence's own behind a prefix, whose part is joined to theirs; a prefix's, then the sequence's own.
+enum Q8Kind { kWhole = 0, kListed = 1, kPrefix = 2, kOwn = 3, kBoth = 4 };
 
 // Attention: the struct of the ABI with its defaults filled in, and the workspace carved up.
 struct Q8AttnArgs {
@@ -105,6 +105,8 @@ struct Q8AttnArgs {
   // kListed: [batch][heads_kv][lists][n_blocks], a list for every `span` query tokens
   const int32_t *blocks = nullptr;
   int n_blocks = 0, span = 0, lists = 0;
+  // kBoth (where c is the sequences' own cache): the prefix's
+  Q8Cache pc{};
   // kPrefix (where batch is 1, n_q counts all sequences' tokens, c and max_len are the prefix's) and kOwn
   const int32_t *prefix_lens = nullptr;
   int max_prefix = 0, fold = 0, own_max = 0;  // fold: a sequence's query tokens; own_max: bounds seq_lens
@@ -149,6 +151,8 @@ bool q8_shared_fits(const Q8AttnArgs &own, int num_sms);
 int launch_q8_shared(const Q8AttnArgs &own, const Q8Cache &prefix, void *workspace, int num_sms, void *stream);
 bool q8_prefix_many_fits(const Q8AttnArgs &a, int num_sms);
 int launch_q8_prefix_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
+bool q8_both_many_fits(const Q8AttnArgs &a, int num_sms);
+int launch_q8_both_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 bool q8_own_many_fits(const Q8AttnArgs &a, int num_sms);
 int launch_q8_own_many(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream);
 int launch_q8_attention(const Q8AttnArgs &a, void *workspace, size_t ws_bytes, int num_sms, void *stream);

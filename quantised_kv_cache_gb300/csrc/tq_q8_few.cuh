@@ -107,7 +107,27 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   // ---- the entries' tiles: one thread each
   const int E = nb * rts;
   int count = 0;
-  if (tid < E) {
+  if (KIND != kWhole && E <= kThreads / 32) {  // a warp each: a lane looks at a token (16 rows of a prefix's are as many sequences')
+    int most = 0;
+    if (warp < E) {
+      int len, m, r0, end, list;
+      unit_span<KIND>(a, rt0 + warp % rts, kUnitRows, &r0, &end, &list);
+      seq_sizes<KIND>(a, b0 + warp / rts, &len, &m, blockIdx.x == 0 && lane == 0);
+      const int i0 = r0 / G, i1 = (min(end, r0 + kUnitRows) - 1) / G;
+      int lo = 0x7fffffff, hi = 0;
+      if (i0 + lane <= i1) {
+        const int2 r = row_range<KIND>(a, b0 + warp / rts, i0 + lane, len, m);
+        if (r.y > r.x) lo = r.x, hi = r.y;
+      }
+      lo = __reduce_min_sync(kFull, lo), hi = __reduce_max_sync(kFull, hi);
+      if (hi == 0) lo = 0;
+      most = i0 < m ? max(1, unit_tiles<KIND>(a, b0 + warp / rts, lo, hi)) : 0;
+      if (lane == 0) sm.ent.lo[warp] = lo, sm.ent.hi[warp] = hi, sm.ent.pre[warp] = most;
+    }
+    __syncthreads();
+    if (tid < E) count = sm.ent.pre[tid];
+    __syncthreads();
+  } else if (tid < E) {
     const int b = b0 + tid / rts;
     int len, m, r0, end, list;
     unit_span<KIND>(a, rt0 + tid % rts, kUnitRows, &r0, &end, &list);
@@ -120,7 +140,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     }
     if (hi == 0) lo = 0;
     // an entry whose rows see nothing keeps one (empty) tile, so that its zeros are written
-    count = i0 < m ? max(1, unit_tiles<KIND>(a, lo, hi)) : 0;
+    count = i0 < m ? max(1, unit_tiles<KIND>(a, b, lo, hi)) : 0;
     sm.ent.lo[tid] = lo;
     sm.ent.hi[tid] = hi;
   }

@@ -67,13 +67,9 @@ struct Plan {
   int entries, pairs, unit;  // pairs: units of a sequence (and head); unit: their rows
 };
 
-// One warp per entry (sequence, unit of rows).
+// An entry (sequence, unit of rows): a warp.
 template <int KIND>
-__global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__ Q8AttnArgs a, Plan p) {
-  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if constexpr (KIND != kWhole) pdl_trigger();  // each of the call's launches waits for all of the one before
-  pdl_wait();
-  if (e >= p.entries) return;
+__device__ __forceinline__ void make_entry(const Q8AttnArgs &a, const Plan &p, int e, int lane) {
   const int b = e / p.pairs, G = a.group;
   int len, m, r0, end, list;
   unit_span<KIND>(a, e % p.pairs, p.unit, &r0, &end, &list);
@@ -94,8 +90,16 @@ __global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__
     if (hi == 0) lo = 0;
     p.entry[e] = Entry{lo, hi, maxbeg, minend};
     // rows that see nothing keep one tile, so that their zeros are written
-    p.pre[e + 1] = i0 < m ? max(1, unit_tiles<KIND>(a, lo, hi)) : 0;
+    p.pre[e + 1] = i0 < m ? max(1, unit_tiles<KIND>(a, b, lo, hi)) : 0;
   }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(256) q8_entries_kernel(const __grid_constant__ Q8AttnArgs a, Plan p) {
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if constexpr (KIND != kWhole) pdl_trigger();  // each of the call's launches waits for all of the one before
+  pdl_wait();
+  if (e < p.entries) make_entry<KIND>(a, p, e, threadIdx.x & 31);
 }
 
 // What a unit's start (its queries, the first tile's chain alone) costs, in tiles: ragged documents of 1 to 11 tiles a unit take 127 us in
@@ -104,13 +108,22 @@ constexpr int kStart = 3;
 
 // Prefix sums of the entries' tiles and the slices, one CTA. Slices are equal in tiles and starts, and none is empty (an
 // interval of kStart + 1 holds a tile); with fewer than two tiles a CTA, in tiles alone, so that as many CTAs as possible work.
+// Up to kPlanned entries are made here as well.
+constexpr int kPlanned = 128;
+constexpr int kJoinTiles = 4;  // what the join costs, in tiles
 template <int KIND>
-__global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p, int heads, int ctas) {
+__global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__ Q8AttnArgs a, Plan p, int ctas) {
+  const int heads = a.heads_kv;
   __shared__ int warp_tiles[32], warp_starts[32];
+  __shared__ unsigned long long largest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0, base_starts = 0;
   if constexpr (KIND != kWhole) pdl_trigger();
   pdl_wait();
+  if (KIND != kWhole && p.entries <= kPlanned) {
+    for (int e = warp; e < p.entries; e += 32) make_entry<KIND>(a, p, e, lane);
+    __syncthreads();
+  }
   if (tid == 0) p.pre[0] = 0, p.starts[0] = 0;
   for (int e0 = 0; e0 < p.entries; e0 += 1024) {
     const int e = e0 + tid;
@@ -135,19 +148,46 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(Plan p, int heads, int 
   const int start = tiles >= 2LL * ctas ? kStart : 0;
   const long long total = tiles + (long long)start * base_starts * heads;
   const long long slices = min((long long)ctas, total / (start + 1));
+  // where slice k begins: its weight, and the unit there (its weight, its first tile's number)
+  auto begin = [&](int k, long long *unit, int *each, long long *tile) {
+    const long long c = total * k / slices;
+    int lo = 0, hi = p.entries - 1;
+    while (lo < hi) {  // the last entry that begins at or before c
+      const int mid = (lo + hi + 1) >> 1;
+      if (((long long)p.pre[mid] + (long long)start * p.starts[mid]) * heads <= c) lo = mid;
+      else hi = mid - 1;
+    }
+    const int cnt = p.pre[lo + 1] - p.pre[lo];
+    *each = cnt + start;
+    const long long from = ((long long)p.pre[lo] + (long long)start * p.starts[lo]) * heads, h = (c - from) / *each;
+    *unit = from + h * *each, *tile = (long long)p.pre[lo] * heads + h * cnt;
+    return c;
+  };
+  // Slices of whole units, each slice's begin moved to the nearer end of the unit that it lies in, save the cut units' further starts
+  // and the join: taken where the largest costs no more than an even slice with these (16 tiles a unit, 256 units: 130 us cut, 119 whole).
+  bool whole = false;
+  if (KIND != kWhole && slices > 0) {
+    auto rounded = [&](int k) {
+      if (k >= slices) return total;
+      long long unit, tile;
+      int each;
+      const long long c = begin(k, &unit, &each, &tile);
+      return 2 * (c - unit) >= each ? unit + each : unit;
+    };
+    if (tid == 0) largest = 0;
+    __syncthreads();
+    for (int k = tid; k < slices; k += 1024) atomicMax(&largest, (unsigned long long)(rounded(k + 1) - rounded(k)));
+    __syncthreads();
+    whole = (long long)largest <= total / slices + kStart + kJoinTiles;
+  }
   for (int k = tid; k <= ctas; k += 1024) {
     long long g = tiles;
     if (k < slices) {
-      const long long c = total * k / slices;
-      int lo = 0, hi = p.entries - 1;
-      while (lo < hi) {  // the last entry that begins at or before c
-        const int mid = (lo + hi + 1) >> 1;
-        if (((long long)p.pre[mid] + (long long)start * p.starts[mid]) * heads <= c) lo = mid;
-        else hi = mid - 1;
-      }
-      const int cnt = p.pre[lo + 1] - p.pre[lo], each = cnt + start;
-      const long long in = c - ((long long)p.pre[lo] + (long long)start * p.starts[lo]) * heads;
-      g = (long long)p.pre[lo] * heads + in / each * cnt + max(0, (int)(in % each) - start);
+      long long unit, tile;
+      int each;
+      const long long c = begin(k, &unit, &each, &tile);
+      g = tile + max(0, (int)(c - unit) - start);
+      if (whole) g = 2 * (c - unit) >= each ? tile + each - start : tile;
     }
     p.cut[k] = g;
   }
@@ -157,7 +197,7 @@ struct Shared {
   uint64_t full[4], empty[4];
   uint64_t bar_q[2], bar_s[2], bar_p[2], bar_o[2];  // of a row tile: queries, scores, probabilities, value sums are there
   float4 info[4];             // of a stage: key scales of the tile's two blocks, value scales (negative: not there)
-  int2 at[4];                 // (kListed) their first slots
+  int2 at[4];                 // (BLOCKS) their first slots
   float top[2][2][128];       // [row tile][half]: row maxima, then sums
   uint32_t tmem;
   int bad;
@@ -282,6 +322,7 @@ template <int TERMS, int EXTRA, bool APART, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Plan p) {
   constexpr int kStages = stages_of(TERMS, APART), kUnit = unit_rows(APART);
+  constexpr bool BLOCKS = KIND == kListed || KIND == kBoth;  // a tile's blocks do not follow each other
   constexpr bool kTurns = !EXTRA && !APART;  // capped or biased scores run without turns (2048 of 8192 tokens, when they took 653 us: 713 with them)
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
@@ -334,6 +375,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         const long long bh = (long long)u.b * a.heads_kv + u.h, blocks = bh * a.c.nblk;
         int r0, rend, list;
         unit_span<KIND>(a, u.pair, kUnit, &r0, &rend, &list);
+        const int prefix = KIND == kBoth ? prefix_of(a, u.b) : 0;
+        const BothTiles both = both_tiles(prefix, en.lo, en.hi);
         for (int k0 = 0; g + k0 < u.end; k0 += 32) {
           const int todo = (int)min(32ll, u.end - g - k0);
           long long src[2] = {-1, -1};
@@ -351,6 +394,23 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               bytes[k] = (m + 31) / 32 * 32 * kD;
               (k ? f.y : f.x) = __ldg(a.c.ks + src[k]);
               (k ? f.w : f.z) = __ldg(a.c.vs + src[k]);
+            }
+          } else if (KIND == kBoth && lane < todo) {  // (src: addresses)
+            const int j = u.t0 + k0 + lane;
+            const bool pre = j < both.prefix;
+            const Q8Cache &c = pre ? a.pc : a.c;
+            const int tok = (pre ? both.first + j : both.own + j - both.prefix) * kTile, base = pre ? 0 : prefix, end = pre ? min(prefix, en.hi) : en.hi;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              at[k] = base + tok + k * kQ8Block;
+              const int m = min(kQ8Block, end - at[k]);
+              if (m <= 0 || at[k] + kQ8Block <= en.lo) continue;  // no row sees a token of it
+              const long long blk = q8_block(c.btab, c.pool_blocks, (pre ? (long long)u.h : bh) * c.nblk + tok / kQ8Block + k, a.error);
+              if (blk < 0) continue;
+              src[k] = (long long)(c.records + blk * kQ8BlockBytes);
+              bytes[k] = (m + 31) / 32 * 32 * kD;
+              (k ? f.y : f.x) = __ldg(c.ks + blk);
+              (k ? f.w : f.z) = __ldg(c.vs + blk);
             }
           } else if (lane < todo) {
             const int tok = (en.lo / kTile + u.t0 + k0 + lane) * kTile, n = min(kTile, max(0, en.hi - tok));
@@ -373,21 +433,21 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
             x.x = __shfl_sync(kFull, f.x, k), x.y = __shfl_sync(kFull, f.y, k);
             x.z = __shfl_sync(kFull, f.z, k), x.w = __shfl_sync(kFull, f.w, k);
             int2 slots = make_int2(0, 0);
-            if constexpr (KIND == kListed) slots.x = __shfl_sync(kFull, at[0], k), slots.y = __shfl_sync(kFull, at[1], k);
+            if constexpr (BLOCKS) slots.x = __shfl_sync(kFull, at[0], k), slots.y = __shfl_sync(kFull, at[1], k);
             if (lane == 0) {
               wait(&sm.empty[s], turn(it) ^ 1);
               if (!*(volatile int *)&sm.bad) {
                 sm.info[s] = x;
-                if constexpr (KIND == kListed) sm.at[s] = slots;
+                if constexpr (BLOCKS) sm.at[s] = slots;
                 uint8_t *dst = ring + s * kStage;
                 mbar_arrive_expect_tx(&sm.full[s], 2 * (n0 + n1));
                 if (n0) {
-                  const uint8_t *q = a.c.records + s0 * kQ8BlockBytes;
+                  const uint8_t *q = KIND == kBoth ? (const uint8_t *)s0 : a.c.records + s0 * kQ8BlockBytes;
                   tma_load_1d(dst, q, n0, &sm.full[s]);
                   tma_load_1d(dst + kTile * kD, q + kQ8Plane, n0, &sm.full[s]);
                 }
                 if (n1) {
-                  const uint8_t *q = a.c.records + s1 * kQ8BlockBytes;
+                  const uint8_t *q = KIND == kBoth ? (const uint8_t *)s1 : a.c.records + s1 * kQ8BlockBytes;
                   tma_load_1d(dst + kQ8Plane, q, n1, &sm.full[s]);
                   tma_load_1d(dst + kTile * kD + kQ8Plane, q + kQ8Plane, n1, &sm.full[s]);
                 }
@@ -413,6 +473,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         for (long long g = g0; g < g1; ++units) {
           const Unit u = unit_at(p, a.heads_kv, g, g1);
           const int first = p.entry[u.e].lo / kTile + u.t0, hi = p.entry[u.e].hi, todo = (int)(u.end - g);
+          const int prefix = KIND == kBoth ? prefix_of(a, u.b) : 0;
           wait(&sm.bar_q[rt], units & 1);
           for (int j = 0; j <= todo; ++j) {
             // the value sums of tile j - 1, then the scores of tile j over its probabilities: in this order, as issued
@@ -421,7 +482,11 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               const float4 f = sm.info[s];
               // the tokens up to the end of either block's (of those that are there)
               int n0 = min(kTile, max(0, hi - (first + j - 1) * kTile)), n1 = n0;
-              if constexpr (KIND == kListed) n0 = min(kQ8Block, hi - sm.at[s].x), n1 = kQ8Block + min(kQ8Block, hi - sm.at[s].y);
+              if constexpr (BLOCKS) {
+                const int2 at = sm.at[s];
+                n0 = min(kQ8Block, (at.x < prefix ? min(prefix, hi) : hi) - at.x);
+                n1 = kQ8Block + min(kQ8Block, (at.y < prefix ? min(prefix, hi) : hi) - at.y);
+              }
               const bool apart = scales_apart(f), whole = n0 >= kQ8Block && n1 == kTile && f.z >= 0.f && f.w >= 0.f && !apart;
               const uint32_t vt = warp_uniform(smem_u32(ring + s * kStage) + kTile * kD);
               for (int part = 0; part <= (int)apart; ++part) {  // the two blocks at once, or one after the other
@@ -493,6 +558,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       int len, m;
       seq_sizes<KIND>(a, u.b, &len, &m, false);
       const int G = a.group;
+      const int prefix = KIND == kBoth ? prefix_of(a, u.b) : 0;
       int unit0, unit1, list;
       unit_span<KIND>(a, u.pair, kUnit, &unit0, &unit1, &list);
 
@@ -535,20 +601,22 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       const int todo = (int)(u.end - g);
       for (int j = 0; j < todo; ++j) {
         const int s = stage(it + j);
-        int tok0 = (first + j) * kTile, n = min(kTile, max(0, hi - tok0));  // (kListed: of this half's block, below)
+        int tok0 = (first + j) * kTile, n = min(kTile, max(0, hi - tok0));  // (BLOCKS: of this half's block, below)
         wait(&sm.full[s], turn(it + j));
         const float4 f = sm.info[s];
         const float ks = half ? f.y : f.x;
         bool masked = !(maxbeg <= tok0 && minend >= tok0 + kTile) || f.x < 0.f || f.y < 0.f;
-        if constexpr (KIND == kListed) {
-          tok0 = half ? sm.at[s].y - kQ8Block : sm.at[s].x;
-          n = 64 * half + (ks < 0.f ? 0 : min(kQ8Block, hi - tok0 - 64 * half));
-          masked = ks < 0.f || !(maxbeg <= tok0 + 64 * half && minend >= tok0 + 64 * half + kQ8Block);
+        if constexpr (BLOCKS) {
+          const int at = half ? sm.at[s].y : sm.at[s].x;  // of a prefix's block: its last tokens may not be the sequence's
+          const int there = ks < 0.f ? 0 : min(kQ8Block, (at < prefix ? min(prefix, hi) : hi) - at);
+          tok0 = at - 64 * half, n = 64 * half + there;
+          masked = there < kQ8Block || !(maxbeg <= at && minend >= at + kQ8Block);
         }
         int from = 0, to = 64;  // the tokens of this half that the row sees
         if (masked) {
           from = min(max(rg.x - tok0 - 64 * half, 0), 64), to = min(max(rg.y - tok0 - 64 * half, 0), 64);
           if (ks < 0.f) to = 0;
+          if constexpr (KIND == kBoth) to = min(to, n - 64 * half);
         }
         // never 0, so that an unseen score of -inf stays -inf (products so small make no difference)
         const float c = EXTRA ? qs * fmaxf(ks, 0.f) * sc.in : fmaxf(qs * fmaxf(ks, 0.f) * (a.scale * kLog2e), 1e-30f);
@@ -690,7 +758,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
         else probabilities(std::false_type{});
         // value rows past the copied tokens, up to a whole K-step, hold what the cache holds there
         if (n & 31) {
-          const int t = n + (KIND == kListed ? tid & 127 : tid & 255);
+          const int t = n + (BLOCKS ? tid & 127 : tid & 255);
           if (t < ((n + 31) & ~31)) {
             uint8_t *vt = ring + s * kStage + kTile * kD;
 #pragma unroll
@@ -826,8 +894,9 @@ int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   const int slices = APART ? 2 * num_sms : num_sms;
   if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA, APART, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TQ_ERR_CUDA;
-  cudaError_t e = launch_overlapped(true, q8_entries_kernel<KIND>, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
-  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel<KIND>, dim3(1), dim3(1024), 0, st, p, a.heads_kv, slices);
+  cudaError_t e = cudaSuccess;
+  if (KIND == kWhole || p.entries > kPlanned) e = launch_overlapped(true, q8_entries_kernel<KIND>, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
+  if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel<KIND>, dim3(1), dim3(1024), 0, st, a, p, slices);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prompt_kernel<TERMS, EXTRA, APART, KIND>, dim3(num_sms), dim3(kThreads), smem, st, a, p);
   if (e == cudaSuccess)
     e = launch_overlapped(true, q8_prompt_join_kernel<APART, KIND>, dim3(slices, unit_rows(APART) / 32), dim3(1024 / kJoin), 0, st, a, p);
@@ -845,7 +914,7 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 // many slices are joined and each has half of the ring. So where a CTA has a dozen tiles. 64 rows, 8 KV heads, bf16 (fp16): 8 sequences of
 // 16384 tokens (54 tiles a CTA) 121 us apart, 165 us (170, 198) not, capped 178 and 284; 2 of them (13) 59 and 63 (73, 73); one (7) 49 and 45.
 bool units_apart(const Q8AttnArgs &a, int num_sms) {
-  const long long tiles = (long long)a.batch * a.heads_kv * ((a.max_len + kTile - 1) / kTile);
+  const long long tiles = (long long)a.batch * a.heads_kv * ((a.max_len + (a.pc.records ? (long long)a.max_prefix : 0) + kTile - 1) / kTile);
   return (long long)a.group * a.n_q <= unit_rows(true) && tiles >= 12LL * num_sms;
 }
 long long units_of(const Q8AttnArgs &a, bool apart) {
@@ -854,7 +923,7 @@ long long units_of(const Q8AttnArgs &a, bool apart) {
 }
 // Entries' tiles are counted in 32 bits.
 bool many_fits(const Q8AttnArgs &a, int num_sms) {
-  const long long entries = units_of(a, units_apart(a, num_sms)) * a.batch, tiles = (a.max_len + kTile - 1) / kTile;
+  const long long entries = units_of(a, units_apart(a, num_sms)) * a.batch, tiles = (a.max_len + kTile - 1) / kTile + (a.pc.records ? (a.max_prefix + kTile - 1) / kTile : 0);
   return entries <= 1 << 24 && entries * tiles <= 0x7fffffff;
 }
 

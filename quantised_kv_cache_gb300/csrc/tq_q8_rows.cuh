@@ -51,11 +51,12 @@ __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, 
   } else {
     int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
     if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
-    if constexpr (KIND == kOwn) {
+    *len = min(max(n, 0), a.max_len);
+    if constexpr (KIND == kOwn || KIND == kBoth) {
       const int prefix = __ldg(a.prefix_lens + b);
       if (report && (prefix < 0 || prefix > a.max_prefix)) set_error(a.error, TQ_ERR_ARG);
+      if constexpr (KIND == kBoth) *len += min(max(prefix, 0), a.max_prefix);
     }
-    *len = min(max(n, 0), a.max_len);
     *m = min(max(q, 0), a.n_q);
   }
 }
@@ -87,11 +88,27 @@ __device__ __forceinline__ void unit_span(const Q8AttnArgs &a, int x, int unit, 
     *end = (int)min((long long)*end, ((long long)*list + 1) * rows);
   }
 }
+// kBoth: the prefix's length of sequence b, and a unit's tiles of 128 of its slots, the first one that its rows see (those of slots from lo to
+// hi - 1), then of the sequence's own.
+__device__ __forceinline__ int prefix_of(const Q8AttnArgs &a, int b) { return min(max(__ldg(a.prefix_lens + b), 0), a.max_prefix); }
+struct BothTiles {
+  int prefix, first, own;  // tiles of the prefix; the first of them; the first of the own ones
+  int total;
+};
+__device__ __forceinline__ BothTiles both_tiles(int prefix, int lo, int hi) {
+  BothTiles t;
+  t.first = lo / 128, t.own = max(lo - prefix, 0) / 128;
+  t.prefix = max(0, (min(hi, prefix) + 127) / 128 - t.first);
+  if (lo >= prefix) t.prefix = 0;
+  t.total = t.prefix + (hi > prefix ? (hi - prefix + 127) / 128 - t.own : 0);
+  return t;
+}
 // Tiles of 128 slots that a unit goes through whose rows see slots from lo to hi - 1 (kListed: of two list entries each; a block of
 // number j is among the first j + 1 of its list).
 template <int KIND>
-__device__ __forceinline__ int unit_tiles(const Q8AttnArgs &a, int lo, int hi) {
+__device__ __forceinline__ int unit_tiles(const Q8AttnArgs &a, int b, int lo, int hi) {
   if constexpr (KIND == kListed) return (min(a.n_blocks, (hi + kQ8Block - 1) / kQ8Block) + 1) / 2;
+  if constexpr (KIND == kBoth) return both_tiles(prefix_of(a, b), lo, hi).total;
   return (hi + 127) / 128 - lo / 128;
 }
 // The block of entry k of list `list` of (sequence, head) bh, -1 for none that counts.

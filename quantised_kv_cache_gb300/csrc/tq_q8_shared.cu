@@ -20,6 +20,19 @@ size_t q8_shared_workspace(int num_sms, int batch, int heads_q, int heads_kv, in
   return prior_bytes(batch, heads_q, n_q) + std::max({few_bytes(num_sms), solo_bytes(num_sms), many});
 }
 
+// Sequences whose rows fill units of their own (up to a quarter of them empty) take one pass over the prefix and their own tokens: each reads
+// the prefix for itself, but nothing passes through memory. 4 sequences of 512 tokens x 4 heads behind 8192 tokens: 341 us, 399 in two passes.
+static bool takes_both(long long rows, int out_dtype) {
+  const long long padded = rows <= 128 ? 128 : (rows + 255) / 256 * 256;
+  return !takes_few(rows, out_dtype) && 4 * padded <= 5 * rows;
+}
+
+static Q8AttnArgs of_both(const Q8AttnArgs &own, const Q8Cache &prefix) {
+  Q8AttnArgs a = own;
+  a.pc = prefix;
+  return a;
+}
+
 static Q8AttnArgs of_prefix(const Q8AttnArgs &own, const Q8Cache &prefix) {
   Q8AttnArgs a = own;
   a.c = prefix, a.batch = 1, a.n_q = own.batch * own.n_q, a.max_len = own.max_prefix, a.fold = own.n_q, a.own_max = own.max_len;
@@ -29,6 +42,7 @@ static Q8AttnArgs of_prefix(const Q8AttnArgs &own, const Q8Cache &prefix) {
 bool q8_shared_fits(const Q8AttnArgs &own, int num_sms) {
   if ((long long)own.group * own.n_q * own.batch > 0x7fffffff - 1023) return false;         // rows of the prefix's KV head
   if ((long long)own.max_prefix + own.max_len > kQ8MostSlots) return false;                 // slots of a sequence
+  if (takes_both((long long)own.group * own.n_q, own.out_dtype)) return q8_both_many_fits(of_both(own, own.c), num_sms);
   const Q8AttnArgs pre = of_prefix(own, own.c);
   return (takes_few((long long)pre.group * pre.n_q, own.out_dtype) || q8_prefix_many_fits(pre, num_sms)) &&
          (takes_few((long long)own.group * own.n_q, own.out_dtype) || q8_own_many_fits(own, num_sms));
@@ -47,6 +61,7 @@ static int launch_part(const Q8AttnArgs &a, char *w, int num_sms, void *stream, 
 
 int launch_q8_shared(const Q8AttnArgs &args, const Q8Cache &prefix, void *workspace, int num_sms, void *stream) {
   Q8AttnArgs own = args;
+  if (takes_both((long long)own.group * own.n_q, own.out_dtype)) return launch_q8_both_many(of_both(own, prefix), workspace, num_sms, stream);
   own.prior = (float *)workspace;
   char *w = (char *)workspace + prior_bytes(own.batch, own.heads_q, own.n_q);
   const int s = launch_part<kPrefix>(of_prefix(own, prefix), w, num_sms, stream, launch_q8_prefix_many);

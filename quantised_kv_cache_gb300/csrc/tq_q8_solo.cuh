@@ -16,6 +16,9 @@ namespace {
 constexpr int kSoloThreads = kConsumers + 32 * kWg;
 constexpr int kPlaces = 3, kPlace = kTile * kD;
 constexpr int kSoloRows = 4;  // rows of a partial record
+// What a unit's start and end cost, in tiles. 0, 1, 2 and 3 of them: 64 sequences over up to 47 blocks 53, 47, 46 and 46 us, 32 over 16 blocks each
+// 24, 22, 23 and 23, 64 sequences' own tokens (1 to 2048) behind a short prefix 73, 68, 66 and 64.
+constexpr int kSoloStart = 2;
 
 struct SoloShared {
   uint64_t full[kWg][kPlaces], empty[kWg][kPlaces], bar_s[kWg], bar_o[kWg];
@@ -27,8 +30,9 @@ struct SoloShared {
   float4 wmax[kWg][kSoloRows];          // row maxima of a warpgroup's four warps
   float4 lw[kWg][kSoloRows], lrw[kWg][kSoloRows];  // row sums of the warps
   uint32_t tmem;
-  int bad, scan[kSoloThreads / 32];
+  int bad, scan[kSoloThreads / 32], scan_starts[kSoloThreads / 32];
   Entries ent;
+  int starts[kEntries + 1];  // entries with tiles before each
 };
 
 template <int NR, int KIND>
@@ -72,35 +76,49 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
       if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
     }
     if (hi == 0) lo = 0;
-    count = i0 < m ? max(1, unit_tiles<KIND>(a, lo, hi)) : 0;
+    count = i0 < m ? max(1, unit_tiles<KIND>(a, b, lo, hi)) : 0;
     sm.ent.lo[tid] = lo;
     sm.ent.hi[tid] = hi;
   }
   {
     int x = count;
+    const uint32_t some = __ballot_sync(kFull, count > 0);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) sm.scan[warp] = x;
+    if (lane == 31) sm.scan[warp] = x, sm.scan_starts[warp] = __popc(some);
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += sm.scan[w];
-    if (tid < E) sm.ent.pre[tid + 1] = before + x;
-    if (tid == 0) sm.ent.pre[0] = 0;
+    int before = 0, starts = __popc(some & (0xffffffffu >> (31 - lane)));
+    for (int w = 0; w < warp; ++w) before += sm.scan[w], starts += sm.scan_starts[w];
+    if (tid < E) sm.ent.pre[tid + 1] = before + x, sm.starts[tid + 1] = starts;
+    if (tid == 0) sm.ent.pre[0] = 0, sm.starts[0] = 0;
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  const long long total = (long long)sm.ent.pre[E] * a.heads_kv;
   const int wg = warp < kConsumers / 32 ? warp >> 2 : warp - kConsumers / 32;
-  // slices, none of them empty: slice c < slices has tiles [total c / slices, total (c + 1) / slices)
+  // Slices are equal in tiles and starts, and none is empty (an interval of kSoloStart + 1 holds a tile).
+  auto weight = [&](int e) { return ((long long)sm.ent.pre[e] + (long long)kSoloStart * sm.starts[e]) * a.heads_kv; };
+  const long long total = weight(E);
   const int slice = blockIdx.x * kWg + wg;
-  const long long slices = min((long long)gridDim.x * kWg, total);
+  const long long slices = min((long long)gridDim.x * kWg, total / (kSoloStart + 1));
   const bool idle = slice >= slices;
-  const long long g0 = idle ? 0 : total * slice / slices, g1 = idle ? 0 : total * (slice + 1) / slices;
+  auto tile_at = [&](long long c) {  // the first tile of a slice that begins at weight c
+    if (c >= total) return (long long)sm.ent.pre[E] * a.heads_kv;
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // the last entry that begins at or before c
+      const int mid = (lo + hi + 1) >> 1;
+      if (weight(mid) <= c) lo = mid;
+      else hi = mid - 1;
+    }
+    const int cnt = sm.ent.pre[lo + 1] - sm.ent.pre[lo], each = cnt + kSoloStart;
+    const long long in = c - weight(lo), h = in / each;
+    return (long long)sm.ent.pre[lo] * a.heads_kv + h * cnt + max(0, (int)(in - h * each) - kSoloStart);
+  };
+  const long long g0 = idle ? 0 : tile_at(total * slice / slices), g1 = idle ? 0 : tile_at(total * (slice + 1) / slices);
   auto locate = [&](long long g, int &e, int &h, int &t, int &cnt) {
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // the last entry that begins at or before g
@@ -257,10 +275,7 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
             if (issue)
               tc_mma_f8(u_s, tc_sdesc_kmajor(u_k + 256 * ks, 128, 1024), tc_sdesc_kmajor(u_q + 256 * ks, 128, 1024),
                         tc_idesc_f8(128, kN, 0, 1, 0, 0), ks > 0);
-          if (issue) {
-            tc_commit(smem_u32(&sm.bar_s[wg]));
-            tc_commit(smem_u32(&sm.empty[wg][pk]));
-          }
+          if (issue) tc_commit(smem_u32(&sm.bar_s[wg]));
           __syncwarp();
         }
         const float4 info = sm.info[wg][it & 3];
@@ -299,6 +314,9 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + 128 * c) = make_uint4(0, 0, 0, 0);
         }
         bar_wg(wg);
+        // The keys are used, and every warp has seen them arrive: a commit behind the products could give the place away, and let the barrier
+        // complete a second time, before a warp that is late has looked at the first.
+        if (wt == 0) mbar_arrive(&sm.empty[wg][pk]);
         // ---- probabilities (times 2^15), their terms, the sums
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -392,9 +410,9 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
         // the slice's last unit: if it goes on beyond it and began in it, the join starts here
         const long long stop = g - t0 + cnt;
         int parts = 0;
-        if (t0 == 0 && stop > g1) {
-          parts = 1;
-          for (long long c = slice + 1; c < slices && total * c / slices < stop; ++c) ++parts;
+        if (t0 == 0 && stop > g1) {  // slices that begin before the unit's end, from this one on
+          const long long last = weight(e) + (long long)(h + 1) * (cnt + kSoloStart);
+          parts = (int)((last * slices + total - 1) / total) - slice;
         }
         cuts[slice] = Cut{b, rt0 + e % rts, h, parts};
       }
@@ -457,6 +475,7 @@ bool solo_wins(const Q8AttnArgs &a, int lists, int num_sms) {
 size_t solo_bytes(int num_sms) {
   return round16((size_t)num_sms * kWg * sizeof(Cut)) + (size_t)num_sms * kWg * 2 * kSoloRows * kPartRow * sizeof(float);
 }
+
 
 template <int NR, int KIND>
 int launch_solo_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
