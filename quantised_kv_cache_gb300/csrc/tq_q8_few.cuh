@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, int rts, Cut *cuts) {
   constexpr int kUnitRows = rows_of(T), kN = stacked_rows(NR, T), kOp = kN * 128;  // an operand's rows and bytes
   constexpr int kCols = 2 * kN;  // a warpgroup's columns: S, in its place O of the first block, then O of the second
-  static_assert(NR <= kUnitRows && kWg * kCols <= 512 && (kWg - 1) * NR * 512 <= kWg * kOp, "");
+  static_assert(NR <= kUnitRows && kWg * kCols <= 512 && kWg * NR * 512 <= kWg * kOp, "");
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
   uint8_t *ring = dyn, *qbuf = dyn + kStages * kStage, *pbuf = qbuf + kOp;
@@ -448,56 +448,49 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         sm.l[wg][wt] = sm.lw[wg][0][wt] + sm.lw[wg][1][wt] + sm.lw[wg][2][wt] + sm.lw[wg][3][wt];
         sm.lr[wg][wt] = sm.lrw[wg][0][wt] + sm.lrw[wg][1][wt] + sm.lrw[wg][2][wt] + sm.lrw[wg][3][wt];
       }
-      float *mix = reinterpret_cast<float *>(pbuf);  // [kWg - 1][NR][128]; every MMA that read the terms is done
+      float *mix = reinterpret_cast<float *>(pbuf);  // [kWg][NR][128]; every MMA that read the terms is done
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
         const float f = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - top);
-        o[r] *= f;
-        if (wg) mix[((wg - 1) * NR + r) * 128 + wt] = o[r];
+        mix[(wg * NR + r) * 128 + wt] = o[r] * f;
       }
       bar_all();
-      if (wg == 0) {
-        const bool whole = t0 == 0 && end == g + cnt;
-        float *part = a.parts + ((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRows * kPartRow;
+      const bool whole = t0 == 0 && end == g + cnt;
+      float *part = a.parts + ((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRows * kPartRow;
+      int len, mm;
+      seq_sizes<KIND>(a, b, &len, &mm, false);
+#pragma unroll 1
+      for (int r = wg; r < NR; r += kWg) {  // a warpgroup finishes every fourth row
+        const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+        float x = mix[r * 128 + wt], sl = 0.f, slr = 0.f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
-          float x = o[r], sl = 0.f, slr = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWg; ++w) {
-            const float mw = sm.m[w][r], f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
-            // a warpgroup without a maximum adds 0, or the NaN of a row whose query is not finite
-            sl = fmaf(sm.l[w][r], mw == -INFINITY && sm.l[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), sl);
-            slr = fmaf(sm.lr[w][r], mw == -INFINITY && sm.lr[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), slr);
-            if (w) x += mix[((w - 1) * NR + r) * 128 + wt];
-          }
-          const int row = row0 + r, i = row / G;
-          int len, mm;
-          seq_sizes<KIND>(a, b, &len, &mm, false);
-          if (row >= row_end || i >= mm) continue;
-          if (whole) {
-            const int hq = h * G + row % G;
-            finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f);
-          } else {
-            part[r * kPartRow + wt] = x;
-            if (wt == 0) {
-              part[r * kPartRow + kD] = top;
-              part[r * kPartRow + kD + 1] = sl;
-              part[r * kPartRow + kD + 2] = slr;
-            }
+        for (int w = 0; w < kWg; ++w) {
+          const float mw = sm.m[w][r], f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
+          // a warpgroup without a maximum adds 0, or the NaN of a row whose query is not finite
+          sl = fmaf(sm.l[w][r], mw == -INFINITY && sm.l[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), sl);
+          slr = fmaf(sm.lr[w][r], mw == -INFINITY && sm.lr[w][r] == 0.f ? 0.f : (mw == -INFINITY ? 1.f : f), slr);
+          if (w) x += mix[(w * NR + r) * 128 + wt];
+        }
+        const int row = row0 + r, i = row / G;
+        if (row >= row_end || i >= mm) continue;
+        if (whole) {
+          const int hq = h * G + row % G;
+          finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f);
+        } else {
+          part[r * kPartRow + wt] = x;
+          if (wt == 0) {
+            part[r * kPartRow + kD] = top;
+            part[r * kPartRow + kD + 1] = sl;
+            part[r * kPartRow + kD + 2] = slr;
           }
         }
-        if (wt == 0 && end == g1) {
-          // the CTA's last unit: if it goes on beyond this slice and began in it, the join starts here
-          const long long stop = g - t0 + cnt;
-          int parts = 0;
-          if (t0 == 0 && stop > g1) {
-            parts = 1;
-            for (long long c = blockIdx.x + 1; c < slices && total * c / slices < stop; ++c) ++parts;
-          }
-          cuts[blockIdx.x] = Cut{b, rt0 + e % rts, h, parts};
-        }
+      }
+      if (tid == 0 && end == g1) {
+        // the CTA's last unit: if it goes on beyond this slice and began in it, the join starts here
+        const long long stop = g - t0 + cnt;  // slices c with total c / slices < stop hold parts of it
+        const int parts = t0 == 0 && stop > g1 ? (int)((stop * slices + total - 1) / total) - (int)blockIdx.x : 0;
+        cuts[blockIdx.x] = Cut{b, rt0 + e % rts, h, parts};
       }
       g = end;
     }

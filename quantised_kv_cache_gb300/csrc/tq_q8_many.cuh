@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
   const int heads = a.heads_kv;
   __shared__ int warp_tiles[32], warp_starts[32];
   __shared__ unsigned long long largest;
+  __shared__ int pre_near[kPlanned + 1], starts_near[kPlanned + 1];  // of few entries
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0, base_starts = 0;
   if constexpr (KIND != kWhole) pdl_trigger();
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
     for (int e = warp; e < p.entries; e += 32) make_entry<KIND>(a, p, e, lane);
     __syncthreads();
   }
-  if (tid == 0) p.pre[0] = 0, p.starts[0] = 0;
+  if (tid == 0) p.pre[0] = 0, p.starts[0] = 0, pre_near[0] = 0, starts_near[0] = 0;
   for (int e0 = 0; e0 < p.entries; e0 += 1024) {
     const int e = e0 + tid;
     int x = e < p.entries ? p.pre[e + 1] : 0, y = x > 0 ? 1 : 0;
@@ -141,11 +142,16 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
       all += warp_tiles[w], sall += warp_starts[w];
     }
     if (e < p.entries) p.pre[e + 1] = before + x, p.starts[e + 1] = sbefore + y;
+    if (KIND != kWhole && e < p.entries && p.entries <= kPlanned) pre_near[e + 1] = before + x, starts_near[e + 1] = sbefore + y;
     base = all, base_starts = sall;
     __syncthreads();
   }
   const long long tiles = (long long)base * heads;
-  const int start = tiles >= 2LL * ctas ? kStart : 0;
+  // Few units of many slices each: every slice begins with a start of its own then (8 units of 256 tiles: DEC us with it counted, ODE without).
+  const bool few = KIND != kWhole && 4LL * base_starts * heads <= ctas;
+  const int start = tiles >= 2LL * ctas && !few ? kStart : 0;
+  const bool near = KIND != kWhole && p.entries <= kPlanned;
+  const int *const pre = near ? pre_near : p.pre, *const starts = near ? starts_near : p.starts;
   const long long total = tiles + (long long)start * base_starts * heads;
   const long long slices = min((long long)ctas, total / (start + 1));
   // where slice k begins: its weight, and the unit there (its weight, its first tile's number)
@@ -154,13 +160,13 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
     int lo = 0, hi = p.entries - 1;
     while (lo < hi) {  // the last entry that begins at or before c
       const int mid = (lo + hi + 1) >> 1;
-      if (((long long)p.pre[mid] + (long long)start * p.starts[mid]) * heads <= c) lo = mid;
+      if (((long long)pre[mid] + (long long)start * starts[mid]) * heads <= c) lo = mid;
       else hi = mid - 1;
     }
-    const int cnt = p.pre[lo + 1] - p.pre[lo];
+    const int cnt = pre[lo + 1] - pre[lo];
     *each = cnt + start;
-    const long long from = ((long long)p.pre[lo] + (long long)start * p.starts[lo]) * heads, h = (c - from) / *each;
-    *unit = from + h * *each, *tile = (long long)p.pre[lo] * heads + h * cnt;
+    const long long from = ((long long)pre[lo] + (long long)start * starts[lo]) * heads, h = (c - from) / *each;
+    *unit = from + h * *each, *tile = (long long)pre[lo] * heads + h * cnt;
     return c;
   };
   // Slices of whole units, each slice's begin moved to the nearer end of the unit that it lies in, save the cut units' further starts
@@ -867,12 +873,12 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   if (row >= unit1 || i >= m) return;
   auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * part_of(kUnit); };
   float top = -INFINITY;
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < cut.parts; ++k) top = fmaxf(top, rec(k)[kUnit * kD + r]);
   float o[kJoin][4], l = 0.f;
 #pragma unroll
   for (int j = 0; j < kJoin; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < cut.parts; ++k) {
     const float *x = rec(k);
     const float mk = x[kUnit * kD + r], f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
