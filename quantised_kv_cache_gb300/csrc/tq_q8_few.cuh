@@ -153,8 +153,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     }
     if (lane == 31) sm.scan[warp] = x;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += sm.scan[w];
+    const int before = __reduce_add_sync(kFull, lane < warp ? sm.scan[lane] : 0);
     if (tid < E) sm.ent.pre[tid + 1] = before + x;
     if (tid == 0) sm.ent.pre[0] = 0;
   }
@@ -166,7 +165,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   // slices, none of them empty: CTA c < slices has tiles [total c / slices, total (c + 1) / slices)
   const long long slices = min((long long)gridDim.x, total);
   const bool idle = blockIdx.x >= slices;
-  const long long g0 = idle ? 0 : total * blockIdx.x / slices, g1 = idle ? 0 : total * (blockIdx.x + 1) / slices;
+  const long long g0 = idle ? 0 : quotient(total * blockIdx.x, slices), g1 = idle ? 0 : quotient(total * (blockIdx.x + 1), slices);
   auto locate = [&](long long g, int &e, int &h, int &t, int &cnt) {
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // the last entry that begins at or before g
@@ -177,7 +176,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     e = lo;
     cnt = sm.ent.pre[e + 1] - sm.ent.pre[e];
     const long long in = g - (long long)sm.ent.pre[e] * a.heads_kv;
-    h = (int)(in / cnt);
+    h = (int)quotient(in, cnt);
     t = (int)(in - (long long)h * cnt);
   };
   auto wait = [&](uint64_t *bar, uint32_t parity) {

@@ -110,12 +110,14 @@ constexpr int kStart = 3;
 // interval of kStart + 1 holds a tile); with fewer than two tiles a CTA, in tiles alone, so that as many CTAs as possible work.
 // Up to kPlanned entries are made here as well.
 constexpr int kPlanned = 128;
+constexpr int kMostSlices = 1023;
 constexpr int kJoinTiles = 4;  // what the join costs, in tiles
 template <int KIND>
 __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__ Q8AttnArgs a, Plan p, int ctas) {
   const int heads = a.heads_kv;
   __shared__ int warp_tiles[32], warp_starts[32];
   __shared__ unsigned long long largest;
+  __shared__ long long rounded[KIND == kWhole ? 1 : kMostSlices + 1];
   __shared__ int pre_near[kPlanned + 1], starts_near[kPlanned + 1];  // of few entries
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0, base_starts = 0;
@@ -136,11 +138,9 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
     }
     if (lane == 31) warp_tiles[warp] = x, warp_starts[warp] = y;
     __syncthreads();
-    int before = base, all = base, sbefore = base_starts, sall = base_starts;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warp_tiles[w], sbefore += warp_starts[w];
-      all += warp_tiles[w], sall += warp_starts[w];
-    }
+    const int wx = warp_tiles[lane], wy = warp_starts[lane];
+    const int before = base + __reduce_add_sync(kFull, lane < warp ? wx : 0), all = base + __reduce_add_sync(kFull, wx);
+    const int sbefore = base_starts + __reduce_add_sync(kFull, lane < warp ? wy : 0), sall = base_starts + __reduce_add_sync(kFull, wy);
     if (e < p.entries) p.pre[e + 1] = before + x, p.starts[e + 1] = sbefore + y;
     if (KIND != kWhole && e < p.entries && p.entries <= kPlanned) pre_near[e + 1] = before + x, starts_near[e + 1] = sbefore + y;
     base = all, base_starts = sall;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
   const long long slices = min((long long)ctas, total / (start + 1));
   // where slice k begins: its weight, and the unit there (its weight, its first tile's number)
   auto begin = [&](int k, long long *unit, int *each, long long *tile) {
-    const long long c = total * k / slices;
+    const long long c = quotient(total * k, slices);
     int lo = 0, hi = p.entries - 1;
     while (lo < hi) {  // the last entry that begins at or before c
       const int mid = (lo + hi + 1) >> 1;
@@ -165,26 +165,25 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
     }
     const int cnt = pre[lo + 1] - pre[lo];
     *each = cnt + start;
-    const long long from = ((long long)pre[lo] + (long long)start * starts[lo]) * heads, h = (c - from) / *each;
+    const long long from = ((long long)pre[lo] + (long long)start * starts[lo]) * heads, h = quotient(c - from, *each);
     *unit = from + h * *each, *tile = (long long)pre[lo] * heads + h * cnt;
     return c;
   };
   // Slices of whole units, each slice's begin moved to the nearer end of the unit that it lies in, save the cut units' further starts
   // and the join: taken where the largest costs no more than an even slice with these (16 tiles a unit, 256 units: 130 us cut, 119 whole).
   bool whole = false;
-  if (KIND != kWhole && slices > 0) {
-    auto rounded = [&](int k) {
-      if (k >= slices) return total;
-      long long unit, tile;
-      int each;
-      const long long c = begin(k, &unit, &each, &tile);
-      return 2 * (c - unit) >= each ? unit + each : unit;
-    };
+  if (KIND != kWhole && slices > 0 && slices <= kMostSlices && !few) {
+    for (int k = tid; k <= slices; k += 1024) {
+      long long unit = total, tile, c = total;
+      int each = 1;
+      if (k < slices) c = begin(k, &unit, &each, &tile);
+      rounded[k] = 2 * (c - unit) >= each ? unit + each : unit;
+    }
     if (tid == 0) largest = 0;
     __syncthreads();
-    for (int k = tid; k < slices; k += 1024) atomicMax(&largest, (unsigned long long)(rounded(k + 1) - rounded(k)));
+    for (int k = tid; k < slices; k += 1024) atomicMax(&largest, (unsigned long long)(rounded[k + 1] - rounded[k]));
     __syncthreads();
-    whole = (long long)largest <= total / slices + kStart + kJoinTiles;
+    whole = (long long)largest <= quotient(total, slices) + kStart + kJoinTiles;
   }
   for (int k = tid; k <= ctas; k += 1024) {
     long long g = tiles;
@@ -224,7 +223,7 @@ __device__ __forceinline__ Unit unit_at(const Plan &p, int heads, long long g, l
   }
   u.e = lo, u.cnt = p.pre[lo + 1] - p.pre[lo];
   const long long in = g - (long long)p.pre[lo] * heads;
-  u.h = (int)(in / u.cnt), u.t0 = (int)(in - (long long)u.h * u.cnt);
+  u.h = (int)quotient(in, u.cnt), u.t0 = (int)(in - (long long)u.h * u.cnt);
   u.b = lo / p.pairs, u.pair = lo % p.pairs;
   u.end = min(g1, g - u.t0 + u.cnt);
   return u;
@@ -873,21 +872,41 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
   if (row >= unit1 || i >= m) return;
   auto rec = [&](int k) { return p.parts + (((long long)blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * part_of(kUnit); };
   float top = -INFINITY;
-#pragma unroll 16
-  for (int k = 0; k < cut.parts; ++k) top = fmaxf(top, rec(k)[kUnit * kD + r]);
   float o[kJoin][4], l = 0.f;
 #pragma unroll
   for (int j = 0; j < kJoin; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < cut.parts; ++k) {
-    const float *x = rec(k);
-    const float mk = x[kUnit * kD + r], f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
+  auto add = [&](float mk, float lk, const float4 (&y)[kJoin]) {
+    const float f = mk == -INFINITY ? 1.f : ex2_approx(mk - top);  // without a maximum: zeros (or NaN)
 #pragma unroll
-    for (int j = 0; j < kJoin; ++j) {
-      const float4 y = reinterpret_cast<const float4 *>(x)[(col + 32 / kJoin * j) * kUnit + r];
-      o[j][0] = fmaf(y.x, f, o[j][0]), o[j][1] = fmaf(y.y, f, o[j][1]), o[j][2] = fmaf(y.z, f, o[j][2]), o[j][3] = fmaf(y.w, f, o[j][3]);
+    for (int j = 0; j < kJoin; ++j)
+      o[j][0] = fmaf(y[j].x, f, o[j][0]), o[j][1] = fmaf(y[j].y, f, o[j][1]), o[j][2] = fmaf(y[j].z, f, o[j][2]), o[j][3] = fmaf(y[j].w, f, o[j][3]);
+    l = fmaf(lk, f, l);
+  };
+  // kPrefix: a unit's parts are many, so that their loads are asked for together (past the last it is the last's again, which is not
+  // used): 64 sequences behind 32768 tokens 106 us, 109 without; where they are few that costs (2048 of 8192 tokens 291 -> 294 us)
+  constexpr int kTops = KIND == kPrefix ? 16 : 1, kParts = KIND == kPrefix ? 8 : 1;
+#pragma unroll(KIND == kPrefix ? 1 : 16)
+  for (int k0 = 0; k0 < cut.parts; k0 += kTops) {
+    float x[kTops];
+#pragma unroll
+    for (int k = 0; k < kTops; ++k) x[k] = rec(min(k0 + k, cut.parts - 1))[kUnit * kD + r];
+#pragma unroll
+    for (int k = 0; k < kTops; ++k) top = fmaxf(top, x[k]);
+  }
+#pragma unroll(KIND == kPrefix ? 1 : 8)
+  for (int k0 = 0; k0 < cut.parts; k0 += kParts) {
+    float mk[kParts], lk[kParts];
+    float4 y[kParts][kJoin];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float *x = rec(kParts > 1 ? min(k0 + k, cut.parts - 1) : k0);
+      mk[k] = x[kUnit * kD + r], lk[k] = x[kUnit * (kD + 1) + r];
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) y[k][j] = reinterpret_cast<const float4 *>(x)[(col + 32 / kJoin * j) * kUnit + r];
     }
-    l = fmaf(x[kUnit * (kD + 1) + r], f, l);
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (k0 + k < cut.parts) add(mk[k], lk[k], y[k]);
   }
   const int hq = cut.h * G + row % G;
 #pragma unroll

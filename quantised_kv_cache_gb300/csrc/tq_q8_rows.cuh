@@ -77,6 +77,11 @@ __device__ __forceinline__ long long query_offset(const Q8AttnArgs &a, int b, in
   return b * a.qs.b + hq * a.qs.h + i * a.qs.t;
 }
 
+// a / b of numbers that are not negative: in 32 bits where they fit (64-bit divisions take some 100 instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The rows [r0, end) of unit x of a sequence, units of `unit` rows; kListed: of list *list.
 template <int KIND>
 __device__ __forceinline__ void unit_span(const Q8AttnArgs &a, int x, int unit, int *r0, int *end, int *list) {

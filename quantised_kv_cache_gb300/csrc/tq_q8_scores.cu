@@ -101,94 +101,121 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
   const int r8 = lane & 7, c8 = lane >> 3;  // a warp's part of an operand's conversion: 8 rows, four columns of 16 bytes
   uint32_t phase = 0;
   bool bad = false;
-  for (long long g = g0; g < g1 && !bad;) {
-    const long long list = g / tiles, bh = list / a.lists;
-    const int t0 = (int)(g - list * tiles), t1 = (int)min((long long)tiles, g1 - list * tiles);
-    g = list * tiles + t1;
-    const int l = (int)(list - bh * a.lists), b = (int)(bh / a.q.heads_kv), h = (int)(bh - (long long)b * a.q.heads_kv);
-    // ---- the list's blocks
-    int len, m;
-    seq_sizes(a.q, b, &len, &m, h == 0 && l == 0 && t0 == 0 && tid == 0);
-    const int tok0 = l * a.span, tok1 = min(m, (int)min((long long)a.q.n_q, (long long)tok0 + a.span));
-    int lo = 0x7fffffff, hi = 0;
-    for (int i = tok0 + tid; i < tok1; i += kThreads) {
-      const int2 r = row_range(a.q, b, i, len, m);
-      if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
+  // A list's part of the slice: its blocks first .. first + n - 1 and its rows, of the tiles ta .. tb - 1. Lists that take all of their
+  // blocks, or see none of the slice's, are passed over. All threads.
+  struct Part {
+    long long list, bh;
+    int b, h, len, m, tok0, rows, first, n, ta, tb;
+  };
+  auto next_part = [&](long long &g, Part &p) {
+    while (g < g1) {
+      p.list = quotient(g, tiles), p.bh = quotient(p.list, a.lists);
+      const int t0 = (int)(g - p.list * tiles), t1 = (int)min((long long)tiles, g1 - p.list * tiles);
+      g = p.list * tiles + t1;
+      const int l = (int)(p.list - p.bh * a.lists);
+      p.b = (int)quotient(p.bh, a.q.heads_kv), p.h = (int)(p.bh - (long long)p.b * a.q.heads_kv);
+      seq_sizes(a.q, p.b, &p.len, &p.m, p.h == 0 && l == 0 && t0 == 0 && tid == 0);
+      p.tok0 = l * a.span;
+      const int tok1 = min(p.m, (int)min((long long)a.q.n_q, (long long)p.tok0 + a.span));
+      int lo = 0x7fffffff, hi = 0;
+      for (int i = p.tok0 + tid; i < tok1; i += kThreads) {
+        const int2 r = row_range(a.q, p.b, i, p.len, p.m);
+        if (r.y > r.x) lo = min(lo, r.x), hi = max(hi, r.y);
+      }
+      lo = __reduce_min_sync(kFull, lo), hi = __reduce_max_sync(kFull, hi);
+      if (lane == 0) sm.lo[warp] = lo, sm.hi[warp] = hi;
+      __syncthreads();
+      lo = __reduce_min_sync(kFull, lane < kWarps ? sm.lo[lane] : 0x7fffffff), hi = __reduce_max_sync(kFull, lane < kWarps ? sm.hi[lane] : 0);
+      __syncthreads();
+      p.first = hi > 0 ? lo / kQ8Block : 0, p.n = (hi + kQ8Block - 1) / kQ8Block - p.first;
+      p.rows = max(0, tok1 - p.tok0) * G;
+      p.ta = max(t0, p.first / kTileBlocks), p.tb = min(t1, (p.first + p.n + kTileBlocks - 1) / kTileBlocks);
+      if (p.n > a.keep && p.ta < p.tb) return true;
     }
-    lo = __reduce_min_sync(kFull, lo), hi = __reduce_max_sync(kFull, hi);
-    if (lane == 0) sm.lo[warp] = lo, sm.hi[warp] = hi;
-    __syncthreads();
+    return false;
+  };
+  // a warp has 8 rows of every 128, four lanes a row: as they lie, on their way
+  constexpr int kTurns = kTileRows / (8 * kWarps);
+  Eight<T> x[kTurns][4];
+  auto load_row = [&](const Part &p, int r, Eight<T> (&y)[4]) {
+    const int i = r / G, hq = p.h * G + r - i * G;
+    const T *src = static_cast<const T *>(a.q.q) + p.b * a.q.qs.b + hq * a.q.qs.h + (p.tok0 + i) * a.q.qs.t + 8 * c8;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) lo = min(lo, sm.lo[w]), hi = max(hi, sm.hi[w]);
-    __syncthreads();
-    const int first = hi > 0 ? lo / kQ8Block : 0, n = (hi + kQ8Block - 1) / kQ8Block - first;
-    if (n <= a.keep || t1 * kTileBlocks <= first || t0 * kTileBlocks >= first + n) continue;  // all are taken, or none of these is seen
-    const int ta = max(t0, first / kTileBlocks), tb = min(t1, (first + n + kTileBlocks - 1) / kTileBlocks);
-    // a warp's 8 blocks of a tile: their bounds on the way
-    uint4 v[4];
-    auto fetch = [&](int t) {
-      const int j = t * kTileBlocks + 8 * warp + r8;
-      const long long at = j >= first && j < first + n ? q8_block(a.q.c.btab, a.q.c.pool_blocks, bh * a.q.c.nblk + j, a.q.error) : -1;
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at, 0ll) * kK);
+    for (int c = 0; c < 4; ++c) y[c].load(src + 32 * c);
+  };
+  auto load = [&](const Part &p, int r0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? __ldg(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
+    for (int u = 0; u < kTurns; ++u)
+      if (r0 + 128 * u + 8 * warp < p.rows) load_row(p, min(r0 + 128 * u + 8 * warp + r8, p.rows - 1), x[u]);
+  };
+  // a warp's 8 blocks of a tile: their bounds on their way; and a block's scale, of the thread that writes its score
+  uint4 v[4];
+  float scale = 0.f;
+  auto fetch = [&](const Part &p, int t) {
+    auto block = [&](int j) {
+      return j >= p.first && j < p.first + p.n ? q8_block(a.q.c.btab, a.q.c.pool_blocks, p.bh * a.q.c.nblk + j, a.q.error) : -1;
     };
-    fetch(ta);
+    const long long at = block(t * kTileBlocks + 8 * warp + r8);
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at, 0ll) * kK);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? __ldg(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
+    if (tid < kTileBlocks) {
+      const long long mine = block(t * kTileBlocks + tid);
+      scale = mine >= 0 ? __ldg(a.q.c.ks + mine) : -1.f;
+    }
+  };
+  long long g = g0;
+  Part cur;
+  bool more = next_part(g, cur);
+  if (more) load(cur, 0), fetch(cur, cur.ta);
+  while (more && !bad) {
     // ---- the largest coordinate of the rows that count, and the first of these rows
-    const int rows = (tok1 - tok0) * G;
-    constexpr int kTurns = kTileRows / (8 * kWarps);  // a warp has 8 rows of every 128, four lanes a row
-    Eight<T> x[kTurns][4];
     bool live[kTurns];
     uint32_t amax = 0;
     int good = 0x7fffffff;
-    auto load_row = [&](int r, Eight<T> (&y)[4]) {
-      const int i = tok0 + r / G, hq = h * G + r % G;
-      const T *src = static_cast<const T *>(a.q.q) + b * a.q.qs.b + hq * a.q.qs.h + i * a.q.qs.t + 8 * c8;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c].load(src + 32 * c);
-    };
-    auto largest = [&](const Eight<T> (&y)[4]) {
-      uint32_t top = max(max(y[0].top(), y[1].top()), max(y[2].top(), y[3].top()));
-      top = max(top, __shfl_xor_sync(kFull, top, 8));
-      return max(top, __shfl_xor_sync(kFull, top, 16));
-    };
-    // rows r0 .. r0 + 255 on their way to x; whether they count
-    auto load = [&](int r0) {
-#pragma unroll
-      for (int u = 0; u < kTurns; ++u)
-        if (r0 + 128 * u + 8 * warp < rows) load_row(min(r0 + 128 * u + 8 * warp + r8, rows - 1), x[u]);
+    auto look = [&](int r0) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
         live[u] = false;
         const int r = r0 + 128 * u + 8 * warp + r8;
-        if (r0 + 128 * u + 8 * warp >= rows) continue;
-        const uint32_t top = largest(x[u]);
-        const int2 rg = row_range(a.q, b, tok0 + min(r, rows - 1) / G, len, m);
-        live[u] = r < rows && top < 0x7f800000u && rg.y > rg.x;
+        if (r0 + 128 * u + 8 * warp >= cur.rows) continue;
+        uint32_t top = max(max(x[u][0].top(), x[u][1].top()), max(x[u][2].top(), x[u][3].top()));
+        top = max(top, __shfl_xor_sync(kFull, top, 8));
+        top = max(top, __shfl_xor_sync(kFull, top, 16));
+        const int2 rg = row_range(a.q, cur.b, cur.tok0 + min(r, cur.rows - 1) / G, cur.len, cur.m);
+        live[u] = r < cur.rows && top < 0x7f800000u && rg.y > rg.x;
         if (live[u]) amax = max(amax, top), good = min(good, r);
       }
     };
-    for (int r0 = (rows - 1) / kTileRows * kTileRows; r0 >= 0; r0 -= kTileRows) load(r0);  // (x holds the first rows in the end)
+    look(0);
+    if (cur.rows > kTileRows) {
+#pragma unroll 1
+      for (int r0 = kTileRows; r0 < cur.rows; r0 += kTileRows) load(cur, r0), look(r0);
+      load(cur, 0), look(0);
+    }
     amax = __reduce_max_sync(kFull, amax), good = __reduce_min_sync(kFull, good);
     if (lane == 0) sm.amax[warp] = amax, sm.good[warp] = good;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) amax = max(amax, sm.amax[w]), good = min(good, sm.good[w]);
+    amax = __reduce_max_sync(kFull, lane < kWarps ? sm.amax[lane] : 0u), good = __reduce_min_sync(kFull, lane < kWarps ? sm.good[lane] : 0x7fffffff);
     const float lift = amax < 0x0d800000u ? pow2i(100) : 1.f;  // as in q8_choose_kernel
     const float by = pow2i(-row_exponent(__float_as_uint(__uint_as_float(amax) * lift), 6));
     const bool none = good == 0x7fffffff;
     const __half2 zero = __half2half2(__ushort_as_half(0)), most = __half2half2(__ushort_as_half(0x57f0));  // 127
-    uint32_t *const keys = a.keys + list * a.keys_ld;
-    for (int r0 = 0; r0 < rows && !bad; r0 += kTileRows) {
+    uint32_t *const keys = a.keys + cur.list * a.keys_ld;
+    Part after;
+    bool next = false;
+#pragma unroll 1
+    for (int r0 = 0; r0 < cur.rows && !bad; r0 += kTileRows) {
       // ---- the rows' operand; it is read by no product any more
-      if (r0) load(r0);
-      const int cols = rows - r0 <= 128 ? 128 : 256;
+      if (r0) load(cur, r0), look(r0);
+      const int cols = cur.rows - r0 <= 128 ? 128 : 256;
+      const bool last = r0 + kTileRows >= cur.rows;
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
         const int q = 128 * u + 8 * warp;
         if (q >= cols) continue;
         if (!none && !__all_sync(kFull, live[u])) {  // rows that do not count are copies of one that does
-          if (!live[u]) load_row(good, x[u]);
+          if (!live[u]) load_row(cur, good, x[u]);
         }
         uint8_t *row = bbuf + (q >> 3) * kGroupBytes + r8 * 16;
 #pragma unroll
@@ -208,7 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
           *reinterpret_cast<uint4 *>(row + (c8 + 4 * c + 16) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      for (int t = ta; t < tb; ++t) {
+      if (last) {  // the next list's rows load behind this one's tiles
+        next = next_part(g, after);
+        if (next) load(after, 0);
+      }
+#pragma unroll 1
+      for (int t = cur.ta; t < cur.tb; ++t) {
         // ---- the blocks' operand: hi, then lo
         {
           uint8_t *row = abuf + warp * kGroupBytes + r8 * 16;
@@ -220,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
             *reinterpret_cast<uint4 *>(row + (col + 1) * 128) = make_uint4(y2.x, y2.y, y3.x, y3.y);
           }
         }
+        const float its = scale;
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncthreads();
@@ -232,8 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
           if (issue) tc_commit(smem_u32(&sm.bar));
           __syncwarp();
         }
-        if (t + 1 < tb) fetch(t + 1);
-        else if (r0 + kTileRows < rows) fetch(ta);
+        if (t + 1 < cur.tb) fetch(cur, t + 1);
+        else if (!last) fetch(cur, cur.ta);
+        else if (next) fetch(after, after.ta);
         bad = !mbar_wait_bounded(&sm.bar, phase & 1, a.q.error);
         ++phase;
         bad = __syncthreads_or(bad);
@@ -242,30 +276,26 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
         // ---- a lane's maximum: a quarter of its columns a warp
         const int part = warp >> 2, row = 32 * (warp & 3) + lane, each = cols / 4;
         float best = -INFINITY;
-        for (int c = 0; c < each; c += 32) {
-          uint32_t w[32];
-          tmem_ld_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + part * each + c, w);
+#pragma unroll 1
+        for (int c = 0; c < each; c += 16) {
+          float w[16];
+          tmem_ld_cols<16>(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + part * each + c, w);
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) best = fmaxf(best, fmaxf(__uint_as_float(w[k]), __uint_as_float(w[k + 1])));
+          for (int k = 0; k < 16; k += 2) best = fmaxf(best, fmaxf(w[k], w[k + 1]));
         }
         if (part) sm.part[part - 1][row] = best;
         tc_fence_before_sync();
         __syncthreads();
         tc_fence_after_sync();
         const int j = t * kTileBlocks + row;
-        if (!part && j >= first && j < first + n) {
+        if (!part && j >= cur.first && j < cur.first + cur.n) {  // (row is tid: its scale is this block's)
           best = fmaxf(fmaxf(best, sm.part[0][row]), fmaxf(sm.part[1][row], sm.part[2][row]));
-          const bool last = r0 + kTileRows >= rows;
           if (r0) best = fmaxf(best, __uint_as_float(keys[j]));
-          uint32_t key = __float_as_uint(best);
-          if (last) {
-            const long long at = q8_block(a.q.c.btab, a.q.c.pool_blocks, bh * a.q.c.nblk + j, a.q.error);
-            key = at < 0 ? 0u : score_key(best * (__ldg(a.q.c.ks + at) * 1.9073486e-6f));
-          }
-          keys[j] = key;
+          keys[j] = !last ? __float_as_uint(best) : its < 0.f ? 0u : score_key(best * (its * 1.9073486e-6f));
         }
       }
     }
+    cur = after, more = next;
     __syncthreads();  // sm.amax and the like are written again
   }
   if (bad) settle();

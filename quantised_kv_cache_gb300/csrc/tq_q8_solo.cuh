@@ -90,8 +90,8 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
     }
     if (lane == 31) sm.scan[warp] = x, sm.scan_starts[warp] = __popc(some);
     __syncthreads();
-    int before = 0, starts = __popc(some & (0xffffffffu >> (31 - lane)));
-    for (int w = 0; w < warp; ++w) before += sm.scan[w], starts += sm.scan_starts[w];
+    const int before = __reduce_add_sync(kFull, lane < warp ? sm.scan[lane] : 0);
+    const int starts = __reduce_add_sync(kFull, lane < warp ? sm.scan_starts[lane] : 0) + __popc(some & (0xffffffffu >> (31 - lane)));
     if (tid < E) sm.ent.pre[tid + 1] = before + x, sm.starts[tid + 1] = starts;
     if (tid == 0) sm.ent.pre[0] = 0, sm.starts[0] = 0;
   }
@@ -115,10 +115,10 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
       else hi = mid - 1;
     }
     const int cnt = sm.ent.pre[lo + 1] - sm.ent.pre[lo], each = cnt + kSoloStart;
-    const long long in = c - weight(lo), h = in / each;
+    const long long in = c - weight(lo), h = quotient(in, each);
     return (long long)sm.ent.pre[lo] * a.heads_kv + h * cnt + max(0, (int)(in - h * each) - kSoloStart);
   };
-  const long long g0 = idle ? 0 : tile_at(total * slice / slices), g1 = idle ? 0 : tile_at(total * (slice + 1) / slices);
+  const long long g0 = idle ? 0 : tile_at(quotient(total * slice, slices)), g1 = idle ? 0 : tile_at(quotient(total * (slice + 1), slices));
   auto locate = [&](long long g, int &e, int &h, int &t, int &cnt) {
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // the last entry that begins at or before g
@@ -129,7 +129,7 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
     e = lo;
     cnt = sm.ent.pre[e + 1] - sm.ent.pre[e];
     const long long in = g - (long long)sm.ent.pre[e] * a.heads_kv;
-    h = (int)(in / cnt);
+    h = (int)quotient(in, cnt);
     t = (int)(in - (long long)h * cnt);
   };
   auto wait = [&](uint64_t *bar, uint32_t parity) {
