@@ -8,10 +8,25 @@
 // MN-major one (the same two strides) without any rearrangement.
 #pragma once
 
+#include <atomic>
+
 #include "tq_ptx.cuh"
 #include "tq_q8.h"
 
 namespace tq {
+
+// Let kernel K have `bytes` of dynamic shared memory on the current device: asked for once a device, not with every launch.
+template <auto K>
+bool allow_shared(int bytes) {
+  static std::atomic<uint64_t> devices{0};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return false;
+  const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+  if (devices.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  devices.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 constexpr float kQ8Largest = 3.1901471898837980e38f;  // 1.875 * 2^127: 240 * 2^120
 

@@ -551,8 +551,7 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
 template <int NR, int T, int KIND>
 int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
   constexpr int smem = kStages * kStage + stacked_rows(NR, T) * 128 * (1 + kWg);
-  if (cudaFuncSetAttribute(q8_attend_kernel<NR, T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return TQ_ERR_CUDA;
+  if (!allow_shared<q8_attend_kernel<NR, T, KIND>>(smem)) return TQ_ERR_CUDA;
   if (launch_overlapped(true, q8_attend_kernel<NR, T, KIND>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
   if (launch_overlapped(true, q8_join_kernel<KIND>, dim3(num_sms, NR), dim3(512), 0, st, a, rows_of(T), (const Cut *)cuts) != cudaSuccess)

@@ -917,8 +917,7 @@ template <int TERMS, int EXTRA, bool APART, int KIND>
 int launch(const Q8AttnArgs &a, const Plan &p, int num_sms, cudaStream_t st) {
   constexpr int smem = stages_of(TERMS, APART) * kStage + 2 * TERMS * kQTerm;
   const int slices = APART ? 2 * num_sms : num_sms;
-  if (cudaFuncSetAttribute(q8_prompt_kernel<TERMS, EXTRA, APART, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return TQ_ERR_CUDA;
+  if (!allow_shared<q8_prompt_kernel<TERMS, EXTRA, APART, KIND>>(smem)) return TQ_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (KIND == kWhole || p.entries > kPlanned) e = launch_overlapped(true, q8_entries_kernel<KIND>, dim3((p.entries + 7) / 8), dim3(256), 0, st, a, p);
   if (e == cudaSuccess) e = launch_overlapped(true, q8_prefix_kernel<KIND>, dim3(1), dim3(1024), 0, st, a, p, slices);

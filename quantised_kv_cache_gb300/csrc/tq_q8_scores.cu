@@ -311,13 +311,14 @@ int launch_q8_scores(const Q8SelectArgs &a, int num_sms, void *stream) {
   constexpr int smem = kABytes + kBBytes;
   const int tiles = (q8_blocks_of(a.q.max_len) + kTileBlocks - 1) / kTileBlocks;
   const long long total = (long long)a.q.batch * a.q.heads_kv * a.lists * tiles;
-  auto run = [&](auto kernel) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
-    return launch_overlapped(true, kernel, dim3((unsigned)std::min((long long)num_sms, total)), dim3(kThreads), smem, (cudaStream_t)stream, a, tiles,
-                             total) == cudaSuccess
-               ? TQ_OK : TQ_ERR_CUDA;
+  const dim3 grid((unsigned)std::min((long long)num_sms, total));
+  auto run = [&](bool allowed, auto kernel) {
+    if (!allowed) return TQ_ERR_CUDA;
+    return launch_overlapped(true, kernel, grid, dim3(kThreads), smem, (cudaStream_t)stream, a, tiles, total) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
   };
-  return a.q.q_dtype == TQ_F32 ? run(q8_scores_kernel<float>) : a.q.q_dtype == TQ_BF16 ? run(q8_scores_kernel<__nv_bfloat16>) : run(q8_scores_kernel<__half>);
+  if (a.q.q_dtype == TQ_F32) return run(allow_shared<q8_scores_kernel<float>>(smem), q8_scores_kernel<float>);
+  if (a.q.q_dtype == TQ_BF16) return run(allow_shared<q8_scores_kernel<__nv_bfloat16>>(smem), q8_scores_kernel<__nv_bfloat16>);
+  return run(allow_shared<q8_scores_kernel<__half>>(smem), q8_scores_kernel<__half>);
 }
 
 }  // namespace tq

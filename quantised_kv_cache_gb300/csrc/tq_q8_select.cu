@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
 
 template <int NT>
 int launch(const Q8SelectArgs &a, int ranks, size_t smem, cudaStream_t st) {
-  if (cudaFuncSetAttribute(q8_choose_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess) return TQ_ERR_CUDA;
+  if (!allow_shared<q8_choose_kernel<NT>>(kHeld * 4)) return TQ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)a.q.batch * a.q.heads_kv * a.lists * ranks));
   cfg.blockDim = dim3(kThreads);

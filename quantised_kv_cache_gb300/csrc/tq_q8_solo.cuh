@@ -480,7 +480,7 @@ size_t solo_bytes(int num_sms) {
 template <int NR, int KIND>
 int launch_solo_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
   constexpr int smem = kWg * (kPlaces * kPlace + 2 * stacked_rows(NR, 4) * 128);
-  if (cudaFuncSetAttribute(q8_solo_kernel<NR, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  if (!allow_shared<q8_solo_kernel<NR, KIND>>(smem)) return TQ_ERR_CUDA;
   if (launch_overlapped(true, q8_solo_kernel<NR, KIND>, dim3(num_sms), dim3(kSoloThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
   return launch_overlapped(true, q8_solo_join_kernel<NR, KIND>, dim3(num_sms * kWg), dim3(128 * NR), 0, st, a, (const Cut *)cuts) == cudaSuccess

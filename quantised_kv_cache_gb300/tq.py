@@ -641,16 +641,13 @@ def tq_q8_select_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: in
 _pack_pick = struct.Struct("@10iP3q6P")
 
 
-def _workspace(workspace: Optional[torch.Tensor], need, stream, index: int, device):
-    """(address, bytes) of a call's workspace, made where the caller brings none."""
+def _scratch(workspace: Optional[torch.Tensor], bytes_: int, stream, index: int, device):
+    """The workspace of a call: the caller's, or one of `bytes_` bytes made here (None for 0)."""
     if workspace is None:
-        n = need()
-        if not n:
-            return None, 0, None
-        workspace = _made(stream, torch.empty, n, dtype=torch.uint8, device=device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
+        return _made(stream, torch.empty, bytes_, dtype=torch.uint8, device=device) if bytes_ else None
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on q's device is wanted")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace
 
 
 def tq_q8_select(ctx, cache: "Cache", bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor, max_len: int, keep: int, sink: int = 0,
@@ -669,12 +666,14 @@ def tq_q8_select(ctx, cache: "Cache", bounds: torch.Tensor, q: torch.Tensor, seq
     lists = (B, H, (n + span - 1) // span, keep)
     if blocks is None:
         blocks = _made(stream, torch.empty, lists, dtype=_i32, device=q.device)
-    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_select_workspace(ctx, B, Hq, H, n, span, max_len), stream, index, q.device)
+    workspace = _scratch(workspace, 0 if workspace is not None else tq_q8_select_workspace(ctx, B, Hq, H, n, span, max_len), stream, index,
+                         q.device)
     a = _pack_pick.pack(B, Hq, H, n, span, max_len, keep, sink, recent, _any_dtype(q.dtype), q.data_ptr(), qs[0], qs[1], qs[2],
                         _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
                         _array(key_begin, (B, n), _i32, index, "key_begin") or 0, _array(key_end, (B, n), _i32, index, "key_end") or 0,
                         _bounds_array(bounds, cache) or 0, _array(blocks, lists, _i32, index, "blocks") or 0)
-    status = lib().tq_q8_select(ctx, cache.struct, a, ws, ws_bytes, _raw_stream(stream, index))
+    status = lib().tq_q8_select(ctx, cache.struct, a, None if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, index))
     if status:
         check(status, "tq_q8_select")
     return blocks
@@ -729,9 +728,10 @@ def tq_q8_sparse_attention(ctx, cache: "Cache", blocks: torch.Tensor, q: torch.T
         raise ValueError("span and blocks: at least 1, and lists [batch][heads_kv][ceil(tokens / span)][blocks], are wanted")
     keep = blocks.shape[3]
     lists = _array(blocks, (B, cache.heads_kv, (n + span - 1) // span, keep), _i32, index, "blocks")
-    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_sparse_attention_workspace(ctx, B, Hq, cache.heads_kv, n, span, keep), stream,
-                                         index, q.device)
-    status = lib().tq_q8_sparse_attention(ctx, cache.struct, a, lists, keep, span, ws, ws_bytes, _raw_stream(stream, index))
+    workspace = _scratch(workspace, 0 if workspace is not None else tq_q8_sparse_attention_workspace(ctx, B, Hq, cache.heads_kv, n, span, keep),
+                         stream, index, q.device)
+    status = lib().tq_q8_sparse_attention(ctx, cache.struct, a, lists, keep, span, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _raw_stream(stream, index))
     if status:
         check(status, "tq_q8_sparse_attention")
     return out
@@ -758,10 +758,10 @@ def tq_q8_shared_attention(ctx, prefix: "Cache", prefix_lens: torch.Tensor, max_
     B, Hq, n, _ = q.shape
     if prefix.device_index != index:
         raise ValueError("prefix: the cache's device is wanted")
-    ws, ws_bytes, workspace = _workspace(workspace, lambda: tq_q8_shared_attention_workspace(ctx, B, Hq, cache.heads_kv, n, max_prefix, max_len),
-                                         stream, index, q.device)
+    workspace = _scratch(workspace, 0 if workspace is not None else
+                         tq_q8_shared_attention_workspace(ctx, B, Hq, cache.heads_kv, n, max_prefix, max_len), stream, index, q.device)
     status = lib().tq_q8_shared_attention(ctx, prefix.struct, _array(prefix_lens, (B,), _i32, index, "prefix_lens"), max_prefix, cache.struct, a,
-                                          ws, ws_bytes, _raw_stream(stream, index))
+                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream, index))
     if status:
         check(status, "tq_q8_shared_attention")
     return out
