@@ -63,6 +63,10 @@ CASES = [  # B, heads_q, heads_kv, n_q, prefix, lens
     (2, 16, 2, 1, 700, [100, 900]), (5, 16, 2, 1, 333, [1, 50, 64, 65, 300]), (2, 8, 2, 5, 200, [5, 90]), (40, 8, 2, 1, 500, [1 + 5 * i for i in range(40)]),
     (3, 4, 1, 7, 1000, [7, 100, 64]), (2, 8, 2, 40, 300, [40, 333]), (1, 8, 2, 100, 200, [150]), (3, 4, 2, 129, 100, [129, 200, 300]),
     (70, 4, 1, 1, 4000, [3] * 70), (1, 4, 1, 1, 20000, [9]), (16, 1, 1, 1, 5000, list(range(1, 17))), (2, 6, 1, 50, 64, [20, 50]),
+    # rows that fill units of their own: one pass over both caches
+    (3, 8, 2, 64, 300, [64, 100, 130]), (2, 4, 1, 32, 1000, [32, 333]), (2, 4, 4, 256, 65, [256, 300]), (1, 8, 1, 250, 129, [700]),
+    # more sequences and heads than processors: warpgroups with units of their own
+    (80, 8, 2, 1, 200, [1 + 3 * i for i in range(80)]), (40, 4, 4, 1, 64, [0, 1, 2000] + [30 * i for i in range(37)]), (200, 3, 1, 1, 100, list(range(200))),
 ]
 
 
@@ -78,6 +82,7 @@ def test_shared_prefix(ctx, case, dtype, out):
     new = [n] * B
     if n > 1 and B > 1:
         new[-1] = n - 2
+    new = [m if L else 0 for m, L in zip(new, lens)]
     lse = torch.empty(B, Hq, n, device=DEV)
     got = torch.full((B, Hq, n, 128), 7.0, dtype=out, device=DEV)
     tq.tq_q8_shared_attention(ctx.handle, pre, ints(prefix), P, own, q, ints(lens), cap, new_lens=ints(new), lse=lse, out=got)
@@ -190,6 +195,25 @@ def test_a_batch_served_behind_a_prefix(ctx):
     for a, b in zip(eager, run(True)[0]):
         assert torch.equal(a, b)
     check(np64(eager[-1]), q, *values, [P] * B, lens, [1] * B, dtype=BF, out_dtype=BF)
+
+
+def test_replayed_many_times(ctx):
+    """A batch of short sequences, thousands of times: the same bytes, and no wait that ran out."""
+    B, H, Hq, P = 100, 4, 16, 300
+    lens = np.random.default_rng(1).integers(1, 600, B).tolist()
+    pre, own, *_ = caches(ctx, B, H, P, 600, lens, 7)
+    q, n, p = queries(5, B, Hq, 1, BF), ints(lens), ints([P] * B)
+    ws = torch.empty(tq.tq_q8_shared_attention_workspace(ctx.handle, B, Hq, H, 1, P, 600), dtype=torch.uint8, device=DEV)
+    first = tq.tq_q8_shared_attention(ctx.handle, pre, p, P, own, q, n, 600)
+    outs = [torch.empty_like(q) for _ in range(20)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for out in outs:
+            tq.tq_q8_shared_attention(ctx.handle, pre, p, P, own, q, n, 600, workspace=ws, out=out)
+    for _ in range(100):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, out) for out in outs) and tq.tq_get_device_error(ctx.handle) == 0
 
 
 def test_two_streams(ctx):

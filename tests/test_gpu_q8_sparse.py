@@ -114,6 +114,60 @@ def test_listed_blocks(ctx, case, dtype, out):
         assert (got[b, :, new[b]:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("B,Hq,H,longest,n_blocks", [(80, 8, 2, 300, 3), (40, 12, 4, 3000, 40), (160, 1, 1, 700, 9), (600, 3, 1, 130, 2)])
+def test_more_lists_than_processors(ctx, B, Hq, H, longest, n_blocks, dtype):
+    """Warpgroups with units of their own: short ones, ones that several slices share, sequences without tokens."""
+    r = np.random.default_rng(B)
+    lens = [longest, 0, 1, 64, 65] + r.integers(0, longest + 1, B - 5).tolist()
+    cache, k, v = make(ctx, B, H, longest + 70, lens, seed=B, paged=B % 3 == 0)
+    lists = some_lists(B, H, 1, n_blocks, lens, B, cache.blocks_per_seq)
+    poison_unlisted(cache, lists)
+    q = queries(5, B, Hq, 1, dtype)
+    slopes = torch.exp2(-torch.arange(1, Hq + 1, device=DEV, dtype=torch.float32))
+    new = r.integers(0, 2, B).tolist()
+    new = [min(x, y) for x, y in zip(new, lens)]
+    lse = torch.empty(B, Hq, 1, device=DEV)
+    for kw, ref in ((dict(), dict()), (dict(softcap=20.0, slopes=slopes, new_lens=ints(new)), dict(softcap=20.0, slopes=slopes))):
+        m = new if "new_lens" in kw else [min(1, x) for x in lens]
+        got = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+        tq.tq_q8_sparse_attention(ctx.handle, cache, torch.from_numpy(lists).to(DEV), q, ints(lens), longest + 70, lse=lse, out=got, **kw)
+        check(np64(got), np64(q), k, v, lists, 1, lens, m, dtype=dtype, out_dtype=dtype, lse=np64(lse), **ref)
+        for b in range(B):
+            assert (got[b] == (7.0 if m[b] == 0 and "new_lens" in kw else got[b])).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("Hq,H,n,span,n_blocks,length", [(64, 8, 320, 16, 8, 2000), (4, 1, 2100, 8, 4, 2500), (16, 8, 600, 100, 20, 1500)])
+def test_prompts_of_many_lists(ctx, Hq, H, n, span, n_blocks, length, dtype):
+    """Slices of whole units, more units than one block plans, units of both sizes."""
+    cache, k, v = make(ctx, 1, H, length, [length], seed=n)
+    q = queries(5, 1, Hq, n, dtype, "tokens")
+    lists = some_lists(1, H, -(-n // span), n_blocks, [length], n, cache.blocks_per_seq)
+    got = tq.tq_q8_sparse_attention(ctx.handle, cache, torch.from_numpy(lists).to(DEV), q, ints([length]), length, span=span)
+    check(np64(got), np64(q), k, v, lists, span, [length], [n], dtype=dtype, out_dtype=dtype)
+
+
+def test_replayed_many_times(ctx):
+    """Short units one after the other, thousands of times: the same bytes, and no wait that ran out."""
+    B, H, Hq = 128, 4, 16
+    lens = np.random.default_rng(1).integers(1, 900, B).tolist()
+    cache, _, _ = make(ctx, B, H, 900, lens, seed=2)
+    lists = torch.from_numpy(some_lists(B, H, 1, 6, lens, 3, cache.blocks_per_seq)).to(DEV)
+    q, n = queries(5, B, Hq, 1, BF), ints(lens)
+    ws = torch.empty(tq.tq_q8_sparse_attention_workspace(ctx.handle, B, Hq, H, 1, 1, 6), dtype=torch.uint8, device=DEV)
+    first = tq.tq_q8_sparse_attention(ctx.handle, cache, lists, q, n, 900)
+    outs = [torch.empty_like(q) for _ in range(20)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for out in outs:
+            tq.tq_q8_sparse_attention(ctx.handle, cache, lists, q, n, 900, workspace=ws, out=out)
+    for _ in range(100):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, out) for out in outs) and tq.tq_get_device_error(ctx.handle) == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("n,span", [(3, 1), (100, 64), (300, 128)])
 def test_masks_caps_and_biases(ctx, n, span, dtype):
