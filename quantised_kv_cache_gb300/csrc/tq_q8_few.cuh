@@ -24,6 +24,8 @@
 
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "tq_q8_rows.cuh"
@@ -45,6 +47,7 @@ constexpr int kPartRow = kD + 4;        // a partial record's row: O, m, l, roun
 
 constexpr int kStages = 5;
 constexpr int kRows = 16;               // rows of a partial record
+constexpr int kMostRanks = 8;           // CTAs of a cluster
 constexpr int rows_of(int T) { return T == 8 ? 8 : 16; }  // rows of a unit: what tensor memory holds the terms' columns of
 
 struct Entries {
@@ -77,7 +80,8 @@ struct Shared {
 
 __device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"(kConsumers) : "memory"); }
 
-template <int NR, int T, int KIND>
+// TEAM: a cluster's CTAs share one unit and join its parts through each other's shared memory; the units are numbered [sequence][rts][head].
+template <int NR, int T, int KIND, bool TEAM>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, int rts, Cut *cuts) {
   constexpr int kUnitRows = rows_of(T), kN = stacked_rows(NR, T), kOp = kN * 128;  // an operand's rows and bytes
@@ -104,8 +108,25 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   if constexpr (KIND != kWhole) pdl_trigger();  // the join waits for all of this grid, but its blocks may come as this one's leave
   pdl_wait();
 
-  // ---- the entries' tiles: one thread each
+  namespace cg = cooperative_groups;
+  const int ranks = TEAM ? (int)cg::this_cluster().num_blocks() : 1, rank = TEAM ? (int)cg::this_cluster().block_rank() : 0;
+  const int team = TEAM ? blockIdx.x / ranks : 0, team_h = team % a.heads_kv, team_x = team / a.heads_kv % rts, team_b = team / a.heads_kv / rts;
+  int team_lo = 0x7fffffff, team_hi = 0, team_tiles = 0;
   const int E = nb * rts;
+  if constexpr (TEAM) {  // every warp looks for itself, a lane at a token
+    int len, m, r0, end, list;
+    unit_span<KIND>(a, team_x, kUnitRows, &r0, &end, &list);
+    seq_sizes<KIND>(a, team_b, &len, &m, tid == 0);
+    const int i0 = r0 / G, i1 = (min(end, r0 + kUnitRows) - 1) / G;
+    if (i0 + lane <= i1) {
+      const int2 r = row_range<KIND>(a, team_b, i0 + lane, len, m);
+      if (r.y > r.x) team_lo = r.x, team_hi = r.y;
+    }
+    team_lo = __reduce_min_sync(kFull, team_lo), team_hi = __reduce_max_sync(kFull, team_hi);
+    if (team_hi == 0) team_lo = 0;
+    team_tiles = i0 < m ? max(1, unit_tiles<KIND>(a, team_b, team_lo, team_hi)) : 0;
+  } else {
+  // ---- the entries' tiles: one thread each
   int count = 0;
   if (KIND != kWhole && E <= kThreads / 32) {  // a warp each: a lane looks at a token (16 rows of a prefix's are as many sequences')
     int most = 0;
@@ -157,16 +178,21 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     if (tid < E) sm.ent.pre[tid + 1] = before + x;
     if (tid == 0) sm.ent.pre[0] = 0;
   }
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  const long long total = (long long)sm.ent.pre[E] * a.heads_kv;
+  const long long total = TEAM ? team_tiles : (long long)sm.ent.pre[E] * a.heads_kv;
   // slices, none of them empty: CTA c < slices has tiles [total c / slices, total (c + 1) / slices)
-  const long long slices = min((long long)gridDim.x, total);
-  const bool idle = blockIdx.x >= slices;
-  const long long g0 = idle ? 0 : quotient(total * blockIdx.x, slices), g1 = idle ? 0 : quotient(total * (blockIdx.x + 1), slices);
+  const long long slices = TEAM ? ranks : min((long long)gridDim.x, total), slice = TEAM ? rank : blockIdx.x;
+  const bool idle = slice >= slices;
+  const long long g0 = idle ? 0 : quotient(total * slice, slices), g1 = idle ? 0 : quotient(total * (slice + 1), slices);
   auto locate = [&](long long g, int &e, int &h, int &t, int &cnt) {
+    if constexpr (TEAM) {
+      e = 0, h = team_h, t = (int)g, cnt = team_tiles;
+      return;
+    }
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // the last entry that begins at or before g
       const int mid = (lo + hi + 1) >> 1;
@@ -179,6 +205,10 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     h = (int)quotient(in, cnt);
     t = (int)(in - (long long)h * cnt);
   };
+  auto seq_of = [&](int e) { return TEAM ? team_b : b0 + e / rts; };
+  auto unit_of = [&](int e) { return TEAM ? team_x : rt0 + e % rts; };
+  auto lo_of = [&](int e) { return TEAM ? team_lo : sm.ent.lo[e]; };
+  auto hi_of = [&](int e) { return TEAM ? team_hi : sm.ent.hi[e]; };
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (*(volatile int *)&sm.bad) return;
     if (!mbar_wait_bounded(bar, parity, a.error)) *(volatile int *)&sm.bad = 1;
@@ -194,14 +224,14 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       if (KIND == kListed && g + lane < g1) {
         int e, h, t, cnt, r0, end, list;
         locate(g + lane, e, h, t, cnt);
-        unit_span<KIND>(a, rt0 + e % rts, kUnitRows, &r0, &end, &list);
-        const long long bh = (long long)(b0 + e / rts) * a.heads_kv + h;
+        unit_span<KIND>(a, unit_of(e), kUnitRows, &r0, &end, &list);
+        const long long bh = (long long)seq_of(e) * a.heads_kv + h;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int blk = list_entry(a, bh, list, 2 * t + k);
           at[k] = max(blk, 0) * kQ8Block;
-          const int m = min(kQ8Block, sm.ent.hi[e] - at[k]);
-          if (blk < 0 || m <= 0 || at[k] + kQ8Block <= sm.ent.lo[e]) continue;  // no row sees a token of it
+          const int m = min(kQ8Block, hi_of(e) - at[k]);
+          if (blk < 0 || m <= 0 || at[k] + kQ8Block <= lo_of(e)) continue;  // no row sees a token of it
           src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + blk, a.error);
           if (src[k] < 0) continue;
           bytes[k] = (m + 31) / 32 * 32 * kD;
@@ -211,8 +241,8 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       } else if (g + lane < g1) {
         int e, h, t, cnt;
         locate(g + lane, e, h, t, cnt);
-        const int lo = sm.ent.lo[e], tok = (lo / kTile + t) * kTile, n = min(kTile, max(0, sm.ent.hi[e] - tok));
-        const long long v = ((long long)(b0 + e / rts) * a.heads_kv + h) * a.c.nblk + tok / kQ8Block;
+        const int lo = lo_of(e), tok = (lo / kTile + t) * kTile, n = min(kTile, max(0, hi_of(e) - tok));
+        const long long v = ((long long)seq_of(e) * a.heads_kv + h) * a.c.nblk + tok / kQ8Block;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int m = min(kQ8Block, n - k * kQ8Block);
@@ -275,14 +305,14 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
     const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
     uint32_t phase = 0;  // of this warpgroup's two barriers: its tiles so far
     long long g = g0;
-    while (g < g1) {
+    while (g < g1 || (TEAM && total > 0)) {
       int e, h, t0, cnt;
       locate(g, e, h, t0, cnt);
-      const int b = b0 + e / rts;
+      const int b = seq_of(e);
       int row0, row_end, list;
-      unit_span<KIND>(a, rt0 + e % rts, kUnitRows, &row0, &row_end, &list);
+      unit_span<KIND>(a, unit_of(e), kUnitRows, &row0, &row_end, &list);
       const long long end = min(g1, g - t0 + cnt);
-      const int first = sm.ent.lo[e] / kTile, hi = sm.ent.hi[e];
+      const int first = lo_of(e) / kTile, hi = hi_of(e);
 
       // ---- the unit's queries: warp w prepares row w
       {
@@ -456,7 +486,8 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       }
       bar_all();
       const bool whole = t0 == 0 && end == g + cnt;
-      float *part = a.parts + ((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRows * kPartRow;
+      // TEAM: where the ring was (no copy is under way, and the products that read it are done)
+      float *part = TEAM ? reinterpret_cast<float *>(ring) : a.parts + ((long long)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRows * kPartRow;
       int len, mm;
       seq_sizes<KIND>(a, b, &len, &mm, false);
 #pragma unroll 1
@@ -473,7 +504,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         }
         const int row = row0 + r, i = row / G;
         if (row >= row_end || i >= mm) continue;
-        if (whole) {
+        if (whole && (!TEAM || ranks == 1)) {
           const int hq = h * G + row % G;
           finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f);
         } else {
@@ -485,15 +516,47 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           }
         }
       }
+      if constexpr (TEAM) break;
       if (tid == 0 && end == g1) {
         // the CTA's last unit: if it goes on beyond this slice and began in it, the join starts here
         const long long stop = g - t0 + cnt;  // slices c with total c / slices < stop hold parts of it
         const int parts = t0 == 0 && stop > g1 ? (int)((stop * slices + total - 1) / total) - (int)blockIdx.x : 0;
-        cuts[blockIdx.x] = Cut{b, rt0 + e % rts, h, parts};
+        cuts[blockIdx.x] = Cut{b, unit_of(e), h, parts};
       }
       g = end;
     }
-    if (tid == 0 && g0 >= g1) cuts[blockIdx.x] = Cut{0, 0, 0, 0};
+    if (!TEAM && tid == 0 && g0 >= g1) cuts[blockIdx.x] = Cut{0, 0, 0, 0};
+  }
+  if constexpr (TEAM) {
+    if (ranks > 1 && total > 0) {  // the parts of a row: thread = coordinate, the ranks and their warpgroups take turns at the rows
+      cg::cluster_group cl = cg::this_cluster();
+      cl.sync();
+      int len, m, row0, row_end, list;
+      unit_span<KIND>(a, team_x, kUnitRows, &row0, &row_end, &list);
+      seq_sizes<KIND>(a, team_b, &len, &m, false);
+#pragma unroll 1
+      for (int r = rank + ranks * (warp >> 2); warp < kConsumers / 32 && r < NR; r += ranks * kWg) {
+        const int row = row0 + r, i = row / G, d = tid & 127;
+        if (row >= row_end || i >= m) continue;
+        float x[kMostRanks], mk[kMostRanks], lk[kMostRanks], lrk[kMostRanks], top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kMostRanks; ++k) {
+          const float *rec = cl.map_shared_rank(reinterpret_cast<float *>(ring), min(k, ranks - 1)) + r * kPartRow;
+          x[k] = rec[d], mk[k] = rec[kD], lk[k] = rec[kD + 1], lrk[k] = rec[kD + 2];
+        }
+#pragma unroll
+        for (int k = 0; k < kMostRanks; ++k) top = fmaxf(top, mk[k]);
+        float o = 0.f, l = 0.f, lr = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMostRanks; ++k) {
+          if (k >= ranks) break;
+          const float f = mk[k] == -INFINITY ? 1.f : ex2_approx(mk[k] - top);  // without a maximum: zeros (or NaN)
+          o = fmaf(x[k], f, o), l = fmaf(lk[k], f, l), lr = fmaf(lrk[k], f, lr);
+        }
+        finish_row<KIND>(a, team_b, team_h * G + row % G, i, d, o, top, l, lr, 15.f);
+      }
+      cl.sync();  // the others have read this CTA's parts
+    }
   }
   if (*(volatile int *)&sm.bad) settle();
   tc_fence_before_sync();
@@ -551,8 +614,8 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
 template <int NR, int T, int KIND>
 int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts, int num_sms, cudaStream_t st) {
   constexpr int smem = kStages * kStage + stacked_rows(NR, T) * 128 * (1 + kWg);
-  if (!allow_shared<q8_attend_kernel<NR, T, KIND>>(smem)) return TQ_ERR_CUDA;
-  if (launch_overlapped(true, q8_attend_kernel<NR, T, KIND>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
+  if (!allow_shared<q8_attend_kernel<NR, T, KIND, false>>(smem)) return TQ_ERR_CUDA;
+  if (launch_overlapped(true, q8_attend_kernel<NR, T, KIND, false>, dim3(num_sms), dim3(kThreads), smem, st, a, b0, nb, rt0, rts, cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
   if (launch_overlapped(true, q8_join_kernel<KIND>, dim3(num_sms, NR), dim3(512), 0, st, a, rows_of(T), (const Cut *)cuts) != cudaSuccess)
     return TQ_ERR_CUDA;
@@ -562,12 +625,49 @@ int launch_rows(const Q8AttnArgs &a, Cut *cuts, int b0, int nb, int rt0, int rts
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 size_t few_bytes(int num_sms) { return round16((size_t)num_sms * sizeof(Cut)) + (size_t)num_sms * 2 * kRows * kPartRow * sizeof(float); }
 
+template <int NR, int T, int KIND>
+int launch_team_rows(const Q8AttnArgs &a, int units, int ranks, cudaStream_t st) {
+  constexpr int smem = kStages * kStage + stacked_rows(NR, T) * 128 * (1 + kWg);
+  if (!allow_shared<q8_attend_kernel<NR, T, KIND, true>>(smem)) return TQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.batch * units * a.heads_kv * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, q8_attend_kernel<NR, T, KIND, true>, a, 0, a.batch, 0, units, (Cut *)nullptr) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+// CTAs that a unit is given where there are few units, 0 where slices do better: one launch instead of two, and no table of entries. Clusters
+// of 8, 4 and 2 as long as there is room for all (no more than two of 8 are counted on in a GPC). `tiles` of a unit at most.
+int team_ranks(const Q8AttnArgs &a, long long units, long long tiles, int num_sms) {
+  const long long n = a.batch * units * a.heads_kv;
+  const int ranks = n <= num_sms / 9 ? 8 : n <= num_sms / 4 - 6 ? 4 : n <= num_sms / 2 - 12 ? 2 : n <= num_sms ? 1 : 0;
+  return ranks && (tiles + ranks - 1) / ranks * 4 <= 5 * n * tiles / num_sms + 32 ? ranks : 0;
+}
+
 // All rows of a call, a few at a time; `units` a sequence, `tiles` at most of each; `w`: few_bytes() of workspace.
 template <int KIND>
 int launch_few(Q8AttnArgs a, int rows, long long units, long long tiles, char *w, int num_sms, cudaStream_t st) {
   Cut *cuts = (Cut *)w;
   a.parts = (float *)(w + round16((size_t)num_sms * sizeof(Cut)));
   const int all = (int)units;
+  if constexpr (KIND != kWhole) {
+    if (const int ranks = team_ranks(a, units, tiles, num_sms)) {
+      if (a.out_dtype == TQ_F32)
+        return rows == 1 ? launch_team_rows<1, 8, KIND>(a, all, ranks, st)
+               : rows <= 4 ? launch_team_rows<4, 8, KIND>(a, all, ranks, st) : launch_team_rows<8, 8, KIND>(a, all, ranks, st);
+      return rows == 1 ? launch_team_rows<1, 4, KIND>(a, all, ranks, st)
+             : rows <= 4 ? launch_team_rows<4, 4, KIND>(a, all, ranks, st)
+             : rows <= 8 ? launch_team_rows<8, 4, KIND>(a, all, ranks, st) : launch_team_rows<16, 4, KIND>(a, all, ranks, st);
+    }
+  }
   // (sequence, unit) pairs of a launch: as many as their table holds, and as keep the number of their tiles within 32 bits
   const int most = tiles * kEntries <= 0x7fffffff ? kEntries : (int)(0x7fffffff / tiles);
   const int per = all < most ? most / all : 1;
