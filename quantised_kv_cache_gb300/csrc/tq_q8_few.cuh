@@ -84,7 +84,7 @@ __device__ __forceinline__ void bar_all() { asm volatile("bar.sync 5, %0;" ::"n"
 template <int NR, int T, int KIND, bool TEAM>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, int rts, Cut *cuts) {
-  constexpr int kUnitRows = rows_of(T), kN = stacked_rows(NR, T), kOp = kN * 128;  // an operand's rows and bytes
+  constexpr int kUnitRows = TEAM ? NR : rows_of(T), kN = stacked_rows(NR, T), kOp = kN * 128;  // an operand's rows and bytes
   constexpr int kCols = 2 * kN;  // a warpgroup's columns: S, in its place O of the first block, then O of the second
   static_assert(NR <= kUnitRows && kWg * kCols <= 512 && kWg * NR * 512 <= kWg * kOp, "");
   extern __shared__ __align__(1024) uint8_t dyn[];
@@ -644,12 +644,47 @@ int launch_team_rows(const Q8AttnArgs &a, int units, int ranks, cudaStream_t st)
   return cudaLaunchKernelEx(&cfg, q8_attend_kernel<NR, T, KIND, true>, a, 0, a.batch, 0, units, (Cut *)nullptr) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
-// CTAs that a unit is given where there are few units, 0 where slices do better: one launch instead of two, and no table of entries. Clusters
-// of 8, 4 and 2 as long as there is room for all (no more than two of 8 are counted on in a GPC). `tiles` of a unit at most.
+// How many clusters of `ranks` CTAs the current device runs at once (their CTAs share a GPC): 15 of 8, 36 of 4, 76 of 2.
+template <int KIND>
+int clusters_of(int ranks) {
+  constexpr int smem = kStages * kStage + stacked_rows(4, 4) * 128 * (1 + kWg);
+  static std::atomic<int> known[64][4];  // plus 1
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || !allow_shared<q8_attend_kernel<4, 4, KIND, true>>(smem)) return 0;
+  const int k = ranks == 8 ? 3 : ranks == 4 ? 2 : ranks == 2 ? 1 : 0;
+  if (device < 64 && known[device][k].load(std::memory_order_relaxed)) return known[device][k].load(std::memory_order_relaxed) - 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, q8_attend_kernel<4, 4, KIND, true>, &cfg) != cudaSuccess) n = 0;
+  if (device < 64) known[device][k].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs that a unit is given where there are few units, 0 where slices do better: one launch instead of two, and no table of entries, but a
+// CTA may get up to a quarter and 8 more tiles than an even slice. `tiles` of a unit at most. 8 KV heads of 4 rows over 64 blocks 12.2 us in
+// slices, 9.7 in clusters of 8; 8 sequences over 48 blocks 20.4 and 14.2 in clusters of 2.
+template <int KIND>
 int team_ranks(const Q8AttnArgs &a, long long units, long long tiles, int num_sms) {
   const long long n = a.batch * units * a.heads_kv;
-  const int ranks = n <= num_sms / 9 ? 8 : n <= num_sms / 4 - 6 ? 4 : n <= num_sms / 2 - 12 ? 2 : n <= num_sms ? 1 : 0;
-  return ranks && (tiles + ranks - 1) / ranks * 4 <= 5 * n * tiles / num_sms + 32 ? ranks : 0;
+  if (n > num_sms) return 0;
+  int ranks = 1;
+  for (int k = 8; k > 1 && ranks == 1; k /= 2)
+    if (n * k <= num_sms && n <= clusters_of<KIND>(k)) ranks = k;
+  return (tiles + ranks - 1) / ranks * 4 <= 5 * n * tiles / num_sms + 32 ? ranks : 0;
+}
+
+// What `tiles` tiles of a CTA cost, and a unit's end, in tenths of a microsecond: a round of one tile a warpgroup and the end of units
+// of 4 rows 2.2 and 1.4, of 8 4.0 and 1.7, of 16 8.5 and 4.0 (8 KV heads of 16 rows over 64 blocks 19.1 us as one unit a head, 12.2 as four).
+inline long long team_cost(int rows, long long tiles) {
+  const long long rounds = (tiles + kWg - 1) / kWg;
+  return rows <= 4 ? 22 * rounds + 14 : rows <= 8 ? 40 * rounds + 17 : 85 * rounds + 40;
 }
 
 // All rows of a call, a few at a time; `units` a sequence, `tiles` at most of each; `w`: few_bytes() of workspace.
@@ -659,7 +694,15 @@ int launch_few(Q8AttnArgs a, int rows, long long units, long long tiles, char *w
   a.parts = (float *)(w + round16((size_t)num_sms * sizeof(Cut)));
   const int all = (int)units;
   if constexpr (KIND != kWhole) {
-    if (const int ranks = team_ranks(a, units, tiles, num_sms)) {
+    const long long lists = rows <= (a.out_dtype == TQ_F32 ? 8 : 16) ? units : 0;  // with one unit each
+    const int ranks = lists ? team_ranks<KIND>(a, units, tiles, num_sms) : 0;
+    if (lists && rows > 4) {  // or as units of 4 rows, which read the list's blocks again (from L2)
+      const long long fours = lists * ((rows + 3) / 4);
+      const int four = team_ranks<KIND>(a, fours, tiles, num_sms);
+      if (four && (!ranks || team_cost(4, (tiles + four - 1) / four) <= team_cost(rows, (tiles + ranks - 1) / ranks)))
+        return a.out_dtype == TQ_F32 ? launch_team_rows<4, 8, KIND>(a, (int)fours, four, st) : launch_team_rows<4, 4, KIND>(a, (int)fours, four, st);
+    }
+    if (ranks) {
       if (a.out_dtype == TQ_F32)
         return rows == 1 ? launch_team_rows<1, 8, KIND>(a, all, ranks, st)
                : rows <= 4 ? launch_team_rows<4, 8, KIND>(a, all, ranks, st) : launch_team_rows<8, 8, KIND>(a, all, ranks, st);
