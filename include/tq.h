@@ -675,7 +675,7 @@ tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pic
  *              ones behind the last; blocks that no row of the list sees are passed over. So is an entry that is not above the one before
  *              it, follows a negative one or lies past the cache's last block, which sets the error word to TQ_ERR_ARG.
  * a->d_weights and a->d_weights_in have to be NULL (TQ_ERR_UNSUPPORTED). Workspace: of these sizes or larger ones in each but span, which has
- * to be the same. Results as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
+ * to be the same. Results at least as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
 tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int n_blocks,
                                            size_t *out);
 tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, const int32_t *d_blocks, int n_blocks,
@@ -687,8 +687,8 @@ tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const
  * the cache is slot d_prefix_lens[b] + s of the sequence, in d_key_begin and d_key_end (default [0, the query's own slot + 1)) and in the bias'
  * distances. a->max_len bounds d_seq_lens, which count the cache's tokens. a->d_q_positions, a->d_k_positions, a->d_weights and a->d_weights_in have to be
  * NULL (TQ_ERR_UNSUPPORTED). A d_prefix_lens[b] out of range is cut and sets the error word to TQ_ERR_ARG. The two
- * parts' sums are joined in fp32 before the one rounding of the result; the prefix's rows are the whole batch's (batch x n_q x group), whose number
- * decides the precision of its probabilities as in tq_q8_attention. Workspace: of these sizes or larger ones. */
+ * parts' sums are joined in fp32 before the one rounding of the result; probabilities are at least as precise as those of tq_q8_attention for
+ * as many rows as the whole batch has (batch x n_q x group). Workspace: of these sizes or larger ones. */
 tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
                                            size_t *out);
 tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix,

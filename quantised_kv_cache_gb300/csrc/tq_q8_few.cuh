@@ -687,6 +687,16 @@ inline long long team_cost(int rows, long long tiles) {
   return rows <= 4 ? 22 * rounds + 14 : rows <= 8 ? 40 * rounds + 17 : 85 * rounds + 40;
 }
 
+// More rows than a unit's, 16-bit results: clusters of 16-row units take them where these are few and short, rather than the kernel for many
+// rows, whose plan, start and join cost some 20 us and a tile of 256 rows 3.1 us of an SM. 8 KV heads: 40 rows over 16 blocks 17 us, 22 there, over 64
+// blocks 25 and 34; 256 rows over 64 slots 12 us less than there; one head, 132 rows over 128 blocks 25 and 45.
+template <int KIND>
+bool team_takes(const Q8AttnArgs &a, long long rows, long long lists, long long tiles, int num_sms) {
+  const int ranks = team_ranks<KIND>(a, (rows + 15) / 16 * lists, tiles, num_sms);
+  const long long there = 200 + 31 * ((rows + 255) / 256 * lists * a.batch * a.heads_kv * tiles) / num_sms;
+  return ranks && team_cost(16, (tiles + ranks - 1) / ranks) <= there;
+}
+
 // All rows of a call, a few at a time; `units` a sequence, `tiles` at most of each; `w`: few_bytes() of workspace.
 template <int KIND>
 int launch_few(Q8AttnArgs a, int rows, long long units, long long tiles, char *w, int num_sms, cudaStream_t st) {
@@ -694,10 +704,9 @@ int launch_few(Q8AttnArgs a, int rows, long long units, long long tiles, char *w
   a.parts = (float *)(w + round16((size_t)num_sms * sizeof(Cut)));
   const int all = (int)units;
   if constexpr (KIND != kWhole) {
-    const long long lists = rows <= (a.out_dtype == TQ_F32 ? 8 : 16) ? units : 0;  // with one unit each
-    const int ranks = lists ? team_ranks<KIND>(a, units, tiles, num_sms) : 0;
-    if (lists && rows > 4) {  // or as units of 4 rows, which read the list's blocks again (from L2)
-      const long long fours = lists * ((rows + 3) / 4);
+    const int ranks = team_ranks<KIND>(a, units, tiles, num_sms);
+    if (rows > 4 && rows <= (a.out_dtype == TQ_F32 ? 8 : 16)) {  // or as units of 4 rows, which read the list's blocks again (from L2)
+      const long long fours = units * ((rows + 3) / 4);
       const int four = team_ranks<KIND>(a, fours, tiles, num_sms);
       if (four && (!ranks || team_cost(4, (tiles + four - 1) / four) <= team_cost(rows, (tiles + ranks - 1) / ranks)))
         return a.out_dtype == TQ_F32 ? launch_team_rows<4, 8, KIND>(a, (int)fours, four, st) : launch_team_rows<4, 4, KIND>(a, (int)fours, four, st);

@@ -19,13 +19,13 @@ bool q8_listed_fits(const Q8AttnArgs &a) {
 }
 
 int launch_q8_listed(const Q8AttnArgs &a, void *workspace, int num_sms, void *stream) {
-  if (!listed_few(a.group, a.span, a.out_dtype)) return launch_q8_listed_many(a, workspace, num_sms, stream);
-  const long long rows = (long long)a.group * a.span, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
+  const long long rows = (long long)a.group * a.span, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4), units = (rows + unit - 1) / unit * a.lists;
   const long long tiles = (std::min(a.n_blocks, a.c.nblk) + 1) / 2;
+  if (!listed_few(a.group, a.span, a.out_dtype) && !team_takes<kListed>(a, rows, a.lists, tiles, num_sms))
+    return launch_q8_listed_many(a, workspace, num_sms, stream);
   if (solo_wins(a, a.lists, num_sms))
     return launch_solo<kListed>(a, (int)rows, a.lists, tiles, (char *)workspace, num_sms, (cudaStream_t)stream);
-  return launch_few<kListed>(a, (int)std::min(rows, 1024ll), (rows + unit - 1) / unit * a.lists, tiles, (char *)workspace, num_sms,
-                             (cudaStream_t)stream);
+  return launch_few<kListed>(a, (int)std::min(rows, 1024ll), units, tiles, (char *)workspace, num_sms, (cudaStream_t)stream);
 }
 
 }  // namespace tq

@@ -50,13 +50,12 @@ bool q8_shared_fits(const Q8AttnArgs &own, int num_sms) {
 
 template <int KIND>
 static int launch_part(const Q8AttnArgs &a, char *w, int num_sms, void *stream, int (*many)(const Q8AttnArgs &, void *, int, void *)) {
-  const long long rows = (long long)a.group * a.n_q, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4);
-  if (!takes_few(rows, a.out_dtype)) return many(a, w, num_sms, stream);
+  const long long rows = (long long)a.group * a.n_q, unit = rows_of(a.out_dtype == TQ_F32 ? 8 : 4), units = (rows + unit - 1) / unit;
+  const long long tiles = (a.max_len + kTile - 1) / kTile;
+  if (!takes_few(rows, a.out_dtype) && !team_takes<KIND>(a, rows, 1, tiles, num_sms)) return many(a, w, num_sms, stream);
   if constexpr (KIND == kOwn)
-    if (solo_wins(a, 1, num_sms))
-      return launch_solo<KIND>(a, (int)rows, 1, (a.max_len + kTile - 1) / kTile, w, num_sms, (cudaStream_t)stream);
-  return launch_few<KIND>(a, (int)std::min(rows, 1024ll), (rows + unit - 1) / unit, (a.max_len + kTile - 1) / kTile, w, num_sms,
-                          (cudaStream_t)stream);
+    if (solo_wins(a, 1, num_sms)) return launch_solo<KIND>(a, (int)rows, 1, tiles, w, num_sms, (cudaStream_t)stream);
+  return launch_few<KIND>(a, (int)std::min(rows, 1024ll), units, tiles, w, num_sms, (cudaStream_t)stream);
 }
 
 int launch_q8_shared(const Q8AttnArgs &args, const Q8Cache &prefix, void *workspace, int num_sms, void *stream) {

@@ -65,6 +65,8 @@ CASES = [  # B, heads_q, heads_kv, n_q, prefix, lens
     (70, 4, 1, 1, 4000, [3] * 70), (1, 4, 1, 1, 20000, [9]), (16, 1, 1, 1, 5000, list(range(1, 17))), (2, 6, 1, 50, 64, [20, 50]),
     # rows that fill units of their own: one pass over both caches
     (3, 8, 2, 64, 300, [64, 100, 130]), (2, 4, 1, 32, 1000, [32, 333]), (2, 4, 4, 256, 65, [256, 300]), (1, 8, 1, 250, 129, [700]),
+    # too many rows for clusters of few: the kernel for many over the prefix, and over the own tokens
+    (64, 64, 8, 1, 300, [5 + b for b in range(64)]), (8, 8, 2, 40, 300, [40 + 30 * b for b in range(8)]), (5, 32, 8, 9, 700, [9, 100, 64, 333, 20]),
     # more sequences and heads than processors: warpgroups with units of their own
     (80, 8, 2, 1, 200, [1 + 3 * i for i in range(80)]), (40, 4, 4, 1, 64, [0, 1, 2000] + [30 * i for i in range(37)]), (200, 3, 1, 1, 100, list(range(200))),
 ]
