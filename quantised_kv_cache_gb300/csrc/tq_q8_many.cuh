@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024) q8_prefix_kernel(const __grid_constant__
     __syncthreads();
   }
   const long long tiles = (long long)base * heads;
-  // Few units of many slices each: every slice begins with a start of its own then (8 units of 256 tiles: DEC us with it counted, ODE without).
+  // Few units of many slices each: every slice begins with a start of its own then (counted, it would leave the first slice of a unit 3 tiles short).
   const bool few = KIND != kWhole && 4LL * base_starts * heads <= ctas;
   const int start = tiles >= 2LL * ctas && !few ? kStart : 0;
   const bool near = KIND != kWhole && p.entries <= kPlanned;

@@ -669,9 +669,11 @@ def tq_q8_select(ctx, cache: "Cache", bounds: torch.Tensor, q: torch.Tensor, seq
     workspace = _scratch(workspace, 0 if workspace is not None else tq_q8_select_workspace(ctx, B, Hq, H, n, span, max_len), stream, index,
                          q.device)
     a = _pack_pick.pack(B, Hq, H, n, span, max_len, keep, sink, recent, _any_dtype(q.dtype), q.data_ptr(), qs[0], qs[1], qs[2],
-                        _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
-                        _array(key_begin, (B, n), _i32, index, "key_begin") or 0, _array(key_end, (B, n), _i32, index, "key_end") or 0,
-                        _bounds_array(bounds, cache) or 0, _array(blocks, lists, _i32, index, "blocks") or 0)
+                        _array(seq_lens, (B,), _i32, index, "seq_lens"),
+                        0 if new_lens is None else _array(new_lens, (B,), _i32, index, "new_lens"),
+                        0 if key_begin is None else _array(key_begin, (B, n), _i32, index, "key_begin"),
+                        0 if key_end is None else _array(key_end, (B, n), _i32, index, "key_end"),
+                        _bounds_array(bounds, cache), _array(blocks, lists, _i32, index, "blocks"))
     status = lib().tq_q8_select(ctx, cache.struct, a, None if workspace is None else workspace.data_ptr(),
                                 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, index))
     if status:
@@ -695,12 +697,14 @@ def _attn(cache: "Cache", q: torch.Tensor, seq_lens, max_len, new_lens, scale, s
     rows = (B, n)
     a = _pack_attn.pack(
         B, Hq, H, n, max_len, _any_dtype(q.dtype), _any_dtype(out.dtype), q.data_ptr(), qs[0], qs[1], qs[2], out.data_ptr(), os[0],
-        os[1], os[2], _array(seq_lens, (B,), _i32, index, "seq_lens") or 0, _array(new_lens, (B,), _i32, index, "new_lens") or 0,
-        scale, softcap, _array(slopes, (Hq,), _f32, index, "slopes") or 0,
-        _array(q_positions, rows, _i32, index, "q_positions") or 0,
-        _array(k_positions, (B, H, cache.capacity), _i32, index, "k_positions") or 0,
-        _array(key_begin, rows, _i32, index, "key_begin") or 0, _array(key_end, rows, _i32, index, "key_end") or 0, 0, 0,
-        _array(lse, (B, Hq, n), _f32, index, "lse") or 0)
+        os[1], os[2], _array(seq_lens, (B,), _i32, index, "seq_lens"),
+        0 if new_lens is None else _array(new_lens, (B,), _i32, index, "new_lens"),
+        scale, softcap, 0 if slopes is None else _array(slopes, (Hq,), _f32, index, "slopes"),
+        0 if q_positions is None else _array(q_positions, rows, _i32, index, "q_positions"),
+        0 if k_positions is None else _array(k_positions, (B, H, cache.capacity), _i32, index, "k_positions"),
+        0 if key_begin is None else _array(key_begin, rows, _i32, index, "key_begin"),
+        0 if key_end is None else _array(key_end, rows, _i32, index, "key_end"), 0, 0,
+        0 if lse is None else _array(lse, (B, Hq, n), _f32, index, "lse"))
     return a, out, index
 
 
@@ -848,6 +852,7 @@ class Cache:
         self.device_index = -1 if self.device.index is None else self.device.index  # as Tensor.get_device()
         self.block_tokens = Q8_BLOCK_TOKENS if ctx.scheme == "Q8" else BLOCK_TOKENS
         self.batch, self.heads_kv, self.capacity = batch, heads_kv, capacity
+        self.bounds_blocks = batch * heads_kv * self.blocks_per_seq  # blocks that the arrays hold
         self.tensors = {}
         self.struct = tq_cache()
         self.struct.batch, self.struct.heads_kv, self.struct.capacity = batch, heads_kv, capacity
@@ -868,11 +873,6 @@ class Cache:
     @property
     def blocks_per_seq(self) -> int:
         return (self.capacity + self.block_tokens - 1) // self.block_tokens
-
-    @property
-    def bounds_blocks(self) -> int:
-        """The blocks that the cache's arrays hold."""
-        return self.batch * self.heads_kv * self.blocks_per_seq
 
     def new_bounds(self) -> torch.Tensor:
         """Zeroed key bounds for an 8-bit cache (tq_q8_bounds): int8 [blocks][2][128]."""
@@ -928,6 +928,7 @@ class PagedCache(Cache):
         self.pool_blocks = int(pool_blocks)
         self.block_tokens = Q8_BLOCK_TOKENS if ctx.scheme == "Q8" else BLOCK_TOKENS
         super().__init__(ctx, batch, heads_kv, capacity, device)
+        self.bounds_blocks = self.pool_blocks
         nblk = self.blocks_per_seq
         assert block_table.dtype == torch.int32 and block_table.is_contiguous()
         assert tuple(block_table.shape) == (batch, heads_kv, nblk)
@@ -941,10 +942,6 @@ class PagedCache(Cache):
         if name in ("k_stats", "v_stats") and self.block_tokens == Q8_BLOCK_TOKENS:
             return self.pool_blocks * 4
         return getattr(self.sizes, name)
-
-    @property
-    def bounds_blocks(self) -> int:
-        return self.pool_blocks
 
     def blocks(self) -> torch.Tensor:
         """The sequence-heads' blocks gathered out of the pool through the table (a copy;
