@@ -7,7 +7,8 @@
 // e4m3 bytes are sign and magnitude. As upper bytes of 16-bit numbers (the lower byte only breaks ties): the largest unsigned number is the
 // smallest code if any is negative, else the smallest unsigned one is; the largest signed number is the largest code if any
 // is not negative, else the smallest unsigned one is. So three running numbers, in instructions that take two new ones at a time.
-// Bound by memory, or for one step's blocks by a launch and the chain of lengths, table and codes.
+// Bound by memory, or for one step's blocks by a launch and the chain of lengths, table and codes. 4 x 16384 tokens, 8 KV heads: 13.3 us where
+// the keys' 67 MB take 9.9 (2.5 us are the launch; ALU 48 % busy); one new token for each of 16 sequences: 2.5 us.
 
 #include <algorithm>
 

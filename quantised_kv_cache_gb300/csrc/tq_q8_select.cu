@@ -11,7 +11,8 @@
 // chooses. A warp forms the scores of 16 blocks and 8 or 16 rows with m16n8k16 products: so few rows would leave a tcgen05 tile empty, and bounds
 // go from memory to the operand's registers as they lie (chains of four byte products in one instruction, dp4a, took 17 clocks each on
 // a quarter of an SM: 6 of the 13 us). Lists of more rows: q8_scores_kernel. Bound by latency for few lists (lengths, bounds, a cluster barrier,
-// the passes of the choice).
+// the passes of the choice): 8 KV heads of 4 rows among 2048 blocks 9.3 us, 2.5 of them the launch; 384 lists among up to 512 blocks (7 MB of
+// bounds) 12.6 us.
 
 #include <cooperative_groups.h>
 
