@@ -665,7 +665,7 @@ typedef struct tq_q8_pick {
  * bounds, no key of a block has a larger product with a row. Rows with an infinity or a NaN
  * do not count (no row left: all scores are 0). Lengths out of range are cut as by tq_q8_attention; blocks with a bad table entry score
  * below all others; both set the error word to TQ_ERR_ARG.
- * Workspace: tq_q8_select_workspace(...) bytes for these sizes or larger ones (0: d_workspace may be NULL). */
+ * Workspace: tq_q8_select_workspace(...) bytes for the same heads and these sizes or larger ones (0: d_workspace may be NULL). */
 tq_status tq_q8_select_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int max_len, size_t *out);
 tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pick *p, void *d_workspace, size_t workspace_bytes,
                        void *stream);
@@ -674,8 +674,8 @@ tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pic
  *   d_blocks : int32 [batch][heads_kv][ceil(n_q / span)][n_blocks], 4-byte aligned, block numbers of the sequence in ascending order, negative
  *              ones behind the last; blocks that no row of the list sees are passed over. So is an entry that is not above the one before
  *              it, follows a negative one or lies past the cache's last block, which sets the error word to TQ_ERR_ARG.
- * a->d_weights and a->d_weights_in have to be NULL (TQ_ERR_UNSUPPORTED). Workspace: of these sizes or larger ones in each but span, which has
- * to be the same. Results at least as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
+ * a->d_weights and a->d_weights_in have to be NULL (TQ_ERR_UNSUPPORTED). Workspace: of the same heads and span, and of these
+ * sizes or larger ones. Results at least as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
 tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int n_blocks,
                                            size_t *out);
 tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, const int32_t *d_blocks, int n_blocks,
@@ -688,7 +688,7 @@ tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const
  * distances. a->max_len bounds d_seq_lens, which count the cache's tokens. a->d_q_positions, a->d_k_positions, a->d_weights and a->d_weights_in have to be
  * NULL (TQ_ERR_UNSUPPORTED). A d_prefix_lens[b] out of range is cut and sets the error word to TQ_ERR_ARG. The two
  * parts' sums are joined in fp32 before the one rounding of the result; probabilities are at least as precise as those of tq_q8_attention for
- * as many rows as the whole batch has (batch x n_q x group). Workspace: of these sizes or larger ones. */
+ * as many rows as the whole batch has (batch x n_q x group). Workspace: of the same heads and these sizes or larger ones. */
 tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
                                            size_t *out);
 tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix,

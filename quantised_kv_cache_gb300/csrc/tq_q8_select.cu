@@ -11,8 +11,8 @@
 // chooses. A warp forms the scores of 16 blocks and 8 or 16 rows with m16n8k16 products: so few rows would leave a tcgen05 tile empty, and bounds
 // go from memory to the operand's registers as they lie (chains of four byte products in one instruction, dp4a, took 17 clocks each on
 // a quarter of an SM: 6 of the 13 us). Lists of more rows: q8_scores_kernel. Bound by latency for few lists (lengths, bounds, a cluster barrier,
-// the passes of the choice): 8 KV heads of 4 rows among 2048 blocks 9.3 us, 2.5 of them the launch; 384 lists among up to 512 blocks (7 MB of
-// bounds) 12.6 us.
+// the passes of the choice): 8 KV heads of 4 rows among 2048 blocks 9.0 us, 2.5 of them the launch; 384 lists among up to 512 blocks (7 MB of
+// bounds) 12.1 us.
 
 #include <cooperative_groups.h>
 
@@ -190,18 +190,14 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   if (tid == 0) sm.rows = 0;
   pdl_trigger();
   pdl_wait();
-  // ---- the first rows and the lengths on their way at once: a warp has rows `warp` and, of 16, `warp` + 8
-  constexpr int NR = 8 * NT;
+  // ---- the rows and the lengths on their way at once: a warp has rows `warp` and, of 16, `warp` + 8
   const int tok0 = l * a.span;
   float x[NT][4];
-  auto load = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      const int r = r0 + warp + 8 * u, i = tok0 + r / G;
-      row_coords(a.q, b, h * G + r % G, i, i < min((long long)a.q.n_q, (long long)tok0 + a.span), lane, x[u]);
-    }
-  };
-  load(0);
+  for (int u = 0; u < NT; ++u) {
+    const int r = warp + 8 * u, i = tok0 + r / G;
+    row_coords(a.q, b, h * G + r % G, i, i < min((long long)a.q.n_q, (long long)tok0 + a.span), lane, x[u]);
+  }
   int len, m, lo, hi;
   seq_sizes(a.q, b, &len, &m, h == 0 && l == 0 && rank == 0 && tid == 0);
   const int tok1 = min(m, (int)min((long long)a.q.n_q, (long long)tok0 + a.span));
@@ -239,27 +235,20 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   };
   const int begin = s0 + 16 * warp;
   fetch(begin);
-  // ---- the rows' largest coordinate, over all rows that count
+  // ---- the rows' largest coordinate, over those that count
   const int rows = max(0, tok1 - tok0) * G;
   bool live[NT];
   uint32_t amax = 0;
-  auto look = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      const int r = r0 + warp + 8 * u;
-      const uint32_t top = row_top(x[u]);
-      live[u] = r < rows && top < 0x7f800000u;
-      if (live[u]) {
-        const int2 rg = row_range(a.q, b, tok0 + r / G, len, m);
-        live[u] = rg.y > rg.x;
-      }
-      if (live[u]) amax = max(amax, top);
+  for (int u = 0; u < NT; ++u) {
+    const int r = warp + 8 * u;
+    const uint32_t top = row_top(x[u]);
+    live[u] = r < rows && top < 0x7f800000u;
+    if (live[u]) {
+      const int2 rg = row_range(a.q, b, tok0 + r / G, len, m);
+      live[u] = rg.y > rg.x;
     }
-  };
-  look(0);
-  if (rows > NR) {
-    for (int r0 = NR; r0 < rows; r0 += NR) load(r0), look(r0);
-    load(0), look(0);
+    if (live[u]) amax = max(amax, top);
   }
   if (lane == 0) sm.amax[warp] = amax;
   __syncthreads();
@@ -270,75 +259,60 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   const float by = pow2i(-row_exponent(__float_as_uint(__uint_as_float(amax) * lift), 6));
   const bool big = n > kHeld;
   uint32_t *const far = a.keys + list * a.keys_ld;
-  uint32_t *const own = big ? far + s0 : held;  // this CTA's scores before the last of several passes
-  for (int r0 = 0; r0 < rows; r0 += NR) {
-    const bool last = r0 + NR >= rows;
-    if (r0) load(r0), look(r0), fetch(begin);
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      const int r = warp + 8 * u;
-      int w[4];
+  for (int u = 0; u < NT; ++u) {
+    const int r = warp + 8 * u;
+    int w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = live[u] ? min(max(__float2int_rn(x[u][k] * lift * by), -127), 127) : 0;
-      auto pair = [](int p, int q) {
-        const __half2 y = __halves2half2(__int2half_rn(p), __int2half_rn(q));
-        return *reinterpret_cast<const uint32_t *>(&y);
-      };
-      // coordinates 4 lane ..: of column lane / 4, step lane % 4 of that column's four
-      const int step = (lane >> 4) * 4 + (lane & 3), at = 4 * warp + ((lane >> 2) & 3);
-      sm.rows8[u][step][at] = make_uint2(pair(max(w[0], 0), max(w[1], 0)), pair(max(w[2], 0), max(w[3], 0)));
-      sm.rows8[u][step + 8][at] = make_uint2(pair(min(w[0], 0), min(w[1], 0)), pair(min(w[2], 0), min(w[3], 0)));
-      if (lane == 0 && live[u]) atomicOr(&sm.rows, 1u << r);
-    }
-    __syncthreads();
-    const uint32_t which = sm.rows;
-    if (last && ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    uint32_t *const dest = big ? far + s0 : ranks > 1 ? cl.map_shared_rank(held, 0) + s0 : held;
-    for (int i0 = begin; i0 < s1; i0 += 16 * kWarps) {
-      if (i0 != begin) fetch(i0);
-      float d[NT][4];
+    for (int k = 0; k < 4; ++k) w[k] = live[u] ? min(max(__float2int_rn(x[u][k] * lift * by), -127), 127) : 0;
+    auto pair = [](int p, int q) {
+      const __half2 y = __halves2half2(__int2half_rn(p), __int2half_rn(q));
+      return *reinterpret_cast<const uint32_t *>(&y);
+    };
+    // coordinates 4 lane ..: of column lane / 4, step lane % 4 of that column's four
+    const int step = (lane >> 4) * 4 + (lane & 3), at = 4 * warp + ((lane >> 2) & 3);
+    sm.rows8[u][step][at] = make_uint2(pair(max(w[0], 0), max(w[1], 0)), pair(max(w[2], 0), max(w[3], 0)));
+    sm.rows8[u][step + 8][at] = make_uint2(pair(min(w[0], 0), min(w[1], 0)), pair(min(w[2], 0), min(w[3], 0)));
+    if (lane == 0 && live[u]) atomicOr(&sm.rows, 1u << r);
+  }
+  __syncthreads();
+  const uint32_t which = sm.rows;
+  if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  uint32_t *const dest = big ? far + s0 : ranks > 1 ? cl.map_shared_rank(held, 0) + s0 : held;
+  for (int i0 = begin; i0 < s1; i0 += 16 * kWarps) {
+    if (i0 != begin) fetch(i0);
+    float d[NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+    for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // hi, lo; either column
+    for (int k = 0; k < 4; ++k) {  // hi, lo; either column
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 p0 = v[0][k >> 1][k & 1], p1 = v[1][k >> 1][k & 1];
-          const uint2 a0 = bytes_h4(q == 0 ? p0.x : q == 1 ? p0.y : q == 2 ? p0.z : p0.w);
-          const uint2 a1 = bytes_h4(q == 0 ? p1.x : q == 1 ? p1.y : q == 2 ? p1.z : p1.w);
+      for (int q = 0; q < 4; ++q) {
+        const uint4 p0 = v[0][k >> 1][k & 1], p1 = v[1][k >> 1][k & 1];
+        const uint2 a0 = bytes_h4(q == 0 ? p0.x : q == 1 ? p0.y : q == 2 ? p0.z : p0.w);
+        const uint2 a1 = bytes_h4(q == 0 ? p1.x : q == 1 ? p1.y : q == 2 ? p1.z : p1.w);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint2 w = sm.rows8[t][4 * k + q][lane];
-            mma_16816(d[t], a0.x, a1.x, a0.y, a1.y, w.x, w.y);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = i0 + g + 8 * u;
-        float best = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if ((which >> (8 * t + 2 * part + e)) & 1u) best = fmaxf(best, d[t][2 * u + e]);
-        best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
-        best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
-        if (part == 0 && i < s1) {
-          if (r0) best = fmaxf(best, __uint_as_float(own[i - s0]));
-          if (last) {
-            const float score = (best == -INFINITY ? 0.f : best) * (ks[u] * 1.9073486e-6f);  // 2^-19: within float32 whatever the scale
-            dest[i - s0] = ks[u] < 0.f ? 0u : score_key(score);
-          } else {
-            own[i - s0] = __float_as_uint(best);
-          }
+        for (int t = 0; t < NT; ++t) {
+          const uint2 w = sm.rows8[t][4 * k + q][lane];
+          mma_16816(d[t], a0.x, a1.x, a0.y, a1.y, w.x, w.y);
         }
       }
     }
-    if (!last) {
-      __syncthreads();  // the rows' words are used
-      if (tid == 0) sm.rows = 0;
-      __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = i0 + g + 8 * u;
+      float best = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if ((which >> (8 * t + 2 * part + e)) & 1u) best = fmaxf(best, d[t][2 * u + e]);
+      best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
+      best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+      if (part == 0 && i < s1) {
+        const float score = (best == -INFINITY ? 0.f : best) * (ks[u] * 1.9073486e-6f);  // 2^-19: within float32 whatever the scale
+        dest[i - s0] = ks[u] < 0.f ? 0u : score_key(score);
+      }
     }
   }
   if (ranks > 1) cl.sync();

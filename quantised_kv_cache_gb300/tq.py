@@ -631,7 +631,7 @@ def tq_q8_bounds(ctx, cache: "Cache", bounds: torch.Tensor, seq_lens: torch.Tens
 
 
 def tq_q8_select_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, span: int, max_len: int) -> int:
-    """Bytes for calls of these sizes and of smaller ones (0: none)."""
+    """Bytes for calls of the same heads and of these sizes or smaller ones (0: none)."""
     out = _sz()
     check(lib().tq_q8_select_workspace(ctx, batch, heads_q, heads_kv, n_q, span, max_len, ctypes.byref(out)), "tq_q8_select_workspace")
     return out.value
@@ -709,7 +709,7 @@ def _attn(cache: "Cache", q: torch.Tensor, seq_lens, max_len, new_lens, scale, s
 
 
 def tq_q8_sparse_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, span: int, n_blocks: int) -> int:
-    """Bytes for calls of these sizes, and of smaller ones with the same span."""
+    """Bytes for calls of the same heads and span and of these sizes or smaller ones."""
     out = _sz()
     check(lib().tq_q8_sparse_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, span, n_blocks, ctypes.byref(out)),
           "tq_q8_sparse_attention_workspace")
@@ -742,7 +742,7 @@ def tq_q8_sparse_attention(ctx, cache: "Cache", blocks: torch.Tensor, q: torch.T
 
 
 def tq_q8_shared_attention_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, max_prefix: int, max_len: int) -> int:
-    """Bytes for calls of these sizes and of smaller ones."""
+    """Bytes for calls of the same heads and of these sizes or smaller ones."""
     out = _sz()
     check(lib().tq_q8_shared_attention_workspace(ctx, batch, heads_q, heads_kv, n_q, max_prefix, max_len, ctypes.byref(out)),
           "tq_q8_shared_attention_workspace")

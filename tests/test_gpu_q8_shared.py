@@ -140,6 +140,21 @@ def test_queries_that_are_not_finite_stay_alone(ctx, n):
     assert torch.equal(got, good)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("B,n", [(1, 1), (3, 1), (60, 1), (3, 60), (2, 64), (70, 2)])
+def test_either_part_without_tokens(ctx, B, n, dtype):
+    """No prefix in any sequence; no own tokens (the queries are the prefix's last tokens, or lie before its first); neither."""
+    Hq, H, P, length = 8, 2, 200, 90
+    pre, own, pk, pv, k, v = caches(ctx, B, H, P, 128, [length] * B, 7)
+    q = queries(5, B, Hq, n, dtype)
+    for prefix, have in ((0, length), (P, 0), (30, 0), (0, 0)):
+        lse = torch.empty(B, Hq, n, device=DEV)
+        got = tq.tq_q8_shared_attention(ctx.handle, pre, ints([prefix] * B), P, own, q, ints([have] * B), 128, lse=lse)
+        check(np64(got), np64(q), pk, pv, k, v, [prefix] * B, [have] * B, [n] * B, dtype=dtype, out_dtype=dtype, lse=np64(lse))
+        if prefix + have == 0:
+            assert not got.any() and torch.isneginf(lse).all()
+
+
 def test_lengths_and_table_entries_out_of_range(ctx):
     B, Hq, H, P, lens = 3, 4, 2, 200, [100, 90, 128]
     pre, own, pk, pv, k, v = caches(ctx, B, H, P, 128, lens, 7, paged=True)
