@@ -6,9 +6,9 @@
 // exactly whatever the order. Blocks are accumulator lanes: a block's largest score over the rows is a maximum along its lane.
 // Rows that do not count, and those that fill the operand up, are copies of one that does.
 //
-// Split: the (list, 128 blocks) space in equal slices, one CTA per SM; a list's rows are converted once a slice and
+// Split: the (list, 128 blocks) space in slices, one CTA per SM, equal ones or of whole lists; a list's rows are converted once a slice and
 // 256 rows, the next list's load behind this one's tiles, the next tile's bounds behind this one's product.
-// 2048 tokens x 32 heads over 256 blocks, one list for 64 tokens: 26 us, and 6 for the choice. A CTA has 1.7 lists, and each a chain of
+// 2048 tokens x 32 heads over 256 blocks, one list for 64 tokens: 21 us, and 6 for the choice. A CTA has one list or two, and each a chain of
 // its rows' loads (3 us in the first), their largest, the conversions (1.6 us) and two tiles of 2 us, 1.1 of them the product; the products
 // alone would take 5 us at the tensor cores' rate, with operands that were made beside them.
 
@@ -80,7 +80,7 @@ struct Eight {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_constant__ Q8SelectArgs a, int tiles, long long total) {
+__global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_constant__ Q8SelectArgs a, int tiles, long long total, int step) {
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared sm;
   uint8_t *const abuf = dyn, *const bbuf = dyn + kABytes;
@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem, u_d = warp_uniform(tmem);
   pdl_wait();
-  const long long g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
+  // slices begin at multiples of `step` tiles
+  const long long g0 = total / step * blockIdx.x / gridDim.x * step, g1 = total / step * (blockIdx.x + 1) / gridDim.x * step;
   const bool issue = elect_lane();
   const uint32_t u_a = warp_uniform(smem_u32(abuf)), u_b = warp_uniform(smem_u32(bbuf));
   const int r8 = lane & 7, c8 = lane >> 3;  // a warp's part of an operand's conversion: 8 rows, four columns of 16 bytes
@@ -313,11 +314,16 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
 int launch_q8_scores(const Q8SelectArgs &a, int num_sms, void *stream) {
   constexpr int smem = kABytes + kBBytes;
   const int tiles = (q8_blocks_of(a.q.max_len) + kTileBlocks - 1) / kTileBlocks;
-  const long long total = (long long)a.q.batch * a.q.heads_kv * a.lists * tiles;
+  const long long lists = (long long)a.q.batch * a.q.heads_kv * a.lists, total = lists * tiles;
   const dim3 grid((unsigned)std::min((long long)num_sms, total));
+  // A tile takes 2 us, a list's start 5: whole lists where the CTA with the most tiles and starts has no more than one of equal slices would (which
+  // may begin with a list's last tile). 32 heads over 256 blocks, lists of 64 tokens, cut and whole: 1024 tokens 22.6 and 17.2 us, 2048
+  // 32.6 and 27.4 (lists of 128: 44.3 and 29.5), 4096 45.9 and 48.0.
+  const long long n = (lists + num_sms - 1) / num_sms, most = (total + num_sms - 1) / num_sms;
+  const int step = 2 * n * tiles + 5 * n <= 2 * most + 5 * (1 + (most + tiles - 2) / tiles) ? tiles : 1;
   auto run = [&](bool allowed, auto kernel) {
     if (!allowed) return TQ_ERR_CUDA;
-    return launch_overlapped(true, kernel, grid, dim3(kThreads), smem, (cudaStream_t)stream, a, tiles, total) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return launch_overlapped(true, kernel, grid, dim3(kThreads), smem, (cudaStream_t)stream, a, tiles, total, step) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
   };
   if (a.q.q_dtype == TQ_F32) return run(allow_shared<q8_scores_kernel<float>>(smem), q8_scores_kernel<float>);
   if (a.q.q_dtype == TQ_BF16) return run(allow_shared<q8_scores_kernel<__nv_bfloat16>>(smem), q8_scores_kernel<__nv_bfloat16>);

@@ -196,6 +196,8 @@ CASES = [  # B, heads_q, heads_kv, n_q, span, lens, keep, sink, recent
     (1, 8, 2, 130, 64, [3333], 9, 1, 3), (1, 2, 1, 300, 1000, [3000], 5, 1, 1), (40, 2, 1, 1, 1, [64 * i + 1 for i in range(40)], 8, 1, 1),
     (1, 4, 1, 1, 1, [64 * 1000], 64, 1, 2), (1, 1, 1, 1, 1, [64 * 5000 + 7], 100, 1, 2), (1, 16, 8, 1, 1, [64 * 1030], 17, 0, 0),
     (1, 4, 2, 2, 1, [64 * 520], 520, 1, 1),
+    # lists of several tiles: a processor's slice is whole lists; begins within one
+    (1, 8, 2, 512, 8, [64 * 300], 9, 1, 1), (1, 8, 2, 640, 8, [64 * 300], 9, 1, 1),
 ]
 
 
