@@ -535,6 +535,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
   if constexpr (TEAM) {
     if (ranks > 1 && total > 0) {  // the parts of a row: thread = coordinate, the ranks and their warpgroups take turns at the rows
       cg::cluster_group cl = cg::this_cluster();
+      __syncwarp();  // a warp's lanes come to the barriers together
       cl.sync();
       int len, m, row0, row_end, list;
       unit_span<KIND>(a, team_x, kUnitRows, &row0, &row_end, &list);
@@ -560,6 +561,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         }
         finish_row<KIND>(a, team_b, team_h * G + row % G, i, d, o, top, l, lr, 15.f);
       }
+      __syncwarp();
       cl.sync();  // the others have read this CTA's parts
     }
   }

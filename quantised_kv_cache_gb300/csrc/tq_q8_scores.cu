@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
     mbar_init(&sm.bar, 1);
     mbar_fence_init();
   }
-  if (warp == 0) {
+  if (warp == 1) {  // (one whose lanes are together: the first's have just parted)
     tmem_alloc(smem_u32(&sm.tmem), kTileRows);
     tmem_relinquish();
   }
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 0) tmem_dealloc(tmem, kTileRows);
+  if (warp == 1) tmem_dealloc(tmem, kTileRows);
 }
 
 }  // namespace

@@ -185,7 +185,12 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   const long long list = blockIdx.x / ranks;  // [batch][heads_kv][lists]
   const long long bh = list / a.lists;
   const int l = (int)(list - bh * a.lists), b = (int)(bh / a.q.heads_kv), h = (int)(bh - (long long)b * a.q.heads_kv), G = a.q.group;
+  // (to an aligned barrier a warp's lanes come together)
   if (ranks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // the first CTA has begun: its shared memory may be written
+  auto cluster_wait = [&] {
+    __syncwarp();
+    if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  };
   for (int i = tid; i < 4 * kBins; i += kThreads) sm.hist[0][i] = 0;
   if (tid == 0) sm.rows = 0;
   pdl_trigger();
@@ -205,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   const int first = hi > 0 ? lo / kQ8Block : 0, n = (hi + kQ8Block - 1) / kQ8Block - first;  // the blocks that are seen
   int32_t *out = a.blocks + list * a.keep;
   if (n <= a.keep) {
+    cluster_wait();  // before the loop, which the lanes of a warp leave at different turns
     if (rank == 0)
       for (int i = tid; i < a.keep; i += kThreads) out[i] = i < n ? first + i : -1;
-    if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
   // ---- a warp's next 16 blocks' bounds on their way: four lanes share a block, and the one 8 after it
@@ -277,10 +282,11 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   }
   __syncthreads();
   const uint32_t which = sm.rows;
-  if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  cluster_wait();
   uint32_t *const dest = big ? far + s0 : ranks > 1 ? cl.map_shared_rank(held, 0) + s0 : held;
   for (int i0 = begin; i0 < s1; i0 += 16 * kWarps) {
     if (i0 != begin) fetch(i0);
+    __syncwarp();  // the products are a warp's
     float d[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
@@ -315,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
       }
     }
   }
+  __syncwarp();
   if (ranks > 1) cl.sync();
   else __syncthreads();
   if (rank) return;
