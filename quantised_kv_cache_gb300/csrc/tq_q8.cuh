@@ -28,6 +28,13 @@ bool allow_shared(int bytes) {
   return true;
 }
 
+// A number that earlier work of the stream may have written, after pdl_wait(). A plain load: __ldg is for what does not change while the kernel
+// lives (and may be moved in front of the wait), but with a programmatic launch a kernel lives while those before it still write.
+template <typename T>
+__device__ __forceinline__ T latest(const T *p) {
+  return *p;
+}
+
 constexpr float kQ8Largest = 3.1901471898837980e38f;  // 1.875 * 2^127: 240 * 2^120
 
 __device__ __forceinline__ int q8_off(int t, int c) { return (t >> 3) * 1024 + (c >> 4) * 128 + (t & 7) * 16 + (c & 15); }
@@ -36,12 +43,38 @@ __device__ __forceinline__ int q8_off(int t, int c) { return (t >> 3) * 1024 + (
 // word set) for a table entry outside the pool.
 __device__ __forceinline__ long long q8_block(const int32_t *btab, int pool_blocks, long long v, int *error) {
   if (btab == nullptr) return v;
-  const int pb = __ldg(btab + v);
+  const int pb = latest(btab + v);
   if (pb < 0 || pb >= pool_blocks) {
     set_error(error, TQ_ERR_ARG);
     return -1;
   }
   return pb;
+}
+
+// The virtual blocks v[k] that are used: where they lie, -1 for the others and for bad table entries. (Both entries are asked for before
+// either is looked at: the error word's store stands between them otherwise.)
+__device__ __forceinline__ void q8_two_blocks(const Q8Cache &c, const long long (&v)[2], const bool (&use)[2], int *error, long long (&at)[2]) {
+  int pb[2] = {0, 0};
+  if (c.btab) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (use[k]) pb[k] = latest(c.btab + v[k]);
+  }
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bool good = use[k] && (!c.btab || (pb[k] >= 0 && pb[k] < c.pool_blocks));
+    at[k] = !good ? -1 : c.btab ? pb[k] : v[k];
+    bad |= use[k] && !good;
+  }
+  if (bad) set_error(error, TQ_ERR_ARG);
+}
+// Their scales, keys' then values', -1 for a block that is not there.
+__device__ __forceinline__ float4 q8_two_scales(const Q8Cache &c, const long long (&at)[2]) {
+  float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
+  if (at[0] >= 0) f.x = latest(c.ks + at[0]), f.z = latest(c.vs + at[0]);
+  if (at[1] >= 0) f.y = latest(c.ks + at[1]), f.w = latest(c.vs + at[1]);
+  return f;
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127

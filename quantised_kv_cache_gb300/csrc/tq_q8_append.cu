@@ -35,7 +35,7 @@ struct Piece {
   __device__ __forceinline__ void load(const T *p, const T *q) {
 #pragma unroll
     for (int i = 0; i < H / 4; ++i) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + i), y = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+      const uint4 x = latest(reinterpret_cast<const uint4 *>(p) + i), y = latest(reinterpret_cast<const uint4 *>(q) + i);
       w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
       w[H + 4 * i] = y.x, w[H + 4 * i + 1] = y.y, w[H + 4 * i + 2] = y.z, w[H + 4 * i + 3] = y.w;
     }
@@ -91,10 +91,10 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   const bool rope = ROPE != kNone && tensor == 0;
 
   pdl_wait();
-  const int len = __ldg(a.seq_lens + b);
+  const int len = latest(a.seq_lens + b);
   int n = a.n_new;
   if (a.new_lens) {
-    n = __ldg(a.new_lens + b);
+    n = latest(a.new_lens + b);
     if (n < 0 || n > a.n_new) {
       if (tid == 0) set_error(a.error, TQ_ERR_ARG);
       return;
@@ -120,7 +120,7 @@ q8_append_kernel(const __grid_constant__ Q8AppendArgs a, int hpc) {
   constexpr int kSines = ROPE == kPartner ? 16 : 8;
   float cs[kSines], sn[kSines];
   if (turn && fresh) {
-    const int pos = a.positions ? __ldg(a.positions + (long long)b * a.n_new + tok) : len + tok;
+    const int pos = a.positions ? latest(a.positions + (long long)b * a.n_new + tok) : len + tok;
 #pragma unroll
     for (int i = 0; i < kSines; ++i) {
       cs[i] = 1.f, sn[i] = 0.f;

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(32 * kWarps) q8_bounds_kernel(const __grid_con
   pdl_trigger();
   pdl_wait();
   if (b >= a.batch) return;
-  const int len = __ldg(a.seq_lens + b), m = a.new_lens ? __ldg(a.new_lens + b) : a.n_new;
+  const int len = latest(a.seq_lens + b), m = a.new_lens ? latest(a.new_lens + b) : a.n_new;
   if (m < 0 || m > a.n_new) {
     if (lane == 0) set_error(a.error, TQ_ERR_ARG);
     return;

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   const int tid = threadIdx.x, ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int bh = blockIdx.x / ranks, b = bh / a.heads;
   pdl_wait();
-  int n = __ldg(a.seq_lens + b);
+  int n = latest(a.seq_lens + b);
   if (n < 0 || n > a.src.capacity) {
     if (tid == 0) set_error(a.error, TQ_ERR_ARG);
     n = n < 0 ? 0 : a.src.capacity;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kSel) q8_select_kernel(const __grid_constant__
   int pick = n > a.keep ? a.keep - a.sink - a.recent : 0;  // tokens chosen by weight
   // slots from the sink to the recent ones have a key, of their weight; where all stay, none
   const int low = n <= a.keep ? cnt : a.sink - s0, high = n - a.recent - s0, held = min(cnt, kSelKeys);
-  auto make = [&](int i) -> uint32_t { return i < low || i >= high ? kAlways : weight_key(__ldg(w + s0 + i)); };
+  auto make = [&](int i) -> uint32_t { return i < low || i >= high ? kAlways : weight_key(latest(w + s0 + i)); };
   auto key = [&](int i) -> uint32_t { return i < kSelKeys ? keys[i] : make(i); };
 #pragma unroll 16
   for (int i = tid; i < held; i += kSel) keys[i] = make(i);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constan
   const long long bh = blockIdx.y;
   const int blocks = (a.keep + kQ8Block - 1) / kQ8Block, j0 = blockIdx.x * per, j1 = min(blocks, j0 + per);
   const int32_t *kept = a.kept + bh * a.keep;
-  auto index = [&](int j) { return j * kQ8Block + t < a.keep ? __ldg(kept + j * kQ8Block + t) : -1; };
+  auto index = [&](int j) { return j * kQ8Block + t < a.keep ? latest(kept + j * kQ8Block + t) : -1; };
   pdl_wait();
   if (blockIdx.x == 0 && bh % a.heads == 0 && tid == 0) {  // here, where no other thread reads the lengths: they may be updated in place
     const int b = (int)(bh / a.heads);
@@ -233,17 +233,17 @@ __global__ void __launch_bounds__(kGather) q8_gather_kernel(const __grid_constan
     const bool live = s >= 0 && s < a.src.capacity;
     if (c < 2 && j * kQ8Block + t < a.keep) {  // its weight and position
       const long long at = bh * a.dst.capacity + j * kQ8Block + t, of = bh * a.src.capacity + s;
-      if (c == 0 && a.dst_weights) a.dst_weights[at] = live ? __ldg(a.weights + of) : 0.f;
-      if (c == 1 && a.dst_positions) a.dst_positions[at] = !live ? 0 : a.positions ? __ldg(a.positions + of) : s;
+      if (c == 0 && a.dst_weights) a.dst_weights[at] = live ? latest(a.weights + of) : 0.f;
+      if (c == 1 && a.dst_positions) a.dst_positions[at] = !live ? 0 : a.positions ? latest(a.positions + of) : s;
     }
     if (live) {
       const long long from = q8_block(a.src.btab, a.src.pool_blocks, bh * a.src.nblk + s / kQ8Block, a.error);
       if (from >= 0) {
         const uint8_t *p = a.src.records + from * kQ8BlockBytes + q8_off(s % kQ8Block, 16 * c);
-        w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[1] = __ldg(reinterpret_cast<const uint4 *>(p + kQ8Plane));
-        e0[0] = log2i(__ldg(a.src.ks + from));
-        e0[1] = log2i(__ldg(a.src.vs + from));
+        w[0] = latest(reinterpret_cast<const uint4 *>(p));
+        w[1] = latest(reinterpret_cast<const uint4 *>(p + kQ8Plane));
+        e0[0] = log2i(latest(a.src.ks + from));
+        e0[1] = log2i(latest(a.src.vs + from));
       }
     }
 #pragma unroll

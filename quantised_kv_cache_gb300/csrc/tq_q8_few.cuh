@@ -226,38 +226,19 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       long long src[2] = {-1, -1};
       float4 info = make_float4(-1.f, -1.f, -1.f, -1.f);
       int bytes[2] = {0, 0}, at[2] = {0, 0};
-      if (KIND == kListed && g + lane < g1) {
-        int e, h, t, cnt, r0, end, list;
+      if (g + lane < g1) {
+        int e, h, t, cnt, blk[2];
         locate(g + lane, e, h, t, cnt);
-        unit_span<KIND>(a, unit_of(e), kUnitRows, &r0, &end, &list);
+        const int lo = lo_of(e);
         const long long bh = (long long)seq_of(e) * a.heads_kv + h;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int blk = list_entry(a, bh, list, 2 * t + k);
-          at[k] = max(blk, 0) * kQ8Block;
-          const int m = min(kQ8Block, hi_of(e) - at[k]);
-          if (blk < 0 || m <= 0 || at[k] + kQ8Block <= lo_of(e)) continue;  // no row sees a token of it
-          src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + blk, a.error);
-          if (src[k] < 0) continue;
-          bytes[k] = (m + 31) / 32 * 32 * kD;
-          (k ? info.y : info.x) = __ldg(a.c.ks + src[k]);
-          (k ? info.w : info.z) = __ldg(a.c.vs + src[k]);
+        if constexpr (KIND == kListed) {
+          int r0, end, list;
+          unit_span<KIND>(a, unit_of(e), kUnitRows, &r0, &end, &list);
+          list_entries(a, bh, list, 2 * t, blk);
+        } else {
+          blk[0] = 2 * (lo / kTile + t), blk[1] = blk[0] + 1;
         }
-      } else if (g + lane < g1) {
-        int e, h, t, cnt;
-        locate(g + lane, e, h, t, cnt);
-        const int lo = lo_of(e), tok = (lo / kTile + t) * kTile, n = min(kTile, max(0, hi_of(e) - tok));
-        const long long v = ((long long)seq_of(e) * a.heads_kv + h) * a.c.nblk + tok / kQ8Block;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int m = min(kQ8Block, n - k * kQ8Block);
-          if (m <= 0 || tok + (k + 1) * kQ8Block <= lo) continue;  // no row sees a token of it
-          src[k] = q8_block(a.c.btab, a.c.pool_blocks, v + k, a.error);
-          if (src[k] < 0) continue;
-          bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
-          (k ? info.y : info.x) = __ldg(a.c.ks + src[k]);
-          (k ? info.w : info.z) = __ldg(a.c.vs + src[k]);
-        }
+        info = tile_sources(a, a.c, bh, blk, 0, lo, hi_of(e), src, bytes, at);
       }
       const int todo = (int)min(32ll, g1 - g);
       for (int k = 0; k < todo; ++k, ++it) {
@@ -325,6 +306,10 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         int len, m;
         seq_sizes<KIND>(a, b, &len, &m, false);
         const bool live = warp < NR && row < row_end && i < m;
+        // (asked for with the query: behind the barrier it would be one more wait)
+        const int2 rg = live ? row_range<KIND>(a, b, i, len, m) : make_int2(0, 0);
+        const float slope = live && a.slopes ? latest(a.slopes + hq) : 0.f;
+        const int qpos = !live ? 0 : a.qpos ? latest(a.qpos + (long long)b * a.n_q + i) : query_slot<KIND>(a, i, len, m);
         uint32_t w[T];
         const int ex = row_e5m2<T, KIND>(a, b, hq, i, live, lane, w);
         bar_all();  // everyone is done with the unit before
@@ -333,10 +318,9 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           for (int k = 0; k < T; ++k) *reinterpret_cast<uint32_t *>(qbuf + q8_off(k * NR + warp, 4 * lane)) = w[k];
           if (lane == 0) {
             sm.qscale[warp] = pow2i(ex);
-            const int2 rg = live ? row_range<KIND>(a, b, i, len, m) : make_int2(0, 0);
             sm.range[warp] = rg;
-            sm.slope[warp] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-            sm.qpos[warp] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : query_slot<KIND>(a, i, len, m);
+            sm.slope[warp] = slope * kLog2e;
+            sm.qpos[warp] = qpos;
           }
         }
         fence_proxy_async_shared();
@@ -379,7 +363,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         }
         const int slot = tok0 + wt;
         int kp = slot;
-        if (a.kpos && slot < hi) kp = __ldg(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
+        if (a.kpos && slot < hi) kp = latest(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
         wait(&sm.bar_s[wg], phase & 1);
         __syncwarp();  // the loads from tensor memory are a warp's
         tc_fence_after_sync();
@@ -511,7 +495,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
         if (row >= row_end || i >= mm) continue;
         if (whole && (!TEAM || ranks == 1)) {
           const int hq = h * G + row % G;
-          finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f);
+          finish_row<KIND>(a, b, hq, i, wt, x, top, sl, slr, 15.f, prior_of<KIND, 1>(a, b, hq, i, wt));
         } else {
           part[r * kPartRow + wt] = x;
           if (wt == 0) {
@@ -544,6 +528,8 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
       for (int r = rank + ranks * (warp >> 2); warp < kConsumers / 32 && r < NR; r += ranks * kWg) {
         const int row = row0 + r, i = row / G, d = tid & 127;
         if (row >= row_end || i >= m) continue;
+        const int hq = team_h * G + row % G;
+        const Prior<1> prior = prior_of<KIND, 1>(a, team_b, hq, i, d);
         float x[kMostRanks], mk[kMostRanks], lk[kMostRanks], lrk[kMostRanks], top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < kMostRanks; ++k) {
@@ -559,7 +545,7 @@ q8_attend_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, 
           const float f = mk[k] == -INFINITY ? 1.f : ex2_approx(mk[k] - top);  // without a maximum: zeros (or NaN)
           o = fmaf(x[k], f, o), l = fmaf(lk[k], f, l), lr = fmaf(lrk[k], f, lr);
         }
-        finish_row<KIND>(a, team_b, team_h * G + row % G, i, d, o, top, l, lr, 15.f);
+        finish_row<KIND>(a, team_b, hq, i, d, o, top, l, lr, 15.f, prior);
       }
       __syncwarp();
       cl.sync();  // the others have read this CTA's parts
@@ -589,7 +575,8 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
   seq_sizes<KIND>(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (i >= m) return;
-  const int d = threadIdx.x & 127, grp = threadIdx.x >> 7;
+  const int d = threadIdx.x & 127, grp = threadIdx.x >> 7, hq = cut.h * G + row % G;
+  const Prior<1> prior = prior_of<KIND, 1>(a, cut.b, hq, i, d);
   auto rec = [&](int p) {
     return a.parts + (((long long)blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * kRows * kPartRow + r * kPartRow;
   };
@@ -614,8 +601,7 @@ __global__ void __launch_bounds__(512) q8_join_kernel(const __grid_constant__ Q8
   o = so[0][d] + so[1][d] + so[2][d] + so[3][d];
   l = sl[0] + sl[1] + sl[2] + sl[3];
   lr = slr[0] + slr[1] + slr[2] + slr[3];
-  const int hq = cut.h * G + row % G;
-  finish_row<KIND>(a, cut.b, hq, i, d, o, top, l, lr, 15.f);
+  finish_row<KIND>(a, cut.b, hq, i, d, o, top, l, lr, 15.f, prior);
 }
 
 template <int NR, int T, int KIND>

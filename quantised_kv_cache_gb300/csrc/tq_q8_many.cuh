@@ -288,7 +288,7 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
 // Coordinates d .. d + N - 1 of a row: o = sum 2^(t - mx + 8) v, l the same of 1. Written to where the kind's results go, joined with the
 // prefix's part where there is one.
 template <int KIND, int N>
-__device__ __forceinline__ void finish_part(const Q8AttnArgs &a, int b, int hq, int i, int d, float (&o)[N], float mx, float l) {
+__device__ __forceinline__ void finish_part(const Q8AttnArgs &a, int b, int hq, int i, int d, float (&o)[N], float mx, float l, const Prior<N> &prior) {
   if constexpr (KIND == kPrefix) {
     float *row = a.prior + ((long long)hq * a.n_q + i) * kPriorRow;
 #pragma unroll
@@ -298,15 +298,11 @@ __device__ __forceinline__ void finish_part(const Q8AttnArgs &a, int b, int hq, 
   }
   float lr = l, m = mx;
   if constexpr (KIND == kOwn) {
-    const Prior p = prior_of(a, b, hq, i, mx - 8.f);
+    const Joined p = joined(prior.was, mx - 8.f);
 #pragma unroll
-    for (int q = 0; q < N; q += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(p.row + d + q));
-      o[q] = fmaf(x.x, p.by, o[q] * p.own), o[q + 1] = fmaf(x.y, p.by, o[q + 1] * p.own);
-      o[q + 2] = fmaf(x.z, p.by, o[q + 2] * p.own), o[q + 3] = fmaf(x.w, p.by, o[q + 3] * p.own);
-    }
-    lr = fmaf(__ldg(p.row + kD + 2), p.by, l * p.own);
-    l = fmaf(__ldg(p.row + kD + 1), p.by, l * p.own);
+    for (int q = 0; q < N; ++q) o[q] = fmaf(prior.x[q], p.by, o[q] * p.own);
+    lr = fmaf(prior.lr, p.by, l * p.own);
+    l = fmaf(prior.l, p.by, l * p.own);
     m = p.m + 8.f;
   }
   const float inv = lr == 0.f ? 0.f : 1.f / lr;
@@ -377,7 +373,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       for (long long g = g0; g < g1;) {
         const Unit u = unit_at(p, a.heads_kv, g, g1);
         const Entry en = p.entry[u.e];
-        const long long bh = (long long)u.b * a.heads_kv + u.h, blocks = bh * a.c.nblk;
+        const long long bh = (long long)u.b * a.heads_kv + u.h;
         int r0, rend, list;
         unit_span<KIND>(a, u.pair, kUnit, &r0, &rend, &list);
         const int prefix = KIND == kBoth ? prefix_of(a, u.b) : 0;
@@ -387,47 +383,21 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
           long long src[2] = {-1, -1};
           float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
           int bytes[2] = {0, 0}, at[2] = {0, 0};
-          if (KIND == kListed && lane < todo) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int blk = list_entry(a, bh, list, 2 * (u.t0 + k0 + lane) + k);
-              at[k] = max(blk, 0) * kQ8Block;
-              const int m = min(kQ8Block, en.hi - at[k]);
-              if (blk < 0 || m <= 0 || at[k] + kQ8Block <= en.lo) continue;  // no row sees a token of it
-              src[k] = q8_block(a.c.btab, a.c.pool_blocks, blocks + blk, a.error);
-              if (src[k] < 0) continue;
-              bytes[k] = (m + 31) / 32 * 32 * kD;
-              (k ? f.y : f.x) = __ldg(a.c.ks + src[k]);
-              (k ? f.w : f.z) = __ldg(a.c.vs + src[k]);
-            }
-          } else if (KIND == kBoth && lane < todo) {  // (src: addresses)
+          if (lane < todo) {
             const int j = u.t0 + k0 + lane;
-            const bool pre = j < both.prefix;
-            const Q8Cache &c = pre ? a.pc : a.c;
-            const int tok = (pre ? both.first + j : both.own + j - both.prefix) * kTile, base = pre ? 0 : prefix, end = pre ? min(prefix, en.hi) : en.hi;
+            int blk[2];
+            if constexpr (KIND == kBoth) {  // (src: addresses)
+              const bool pre = j < both.prefix;
+              const Q8Cache &c = pre ? a.pc : a.c;
+              blk[0] = 2 * (pre ? both.first + j : both.own + j - both.prefix), blk[1] = blk[0] + 1;
+              f = tile_sources(a, c, pre ? u.h : bh, blk, pre ? 0 : prefix, en.lo, pre ? min(prefix, en.hi) : en.hi, src, bytes, at);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              at[k] = base + tok + k * kQ8Block;
-              const int m = min(kQ8Block, end - at[k]);
-              if (m <= 0 || at[k] + kQ8Block <= en.lo) continue;  // no row sees a token of it
-              const long long blk = q8_block(c.btab, c.pool_blocks, (pre ? (long long)u.h : bh) * c.nblk + tok / kQ8Block + k, a.error);
-              if (blk < 0) continue;
-              src[k] = (long long)(c.records + blk * kQ8BlockBytes);
-              bytes[k] = (m + 31) / 32 * 32 * kD;
-              (k ? f.y : f.x) = __ldg(c.ks + blk);
-              (k ? f.w : f.z) = __ldg(c.vs + blk);
-            }
-          } else if (lane < todo) {
-            const int tok = (en.lo / kTile + u.t0 + k0 + lane) * kTile, n = min(kTile, max(0, en.hi - tok));
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int m = min(kQ8Block, n - k * kQ8Block);
-              if (m <= 0 || tok + (k + 1) * kQ8Block <= en.lo) continue;  // no row sees a token of it
-              src[k] = q8_block(a.c.btab, a.c.pool_blocks, blocks + tok / kQ8Block + k, a.error);
-              if (src[k] < 0) continue;
-              bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
-              (k ? f.y : f.x) = __ldg(a.c.ks + src[k]);
-              (k ? f.w : f.z) = __ldg(a.c.vs + src[k]);
+              for (int k = 0; k < 2; ++k)
+                if (src[k] >= 0) src[k] = (long long)(c.records + src[k] * kQ8BlockBytes);
+            } else {
+              if constexpr (KIND == kListed) list_entries(a, bh, list, 2 * j, blk);
+              else blk[0] = 2 * (en.lo / kTile + j), blk[1] = blk[0] + 1;
+              f = tile_sources(a, a.c, bh, blk, 0, en.lo, en.hi, src, bytes, at);
             }
           }
           for (int k = 0; k < todo; ++k, ++it) {
@@ -595,8 +565,8 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       const int row = unit0 + in_unit, qi = row / G, hq = u.h * G + row % G;
       const bool live = row < unit1 && qi < m;
       const int2 rg = live ? row_range<KIND>(a, u.b, qi, len, m) : make_int2(0, 0);
-      const float slope = EXTRA && live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-      const int qp = !EXTRA || !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)u.b * a.n_q + qi) : query_slot<KIND>(a, qi, len, m);
+      const float slope = EXTRA && live && a.slopes ? latest(a.slopes + hq) * kLog2e : 0.f;
+      const int qp = !EXTRA || !live ? 0 : a.qpos ? latest(a.qpos + (long long)u.b * a.n_q + qi) : query_slot<KIND>(a, qi, len, m);
       bar_rt(rt);
 
       float o[64];
@@ -658,7 +628,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
               if (a.kpos && a.slopes) {
                 const int32_t *kp = a.kpos + bh * a.c.capacity + slot0 + 16 * q;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, (float)__sad(qp, slot0 + 16 * q + i < hi ? __ldg(kp + i) : 0, 0u), x[i]);
+                for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, (float)__sad(qp, slot0 + 16 * q + i < hi ? latest(kp + i) : 0, 0u), x[i]);
               } else if (a.slopes) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = fmaf(-slope, fabsf(far - (float)(16 * q + i)), x[i]);
@@ -823,7 +793,7 @@ q8_prompt_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ P
       const bool whole = u.t0 == 0 && u.end == g + u.cnt;
       if (live) {
         if (whole) {
-          finish_part<KIND>(a, u.b, hq, qi, 64 * half, o, mx, l);
+          finish_part<KIND>(a, u.b, hq, qi, 64 * half, o, mx, l, prior_of<KIND, 64>(a, u.b, hq, qi, 64 * half));
         } else {
           float *part = p.parts + ((long long)slice * 2 + (u.t0 == 0 ? 1 : 0)) * part_of(kUnit);
           const int r = in_unit;
@@ -909,8 +879,11 @@ __global__ void __launch_bounds__(1024 / kJoin) q8_prompt_join_kernel(const __gr
       if (k0 + k < cut.parts) add(mk[k], lk[k], y[k]);
   }
   const int hq = cut.h * G + row % G;
+  Prior<4> prior[kJoin];
 #pragma unroll
-  for (int j = 0; j < kJoin; ++j) finish_part<KIND>(a, cut.b, hq, i, 4 * (col + 32 / kJoin * j), o[j], top, l);
+  for (int j = 0; j < kJoin; ++j) prior[j] = prior_of<KIND, 4>(a, cut.b, hq, i, 4 * (col + 32 / kJoin * j));
+#pragma unroll
+  for (int j = 0; j < kJoin; ++j) finish_part<KIND>(a, cut.b, hq, i, 4 * (col + 32 / kJoin * j), o[j], top, l, prior[j]);
 }
 
 template <int TERMS, int EXTRA, bool APART, int KIND>

@@ -12,9 +12,9 @@ struct Folded {
 __device__ __forceinline__ Folded folded(const Q8AttnArgs &a, int i) {
   Folded f;
   f.b = i / a.fold, f.i = i - f.b * a.fold;
-  f.prefix = min(max(__ldg(a.prefix_lens + f.b), 0), a.max_prefix);
-  f.len = min(max(__ldg(a.seq_lens + f.b), 0), a.own_max);
-  f.m = a.new_lens ? min(max(__ldg(a.new_lens + f.b), 0), a.fold) : a.fold;
+  f.prefix = min(max(latest(a.prefix_lens + f.b), 0), a.max_prefix);
+  f.len = min(max(latest(a.seq_lens + f.b), 0), a.own_max);
+  f.m = a.new_lens ? min(max(latest(a.new_lens + f.b), 0), a.fold) : a.fold;
   return f;
 }
 
@@ -27,15 +27,15 @@ __device__ __forceinline__ int2 row_range(const Q8AttnArgs &a, int b, int i, int
     const Folded f = folded(a, i);
     if (f.i >= f.m) return make_int2(0, 0);
     end = f.prefix + f.len - f.m + f.i + 1;
-    if (a.kbeg) beg = max(0, __ldg(a.kbeg + i));
-    if (a.kend) end = __ldg(a.kend + i);
+    if (a.kbeg) beg = max(0, latest(a.kbeg + i));
+    if (a.kend) end = latest(a.kend + i);
     end = min(end, f.prefix);
   } else {
     end = len - m + i + 1;
-    if (a.kbeg) beg = max(0, __ldg(a.kbeg + (long long)b * a.n_q + i));
-    if (a.kend) end = __ldg(a.kend + (long long)b * a.n_q + i);
+    if (a.kbeg) beg = max(0, latest(a.kbeg + (long long)b * a.n_q + i));
+    if (a.kend) end = latest(a.kend + (long long)b * a.n_q + i);
     if constexpr (KIND == kOwn) {  // ranges count the prefix's slots
-      const int prefix = min(max(__ldg(a.prefix_lens + b), 0), a.max_prefix);
+      const int prefix = min(max(latest(a.prefix_lens + b), 0), a.max_prefix);
       beg = max(0, beg - prefix);
       if (a.kend) end = max(end, 0) - prefix;
     }
@@ -49,14 +49,12 @@ __device__ __forceinline__ void seq_sizes(const Q8AttnArgs &a, int b, int *len, 
   if constexpr (KIND == kPrefix) {
     *len = a.max_len, *m = a.n_q;
   } else {
-    int n = __ldg(a.seq_lens + b), q = a.new_lens ? __ldg(a.new_lens + b) : a.n_q;
-    if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q)) set_error(a.error, TQ_ERR_ARG);
+    int n = latest(a.seq_lens + b), q = a.new_lens ? latest(a.new_lens + b) : a.n_q;
+    [[maybe_unused]] int prefix = 0;
+    if constexpr (KIND == kOwn || KIND == kBoth) prefix = latest(a.prefix_lens + b);
+    if (report && (n < 0 || n > a.max_len || q < 0 || q > a.n_q || prefix < 0 || prefix > a.max_prefix)) set_error(a.error, TQ_ERR_ARG);
     *len = min(max(n, 0), a.max_len);
-    if constexpr (KIND == kOwn || KIND == kBoth) {
-      const int prefix = __ldg(a.prefix_lens + b);
-      if (report && (prefix < 0 || prefix > a.max_prefix)) set_error(a.error, TQ_ERR_ARG);
-      if constexpr (KIND == kBoth) *len += min(max(prefix, 0), a.max_prefix);
-    }
+    if constexpr (KIND == kBoth) *len += min(max(prefix, 0), a.max_prefix);
     *m = min(max(q, 0), a.n_q);
   }
 }
@@ -95,7 +93,7 @@ __device__ __forceinline__ void unit_span(const Q8AttnArgs &a, int x, int unit, 
 }
 // kBoth: the prefix's length of sequence b, and a unit's tiles of 128 of its slots, the first one that its rows see (those of slots from lo to
 // hi - 1), then of the sequence's own.
-__device__ __forceinline__ int prefix_of(const Q8AttnArgs &a, int b) { return min(max(__ldg(a.prefix_lens + b), 0), a.max_prefix); }
+__device__ __forceinline__ int prefix_of(const Q8AttnArgs &a, int b) { return min(max(latest(a.prefix_lens + b), 0), a.max_prefix); }
 struct BothTiles {
   int prefix, first, own;  // tiles of the prefix; the first of them; the first of the own ones
   int total;
@@ -116,17 +114,39 @@ __device__ __forceinline__ int unit_tiles(const Q8AttnArgs &a, int b, int lo, in
   if constexpr (KIND == kBoth) return both_tiles(prefix_of(a, b), lo, hi).total;
   return (hi + 127) / 128 - lo / 128;
 }
-// The block of entry k of list `list` of (sequence, head) bh, -1 for none that counts.
-__device__ __forceinline__ int list_entry(const Q8AttnArgs &a, long long bh, int list, int k) {
-  if (k >= a.n_blocks) return -1;
+// The blocks of entries k and k + 1 (k even) of list `list` of (sequence, head) bh, -1 for none that counts.
+__device__ __forceinline__ void list_entries(const Q8AttnArgs &a, long long bh, int list, int k, int (&blk)[2]) {
   const int32_t *p = a.blocks + (bh * a.lists + list) * a.n_blocks + k;
-  const int blk = __ldg(p), before = k ? __ldg(p - 1) : -1;
-  if (blk < 0) return -1;
-  if ((k && before < 0) || blk <= before || blk >= a.c.nblk) {
-    set_error(a.error, TQ_ERR_ARG);
-    return -1;
+  int e[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) e[j] = k + j > 0 && k + j <= a.n_blocks ? latest(p + j - 1) : -1;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    blk[j] = e[j + 1] > e[j] && e[j + 1] < a.c.nblk && (e[j] >= 0 || k + j == 0) ? e[j + 1] : -1;
+    bad |= e[j + 1] >= 0 && blk[j] < 0;
   }
-  return blk;
+  if (bad) set_error(a.error, TQ_ERR_ARG);
+}
+// The sources of a unit's tile whose rows see slots from lo to hi - 1: of its blocks blk[k], the first at slot `base` of the rows' count, which
+// slots they begin at, where they lie (src, -1 for one of which no row sees a token) and how many bytes of a plane are copied: whole
+// K-steps of the value product.
+__device__ __forceinline__ float4 tile_sources(const Q8AttnArgs &a, const Q8Cache &c, long long bh, const int (&blk)[2], int base, int lo, int hi,
+                                               long long (&src)[2], int (&bytes)[2], int (&at)[2]) {
+  long long v[2];
+  bool use[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    at[k] = base + max(blk[k], 0) * kQ8Block;
+    const int m = min(kQ8Block, hi - at[k]);
+    use[k] = blk[k] >= 0 && m > 0 && at[k] + kQ8Block > lo;
+    v[k] = bh * c.nblk + blk[k];
+    bytes[k] = (m + 31) / 32 * 32 * kD;
+  }
+  q8_two_blocks(c, v, use, a.error, src);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) bytes[k] = src[k] < 0 ? 0 : bytes[k];
+  return q8_two_scales(c, src);
 }
 
 // The bits of a row's largest magnitude, a lane holding four of its coordinates.
@@ -186,7 +206,7 @@ __device__ __forceinline__ void load_rows(const Q8AttnArgs &a, int b, int h, int
   for (int k = 0; k < 8; ++k) {
     const int row = min(first_row + k, a.group * a.n_q - 1), i = row / a.group;
     const long long off = query_offset<KIND>(a, b, h * a.group + row - i * a.group, min(i, max(m - 1, 0))) + 4 * lane;
-    raw[k] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
+    raw[k] = latest(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + off));
   }
 }
 __device__ __forceinline__ void row_floats(const Q8AttnArgs &a, uint2 raw, bool live, float (&x)[4]) {
@@ -218,15 +238,28 @@ __device__ __forceinline__ void tmem_term_sums(uint32_t taddr, float (&out)[NR])
   }
 }
 
-// A row's part of the prefix, and the factors that bring it and the row's own part (whose sums are relative to 2^m) to one reference.
+// A row's part of the prefix (coordinates d .. d + N - 1), as it lies: asked for before results are stored, behind which it would wait.
+template <int N>
 struct Prior {
-  const float *row;
+  float x[N], was, l, lr;
+};
+template <int KIND, int N>
+__device__ __forceinline__ Prior<N> prior_of(const Q8AttnArgs &a, int b, int hq, int i, int d) {
+  Prior<N> p{};
+  if constexpr (KIND == kOwn) {
+    const float *row = a.prior + (((long long)hq * a.batch + b) * a.n_q + i) * kPriorRow;
+    if constexpr (N == 1) p.x[0] = latest(row + d);
+    else load_vec<float, N>(row + d, p.x);
+    p.was = latest(row + kD), p.l = latest(row + kD + 1), p.lr = latest(row + kD + 2);
+  }
+  return p;
+}
+// The reference of a row's own part (its sums are relative to 2^m) and that of the prefix, and the factors that bring either to it.
+struct Joined {
   float m, by, own;  // the reference, the prefix part's factor, the own part's
 };
-__device__ __forceinline__ Prior prior_of(const Q8AttnArgs &a, int b, int hq, int i, float m) {
-  Prior p;
-  p.row = a.prior + (((long long)hq * a.batch + b) * a.n_q + i) * kPriorRow;
-  const float was = __ldg(p.row + kD);
+__device__ __forceinline__ Joined joined(float was, float m) {
+  Joined p;
   p.m = fmaxf(m, was);
   p.by = was == -INFINITY ? 1.f : ex2_approx(was - p.m);  // without a maximum: zeros (or NaN)
   p.own = m == -INFINITY ? 1.f : ex2_approx(m - p.m);
@@ -236,7 +269,8 @@ __device__ __forceinline__ Prior prior_of(const Q8AttnArgs &a, int b, int hq, in
 // Coordinate d of a row: x = sum 2^(t - top + shift) v, l and lr the same of 1 (lr of the numbers as they entered x). Written to where the kind's
 // results go, joined with the prefix's part where there is one.
 template <int KIND>
-__device__ __forceinline__ void finish_row(const Q8AttnArgs &a, int b, int hq, int i, int d, float x, float top, float l, float lr, float shift) {
+__device__ __forceinline__ void finish_row(const Q8AttnArgs &a, int b, int hq, int i, int d, float x, float top, float l, float lr, float shift,
+                                           const Prior<1> &prior) {
   if constexpr (KIND == kPrefix) {
     float *row = a.prior + ((long long)hq * a.n_q + i) * kPriorRow;
     row[d] = x;
@@ -245,10 +279,10 @@ __device__ __forceinline__ void finish_row(const Q8AttnArgs &a, int b, int hq, i
   }
   float m = top;
   if constexpr (KIND == kOwn) {
-    const Prior p = prior_of(a, b, hq, i, top - shift);
-    x = fmaf(__ldg(p.row + d), p.by, x * p.own);
-    l = fmaf(__ldg(p.row + kD + 1), p.by, l * p.own);
-    lr = fmaf(__ldg(p.row + kD + 2), p.by, lr * p.own);
+    const Joined p = joined(prior.was, top - shift);
+    x = fmaf(prior.x[0], p.by, x * p.own);
+    l = fmaf(prior.l, p.by, l * p.own);
+    lr = fmaf(prior.lr, p.by, lr * p.own);
     m = p.m + shift;
   }
   const float y = lr == 0.f ? 0.f : x / lr;

@@ -50,7 +50,7 @@ struct Eight {
   uint4 w[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = latest(reinterpret_cast<const uint4 *>(p) + k);
   }
   // the largest magnitude's bits, as of a float32 (16-bit magnitudes have the order of their bits)
   __device__ __forceinline__ uint32_t top() const {
@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_scores_kernel(const __grid_con
     const long long at = block(t * kTileBlocks + 8 * warp + r8);
     const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at, 0ll) * kK);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? __ldg(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
+    for (int c = 0; c < 4; ++c) v[c] = at >= 0 ? latest(src + c8 + 4 * c) : make_uint4(0, 0, 0, 0);  // 16 bounds, lo's first
     if (tid < kTileBlocks) {
       const long long mine = block(t * kTileBlocks + tid);
-      scale = mine >= 0 ? __ldg(a.q.c.ks + mine) : -1.f;
+      scale = mine >= 0 ? latest(a.q.c.ks + mine) : -1.f;
     }
   };
   long long g = g0;

@@ -222,11 +222,8 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
   float ks[2];
   auto fetch = [&](int i0) {
     long long at[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = i0 + g + 8 * u;
-      at[u] = i < s1 ? q8_block(a.q.c.btab, a.q.c.pool_blocks, blocks + i, a.q.error) : -1;
-    }
+    const int i = i0 + g;
+    q8_two_blocks(a.q.c, {blocks + i, blocks + i + 8}, {i < s1, i + 8 < s1}, a.q.error, at);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + max(at[u], 0ll) * (2 * kD)) + part;
@@ -234,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 2) q8_choose_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[u][k >> 1][k & 1] = make_uint4(0, 0, 0, 0);
       if (at[u] < 0) continue;
-      v[u][0][0] = __ldg(src + 8), v[u][0][1] = __ldg(src + 12), v[u][1][0] = __ldg(src), v[u][1][1] = __ldg(src + 4);
-      ks[u] = __ldg(a.q.c.ks + at[u]);
+      v[u][0][0] = latest(src + 8), v[u][0][1] = latest(src + 12), v[u][1][0] = latest(src), v[u][1][1] = latest(src + 4);
+      ks[u] = latest(a.q.c.ks + at[u]);
     }
   };
   const int begin = s0 + 16 * warp;

@@ -151,24 +151,28 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
       float4 info = make_float4(-1.f, -1.f, -1.f, -1.f);
       int bytes[2] = {0, 0}, at[2] = {0, 0};
       if (g + lane < g1) {
-        int e, h, t, cnt, r0, end, list;
+        int e, h, t, cnt, blk[2];
         locate(g + lane, e, h, t, cnt);
-        unit_span<KIND>(a, rt0 + e % rts, NR, &r0, &end, &list);
+        const int lo = sm.ent.lo[e];
         const long long bh = (long long)(b0 + e / rts) * a.heads_kv + h;
-        const int lo = sm.ent.lo[e], hi = sm.ent.hi[e], tok = (lo / kTile + t) * kTile;
+        if constexpr (KIND == kListed) {
+          int r0, end, list;
+          unit_span<KIND>(a, rt0 + e % rts, NR, &r0, &end, &list);
+          list_entries(a, bh, list, 2 * t, blk);
+        } else {
+          blk[0] = 2 * (lo / kTile + t), blk[1] = blk[0] + 1;
+        }
+        const int hi = sm.ent.hi[e];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          int blk;
-          if constexpr (KIND == kListed) blk = list_entry(a, bh, list, 2 * t + k);
-          else blk = tok / kQ8Block + k;
-          at[k] = max(blk, 0) * kQ8Block;
+          at[k] = max(blk[k], 0) * kQ8Block;
           const int m = min(kQ8Block, hi - at[k]);
-          if (blk < 0 || m <= 0 || at[k] + kQ8Block <= lo) continue;  // no row sees a token of it
-          src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + blk, a.error);
+          if (blk[k] < 0 || m <= 0 || at[k] + kQ8Block <= lo) continue;  // no row sees a token of it
+          src[k] = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + blk[k], a.error);
           if (src[k] < 0) continue;
           bytes[k] = (m + 31) / 32 * 32 * kD;  // whole K-steps of the value MMA
-          (k ? info.y : info.x) = __ldg(a.c.ks + src[k]);
-          (k ? info.w : info.z) = __ldg(a.c.vs + src[k]);
+          (k ? info.y : info.x) = latest(a.c.ks + src[k]);
+          (k ? info.w : info.z) = latest(a.c.vs + src[k]);
         }
       }
       const int todo = (int)min(32ll, g1 - g);
@@ -243,6 +247,10 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
       {
         const int row = row0 + w4, i = row / G, hq = h * G + row % G;
         const bool live = w4 < NR && row < row_end && i < m;
+        // (asked for with the query: behind the barrier it would be one more wait)
+        const int2 rg = live ? row_range<KIND>(a, b, i, len, m) : make_int2(0, 0);
+        const float slope = live && a.slopes ? latest(a.slopes + hq) : 0.f;
+        const int qpos = !live ? 0 : a.qpos ? latest(a.qpos + (long long)b * a.n_q + i) : query_slot<KIND>(a, i, len, m);
         uint32_t w[T];
         const int ex = row_e5m2<T, KIND>(a, b, hq, i, live, lane, w);
         bar_wg(wg);  // everyone is done with the unit before
@@ -251,9 +259,9 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
           for (int k = 0; k < T; ++k) *reinterpret_cast<uint32_t *>(qmine + q8_off(k * NR + w4, 4 * lane)) = w[k];
           if (lane == 0) {
             sm.qscale[wg][w4] = pow2i(ex);
-            sm.range[wg][w4] = live ? row_range<KIND>(a, b, i, len, m) : make_int2(0, 0);
-            sm.slope[wg][w4] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-            sm.qpos[wg][w4] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : query_slot<KIND>(a, i, len, m);
+            sm.range[wg][w4] = rg;
+            sm.slope[wg][w4] = slope * kLog2e;
+            sm.qpos[wg][w4] = qpos;
           }
         }
         fence_proxy_async_shared();
@@ -290,7 +298,7 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
         }
         const int slot = tok0 + wt;
         int kp = slot;
-        if (a.kpos && slot < hi) kp = __ldg(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
+        if (a.kpos && slot < hi) kp = latest(a.kpos + ((long long)b * a.heads_kv + h) * a.c.capacity + slot);
         wait(&sm.bar_s[wg], it & 1);
         __syncwarp();  // the loads from tensor memory are a warp's
         tc_fence_after_sync();
@@ -387,13 +395,19 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
       }
 
       // ---- the rows' sums over the warps (thread = coordinate of O)
+      const bool whole = t0 == 0 && end == g + cnt;
+      Prior<1> prior[NR];  // of a row that is not there, another's
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int row = min(row0 + r, row_end - 1), i = row / G;
+        prior[r] = prior_of<KIND, 1>(a, b, h * G + row - i * G, i, wt);
+      }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float x = warp_sum(l[r]), y = warp_sum(lr[r]);
         if (lane == 0) reinterpret_cast<float *>(&sm.lw[wg][r])[w4] = x, reinterpret_cast<float *>(&sm.lrw[wg][r])[w4] = y;
       }
       bar_wg(wg);
-      const bool whole = t0 == 0 && end == g + cnt;
       float *part = a.parts + ((long long)slice * 2 + (t0 == 0 ? 1 : 0)) * kSoloRows * kPartRow;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
@@ -402,7 +416,7 @@ q8_solo_kernel(const __grid_constant__ Q8AttnArgs a, int b0, int nb, int rt0, in
         const int row = row0 + r, i = row / G;
         if (row >= row_end || i >= m) continue;
         if (whole) {
-          finish_row<KIND>(a, b, h * G + row % G, i, wt, o[r], mx[r], sl, slr, 15.f);
+          finish_row<KIND>(a, b, h * G + row % G, i, wt, o[r], mx[r], sl, slr, 15.f, prior[r]);
         } else {
           part[r * kPartRow + wt] = o[r];
           if (wt == 0) part[r * kPartRow + kD] = mx[r], part[r * kPartRow + kD + 1] = sl, part[r * kPartRow + kD + 2] = slr;
@@ -443,6 +457,8 @@ __global__ void __launch_bounds__(128 * NR) q8_solo_join_kernel(const __grid_con
   seq_sizes<KIND>(a, cut.b, &len, &m, false);
   const int i = row / G;
   if (row >= row_end || i >= m) return;
+  const int hq = cut.h * G + row % G;
+  const Prior<1> prior = prior_of<KIND, 1>(a, cut.b, hq, i, d);
   const float *rec = a.parts + ((long long)blockIdx.x * 2 + 1) * kSoloRows * kPartRow + r * kPartRow;  // the first part's; then two records a slice
   float top = -INFINITY, o = 0.f, l = 0.f, lr = 0.f;
   for (int p0 = 0; p0 < cut.parts; p0 += 4) {
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(128 * NR) q8_solo_join_kernel(const __grid_con
       top = now;
     }
   }
-  finish_row<KIND>(a, cut.b, cut.h * G + row % G, i, d, o, top, l, lr, 15.f);
+  finish_row<KIND>(a, cut.b, hq, i, d, o, top, l, lr, 15.f, prior);
 }
 
 // Where there is a unit for every SM. 8 KV heads x 4 rows, here and in q8_attend_kernel: 32 sequences over 128 blocks 97 and 99 us (of up to

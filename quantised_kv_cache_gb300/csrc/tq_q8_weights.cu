@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   float ks = -1.f;
   if (wt < n) {
     const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + (tok0 + wt) / kQ8Block, nullptr);
-    if (blk >= 0) ks = __ldg(a.c.ks + blk);
+    if (blk >= 0) ks = latest(a.c.ks + blk);
   }
   if (tid == 0) {
     int bytes = 0;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
   };
   wait(&sm.full, 0);
   const int slot = tok0 + wt;
-  const int kp = a.kpos && wt < n ? __ldg(a.kpos + at + wt) : slot;
+  const int kp = a.kpos && wt < n ? latest(a.kpos + at + wt) : slot;
   const Q8Score sc{a.scale, a.softcap, a.softcap != 0.f ? 1.f / a.softcap : 0.f};
   const bool issue = elect_lane();  // of the warpgroup's first warp
   const uint32_t u_s = warp_uniform(t_s), u_k = smem_u32(ktile), u_q = warp_uniform(smem_u32(qbuf));
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads) q8_weights_kernel(const __grid_const
       for (int t = 0; t < T; ++t) *reinterpret_cast<uint32_t *>(qbuf + q8_off(t * NR + r, 4 * lane)) = w[t];
       if (lane == 0) {
         sm.qscale[wg][r] = pow2i(ex);
-        sm.slope[wg][r] = live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f;
-        sm.qpos[wg][r] = !live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : len - m + i;
+        sm.slope[wg][r] = live && a.slopes ? latest(a.slopes + hq) * kLog2e : 0.f;
+        sm.qpos[wg][r] = !live ? 0 : a.qpos ? latest(a.qpos + (long long)b * a.n_q + i) : len - m + i;
         sm.lse[wg][r] = live ? a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] * kLog2e : 0.f;
       }
     }
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(256) q8_row_tiles_kernel(const __grid_constant
     range[tid] = rg;
     // a row that is not there weighs nothing wherever it looks
     cl[tid].y = live ? a.lse[((long long)b * a.heads_q + hq) * a.n_q + i] * kLog2e : INFINITY;
-    extra[tid] = make_float2(live && a.slopes ? __ldg(a.slopes + hq) * kLog2e : 0.f,
-                             __int_as_float(!live ? 0 : a.qpos ? __ldg(a.qpos + (long long)b * a.n_q + i) : len - m + i));
+    extra[tid] = make_float2(live && a.slopes ? latest(a.slopes + hq) * kLog2e : 0.f,
+                             __int_as_float(!live ? 0 : a.qpos ? latest(a.qpos + (long long)b * a.n_q + i) : len - m + i));
     const int lo = __reduce_min_sync(kFull, sees ? rg.x : 0x7fffffff), hi = __reduce_max_sync(kFull, sees ? rg.y : 0);
     const int maxbeg = __reduce_max_sync(kFull, live ? rg.x : 0), minend = __reduce_min_sync(kFull, live ? rg.y : 0x7fffffff);
     if (lane == 0) see[warp][0] = lo, see[warp][1] = hi, see[warp][2] = maxbeg, see[warp][3] = minend;
@@ -294,7 +294,7 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
     int it = 0;
     for (int r0 = rt0; r0 < rt1; r0 += 32) {
       int4 see = make_int4(0, 0, 0, 0);
-      if (r0 + lane < rt1) see = __ldg(w.see + bh * w.rts + r0 + lane);
+      if (r0 + lane < rt1) see = latest(w.see + bh * w.rts + r0 + lane);
       uint32_t some = __ballot_sync(kFull, see.x < tok0 + n && see.y > tok0);
       for (; some; some &= some - 1, ++it) {
         const int k = __ffs(some) - 1, s = it % kS;
@@ -351,9 +351,9 @@ q8_weights_many_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_consta
     float ks = -1.f;
     if (tok < n) {
       const long long blk = q8_block(a.c.btab, a.c.pool_blocks, bh * a.c.nblk + slot / kQ8Block, nullptr);
-      if (blk >= 0) ks = __ldg(a.c.ks + blk);
+      if (blk >= 0) ks = latest(a.c.ks + blk);
     }
-    const int kp = EXTRA && a.kpos && tok < n ? __ldg(a.kpos + at + tok) : slot;
+    const int kp = EXTRA && a.kpos && tok < n ? latest(a.kpos + at + tok) : slot;
     const float cap = score_cap(a.scale, a.softcap).cap;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float k1 = fmaxf(ks, 0.f);

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) rotary_kernel(con
   const int c0 = IL || !turn ? 2 * V * j : V * j, c1 = IL || !turn ? c0 + V : c0 + dim / 2;
   float cs[V], sn[V];
   if (turn) {
-    const int pos = __ldg(a.positions + (long long)b * a.n + t);
+    const int pos = latest(a.positions + (long long)b * a.n + t);
     const float sign = a.transpose ? -a.rope.gain : a.rope.gain;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
