@@ -665,7 +665,8 @@ typedef struct tq_q8_pick {
  * bounds, no key of a block has a larger product with a row. Rows with an infinity or a NaN
  * do not count (no row left: all scores are 0). Lengths out of range are cut as by tq_q8_attention; blocks with a bad table entry score
  * below all others; both set the error word to TQ_ERR_ARG.
- * Workspace: tq_q8_select_workspace(...) bytes for the same heads and these sizes or larger ones (0: d_workspace may be NULL). */
+ * Workspace: tq_q8_select_workspace(...) bytes for the same heads and span, and these sizes or larger ones (0: d_workspace may be NULL; a smaller span
+ * has more lists, and may need more). */
 tq_status tq_q8_select_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int max_len, size_t *out);
 tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pick *p, void *d_workspace, size_t workspace_bytes,
                        void *stream);

@@ -631,7 +631,7 @@ def tq_q8_bounds(ctx, cache: "Cache", bounds: torch.Tensor, seq_lens: torch.Tens
 
 
 def tq_q8_select_workspace(ctx, batch: int, heads_q: int, heads_kv: int, n_q: int, span: int, max_len: int) -> int:
-    """Bytes for calls of the same heads and of these sizes or smaller ones (0: none)."""
+    """Bytes for calls of the same heads and span and of these sizes or smaller ones (0: none; a smaller span may need more)."""
     out = _sz()
     check(lib().tq_q8_select_workspace(ctx, batch, heads_q, heads_kv, n_q, span, max_len, ctypes.byref(out)), "tq_q8_select_workspace")
     return out.value
