@@ -674,7 +674,9 @@ tq_status tq_q8_select(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_pic
 /* tq_q8_attention over listed blocks alone: a row sees the slots of its range that lie in a block of its list.
  *   d_blocks : int32 [batch][heads_kv][ceil(n_q / span)][n_blocks], 4-byte aligned, block numbers of the sequence in ascending order, negative
  *              ones behind the last; blocks that no row of the list sees are passed over. So is an entry that is not above the one before
- *              it, follows a negative one or lies past the cache's last block, which sets the error word to TQ_ERR_ARG.
+ *              it, follows a negative one or lies past the cache's last block, which sets the error word to TQ_ERR_ARG. For a row no more of its
+ *              list need be looked at than as many entries as there are blocks up to the last that it sees (behind them a list in order names
+ *              later blocks): what stands there may be neither attended nor checked.
  * a->d_weights and a->d_weights_in have to be NULL (TQ_ERR_UNSUPPORTED). Workspace: of the same heads and span, and of these
  * sizes or larger ones. Results at least as precise as tq_q8_attention's, with a list's rows (span x group) in place of a sequence's. */
 tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int span, int n_blocks,
