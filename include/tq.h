@@ -684,14 +684,17 @@ tq_status tq_q8_sparse_attention_workspace(const tq_ctx *ctx, int batch, int hea
 tq_status tq_q8_sparse_attention(const tq_ctx *ctx, const tq_cache *cache, const tq_q8_attn *a, const int32_t *d_blocks, int n_blocks,
                                  int span, void *d_workspace, size_t workspace_bytes, void *stream);
 
-/* tq_q8_attention of a batch whose sequences share a prefix, which is read once for all of them. Sequence b is the first
+/* tq_q8_attention of a batch whose sequences share a prefix, which is read for many of their rows at once: for up to 256 of a KV head's batch x n_q x
+ * group rows (16-bit results; 16 where a short prefix goes quicker so), for 4 or 8 of them (32-bit results); sequences of so many query tokens that
+ * their own rows fill such units read it each for itself, 128 or 256 rows at a time. Sequence b is the first
  * d_prefix_lens[b] tokens of `prefix` (a cache of batch 1 and the same KV heads and context; each in [0, max_prefix],
  * max_prefix <= its capacity) followed by the d_seq_lens[b] tokens that `cache` holds for it. Slots and positions count through both: slot s of
  * the cache is slot d_prefix_lens[b] + s of the sequence, in d_key_begin and d_key_end (default [0, the query's own slot + 1)) and in the bias'
  * distances. a->max_len bounds d_seq_lens, which count the cache's tokens. a->d_q_positions, a->d_k_positions, a->d_weights and a->d_weights_in have to be
  * NULL (TQ_ERR_UNSUPPORTED). A d_prefix_lens[b] out of range is cut and sets the error word to TQ_ERR_ARG. The two
  * parts' sums are joined in fp32 before the one rounding of the result; probabilities are at least as precise as those of tq_q8_attention for
- * as many rows as the whole batch has (batch x n_q x group). Workspace: of the same heads and these sizes or larger ones. */
+ * as many rows as the whole batch has (batch x n_q x group): so behind the prefix the rows of a step may have the 8 (bf16) or 11 (fp16) significant
+ * bits of prompts where they have more than 16 in all, and 12 where they are fewer; how many serve together decides. Workspace: of the same heads and these sizes or larger ones. */
 tq_status tq_q8_shared_attention_workspace(const tq_ctx *ctx, int batch, int heads_q, int heads_kv, int n_q, int max_prefix, int max_len,
                                            size_t *out);
 tq_status tq_q8_shared_attention(const tq_ctx *ctx, const tq_cache *prefix, const int32_t *d_prefix_lens, int max_prefix,

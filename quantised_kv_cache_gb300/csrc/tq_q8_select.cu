@@ -12,7 +12,7 @@
 // go from memory to the operand's registers as they lie (chains of four byte products in one instruction, dp4a, took 17 clocks each on
 // a quarter of an SM: 6 of the 13 us). Lists of more rows: q8_scores_kernel. Bound by latency for few lists (lengths, bounds, a cluster barrier,
 // the passes of the choice): 8 KV heads of 4 rows among 2048 blocks 9.0 us, 2.5 of them the launch; 384 lists among up to 512 blocks (7 MB of
-// bounds) 12.1 us.
+// bounds) 11.8 us.
 
 #include <cooperative_groups.h>
 
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kHeld = 32768;  // scores kept in shared memory (128 KB): 2 M tokens
-// Rows up to which a list's scores are formed here, by products of bytes; more go to the tensor cores.
+// Rows up to which a list's scores are formed here, by m16n8k16 products; more go to q8_scores_kernel's of 128 x 256.
 constexpr long long kFewRows = 16;
 constexpr int kBins = 256;
 

@@ -2,10 +2,11 @@
 //
 // out = (X1 + X2) / (l1 + l2): the rows' sums over the prefix, X1 = sum 2^(t - m) v and l1 = sum 2^(t - m), then those over the sequence's own
 // tokens, on one reference. Over the prefix the rows of all sequences are the rows of one (its head's, batch x query tokens x
-// group of them), so that its keys and values are read once for the batch and make operands of up to 256 rows. Their parts go to the workspace,
+// group of them), so that its keys and values are read once for every 256 of them (32-bit results: 8). Their parts go to the workspace,
 // where the kernels of the own tokens fetch them as they finish a row: no pass of its own joins them. 64 sequences of up to 2048 tokens behind
-// 32768, 8 KV heads of 4 rows, bf16: 106 us, of which the prefix takes 60 (48 in its tiles of 256 rows, 3.5 us each; its bytes would take 10)
-// and the own tokens 40 (20). Each sequence over a cache of its own with the prefix in it: 64 times its bytes, 640 us at the copy's rate.
+// 32768, 8 KV heads of 4 rows, bf16: 109 us (cold and one after the other: plan 5.5, the prefix's tiles 54.7, their join 12.6, the own tokens
+// 33.5, their join 5.7; the prefix's bytes would take 10, the own tokens' 20). Each sequence over a cache of its own with the prefix in it: 64 times
+// its bytes, 640 us at the copy's rate. 32-bit results: 490 us, 438 of them the prefix, 32 units of 8 rows that each read it (from L2 for the most part).
 
 #include "tq_q8_solo.cuh"
 

@@ -6,7 +6,7 @@
 //
 // Ring: three places of 16 KB for each warpgroup that its tiles' keys and values take in turn (keys of a tile, its values, keys of the next), so that
 // the next tile's keys load while this one's values are used, in 192 KB. One producer warp a warpgroup. A tile's chain is some 3500 clocks, so that
-// four at a time are faster than memory; 32 sequences of up to 16383 tokens over 128 blocks each, 4 rows, capped, paged: 67 us, 5.0 TB/s
+// four at a time are faster than memory; 32 sequences of up to 16383 tokens over 128 blocks each, 4 rows, capped, paged: 66 us, 5.1 TB/s
 // (the chosen blocks' 335 MB take 49): some 6 us until the first tile's scores, 5 of join, the rest the slices' unequal ends.
 #pragma once
 

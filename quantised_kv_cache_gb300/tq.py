@@ -755,8 +755,8 @@ def tq_q8_shared_attention(ctx, prefix: "Cache", prefix_lens: torch.Tensor, max_
                            key_end: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                            out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
-    """tq_q8_attention of a batch whose sequences are the first prefix_lens[b] tokens of `prefix` (a cache of batch 1), read once for
-    all of them, followed by the seq_lens[b] tokens that `cache` holds for each; key ranges count through both (include/tq.h)."""
+    """tq_q8_attention of a batch whose sequences are the first prefix_lens[b] tokens of `prefix` (a cache of batch 1), read for many of
+    their rows at once, followed by the seq_lens[b] tokens that `cache` holds for each; key ranges count through both (include/tq.h)."""
     a, out, index = _attn(cache, q, seq_lens, max_len, new_lens, scale, softcap, slopes, None, None, key_begin, key_end, lse, out, out_dtype,
                           stream)
     B, Hq, n, _ = q.shape
